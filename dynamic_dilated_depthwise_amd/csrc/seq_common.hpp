@@ -1,0 +1,228 @@
+// seq_common.hpp -- device helpers of the sequence operators (layer norm, short causal
+// convolution, selective scan): loads of any alignment, matrix fragments of either type.
+//
+// Fragments.  Every product runs in steps of 32 along its contraction.  A lane (l16 =
+// lane % 16, g = lane / 16) holds eight elements of one row (A) or column (B) l16; slot
+// e of group g stands for the contraction index
+//     k(g, e) = 4g + e          (e < 4)
+//               16 + 4g + e - 4 (e >= 4)
+// Any assignment is right as long as A and B share it.  This one is what the accumulator
+// layout gives (component v of group g is row 4g + v of a 16 x 16 tile), so two result
+// tiles one above the other are the operand of the next product with no exchange between
+// lanes, and what the transposing LDS read gives (four rows of a column per lane).  For
+// float32 the same eight slots feed eight 16x16x4 products.
+#pragma once
+
+#include "common.hpp"
+
+namespace ddpm {
+namespace seq {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint16_t u16x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// Elements of one 16-byte vector.
+template <typename T> constexpr int kVec = 16 / (int)sizeof(T);
+
+// 16 bytes from `p`, which need only be aligned to its element, when n >= kVec of them
+// are there; otherwise the n that are, and zeros.  Nothing past p[n - 1] is read.
+template <typename T>
+__device__ __forceinline__ u32x4 load_vec(const T *__restrict__ p, int64_t n) {
+    u32x4 r = {0, 0, 0, 0};
+    if (n >= kVec<T>) {
+        r = *(const u32x4_a2 *)p;
+    } else if (n > 0) {
+        if constexpr (Elem<T>::is_bf16) {
+            for (int e = 0; e < 7; ++e)
+                if (e < n) r[e / 2] |= (uint32_t)p[e] << (16 * (e % 2));
+        } else {
+            for (int e = 0; e < 3; ++e)
+                if (e < n) r[e] = __float_as_uint(p[e]);
+        }
+    }
+    return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void widen(const u32x4 &r, float (&v)[kVec<T>]) {
+    if constexpr (Elem<T>::is_bf16) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[2 * e] = __uint_as_float(r[e] << 16);
+            v[2 * e + 1] = __uint_as_float(r[e] & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(r[e]);
+    }
+}
+
+// Stores the first n (at most kVec) of v, rounded to T once.
+template <typename T>
+__device__ __forceinline__ void store_vec(T *__restrict__ p, const float (&v)[kVec<T>], int64_t n) {
+    if (n >= kVec<T>) {
+        u32x4 r;
+        if constexpr (Elem<T>::is_bf16) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                r[e] = (uint32_t)f32_to_bf16_bits(v[2 * e]) | (uint32_t)f32_to_bf16_bits(v[2 * e + 1]) << 16;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) r[e] = __float_as_uint(v[e]);
+        }
+        *(u32x4_a2 *)p = r;
+    } else {
+#pragma unroll
+        for (int e = 0; e < kVec<T>; ++e)
+            if (e < n) p[e] = Elem<T>::from_f32(v[e]);
+    }
+}
+
+// Four elements at `p` (element-aligned), the first n of them.
+template <typename T>
+__device__ __forceinline__ void store4(T *__restrict__ p, const f32x4 &v, int n) {
+    if (n >= 4) {
+        if constexpr (Elem<T>::is_bf16) {
+            u16x4 u;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[e] = f32_to_bf16_bits(v[e]);
+            *(u16x4_a2 *)p = u;
+        } else {
+            *(f32x4_a4 *)p = v;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            if (e < n) p[e] = Elem<T>::from_f32(v[e]);
+    }
+}
+
+__device__ __forceinline__ f32x4 load4(const float *__restrict__ p, int n) {
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    if (n >= 4) {
+        v = *(const f32x4_a4 *)p;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            if (e < n) v[e] = p[e];
+    }
+    return v;
+}
+
+// softplus and its derivative, in the form that neither overflows nor cancels.
+__device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
+__device__ __forceinline__ float sigmoid(float v) {
+    const float e = expf(-fabsf(v));
+    return (v >= 0.f ? 1.f : e) / (1.f + e);
+}
+
+// ------------------------------------------------------------------------------ fragments
+struct FragF {
+    float v[8];
+};
+template <typename T> struct FragOf { typedef FragF type; };
+template <> struct FragOf<bf16_t> { typedef bf16x8 type; };
+template <typename T> using Frag = typename FragOf<T>::type;
+
+// LDS rows carry 16 bytes of padding: 16 rows read at one column then start in 16
+// different quarters of the banks.
+template <typename T> constexpr int ld_of(int cols) { return cols + kVec<T>; }
+
+__device__ __forceinline__ f32x4 mma(const bf16x8 &a, const bf16x8 &b, f32x4 c) { return mfma_16x16x32_bf16(a, b, c); }
+__device__ __forceinline__ f32x4 mma(const FragF &a, const FragF &b, f32x4 c) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c = mfma_16x16x4_f32(a.v[e], b.v[e], c);
+    return c;
+}
+
+// Contraction along a row: `row` points at element k0 of the lane's own row.
+__device__ __forceinline__ bf16x8 row_frag(const bf16_t *row, int g) {
+    const u16x4 a = *(const u16x4 *)(row + 4 * g), b = *(const u16x4 *)(row + 16 + 4 * g);
+    u16x8 r;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) { r[e] = a[e]; r[4 + e] = b[e]; }
+    return __builtin_bit_cast(bf16x8, r);
+}
+__device__ __forceinline__ FragF row_frag(const float *row, int g) {
+    const f32x4 a = *(const f32x4 *)(row + 4 * g), b = *(const f32x4 *)(row + 16 + 4 * g);
+    FragF r;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) { r.v[e] = a[e]; r.v[4 + e] = b[e]; }
+    return r;
+}
+
+// Contraction down the rows r0 .. r0 + 31 of an LDS tile, column c0 + l16.
+__device__ __forceinline__ bf16x8 col_frag(const bf16_t *tile, int ld, int r0, int c0, int l16, int g) {
+    typedef __attribute__((address_space(3))) s16x4 *lds_ptr;
+    const bf16_t *p = tile + (r0 + 4 * g + l16 / 4) * ld + c0 + 4 * (l16 % 4);
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)p);
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + 16 * ld));
+    u16x8 r;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) { r[e] = (uint16_t)a[e]; r[4 + e] = (uint16_t)b[e]; }
+    return __builtin_bit_cast(bf16x8, r);
+}
+__device__ __forceinline__ FragF col_frag(const float *tile, int ld, int r0, int c0, int l16, int g) {
+    const float *p = tile + (r0 + 4 * g) * ld + c0 + l16;
+    FragF r;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) { r.v[e] = p[e * ld]; r.v[4 + e] = p[(16 + e) * ld]; }
+    return r;
+}
+
+// Two result tiles, rows 0..15 and 16..31 of the contraction, as an operand; bf16 rounds.
+template <typename T>
+__device__ __forceinline__ Frag<T> pack_frag(const f32x4 &a, const f32x4 &b) {
+    Frag<T> r;
+    if constexpr (Elem<T>::is_bf16) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) { r[e] = (__bf16)a[e]; r[4 + e] = (__bf16)b[e]; }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) { r.v[e] = a[e]; r.v[4 + e] = b[e]; }
+    }
+    return r;
+}
+
+// A float32 as the sum of three bfloat16: 8 + 8 + 8 significant bits, so the sum is the
+// float32 itself (down to the subnormals) and a product with a bfloat16 operand keeps
+// float32's precision at three matrix instructions.
+__device__ __forceinline__ void split3(float f, __bf16 &hi, __bf16 &mid, __bf16 &lo) {
+    hi = (__bf16)f;
+    const float r = f - (float)hi;
+    mid = (__bf16)r;
+    lo = (__bf16)(r - (float)mid);
+}
+
+// Terms an exact float32 operand takes in the type's matrix products.
+template <typename T> constexpr int kTerms = Elem<T>::is_bf16 ? 3 : 1;
+
+// A tile of ROWS token rows by COLS columns (of which ncols hold data), fetched into
+// registers and put into LDS later, so that the fetch runs behind other work.  Rows past
+// `rows` and columns past `ncols` read as zero and are not touched in memory.
+template <typename T, int ROWS, int COLS, int THREADS>
+struct TileFetch {
+    static constexpr int kPerRow = COLS / kVec<T>;
+    static constexpr int kCount = ROWS * kPerRow / THREADS;
+    static_assert(ROWS * kPerRow % THREADS == 0, "tile must divide over the threads");
+    u32x4 r[kCount];
+    __device__ __forceinline__ void fetch(const T *__restrict__ base, int64_t stride, int rows, int ncols, int tid) {
+#pragma unroll
+        for (int k = 0; k < kCount; ++k) {
+            const int i = tid + k * THREADS, row = i / kPerRow, c = (i % kPerRow) * kVec<T>;
+            r[k] = load_vec<T>(base + row * stride + c, row < rows ? ncols - c : 0);
+        }
+    }
+    __device__ __forceinline__ void put(T *tile, int tid) const {
+#pragma unroll
+        for (int k = 0; k < kCount; ++k) {
+            const int i = tid + k * THREADS, row = i / kPerRow, c = (i % kPerRow) * kVec<T>;
+            *(u32x4 *)(tile + row * ld_of<T>(COLS) + c) = r[k];
+        }
+    }
+};
+
+}  // namespace seq
+}  // namespace ddpm

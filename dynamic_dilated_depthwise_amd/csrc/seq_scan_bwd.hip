@@ -1,0 +1,547 @@
+// seq_scan_bwd.hip -- the selective scan's backward pass (seq_scan.hpp has the forward's
+// formulas).
+//
+// For a chunk, with h0 the state that enters it, g1 the gradient that reaches its end from
+// later tokens, E[t, i] = exp(s[t] - s[i]) for i <= t, CB[t, i] = C[t] . B[i] and
+// Z[t, i] = grad[t] . x[i]:
+//
+//   grad_x[i] = dt[i] (sum_t CB E grad[t] + exp(s_end - s[i]) g1 B[i]) + D grad[i]
+//   grad_B[i] = dt[i] (sum_t Z E C[t] + exp(s_end - s[i]) g1' x[i])      summed over heads
+//   grad_C[t] = sum_i Z E dt[i] B[i] + exp(s[t]) h0' grad[t]             summed over heads
+//
+// The times.  Let r[t] = grad[t] . (y[t] - D x[t]) and q[i] = dt[i] * (what multiplies dt[i]
+// x[i] in the sums above, dotted with x[i]).  The gradient of the decay that token t applies
+// is what flows from tokens before t to t and later,
+//
+//   e[t] = exp(s_end) <g1, h0> + sum_{i < t} q_end[i] + sum_{k >= t} r_in[k]
+//          + sum_{k >= t} (r_own[k] - q_own[k]),
+//
+// where q_end is q's part through g1, r_in r's part through h0, and r_own, q_own the parts
+// inside the chunk without their common diagonal (which would only cancel).  Then
+// grad_dt = (q / dt + A e) sigmoid(raw + dt_bias) and grad_A = sum_t dt e.  These are sums
+// of many terms of both signs, so every factor keeps float32's precision: Z and CB come
+// from products of the inputs themselves, and h0 and g1 enter as three bfloat16 terms.
+// grad_x, grad_B and grad_C are rounded to bfloat16 at their end; the scaled Z and CB that
+// they are summed from are operands rounded to bfloat16 once.
+#include "seq_scan.hpp"
+
+namespace ddpm {
+namespace seq {
+
+struct BwdArgs {
+    ScanDims d;
+    ChunkPlan plan;
+    int64_t x_batch, x_token, b_batch, b_token, c_batch, c_token, g_batch, g_token;
+    const float *states, *adjoints;  // [B, H, nc, P, N]; adjoints null: nothing reaches the only chunk's end
+    const float *A, *D;
+    float *part;   // [splits, 2, B, L, G, N] or null (one split: grad_B and grad_C at once)
+    float *heads;  // [3, H, B * nc]: every chunk's part of grad_A, grad_dt_bias, grad_D
+    int has_first, has_last;  // an initial state, a gradient of the final one
+};
+
+template <typename T, int NP>
+struct BwdLds {
+    static constexpr int QS = kStrips<T>, Q = 16 * QS, LDN = ld_of<T>(NP), LDP = ld_of<T>(kSlab);
+    T b[Q * LDN], c[Q * LDN], x[Q * LDP], g[Q * LDP];
+    T plane[kTerms<T>][kSlab * LDN];  // h0, then g1
+    float shi[Q], slo[Q], dt[Q];
+    float rin[Q], own[Q], direct[Q], qend[Q], dt_done[Q];  // of the head before, for the sums over its tokens
+    float dots[QS], diag[QS], end_done, pad[7];
+};
+
+// Sum over the four lane groups that hold a column's rows.
+__device__ __forceinline__ float over_groups(float v) {
+    v += __shfl_xor(v, 16, kWave);
+    return v + __shfl_xor(v, 32, kWave);
+}
+__device__ __forceinline__ float over_wave(float v) {
+#pragma unroll
+    for (int m = 1; m < kWave; m *= 2) v += __shfl_xor(v, m, kWave);
+    return v;
+}
+
+// One chunk, some heads of a group.  Wave w has strip w of the chunk's tokens both as rows t
+// (grad_C, r) and as columns i (grad_x, grad_B, q): w + 1 tiles of the triangle as rows and
+// QS - w as columns, the same for every wave.
+template <typename T, int NP>
+__global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, const T *__restrict__ X,
+                                                                   const T *__restrict__ Bm, const T *__restrict__ Cm,
+                                                                   const T *__restrict__ grad, T *__restrict__ grad_x,
+                                                                   T *__restrict__ grad_dt, T *__restrict__ grad_B,
+                                                                   T *__restrict__ grad_C) {
+    typedef BwdLds<T, NP> Lds;
+    constexpr int QS = Lds::QS, Q = Lds::Q, THREADS = 64 * QS, LDN = Lds::LDN, LDP = Lds::LDP, NS = NP / 16;
+    extern __shared__ __align__(16) char raw_lds[];
+    Lds &s = *(Lds *)raw_lds;
+    const ScanDims &d = a.d;
+    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, l16 = lane % 16, g = lane / 16;
+    int id = blockIdx.x;
+    const int split = id % a.plan.splits;
+    id /= a.plan.splits;
+    const int grp = id % d.G;
+    id /= d.G;
+    const int c = id % d.nc, b = id / d.nc;
+    const int rows = d.L - c * Q < Q ? d.L - c * Q : Q;
+    const int len = valid_tokens(d.lengths, b, d.L);
+    int n = len - c * Q;
+    n = n < 0 ? 0 : n > Q ? Q : n;
+    const int hg = d.H / d.G, h0 = grp * hg + split * a.plan.per;
+    const int h1 = h0 + a.plan.per < (grp + 1) * hg ? h0 + a.plan.per : (grp + 1) * hg;
+    const int slabs = (d.P + kSlab - 1) / kSlab, items = (h1 - h0) * slabs;
+    const int64_t tok0 = (int64_t)b * d.L + c * Q;  // first token's row in the contiguous outputs
+    const bool has_h = n > 0 && (c > 0 || a.has_first), has_g = (c + 1) * Q < len || (a.has_last && n > 0);
+    const T *xb = X + b * a.x_batch + (int64_t)c * Q * a.x_token;
+    const T *gb = grad + b * a.g_batch + (int64_t)c * Q * a.g_token;
+    const int me = 16 * wave + l16;  // this lane's token, as a row t and as a column i
+    const int kw = wave / 2;
+
+    TileFetch<T, Q, kSlab, THREADS> xf, gf;
+    TileFetch<float, kSlab, NP, THREADS> hf, af;
+    float tf[3];
+    auto fetch = [&](int it) {
+        const int h = h0 + it / slabs, p0 = it % slabs * kSlab;
+        xf.fetch(xb + (int64_t)h * d.P + p0, a.x_token, n, d.P - p0, tid);
+        gf.fetch(gb + (int64_t)h * d.P + p0, a.g_token, n, d.P - p0, tid);
+        const int64_t chunk = ((int64_t)b * d.H + h) * d.nc + c;
+        if (has_h) hf.fetch(a.states + chunk * d.P * d.N + (int64_t)p0 * d.N, d.N, d.P - p0, d.N, tid);
+        if (tid < Q) {
+            tf[0] = d.shi[chunk * Q + tid];
+            tf[1] = d.slo[chunk * Q + tid];
+            tf[2] = d.dt[chunk * Q + tid];
+        }
+    };
+    // a float32 tile into the planes
+    auto put_planes = [&](const TileFetch<float, kSlab, NP, THREADS> &f) {
+#pragma unroll
+        for (int k = 0; k < TileFetch<float, kSlab, NP, THREADS>::kCount; ++k) {
+            const int i = tid + k * THREADS, at = i / (NP / 4) * LDN + i % (NP / 4) * 4;
+            float v[4];
+            widen<float>(f.r[k], v);
+            if constexpr (Elem<T>::is_bf16) {
+                u16x4 t[3];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    __bf16 q0, q1, q2;
+                    split3(v[e], q0, q1, q2);
+                    t[0][e] = __builtin_bit_cast(uint16_t, q0);
+                    t[1][e] = __builtin_bit_cast(uint16_t, q1);
+                    t[2][e] = __builtin_bit_cast(uint16_t, q2);
+                }
+#pragma unroll
+                for (int m = 0; m < 3; ++m) *(u16x4 *)(s.plane[m] + at) = t[m];
+            } else {
+                *(f32x4 *)(s.plane[0] + at) = f32x4{v[0], v[1], v[2], v[3]};
+            }
+        }
+    };
+    // The sums over the tokens of a head: one wave, Q / 64 tokens a lane.
+    auto finish_head = [&](int h) {
+        constexpr int PER = Q / kWave;
+        float dot = 0.f, diag = 0.f;
+#pragma unroll
+        for (int w = 0; w < QS; ++w) {
+            dot += s.dots[w];
+            diag += s.diag[w];
+        }
+        float pre[PER], suf[PER], before = 0.f, after = 0.f;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            pre[e] = before;
+            before += s.qend[lane * PER + e];
+        }
+#pragma unroll
+        for (int e = PER - 1; e >= 0; --e) {
+            after += s.rin[lane * PER + e] + s.own[lane * PER + e];
+            suf[e] = after;
+        }
+        float up = before, down = after;
+#pragma unroll
+        for (int m = 1; m < kWave; m *= 2) {
+            const float u = __shfl_up(up, m, kWave), o = __shfl_down(down, m, kWave);
+            if (lane >= m) up += u;
+            if (lane + m < kWave) down += o;
+        }
+        up -= before;
+        down -= after;
+        const float A = a.A[h];
+        float sum_a = 0.f, sum_b = 0.f;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            const int t = lane * PER + e;
+            const float dt = s.dt_done[t], flow = s.end_done * dot + (up + pre[e]) + (down + suf[e]);
+            // softplus's derivative from its value: 1 - exp(-dt)
+            const float raw = t < n ? (s.direct[t] + A * flow) * -expm1f(-dt) : 0.f;
+            sum_a += t < n ? dt * flow : 0.f;
+            sum_b += raw;
+            if (t < rows) grad_dt[(tok0 + t) * d.H + h] = Elem<T>::from_f32(raw);
+        }
+        sum_a = over_wave(sum_a);
+        sum_b = over_wave(sum_b);
+        if (lane == 0) {
+            const int64_t M = (int64_t)d.B * d.nc, at = (int64_t)h * M + (int64_t)b * d.nc + c;
+            a.heads[at] = sum_a;
+            a.heads[d.H * M + at] = sum_b;
+            a.heads[2 * d.H * M + at] = diag;
+        }
+    };
+
+    // B and C, and the tiles of C . B: rows t of this strip (transposed: D[i][t]) for the
+    // pairs of strips up to its own, columns i of it (D[t][i]) from its own on.
+    f32x4 cbp[QS / 2][2], cbd[2];
+    {
+        TileFetch<T, Q, NP, THREADS> bf, cf;
+        bf.fetch(Bm + b * a.b_batch + (int64_t)c * Q * a.b_token + grp * d.N, a.b_token, n, d.N, tid);
+        cf.fetch(Cm + b * a.c_batch + (int64_t)c * Q * a.c_token + grp * d.N, a.c_token, n, d.N, tid);
+        fetch(0);
+        bf.put(s.b, tid);
+        cf.put(s.c, tid);
+        __syncthreads();
+        auto tile = [&](const T *rows_of, int strip, const T *cols_of) {
+            f32x4 r = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < NP / 32; ++k)
+                if (32 * k < d.N)
+                    r = mma(row_frag(rows_of + (16 * strip + l16) * LDN + 32 * k, g),
+                            row_frag(cols_of + me * LDN + 32 * k, g), r);
+            return r;
+        };
+#pragma unroll
+        for (int k = 0; k < QS / 2; ++k)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (k <= kw) cbp[k][u] = tile(s.b, 2 * k + u, s.c);
+                else cbp[k][u] = tile(s.c, 2 * k + u, s.b);
+            }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) cbd[u] = tile(s.c, 2 * kw + u, s.b);
+    }
+    f32x4 dB[NS], dC[NS];
+#pragma unroll
+    for (int k = 0; k < NS; ++k) dB[k] = dC[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    float rin = 0.f, rown = 0.f, qown = 0.f, qdiag = 0.f, qend = 0.f, dot = 0.f, zdiag = 0.f;
+    for (int it = 0; it < items; ++it) {
+        const int h = h0 + it / slabs, slab = it % slabs, p0 = slab * kSlab;
+        const int64_t chunk = ((int64_t)b * d.H + h) * d.nc + c;
+        __syncthreads();
+        if (it > 0 && slab == 0 && wave == it / slabs % QS) finish_head(h - 1);
+        xf.put(s.x, tid);
+        gf.put(s.g, tid);
+        if (has_h) put_planes(hf);
+        if (tid < Q) {
+            s.shi[tid] = tf[0];
+            s.slo[tid] = tf[1];
+            s.dt[tid] = tf[2];
+        }
+        __syncthreads();
+        if (has_g) af.fetch(a.adjoints + chunk * d.P * d.N + (int64_t)p0 * d.N, d.N, d.P - p0, d.N, tid);
+        const float mhi = s.shi[me], mlo = s.slo[me], mdt = s.dt[me];
+        Frag<T> xr[2], gr[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            xr[k] = row_frag(s.x + me * LDP + 32 * k, g);
+            gr[k] = row_frag(s.g + me * LDP + 32 * k, g);
+        }
+        const int ks = d.P - p0 > 32 ? 2 : 1;
+
+        // rows t
+#pragma unroll
+        for (int k = 0; k < QS / 2; ++k) {
+            if (k > kw) continue;
+            f32x4 wt[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int is = 2 * k + u;
+                wt[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+                if (is > wave) continue;
+                f32x4 z = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    if (q < ks) z = mma(row_frag(s.x + (16 * is + l16) * LDP + 32 * q, g), gr[q], z);
+                const f32x4 ih = *(const f32x4 *)(s.shi + 16 * is + 4 * g), il = *(const f32x4 *)(s.slo + 16 * is + 4 * g);
+                const f32x4 id4 = *(const f32x4 *)(s.dt + 16 * is + 4 * g);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const float e = __builtin_amdgcn_exp2f((mhi - ih[v]) + (mlo - il[v])) * id4[v];
+                    const bool before = is < wave || 4 * g + v < l16, same = is == wave && 4 * g + v == l16;
+                    wt[u][v] = before || same ? z[v] * e : 0.f;
+                    rown += before ? cbp[k][u][v] * wt[u][v] : 0.f;
+                    zdiag += same ? z[v] : 0.f;
+                }
+            }
+            const Frag<T> wf = pack_frag<T>(wt[0], wt[1]);
+#pragma unroll
+            for (int m = 0; m < NS; ++m)
+                if (16 * m < d.N) dC[m] = mma(col_frag(s.b, LDN, 32 * k, 16 * m, l16, g), wf, dC[m]);
+        }
+        if (has_h) {
+            const float f = __builtin_amdgcn_exp2f(mhi + mlo);
+#pragma unroll
+            for (int m = 0; m < NS; ++m) {
+                if (16 * m >= d.N) continue;
+                f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    if (q < ks)
+#pragma unroll
+                        for (int t = 0; t < kTerms<T>; ++t) o = mma(col_frag(s.plane[t], LDN, 32 * q, 16 * m, l16, g), gr[q], o);
+                o *= f;
+                dC[m] += o;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) rin += o[v] * Elem<T>::to_f32(s.c[me * LDN + 16 * m + 4 * g + v]);
+            }
+        }
+
+        // columns i, inside the chunk
+        f32x4 dx[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) dx[p] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < QS / 2; ++k) {
+            if (k < kw) continue;
+            f32x4 nt[2], wt[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int ts = 2 * k + u;
+                nt[u] = wt[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+                if (ts < wave) continue;
+                f32x4 z = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    if (q < ks) z = mma(row_frag(s.g + (16 * ts + l16) * LDP + 32 * q, g), xr[q], z);
+                const f32x4 th = *(const f32x4 *)(s.shi + 16 * ts + 4 * g), tl = *(const f32x4 *)(s.slo + 16 * ts + 4 * g);
+                const f32x4 cb = k == kw ? cbd[u] : cbp[k][u];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const float e = __builtin_amdgcn_exp2f((th[v] - mhi) + (tl[v] - mlo));
+                    const bool after = ts > wave || 4 * g + v > l16, same = ts == wave && 4 * g + v == l16;
+                    nt[u][v] = after || same ? cb[v] * e : 0.f;
+                    wt[u][v] = after || same ? z[v] * e * mdt : 0.f;
+                    qown += after ? nt[u][v] * z[v] : 0.f;
+                    qdiag += same ? nt[u][v] * z[v] : 0.f;
+                }
+            }
+            const Frag<T> nf = pack_frag<T>(nt[0], nt[1]), wf = pack_frag<T>(wt[0], wt[1]);
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+                if (p0 + 16 * p < d.P) dx[p] = mma(col_frag(s.g, LDP, 32 * k, 16 * p, l16, g), nf, dx[p]);
+#pragma unroll
+            for (int m = 0; m < NS; ++m)
+                if (16 * m < d.N) dB[m] = mma(col_frag(s.c, LDN, 32 * k, 16 * m, l16, g), wf, dB[m]);
+        }
+
+        // the gradient from later chunks, in the planes of h0
+        const float end = __builtin_amdgcn_exp2f(s.shi[Q - 1] + s.slo[Q - 1]);
+        const float f1 = __builtin_amdgcn_exp2f((s.shi[Q - 1] - mhi) + (s.slo[Q - 1] - mlo));
+        if (has_g) {
+            __syncthreads();
+            put_planes(af);
+            if (has_h) {
+#pragma unroll
+                for (int k = 0; k < decltype(af)::kCount; ++k)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) dot += __uint_as_float(hf.r[k][e]) * __uint_as_float(af.r[k][e]);
+            }
+            __syncthreads();
+        }
+        if (it + 1 < items) fetch(it + 1);
+        if (has_g) {
+            f32x4 o[4];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) o[p] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < NP / 32; ++k) {
+                if (32 * k >= d.N) continue;
+                const Frag<T> br = row_frag(s.b + me * LDN + 32 * k, g);
+#pragma unroll
+                for (int p = 0; p < 4; ++p)
+                    if (p0 + 16 * p < d.P)
+#pragma unroll
+                        for (int t = 0; t < kTerms<T>; ++t)
+                            o[p] = mma(row_frag(s.plane[t] + (16 * p + l16) * LDN + 32 * k, g), br, o[p]);
+            }
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                o[p] *= f1;
+                dx[p] += o[p];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) qend += o[p][v] * Elem<T>::to_f32(s.x[me * LDP + 16 * p + 4 * g + v]);
+            }
+#pragma unroll
+            for (int m = 0; m < NS; ++m) {
+                if (16 * m >= d.N) continue;
+                f32x4 w = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    if (q < ks) w = mma(col_frag(s.plane[0], LDN, 32 * q, 16 * m, l16, g), xr[q], w);
+                dB[m] += w * (f1 * mdt);
+            }
+        }
+        if (me < rows) {
+            const float skip = a.D[h];
+            T *o = grad_x + ((tok0 + me) * d.H + h) * d.P + p0;
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const int at = 16 * p + 4 * g;
+                if (p0 + at >= d.P) continue;
+                f32x4 r;
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    r[v] = me < n ? mdt * dx[p][v] + skip * Elem<T>::to_f32(s.g[me * LDP + at + v]) : 0.f;
+                store4<T>(o + at, r, d.P - p0 - at);
+            }
+        }
+        if (slab + 1 == slabs) {
+            rin = over_groups(rin);
+            rown = over_groups(rown);
+            qown = over_groups(qown);
+            qdiag = over_groups(qdiag);
+            qend = over_groups(qend);
+            dot = over_wave(dot);
+            zdiag = over_wave(zdiag);
+            if (g == 0) {
+                s.rin[me] = rin;
+                s.own[me] = rown - mdt * qown;
+                s.direct[me] = qown + qdiag + qend;
+                s.qend[me] = mdt * qend;
+                s.dt_done[me] = mdt;
+            }
+            if (lane == 0) {
+                s.dots[wave] = dot;
+                s.diag[wave] = zdiag;
+                if (wave == 0) s.end_done = end;
+            }
+            rin = rown = qown = qdiag = qend = dot = zdiag = 0.f;
+        }
+    }
+    __syncthreads();
+    if (wave == 0) finish_head(h1 - 1);
+
+    if (me < rows) {
+        const int64_t at = ((tok0 + me) * d.G + grp) * d.N;
+        const int64_t all = (int64_t)d.B * d.L * d.G * d.N;
+#pragma unroll
+        for (int m = 0; m < NS; ++m) {
+            const int k = 16 * m + 4 * g;
+            if (k >= d.N) continue;
+            if (a.part != nullptr) {
+                store4<float>(a.part + 2 * split * all + at + k, dB[m], d.N - k);
+                store4<float>(a.part + (2 * split + 1) * all + at + k, dC[m], d.N - k);
+            } else {
+                store4<T>(grad_B + at + k, dB[m], d.N - k);
+                store4<T>(grad_C + at + k, dC[m], d.N - k);
+            }
+        }
+    }
+}
+
+// grad_B and grad_C from the splits' parts (in their order), and the heads' sums over all
+// chunks (a wave a sum, in 64 bits).
+template <typename T>
+__global__ __launch_bounds__(256) void scan_bwd_sum_kernel(const float *__restrict__ part, int splits, int64_t all,
+                                                           T *__restrict__ grad_B, T *__restrict__ grad_C,
+                                                           const float *__restrict__ heads, int H, int64_t chunks,
+                                                           float *__restrict__ grad_A, float *__restrict__ grad_bias,
+                                                           float *__restrict__ grad_D, int64_t blocks_part) {
+    if (blockIdx.x < blocks_part) {
+        const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+        if (i >= 2 * all) return;
+        const int left = 2 * all - i < 4 ? (int)(2 * all - i) : 4;
+        f32x4 t = load4(part + i, left);
+        for (int s = 1; s < splits; ++s) t += load4(part + 2 * s * all + i, left);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < left) (i + e < all ? grad_B + i + e : grad_C + i + e - all)[0] = Elem<T>::from_f32(t[e]);
+        return;
+    }
+    const int64_t k = (blockIdx.x - blocks_part) * 4 + threadIdx.x / kWave;
+    if (k >= 3 * H) return;
+    double t = 0.;
+    for (int64_t c = threadIdx.x % kWave; c < chunks; c += kWave) t += heads[k * chunks + c];
+#pragma unroll
+    for (int m = 1; m < kWave; m *= 2) t += __shfl_xor(t, m, kWave);
+    if (threadIdx.x % kWave == 0) (k < H ? grad_A + k : k < 2 * H ? grad_bias + k - H : grad_D + k - 2 * H)[0] = (float)t;
+}
+
+namespace {
+
+struct BwdWork {
+    ChunkPlan plan;
+    int64_t adjoints, heads, part, total;
+};
+BwdWork bwd_work(int64_t B, int64_t L, int H, int P, int G, int N, int Q) {
+    const int64_t nc = (L + Q - 1) / Q;
+    BwdWork w;
+    w.plan = plan_heads(B, nc, H, G, 512);
+    w.adjoints = 0;
+    w.heads = pad64(B * H * nc * P * N);
+    w.part = w.heads + pad64(3 * H * B * nc);
+    w.total = w.part + (w.plan.splits > 1 ? pad64(2 * w.plan.splits * B * L * G * N) : 0);
+    return w;
+}
+
+template <typename T, int NP>
+hipError_t launch_main(const BwdArgs &k, int64_t blocks, const Scan &a, const void *grad, void *grad_x, void *grad_dt,
+                       void *grad_B, void *grad_C, hipStream_t stream) {
+    constexpr int bytes = sizeof(BwdLds<T, NP>);
+    static_assert(bytes <= 160 * 1024, "a workgroup's LDS");
+    auto kern = scan_bwd_kernel<T, NP>;
+    hipError_t e = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(64 * kStrips<T>), bytes, stream, k, (const T *)a.x,
+                       (const T *)a.Bm, (const T *)a.Cm, (const T *)grad, (T *)grad_x, (T *)grad_dt, (T *)grad_B,
+                       (T *)grad_C);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t scan_bwd(const Scan &a, const float *saved, const void *grad, int64_t g_batch, int64_t g_token,
+                    const float *grad_state, float *work, void *grad_x, void *grad_dt, float *grad_A, void *grad_B,
+                    void *grad_C, float *grad_D, float *grad_dt_bias, float *grad_initial, hipStream_t stream) {
+    constexpr int Q = 16 * kStrips<T>;
+    const ScanWork f = scan_work(a.B, a.L, a.H, a.P, a.N, Q);
+    const BwdWork w = bwd_work(a.B, a.L, a.H, a.P, a.G, a.N, Q);
+    float *sv = const_cast<float *>(saved);  // only read here
+    const ScanDims d = {(int)a.B, (int)a.L, a.H, a.P, a.G, a.N, f.nc, a.lengths, sv + f.dt, sv + f.shi, sv + f.slo};
+    const int64_t blocks = a.B * f.nc * a.G * w.plan.splits, all = a.B * a.L * a.G * a.N;
+    const int64_t blocks_part = w.plan.splits > 1 ? (2 * all + 1023) / 1024 : 0, blocks_sum = blocks_part + (3 * a.H + 3) / 4;
+    if (blocks > 0x7fffffff || blocks_sum > 0x7fffffff) return hipErrorInvalidConfiguration;
+    float *adjoints = nullptr;
+    hipError_t e = hipSuccess;
+    if (f.nc > 1 || grad_state != nullptr || grad_initial != nullptr) {
+        adjoints = work + w.adjoints;
+        e = launch_scan_states<T>(d, (const T *)grad, g_batch, g_token, (const T *)a.Cm, a.c_batch, a.c_token, adjoints,
+                                  true, stream);
+        if (e == hipSuccess) e = launch_scan_pass(d, adjoints, grad_state, grad_initial, Q, true, stream);
+    }
+    if (e != hipSuccess) return e;
+    const BwdArgs k = {d, w.plan, a.x_batch, a.x_token, a.b_batch, a.b_token, a.c_batch, a.c_token, g_batch, g_token,
+                       saved + f.states, adjoints, a.A, a.D, w.plan.splits > 1 ? work + w.part : nullptr, work + w.heads,
+                       a.initial != nullptr, grad_state != nullptr};
+    e = a.N <= 64 ? launch_main<T, 64>(k, blocks, a, grad, grad_x, grad_dt, grad_B, grad_C, stream)
+                  : launch_main<T, 128>(k, blocks, a, grad, grad_x, grad_dt, grad_B, grad_C, stream);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((scan_bwd_sum_kernel<T>), dim3((unsigned)blocks_sum), dim3(256), 0, stream, k.part,
+                       w.plan.splits, all, (T *)grad_B, (T *)grad_C, k.heads, a.H, a.B * f.nc, grad_A, grad_dt_bias,
+                       grad_D, blocks_part);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t scan_bwd_floats(int64_t B, int64_t L, int H, int P, int G, int N, bool bf16) {
+    return bwd_work(B, L, H, P, G, N, scan_chunk(bf16)).total;
+}
+
+hipError_t launch_scan_bwd(const Scan &a, const float *saved, const void *grad, int64_t g_batch, int64_t g_token,
+                           const float *grad_state, float *work, void *grad_x, void *grad_dt, float *grad_A,
+                           void *grad_B, void *grad_C, float *grad_D, float *grad_dt_bias, float *grad_initial,
+                           bool bf16, hipStream_t stream) {
+    return bf16 ? scan_bwd<bf16_t>(a, saved, grad, g_batch, g_token, grad_state, work, grad_x, grad_dt, grad_A, grad_B,
+                                   grad_C, grad_D, grad_dt_bias, grad_initial, stream)
+                : scan_bwd<float>(a, saved, grad, g_batch, g_token, grad_state, work, grad_x, grad_dt, grad_A, grad_B,
+                                  grad_C, grad_D, grad_dt_bias, grad_initial, stream);
+}
+
+}  // namespace seq
+}  // namespace ddpm

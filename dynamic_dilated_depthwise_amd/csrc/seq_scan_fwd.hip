@@ -1,0 +1,388 @@
+// seq_scan_fwd.hip -- the selective scan over whole sequences: times and outputs of the
+// chunks (seq_scan.hpp has the formulas), and the single-token step.
+#include "seq_scan.hpp"
+
+namespace ddpm {
+namespace seq {
+
+constexpr int kThreads = 256;
+constexpr int kTimeHeads = 16;
+constexpr double kLog2e = 1.4426950408889634;
+
+// dt and the running sums s of a chunk, 16 heads a workgroup (dt's rows lie token by
+// token in memory, what comes out head by head); a wave a head, 64-bit sums.  A token past
+// the sequence's length has dt = 0: it leaves the state alone.  A step's decay is bounded
+// to 2^-2000 and 2^2000, beyond which float32 has only 0 and infinity, so that s stays
+// finite.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void scan_times_kernel(ScanDims d, const T *__restrict__ raw, int64_t batch,
+                                                              int64_t token, const float *__restrict__ A,
+                                                              const float *__restrict__ bias, int blocks_h) {
+    constexpr int Q = 16 * kStrips<T>, PER = Q / kWave;
+    __shared__ float tile[kTimeHeads][Q + 1];
+    const int h0 = blockIdx.x % blocks_h * kTimeHeads, c = blockIdx.x / blocks_h % d.nc, b = blockIdx.x / blocks_h / d.nc;
+    const int n = valid_tokens(d.lengths, b, d.L) - c * Q;
+    for (int i = threadIdx.x; i < Q * kTimeHeads; i += kThreads) {
+        const int t = i / kTimeHeads, h = h0 + i % kTimeHeads;
+        float v = 0.f;
+        if (t < n && h < d.H) v = softplus(Elem<T>::to_f32(raw[b * batch + (int64_t)(c * Q + t) * token + h]) + bias[h]);
+        tile[i % kTimeHeads][t] = v;
+    }
+    __syncthreads();
+    const int lane = threadIdx.x % kWave;
+    for (int k = threadIdx.x / kWave; k < kTimeHeads && h0 + k < d.H; k += kThreads / kWave) {
+        const double a = A[h0 + k] * kLog2e;
+        const int64_t at = ((int64_t)(b * d.H + h0 + k) * d.nc + c) * Q + lane * PER;
+        double s[PER], run = 0.;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            const float v = tile[k][lane * PER + e];
+            d.dt[at + e] = v;
+            run += fmin(fmax(v * a, -2000.), 2000.);
+            s[e] = run;
+        }
+        double before = run;
+#pragma unroll
+        for (int m = 1; m < kWave; m *= 2) {
+            const double o = __shfl_up(before, m, kWave);
+            if (lane >= m) before += o;
+        }
+        before -= run;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            const float hi = (float)(before + s[e]);
+            d.shi[at + e] = hi;
+            d.slo[at + e] = (float)(before + s[e] - hi);
+        }
+    }
+}
+
+// Eight elements of a row of global memory in a fragment's order; columns past N are zero.
+template <typename T>
+__device__ __forceinline__ Frag<T> global_row_frag(const T *__restrict__ row, int k0, int g, int N, bool on) {
+    Frag<T> r;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int k = k0 + (e < 4 ? 4 * g + e : 12 + 4 * g + e);
+        const float v = on && k < N ? Elem<T>::to_f32(row[k]) : 0.f;
+        if constexpr (Elem<T>::is_bf16) r[e] = (__bf16)v;
+        else r.v[e] = v;
+    }
+    return r;
+}
+
+struct OutArgs {
+    ScanDims d;
+    ChunkPlan plan;
+    int64_t x_batch, x_token, b_batch, b_token, c_batch, c_token;
+    const float *states;   // [B, H, nc, P, N]: the state that enters each chunk; or null (one chunk)
+    const float *initial;  // [B, H, P, N] or null
+    const float *D;
+};
+
+// y of a chunk for some heads of a group.  C . B is theirs together and stays in registers
+// (transposed: rows i, columns t); each head scales it by its decays, which makes it the
+// operand that x is multiplied by.  A wave has rows t of strips w and 7 - w (bfloat16), so
+// that the four waves have the same share of the triangle i <= t.  The scaled C . B and the
+// entering state are rounded to bfloat16 once, as the operands of matrix products whose sums
+// are float32; y is rounded to bfloat16 at the end by as much.
+template <typename T, int NP>
+__global__ __launch_bounds__(kThreads) void scan_out_kernel(OutArgs a, const T *__restrict__ X, const T *__restrict__ Bm,
+                                                            const T *__restrict__ Cm, T *__restrict__ y) {
+    constexpr int QS = kStrips<T>, Q = 16 * QS, SPW = QS / 4;
+    constexpr int LDN = ld_of<T>(NP), LDP = ld_of<T>(kSlab);
+    constexpr int kTiles = Q * LDP + kSlab * LDN;
+    __shared__ __align__(16) T lds[kTiles > Q * LDN ? kTiles : Q * LDN];
+    __shared__ __align__(16) float shi[Q], slo[Q], dts[Q];
+    T *xtile = lds, *htile = lds + Q * LDP;
+    const ScanDims &d = a.d;
+    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, l16 = lane % 16, g = lane / 16;
+    int id = blockIdx.x;
+    const int split = id % a.plan.splits;
+    id /= a.plan.splits;
+    const int grp = id % d.G;
+    id /= d.G;
+    const int c = id % d.nc, b = id / d.nc;
+    const int rows = d.L - c * Q < Q ? d.L - c * Q : Q;  // rows of y
+    int n = valid_tokens(d.lengths, b, d.L) - c * Q;
+    n = n < 0 ? 0 : n > Q ? Q : n;
+    const int hg = d.H / d.G, h0 = grp * hg + split * a.plan.per;
+    const int h1 = h0 + a.plan.per < (grp + 1) * hg ? h0 + a.plan.per : (grp + 1) * hg;
+    const int slabs = (d.P + kSlab - 1) / kSlab, items = (h1 - h0) * slabs;
+    const T *xb = X + b * a.x_batch + (int64_t)c * Q * a.x_token;
+    const bool has_h = n > 0 && (c > 0 || a.initial != nullptr);
+
+    // C of the wave's rows, and C . B for every i <= t
+    Frag<T> cf[SPW][NP / 32];
+    f32x4 cb[SPW][QS];
+    {
+        TileFetch<T, Q, NP, kThreads> bf;
+        bf.fetch(Bm + b * a.b_batch + (int64_t)c * Q * a.b_token + grp * d.N, a.b_token, n, d.N, tid);
+        bf.put(lds, tid);
+        const T *cp = Cm + b * a.c_batch + (int64_t)c * Q * a.c_token + grp * d.N;
+#pragma unroll
+        for (int j = 0; j < SPW; ++j) {
+            const int t = 16 * (j == 0 ? wave : QS - 1 - wave) + l16;
+#pragma unroll
+            for (int k = 0; k < NP / 32; ++k)
+                cf[j][k] = global_row_frag<T>(cp + (t < n ? t : 0) * a.c_token, 32 * k, g, d.N, t < n);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < SPW; ++j) {
+            const int ts = j == 0 ? wave : QS - 1 - wave;
+#pragma unroll
+            for (int i = 0; i < (SPW == 2 && j == 0 ? QS / 2 : QS); ++i) {
+                cb[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+                if (i > ts) continue;
+#pragma unroll
+                for (int k = 0; k < NP / 32; ++k)
+                    if (32 * k < d.N) cb[j][i] = mma(row_frag(lds + (16 * i + l16) * LDN + 32 * k, g), cf[j][k], cb[j][i]);
+            }
+        }
+    }
+
+    TileFetch<T, Q, kSlab, kThreads> xf;
+    TileFetch<float, kSlab, NP, kThreads> hf;
+    float tf[3];
+    auto fetch = [&](int it) {
+        const int h = h0 + it / slabs, p0 = it % slabs * kSlab;
+        xf.fetch(xb + (int64_t)h * d.P + p0, a.x_token, n, d.P - p0, tid);
+        if (has_h) {
+            const int64_t head = (int64_t)b * d.H + h;
+            const float *src = a.states != nullptr ? a.states + (head * d.nc + c) * d.P * d.N : a.initial + head * d.P * d.N;
+            hf.fetch(src + (int64_t)p0 * d.N, d.N, d.P - p0, d.N, tid);
+        }
+        if (tid < Q) {
+            const int64_t at = ((int64_t)(b * d.H + h) * d.nc + c) * Q + tid;
+            tf[0] = d.shi[at];
+            tf[1] = d.slo[at];
+            tf[2] = d.dt[at];
+        }
+    };
+    fetch(0);
+    for (int it = 0; it < items; ++it) {
+        const int h = h0 + it / slabs, p0 = it % slabs * kSlab;
+        __syncthreads();
+        xf.put(xtile, tid);
+        if (has_h) {
+#pragma unroll
+            for (int k = 0; k < decltype(hf)::kCount; ++k) {
+                const int i = tid + k * kThreads, row = i / (NP / 4), col = i % (NP / 4) * 4;
+                float v[4];
+                widen<float>(hf.r[k], v);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) htile[row * LDN + col + e] = Elem<T>::from_f32(v[e]);
+            }
+        }
+        if (tid < Q) {
+            shi[tid] = tf[0];
+            slo[tid] = tf[1];
+            dts[tid] = tf[2];
+        }
+        __syncthreads();
+        if (it + 1 < items) fetch(it + 1);
+        const float skip = a.D[h];
+#pragma unroll
+        for (int j = 0; j < SPW; ++j) {
+            const int ts = j == 0 ? wave : QS - 1 - wave, t = 16 * ts + l16;
+            if (16 * ts >= rows) continue;
+            f32x4 acc[4];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) acc[p] = f32x4{0.f, 0.f, 0.f, 0.f};
+            const float th = shi[t], tl = slo[t];
+            if (has_h) {
+#pragma unroll
+                for (int k = 0; k < NP / 32; ++k) {
+                    if (32 * k >= d.N) continue;
+#pragma unroll
+                    for (int p = 0; p < 4; ++p)
+                        if (p0 + 16 * p < d.P)
+                            acc[p] = mma(row_frag(htile + (16 * p + l16) * LDN + 32 * k, g), cf[j][k], acc[p]);
+                }
+                const float f = __builtin_amdgcn_exp2f(th + tl);
+#pragma unroll
+                for (int p = 0; p < 4; ++p) acc[p] *= f;
+            }
+#pragma unroll
+            for (int i = 0; i < (SPW == 2 && j == 0 ? QS / 4 : QS / 2); ++i) {
+                if (2 * i > ts) continue;
+                f32x4 m[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int is = 2 * i + u;
+                    m[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    if (is > ts) continue;
+                    const f32x4 ih = *(const f32x4 *)(shi + 16 * is + 4 * g), il = *(const f32x4 *)(slo + 16 * is + 4 * g);
+                    const f32x4 id4 = *(const f32x4 *)(dts + 16 * is + 4 * g);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        const float e = __builtin_amdgcn_exp2f((th - ih[v]) + (tl - il[v])) * id4[v];
+                        m[u][v] = is < ts || 4 * g + v <= l16 ? cb[j][is][v] * e : 0.f;
+                    }
+                }
+                const Frag<T> mf = pack_frag<T>(m[0], m[1]);
+#pragma unroll
+                for (int p = 0; p < 4; ++p)
+                    if (p0 + 16 * p < d.P) acc[p] = mma(col_frag(xtile, LDP, 32 * i, 16 * p, l16, g), mf, acc[p]);
+            }
+            if (t >= rows) continue;
+            T *yr = y + (((int64_t)b * d.L + c * Q + t) * d.H + h) * d.P + p0;
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const int at = 16 * p + 4 * g;
+                if (p0 + at >= d.P) continue;
+                f32x4 o;
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    o[v] = t < n ? acc[p][v] + skip * Elem<T>::to_f32(xtile[t * LDP + at + v]) : 0.f;
+                store4<T>(yr + at, o, d.P - p0 - at);
+            }
+        }
+    }
+}
+
+// One token of each sequence.  The state's traffic is everything (8 bytes and 5 operations
+// an element); LN lanes hold a row of N, V elements each, UNROLL rows a thread at once.  A
+// slot outside [0, S) is a place without a sequence: y is zero and no state is touched.
+template <typename T, int V, int UNROLL>
+__global__ __launch_bounds__(kThreads) void scan_step_kernel(Scan a, float *__restrict__ state,
+                                                             const int *__restrict__ slots, int64_t S,
+                                                             T *__restrict__ y, int ln, int blocks_p) {
+    const int bp = blockIdx.x % blocks_p;
+    const int64_t bh = blockIdx.x / blocks_p;
+    const int h = (int)(bh % a.H);
+    const int64_t b = bh / a.H;
+    const int lane = threadIdx.x % ln, rows = kThreads / ln, r0 = bp * rows * UNROLL + threadIdx.x / ln;
+    const int64_t slot = slots != nullptr ? slots[b] : b;
+    const bool on = slot >= 0 && slot < S;
+    const T *xr = (const T *)a.x + b * a.x_batch + (int64_t)h * a.P;
+    T *yr = y + bh * a.P;
+    if (!on) {
+        for (int k = 0; k < UNROLL; ++k)
+            if (lane == 0 && r0 + k * rows < a.P) yr[r0 + k * rows] = Elem<T>::from_f32(0.f);
+        return;
+    }
+    const int grp = h / (a.H / a.G);
+    const T *Bv = (const T *)a.Bm + b * a.b_batch + (int64_t)grp * a.N, *Cv = (const T *)a.Cm + b * a.c_batch + (int64_t)grp * a.N;
+    float *st = state + (slot * a.H + h) * a.P * a.N;
+    const float dt = softplus(Elem<T>::to_f32(((const T *)a.dt)[b * a.dt_batch + h]) + a.dt_bias[h]);
+    const float decay = expf(dt * a.A[h]), skip = a.D[h];
+    float sum[UNROLL], xv[UNROLL];
+#pragma unroll
+    for (int k = 0; k < UNROLL; ++k) {
+        sum[k] = 0.f;
+        xv[k] = r0 + k * rows < a.P ? Elem<T>::to_f32(xr[r0 + k * rows]) : 0.f;
+    }
+    for (int n = lane * V; n < a.N; n += ln * V) {  // one turn for N up to 64 V
+        typedef float vec __attribute__((ext_vector_type(V), aligned(4)));
+        vec v[UNROLL];
+#pragma unroll
+        for (int k = 0; k < UNROLL; ++k)
+            if (r0 + k * rows < a.P) v[k] = *(const vec *)(st + (int64_t)(r0 + k * rows) * a.N + n);
+        float bv[V], cv[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            bv[e] = dt * Elem<T>::to_f32(Bv[n + e]);
+            cv[e] = Elem<T>::to_f32(Cv[n + e]);
+        }
+#pragma unroll
+        for (int k = 0; k < UNROLL; ++k) {
+            if (r0 + k * rows >= a.P) continue;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                v[k][e] = decay * v[k][e] + xv[k] * bv[e];
+                sum[k] += v[k][e] * cv[e];
+            }
+            *(vec *)(st + (int64_t)(r0 + k * rows) * a.N + n) = v[k];
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < UNROLL; ++k) {
+        for (int m = 1; m < ln; m *= 2) sum[k] += __shfl_xor(sum[k], m, kWave);
+        if (lane == 0 && r0 + k * rows < a.P) yr[r0 + k * rows] = Elem<T>::from_f32(sum[k] + skip * xv[k]);
+    }
+}
+
+namespace {
+
+template <typename T>
+hipError_t scan_fwd(const Scan &a, float *work, void *y, float *final_state, bool save, hipStream_t stream) {
+    constexpr int Q = 16 * kStrips<T>;
+    const ScanWork w = scan_work(a.B, a.L, a.H, a.P, a.N, Q);
+    const ScanDims d = {(int)a.B, (int)a.L, a.H, a.P, a.G, a.N, w.nc, a.lengths, work + w.dt, work + w.shi, work + w.slo};
+    const int blocks_h = (a.H + kTimeHeads - 1) / kTimeHeads;
+    const ChunkPlan plan = plan_heads(a.B, w.nc, a.H, a.G, 1024);
+    const int64_t bt = a.B * w.nc * blocks_h, bo = a.B * w.nc * a.G * plan.splits;
+    if (bt > 0x7fffffff || bo > 0x7fffffff) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((scan_times_kernel<T>), dim3((unsigned)bt), dim3(kThreads), 0, stream, d, (const T *)a.dt, a.dt_batch,
+                       a.dt_token, a.A, a.dt_bias, blocks_h);
+    hipError_t e = hipGetLastError();
+    float *states = nullptr;
+    if (e == hipSuccess && (w.nc > 1 || final_state != nullptr || save)) {
+        states = work + w.states;
+        e = launch_scan_states<T>(d, (const T *)a.x, a.x_batch, a.x_token, (const T *)a.Bm, a.b_batch, a.b_token, states,
+                                  false, stream);
+        if (e == hipSuccess) e = launch_scan_pass(d, states, a.initial, final_state, Q, false, stream);
+    }
+    if (e != hipSuccess) return e;
+    const OutArgs o = {d, plan, a.x_batch, a.x_token, a.b_batch, a.b_token, a.c_batch, a.c_token, states, a.initial, a.D};
+    if (a.N <= 64)
+        hipLaunchKernelGGL((scan_out_kernel<T, 64>), dim3((unsigned)bo), dim3(kThreads), 0, stream, o, (const T *)a.x,
+                           (const T *)a.Bm, (const T *)a.Cm, (T *)y);
+    else
+        hipLaunchKernelGGL((scan_out_kernel<T, 128>), dim3((unsigned)bo), dim3(kThreads), 0, stream, o, (const T *)a.x,
+                           (const T *)a.Bm, (const T *)a.Cm, (T *)y);
+    return hipGetLastError();
+}
+
+template <typename T, int V>
+hipError_t scan_step(const Scan &a, float *state, const int *slots, int64_t S, void *y, hipStream_t stream) {
+    int ln = 1;
+    while (ln < kWave && ln * V < a.N) ln *= 2;
+    // rows at once: as many as still leave two workgroups a compute unit
+    const int rows = kThreads / ln;
+    int unroll = 8;
+    while (unroll > 1 && (a.P <= rows * (unroll / 2) || a.B * a.H * ((a.P + rows * unroll - 1) / (rows * unroll)) < 512))
+        unroll /= 2;
+    const int blocks_p = (a.P + rows * unroll - 1) / (rows * unroll);
+    const int64_t blocks = a.B * a.H * blocks_p;
+    if (blocks > 0x7fffffff) return hipErrorInvalidConfiguration;
+#define X(U)                                                                                                           \
+    if (unroll == U)                                                                                                   \
+        hipLaunchKernelGGL((scan_step_kernel<T, V, U>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, a, state,   \
+                           slots, S, (T *)y, ln, blocks_p);
+    X(1) X(2) X(4) X(8)
+#undef X
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t scan_step(const Scan &a, float *state, const int *slots, int64_t S, void *y, hipStream_t stream) {
+    if (a.N % 4 == 0) return scan_step<T, 4>(a, state, slots, S, y, stream);
+    if (a.N % 2 == 0) return scan_step<T, 2>(a, state, slots, S, y, stream);
+    return scan_step<T, 1>(a, state, slots, S, y, stream);
+}
+
+}  // namespace
+
+int scan_chunk(bool bf16) { return 16 * (bf16 ? kStrips<bf16_t> : kStrips<float>); }
+
+int64_t scan_fwd_floats(int64_t B, int64_t L, int H, int P, int G, int N, bool bf16) {
+    (void)G;
+    return scan_work(B, L, H, P, N, scan_chunk(bf16)).total;
+}
+
+hipError_t launch_scan_fwd(const Scan &a, float *work, void *y, float *final_state, bool save, bool bf16,
+                           hipStream_t stream) {
+    return bf16 ? scan_fwd<bf16_t>(a, work, y, final_state, save, stream)
+                : scan_fwd<float>(a, work, y, final_state, save, stream);
+}
+
+hipError_t launch_scan_step(const Scan &a, float *state, const int *slots, int64_t S, void *y, bool bf16,
+                            hipStream_t stream) {
+    return bf16 ? scan_step<bf16_t>(a, state, slots, S, y, stream) : scan_step<float>(a, state, slots, S, y, stream);
+}
+
+}  // namespace seq
+}  // namespace ddpm
