@@ -111,6 +111,10 @@ __device__ __forceinline__ f32x4 load4(const float *__restrict__ p, int n) {
     return v;
 }
 
+// The wave's number in its workgroup, as a scalar: branches on it are then branches and not
+// masks (left in a vector register it costs the scan's kernels a factor of two and more).
+__device__ __forceinline__ int wave_of(int tid) { return __builtin_amdgcn_readfirstlane(tid / kWave); }
+
 // softplus and its derivative, in the form that neither overflows nor cancels.
 __device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
 __device__ __forceinline__ float sigmoid(float v) {
@@ -201,8 +205,10 @@ template <typename T> constexpr int kTerms = Elem<T>::is_bf16 ? 3 : 1;
 
 // A tile of ROWS token rows by COLS columns (of which ncols hold data), fetched into
 // registers and put into LDS later, so that the fetch runs behind other work.  Rows past
-// `rows` and columns past `ncols` read as zero and are not touched in memory.
-template <typename T, int ROWS, int COLS, int THREADS>
+// `rows` and columns past `ncols` read as zero and are not touched in memory.  WHOLE: ncols
+// is a multiple of the vector, so a vector is there or not; those that are not are read at
+// `base` (which must be readable) and dropped, with no branch.
+template <typename T, int ROWS, int COLS, int THREADS, bool WHOLE>
 struct TileFetch {
     static constexpr int kPerRow = COLS / kVec<T>;
     static constexpr int kCount = ROWS * kPerRow / THREADS;
@@ -212,7 +218,13 @@ struct TileFetch {
 #pragma unroll
         for (int k = 0; k < kCount; ++k) {
             const int i = tid + k * THREADS, row = i / kPerRow, c = (i % kPerRow) * kVec<T>;
-            r[k] = load_vec<T>(base + row * stride + c, row < rows ? ncols - c : 0);
+            if constexpr (WHOLE) {
+                const bool on = row < rows && c < ncols;
+                const u32x4 v = *(const u32x4_a2 *)(base + (on ? row * stride + c : 0));
+                r[k] = on ? v : u32x4{0, 0, 0, 0};
+            } else {
+                r[k] = load_vec<T>(base + row * stride + c, row < rows ? ncols - c : 0);
+            }
         }
     }
     __device__ __forceinline__ void put(T *tile, int tid) const {

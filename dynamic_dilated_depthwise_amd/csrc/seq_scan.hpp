@@ -40,7 +40,12 @@ struct ScanDims {
     int B, L, H, P, G, N, nc;  // nc: chunks
     const int *lengths;
     float *dt, *shi, *slo;  // [B, H, nc * Q]
+    float *decay;           // [B, H, nc]: exp of each chunk's whole sum
 };
+
+// Rows of N of the states in the workspaces start at multiples of four: [P, state_cols(N)],
+// zeros behind N.
+__host__ __device__ constexpr int state_cols(int N) { return (N + 3) / 4 * 4; }
 
 struct ChunkPlan {
     int per, splits;  // heads of a workgroup; workgroups that share a chunk and a group
@@ -68,7 +73,7 @@ inline int64_t pad64(int64_t n) { return (n + 63) / 64 * 64; }
 // Sections of the forward's workspace, which the backward reads again.
 struct ScanWork {
     int nc;
-    int64_t times, dt, shi, slo, states, total;
+    int64_t times, dt, shi, slo, decay, states, total;
 };
 inline ScanWork scan_work(int64_t B, int64_t L, int H, int P, int N, int Q) {
     ScanWork w;
@@ -77,18 +82,30 @@ inline ScanWork scan_work(int64_t B, int64_t L, int H, int P, int N, int Q) {
     w.dt = 0;
     w.shi = w.times;
     w.slo = 2 * w.times;
-    w.states = 3 * w.times;
-    w.total = w.states + pad64(B * H * w.nc * (int64_t)P * N);
+    w.decay = 3 * w.times;
+    w.states = w.decay + pad64(B * H * w.nc);
+    w.total = w.states + pad64(B * H * w.nc * (int64_t)P * state_cols(N));
     return w;
 }
 
-// The chunks' own parts of the state (reverse: of the adjoint) into out [B, H, nc, P, N].
+// The chunks' own parts of the state (reverse: of the adjoint) into out [B, H, nc, P, cols].
 template <typename T>
 hipError_t launch_scan_states(const ScanDims &d, const T *X, int64_t x_batch, int64_t x_token, const T *Y,
                               int64_t y_batch, int64_t y_token, float *out, bool reverse, hipStream_t stream);
 // The recurrence over the chunks, in place; first / final [B, H, P, N] or null.
 hipError_t launch_scan_pass(const ScanDims &d, float *states, const float *first, float *final_state, int Q,
                             bool reverse, hipStream_t stream);
+
+// Runs X(NP, WHOLE) for the padded columns of the state and for P in whole vectors or not.
+#define DDPM_SEQ_SCAN_SHAPES(T, N, P, X)             \
+    if ((P) % kVec<T> == 0) {                        \
+        if ((N) <= 32) X(32, true)                   \
+        else if ((N) <= 64) X(64, true)              \
+        else X(128, true)                            \
+    } else {                                         \
+        if ((N) <= 64) X(64, false)                  \
+        else X(128, false)                           \
+    }
 
 }  // namespace seq
 }  // namespace ddpm

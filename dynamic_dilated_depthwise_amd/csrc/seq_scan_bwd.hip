@@ -17,7 +17,9 @@
 //          + sum_{k >= t} (r_own[k] - q_own[k]),
 //
 // where q_end is q's part through g1, r_in r's part through h0, and r_own, q_own the parts
-// inside the chunk without their common diagonal (which would only cancel).  Then
+// inside the chunk.  What r_own and q_own share, the diagonal and the pairs after t,
+// cancels: both add the very same float32 products, in 64 bits, so that no more than the
+// other products' own roundings is left.  Then
 // grad_dt = (q / dt + A e) sigmoid(raw + dt_bias) and grad_A = sum_t dt e.  These are sums
 // of many terms of both signs, so every factor keeps float32's precision: Z and CB come
 // from products of the inputs themselves, and h0 and g1 enter as three bfloat16 terms.
@@ -32,7 +34,7 @@ struct BwdArgs {
     ScanDims d;
     ChunkPlan plan;
     int64_t x_batch, x_token, b_batch, b_token, c_batch, c_token, g_batch, g_token;
-    const float *states, *adjoints;  // [B, H, nc, P, N]; adjoints null: nothing reaches the only chunk's end
+    const float *states, *adjoints;  // [B, H, nc, P, cols]; adjoints null: nothing reaches the only chunk's end
     const float *A, *D;
     float *part;   // [splits, 2, B, L, G, N] or null (one split: grad_B and grad_C at once)
     float *heads;  // [3, H, B * nc]: every chunk's part of grad_A, grad_dt_bias, grad_D
@@ -45,12 +47,15 @@ struct BwdLds {
     T b[Q * LDN], c[Q * LDN], x[Q * LDP], g[Q * LDP];
     T plane[kTerms<T>][kSlab * LDN];  // h0, then g1
     float shi[Q], slo[Q], dt[Q];
-    float rin[Q], own[Q], direct[Q], qend[Q], dt_done[Q];  // of the head before, for the sums over its tokens
+    // of the head before, for the sums over its tokens
+    double own[Q];
+    float rin[Q], direct[Q], qend[Q], dt_done[Q];
     float dots[QS], diag[QS], end_done, pad[7];
 };
 
 // Sum over the four lane groups that hold a column's rows.
-__device__ __forceinline__ float over_groups(float v) {
+template <typename V>
+__device__ __forceinline__ V over_groups(V v) {
     v += __shfl_xor(v, 16, kWave);
     return v + __shfl_xor(v, 32, kWave);
 }
@@ -60,10 +65,13 @@ __device__ __forceinline__ float over_wave(float v) {
     return v;
 }
 
+__device__ __forceinline__ float frag_at(const bf16x8 &f, int e) { return (float)f[e]; }
+__device__ __forceinline__ float frag_at(const FragF &f, int e) { return f.v[e]; }
+
 // One chunk, some heads of a group.  Wave w has strip w of the chunk's tokens both as rows t
 // (grad_C, r) and as columns i (grad_x, grad_B, q): w + 1 tiles of the triangle as rows and
 // QS - w as columns, the same for every wave.
-template <typename T, int NP>
+template <typename T, int NP, bool WHOLE>
 __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, const T *__restrict__ X,
                                                                    const T *__restrict__ Bm, const T *__restrict__ Cm,
                                                                    const T *__restrict__ grad, T *__restrict__ grad_x,
@@ -74,7 +82,7 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
     extern __shared__ __align__(16) char raw_lds[];
     Lds &s = *(Lds *)raw_lds;
     const ScanDims &d = a.d;
-    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, l16 = lane % 16, g = lane / 16;
+    const int tid = threadIdx.x, lane = tid % kWave, wave = wave_of(tid), l16 = lane % 16, g = lane / 16;
     int id = blockIdx.x;
     const int split = id % a.plan.splits;
     id /= a.plan.splits;
@@ -87,7 +95,7 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
     n = n < 0 ? 0 : n > Q ? Q : n;
     const int hg = d.H / d.G, h0 = grp * hg + split * a.plan.per;
     const int h1 = h0 + a.plan.per < (grp + 1) * hg ? h0 + a.plan.per : (grp + 1) * hg;
-    const int slabs = (d.P + kSlab - 1) / kSlab, items = (h1 - h0) * slabs;
+    const int slabs = (d.P + kSlab - 1) / kSlab, items = (h1 - h0) * slabs, cols = state_cols(d.N);
     const int64_t tok0 = (int64_t)b * d.L + c * Q;  // first token's row in the contiguous outputs
     const bool has_h = n > 0 && (c > 0 || a.has_first), has_g = (c + 1) * Q < len || (a.has_last && n > 0);
     const T *xb = X + b * a.x_batch + (int64_t)c * Q * a.x_token;
@@ -95,15 +103,22 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
     const int me = 16 * wave + l16;  // this lane's token, as a row t and as a column i
     const int kw = wave / 2;
 
-    TileFetch<T, Q, kSlab, THREADS> xf, gf;
-    TileFetch<float, kSlab, NP, THREADS> hf, af;
+    float upto[4], from[4];  // masks of the diagonal tile: rows i up to column t, rows t from column i on
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+        upto[v] = 4 * g + v <= l16 ? 0.f : -INFINITY;
+        from[v] = 4 * g + v >= l16 ? 0.f : -INFINITY;
+    }
+
+    TileFetch<T, Q, kSlab, THREADS, WHOLE> xf, gf;
+    TileFetch<float, kSlab, NP, THREADS, true> hf, af;
     float tf[3];
     auto fetch = [&](int it) {
         const int h = h0 + it / slabs, p0 = it % slabs * kSlab;
         xf.fetch(xb + (int64_t)h * d.P + p0, a.x_token, n, d.P - p0, tid);
         gf.fetch(gb + (int64_t)h * d.P + p0, a.g_token, n, d.P - p0, tid);
         const int64_t chunk = ((int64_t)b * d.H + h) * d.nc + c;
-        if (has_h) hf.fetch(a.states + chunk * d.P * d.N + (int64_t)p0 * d.N, d.N, d.P - p0, d.N, tid);
+        if (has_h) hf.fetch(a.states + (chunk * d.P + p0) * cols, cols, d.P - p0, cols, tid);
         if (tid < Q) {
             tf[0] = d.shi[chunk * Q + tid];
             tf[1] = d.slo[chunk * Q + tid];
@@ -111,9 +126,9 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
         }
     };
     // a float32 tile into the planes
-    auto put_planes = [&](const TileFetch<float, kSlab, NP, THREADS> &f) {
+    auto put_planes = [&](const decltype(hf) &f) {
 #pragma unroll
-        for (int k = 0; k < TileFetch<float, kSlab, NP, THREADS>::kCount; ++k) {
+        for (int k = 0; k < decltype(hf)::kCount; ++k) {
             const int i = tid + k * THREADS, at = i / (NP / 4) * LDN + i % (NP / 4) * 4;
             float v[4];
             widen<float>(f.r[k], v);
@@ -143,7 +158,8 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
             dot += s.dots[w];
             diag += s.diag[w];
         }
-        float pre[PER], suf[PER], before = 0.f, after = 0.f;
+        float pre[PER], before = 0.f;
+        double suf[PER], after = 0.;
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
             pre[e] = before;
@@ -151,13 +167,15 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
         }
 #pragma unroll
         for (int e = PER - 1; e >= 0; --e) {
-            after += s.rin[lane * PER + e] + s.own[lane * PER + e];
+            after += s.own[lane * PER + e] + s.rin[lane * PER + e];
             suf[e] = after;
         }
-        float up = before, down = after;
+        float up = before;
+        double down = after;
 #pragma unroll
         for (int m = 1; m < kWave; m *= 2) {
-            const float u = __shfl_up(up, m, kWave), o = __shfl_down(down, m, kWave);
+            const float u = __shfl_up(up, m, kWave);
+            const double o = __shfl_down(down, m, kWave);
             if (lane >= m) up += u;
             if (lane + m < kWave) down += o;
         }
@@ -168,7 +186,7 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
             const int t = lane * PER + e;
-            const float dt = s.dt_done[t], flow = s.end_done * dot + (up + pre[e]) + (down + suf[e]);
+            const float dt = s.dt_done[t], flow = s.end_done * dot + (up + pre[e]) + (float)(down + suf[e]);
             // softplus's derivative from its value: 1 - exp(-dt)
             const float raw = t < n ? (s.direct[t] + A * flow) * -expm1f(-dt) : 0.f;
             sum_a += t < n ? dt * flow : 0.f;
@@ -189,7 +207,7 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
     // pairs of strips up to its own, columns i of it (D[t][i]) from its own on.
     f32x4 cbp[QS / 2][2], cbd[2];
     {
-        TileFetch<T, Q, NP, THREADS> bf, cf;
+        TileFetch<T, Q, NP, THREADS, false> bf, cf;
         bf.fetch(Bm + b * a.b_batch + (int64_t)c * Q * a.b_token + grp * d.N, a.b_token, n, d.N, tid);
         cf.fetch(Cm + b * a.c_batch + (int64_t)c * Q * a.c_token + grp * d.N, a.c_token, n, d.N, tid);
         fetch(0);
@@ -200,9 +218,7 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
             f32x4 r = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int k = 0; k < NP / 32; ++k)
-                if (32 * k < d.N)
-                    r = mma(row_frag(rows_of + (16 * strip + l16) * LDN + 32 * k, g),
-                            row_frag(cols_of + me * LDN + 32 * k, g), r);
+                r = mma(row_frag(rows_of + (16 * strip + l16) * LDN + 32 * k, g), row_frag(cols_of + me * LDN + 32 * k, g), r);
             return r;
         };
 #pragma unroll
@@ -219,7 +235,8 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
 #pragma unroll
     for (int k = 0; k < NS; ++k) dB[k] = dC[k] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    float rin = 0.f, rown = 0.f, qown = 0.f, qdiag = 0.f, qend = 0.f, dot = 0.f, zdiag = 0.f;
+    double rown = 0., qown = 0.;
+    float rin = 0.f, qdt = 0.f, qend = 0.f, dot = 0.f, zdiag = 0.f;
     for (int it = 0; it < items; ++it) {
         const int h = h0 + it / slabs, slab = it % slabs, p0 = slab * kSlab;
         const int64_t chunk = ((int64_t)b * d.H + h) * d.nc + c;
@@ -234,7 +251,7 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
             s.dt[tid] = tf[2];
         }
         __syncthreads();
-        if (has_g) af.fetch(a.adjoints + chunk * d.P * d.N + (int64_t)p0 * d.N, d.N, d.P - p0, d.N, tid);
+        if (has_g) af.fetch(a.adjoints + (chunk * d.P + p0) * cols, cols, d.P - p0, cols, tid);
         const float mhi = s.shi[me], mlo = s.slo[me], mdt = s.dt[me];
         Frag<T> xr[2], gr[2];
 #pragma unroll
@@ -242,7 +259,10 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
             xr[k] = row_frag(s.x + me * LDP + 32 * k, g);
             gr[k] = row_frag(s.g + me * LDP + 32 * k, g);
         }
-        const int ks = d.P - p0 > 32 ? 2 : 1;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) zdiag += frag_at(xr[q], e) * frag_at(gr[q], e);
 
         // rows t
 #pragma unroll
@@ -257,34 +277,35 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
                 f32x4 z = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
-                    if (q < ks) z = mma(row_frag(s.x + (16 * is + l16) * LDP + 32 * q, g), gr[q], z);
+                    z = mma(row_frag(s.x + (16 * is + l16) * LDP + 32 * q, g), gr[q], z);
                 const f32x4 ih = *(const f32x4 *)(s.shi + 16 * is + 4 * g), il = *(const f32x4 *)(s.slo + 16 * is + 4 * g);
                 const f32x4 id4 = *(const f32x4 *)(s.dt + 16 * is + 4 * g);
+                f32x4 dif;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) dif[v] = (mhi - ih[v]) + (mlo - il[v]);
+                if (is == wave)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) dif[v] += upto[v];
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
-                    const float e = __builtin_amdgcn_exp2f((mhi - ih[v]) + (mlo - il[v])) * id4[v];
-                    const bool before = is < wave || 4 * g + v < l16, same = is == wave && 4 * g + v == l16;
-                    wt[u][v] = before || same ? z[v] * e : 0.f;
-                    rown += before ? cbp[k][u][v] * wt[u][v] : 0.f;
-                    zdiag += same ? z[v] : 0.f;
+                    wt[u][v] = z[v] * (__builtin_amdgcn_exp2f(dif[v]) * id4[v]);
+                    rown += cbp[k][u][v] * wt[u][v];  // the columns add the very same products
                 }
             }
             const Frag<T> wf = pack_frag<T>(wt[0], wt[1]);
 #pragma unroll
             for (int m = 0; m < NS; ++m)
-                if (16 * m < d.N) dC[m] = mma(col_frag(s.b, LDN, 32 * k, 16 * m, l16, g), wf, dC[m]);
+                dC[m] = mma(col_frag(s.b, LDN, 32 * k, 16 * m, l16, g), wf, dC[m]);
         }
         if (has_h) {
             const float f = __builtin_amdgcn_exp2f(mhi + mlo);
 #pragma unroll
             for (int m = 0; m < NS; ++m) {
-                if (16 * m >= d.N) continue;
                 f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
-                    if (q < ks)
-#pragma unroll
-                        for (int t = 0; t < kTerms<T>; ++t) o = mma(col_frag(s.plane[t], LDN, 32 * q, 16 * m, l16, g), gr[q], o);
+    #pragma unroll
+                    for (int t = 0; t < kTerms<T>; ++t) o = mma(col_frag(s.plane[t], LDN, 32 * q, 16 * m, l16, g), gr[q], o);
                 o *= f;
                 dC[m] += o;
 #pragma unroll
@@ -308,26 +329,31 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
                 f32x4 z = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
-                    if (q < ks) z = mma(row_frag(s.g + (16 * ts + l16) * LDP + 32 * q, g), xr[q], z);
+                    z = mma(row_frag(s.g + (16 * ts + l16) * LDP + 32 * q, g), xr[q], z);
                 const f32x4 th = *(const f32x4 *)(s.shi + 16 * ts + 4 * g), tl = *(const f32x4 *)(s.slo + 16 * ts + 4 * g);
                 const f32x4 cb = k == kw ? cbd[u] : cbp[k][u];
+                f32x4 dif;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) dif[v] = (th[v] - mhi) + (tl[v] - mlo);
+                if (ts == wave)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) dif[v] += from[v];
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
-                    const float e = __builtin_amdgcn_exp2f((th[v] - mhi) + (tl[v] - mlo));
-                    const bool after = ts > wave || 4 * g + v > l16, same = ts == wave && 4 * g + v == l16;
-                    nt[u][v] = after || same ? cb[v] * e : 0.f;
-                    wt[u][v] = after || same ? z[v] * e * mdt : 0.f;
-                    qown += after ? nt[u][v] * z[v] : 0.f;
-                    qdiag += same ? nt[u][v] * z[v] : 0.f;
+                    const float e = __builtin_amdgcn_exp2f(dif[v]);
+                    nt[u][v] = cb[v] * e;
+                    wt[u][v] = z[v] * (e * mdt);
+                    qown += cb[v] * wt[u][v];
+                    qdt += nt[u][v] * z[v];
                 }
             }
             const Frag<T> nf = pack_frag<T>(nt[0], nt[1]), wf = pack_frag<T>(wt[0], wt[1]);
 #pragma unroll
             for (int p = 0; p < 4; ++p)
-                if (p0 + 16 * p < d.P) dx[p] = mma(col_frag(s.g, LDP, 32 * k, 16 * p, l16, g), nf, dx[p]);
+                dx[p] = mma(col_frag(s.g, LDP, 32 * k, 16 * p, l16, g), nf, dx[p]);
 #pragma unroll
             for (int m = 0; m < NS; ++m)
-                if (16 * m < d.N) dB[m] = mma(col_frag(s.c, LDN, 32 * k, 16 * m, l16, g), wf, dB[m]);
+                dB[m] = mma(col_frag(s.c, LDN, 32 * k, 16 * m, l16, g), wf, dB[m]);
         }
 
         // the gradient from later chunks, in the planes of h0
@@ -351,14 +377,12 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
             for (int p = 0; p < 4; ++p) o[p] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int k = 0; k < NP / 32; ++k) {
-                if (32 * k >= d.N) continue;
                 const Frag<T> br = row_frag(s.b + me * LDN + 32 * k, g);
 #pragma unroll
                 for (int p = 0; p < 4; ++p)
-                    if (p0 + 16 * p < d.P)
 #pragma unroll
-                        for (int t = 0; t < kTerms<T>; ++t)
-                            o[p] = mma(row_frag(s.plane[t] + (16 * p + l16) * LDN + 32 * k, g), br, o[p]);
+                    for (int t = 0; t < kTerms<T>; ++t)
+                        o[p] = mma(row_frag(s.plane[t] + (16 * p + l16) * LDN + 32 * k, g), br, o[p]);
             }
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
@@ -369,11 +393,10 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
             }
 #pragma unroll
             for (int m = 0; m < NS; ++m) {
-                if (16 * m >= d.N) continue;
                 f32x4 w = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
-                    if (q < ks) w = mma(col_frag(s.plane[0], LDN, 32 * q, 16 * m, l16, g), xr[q], w);
+                    w = mma(col_frag(s.plane[0], LDN, 32 * q, 16 * m, l16, g), xr[q], w);
                 dB[m] += w * (f1 * mdt);
             }
         }
@@ -383,26 +406,25 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
                 const int at = 16 * p + 4 * g;
-                if (p0 + at >= d.P) continue;
                 f32x4 r;
 #pragma unroll
                 for (int v = 0; v < 4; ++v)
                     r[v] = me < n ? mdt * dx[p][v] + skip * Elem<T>::to_f32(s.g[me * LDP + at + v]) : 0.f;
-                store4<T>(o + at, r, d.P - p0 - at);
+                if (p0 + at < d.P) store4<T>(o + at, r, WHOLE ? 4 : d.P - p0 - at);
             }
         }
         if (slab + 1 == slabs) {
             rin = over_groups(rin);
             rown = over_groups(rown);
             qown = over_groups(qown);
-            qdiag = over_groups(qdiag);
+            qdt = over_groups(qdt);
             qend = over_groups(qend);
             dot = over_wave(dot);
             zdiag = over_wave(zdiag);
             if (g == 0) {
                 s.rin[me] = rin;
-                s.own[me] = rown - mdt * qown;
-                s.direct[me] = qown + qdiag + qend;
+                s.own[me] = rown - qown;
+                s.direct[me] = qdt + qend;
                 s.qend[me] = mdt * qend;
                 s.dt_done[me] = mdt;
             }
@@ -411,7 +433,8 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
                 s.diag[wave] = zdiag;
                 if (wave == 0) s.end_done = end;
             }
-            rin = rown = qown = qdiag = qend = dot = zdiag = 0.f;
+            rown = qown = 0.;
+            rin = qdt = qend = dot = zdiag = 0.f;
         }
     }
     __syncthreads();
@@ -474,18 +497,18 @@ BwdWork bwd_work(int64_t B, int64_t L, int H, int P, int G, int N, int Q) {
     BwdWork w;
     w.plan = plan_heads(B, nc, H, G, 512);
     w.adjoints = 0;
-    w.heads = pad64(B * H * nc * P * N);
+    w.heads = pad64(B * H * nc * P * state_cols(N));
     w.part = w.heads + pad64(3 * H * B * nc);
     w.total = w.part + (w.plan.splits > 1 ? pad64(2 * w.plan.splits * B * L * G * N) : 0);
     return w;
 }
 
-template <typename T, int NP>
+template <typename T, int NP, bool WHOLE>
 hipError_t launch_main(const BwdArgs &k, int64_t blocks, const Scan &a, const void *grad, void *grad_x, void *grad_dt,
                        void *grad_B, void *grad_C, hipStream_t stream) {
     constexpr int bytes = sizeof(BwdLds<T, NP>);
     static_assert(bytes <= 160 * 1024, "a workgroup's LDS");
-    auto kern = scan_bwd_kernel<T, NP>;
+    auto kern = scan_bwd_kernel<T, NP, WHOLE>;
     hipError_t e = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(64 * kStrips<T>), bytes, stream, k, (const T *)a.x,
@@ -502,7 +525,8 @@ hipError_t scan_bwd(const Scan &a, const float *saved, const void *grad, int64_t
     const ScanWork f = scan_work(a.B, a.L, a.H, a.P, a.N, Q);
     const BwdWork w = bwd_work(a.B, a.L, a.H, a.P, a.G, a.N, Q);
     float *sv = const_cast<float *>(saved);  // only read here
-    const ScanDims d = {(int)a.B, (int)a.L, a.H, a.P, a.G, a.N, f.nc, a.lengths, sv + f.dt, sv + f.shi, sv + f.slo};
+    const ScanDims d = {(int)a.B, (int)a.L, a.H, a.P, a.G, a.N, f.nc, a.lengths, sv + f.dt, sv + f.shi, sv + f.slo,
+                        sv + f.decay};
     const int64_t blocks = a.B * f.nc * a.G * w.plan.splits, all = a.B * a.L * a.G * a.N;
     const int64_t blocks_part = w.plan.splits > 1 ? (2 * all + 1023) / 1024 : 0, blocks_sum = blocks_part + (3 * a.H + 3) / 4;
     if (blocks > 0x7fffffff || blocks_sum > 0x7fffffff) return hipErrorInvalidConfiguration;
@@ -518,8 +542,9 @@ hipError_t scan_bwd(const Scan &a, const float *saved, const void *grad, int64_t
     const BwdArgs k = {d, w.plan, a.x_batch, a.x_token, a.b_batch, a.b_token, a.c_batch, a.c_token, g_batch, g_token,
                        saved + f.states, adjoints, a.A, a.D, w.plan.splits > 1 ? work + w.part : nullptr, work + w.heads,
                        a.initial != nullptr, grad_state != nullptr};
-    e = a.N <= 64 ? launch_main<T, 64>(k, blocks, a, grad, grad_x, grad_dt, grad_B, grad_C, stream)
-                  : launch_main<T, 128>(k, blocks, a, grad, grad_x, grad_dt, grad_B, grad_C, stream);
+#define X_(NP, WHOLE) e = launch_main<T, NP, WHOLE>(k, blocks, a, grad, grad_x, grad_dt, grad_B, grad_C, stream);
+    DDPM_SEQ_SCAN_SHAPES(T, a.N, a.P, X_)
+#undef X_
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((scan_bwd_sum_kernel<T>), dim3((unsigned)blocks_sum), dim3(256), 0, stream, k.part,
                        w.plan.splits, all, (T *)grad_B, (T *)grad_C, k.heads, a.H, a.B * f.nc, grad_A, grad_dt_bias,

@@ -6,11 +6,11 @@ namespace ddpm {
 namespace seq {
 
 constexpr int kThreads = 256;
-constexpr int kTimeHeads = 16;
+constexpr int kTimeHeads = 4;
 constexpr double kLog2e = 1.4426950408889634;
 
-// dt and the running sums s of a chunk, 16 heads a workgroup (dt's rows lie token by
-// token in memory, what comes out head by head); a wave a head, 64-bit sums.  A token past
+// dt and the running sums s of a chunk, four heads a workgroup (dt's rows lie token by
+// token in memory, what comes out head by head), a wave a head, 64-bit sums.  A token past
 // the sequence's length has dt = 0: it leaves the state alone.  A step's decay is bounded
 // to 2^-2000 and 2^2000, beyond which float32 has only 0 and infinity, so that s stays
 // finite.
@@ -30,7 +30,8 @@ __global__ __launch_bounds__(kThreads) void scan_times_kernel(ScanDims d, const 
     }
     __syncthreads();
     const int lane = threadIdx.x % kWave;
-    for (int k = threadIdx.x / kWave; k < kTimeHeads && h0 + k < d.H; k += kThreads / kWave) {
+    const int k = threadIdx.x / kWave;
+    if (h0 + k < d.H) {
         const double a = A[h0 + k] * kLog2e;
         const int64_t at = ((int64_t)(b * d.H + h0 + k) * d.nc + c) * Q + lane * PER;
         double s[PER], run = 0.;
@@ -54,41 +55,31 @@ __global__ __launch_bounds__(kThreads) void scan_times_kernel(ScanDims d, const 
             d.shi[at + e] = hi;
             d.slo[at + e] = (float)(before + s[e] - hi);
         }
+        if (lane == kWave - 1)
+            d.decay[(int64_t)(b * d.H + h0 + k) * d.nc + c] = __builtin_amdgcn_exp2f((float)(before + run));
     }
-}
-
-// Eight elements of a row of global memory in a fragment's order; columns past N are zero.
-template <typename T>
-__device__ __forceinline__ Frag<T> global_row_frag(const T *__restrict__ row, int k0, int g, int N, bool on) {
-    Frag<T> r;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int k = k0 + (e < 4 ? 4 * g + e : 12 + 4 * g + e);
-        const float v = on && k < N ? Elem<T>::to_f32(row[k]) : 0.f;
-        if constexpr (Elem<T>::is_bf16) r[e] = (__bf16)v;
-        else r.v[e] = v;
-    }
-    return r;
 }
 
 struct OutArgs {
     ScanDims d;
     ChunkPlan plan;
     int64_t x_batch, x_token, b_batch, b_token, c_batch, c_token;
-    const float *states;   // [B, H, nc, P, N]: the state that enters each chunk; or null (one chunk)
-    const float *initial;  // [B, H, P, N] or null
+    const float *states;  // [B, H, nc, P, cols]: the state that enters each chunk
+    int has_first;        // an initial state
     const float *D;
 };
 
 // y of a chunk for some heads of a group.  C . B is theirs together and stays in registers
 // (transposed: rows i, columns t); each head scales it by its decays, which makes it the
 // operand that x is multiplied by.  A wave has rows t of strips w and 7 - w (bfloat16), so
-// that the four waves have the same share of the triangle i <= t.  The scaled C . B and the
-// entering state are rounded to bfloat16 once, as the operands of matrix products whose sums
-// are float32; y is rounded to bfloat16 at the end by as much.
-template <typename T, int NP>
-__global__ __launch_bounds__(kThreads) void scan_out_kernel(OutArgs a, const T *__restrict__ X, const T *__restrict__ Bm,
-                                                            const T *__restrict__ Cm, T *__restrict__ y) {
+// that the four waves have the same share of the triangle i <= t and each operand from LDS
+// serves two strips.  The scaled C . B and the entering state are rounded to bfloat16 once, as
+// the operands of matrix products whose sums are float32; y is rounded to bfloat16 at the end
+// by as much, which is also why s alone (without its low part) is enough there.
+template <typename T, int NP, bool WHOLE>
+__global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const T *__restrict__ X,
+                                                               const T *__restrict__ Bm, const T *__restrict__ Cm,
+                                                               T *__restrict__ y) {
     constexpr int QS = kStrips<T>, Q = 16 * QS, SPW = QS / 4;
     constexpr int LDN = ld_of<T>(NP), LDP = ld_of<T>(kSlab);
     constexpr int kTiles = Q * LDP + kSlab * LDN;
@@ -96,7 +87,7 @@ __global__ __launch_bounds__(kThreads) void scan_out_kernel(OutArgs a, const T *
     __shared__ __align__(16) float shi[Q], slo[Q], dts[Q];
     T *xtile = lds, *htile = lds + Q * LDP;
     const ScanDims &d = a.d;
-    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, l16 = lane % 16, g = lane / 16;
+    const int tid = threadIdx.x, lane = tid % kWave, wave = wave_of(tid), l16 = lane % 16, g = lane / 16;
     int id = blockIdx.x;
     const int split = id % a.plan.splits;
     id /= a.plan.splits;
@@ -108,59 +99,63 @@ __global__ __launch_bounds__(kThreads) void scan_out_kernel(OutArgs a, const T *
     n = n < 0 ? 0 : n > Q ? Q : n;
     const int hg = d.H / d.G, h0 = grp * hg + split * a.plan.per;
     const int h1 = h0 + a.plan.per < (grp + 1) * hg ? h0 + a.plan.per : (grp + 1) * hg;
-    const int slabs = (d.P + kSlab - 1) / kSlab, items = (h1 - h0) * slabs;
+    const int slabs = (d.P + kSlab - 1) / kSlab, items = (h1 - h0) * slabs, cols = state_cols(d.N);
     const T *xb = X + b * a.x_batch + (int64_t)c * Q * a.x_token;
-    const bool has_h = n > 0 && (c > 0 || a.initial != nullptr);
+    const bool has_h = n > 0 && (c > 0 || a.has_first);
+    int strip[SPW];
+    float mask[4];  // of the diagonal tile, where row i comes after column t
+#pragma unroll
+    for (int j = 0; j < SPW; ++j) strip[j] = j == 0 ? wave : QS - 1 - wave;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) mask[v] = 4 * g + v <= l16 ? 0.f : -INFINITY;
+
+    TileFetch<T, Q, kSlab, kThreads, WHOLE> xf;
+    TileFetch<float, kSlab, NP, kThreads, true> hf;
+    float tf[3];
+    auto fetch = [&](int it) {
+        const int h = h0 + it / slabs, p0 = it % slabs * kSlab;
+        xf.fetch(xb + (int64_t)h * d.P + p0, a.x_token, n, d.P - p0, tid);
+        const int64_t chunk = ((int64_t)b * d.H + h) * d.nc + c;
+        if (has_h) hf.fetch(a.states + (chunk * d.P + p0) * cols, cols, d.P - p0, cols, tid);
+        if (tid < Q) {
+            tf[0] = d.shi[chunk * Q + tid];
+            tf[1] = d.slo[chunk * Q + tid];
+            tf[2] = d.dt[chunk * Q + tid];
+        }
+    };
 
     // C of the wave's rows, and C . B for every i <= t
     Frag<T> cf[SPW][NP / 32];
     f32x4 cb[SPW][QS];
     {
-        TileFetch<T, Q, NP, kThreads> bf;
-        bf.fetch(Bm + b * a.b_batch + (int64_t)c * Q * a.b_token + grp * d.N, a.b_token, n, d.N, tid);
-        bf.put(lds, tid);
-        const T *cp = Cm + b * a.c_batch + (int64_t)c * Q * a.c_token + grp * d.N;
-#pragma unroll
-        for (int j = 0; j < SPW; ++j) {
-            const int t = 16 * (j == 0 ? wave : QS - 1 - wave) + l16;
-#pragma unroll
-            for (int k = 0; k < NP / 32; ++k)
-                cf[j][k] = global_row_frag<T>(cp + (t < n ? t : 0) * a.c_token, 32 * k, g, d.N, t < n);
-        }
+        TileFetch<T, Q, NP, kThreads, false> cg, bg;
+        cg.fetch(Cm + b * a.c_batch + (int64_t)c * Q * a.c_token + grp * d.N, a.c_token, n, d.N, tid);
+        bg.fetch(Bm + b * a.b_batch + (int64_t)c * Q * a.b_token + grp * d.N, a.b_token, n, d.N, tid);
+        cg.put(lds, tid);
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < SPW; ++j) {
-            const int ts = j == 0 ? wave : QS - 1 - wave;
+        for (int j = 0; j < SPW; ++j)
 #pragma unroll
-            for (int i = 0; i < (SPW == 2 && j == 0 ? QS / 2 : QS); ++i) {
+            for (int k = 0; k < NP / 32; ++k) cf[j][k] = row_frag(lds + (16 * strip[j] + l16) * LDN + 32 * k, g);
+        __syncthreads();
+        bg.put(lds, tid);
+        __syncthreads();
+        fetch(0);
+#pragma unroll
+        for (int i = 0; i < QS; ++i) {
+            Frag<T> bf[NP / 32];
+#pragma unroll
+            for (int k = 0; k < NP / 32; ++k) bf[k] = row_frag(lds + (16 * i + l16) * LDN + 32 * k, g);
+#pragma unroll
+            for (int j = 0; j < SPW; ++j) {
                 cb[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-                if (i > ts) continue;
+                if (SPW == 2 && j == 0 && i >= QS / 2) continue;  // strip[0] is in the first half
 #pragma unroll
-                for (int k = 0; k < NP / 32; ++k)
-                    if (32 * k < d.N) cb[j][i] = mma(row_frag(lds + (16 * i + l16) * LDN + 32 * k, g), cf[j][k], cb[j][i]);
+                for (int k = 0; k < NP / 32; ++k) cb[j][i] = mma(bf[k], cf[j][k], cb[j][i]);
             }
         }
     }
 
-    TileFetch<T, Q, kSlab, kThreads> xf;
-    TileFetch<float, kSlab, NP, kThreads> hf;
-    float tf[3];
-    auto fetch = [&](int it) {
-        const int h = h0 + it / slabs, p0 = it % slabs * kSlab;
-        xf.fetch(xb + (int64_t)h * d.P + p0, a.x_token, n, d.P - p0, tid);
-        if (has_h) {
-            const int64_t head = (int64_t)b * d.H + h;
-            const float *src = a.states != nullptr ? a.states + (head * d.nc + c) * d.P * d.N : a.initial + head * d.P * d.N;
-            hf.fetch(src + (int64_t)p0 * d.N, d.N, d.P - p0, d.N, tid);
-        }
-        if (tid < Q) {
-            const int64_t at = ((int64_t)(b * d.H + h) * d.nc + c) * Q + tid;
-            tf[0] = d.shi[at];
-            tf[1] = d.slo[at];
-            tf[2] = d.dt[at];
-        }
-    };
-    fetch(0);
     for (int it = 0; it < items; ++it) {
         const int h = h0 + it / slabs, p0 = it % slabs * kSlab;
         __syncthreads();
@@ -169,10 +164,14 @@ __global__ __launch_bounds__(kThreads) void scan_out_kernel(OutArgs a, const T *
 #pragma unroll
             for (int k = 0; k < decltype(hf)::kCount; ++k) {
                 const int i = tid + k * kThreads, row = i / (NP / 4), col = i % (NP / 4) * 4;
-                float v[4];
-                widen<float>(hf.r[k], v);
+                if constexpr (Elem<T>::is_bf16) {
+                    u16x4 v;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) htile[row * LDN + col + e] = Elem<T>::from_f32(v[e]);
+                    for (int e = 0; e < 4; ++e) v[e] = f32_to_bf16_bits(__uint_as_float(hf.r[k][e]));
+                    *(u16x4 *)(htile + row * LDN + col) = v;
+                } else {
+                    *(u32x4 *)(htile + row * LDN + col) = hf.r[k];
+                }
             }
         }
         if (tid < Q) {
@@ -182,61 +181,82 @@ __global__ __launch_bounds__(kThreads) void scan_out_kernel(OutArgs a, const T *
         }
         __syncthreads();
         if (it + 1 < items) fetch(it + 1);
-        const float skip = a.D[h];
+        f32x4 acc[SPW][4];
+#pragma unroll
+        for (int j = 0; j < SPW; ++j)
+#pragma unroll
+            for (int p = 0; p < 4; ++p) acc[j][p] = f32x4{0.f, 0.f, 0.f, 0.f};
+        float th[SPW], tl[SPW];
 #pragma unroll
         for (int j = 0; j < SPW; ++j) {
-            const int ts = j == 0 ? wave : QS - 1 - wave, t = 16 * ts + l16;
-            if (16 * ts >= rows) continue;
-            f32x4 acc[4];
+            th[j] = shi[16 * strip[j] + l16];
+            tl[j] = slo[16 * strip[j] + l16];
+        }
+        if (has_h) {
 #pragma unroll
-            for (int p = 0; p < 4; ++p) acc[p] = f32x4{0.f, 0.f, 0.f, 0.f};
-            const float th = shi[t], tl = slo[t];
-            if (has_h) {
+            for (int k = 0; k < NP / 32; ++k)
 #pragma unroll
-                for (int k = 0; k < NP / 32; ++k) {
-                    if (32 * k >= d.N) continue;
+                for (int p = 0; p < 4; ++p) {
+                    const Frag<T> hr = row_frag(htile + (16 * p + l16) * LDN + 32 * k, g);
 #pragma unroll
-                    for (int p = 0; p < 4; ++p)
-                        if (p0 + 16 * p < d.P)
-                            acc[p] = mma(row_frag(htile + (16 * p + l16) * LDN + 32 * k, g), cf[j][k], acc[p]);
+                    for (int j = 0; j < SPW; ++j) acc[j][p] = mma(hr, cf[j][k], acc[j][p]);
                 }
-                const float f = __builtin_amdgcn_exp2f(th + tl);
 #pragma unroll
-                for (int p = 0; p < 4; ++p) acc[p] *= f;
+            for (int j = 0; j < SPW; ++j) {
+                const float f = __builtin_amdgcn_exp2f(th[j] + tl[j]);
+#pragma unroll
+                for (int p = 0; p < 4; ++p) acc[j][p] *= f;
             }
+        }
 #pragma unroll
-            for (int i = 0; i < (SPW == 2 && j == 0 ? QS / 4 : QS / 2); ++i) {
-                if (2 * i > ts) continue;
+        for (int i = 0; i < QS / 2; ++i) {
+            if (2 * i > strip[SPW - 1]) continue;
+            Frag<T> xr[4];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) xr[p] = col_frag(xtile, LDP, 32 * i, 16 * p, l16, g);
+#pragma unroll
+            for (int j = 0; j < SPW; ++j) {
+                if ((SPW == 2 && j == 0 && i >= QS / 4) || 2 * i > strip[j]) continue;
                 f32x4 m[2];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int is = 2 * i + u;
                     m[u] = f32x4{0.f, 0.f, 0.f, 0.f};
-                    if (is > ts) continue;
-                    const f32x4 ih = *(const f32x4 *)(shi + 16 * is + 4 * g), il = *(const f32x4 *)(slo + 16 * is + 4 * g);
-                    const f32x4 id4 = *(const f32x4 *)(dts + 16 * is + 4 * g);
+                    if (is > strip[j]) continue;
+                    const f32x4 ih = *(const f32x4 *)(shi + 16 * is + 4 * g), id4 = *(const f32x4 *)(dts + 16 * is + 4 * g);
+                    f32x4 dif;
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        const float e = __builtin_amdgcn_exp2f((th - ih[v]) + (tl - il[v])) * id4[v];
-                        m[u][v] = is < ts || 4 * g + v <= l16 ? cb[j][is][v] * e : 0.f;
+                    for (int v = 0; v < 4; ++v) dif[v] = th[j] - ih[v];
+                    if constexpr (!Elem<T>::is_bf16) {
+                        const f32x4 il = *(const f32x4 *)(slo + 16 * is + 4 * g);
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) dif[v] += tl[j] - il[v];
                     }
+                    if (is == strip[j])
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) dif[v] += mask[v];
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) m[u][v] = cb[j][is][v] * (__builtin_amdgcn_exp2f(dif[v]) * id4[v]);
                 }
                 const Frag<T> mf = pack_frag<T>(m[0], m[1]);
 #pragma unroll
-                for (int p = 0; p < 4; ++p)
-                    if (p0 + 16 * p < d.P) acc[p] = mma(col_frag(xtile, LDP, 32 * i, 16 * p, l16, g), mf, acc[p]);
+                for (int p = 0; p < 4; ++p) acc[j][p] = mma(xr[p], mf, acc[j][p]);
             }
+        }
+        const float skip = a.D[h];
+#pragma unroll
+        for (int j = 0; j < SPW; ++j) {
+            const int t = 16 * strip[j] + l16;
             if (t >= rows) continue;
             T *yr = y + (((int64_t)b * d.L + c * Q + t) * d.H + h) * d.P + p0;
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
                 const int at = 16 * p + 4 * g;
-                if (p0 + at >= d.P) continue;
                 f32x4 o;
 #pragma unroll
                 for (int v = 0; v < 4; ++v)
-                    o[v] = t < n ? acc[p][v] + skip * Elem<T>::to_f32(xtile[t * LDP + at + v]) : 0.f;
-                store4<T>(yr + at, o, d.P - p0 - at);
+                    o[v] = t < n ? acc[j][p][v] + skip * Elem<T>::to_f32(xtile[t * LDP + at + v]) : 0.f;
+                if (p0 + at < d.P) store4<T>(yr + at, o, WHOLE ? 4 : d.P - p0 - at);
             }
         }
     }
@@ -310,7 +330,8 @@ template <typename T>
 hipError_t scan_fwd(const Scan &a, float *work, void *y, float *final_state, bool save, hipStream_t stream) {
     constexpr int Q = 16 * kStrips<T>;
     const ScanWork w = scan_work(a.B, a.L, a.H, a.P, a.N, Q);
-    const ScanDims d = {(int)a.B, (int)a.L, a.H, a.P, a.G, a.N, w.nc, a.lengths, work + w.dt, work + w.shi, work + w.slo};
+    const ScanDims d = {(int)a.B, (int)a.L, a.H, a.P, a.G, a.N, w.nc, a.lengths, work + w.dt, work + w.shi, work + w.slo,
+                        work + w.decay};
     const int blocks_h = (a.H + kTimeHeads - 1) / kTimeHeads;
     const ChunkPlan plan = plan_heads(a.B, w.nc, a.H, a.G, 1024);
     const int64_t bt = a.B * w.nc * blocks_h, bo = a.B * w.nc * a.G * plan.splits;
@@ -319,20 +340,20 @@ hipError_t scan_fwd(const Scan &a, float *work, void *y, float *final_state, boo
                        a.dt_token, a.A, a.dt_bias, blocks_h);
     hipError_t e = hipGetLastError();
     float *states = nullptr;
-    if (e == hipSuccess && (w.nc > 1 || final_state != nullptr || save)) {
+    if (e == hipSuccess && (w.nc > 1 || a.initial != nullptr || final_state != nullptr || save)) {
         states = work + w.states;
         e = launch_scan_states<T>(d, (const T *)a.x, a.x_batch, a.x_token, (const T *)a.Bm, a.b_batch, a.b_token, states,
                                   false, stream);
         if (e == hipSuccess) e = launch_scan_pass(d, states, a.initial, final_state, Q, false, stream);
     }
     if (e != hipSuccess) return e;
-    const OutArgs o = {d, plan, a.x_batch, a.x_token, a.b_batch, a.b_token, a.c_batch, a.c_token, states, a.initial, a.D};
-    if (a.N <= 64)
-        hipLaunchKernelGGL((scan_out_kernel<T, 64>), dim3((unsigned)bo), dim3(kThreads), 0, stream, o, (const T *)a.x,
-                           (const T *)a.Bm, (const T *)a.Cm, (T *)y);
-    else
-        hipLaunchKernelGGL((scan_out_kernel<T, 128>), dim3((unsigned)bo), dim3(kThreads), 0, stream, o, (const T *)a.x,
-                           (const T *)a.Bm, (const T *)a.Cm, (T *)y);
+    const OutArgs o = {d, plan, a.x_batch, a.x_token, a.b_batch, a.b_token, a.c_batch, a.c_token, states,
+                       a.initial != nullptr, a.D};
+#define X_(NP, WHOLE)                                                                                              \
+    hipLaunchKernelGGL((scan_out_kernel<T, NP, WHOLE>), dim3((unsigned)bo), dim3(kThreads), 0, stream, o,          \
+                       (const T *)a.x, (const T *)a.Bm, (const T *)a.Cm, (T *)y);
+    DDPM_SEQ_SCAN_SHAPES(T, a.N, a.P, X_)
+#undef X_
     return hipGetLastError();
 }
 

@@ -18,7 +18,7 @@ struct StateArgs {
 // exp(s) for the adjoint.  A wave holds 16 rows p by all n.  The state is summed over the
 // whole sequence, so it keeps float32's precision: X * w enters the bfloat16 products as
 // three terms (Y is bfloat16 already).
-template <typename T, int NP>
+template <typename T, int NP, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void scan_states_kernel(StateArgs a, const T *__restrict__ X,
                                                                const T *__restrict__ Y, float *__restrict__ out) {
     constexpr int Q = 16 * kStrips<T>, LDN = ld_of<T>(NP), LDP = ld_of<T>(kSlab);
@@ -26,7 +26,7 @@ __global__ __launch_bounds__(kThreads) void scan_states_kernel(StateArgs a, cons
     __shared__ __align__(16) T xtile[Q * LDP];
     __shared__ __align__(16) float w[Q];
     const ScanDims &d = a.d;
-    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, l16 = lane % 16, g = lane / 16;
+    const int tid = threadIdx.x, lane = tid % kWave, wave = wave_of(tid), l16 = lane % 16, g = lane / 16;
     int id = blockIdx.x;
     const int split = id % a.plan.splits;
     id /= a.plan.splits;
@@ -39,8 +39,8 @@ __global__ __launch_bounds__(kThreads) void scan_states_kernel(StateArgs a, cons
     const int h1 = h0 + a.plan.per < (grp + 1) * hg ? h0 + a.plan.per : (grp + 1) * hg;
     const int slabs = (d.P + kSlab - 1) / kSlab, items = (h1 - h0) * slabs;
     const T *xb = X + b * a.x_batch + (int64_t)c * Q * a.x_token;
-    TileFetch<T, Q, NP, kThreads> yf;
-    TileFetch<T, Q, kSlab, kThreads> xf;
+    TileFetch<T, Q, NP, kThreads, false> yf;
+    TileFetch<T, Q, kSlab, kThreads, WHOLE> xf;
     yf.fetch(Y + b * a.y_batch + (int64_t)c * Q * a.y_token + grp * d.N, a.y_token, n, d.N, tid);
     xf.fetch(xb + (int64_t)h0 * d.P, a.x_token, n, d.P, tid);
     yf.put(ytile, tid);
@@ -86,65 +86,94 @@ __global__ __launch_bounds__(kThreads) void scan_states_kernel(StateArgs a, cons
             }
 #pragma unroll
             for (int k = 0; k < NP / 16; ++k) {
-                if (16 * k >= d.N) continue;
                 const Frag<T> yr = col_frag(ytile, LDN, r, 16 * k, l16, g);
 #pragma unroll
                 for (int t = 0; t < kTerms<T>; ++t) acc[k] = mma(yr, xs[t], acc[k]);
             }
         }
         if (p0 + p + l16 < d.P) {
-            float *o = out + ((int64_t)(b * d.H + h) * d.nc + c) * d.P * d.N + (int64_t)(p0 + p + l16) * d.N;
+            const int cols = state_cols(d.N);
+            float *o = out + (((int64_t)(b * d.H + h) * d.nc + c) * d.P + p0 + p + l16) * cols;
 #pragma unroll
-            for (int k = 0; k < NP / 16; ++k) {
-                const int at = 16 * k + 4 * g;
-                if (at < d.N) store4<float>(o + at, acc[k], d.N - at);
-            }
+            for (int k = 0; k < NP / 16; ++k)
+                if (16 * k + 4 * g < cols) *(f32x4 *)(o + 16 * k + 4 * g) = acc[k];
         }
     }
 }
 
-constexpr int kPassLanes = 16, kPassParts = kThreads / kPassLanes;
+constexpr int kPassLanes = 16;
 
-// h = first; for every chunk in order: part = states[c], states[c] = h, h = a[c] h + part.
-// Sixteen lanes of four elements by sixteen parts of the chunks: each part is run from
-// zero, the parts are joined in LDS, and each is run again from its true start.
-__global__ __launch_bounds__(kThreads) void scan_pass_kernel(ScanDims d, int Q, float *__restrict__ states,
-                                                             const float *__restrict__ first,
-                                                             float *__restrict__ final_state, int groups, int reverse) {
-    __shared__ f32x4 ends[kPassParts][kPassLanes];
-    __shared__ float mults[kPassParts];
+// h = first; for every chunk in order: part = states[c], states[c] = h, h = decay[c] h + part.
+// Sixteen lanes of four elements by PARTS runs of chunks: each run goes from zero, the runs'
+// ends are joined in LDS, and each run goes again from its true start; the parts stay in
+// registers between where a run has at most KEEP chunks and are read again otherwise.
+template <int PARTS>
+__global__ __launch_bounds__(PARTS *kPassLanes) void scan_pass_kernel(ScanDims d, int Q, float *__restrict__ states,
+                                                                      const float *__restrict__ first,
+                                                                      float *__restrict__ final_state, int groups,
+                                                                      int reverse) {
+    constexpr int KEEP = 4;
+    __shared__ f32x4 ends[PARTS][kPassLanes];
+    __shared__ float mults[PARTS];
     const int lane = threadIdx.x % kPassLanes, part = threadIdx.x / kPassLanes;
     const int64_t head = blockIdx.x / groups;  // b * H + h
-    const int E = d.P * d.N, e = (blockIdx.x % groups * kPassLanes + lane) * 4;
+    const int cols = state_cols(d.N), per_row = cols / 4;
+    const int e = blockIdx.x % groups * kPassLanes + lane;  // in vectors of four
+    const int64_t E = (int64_t)d.P * cols;
+    const bool on = e < d.P * per_row;
     const int n = valid_tokens(d.lengths, (int)(head / d.H), d.L), nc = (n + Q - 1) / Q;
-    const int per = (nc + kPassParts - 1) / kPassParts;
+    const int per = (nc + PARTS - 1) / PARTS;
     const int from = part * per < nc ? part * per : nc, to = from + per < nc ? from + per : nc;
-    const int left = e < E ? E - e : 0;
-    float *st = states + head * d.nc * E + e;
-    const float *shi = d.shi + head * d.nc * Q + Q - 1, *slo = d.slo + head * d.nc * Q + Q - 1;
+    // where the caller's unpadded states have these four
+    const int64_t user = head * d.P * d.N + (int64_t)(e / per_row) * d.N + e % per_row * 4;
+    const int left = on ? d.N - e % per_row * 4 : 0;
+    f32x4 *st = (f32x4 *)(states + head * d.nc * E) + (on ? e : 0);
+    const float *decay = d.decay + head * d.nc;
+    const int64_t step = reverse ? -E / 4 : E / 4;
+    const int dir = reverse ? -1 : 1, c0 = reverse ? nc - 1 - from : from;
+    f32x4 keep[KEEP];
     f32x4 h = {0.f, 0.f, 0.f, 0.f};
     float m = 1.f;
-#pragma unroll 4
-    for (int k = from; k < to; ++k) {
-        const int c = reverse ? nc - 1 - k : k;
-        const float am = __builtin_amdgcn_exp2f(shi[(int64_t)c * Q] + slo[(int64_t)c * Q]);
-        h = h * am + load4(st + (int64_t)c * E, left);
-        m *= am;
+    st += c0 * (E / 4);
+    decay += c0;
+    if (per <= KEEP) {
+#pragma unroll
+        for (int k = 0; k < KEEP; ++k)
+            if (from + k < to) keep[k] = st[k * step];
+#pragma unroll
+        for (int k = 0; k < KEEP; ++k)
+            if (from + k < to) {
+                h = h * decay[k * dir] + keep[k];
+                m *= decay[k * dir];
+            }
+    } else {
+#pragma unroll 8
+        for (int k = 0; k < to - from; ++k) {
+            h = h * decay[k * dir] + st[k * step];
+            m *= decay[k * dir];
+        }
     }
     ends[part][lane] = h;
     if (lane == 0) mults[part] = m;
     __syncthreads();
-    h = first != nullptr ? load4(first + head * E + e, left) : f32x4{0.f, 0.f, 0.f, 0.f};
+    h = first != nullptr ? load4(first + user, left) : f32x4{0.f, 0.f, 0.f, 0.f};
     for (int k = 0; k < part; ++k) h = h * mults[k] + ends[k][lane];
-    if (part == kPassParts - 1 && final_state != nullptr && left > 0)
-        store4<float>(final_state + head * E + e, h * mults[part] + ends[part][lane], left);
-#pragma unroll 4
-    for (int k = from; k < to; ++k) {
-        const int c = reverse ? nc - 1 - k : k;
-        const float am = __builtin_amdgcn_exp2f(shi[(int64_t)c * Q] + slo[(int64_t)c * Q]);
-        const f32x4 own = load4(st + (int64_t)c * E, left);
-        if (left > 0) store4<float>(st + (int64_t)c * E, h, left);
-        h = h * am + own;
+    if (part == PARTS - 1 && final_state != nullptr && on) store4<float>(final_state + user, h * mults[part] + ends[part][lane], left);
+    if (!on) return;
+    if (per <= KEEP) {
+#pragma unroll
+        for (int k = 0; k < KEEP; ++k)
+            if (from + k < to) {
+                st[k * step] = h;
+                h = h * decay[k * dir] + keep[k];
+            }
+    } else {
+#pragma unroll 8
+        for (int k = 0; k < to - from; ++k) {
+            const f32x4 own = st[k * step];
+            st[k * step] = h;
+            h = h * decay[k * dir] + own;
+        }
     }
 }
 
@@ -155,10 +184,10 @@ hipError_t launch_scan_states(const ScanDims &d, const T *X, int64_t x_batch, in
     const StateArgs a = {d, plan, x_batch, x_token, y_batch, y_token, reverse ? 1 : 0};
     const int64_t blocks = (int64_t)d.B * d.nc * d.G * plan.splits;
     if (blocks > 0x7fffffff) return hipErrorInvalidConfiguration;
-    if (d.N <= 64)
-        hipLaunchKernelGGL((scan_states_kernel<T, 64>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, a, X, Y, out);
-    else
-        hipLaunchKernelGGL((scan_states_kernel<T, 128>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, a, X, Y, out);
+#define X_(NP, WHOLE) \
+    hipLaunchKernelGGL((scan_states_kernel<T, NP, WHOLE>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, a, X, Y, out);
+    DDPM_SEQ_SCAN_SHAPES(T, d.N, d.P, X_)
+#undef X_
     return hipGetLastError();
 }
 template hipError_t launch_scan_states<float>(const ScanDims &, const float *, int64_t, int64_t, const float *, int64_t,
@@ -168,11 +197,16 @@ template hipError_t launch_scan_states<bf16_t>(const ScanDims &, const bf16_t *,
 
 hipError_t launch_scan_pass(const ScanDims &d, float *states, const float *first, float *final_state, int Q,
                             bool reverse, hipStream_t stream) {
-    const int groups = (d.P * d.N + 4 * kPassLanes - 1) / (4 * kPassLanes);
+    const int groups = (d.P * state_cols(d.N) / 4 + kPassLanes - 1) / kPassLanes;
     const int64_t blocks = (int64_t)d.B * d.H * groups;
     if (blocks > 0x7fffffff) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(scan_pass_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, stream, d, Q, states, first,
-                       final_state, groups, reverse ? 1 : 0);
+    // many chunks: four times the runs, so that a run is short beside a memory access
+    if (d.nc <= 128)
+        hipLaunchKernelGGL((scan_pass_kernel<16>), dim3((unsigned)blocks), dim3(16 * kPassLanes), 0, stream, d, Q, states,
+                           first, final_state, groups, reverse ? 1 : 0);
+    else
+        hipLaunchKernelGGL((scan_pass_kernel<64>), dim3((unsigned)blocks), dim3(64 * kPassLanes), 0, stream, d, Q, states,
+                           first, final_state, groups, reverse ? 1 : 0);
     return hipGetLastError();
 }
 
