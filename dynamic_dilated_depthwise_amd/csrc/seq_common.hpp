@@ -141,7 +141,18 @@ __device__ __forceinline__ f32x4 mma(const FragF &a, const FragF &b, f32x4 c) {
     return c;
 }
 
-// Contraction along a row: `row` points at element k0 of the lane's own row.
+// Contraction along a row: `row` points at element k0 of the lane's own row.  near_frag is
+// for products whose operands both run along rows: slot e of group g then stands for 8g + e,
+// one 16-byte read (the two halves of row_frag, which matches col_frag, are fused by the
+// compiler into a read with a short offset, at the price of an address register a tile).
+__device__ __forceinline__ bf16x8 near_frag(const bf16_t *row, int g) { return *(const bf16x8 *)(row + 8 * g); }
+__device__ __forceinline__ FragF near_frag(const float *row, int g) {
+    const f32x4 a = *(const f32x4 *)(row + 8 * g), b = *(const f32x4 *)(row + 8 * g + 4);
+    FragF r;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) { r.v[e] = a[e]; r.v[4 + e] = b[e]; }
+    return r;
+}
 __device__ __forceinline__ bf16x8 row_frag(const bf16_t *row, int g) {
     const u16x4 a = *(const u16x4 *)(row + 4 * g), b = *(const u16x4 *)(row + 16 + 4 * g);
     u16x8 r;

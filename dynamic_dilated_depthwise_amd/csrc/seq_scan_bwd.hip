@@ -38,6 +38,10 @@ struct BwdArgs {
     const float *A, *D;
     float *part;   // [splits, 2, B, L, G, N] or null (one split: grad_B and grad_C at once)
     float *heads;  // [3, H, B * nc]: every chunk's part of grad_A, grad_dt_bias, grad_D
+    // for the sums over a head's tokens at a workgroup's end, [B, H, nc, Q]: r_own - q_own,
+    // r_in, q / dt, q_end; and [B, H, nc, QS, 2]: the waves' parts of <g1, h0> and grad . x
+    double *own;
+    float *rin, *direct, *qend, *marks;
     int has_first, has_last;  // an initial state, a gradient of the final one
 };
 
@@ -47,10 +51,6 @@ struct BwdLds {
     T b[Q * LDN], c[Q * LDN], x[Q * LDP], g[Q * LDP];
     T plane[kTerms<T>][kSlab * LDN];  // h0, then g1
     float shi[Q], slo[Q], dt[Q];
-    // of the head before, for the sums over its tokens
-    double own[Q];
-    float rin[Q], direct[Q], qend[Q], dt_done[Q];
-    float dots[QS], diag[QS], end_done, pad[7];
 };
 
 // Sum over the four lane groups that hold a column's rows.
@@ -69,8 +69,9 @@ __device__ __forceinline__ float frag_at(const bf16x8 &f, int e) { return (float
 __device__ __forceinline__ float frag_at(const FragF &f, int e) { return f.v[e]; }
 
 // One chunk, some heads of a group.  Wave w has strip w of the chunk's tokens both as rows t
-// (grad_C, r) and as columns i (grad_x, grad_B, q): w + 1 tiles of the triangle as rows and
-// QS - w as columns, the same for every wave.
+// (grad_C, r) and as columns i (grad_x, grad_B, q).  Strips go in pairs, 32 of a contraction:
+// a wave in pair kw has the pairs before kw as rows, those after it as columns, and its own as
+// both, masked; the same work for every wave, and its tiles of C . B stay in registers.
 template <typename T, int NP, bool WHOLE>
 __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, const T *__restrict__ X,
                                                                    const T *__restrict__ Bm, const T *__restrict__ Cm,
@@ -102,13 +103,6 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
     const T *gb = grad + b * a.g_batch + (int64_t)c * Q * a.g_token;
     const int me = 16 * wave + l16;  // this lane's token, as a row t and as a column i
     const int kw = wave / 2;
-
-    float upto[4], from[4];  // masks of the diagonal tile: rows i up to column t, rows t from column i on
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-        upto[v] = 4 * g + v <= l16 ? 0.f : -INFINITY;
-        from[v] = 4 * g + v >= l16 ? 0.f : -INFINITY;
-    }
 
     TileFetch<T, Q, kSlab, THREADS, WHOLE> xf, gf;
     TileFetch<float, kSlab, NP, THREADS, true> hf, af;
@@ -152,22 +146,23 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
     // The sums over the tokens of a head: one wave, Q / 64 tokens a lane.
     auto finish_head = [&](int h) {
         constexpr int PER = Q / kWave;
+        const int64_t chunk = ((int64_t)b * d.H + h) * d.nc + c, at = chunk * Q + lane * PER;
         float dot = 0.f, diag = 0.f;
 #pragma unroll
         for (int w = 0; w < QS; ++w) {
-            dot += s.dots[w];
-            diag += s.diag[w];
+            dot += a.marks[(chunk * QS + w) * 2];
+            diag += a.marks[(chunk * QS + w) * 2 + 1];
         }
         float pre[PER], before = 0.f;
         double suf[PER], after = 0.;
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
             pre[e] = before;
-            before += s.qend[lane * PER + e];
+            before += a.qend[at + e];
         }
 #pragma unroll
         for (int e = PER - 1; e >= 0; --e) {
-            after += s.own[lane * PER + e] + s.rin[lane * PER + e];
+            after += a.own[at + e] + a.rin[at + e];
             suf[e] = after;
         }
         float up = before;
@@ -181,14 +176,14 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
         }
         up -= before;
         down -= after;
-        const float A = a.A[h];
+        const float A = a.A[h], end = d.decay[chunk];
         float sum_a = 0.f, sum_b = 0.f;
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
             const int t = lane * PER + e;
-            const float dt = s.dt_done[t], flow = s.end_done * dot + (up + pre[e]) + (float)(down + suf[e]);
+            const float dt = d.dt[at + e], flow = end * dot + (up + pre[e]) + (float)(down + suf[e]);
             // softplus's derivative from its value: 1 - exp(-dt)
-            const float raw = t < n ? (s.direct[t] + A * flow) * -expm1f(-dt) : 0.f;
+            const float raw = t < n ? (a.direct[at + e] + A * flow) * -expm1f(-dt) : 0.f;
             sum_a += t < n ? dt * flow : 0.f;
             sum_b += raw;
             if (t < rows) grad_dt[(tok0 + t) * d.H + h] = Elem<T>::from_f32(raw);
@@ -196,16 +191,17 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
         sum_a = over_wave(sum_a);
         sum_b = over_wave(sum_b);
         if (lane == 0) {
-            const int64_t M = (int64_t)d.B * d.nc, at = (int64_t)h * M + (int64_t)b * d.nc + c;
-            a.heads[at] = sum_a;
-            a.heads[d.H * M + at] = sum_b;
-            a.heads[2 * d.H * M + at] = diag;
+            const int64_t M = (int64_t)d.B * d.nc, to = (int64_t)h * M + (int64_t)b * d.nc + c;
+            a.heads[to] = sum_a;
+            a.heads[d.H * M + to] = sum_b;
+            a.heads[2 * d.H * M + to] = diag;
         }
     };
 
-    // B and C, and the tiles of C . B: rows t of this strip (transposed: D[i][t]) for the
-    // pairs of strips up to its own, columns i of it (D[t][i]) from its own on.
-    f32x4 cbp[QS / 2][2], cbd[2];
+    // B and C, and the tiles of C . B: as rows transposed, D[i][t], as columns D[t][i].  Slot k
+    // is pair k as rows for k < kw and pair k + 1 as columns from kw on.
+    constexpr int SLOTS = QS / 2 - 1;
+    f32x4 cbs[SLOTS][2], cbr[2], cbc[2];
     {
         TileFetch<T, Q, NP, THREADS, false> bf, cf;
         bf.fetch(Bm + b * a.b_batch + (int64_t)c * Q * a.b_token + grp * d.N, a.b_token, n, d.N, tid);
@@ -218,18 +214,18 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
             f32x4 r = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int k = 0; k < NP / 32; ++k)
-                r = mma(row_frag(rows_of + (16 * strip + l16) * LDN + 32 * k, g), row_frag(cols_of + me * LDN + 32 * k, g), r);
+                r = mma(near_frag(rows_of + (16 * strip + l16) * LDN + 32 * k, g), near_frag(cols_of + me * LDN + 32 * k, g), r);
             return r;
         };
 #pragma unroll
-        for (int k = 0; k < QS / 2; ++k)
+        for (int k = 0; k < SLOTS; ++k)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                if (k <= kw) cbp[k][u] = tile(s.b, 2 * k + u, s.c);
-                else cbp[k][u] = tile(s.c, 2 * k + u, s.b);
-            }
+            for (int u = 0; u < 2; ++u) cbs[k][u] = k < kw ? tile(s.b, 2 * k + u, s.c) : tile(s.c, 2 * k + 2 + u, s.b);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) cbd[u] = tile(s.c, 2 * kw + u, s.b);
+        for (int u = 0; u < 2; ++u) {
+            cbr[u] = tile(s.b, 2 * kw + u, s.c);
+            cbc[u] = tile(s.c, 2 * kw + u, s.b);
+        }
     }
     f32x4 dB[NS], dC[NS];
 #pragma unroll
@@ -241,7 +237,6 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
         const int h = h0 + it / slabs, slab = it % slabs, p0 = slab * kSlab;
         const int64_t chunk = ((int64_t)b * d.H + h) * d.nc + c;
         __syncthreads();
-        if (it > 0 && slab == 0 && wave == it / slabs % QS) finish_head(h - 1);
         xf.put(s.x, tid);
         gf.put(s.g, tid);
         if (has_h) put_planes(hf);
@@ -256,108 +251,97 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
         Frag<T> xr[2], gr[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            xr[k] = row_frag(s.x + me * LDP + 32 * k, g);
-            gr[k] = row_frag(s.g + me * LDP + 32 * k, g);
+            xr[k] = near_frag(s.x + me * LDP + 32 * k, g);
+            gr[k] = near_frag(s.g + me * LDP + 32 * k, g);
         }
 #pragma unroll
         for (int q = 0; q < 2; ++q)
 #pragma unroll
             for (int e = 0; e < 8; ++e) zdiag += frag_at(xr[q], e) * frag_at(gr[q], e);
 
-        // rows t
+        f32x4 dx[4];
 #pragma unroll
-        for (int k = 0; k < QS / 2; ++k) {
-            if (k > kw) continue;
+        for (int p = 0; p < 4; ++p) dx[p] = f32x4{0.f, 0.f, 0.f, 0.f};
+        // a pair of strips i = 2 k, 2 k + 1 against this strip's rows t
+        auto as_rows = [&](int k, const f32x4 (&cb)[2], bool own) {
             f32x4 wt[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int is = 2 * k + u;
-                wt[u] = f32x4{0.f, 0.f, 0.f, 0.f};
-                if (is > wave) continue;
-                f32x4 z = {0.f, 0.f, 0.f, 0.f};
+                f32x4 z = {0.f, 0.f, 0.f, 0.f}, dif;
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
-                    z = mma(row_frag(s.x + (16 * is + l16) * LDP + 32 * q, g), gr[q], z);
+                for (int q = 0; q < 2; ++q) z = mma(near_frag(s.x + (16 * is + l16) * LDP + 32 * q, g), gr[q], z);
                 const f32x4 ih = *(const f32x4 *)(s.shi + 16 * is + 4 * g), il = *(const f32x4 *)(s.slo + 16 * is + 4 * g);
                 const f32x4 id4 = *(const f32x4 *)(s.dt + 16 * is + 4 * g);
-                f32x4 dif;
-#pragma unroll
-                for (int v = 0; v < 4; ++v) dif[v] = (mhi - ih[v]) + (mlo - il[v]);
-                if (is == wave)
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) dif[v] += upto[v];
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
+                    dif[v] = (mhi - ih[v]) + (mlo - il[v]);
+                    if (own) dif[v] = 16 * is + 4 * g + v <= me ? dif[v] : -INFINITY;
                     wt[u][v] = z[v] * (__builtin_amdgcn_exp2f(dif[v]) * id4[v]);
-                    rown += cbp[k][u][v] * wt[u][v];  // the columns add the very same products
+                    rown += cb[u][v] * wt[u][v];  // the columns add the very same products
                 }
             }
             const Frag<T> wf = pack_frag<T>(wt[0], wt[1]);
 #pragma unroll
-            for (int m = 0; m < NS; ++m)
-                dC[m] = mma(col_frag(s.b, LDN, 32 * k, 16 * m, l16, g), wf, dC[m]);
-        }
-        if (has_h) {
-            const float f = __builtin_amdgcn_exp2f(mhi + mlo);
-#pragma unroll
-            for (int m = 0; m < NS; ++m) {
-                f32x4 o = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int q = 0; q < 2; ++q)
-    #pragma unroll
-                    for (int t = 0; t < kTerms<T>; ++t) o = mma(col_frag(s.plane[t], LDN, 32 * q, 16 * m, l16, g), gr[q], o);
-                o *= f;
-                dC[m] += o;
-#pragma unroll
-                for (int v = 0; v < 4; ++v) rin += o[v] * Elem<T>::to_f32(s.c[me * LDN + 16 * m + 4 * g + v]);
-            }
-        }
-
-        // columns i, inside the chunk
-        f32x4 dx[4];
-#pragma unroll
-        for (int p = 0; p < 4; ++p) dx[p] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < QS / 2; ++k) {
-            if (k < kw) continue;
+            for (int m = 0; m < NS; ++m) dC[m] = mma(col_frag(s.b, LDN, 32 * k, 16 * m, l16, g), wf, dC[m]);
+        };
+        // a pair of strips t = 2 k, 2 k + 1 against this strip's columns i
+        auto as_columns = [&](int k, const f32x4 (&cb)[2], bool own) {
             f32x4 nt[2], wt[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int ts = 2 * k + u;
-                nt[u] = wt[u] = f32x4{0.f, 0.f, 0.f, 0.f};
-                if (ts < wave) continue;
-                f32x4 z = {0.f, 0.f, 0.f, 0.f};
+                f32x4 z = {0.f, 0.f, 0.f, 0.f}, dif;
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
-                    z = mma(row_frag(s.g + (16 * ts + l16) * LDP + 32 * q, g), xr[q], z);
+                for (int q = 0; q < 2; ++q) z = mma(near_frag(s.g + (16 * ts + l16) * LDP + 32 * q, g), xr[q], z);
                 const f32x4 th = *(const f32x4 *)(s.shi + 16 * ts + 4 * g), tl = *(const f32x4 *)(s.slo + 16 * ts + 4 * g);
-                const f32x4 cb = k == kw ? cbd[u] : cbp[k][u];
-                f32x4 dif;
-#pragma unroll
-                for (int v = 0; v < 4; ++v) dif[v] = (th[v] - mhi) + (tl[v] - mlo);
-                if (ts == wave)
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) dif[v] += from[v];
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
+                    dif[v] = (th[v] - mhi) + (tl[v] - mlo);
+                    if (own) dif[v] = 16 * ts + 4 * g + v >= me ? dif[v] : -INFINITY;
                     const float e = __builtin_amdgcn_exp2f(dif[v]);
-                    nt[u][v] = cb[v] * e;
+                    nt[u][v] = cb[u][v] * e;
                     wt[u][v] = z[v] * (e * mdt);
-                    qown += cb[v] * wt[u][v];
+                    qown += cb[u][v] * wt[u][v];
                     qdt += nt[u][v] * z[v];
                 }
             }
             const Frag<T> nf = pack_frag<T>(nt[0], nt[1]), wf = pack_frag<T>(wt[0], wt[1]);
 #pragma unroll
-            for (int p = 0; p < 4; ++p)
-                dx[p] = mma(col_frag(s.g, LDP, 32 * k, 16 * p, l16, g), nf, dx[p]);
+            for (int p = 0; p < 4; ++p) dx[p] = mma(col_frag(s.g, LDP, 32 * k, 16 * p, l16, g), nf, dx[p]);
 #pragma unroll
-            for (int m = 0; m < NS; ++m)
-                dB[m] = mma(col_frag(s.c, LDN, 32 * k, 16 * m, l16, g), wf, dB[m]);
+            for (int m = 0; m < NS; ++m) dB[m] = mma(col_frag(s.c, LDN, 32 * k, 16 * m, l16, g), wf, dB[m]);
+        };
+        as_rows(kw, cbr, true);
+        as_columns(kw, cbc, true);
+#pragma unroll
+        for (int k = 0; k < SLOTS; ++k) {
+            if (k < kw) as_rows(k, cbs[k], false);
+            else as_columns(k + 1, cbs[k], false);
+        }
+        if (has_h) {
+            f32x4 o[NS];
+#pragma unroll
+            for (int m = 0; m < NS; ++m) o[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const Frag<T> go = row_frag(s.g + me * LDP + 32 * q, g);
+#pragma unroll
+                for (int t = 0; t < kTerms<T>; ++t)
+#pragma unroll
+                    for (int m = 0; m < NS; ++m) o[m] = mma(col_frag(s.plane[t], LDN, 32 * q, 16 * m, l16, g), go, o[m]);
+            }
+            const float f = __builtin_amdgcn_exp2f(mhi + mlo);
+#pragma unroll
+            for (int m = 0; m < NS; ++m) {
+                o[m] *= f;
+                dC[m] += o[m];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) rin += o[m][v] * Elem<T>::to_f32(s.c[me * LDN + 16 * m + 4 * g + v]);
+            }
         }
 
         // the gradient from later chunks, in the planes of h0
-        const float end = __builtin_amdgcn_exp2f(s.shi[Q - 1] + s.slo[Q - 1]);
         const float f1 = __builtin_amdgcn_exp2f((s.shi[Q - 1] - mhi) + (s.slo[Q - 1] - mlo));
         if (has_g) {
             __syncthreads();
@@ -377,12 +361,12 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
             for (int p = 0; p < 4; ++p) o[p] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int k = 0; k < NP / 32; ++k) {
-                const Frag<T> br = row_frag(s.b + me * LDN + 32 * k, g);
+                const Frag<T> br = near_frag(s.b + me * LDN + 32 * k, g);
 #pragma unroll
-                for (int p = 0; p < 4; ++p)
+                for (int t = 0; t < kTerms<T>; ++t)
 #pragma unroll
-                    for (int t = 0; t < kTerms<T>; ++t)
-                        o[p] = mma(row_frag(s.plane[t] + (16 * p + l16) * LDN + 32 * k, g), br, o[p]);
+                    for (int p = 0; p < 4; ++p)
+                        o[p] = mma(near_frag(s.plane[t] + (16 * p + l16) * LDN + 32 * k, g), br, o[p]);
             }
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
@@ -391,14 +375,18 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
 #pragma unroll
                 for (int v = 0; v < 4; ++v) qend += o[p][v] * Elem<T>::to_f32(s.x[me * LDP + 16 * p + 4 * g + v]);
             }
+            const float f2 = f1 * mdt;
+            f32x4 w[NS];
 #pragma unroll
-            for (int m = 0; m < NS; ++m) {
-                f32x4 w = {0.f, 0.f, 0.f, 0.f};
+            for (int m = 0; m < NS; ++m) w[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
-                    w = mma(col_frag(s.plane[0], LDN, 32 * q, 16 * m, l16, g), xr[q], w);
-                dB[m] += w * (f1 * mdt);
+            for (int q = 0; q < 2; ++q) {
+                const Frag<T> xo = row_frag(s.x + me * LDP + 32 * q, g);
+#pragma unroll
+                for (int m = 0; m < NS; ++m) w[m] = mma(col_frag(s.plane[0], LDN, 32 * q, 16 * m, l16, g), xo, w[m]);
             }
+#pragma unroll
+            for (int m = 0; m < NS; ++m) dB[m] += w[m] * f2;
         }
         if (me < rows) {
             const float skip = a.D[h];
@@ -422,23 +410,22 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
             dot = over_wave(dot);
             zdiag = over_wave(zdiag);
             if (g == 0) {
-                s.rin[me] = rin;
-                s.own[me] = rown - qown;
-                s.direct[me] = qdt + qend;
-                s.qend[me] = mdt * qend;
-                s.dt_done[me] = mdt;
+                const int64_t at = chunk * Q + me;
+                a.own[at] = rown - qown;
+                a.rin[at] = rin;
+                a.direct[at] = qdt + qend;
+                a.qend[at] = mdt * qend;
             }
             if (lane == 0) {
-                s.dots[wave] = dot;
-                s.diag[wave] = zdiag;
-                if (wave == 0) s.end_done = end;
+                a.marks[(chunk * QS + wave) * 2] = dot;
+                a.marks[(chunk * QS + wave) * 2 + 1] = zdiag;
             }
             rown = qown = 0.;
             rin = qdt = qend = dot = zdiag = 0.f;
         }
     }
     __syncthreads();
-    if (wave == 0) finish_head(h1 - 1);
+    for (int h = h0 + wave; h < h1; h += QS) finish_head(h);
 
     if (me < rows) {
         const int64_t at = ((tok0 + me) * d.G + grp) * d.N;
@@ -490,7 +477,7 @@ namespace {
 
 struct BwdWork {
     ChunkPlan plan;
-    int64_t adjoints, heads, part, total;
+    int64_t adjoints, heads, own, tokens, rin, direct, qend, marks, part, total;
 };
 BwdWork bwd_work(int64_t B, int64_t L, int H, int P, int G, int N, int Q) {
     const int64_t nc = (L + Q - 1) / Q;
@@ -498,7 +485,13 @@ BwdWork bwd_work(int64_t B, int64_t L, int H, int P, int G, int N, int Q) {
     w.plan = plan_heads(B, nc, H, G, 512);
     w.adjoints = 0;
     w.heads = pad64(B * H * nc * P * state_cols(N));
-    w.part = w.heads + pad64(3 * H * B * nc);
+    w.own = w.heads + pad64(3 * H * B * nc);
+    w.tokens = pad64(B * H * nc * Q);
+    w.rin = w.own + 2 * w.tokens;
+    w.direct = w.rin + w.tokens;
+    w.qend = w.direct + w.tokens;
+    w.marks = w.qend + w.tokens;
+    w.part = w.marks + pad64(B * H * nc * (Q / 16) * 2);
     w.total = w.part + (w.plan.splits > 1 ? pad64(2 * w.plan.splits * B * L * G * N) : 0);
     return w;
 }
@@ -541,6 +534,7 @@ hipError_t scan_bwd(const Scan &a, const float *saved, const void *grad, int64_t
     if (e != hipSuccess) return e;
     const BwdArgs k = {d, w.plan, a.x_batch, a.x_token, a.b_batch, a.b_token, a.c_batch, a.c_token, g_batch, g_token,
                        saved + f.states, adjoints, a.A, a.D, w.plan.splits > 1 ? work + w.part : nullptr, work + w.heads,
+                       (double *)(work + w.own), work + w.rin, work + w.direct, work + w.qend, work + w.marks,
                        a.initial != nullptr, grad_state != nullptr};
 #define X_(NP, WHOLE) e = launch_main<T, NP, WHOLE>(k, blocks, a, grad, grad_x, grad_dt, grad_B, grad_C, stream);
     DDPM_SEQ_SCAN_SHAPES(T, a.N, a.P, X_)

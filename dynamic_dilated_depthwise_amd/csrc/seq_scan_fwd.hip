@@ -103,11 +103,9 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
     const T *xb = X + b * a.x_batch + (int64_t)c * Q * a.x_token;
     const bool has_h = n > 0 && (c > 0 || a.has_first);
     int strip[SPW];
-    float mask[4];  // of the diagonal tile, where row i comes after column t
+    const int below = l16 - 4 * g;  // on the diagonal tile, row v of this lane is column t's token at v == below
 #pragma unroll
     for (int j = 0; j < SPW; ++j) strip[j] = j == 0 ? wave : QS - 1 - wave;
-#pragma unroll
-    for (int v = 0; v < 4; ++v) mask[v] = 4 * g + v <= l16 ? 0.f : -INFINITY;
 
     TileFetch<T, Q, kSlab, kThreads, WHOLE> xf;
     TileFetch<float, kSlab, NP, kThreads, true> hf;
@@ -136,7 +134,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
 #pragma unroll
         for (int j = 0; j < SPW; ++j)
 #pragma unroll
-            for (int k = 0; k < NP / 32; ++k) cf[j][k] = row_frag(lds + (16 * strip[j] + l16) * LDN + 32 * k, g);
+            for (int k = 0; k < NP / 32; ++k) cf[j][k] = near_frag(lds + (16 * strip[j] + l16) * LDN + 32 * k, g);
         __syncthreads();
         bg.put(lds, tid);
         __syncthreads();
@@ -145,7 +143,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
         for (int i = 0; i < QS; ++i) {
             Frag<T> bf[NP / 32];
 #pragma unroll
-            for (int k = 0; k < NP / 32; ++k) bf[k] = row_frag(lds + (16 * i + l16) * LDN + 32 * k, g);
+            for (int k = 0; k < NP / 32; ++k) bf[k] = near_frag(lds + (16 * i + l16) * LDN + 32 * k, g);
 #pragma unroll
             for (int j = 0; j < SPW; ++j) {
                 cb[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -197,7 +195,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
             for (int k = 0; k < NP / 32; ++k)
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
-                    const Frag<T> hr = row_frag(htile + (16 * p + l16) * LDN + 32 * k, g);
+                    const Frag<T> hr = near_frag(htile + (16 * p + l16) * LDN + 32 * k, g);
 #pragma unroll
                     for (int j = 0; j < SPW; ++j) acc[j][p] = mma(hr, cf[j][k], acc[j][p]);
                 }
@@ -234,7 +232,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
                     }
                     if (is == strip[j])
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) dif[v] += mask[v];
+                        for (int v = 0; v < 4; ++v) dif[v] = v <= below ? dif[v] : -INFINITY;
 #pragma unroll
                     for (int v = 0; v < 4; ++v) m[u][v] = cb[j][is][v] * (__builtin_amdgcn_exp2f(dif[v]) * id4[v]);
                 }
