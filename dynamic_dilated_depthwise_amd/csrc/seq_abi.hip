@@ -199,7 +199,7 @@ int ddpm_causal_conv_fwd(const void *x, const void *weight, const void *bias, co
 int64_t ddpm_causal_conv_bwd_workspace(int64_t batch, int64_t length, int64_t D, int width, int dtype) {
     Check c(dtype);
     if (conv_sizes(c, batch, length, D, width, 0, 0) != DDPM_OK) return 0;
-    return (int64_t)ddpm::seq::conv_partials(batch, length, D, is_bf16(dtype)) * D * (width + 1) * 4;
+    return (int64_t)ddpm::seq::conv_partials(batch, length, D, width) * D * (width + 1) * 4;
 }
 
 int ddpm_causal_conv_bwd(const void *grad, const void *x, const void *weight, const void *bias,

@@ -59,26 +59,99 @@ __device__ __forceinline__ void widen(const u32x4 &r, float (&v)[kVec<T>]) {
     }
 }
 
-// Stores the first n (at most kVec) of v, rounded to T once.
-template <typename T>
-__device__ __forceinline__ void store_vec(T *__restrict__ p, const float (&v)[kVec<T>], int64_t n) {
-    if (n >= kVec<T>) {
-        u32x4 r;
-        if constexpr (Elem<T>::is_bf16) {
+// V neighbouring elements of a row of `size`, as they lie in memory.  How they are reached:
+//   kWhole  size is a multiple of V: a vector is there or not
+//   kOdd    size is at least V: the last vector is read ending with the row and moved down
+//   kShort  the row is shorter than a vector: element by element
+// Every form reads only the row's own elements.
+enum Reach { kWhole, kOdd, kShort };
+inline Reach reach_of(int64_t size, int V) { return size % V == 0 ? kWhole : size > V ? kOdd : kShort; }
+
+template <typename T, int V>
+struct Raw {
+    static constexpr int kWords = V * (int)sizeof(T) / 4, kPer = 4 / (int)sizeof(T);
+    typedef uint32_t words __attribute__((ext_vector_type(kWords)));
+    typedef uint32_t words_a __attribute__((ext_vector_type(kWords), aligned(2)));
+    words r;
+    // Elements c .. c + V - 1 of `row`, zeros past its end or (on = false) altogether; `row`
+    // is readable in any case.
+    template <Reach R>
+    __device__ __forceinline__ void load(const T *__restrict__ row, int c, int size, bool on) {
+        if constexpr (R == kWhole) {
+            on = on && c < size;
+            r = *(const words_a *)(row + (on ? c : 0));
+            r = on ? r : words(0);
+        } else if constexpr (R == kOdd) {
+            on = on && c < size;
+            const int over = on ? (c + V > size ? c + V - size : 0) : 0;
+            r = *(const words_a *)(row + (on ? c - over : 0));
+            r = on ? r : words(0);
+            if (over > 0) {
+                if constexpr (kPer == 2) {
+                    if (over & 1) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                r[e] = (uint32_t)f32_to_bf16_bits(v[2 * e]) | (uint32_t)f32_to_bf16_bits(v[2 * e + 1]) << 16;
+                        for (int k = 0; k < kWords; ++k) r[k] = r[k] >> 16 | (k + 1 < kWords ? r[k + 1] << 16 : 0);
+                    }
+                }
+#pragma unroll
+                for (int m = 1; m < kWords; m *= 2) {
+                    if (over / kPer & m) {
+#pragma unroll
+                        for (int k = 0; k < kWords; ++k) r[k] = k + m < kWords ? r[k + m] : 0;
+                    }
+                }
+            }
         } else {
+            r = words(0);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) r[e] = __float_as_uint(v[e]);
+            for (int e = 0; e < V; ++e)
+                if (on && c + e < size) {
+                    if constexpr (kPer == 2) r[e / 2] |= (uint32_t)row[c + e] << (16 * (e % 2));
+                    else r[e] = __float_as_uint(row[c + e]);
+                }
         }
-        *(u32x4_a2 *)p = r;
-    } else {
-#pragma unroll
-        for (int e = 0; e < kVec<T>; ++e)
-            if (e < n) p[e] = Elem<T>::from_f32(v[e]);
     }
-}
+    __device__ __forceinline__ float operator[](int e) const {
+        if constexpr (kPer == 2) return __uint_as_float(e % 2 ? r[e / 2] & 0xffff0000u : r[e / 2] << 16);
+        else return __uint_as_float(r[e]);
+    }
+    __device__ __forceinline__ void set(const float (&v)[V]) {
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) {
+            if constexpr (kPer == 2)
+                r[k] = (uint32_t)f32_to_bf16_bits(v[2 * k]) | (uint32_t)f32_to_bf16_bits(v[2 * k + 1]) << 16;
+            else
+                r[k] = __float_as_uint(v[k]);
+        }
+    }
+    // Into elements c .. of `row`, those before its end.
+    template <Reach R>
+    __device__ __forceinline__ void store(T *__restrict__ row, int c, int size) const {
+        if (R == kWhole || c + V <= size) {
+            if (c < size) *(words_a *)(row + c) = r;
+            return;
+        }
+        words t = r;
+        int left = size - c;
+        T *p = row + c;
+#pragma unroll
+        for (int m = kWords / 2; m > 0; m /= 2) {  // halves, quarters: few stores for any length
+            if (left >= m * kPer) {
+#pragma unroll
+                for (int k = 0; k < m; ++k) store_word(p + k * kPer, t[k]);
+#pragma unroll
+                for (int k = 0; k < kWords; ++k) t[k] = k + m < kWords ? t[k + m] : 0;
+                p += m * kPer;
+                left -= m * kPer;
+            }
+        }
+        if (kPer == 2 && left > 0) *p = (T)(t[0] & 0xffffu);
+    }
+    __device__ static __forceinline__ void store_word(T *p, uint32_t w) {
+        typedef uint32_t word_a __attribute__((aligned(2)));
+        *(word_a *)p = w;
+    }
+};
 
 // Four elements at `p` (element-aligned), the first n of them.
 template <typename T>

@@ -34,93 +34,107 @@ __device__ __forceinline__ int length_of(const int *lengths, int b, int L) {
     return n < 0 ? 0 : n > L ? L : n;
 }
 
-// The weights of V channels, tap by tap, in the last W of KW taps (the first KW - W are 0).
-template <typename T, int KW>
-__device__ __forceinline__ void load_taps(const T *weight, int c, int D, int W, float (&w)[KW][kVec<T>]) {
+// The taps of V channels from c on (those below D), in the last W of KW; the older are 0.
+template <typename T, int KW, int V, Reach R, bool EXACT>
+__device__ __forceinline__ void load_taps(const T *__restrict__ weight, int c, int D, int W, float (&w)[KW][V]) {
+    const int n = D - c;
+    if (EXACT && R != kShort && n >= V) {  // V * KW neighbouring elements
+        Raw<T, 4> r[V * KW / 4];
 #pragma unroll
-    for (int j = 0; j < KW; ++j)
+        for (int k = 0; k < V * KW / 4; ++k) r[k].template load<kWhole>(weight + (int64_t)c * KW + 4 * k, 0, 4, true);
 #pragma unroll
-        for (int e = 0; e < kVec<T>; ++e) {
-            const int i = j - (KW - W);
-            w[j][e] = i >= 0 && c + e < D ? Elem<T>::to_f32(weight[(int64_t)(c + e) * W + i]) : 0.f;
-        }
+        for (int e = 0; e < V; ++e)
+#pragma unroll
+            for (int j = 0; j < KW; ++j) w[j][e] = r[(e * KW + j) / 4][(e * KW + j) % 4];
+    } else {
+#pragma unroll
+        for (int j = 0; j < KW; ++j)
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const int i = j - (KW - W);
+                w[j][e] = i >= 0 && e < n ? Elem<T>::to_f32(weight[(int64_t)(c + e) * W + i]) : 0.f;
+            }
+    }
 }
 
-// x at token t of sequence b (t < 0: the initial state's row W - 1 + t), as raw bytes.
-template <typename T>
-__device__ __forceinline__ u32x4 token(const ConvArgs &a, const T *xb, const T *ib, int t, int c) {
-    if (t >= 0) return load_vec<T>(xb + (int64_t)t * a.x_token + c, a.D - c);
-    if (ib != nullptr && t >= 1 - a.W) return load_vec<T>(ib + (int64_t)(a.W - 1 + t) * a.D + c, a.D - c);
-    return u32x4{0, 0, 0, 0};
+// sigmoid by the hardware's exponential and reciprocal (an ulp each; the exponent's own
+// rounding is relative to u, as are those of the sum that u is).
+__device__ __forceinline__ float fast_sigmoid(float u) {
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * u));
 }
 
-template <typename T, int KW, bool EXACT>
+// x of sequence b (ib: its initial state) at token t < n, zero before the state's first.
+template <typename T, int V, Reach R>
+__device__ __forceinline__ Raw<T, V> token(const ConvArgs &a, const T *xb, const T *ib, int t, int n, int c) {
+    Raw<T, V> r;
+    const bool early = t < 0, on = t < n && (!early || (ib != nullptr && t > -a.W));
+    const T *p = on ? (early ? ib + (int64_t)(a.W - 1 + t) * a.D : xb + (int64_t)t * a.x_token) : xb;
+    r.template load<R>(p, c, a.D, on);
+    return r;
+}
+
+// A thread makes `RUN` tokens: their inputs and the W - 1 before are all asked for first.
+template <typename T, int KW, bool EXACT, int V, Reach R, int RUN>
 __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvArgs a, T *__restrict__ y, T *__restrict__ last,
                                                             int64_t walks) {
-    constexpr int V = kVec<T>;
     if (EXACT) a.W = KW;
     const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int runs = (a.L + a.run - 1) / a.run;
+    const int runs = (a.L + RUN - 1) / RUN;
     if (id >= walks) {  // the state behind the last token: W - 1 rows a sequence
         const int64_t k = id - walks;
         const int W1 = a.W - 1;
         if (last == nullptr || k >= (int64_t)a.B * W1 * a.nvec) return;
         const int c = (int)(k % a.nvec) * V, j = (int)(k / a.nvec) % W1, b = (int)(k / a.nvec / W1);
         const T *ib = a.initial ? (const T *)a.initial + (int64_t)b * W1 * a.D : nullptr;
-        float v[V];
-        widen<T>(token<T>(a, (const T *)a.x + b * a.x_batch, ib, length_of(a.lengths, b, a.L) - W1 + j, c), v);
-        store_vec<T>(last + ((int64_t)b * W1 + j) * a.D + c, v, a.D - c);
+        const int n = length_of(a.lengths, b, a.L);
+        token<T, V, R>(a, (const T *)a.x + b * a.x_batch, ib, n - W1 + j, n, c)
+            .template store<R>(last + ((int64_t)b * W1 + j) * a.D, c, a.D);
         return;
     }
     const int c = (int)(id % a.nvec) * V;
     const int64_t rest = id / a.nvec;
-    const int t0 = (int)(rest % runs) * a.run, b = (int)(rest / runs);
+    const int t0 = (int)(rest % runs) * RUN, b = (int)(rest / runs);
     const int n = length_of(a.lengths, b, a.L);
-    const int t1 = t0 + a.run < a.L ? t0 + a.run : a.L;
     const T *xb = (const T *)a.x + b * a.x_batch;
     const T *ib = a.initial ? (const T *)a.initial + (int64_t)b * (a.W - 1) * a.D : nullptr;
-    T *yb = y + (int64_t)b * a.L * a.D + c;
-    float w[KW][V], bias[V], win[KW][V];
-    load_taps<T, KW>((const T *)a.weight, c, a.D, a.W, w);
-    widen<T>(load_vec<T>((const T *)a.bias + c, a.D - c), bias);
+    T *yb = y + ((int64_t)b * a.L + t0) * a.D;
+    Raw<T, V> in[RUN + KW - 1], bias;
+    float w[KW][V];
 #pragma unroll
-    for (int j = 1; j < KW; ++j)  // taps older than W - 1 read as zero: their weight is zero, x there need not be finite
-        if (t0 < n && j >= KW - a.W + 1) widen<T>(token<T>(a, xb, ib, t0 - KW + j, c), win[j]);
-        else
+    for (int k = 0; k < RUN + KW - 1; ++k) {
+        if (k < KW - a.W) in[k].r = typename Raw<T, V>::words(0);  // older than the taps
+        else in[k] = token<T, V, R>(a, xb, ib, t0 - (KW - 1) + k, n, c);
+    }
+    load_taps<T, KW, V, R, EXACT>((const T *)a.weight, c, a.D, a.W, w);
+    bias.template load<R>((const T *)a.bias, c, a.D, true);
 #pragma unroll
-            for (int e = 0; e < V; ++e) win[j][e] = 0.f;
-#pragma unroll 4
-    for (int t = t0; t < t1; ++t) {
-        float u[V];
-        if (t < n) {
+    for (int k = 0; k < RUN; ++k) {
+        if (t0 + k >= a.L) break;
+        float o[V];
 #pragma unroll
-            for (int j = 0; j + 1 < KW; ++j)
+        for (int e = 0; e < V; ++e) {
+            float u = bias[e];
 #pragma unroll
-                for (int e = 0; e < V; ++e) win[j][e] = j >= KW - a.W ? win[j + 1][e] : 0.f;
-            widen<T>(load_vec<T>(xb + (int64_t)t * a.x_token + c, a.D - c), win[KW - 1]);
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                float s = bias[e];
-#pragma unroll
-                for (int j = 0; j < KW; ++j) s += w[j][e] * win[j][e];
-                u[e] = s * sigmoid(s);
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < V; ++e) u[e] = 0.f;
+            for (int j = 0; j < KW; ++j) u += (EXACT || j >= KW - a.W) ? w[j][e] * in[k + j][e] : 0.f;
+            o[e] = t0 + k < n ? u * fast_sigmoid(u) : 0.f;
         }
-        store_vec<T>(yb + (int64_t)t * a.D, u, a.D - c);
+        Raw<T, V> out;
+        out.set(o);
+        out.template store<R>(yb + (int64_t)k * a.D, c, a.D);
     }
 }
 
+constexpr int kBwdVec = 4;    // channels of a thread where it keeps windows and sums of them (backward), or has few (step)
+constexpr int kBwdBatch = 8;  // tokens asked for at once, a batch ahead of the one at work
+
 // Workgroup: cl threads along the channels by kThreads / cl walks of a.run tokens; its sums
 // over the walks go to row `split` of part [splits, D * W + D].
-template <typename T, int KW, bool EXACT>
+template <typename T, int KW, bool EXACT, Reach R>
 __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs a, const T *__restrict__ grad, int64_t g_batch,
                                                             int64_t g_token, const T *__restrict__ grad_state,
                                                             T *__restrict__ grad_x, T *__restrict__ grad_initial,
                                                             float *__restrict__ part, int cl, int blocks_c) {
-    constexpr int V = kVec<T>;
+    constexpr int V = kBwdVec, U = kBwdBatch;
     if (EXACT) a.W = KW;
     __shared__ float red[kThreads * V];
     const int lane = threadIdx.x % cl, walk = threadIdx.x / cl, walks = kThreads / cl;
@@ -128,7 +142,7 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs a, const T 
     const int block_c = blockIdx.x % blocks_c, split = blockIdx.x / blocks_c;
     const int c = (block_c * cl + lane) * V;
     const int64_t id = (int64_t)split * walks + walk;
-    float w[KW][V], bias[V], sw[KW][V] = {}, sb[V] = {};
+    float sw[KW][V] = {}, sb[V] = {};
     if (c < a.D && id < (int64_t)a.B * runs) {
         const int t0 = (int)(id % runs) * a.run, b = (int)(id / runs);
         const int n = length_of(a.lengths, b, a.L);
@@ -136,76 +150,88 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs a, const T 
         const int W1 = a.W - 1;
         const T *xb = (const T *)a.x + b * a.x_batch;
         const T *ib = a.initial ? (const T *)a.initial + (int64_t)b * W1 * a.D : nullptr;
-        const T *gb = grad + b * g_batch + c;
-        const T *gs = grad_state ? grad_state + (int64_t)b * W1 * a.D + c : nullptr;
-        T *gx = grad_x + (int64_t)b * a.L * a.D + c;
-        T *gi = grad_initial ? grad_initial + (int64_t)b * W1 * a.D + c : nullptr;
-        load_taps<T, KW>((const T *)a.weight, c, a.D, a.W, w);
-        widen<T>(load_vec<T>((const T *)a.bias + c, a.D - c), bias);
-        float win[KW][V], du[KW][V] = {};
+        const T *gb = grad + b * g_batch;
+        const T *gs = grad_state ? grad_state + (int64_t)b * W1 * a.D : nullptr;
+        T *gx = grad_x + (int64_t)b * a.L * a.D;
+        T *gi = grad_initial ? grad_initial + (int64_t)b * W1 * a.D : nullptr;
+        float w[KW][V], du[KW][V] = {};
+        Raw<T, V> win[KW], bias, x[U], g[U];
+        load_taps<T, KW, V, R, EXACT>((const T *)a.weight, c, a.D, a.W, w);
+        bias.template load<R>((const T *)a.bias, c, a.D, true);
 #pragma unroll
-        for (int j = 1; j < KW; ++j)
-            if (t0 < n && j >= KW - a.W + 1) widen<T>(token<T>(a, xb, ib, t0 - KW + j, c), win[j]);
-            else
+        for (int j = 1; j < KW; ++j) {
+            if (j > KW - a.W) win[j] = token<T, V, R>(a, xb, ib, t0 - KW + j, n, c);
+            else win[j].r = typename Raw<T, V>::words(0);
+        }
+        auto ask = [&](int from) {
 #pragma unroll
-                for (int e = 0; e < V; ++e) win[j][e] = 0.f;
-        // Step t makes du[t] and emits the gradient of x at t - W1, whose last term it is.
-        for (int t = t0; t < t1 + W1; ++t) {
-#pragma unroll
-            for (int j = 0; j + 1 < KW; ++j)
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    win[j][e] = j >= KW - a.W ? win[j + 1][e] : 0.f;
-                    du[j][e] = du[j + 1][e];
-                }
-            if (t < n) {
-                float g[V];
-                widen<T>(load_vec<T>(xb + (int64_t)t * a.x_token + c, a.D - c), win[KW - 1]);
-                widen<T>(load_vec<T>(gb + (int64_t)t * g_token, a.D - c), g);
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    float s = bias[e];
-#pragma unroll
-                    for (int j = 0; j < KW; ++j) s += w[j][e] * win[j][e];
-                    const float sg = sigmoid(s);
-                    du[KW - 1][e] = g[e] * sg * (1.f + s * (1.f - sg));
-                }
-                if (t < t1) {
-#pragma unroll
-                    for (int e = 0; e < V; ++e) {
-#pragma unroll
-                        for (int j = 0; j < KW; ++j) sw[j][e] += du[KW - 1][e] * win[j][e];
-                        sb[e] += du[KW - 1][e];
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < V; ++e) du[KW - 1][e] = win[KW - 1][e] = 0.f;
+            for (int k = 0; k < U; ++k) {
+                const int t = from + k;
+                const bool on = t < n && t < t1 + W1;
+                x[k].template load<R>(xb + (on ? (int64_t)t * a.x_token : 0), c, a.D, on);
+                g[k].template load<R>(gb + (on ? (int64_t)t * g_token : 0), c, a.D, on);
             }
-            const int at = t - W1;  // grad_x[at] = sum_k w[KW - 1 - k] du[at + k], du[at + k] in slot KW - W + k
-            if (at < t0 && !(t0 == 0 && gi != nullptr)) continue;
-            if (at >= t1) continue;
-            float s[V] = {};
+        };
+        ask(t0);
+        for (int from = t0; from < t1 + W1; from += U) {
+            Raw<T, V> xc[U], gc[U];
 #pragma unroll
-            for (int q = 0; q < KW; ++q) {
-                // slot q holds du[t - (KW - 1) + q] = du[at + k], k = q - (KW - W); its weight's tap is W - 1 - k
-                if (q >= KW - a.W) {
+            for (int k = 0; k < U; ++k) {
+                xc[k] = x[k];
+                gc[k] = g[k];
+            }
+            if (from + U < t1 + W1) ask(from + U);
+            // step t makes du[t] (zero past the length, as g is) and emits the gradient of x at t - W1, whose last
+            // term it is
 #pragma unroll
-                    for (int r = 0; r < KW; ++r)
-                        if (r == 2 * KW - 1 - a.W - q) {
+            for (int k = 0; k < U; ++k) {
+                const int t = from + k, at = t - W1;
+                const float own = t < t1 ? 1.f : 0.f;
 #pragma unroll
-                            for (int e = 0; e < V; ++e) s[e] += w[r][e] * du[q][e];
+                for (int j = 0; j + 1 < KW; ++j) {
+                    win[j].r = EXACT || j >= KW - a.W ? win[j + 1].r : typename Raw<T, V>::words(0);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) du[j][e] = du[j + 1][e];
+                }
+                win[KW - 1] = xc[k];
+                float o[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    float u = bias[e];
+#pragma unroll
+                    for (int j = 0; j < KW; ++j) u += w[j][e] * win[j][e];
+                    const float sg = fast_sigmoid(u);
+                    const float d = gc[k][e] * (sg * (1.f + u * (1.f - sg)));
+                    du[KW - 1][e] = d;
+                    const float mine = d * own;
+#pragma unroll
+                    for (int j = 0; j < KW; ++j) sw[j][e] += mine * win[j][e];
+                    sb[e] += mine;
+                    // du[at + k] is in slot KW - W + k, the tap that it meets W - 1 - k
+                    float s = 0.f;
+#pragma unroll
+                    for (int q = 0; q < KW; ++q) {
+                        if constexpr (EXACT) {
+                            s += w[KW - 1 - q][e] * du[q][e];
+                        } else {
+#pragma unroll
+                            for (int r = 0; r < KW; ++r)
+                                if (q >= KW - a.W && r == 2 * KW - 1 - a.W - q) s += w[r][e] * du[q][e];
                         }
+                    }
+                    o[e] = s;
                 }
-            }
-            if (gs != nullptr && at >= n - W1 && at < n) {
-                float f[V];
-                widen<T>(load_vec<T>(gs + (int64_t)(at - (n - W1)) * a.D, a.D - c), f);
+                if (at >= t1 || (at < t0 && !(t0 == 0 && gi != nullptr && at >= -W1))) continue;
+                if (gs != nullptr && at >= n - W1 && at < n) {
+                    Raw<T, V> f;
+                    f.template load<R>(gs + (int64_t)(at - (n - W1)) * a.D, c, a.D, true);
 #pragma unroll
-                for (int e = 0; e < V; ++e) s[e] += f[e];
+                    for (int e = 0; e < V; ++e) o[e] += f[e];
+                }
+                Raw<T, V> out;
+                out.set(o);
+                out.template store<R>(at >= 0 ? gx + (int64_t)at * a.D : gi + (int64_t)(W1 + at) * a.D, c, a.D);
             }
-            if (at >= 0) store_vec<T>(gx + (int64_t)at * a.D, s, a.D - c);
-            else store_vec<T>(gi + (int64_t)(W1 + at) * a.D, s, a.D - c);
         }
     }
     const int64_t M = (int64_t)a.D * (a.W + 1);
@@ -230,121 +256,143 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs a, const T 
 
 // One token of each sequence: state rows hold the W - 1 inputs before it.  A slot outside
 // [0, S) is a place without a sequence: y is zero and no state is touched.
-template <typename T, int KW, bool EXACT>
+template <typename T, int KW, bool EXACT, Reach R>
 __global__ __launch_bounds__(kThreads) void conv_step_kernel(const T *__restrict__ x, int64_t x_stride,
                                                              const T *__restrict__ weight, const T *__restrict__ bias,
                                                              T *__restrict__ state, const int *__restrict__ slots,
                                                              T *__restrict__ y, int B, int64_t S, int D, int W,
                                                              int nvec) {
-    constexpr int V = kVec<T>;
+    constexpr int V = kBwdVec;
     if (EXACT) W = KW;
     const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     if (id >= (int64_t)B * nvec) return;
     const int c = (int)(id % nvec) * V, b = (int)(id / nvec);
     const int64_t slot = slots != nullptr ? slots[b] : b;
-    float u[V] = {};
+    float w[KW][V], u[V];
+    Raw<T, V> in[KW], out;
+    in[KW - 1].template load<R>(x + b * x_stride, c, D, true);
+    load_taps<T, KW, V, R, EXACT>(weight, c, D, W, w);
+    out.template load<R>(bias, c, D, true);
     if (slot >= 0 && slot < S) {
-        T *st = state + slot * (W - 1) * D + c;
-        float w[KW][V], v[V];
-        u32x4 in[KW];
+        T *st = state + slot * (W - 1) * D;
+#pragma unroll
+        for (int j = 0; j < KW - 1; ++j)
+            if (j >= KW - W) in[j].template load<R>(st + (int64_t)(j - (KW - W)) * D, c, D, true);
+#pragma unroll
+        for (int e = 0; e < V; ++e) u[e] = out[e];
 #pragma unroll
         for (int j = 0; j < KW; ++j) {
-            in[j] = u32x4{0, 0, 0, 0};
-            if (j == KW - 1) in[j] = load_vec<T>(x + b * x_stride + c, D - c);
-            else if (j >= KW - W) in[j] = load_vec<T>(st + (int64_t)(j - (KW - W)) * D, D - c);
-        }
-        load_taps<T, KW>(weight, c, D, W, w);
-        widen<T>(load_vec<T>(bias + c, D - c), u);
+            if (j < KW - W) continue;
 #pragma unroll
-        for (int j = 0; j < KW; ++j) {
-            widen<T>(in[j], v);
-#pragma unroll
-            for (int e = 0; e < V; ++e) u[e] += w[j][e] * v[e];
-            if (j >= KW - W + 1) store_vec<T>(st + (int64_t)(j - (KW - W) - 1) * D, v, D - c);
+            for (int e = 0; e < V; ++e) u[e] += w[j][e] * in[j][e];
+            if (j > KW - W) in[j].template store<R>(st + (int64_t)(j - (KW - W) - 1) * D, c, D);
         }
 #pragma unroll
-        for (int e = 0; e < V; ++e) u[e] *= sigmoid(u[e]);
+        for (int e = 0; e < V; ++e) u[e] *= fast_sigmoid(u[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) u[e] = 0.f;
     }
-    store_vec<T>(y + (int64_t)b * D + c, u, D - c);
+    out.set(u);
+    out.template store<R>(y + (int64_t)b * D, c, D);
 }
 
 namespace {
-
-// Tokens a thread walks: as long as at least 2^18 threads (16 waves a SIMD's worth of
-// loads in flight over the chip) are left, from 1 to 32.
-int run_of(int64_t B, int64_t L, int64_t nvec) {
-    int run = 1;
-    while (run < 32 && B * L * nvec / (2 * run) >= (1 << 18)) run *= 2;
-    return run;
-}
 
 struct BwdShape {
     int run, cl;
     int64_t blocks_c, splits;
 };
-// The backward's halo costs W - 1 extra tokens a run and its partials one row a
-// workgroup: runs of 32, shorter only where too few threads would be left.
-BwdShape bwd_shape(int64_t B, int64_t L, int64_t D, bool bf16) {
-    const int64_t nvec = (D * (bf16 ? 2 : 4) + 15) / 16;
+// A walk takes whole batches with the W - 1 tokens past its run: four of them (the halo is
+// then a tenth for W = 4), fewer only where too few threads would be left.
+BwdShape bwd_shape(int64_t B, int64_t L, int64_t D, int W) {
+    const int64_t nvec = (D + kBwdVec - 1) / kBwdVec;
     int cl = 8;
-    while (cl < 32 && cl < nvec) cl *= 2;
-    int run = 32;
-    while (run > 4 && B * ((L + run - 1) / run) * nvec < (1 << 16)) run /= 2;
+    while (cl < 64 && cl < nvec) cl *= 2;
+    int batches = 4;
+    while (batches > 1 && B * (L / (kBwdBatch * batches) + 1) * nvec < (1 << 16)) batches /= 2;
+    const int run = kBwdBatch * batches - (W - 1);
     const int64_t walks = B * ((L + run - 1) / run), per = kThreads / cl;
     return {run, cl, (nvec + cl - 1) / cl, (walks + per - 1) / per};
 }
 
-ConvArgs args_of(const Conv &a, bool bf16, int run) {
+ConvArgs args_of(const Conv &a, int V, int run) {
     return {a.x, a.weight, a.bias, a.initial, a.lengths, a.x_batch, a.x_token, (int)a.B, (int)a.L, (int)a.D, a.W,
-            (int)((a.D * (bf16 ? 2 : 4) + 15) / 16), run};
+            (int)((a.D + V - 1) / V), run};
 }
 
 // Widths 2 to 4 have kernels of their own; 1 runs in two taps and 5 to 8 in eight, the
-// older ones with zero weights and no reads.
-#define DDPM_SEQ_CONV_WIDTHS(X)    \
-    if (a.W == 4) X(4, true)       \
-    else if (a.W == 3) X(3, true)  \
-    else if (a.W == 2) X(2, true)  \
-    else if (a.W == 1) X(2, false) \
-    else X(8, false)
+// older ones with zero weights and no reads.  Each by how the rows of D channels are reached.
+#define DDPM_SEQ_CONV_REACH(R, W, X)     \
+    if ((W) == 4) X(4, true, R)          \
+    else if ((W) == 3) X(3, true, R)     \
+    else if ((W) == 2) X(2, true, R)     \
+    else if ((W) == 1) X(2, false, R)    \
+    else X(8, false, R)
+#define DDPM_SEQ_CONV_WIDTHS(W, D, V, X)                              \
+    if (reach_of(D, V) == kWhole) { DDPM_SEQ_CONV_REACH(kWhole, W, X) } \
+    else if (reach_of(D, V) == kOdd) { DDPM_SEQ_CONV_REACH(kOdd, W, X) } \
+    else { DDPM_SEQ_CONV_REACH(kShort, W, X) }
 
-template <typename T>
+template <typename T, int RUN>
 hipError_t conv_fwd(const Conv &a, void *y, void *last, hipStream_t stream) {
-    ConvArgs k = args_of(a, Elem<T>::is_bf16, 1);
-    k.run = run_of(a.B, a.L, k.nvec);
-    const int64_t walks = a.B * ((a.L + k.run - 1) / k.run) * k.nvec;
+    constexpr int V = kVec<T>;
+    const ConvArgs k = args_of(a, V, RUN);
+    const int64_t walks = a.B * ((a.L + RUN - 1) / RUN) * k.nvec;
     const int64_t items = walks + (last != nullptr ? a.B * (a.W - 1) * k.nvec : 0);
     const int64_t blocks = (items + kThreads - 1) / kThreads;
     if (blocks > 0x7fffffff) return hipErrorInvalidConfiguration;
-#define X(KW, EX)                                                                                                  \
-    hipLaunchKernelGGL((conv_fwd_kernel<T, KW, EX>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, k, (T *)y, \
-                       (T *)last, walks);
-    DDPM_SEQ_CONV_WIDTHS(X)
+#define X(KW, EX, R)                                                                                               \
+    hipLaunchKernelGGL((conv_fwd_kernel<T, KW, EX, V, R, RUN>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, \
+                       k, (T *)y, (T *)last, walks);
+    DDPM_SEQ_CONV_WIDTHS(a.W, a.D, V, X)
 #undef X
     return hipGetLastError();
+}
+
+// Eight tokens a thread (11 reads for 8 results at W = 4); two where that would leave the
+// chip with fewer than eight waves a compute unit.
+template <typename T>
+hipError_t conv_fwd(const Conv &a, void *y, void *last, hipStream_t stream) {
+    const int64_t vectors = a.B * a.L * ((a.D + kVec<T> - 1) / kVec<T>);
+    return vectors / 8 >= 256 * 8 * kWave ? conv_fwd<T, 8>(a, y, last, stream) : conv_fwd<T, 2>(a, y, last, stream);
 }
 
 template <typename T>
 hipError_t conv_bwd(const Conv &a, const void *grad, int64_t g_batch, int64_t g_token, const void *grad_state,
                     void *grad_x, void *grad_initial, void *grad_weight, void *grad_bias, float *part,
                     hipStream_t stream) {
-    const BwdShape s = bwd_shape(a.B, a.L, a.D, Elem<T>::is_bf16);
-    const ConvArgs k = args_of(a, Elem<T>::is_bf16, s.run);
+    const BwdShape s = bwd_shape(a.B, a.L, a.D, a.W);
+    const ConvArgs k = args_of(a, kBwdVec, s.run);
     if (s.splits * s.blocks_c > 0x7fffffff) return hipErrorInvalidConfiguration;
-#define X(KW, EX)                                                                                                         \
-    hipLaunchKernelGGL((conv_bwd_kernel<T, KW, EX>), dim3((unsigned)(s.blocks_c * s.splits)), dim3(kThreads), 0,     \
-                       stream, k, (const T *)grad, g_batch, g_token, (const T *)grad_state, (T *)grad_x,              \
+#define X(KW, EX, R)                                                                                              \
+    hipLaunchKernelGGL((conv_bwd_kernel<T, KW, EX, R>), dim3((unsigned)(s.blocks_c * s.splits)), dim3(kThreads),  \
+                       0, stream, k, (const T *)grad, g_batch, g_token, (const T *)grad_state, (T *)grad_x,           \
                        (T *)grad_initial, part, s.cl, (int)s.blocks_c);
-    DDPM_SEQ_CONV_WIDTHS(X)
+    DDPM_SEQ_CONV_WIDTHS(a.W, a.D, kBwdVec, X)
 #undef X
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     return launch_sum_rows(part, (int)s.splits, a.D * a.W, a.D, grad_weight, grad_bias, Elem<T>::is_bf16, stream);
 }
 
+template <typename T>
+hipError_t conv_step(const void *x, int64_t x_stride, const void *weight, const void *bias, void *state,
+                     const int *slots, void *y, int64_t B, int64_t S, int64_t D, int W, hipStream_t stream) {
+    const int64_t nvec = (D + kBwdVec - 1) / kBwdVec, blocks = (B * nvec + kThreads - 1) / kThreads;
+    if (blocks > 0x7fffffff) return hipErrorInvalidConfiguration;
+#define X(KW, EX, R)                                                                                              \
+    hipLaunchKernelGGL((conv_step_kernel<T, KW, EX, R>), dim3((unsigned)blocks), dim3(kThreads), 0, stream,       \
+                       (const T *)x, x_stride, (const T *)weight, (const T *)bias, (T *)state, slots, (T *)y, (int)B, \
+                       S, (int)D, W, (int)nvec);
+    DDPM_SEQ_CONV_WIDTHS(W, D, kBwdVec, X)
+#undef X
+    return hipGetLastError();
+}
+
 }  // namespace
 
-int conv_partials(int64_t B, int64_t L, int64_t D, bool bf16) { return (int)bwd_shape(B, L, D, bf16).splits; }
+int conv_partials(int64_t B, int64_t L, int64_t D, int W) { return (int)bwd_shape(B, L, D, W).splits; }
 
 hipError_t launch_conv_fwd(const Conv &a, void *y, void *last, bool bf16, hipStream_t stream) {
     return bf16 ? conv_fwd<bf16_t>(a, y, last, stream) : conv_fwd<float>(a, y, last, stream);
@@ -357,23 +405,6 @@ hipError_t launch_conv_bwd(const Conv &a, const void *grad, int64_t g_batch, int
                                    part, stream)
                 : conv_bwd<float>(a, grad, g_batch, g_token, grad_state, grad_x, grad_initial, grad_weight, grad_bias,
                                   part, stream);
-}
-
-template <typename T>
-static hipError_t conv_step(const void *x, int64_t x_stride, const void *weight, const void *bias, void *state,
-                            const int *slots, void *y, int64_t B, int64_t S, int64_t D, int W, hipStream_t stream) {
-    const int64_t nvec = (D + kVec<T> - 1) / kVec<T>, blocks = (B * nvec + kThreads - 1) / kThreads;
-    if (blocks > 0x7fffffff) return hipErrorInvalidConfiguration;
-    struct {
-        int W;
-    } a = {W};
-#define X(KW, EX)                                                                                                          \
-    hipLaunchKernelGGL((conv_step_kernel<T, KW, EX>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, (const T *)x,     \
-                       x_stride, (const T *)weight, (const T *)bias, (T *)state, slots, (T *)y, (int)B, S, (int)D, W,  \
-                       (int)nvec);
-    DDPM_SEQ_CONV_WIDTHS(X)
-#undef X
-    return hipGetLastError();
 }
 
 hipError_t launch_conv_step(const void *x, int64_t x_stride, const void *weight, const void *bias, void *state,

@@ -28,7 +28,7 @@ struct Conv {
     int W;
 };
 // Rows of the float32 partials [S, D * W + D] of launch_conv_bwd.
-int conv_partials(int64_t B, int64_t L, int64_t D, bool bf16);
+int conv_partials(int64_t B, int64_t L, int64_t D, int W);
 hipError_t launch_conv_fwd(const Conv &a, void *y, void *final_state, bool bf16, hipStream_t stream);
 hipError_t launch_conv_bwd(const Conv &a, const void *grad, int64_t g_batch, int64_t g_token, const void *grad_state,
                            void *grad_x, void *grad_initial, void *grad_weight, void *grad_bias, float *part, bool bf16,

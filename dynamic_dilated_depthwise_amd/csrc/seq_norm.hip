@@ -36,7 +36,7 @@ __device__ __forceinline__ float group_sum(float v, float *red) {
     return v;
 }
 
-template <typename T, int LPR, int NV>
+template <typename T, int LPR, int NV, Reach R>
 __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(const T *__restrict__ x, const T *__restrict__ weight,
                                                             const T *__restrict__ bias, T *__restrict__ y,
                                                             float *__restrict__ mean, float *__restrict__ rstd,
@@ -47,12 +47,11 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(const T *__restrict_
     const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / LPR;
     const bool on = row < rows;
     const T *xr = x + (on ? row : 0) * x_stride;
-    float v[NV][V];
+    Raw<T, V> v[NV];
     float sum = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        const int c = (k * LPR + lane) * V;
-        widen<T>(load_vec<T>(xr + c, on ? C - c : 0), v[k]);
+        v[k].template load<R>(xr, (k * LPR + lane) * V, C, on);
 #pragma unroll
         for (int e = 0; e < V; ++e) sum += v[k][e];
     }
@@ -76,18 +75,20 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(const T *__restrict_
     for (int k = 0; k < NV; ++k) {
         const int c = (k * LPR + lane) * V;
         if (c >= C) continue;
-        float w[V], b[V];
-        widen<T>(load_vec<T>(weight + c, C - c), w);
-        widen<T>(load_vec<T>(bias + c, C - c), b);
+        Raw<T, V> w, b;
+        float o[V];
+        w.template load<R>(weight, c, C, true);
+        b.template load<R>(bias, c, C, true);
 #pragma unroll
-        for (int e = 0; e < V; ++e) w[e] = (v[k][e] - mu) * rs * w[e] + b[e];
-        store_vec<T>(yr + c, w, C - c);
+        for (int e = 0; e < V; ++e) o[e] = (v[k][e] - mu) * rs * w[e] + b[e];
+        w.set(o);
+        w.template store<R>(yr, c, C);
     }
 }
 
 // Rows longer than the registers of a workgroup hold: three passes, the later two mostly
 // from the caches.
-template <typename T>
+template <typename T, Reach R>
 __global__ __launch_bounds__(kThreads) void norm_fwd_long_kernel(const T *__restrict__ x, const T *__restrict__ weight,
                                                                  const T *__restrict__ bias, T *__restrict__ y,
                                                                  float *__restrict__ mean, float *__restrict__ rstd,
@@ -96,15 +97,16 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_long_kernel(const T *__rest
     __shared__ float red[4];
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
         const T *xr = x + row * x_stride;
-        float v[V], sum = 0.f, sq = 0.f;
+        Raw<T, V> v, w, b;
+        float sum = 0.f, sq = 0.f, o[V];
         for (int c = threadIdx.x * V; c < C; c += kThreads * V) {
-            widen<T>(load_vec<T>(xr + c, C - c), v);
+            v.template load<R>(xr, c, C, true);
 #pragma unroll
             for (int e = 0; e < V; ++e) sum += v[e];
         }
         const float mu = group_sum<kThreads>(sum, red) / (float)C;
         for (int c = threadIdx.x * V; c < C; c += kThreads * V) {
-            widen<T>(load_vec<T>(xr + c, C - c), v);
+            v.template load<R>(xr, c, C, true);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 const float d = c + e < C ? v[e] - mu : 0.f;
@@ -117,20 +119,20 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_long_kernel(const T *__rest
             rstd[row] = rs;
         }
         for (int c = threadIdx.x * V; c < C; c += kThreads * V) {
-            float w[V], b[V];
-            widen<T>(load_vec<T>(xr + c, C - c), v);
-            widen<T>(load_vec<T>(weight + c, C - c), w);
-            widen<T>(load_vec<T>(bias + c, C - c), b);
+            v.template load<R>(xr, c, C, true);
+            w.template load<R>(weight, c, C, true);
+            b.template load<R>(bias, c, C, true);
 #pragma unroll
-            for (int e = 0; e < V; ++e) w[e] = (v[e] - mu) * rs * w[e] + b[e];
-            store_vec<T>(y + row * C + c, w, C - c);
+            for (int e = 0; e < V; ++e) o[e] = (v[e] - mu) * rs * w[e] + b[e];
+            v.set(o);
+            v.template store<R>(y + row * C, c, C);
         }
     }
 }
 
 // Each workgroup walks rows blockIdx * ROWS + group, + gridDim * ROWS, ..., and writes its
 // column sums as row blockIdx of part_w and part_b [gridDim, C].
-template <typename T, int LPR, int NV>
+template <typename T, int LPR, int NV, Reach R>
 __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(const T *__restrict__ grad, const T *__restrict__ x,
                                                             const T *__restrict__ weight, const float *__restrict__ mean,
                                                             const float *__restrict__ rstd, T *__restrict__ grad_x,
@@ -140,38 +142,32 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(const T *__restrict_
     __shared__ float red[4];
     __shared__ float cols[ROWS > 1 ? kThreads * V : 1];
     const int lane = threadIdx.x % LPR, group = threadIdx.x / LPR;
-    float w[NV][V], sw[NV][V] = {}, sb[NV][V] = {};
+    Raw<T, V> w[NV];
+    float sw[NV][V] = {}, sb[NV][V] = {};
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int c = (k * LPR + lane) * V;
-        widen<T>(load_vec<T>(weight + c, C - c), w[k]);
-    }
+    for (int k = 0; k < NV; ++k) w[k].template load<R>(weight, (k * LPR + lane) * V, C, true);
     const float inv = 1.f / (float)C;
     for (int64_t first = (int64_t)blockIdx.x * ROWS; first < rows; first += (int64_t)gridDim.x * ROWS) {
         const int64_t row = first + group;
         const bool on = row < rows;
         const T *xr = x + (on ? row : 0) * x_stride, *gr = grad + (on ? row : 0) * g_stride;
         const float mu = on ? mean[row] : 0.f, rs = on ? rstd[row] : 0.f;
-        u32x4 rx[NV], rg[NV];
+        Raw<T, V> xv[NV], gv[NV];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int c = (k * LPR + lane) * V;
-            rx[k] = load_vec<T>(xr + c, on ? C - c : 0);
-            rg[k] = load_vec<T>(gr + c, on ? C - c : 0);
+            xv[k].template load<R>(xr, (k * LPR + lane) * V, C, on);
+            gv[k].template load<R>(gr, (k * LPR + lane) * V, C, on);
         }
         float s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            float xv[V], gv[V];
-            widen<T>(rx[k], xv);
-            widen<T>(rg[k], gv);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                const float xh = (xv[e] - mu) * rs, gw = gv[e] * w[k][e];  // g is zero past the row's end
+                const float xh = (xv[k][e] - mu) * rs, gw = gv[k][e] * w[k][e];  // g is zero past the row's end
                 s1 += gw;
                 s2 += gw * xh;
-                sw[k][e] += gv[e] * xh;
-                sb[k][e] += gv[e];
+                sw[k][e] += gv[k][e] * xh;
+                sb[k][e] += gv[k][e];
             }
         }
         s1 = group_sum<LPR>(s1, red) * inv;
@@ -181,12 +177,11 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(const T *__restrict_
             for (int k = 0; k < NV; ++k) {
                 const int c = (k * LPR + lane) * V;
                 if (c >= C) continue;
-                float xv[V], gv[V];
-                widen<T>(rx[k], xv);
-                widen<T>(rg[k], gv);
+                float o[V];
 #pragma unroll
-                for (int e = 0; e < V; ++e) gv[e] = rs * (gv[e] * w[k][e] - s1 - (xv[e] - mu) * rs * s2);
-                store_vec<T>(grad_x + row * C + c, gv, C - c);
+                for (int e = 0; e < V; ++e) o[e] = rs * (gv[k][e] * w[k][e] - s1 - (xv[k][e] - mu) * rs * s2);
+                xv[k].set(o);
+                xv[k].template store<R>(grad_x + row * C, c, C);
             }
         }
     }
@@ -216,9 +211,9 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_kernel(const T *__restrict_
     }
 }
 
-// Rows longer than the registers hold: grad_x from three passes over the row, one
+// Rows longer than the registers hold: grad_x from two passes over the row, one
 // workgroup a row; the column sums from a second kernel, a thread a column.
-template <typename T>
+template <typename T, Reach R>
 __global__ __launch_bounds__(kThreads) void norm_bwd_long_kernel(const T *__restrict__ grad, const T *__restrict__ x,
                                                                  const T *__restrict__ weight,
                                                                  const float *__restrict__ mean,
@@ -229,11 +224,12 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_long_kernel(const T *__rest
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
         const T *xr = x + row * x_stride, *gr = grad + row * g_stride;
         const float mu = mean[row], rs = rstd[row];
-        float s1 = 0.f, s2 = 0.f, xv[V], gv[V], w[V];
+        float s1 = 0.f, s2 = 0.f, o[V];
+        Raw<T, V> xv, gv, w;
         for (int c = threadIdx.x * V; c < C; c += kThreads * V) {
-            widen<T>(load_vec<T>(xr + c, C - c), xv);
-            widen<T>(load_vec<T>(gr + c, C - c), gv);
-            widen<T>(load_vec<T>(weight + c, C - c), w);
+            xv.template load<R>(xr, c, C, true);
+            gv.template load<R>(gr, c, C, true);
+            w.template load<R>(weight, c, C, true);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 s1 += gv[e] * w[e];
@@ -243,12 +239,13 @@ __global__ __launch_bounds__(kThreads) void norm_bwd_long_kernel(const T *__rest
         s1 = group_sum<kThreads>(s1, red) / (float)C;
         s2 = group_sum<kThreads>(s2, red) / (float)C;
         for (int c = threadIdx.x * V; c < C; c += kThreads * V) {
-            widen<T>(load_vec<T>(xr + c, C - c), xv);
-            widen<T>(load_vec<T>(gr + c, C - c), gv);
-            widen<T>(load_vec<T>(weight + c, C - c), w);
+            xv.template load<R>(xr, c, C, true);
+            gv.template load<R>(gr, c, C, true);
+            w.template load<R>(weight, c, C, true);
 #pragma unroll
-            for (int e = 0; e < V; ++e) gv[e] = rs * (gv[e] * w[e] - s1 - (xv[e] - mu) * rs * s2);
-            store_vec<T>(grad_x + row * C + c, gv, C - c);
+            for (int e = 0; e < V; ++e) o[e] = rs * (gv[e] * w[e] - s1 - (xv[e] - mu) * rs * s2);
+            xv.set(o);
+            xv.template store<R>(grad_x + row * C, c, C);
         }
     }
 }
@@ -337,7 +334,7 @@ Shape shape_of(int64_t C) {
 
 #define DDPM_SEQ_NORM_SHAPES(X) X(16, 1) X(64, 1) X(64, 2) X(64, 4) X(256, 2) X(256, 4) X(256, 8)
 
-template <typename T>
+template <typename T, Reach R>
 hipError_t norm_fwd(const void *x, const void *weight, const void *bias, void *y, float *mean, float *rstd, int64_t rows,
                     int64_t C, int64_t x_stride, float eps, hipStream_t stream) {
     const Shape s = shape_of<T>(C);
@@ -345,18 +342,23 @@ hipError_t norm_fwd(const void *x, const void *weight, const void *bias, void *y
     if (blocks > 0x7fffffff) return hipErrorInvalidConfiguration;
 #define X(L, NV)                                                                                                      \
     if (s.lanes == L && s.nv == NV)                                                                                   \
-        hipLaunchKernelGGL((norm_fwd_kernel<T, L, NV>), dim3((unsigned)blocks), dim3(kThreads), 0, stream,            \
+        hipLaunchKernelGGL((norm_fwd_kernel<T, L, NV, R>), dim3((unsigned)blocks), dim3(kThreads), 0, stream,         \
                            (const T *)x, (const T *)weight, (const T *)bias, (T *)y, mean, rstd, rows, (int)C,        \
                            x_stride, eps);
-    DDPM_SEQ_NORM_SHAPES(X)
+    if constexpr (R == kShort) {
+        X(16, 1)
+    } else {
+        DDPM_SEQ_NORM_SHAPES(X)
+        if (!s.lanes)
+            hipLaunchKernelGGL((norm_fwd_long_kernel<T, R>), dim3((unsigned)blocks), dim3(kThreads), 0, stream,
+                               (const T *)x, (const T *)weight, (const T *)bias, (T *)y, mean, rstd, rows, (int)C,
+                               x_stride, eps);
+    }
 #undef X
-    if (!s.lanes)
-        hipLaunchKernelGGL((norm_fwd_long_kernel<T>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, (const T *)x,
-                           (const T *)weight, (const T *)bias, (T *)y, mean, rstd, rows, (int)C, x_stride, eps);
     return hipGetLastError();
 }
 
-template <typename T>
+template <typename T, Reach R>
 hipError_t norm_bwd(const void *grad, const void *x, const void *weight, const float *mean, const float *rstd,
                     void *grad_x, void *grad_weight, void *grad_bias, float *part, int64_t rows, int64_t C,
                     int64_t x_stride, int64_t g_stride, hipStream_t stream) {
@@ -364,21 +366,49 @@ hipError_t norm_bwd(const void *grad, const void *x, const void *weight, const f
     const int S = norm_partials(rows, C, Elem<T>::is_bf16);
 #define X(L, NV)                                                                                                      \
     if (s.lanes == L && s.nv == NV)                                                                                   \
-        hipLaunchKernelGGL((norm_bwd_kernel<T, L, NV>), dim3(S), dim3(kThreads), 0, stream, (const T *)grad,          \
+        hipLaunchKernelGGL((norm_bwd_kernel<T, L, NV, R>), dim3(S), dim3(kThreads), 0, stream, (const T *)grad,       \
                            (const T *)x, (const T *)weight, mean, rstd, (T *)grad_x, part, rows, (int)C, x_stride,    \
                            g_stride);
-    DDPM_SEQ_NORM_SHAPES(X)
-#undef X
-    if (!s.lanes) {
-        hipLaunchKernelGGL((norm_bwd_long_kernel<T>), dim3((unsigned)(rows < 4096 ? rows : 4096)), dim3(kThreads), 0,
-                           stream, (const T *)grad, (const T *)x, (const T *)weight, mean, rstd, (T *)grad_x, rows,
-                           (int)C, x_stride, g_stride);
-        hipLaunchKernelGGL((norm_cols_kernel<T>), dim3((unsigned)((C + kThreads - 1) / kThreads), S), dim3(kThreads), 0,
-                           stream, (const T *)grad, (const T *)x, mean, rstd, part, rows, (int)C, x_stride, g_stride);
+    if constexpr (R == kShort) {
+        X(16, 1)
+    } else {
+        DDPM_SEQ_NORM_SHAPES(X)
+        if (!s.lanes) {
+            hipLaunchKernelGGL((norm_bwd_long_kernel<T, R>), dim3((unsigned)(rows < 4096 ? rows : 4096)), dim3(kThreads),
+                               0, stream, (const T *)grad, (const T *)x, (const T *)weight, mean, rstd, (T *)grad_x,
+                               rows, (int)C, x_stride, g_stride);
+            hipLaunchKernelGGL((norm_cols_kernel<T>), dim3((unsigned)((C + kThreads - 1) / kThreads), S), dim3(kThreads),
+                               0, stream, (const T *)grad, (const T *)x, mean, rstd, part, rows, (int)C, x_stride,
+                               g_stride);
+        }
     }
+#undef X
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     return launch_sum_rows(part, S, C, C, grad_weight, grad_bias, Elem<T>::is_bf16, stream);
+}
+
+#define DDPM_SEQ_NORM_REACH(T, C, CALL)                   \
+    const Reach r = reach_of(C, kVec<T>);                 \
+    if (r == kWhole) return CALL(kWhole);                 \
+    return r == kOdd ? CALL(kOdd) : CALL(kShort);
+
+template <typename T>
+hipError_t norm_fwd(const void *x, const void *weight, const void *bias, void *y, float *mean, float *rstd, int64_t rows,
+                    int64_t C, int64_t x_stride, float eps, hipStream_t stream) {
+#define CALL(R) norm_fwd<T, R>(x, weight, bias, y, mean, rstd, rows, C, x_stride, eps, stream)
+    DDPM_SEQ_NORM_REACH(T, C, CALL)
+#undef CALL
+}
+
+template <typename T>
+hipError_t norm_bwd(const void *grad, const void *x, const void *weight, const float *mean, const float *rstd,
+                    void *grad_x, void *grad_weight, void *grad_bias, float *part, int64_t rows, int64_t C,
+                    int64_t x_stride, int64_t g_stride, hipStream_t stream) {
+#define CALL(R) \
+    norm_bwd<T, R>(grad, x, weight, mean, rstd, grad_x, grad_weight, grad_bias, part, rows, C, x_stride, g_stride, stream)
+    DDPM_SEQ_NORM_REACH(T, C, CALL)
+#undef CALL
 }
 
 }  // namespace
