@@ -10,7 +10,6 @@ import pytest
 import torch
 
 import dynamic_dilated_depthwise_amd as ddpm
-from dynamic_dilated_depthwise_amd import sequence as seq
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 INVALID, UNSUPPORTED = -1, -2
@@ -19,18 +18,51 @@ F32, BF16 = 0, 1
 A = [(k + 1) << 40 for k in range(24)]
 
 
+_P, _I64, _I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+
+
+class Scan(ctypes.Structure):
+    """ddpm_scan of the C header."""
+    _fields_ = ([(n, _P) for n in ("x", "dt", "B", "C", "A", "D", "dt_bias", "initial_state", "lengths")] +
+                [(n, _I64) for n in ("batch", "length", "x_batch", "x_token", "dt_batch", "dt_token", "B_batch", "B_token",
+                                     "C_batch", "C_token")] +
+                [(n, ctypes.c_int32) for n in ("heads", "P", "groups", "N", "dtype")])
+
+
+_SCAN = ctypes.POINTER(Scan)
+SIGNATURES = {
+    "ddpm_layer_norm_fwd": [_P] * 6 + [_I64] * 3 + [ctypes.c_float, _I, _P],
+    "ddpm_layer_norm_bwd": [_P] * 9 + [_I64] * 4 + [_I, _P],
+    "ddpm_causal_conv_fwd": [_P] * 7 + [_I64] * 3 + [_I] + [_I64] * 2 + [_I, _P],
+    "ddpm_causal_conv_bwd": [_P] * 12 + [_I64] * 3 + [_I] + [_I64] * 4 + [_I, _P],
+    "ddpm_causal_conv_step": [_P] * 6 + [_I64] * 3 + [_I, _I64, _I, _P],
+    "ddpm_selective_scan_fwd": [_SCAN, _P, _P, _I, _P, _P],
+    "ddpm_selective_scan_bwd": [_SCAN, _P, _P, _I64, _I64] + [_P] * 11,
+    "ddpm_selective_scan_step": [_SCAN, _P, _P, _I64, _P, _P],
+    "ddpm_layer_norm_bwd_workspace": [_I64, _I64, _I],
+    "ddpm_causal_conv_bwd_workspace": [_I64, _I64, _I64, _I, _I],
+    "ddpm_selective_scan_fwd_workspace": [_SCAN],
+    "ddpm_selective_scan_bwd_workspace": [_SCAN],
+}
+
+
 @pytest.fixture(scope="module")
 def lib():
     if not os.path.exists(ddpm.library_path()):
         from dynamic_dilated_depthwise_amd import build
         build.build(verbose=False)
-    return seq._load()
+    lib = ctypes.CDLL(ddpm.library_path())  # its own handle: declarations of this file only
+    for name, args in SIGNATURES.items():
+        f = getattr(lib, name)
+        f.argtypes = args
+        f.restype = _I64 if name.endswith("_workspace") else _I
+    return lib
 
 
 def test_exports_every_declared_function(lib):
     text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "ddpm_seq.h")).read(), flags=re.S)
     names = sorted(set(re.findall(r"\b(ddpm_[a-z_]+)\s*\(", text)))
-    assert len(names) == 12
+    assert names == sorted(SIGNATURES)
     for name in names:
         assert hasattr(lib, name), name
 
@@ -62,7 +94,7 @@ def _struct(L=8, **kw):
              length=L, x_batch=8 * 8, x_token=8, dt_batch=16, dt_token=2, B_batch=64, B_token=8, C_batch=64, C_token=8,
              heads=2, P=4, groups=1, N=8, dtype=F32)
     v.update(kw)
-    return seq._Scan(**v)
+    return Scan(**v)
 
 
 def _scan(lib, y=A[10], f=A[11], ws=A[12], **kw):
@@ -138,7 +170,8 @@ def test_workspace_sizes(lib):
     assert lib.ddpm_causal_conv_bwd_workspace(1, 1, 1, 9, BF16) == 0
 
 
-def test_binding_rejects_host_tensors():
+def test_binding_rejects_host_tensors(lib):
+    from dynamic_dilated_depthwise_amd import sequence as seq
     x = torch.zeros(2, 8, 16)
     with pytest.raises(ValueError):
         seq.layer_norm_fwd(x, torch.ones(16), torch.zeros(16))
@@ -158,5 +191,5 @@ def test_struct_matches_the_header():
     body = re.search(r"typedef struct \{(.*?)\} ddpm_scan;", text, re.S).group(1)
     names = [re.sub(r"\W", "", v.split()[-1]) for line in body.split(";") if line.strip()
              for v in line.replace("*", " ").split(",")]
-    assert names == [n for n, _ in seq._Scan._fields_]
-    assert ctypes.sizeof(seq._Scan) == 9 * 8 + 10 * 8 + 5 * 4 + 4
+    assert names == [n for n, _ in Scan._fields_]
+    assert ctypes.sizeof(Scan) == 9 * 8 + 10 * 8 + 5 * 4 + 4
