@@ -188,6 +188,13 @@ __device__ __forceinline__ f32x4 load4(const float *__restrict__ p, int n) {
 // masks (left in a vector register it costs the scan's kernels a factor of two and more).
 __device__ __forceinline__ int wave_of(int tid) { return __builtin_amdgcn_readfirstlane(tid / kWave); }
 
+// The same number, which the compiler takes for a new one: addresses made from it inside a
+// loop are made there and hold no registers between its turns.
+__device__ __forceinline__ int afresh(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
 // softplus and its derivative, in the form that neither overflows nor cancels.
 __device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))); }
 __device__ __forceinline__ float sigmoid(float v) {
@@ -289,34 +296,35 @@ template <typename T> constexpr int kTerms = Elem<T>::is_bf16 ? 3 : 1;
 
 // A tile of ROWS token rows by COLS columns (of which ncols hold data), fetched into
 // registers and put into LDS later, so that the fetch runs behind other work.  Rows past
-// `rows` and columns past `ncols` read as zero and are not touched in memory.  WHOLE: ncols
+// `rows` and columns past `ncols` become zero and are not touched in memory.  WHOLE: ncols
 // is a multiple of the vector, so a vector is there or not; those that are not are read at
-// `base` (which must be readable) and dropped, with no branch.
+// `base` (which must be readable) with no branch, and made zero when they are put: a select
+// next to the read would wait for it there.
 template <typename T, int ROWS, int COLS, int THREADS, bool WHOLE>
 struct TileFetch {
     static constexpr int kPerRow = COLS / kVec<T>;
     static constexpr int kCount = ROWS * kPerRow / THREADS;
     static_assert(ROWS * kPerRow % THREADS == 0, "tile must divide over the threads");
     u32x4 r[kCount];
+    __device__ __forceinline__ static int row_of(int k, int tid) { return (tid + k * THREADS) / kPerRow; }
+    __device__ __forceinline__ static int col_of(int k, int tid) { return (tid + k * THREADS) % kPerRow * kVec<T>; }
     __device__ __forceinline__ void fetch(const T *__restrict__ base, int64_t stride, int rows, int ncols, int tid) {
 #pragma unroll
         for (int k = 0; k < kCount; ++k) {
-            const int i = tid + k * THREADS, row = i / kPerRow, c = (i % kPerRow) * kVec<T>;
-            if constexpr (WHOLE) {
-                const bool on = row < rows && c < ncols;
-                const u32x4 v = *(const u32x4_a2 *)(base + (on ? row * stride + c : 0));
-                r[k] = on ? v : u32x4{0, 0, 0, 0};
-            } else {
-                r[k] = load_vec<T>(base + row * stride + c, row < rows ? ncols - c : 0);
-            }
+            const int row = row_of(k, tid), c = col_of(k, tid);
+            if constexpr (WHOLE) r[k] = *(const u32x4_a2 *)(base + (row < rows && c < ncols ? row * stride + c : 0));
+            else r[k] = load_vec<T>(base + row * stride + c, row < rows ? ncols - c : 0);
         }
     }
-    __device__ __forceinline__ void put(T *tile, int tid) const {
+    // Vector k as it was fetched with these rows and ncols.
+    __device__ __forceinline__ u32x4 get(int k, int rows, int ncols, int tid) const {
+        if (!WHOLE) return r[k];
+        return row_of(k, tid) < rows && col_of(k, tid) < ncols ? r[k] : u32x4{0, 0, 0, 0};
+    }
+    __device__ __forceinline__ void put(T *tile, int rows, int ncols, int tid) const {
 #pragma unroll
-        for (int k = 0; k < kCount; ++k) {
-            const int i = tid + k * THREADS, row = i / kPerRow, c = (i % kPerRow) * kVec<T>;
-            *(u32x4 *)(tile + row * ld_of<T>(COLS) + c) = r[k];
-        }
+        for (int k = 0; k < kCount; ++k)
+            *(u32x4 *)(tile + row_of(k, tid) * ld_of<T>(COLS) + col_of(k, tid)) = get(k, rows, ncols, tid);
     }
 };
 

@@ -39,7 +39,7 @@ struct BwdArgs {
     float *part;   // [splits, 2, B, L, G, N] or null (one split: grad_B and grad_C at once)
     float *heads;  // [3, H, B * nc]: every chunk's part of grad_A, grad_dt_bias, grad_D
     // for the sums over a head's tokens at a workgroup's end, [B, H, nc, Q]: r_own - q_own,
-    // r_in, q / dt, q_end; and [B, H, nc, QS, 2]: the waves' parts of <g1, h0> and grad . x
+    // r_in, q / dt, q_end; and [B, H, nc, waves, 2]: the waves' parts of <g1, h0> and grad . x
     double *own;
     float *rin, *direct, *qend, *marks;
     int has_first, has_last;  // an initial state, a gradient of the final one
@@ -68,18 +68,24 @@ __device__ __forceinline__ float over_wave(float v) {
 __device__ __forceinline__ float frag_at(const bf16x8 &f, int e) { return (float)f[e]; }
 __device__ __forceinline__ float frag_at(const FragF &f, int e) { return f.v[e]; }
 
-// One chunk, some heads of a group.  Wave w has strip w of the chunk's tokens both as rows t
+// Strips of 16 tokens that a wave owns: two in bfloat16, so that each operand read from LDS
+// serves two products and two independent chains run in a wave; one in float32, whose matrix
+// products leave LDS idle.
+template <typename T> constexpr int kOwn = Elem<T>::is_bf16 ? 1 : 1;
+
+// One chunk, some heads of a group.  A wave has its strips of the chunk's tokens both as rows t
 // (grad_C, r) and as columns i (grad_x, grad_B, q).  Strips go in pairs, 32 of a contraction:
 // a wave in pair kw has the pairs before kw as rows, those after it as columns, and its own as
 // both, masked; the same work for every wave, and its tiles of C . B stay in registers.
 template <typename T, int NP, bool WHOLE>
-__global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, const T *__restrict__ X,
+__global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(BwdArgs a, const T *__restrict__ X,
                                                                    const T *__restrict__ Bm, const T *__restrict__ Cm,
                                                                    const T *__restrict__ grad, T *__restrict__ grad_x,
                                                                    T *__restrict__ grad_dt, T *__restrict__ grad_B,
                                                                    T *__restrict__ grad_C) {
     typedef BwdLds<T, NP> Lds;
-    constexpr int QS = Lds::QS, Q = Lds::Q, THREADS = 64 * QS, LDN = Lds::LDN, LDP = Lds::LDP, NS = NP / 16;
+    constexpr int QS = Lds::QS, Q = Lds::Q, OWN = kOwn<T>, WAVES = QS / OWN, THREADS = 64 * WAVES;
+    constexpr int LDN = Lds::LDN, LDP = Lds::LDP, NS = NP / 16;
     extern __shared__ __align__(16) char raw_lds[];
     Lds &s = *(Lds *)raw_lds;
     const ScanDims &d = a.d;
@@ -101,32 +107,50 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
     const bool has_h = n > 0 && (c > 0 || a.has_first), has_g = (c + 1) * Q < len || (a.has_last && n > 0);
     const T *xb = X + b * a.x_batch + (int64_t)c * Q * a.x_token;
     const T *gb = grad + b * a.g_batch + (int64_t)c * Q * a.g_token;
-    const int me = 16 * wave + l16;  // this lane's token, as a row t and as a column i
-    const int kw = wave / 2;
+    const int kw = OWN == 2 ? wave : wave / 2;
+    int me[OWN];  // this lane's tokens, as rows t and as columns i
+#pragma unroll
+    for (int j = 0; j < OWN; ++j) me[j] = 16 * (OWN * wave + j) + l16;
 
     TileFetch<T, Q, kSlab, THREADS, WHOLE> xf, gf;
     TileFetch<float, kSlab, NP, THREADS, true> hf, af;
     float tf[3];
+    auto chunk_of = [&](int it) { return ((int64_t)b * d.H + h0 + it / slabs) * d.nc + c; };
+    // everything of an item but its adjoint, which is asked for when the one before has been used
     auto fetch = [&](int it) {
-        const int h = h0 + it / slabs, p0 = it % slabs * kSlab;
-        xf.fetch(xb + (int64_t)h * d.P + p0, a.x_token, n, d.P - p0, tid);
-        gf.fetch(gb + (int64_t)h * d.P + p0, a.g_token, n, d.P - p0, tid);
-        const int64_t chunk = ((int64_t)b * d.H + h) * d.nc + c;
-        if (has_h) hf.fetch(a.states + (chunk * d.P + p0) * cols, cols, d.P - p0, cols, tid);
+        const int h = h0 + it / slabs, p0 = it % slabs * kSlab, tid = afresh(threadIdx.x);
+        const int64_t chunk = chunk_of(it);
         if (tid < Q) {
             tf[0] = d.shi[chunk * Q + tid];
             tf[1] = d.slo[chunk * Q + tid];
             tf[2] = d.dt[chunk * Q + tid];
         }
+        xf.fetch(xb + (int64_t)h * d.P + p0, a.x_token, n, d.P - p0, tid);
+        gf.fetch(gb + (int64_t)h * d.P + p0, a.g_token, n, d.P - p0, tid);
+        if (has_h) hf.fetch(a.states + (chunk * d.P + p0) * cols, cols, d.P - p0, cols, tid);
     };
-    // a float32 tile into the planes
-    auto put_planes = [&](const decltype(hf) &f) {
+    auto fetch_adjoint = [&](int it) {
+        const int p0 = it % slabs * kSlab, tid = afresh(threadIdx.x);
+        if (has_g) af.fetch(a.adjoints + (chunk_of(it) * d.P + p0) * cols, cols, d.P - p0, cols, tid);
+    };
+    // a float32 tile into the planes; `dot` gains its product with what this thread put there before
+    float dot = 0.f;
+    auto put_planes = [&](const decltype(hf) &f, int p0, bool against) {
+        const int tid = afresh(threadIdx.x);
 #pragma unroll
         for (int k = 0; k < decltype(hf)::kCount; ++k) {
-            const int i = tid + k * THREADS, at = i / (NP / 4) * LDN + i % (NP / 4) * 4;
+            const int at = f.row_of(k, tid) * LDN + f.col_of(k, tid);
             float v[4];
-            widen<float>(f.r[k], v);
+            widen<float>(f.get(k, d.P - p0, cols, tid), v);
             if constexpr (Elem<T>::is_bf16) {
+                if (against) {
+                    u16x4 t[3];
+#pragma unroll
+                    for (int m = 0; m < 3; ++m) t[m] = *(const u16x4 *)(s.plane[m] + at);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)  // the three terms' sum is the float32 that they came from
+                        dot += v[e] * (bf16_bits_to_f32(t[0][e]) + (bf16_bits_to_f32(t[1][e]) + bf16_bits_to_f32(t[2][e])));
+                }
                 u16x4 t[3];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -139,6 +163,11 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
 #pragma unroll
                 for (int m = 0; m < 3; ++m) *(u16x4 *)(s.plane[m] + at) = t[m];
             } else {
+                if (against) {
+                    const f32x4 t = *(const f32x4 *)(s.plane[0] + at);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) dot += v[e] * t[e];
+                }
                 *(f32x4 *)(s.plane[0] + at) = f32x4{v[0], v[1], v[2], v[3]};
             }
         }
@@ -149,9 +178,9 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
         const int64_t chunk = ((int64_t)b * d.H + h) * d.nc + c, at = chunk * Q + lane * PER;
         float dot = 0.f, diag = 0.f;
 #pragma unroll
-        for (int w = 0; w < QS; ++w) {
-            dot += a.marks[(chunk * QS + w) * 2];
-            diag += a.marks[(chunk * QS + w) * 2 + 1];
+        for (int w = 0; w < WAVES; ++w) {
+            dot += a.marks[(chunk * WAVES + w) * 2];
+            diag += a.marks[(chunk * WAVES + w) * 2 + 1];
         }
         float pre[PER], before = 0.f;
         double suf[PER], after = 0.;
@@ -201,116 +230,152 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
     // B and C, and the tiles of C . B: as rows transposed, D[i][t], as columns D[t][i].  Slot k
     // is pair k as rows for k < kw and pair k + 1 as columns from kw on.
     constexpr int SLOTS = QS / 2 - 1;
-    f32x4 cbs[SLOTS][2], cbr[2], cbc[2];
+    f32x4 cbs[SLOTS][OWN][2], cbr[OWN][2], cbc[OWN][2];
     {
         TileFetch<T, Q, NP, THREADS, false> bf, cf;
         bf.fetch(Bm + b * a.b_batch + (int64_t)c * Q * a.b_token + grp * d.N, a.b_token, n, d.N, tid);
         cf.fetch(Cm + b * a.c_batch + (int64_t)c * Q * a.c_token + grp * d.N, a.c_token, n, d.N, tid);
+        bf.put(s.b, n, d.N, tid);
+        cf.put(s.c, n, d.N, tid);
         fetch(0);
-        bf.put(s.b, tid);
-        cf.put(s.c, tid);
+        fetch_adjoint(0);
         __syncthreads();
-        auto tile = [&](const T *rows_of, int strip, const T *cols_of) {
-            f32x4 r = {0.f, 0.f, 0.f, 0.f};
+        auto tiles = [&](const T *rows_of, int strip, const T *cols_of, f32x4 (&r)[OWN][2], int u) {
 #pragma unroll
-            for (int k = 0; k < NP / 32; ++k)
-                r = mma(near_frag(rows_of + (16 * strip + l16) * LDN + 32 * k, g), near_frag(cols_of + me * LDN + 32 * k, g), r);
-            return r;
+            for (int j = 0; j < OWN; ++j) r[j][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < NP / 32; ++k) {
+                const Frag<T> f = near_frag(rows_of + (16 * strip + l16) * LDN + 32 * k, g);
+#pragma unroll
+                for (int j = 0; j < OWN; ++j) r[j][u] = mma(f, near_frag(cols_of + me[j] * LDN + 32 * k, g), r[j][u]);
+            }
         };
 #pragma unroll
-        for (int k = 0; k < SLOTS; ++k)
-#pragma unroll
-            for (int u = 0; u < 2; ++u) cbs[k][u] = k < kw ? tile(s.b, 2 * k + u, s.c) : tile(s.c, 2 * k + 2 + u, s.b);
-#pragma unroll
         for (int u = 0; u < 2; ++u) {
-            cbr[u] = tile(s.b, 2 * kw + u, s.c);
-            cbc[u] = tile(s.c, 2 * kw + u, s.b);
+#pragma unroll
+            for (int k = 0; k < SLOTS; ++k) {
+                if (k < kw) tiles(s.b, 2 * k + u, s.c, cbs[k], u);
+                else tiles(s.c, 2 * k + 2 + u, s.b, cbs[k], u);
+            }
+            tiles(s.b, 2 * kw + u, s.c, cbr, u);
+            tiles(s.c, 2 * kw + u, s.b, cbc, u);
         }
     }
-    f32x4 dB[NS], dC[NS];
+    f32x4 dB[OWN][NS], dC[OWN][NS];
 #pragma unroll
-    for (int k = 0; k < NS; ++k) dB[k] = dC[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < OWN; ++j)
+#pragma unroll
+        for (int k = 0; k < NS; ++k) dB[j][k] = dC[j][k] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    double rown = 0., qown = 0.;
-    float rin = 0.f, qdt = 0.f, qend = 0.f, dot = 0.f, zdiag = 0.f;
+    double rown[OWN] = {}, qown[OWN] = {};
+    float rin[OWN] = {}, qdt[OWN] = {}, qend[OWN] = {}, zdiag = 0.f;
     for (int it = 0; it < items; ++it) {
         const int h = h0 + it / slabs, slab = it % slabs, p0 = slab * kSlab;
-        const int64_t chunk = ((int64_t)b * d.H + h) * d.nc + c;
+        const int64_t chunk = chunk_of(it);
+        const int tid = afresh(threadIdx.x);
         __syncthreads();
-        xf.put(s.x, tid);
-        gf.put(s.g, tid);
-        if (has_h) put_planes(hf);
+        xf.put(s.x, n, d.P - p0, tid);
+        gf.put(s.g, n, d.P - p0, tid);
+        if (has_h) put_planes(hf, p0, false);
         if (tid < Q) {
             s.shi[tid] = tf[0];
             s.slo[tid] = tf[1];
             s.dt[tid] = tf[2];
         }
         __syncthreads();
-        if (has_g) af.fetch(a.adjoints + (chunk * d.P + p0) * cols, cols, d.P - p0, cols, tid);
-        const float mhi = s.shi[me], mlo = s.slo[me], mdt = s.dt[me];
-        Frag<T> xr[2], gr[2];
+        if (it + 1 < items) fetch(it + 1);
+        float mhi[OWN], mlo[OWN], mdt[OWN];
+        Frag<T> xr[OWN][2], gr[OWN][2];
+        f32x4 dx[OWN][4];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            xr[k] = near_frag(s.x + me * LDP + 32 * k, g);
-            gr[k] = near_frag(s.g + me * LDP + 32 * k, g);
+        for (int j = 0; j < OWN; ++j) {
+            mhi[j] = s.shi[me[j]];
+            mlo[j] = s.slo[me[j]];
+            mdt[j] = s.dt[me[j]];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                xr[j][q] = near_frag(s.x + me[j] * LDP + 32 * q, g);
+                gr[j][q] = near_frag(s.g + me[j] * LDP + 32 * q, g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) zdiag += frag_at(xr[j][q], e) * frag_at(gr[j][q], e);
+            }
+#pragma unroll
+            for (int p = 0; p < 4; ++p) dx[j][p] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) zdiag += frag_at(xr[q], e) * frag_at(gr[q], e);
-
-        f32x4 dx[4];
-#pragma unroll
-        for (int p = 0; p < 4; ++p) dx[p] = f32x4{0.f, 0.f, 0.f, 0.f};
-        // a pair of strips i = 2 k, 2 k + 1 against this strip's rows t
-        auto as_rows = [&](int k, const f32x4 (&cb)[2], bool own) {
-            f32x4 wt[2];
+        // a pair of strips i = 2 k, 2 k + 1 against the wave's rows t
+        auto as_rows = [&](int k, const f32x4 (&cb)[OWN][2], bool own) {
+            f32x4 wt[OWN][2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int is = 2 * k + u;
-                f32x4 z = {0.f, 0.f, 0.f, 0.f}, dif;
-#pragma unroll
-                for (int q = 0; q < 2; ++q) z = mma(near_frag(s.x + (16 * is + l16) * LDP + 32 * q, g), gr[q], z);
+                const Frag<T> x0 = near_frag(s.x + (16 * is + l16) * LDP, g), x1 = near_frag(s.x + (16 * is + l16) * LDP + 32, g);
                 const f32x4 ih = *(const f32x4 *)(s.shi + 16 * is + 4 * g), il = *(const f32x4 *)(s.slo + 16 * is + 4 * g);
                 const f32x4 id4 = *(const f32x4 *)(s.dt + 16 * is + 4 * g);
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    dif[v] = (mhi - ih[v]) + (mlo - il[v]);
-                    if (own) dif[v] = 16 * is + 4 * g + v <= me ? dif[v] : -INFINITY;
-                    wt[u][v] = z[v] * (__builtin_amdgcn_exp2f(dif[v]) * id4[v]);
-                    rown += cb[u][v] * wt[u][v];  // the columns add the very same products
+                for (int j = 0; j < OWN; ++j) {
+                    f32x4 z = {0.f, 0.f, 0.f, 0.f}, dif;
+                    z = mma(x1, gr[j][1], mma(x0, gr[j][0], z));
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        dif[v] = (mhi[j] - ih[v]) + (mlo[j] - il[v]);
+                        if (own) dif[v] = 16 * is + 4 * g + v <= me[j] ? dif[v] : -INFINITY;
+                        wt[j][u][v] = z[v] * (__builtin_amdgcn_exp2f(dif[v]) * id4[v]);
+                        rown[j] += cb[j][u][v] * wt[j][u][v];  // the columns add the very same products
+                    }
                 }
             }
-            const Frag<T> wf = pack_frag<T>(wt[0], wt[1]);
+            Frag<T> wf[OWN];
 #pragma unroll
-            for (int m = 0; m < NS; ++m) dC[m] = mma(col_frag(s.b, LDN, 32 * k, 16 * m, l16, g), wf, dC[m]);
+            for (int j = 0; j < OWN; ++j) wf[j] = pack_frag<T>(wt[j][0], wt[j][1]);
+#pragma unroll
+            for (int m = 0; m < NS; ++m) {
+                const Frag<T> f = col_frag(s.b, LDN, 32 * k, 16 * m, l16, g);
+#pragma unroll
+                for (int j = 0; j < OWN; ++j) dC[j][m] = mma(f, wf[j], dC[j][m]);
+            }
         };
-        // a pair of strips t = 2 k, 2 k + 1 against this strip's columns i
-        auto as_columns = [&](int k, const f32x4 (&cb)[2], bool own) {
-            f32x4 nt[2], wt[2];
+        // a pair of strips t = 2 k, 2 k + 1 against the wave's columns i
+        auto as_columns = [&](int k, const f32x4 (&cb)[OWN][2], bool own) {
+            f32x4 nt[OWN][2], wt[OWN][2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int ts = 2 * k + u;
-                f32x4 z = {0.f, 0.f, 0.f, 0.f}, dif;
-#pragma unroll
-                for (int q = 0; q < 2; ++q) z = mma(near_frag(s.g + (16 * ts + l16) * LDP + 32 * q, g), xr[q], z);
+                const Frag<T> g0 = near_frag(s.g + (16 * ts + l16) * LDP, g), g1 = near_frag(s.g + (16 * ts + l16) * LDP + 32, g);
                 const f32x4 th = *(const f32x4 *)(s.shi + 16 * ts + 4 * g), tl = *(const f32x4 *)(s.slo + 16 * ts + 4 * g);
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    dif[v] = (th[v] - mhi) + (tl[v] - mlo);
-                    if (own) dif[v] = 16 * ts + 4 * g + v >= me ? dif[v] : -INFINITY;
-                    const float e = __builtin_amdgcn_exp2f(dif[v]);
-                    nt[u][v] = cb[u][v] * e;
-                    wt[u][v] = z[v] * (e * mdt);
-                    qown += cb[u][v] * wt[u][v];
-                    qdt += nt[u][v] * z[v];
+                for (int j = 0; j < OWN; ++j) {
+                    f32x4 z = {0.f, 0.f, 0.f, 0.f}, dif;
+                    z = mma(g1, xr[j][1], mma(g0, xr[j][0], z));
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        dif[v] = (th[v] - mhi[j]) + (tl[v] - mlo[j]);
+                        if (own) dif[v] = 16 * ts + 4 * g + v >= me[j] ? dif[v] : -INFINITY;
+                        const float e = __builtin_amdgcn_exp2f(dif[v]);
+                        nt[j][u][v] = cb[j][u][v] * e;
+                        wt[j][u][v] = z[v] * (e * mdt[j]);
+                        qown[j] += cb[j][u][v] * wt[j][u][v];
+                        qdt[j] += nt[j][u][v] * z[v];
+                    }
                 }
             }
-            const Frag<T> nf = pack_frag<T>(nt[0], nt[1]), wf = pack_frag<T>(wt[0], wt[1]);
+            Frag<T> nf[OWN], wf[OWN];
 #pragma unroll
-            for (int p = 0; p < 4; ++p) dx[p] = mma(col_frag(s.g, LDP, 32 * k, 16 * p, l16, g), nf, dx[p]);
+            for (int j = 0; j < OWN; ++j) {
+                nf[j] = pack_frag<T>(nt[j][0], nt[j][1]);
+                wf[j] = pack_frag<T>(wt[j][0], wt[j][1]);
+            }
 #pragma unroll
-            for (int m = 0; m < NS; ++m) dB[m] = mma(col_frag(s.c, LDN, 32 * k, 16 * m, l16, g), wf, dB[m]);
+            for (int p = 0; p < 4; ++p) {
+                const Frag<T> f = col_frag(s.g, LDP, 32 * k, 16 * p, l16, g);
+#pragma unroll
+                for (int j = 0; j < OWN; ++j) dx[j][p] = mma(f, nf[j], dx[j][p]);
+            }
+#pragma unroll
+            for (int m = 0; m < NS; ++m) {
+                const Frag<T> f = col_frag(s.c, LDN, 32 * k, 16 * m, l16, g);
+#pragma unroll
+                for (int j = 0; j < OWN; ++j) dB[j][m] = mma(f, wf[j], dB[j][m]);
+            }
         };
         as_rows(kw, cbr, true);
         as_columns(kw, cbc, true);
@@ -320,126 +385,149 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
             else as_columns(k + 1, cbs[k], false);
         }
         if (has_h) {
-            f32x4 o[NS];
+            f32x4 o[OWN][NS];
 #pragma unroll
-            for (int m = 0; m < NS; ++m) o[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int j = 0; j < OWN; ++j)
+#pragma unroll
+                for (int m = 0; m < NS; ++m) o[j][m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const Frag<T> go = row_frag(s.g + me * LDP + 32 * q, g);
+                Frag<T> go[OWN];
+#pragma unroll
+                for (int j = 0; j < OWN; ++j) go[j] = row_frag(s.g + me[j] * LDP + 32 * q, g);
 #pragma unroll
                 for (int t = 0; t < kTerms<T>; ++t)
 #pragma unroll
-                    for (int m = 0; m < NS; ++m) o[m] = mma(col_frag(s.plane[t], LDN, 32 * q, 16 * m, l16, g), go, o[m]);
+                    for (int m = 0; m < NS; ++m) {
+                        const Frag<T> f = col_frag(s.plane[t], LDN, 32 * q, 16 * m, l16, g);
+#pragma unroll
+                        for (int j = 0; j < OWN; ++j) o[j][m] = mma(f, go[j], o[j][m]);
+                    }
             }
-            const float f = __builtin_amdgcn_exp2f(mhi + mlo);
 #pragma unroll
-            for (int m = 0; m < NS; ++m) {
-                o[m] *= f;
-                dC[m] += o[m];
+            for (int j = 0; j < OWN; ++j) {
+                const float f = __builtin_amdgcn_exp2f(mhi[j] + mlo[j]);
 #pragma unroll
-                for (int v = 0; v < 4; ++v) rin += o[m][v] * Elem<T>::to_f32(s.c[me * LDN + 16 * m + 4 * g + v]);
+                for (int m = 0; m < NS; ++m) {
+                    o[j][m] *= f;
+                    dC[j][m] += o[j][m];
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) rin[j] += o[j][m][v] * Elem<T>::to_f32(s.c[me[j] * LDN + 16 * m + 4 * g + v]);
+                }
             }
         }
 
         // the gradient from later chunks, in the planes of h0
-        const float f1 = __builtin_amdgcn_exp2f((s.shi[Q - 1] - mhi) + (s.slo[Q - 1] - mlo));
         if (has_g) {
             __syncthreads();
-            put_planes(af);
-            if (has_h) {
+            put_planes(af, p0, has_h);
+            if (it + 1 < items) fetch_adjoint(it + 1);
+            __syncthreads();
+            f32x4 o[OWN][4], w[OWN][NS];
 #pragma unroll
-                for (int k = 0; k < decltype(af)::kCount; ++k)
+            for (int j = 0; j < OWN; ++j) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) dot += __uint_as_float(hf.r[k][e]) * __uint_as_float(af.r[k][e]);
+                for (int p = 0; p < 4; ++p) o[j][p] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int m = 0; m < NS; ++m) w[j][m] = f32x4{0.f, 0.f, 0.f, 0.f};
             }
-            __syncthreads();
-        }
-        if (it + 1 < items) fetch(it + 1);
-        if (has_g) {
-            f32x4 o[4];
-#pragma unroll
-            for (int p = 0; p < 4; ++p) o[p] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int k = 0; k < NP / 32; ++k) {
-                const Frag<T> br = near_frag(s.b + me * LDN + 32 * k, g);
+                Frag<T> br[OWN];
+#pragma unroll
+                for (int j = 0; j < OWN; ++j) br[j] = near_frag(s.b + me[j] * LDN + 32 * k, g);
 #pragma unroll
                 for (int t = 0; t < kTerms<T>; ++t)
 #pragma unroll
-                    for (int p = 0; p < 4; ++p)
-                        o[p] = mma(near_frag(s.plane[t] + (16 * p + l16) * LDN + 32 * k, g), br, o[p]);
+                    for (int p = 0; p < 4; ++p) {
+                        const Frag<T> f = near_frag(s.plane[t] + (16 * p + l16) * LDN + 32 * k, g);
+#pragma unroll
+                        for (int j = 0; j < OWN; ++j) o[j][p] = mma(f, br[j], o[j][p]);
+                    }
             }
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                o[p] *= f1;
-                dx[p] += o[p];
-#pragma unroll
-                for (int v = 0; v < 4; ++v) qend += o[p][v] * Elem<T>::to_f32(s.x[me * LDP + 16 * p + 4 * g + v]);
-            }
-            const float f2 = f1 * mdt;
-            f32x4 w[NS];
-#pragma unroll
-            for (int m = 0; m < NS; ++m) w[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const Frag<T> xo = row_frag(s.x + me * LDP + 32 * q, g);
+                Frag<T> xo[OWN];
 #pragma unroll
-                for (int m = 0; m < NS; ++m) w[m] = mma(col_frag(s.plane[0], LDN, 32 * q, 16 * m, l16, g), xo, w[m]);
+                for (int j = 0; j < OWN; ++j) xo[j] = row_frag(s.x + me[j] * LDP + 32 * q, g);
+#pragma unroll
+                for (int m = 0; m < NS; ++m) {
+                    const Frag<T> f = col_frag(s.plane[0], LDN, 32 * q, 16 * m, l16, g);
+#pragma unroll
+                    for (int j = 0; j < OWN; ++j) w[j][m] = mma(f, xo[j], w[j][m]);
+                }
             }
 #pragma unroll
-            for (int m = 0; m < NS; ++m) dB[m] += w[m] * f2;
+            for (int j = 0; j < OWN; ++j) {
+                const float f1 = __builtin_amdgcn_exp2f((s.shi[Q - 1] - mhi[j]) + (s.slo[Q - 1] - mlo[j])), f2 = f1 * mdt[j];
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    o[j][p] *= f1;
+                    dx[j][p] += o[j][p];
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) qend[j] += o[j][p][v] * Elem<T>::to_f32(s.x[me[j] * LDP + 16 * p + 4 * g + v]);
+                }
+#pragma unroll
+                for (int m = 0; m < NS; ++m) dB[j][m] += w[j][m] * f2;
+            }
         }
-        if (me < rows) {
-            const float skip = a.D[h];
-            T *o = grad_x + ((tok0 + me) * d.H + h) * d.P + p0;
+        const float skip = a.D[h];
+#pragma unroll
+        for (int j = 0; j < OWN; ++j) {
+            if (me[j] >= rows) continue;
+            T *o = grad_x + ((tok0 + me[j]) * d.H + h) * d.P + p0;
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
                 const int at = 16 * p + 4 * g;
                 f32x4 r;
 #pragma unroll
                 for (int v = 0; v < 4; ++v)
-                    r[v] = me < n ? mdt * dx[p][v] + skip * Elem<T>::to_f32(s.g[me * LDP + at + v]) : 0.f;
+                    r[v] = me[j] < n ? mdt[j] * dx[j][p][v] + skip * Elem<T>::to_f32(s.g[me[j] * LDP + at + v]) : 0.f;
                 if (p0 + at < d.P) store4<T>(o + at, r, WHOLE ? 4 : d.P - p0 - at);
             }
         }
         if (slab + 1 == slabs) {
-            rin = over_groups(rin);
-            rown = over_groups(rown);
-            qown = over_groups(qown);
-            qdt = over_groups(qdt);
-            qend = over_groups(qend);
+#pragma unroll
+            for (int j = 0; j < OWN; ++j) {
+                const double own = over_groups(rown[j] - qown[j]);
+                const float r = over_groups(rin[j]), q0 = over_groups(qdt[j]), q1 = over_groups(qend[j]);
+                if (g == 0) {
+                    const int64_t at = chunk * Q + me[j];
+                    a.own[at] = own;
+                    a.rin[at] = r;
+                    a.direct[at] = q0 + q1;
+                    a.qend[at] = mdt[j] * q1;
+                }
+                rown[j] = qown[j] = 0.;
+                rin[j] = qdt[j] = qend[j] = 0.f;
+            }
             dot = over_wave(dot);
             zdiag = over_wave(zdiag);
-            if (g == 0) {
-                const int64_t at = chunk * Q + me;
-                a.own[at] = rown - qown;
-                a.rin[at] = rin;
-                a.direct[at] = qdt + qend;
-                a.qend[at] = mdt * qend;
-            }
             if (lane == 0) {
-                a.marks[(chunk * QS + wave) * 2] = dot;
-                a.marks[(chunk * QS + wave) * 2 + 1] = zdiag;
+                a.marks[(chunk * WAVES + wave) * 2] = dot;
+                a.marks[(chunk * WAVES + wave) * 2 + 1] = zdiag;
             }
-            rown = qown = 0.;
-            rin = qdt = qend = dot = zdiag = 0.f;
+            dot = zdiag = 0.f;
         }
     }
     __syncthreads();
-    for (int h = h0 + wave; h < h1; h += QS) finish_head(h);
+    for (int h = h0 + wave; h < h1; h += WAVES) finish_head(h);
 
-    if (me < rows) {
-        const int64_t at = ((tok0 + me) * d.G + grp) * d.N;
+#pragma unroll
+    for (int j = 0; j < OWN; ++j) {
+        if (me[j] >= rows) continue;
+        const int64_t at = ((tok0 + me[j]) * d.G + grp) * d.N;
         const int64_t all = (int64_t)d.B * d.L * d.G * d.N;
 #pragma unroll
         for (int m = 0; m < NS; ++m) {
             const int k = 16 * m + 4 * g;
             if (k >= d.N) continue;
             if (a.part != nullptr) {
-                store4<float>(a.part + 2 * split * all + at + k, dB[m], d.N - k);
-                store4<float>(a.part + (2 * split + 1) * all + at + k, dC[m], d.N - k);
+                store4<float>(a.part + 2 * split * all + at + k, dB[j][m], d.N - k);
+                store4<float>(a.part + (2 * split + 1) * all + at + k, dC[j][m], d.N - k);
             } else {
-                store4<T>(grad_B + at + k, dB[m], d.N - k);
-                store4<T>(grad_C + at + k, dC[m], d.N - k);
+                store4<T>(grad_B + at + k, dB[j][m], d.N - k);
+                store4<T>(grad_C + at + k, dC[j][m], d.N - k);
             }
         }
     }
@@ -504,7 +592,7 @@ hipError_t launch_main(const BwdArgs &k, int64_t blocks, const Scan &a, const vo
     auto kern = scan_bwd_kernel<T, NP, WHOLE>;
     hipError_t e = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(64 * kStrips<T>), bytes, stream, k, (const T *)a.x,
+    hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(64 * kStrips<T> / kOwn<T>), bytes, stream, k, (const T *)a.x,
                        (const T *)a.Bm, (const T *)a.Cm, (const T *)grad, (T *)grad_x, (T *)grad_dt, (T *)grad_B,
                        (T *)grad_C);
     return hipGetLastError();

@@ -129,14 +129,14 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
         TileFetch<T, Q, NP, kThreads, false> cg, bg;
         cg.fetch(Cm + b * a.c_batch + (int64_t)c * Q * a.c_token + grp * d.N, a.c_token, n, d.N, tid);
         bg.fetch(Bm + b * a.b_batch + (int64_t)c * Q * a.b_token + grp * d.N, a.b_token, n, d.N, tid);
-        cg.put(lds, tid);
+        cg.put(lds, n, d.N, tid);
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < SPW; ++j)
 #pragma unroll
             for (int k = 0; k < NP / 32; ++k) cf[j][k] = near_frag(lds + (16 * strip[j] + l16) * LDN + 32 * k, g);
         __syncthreads();
-        bg.put(lds, tid);
+        bg.put(lds, n, d.N, tid);
         __syncthreads();
         fetch(0);
 #pragma unroll
@@ -157,18 +157,19 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
     for (int it = 0; it < items; ++it) {
         const int h = h0 + it / slabs, p0 = it % slabs * kSlab;
         __syncthreads();
-        xf.put(xtile, tid);
+        xf.put(xtile, n, d.P - p0, tid);
         if (has_h) {
 #pragma unroll
             for (int k = 0; k < decltype(hf)::kCount; ++k) {
-                const int i = tid + k * kThreads, row = i / (NP / 4), col = i % (NP / 4) * 4;
+                T *to = htile + hf.row_of(k, tid) * LDN + hf.col_of(k, tid);
+                const u32x4 f = hf.get(k, d.P - p0, cols, tid);
                 if constexpr (Elem<T>::is_bf16) {
                     u16x4 v;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = f32_to_bf16_bits(__uint_as_float(hf.r[k][e]));
-                    *(u16x4 *)(htile + row * LDN + col) = v;
+                    for (int e = 0; e < 4; ++e) v[e] = f32_to_bf16_bits(__uint_as_float(f[e]));
+                    *(u16x4 *)to = v;
                 } else {
-                    *(u32x4 *)(htile + row * LDN + col) = hf.r[k];
+                    *(u32x4 *)to = f;
                 }
             }
         }

@@ -43,11 +43,11 @@ __global__ __launch_bounds__(kThreads) void scan_states_kernel(StateArgs a, cons
     TileFetch<T, Q, kSlab, kThreads, WHOLE> xf;
     yf.fetch(Y + b * a.y_batch + (int64_t)c * Q * a.y_token + grp * d.N, a.y_token, n, d.N, tid);
     xf.fetch(xb + (int64_t)h0 * d.P, a.x_token, n, d.P, tid);
-    yf.put(ytile, tid);
+    yf.put(ytile, n, d.N, tid);
     for (int it = 0; it < items; ++it) {
         const int h = h0 + it / slabs, p0 = it % slabs * kSlab;
         __syncthreads();
-        xf.put(xtile, tid);
+        xf.put(xtile, n, d.P - p0, tid);
         if (tid < Q) {
             const int64_t at = ((int64_t)(b * d.H + h) * d.nc + c) * Q;
             float f = d.shi[at + tid], l = d.slo[at + tid];
