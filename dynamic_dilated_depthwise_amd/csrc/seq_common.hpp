@@ -294,6 +294,13 @@ __device__ __forceinline__ void split3(float f, __bf16 &hi, __bf16 &mid, __bf16 
 // Terms an exact float32 operand takes in the type's matrix products.
 template <typename T> constexpr int kTerms = Elem<T>::is_bf16 ? 3 : 1;
 
+// Four neighbouring elements of an LDS row, 4-element aligned.
+__device__ __forceinline__ f32x4 lds4(const float *p) { return *(const f32x4 *)p; }
+__device__ __forceinline__ f32x4 lds4(const bf16_t *p) {
+    const u16x4 u = *(const u16x4 *)p;
+    return f32x4{bf16_bits_to_f32(u[0]), bf16_bits_to_f32(u[1]), bf16_bits_to_f32(u[2]), bf16_bits_to_f32(u[3])};
+}
+
 // A tile of ROWS token rows by COLS columns (of which ncols hold data), fetched into
 // registers and put into LDS later, so that the fetch runs behind other work.  Rows past
 // `rows` and columns past `ncols` become zero and are not touched in memory.  WHOLE: ncols

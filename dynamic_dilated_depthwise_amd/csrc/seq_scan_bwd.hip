@@ -114,12 +114,13 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
 
     TileFetch<T, Q, kSlab, THREADS, WHOLE> xf, gf;
     TileFetch<float, kSlab, NP, THREADS, true> hf, af;
-    float tf[3];
+    float tf[3], skip_next;
     auto chunk_of = [&](int it) { return ((int64_t)b * d.H + h0 + it / slabs) * d.nc + c; };
     // everything of an item but its adjoint, which is asked for when the one before has been used
     auto fetch = [&](int it) {
         const int h = h0 + it / slabs, p0 = it % slabs * kSlab, tid = afresh(threadIdx.x);
         const int64_t chunk = chunk_of(it);
+        skip_next = a.D[h];
         if (tid < Q) {
             tf[0] = d.shi[chunk * Q + tid];
             tf[1] = d.slo[chunk * Q + tid];
@@ -283,6 +284,7 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
             s.dt[tid] = tf[2];
         }
         __syncthreads();
+        const float skip = skip_next;  // asked for with the item: a read here would wait for the next item's too
         if (it + 1 < items) fetch(it + 1);
         float mhi[OWN], mlo[OWN], mdt[OWN];
         Frag<T> xr[OWN][2], gr[OWN][2];
@@ -411,8 +413,9 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
                 for (int m = 0; m < NS; ++m) {
                     o[j][m] *= f;
                     dC[j][m] += o[j][m];
+                    const f32x4 cv = lds4(s.c + me[j] * LDN + 16 * m + 4 * g);
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) rin[j] += o[j][m][v] * Elem<T>::to_f32(s.c[me[j] * LDN + 16 * m + 4 * g + v]);
+                    for (int v = 0; v < 4; ++v) rin[j] += o[j][m][v] * cv[v];
                 }
             }
         }
@@ -464,14 +467,14 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
                 for (int p = 0; p < 4; ++p) {
                     o[j][p] *= f1;
                     dx[j][p] += o[j][p];
+                    const f32x4 xv = lds4(s.x + me[j] * LDP + 16 * p + 4 * g);
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) qend[j] += o[j][p][v] * Elem<T>::to_f32(s.x[me[j] * LDP + 16 * p + 4 * g + v]);
+                    for (int v = 0; v < 4; ++v) qend[j] += o[j][p][v] * xv[v];
                 }
 #pragma unroll
                 for (int m = 0; m < NS; ++m) dB[j][m] += w[j][m] * f2;
             }
         }
-        const float skip = a.D[h];
 #pragma unroll
         for (int j = 0; j < OWN; ++j) {
             if (me[j] >= rows) continue;
@@ -479,10 +482,9 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
                 const int at = 16 * p + 4 * g;
-                f32x4 r;
+                f32x4 r = dx[j][p] * mdt[j] + skip * lds4(s.g + me[j] * LDP + at);
 #pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    r[v] = me[j] < n ? mdt[j] * dx[j][p][v] + skip * Elem<T>::to_f32(s.g[me[j] * LDP + at + v]) : 0.f;
+                for (int v = 0; v < 4; ++v) r[v] = me[j] < n ? r[v] : 0.f;
                 if (p0 + at < d.P) store4<T>(o + at, r, WHOLE ? 4 : d.P - p0 - at);
             }
         }

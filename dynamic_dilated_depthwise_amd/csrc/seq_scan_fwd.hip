@@ -109,9 +109,10 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
 
     TileFetch<T, Q, kSlab, kThreads, WHOLE> xf;
     TileFetch<float, kSlab, NP, kThreads, true> hf;
-    float tf[3];
+    float tf[3], skip_next;
     auto fetch = [&](int it) {
         const int h = h0 + it / slabs, p0 = it % slabs * kSlab;
+        skip_next = a.D[h];
         xf.fetch(xb + (int64_t)h * d.P + p0, a.x_token, n, d.P - p0, tid);
         const int64_t chunk = ((int64_t)b * d.H + h) * d.nc + c;
         if (has_h) hf.fetch(a.states + (chunk * d.P + p0) * cols, cols, d.P - p0, cols, tid);
@@ -179,6 +180,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
             dts[tid] = tf[2];
         }
         __syncthreads();
+        const float skip = skip_next;  // asked for with the item: a read here would wait for the next item's too
         if (it + 1 < items) fetch(it + 1);
         f32x4 acc[SPW][4];
 #pragma unroll
@@ -242,7 +244,6 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
                 for (int p = 0; p < 4; ++p) acc[j][p] = mma(xr[p], mf, acc[j][p]);
             }
         }
-        const float skip = a.D[h];
 #pragma unroll
         for (int j = 0; j < SPW; ++j) {
             const int t = 16 * strip[j] + l16;
@@ -251,10 +252,9 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
                 const int at = 16 * p + 4 * g;
-                f32x4 o;
+                f32x4 o = acc[j][p] + skip * lds4(xtile + t * LDP + at);
 #pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    o[v] = t < n ? acc[j][p][v] + skip * Elem<T>::to_f32(xtile[t * LDP + at + v]) : 0.f;
+                for (int v = 0; v < 4; ++v) o[v] = t < n ? o[v] : 0.f;
                 if (p0 + at < d.P) store4<T>(yr + at, o, WHOLE ? 4 : d.P - p0 - at);
             }
         }
