@@ -212,7 +212,7 @@ template <typename T> using Frag = typename FragOf<T>::type;
 
 // LDS rows carry 16 bytes of padding: 16 rows read at one column then start in 16
 // different quarters of the banks.
-template <typename T> constexpr int ld_of(int cols) { return cols + kVec<T>; }
+template <typename T> constexpr int ld_of(int cols) { return cols + (Elem<T>::is_bf16 && cols <= 64 ? 16 : kVec<T>); }
 
 __device__ __forceinline__ f32x4 mma(const bf16x8 &a, const bf16x8 &b, f32x4 c) { return mfma_16x16x32_bf16(a, b, c); }
 __device__ __forceinline__ f32x4 mma(const FragF &a, const FragF &b, f32x4 c) {
@@ -328,10 +328,10 @@ struct TileFetch {
         if (!WHOLE) return r[k];
         return row_of(k, tid) < rows && col_of(k, tid) < ncols ? r[k] : u32x4{0, 0, 0, 0};
     }
-    __device__ __forceinline__ void put(T *tile, int rows, int ncols, int tid) const {
+    __device__ __forceinline__ void put(T *tile, int ld, int rows, int ncols, int tid) const {
 #pragma unroll
         for (int k = 0; k < kCount; ++k)
-            *(u32x4 *)(tile + row_of(k, tid) * ld_of<T>(COLS) + col_of(k, tid)) = get(k, rows, ncols, tid);
+            *(u32x4 *)(tile + row_of(k, tid) * ld + col_of(k, tid)) = get(k, rows, ncols, tid);
     }
 };
 

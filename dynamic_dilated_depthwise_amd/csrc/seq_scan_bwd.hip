@@ -47,7 +47,8 @@ struct BwdArgs {
 
 template <typename T, int NP>
 struct BwdLds {
-    static constexpr int QS = kStrips<T>, Q = 16 * QS, LDN = ld_of<T>(NP), LDP = ld_of<T>(kSlab);
+    static constexpr int QS = kStrips<T>, Q = 16 * QS, LDN = ld_of<T>(NP);
+    static constexpr int LDP = NP <= 64 ? ld_of<T>(kSlab) : kSlab + kVec<T>;  // 160 KB hold no more at 128
     T b[Q * LDN], c[Q * LDN], x[Q * LDP], g[Q * LDP];
     T plane[kTerms<T>][kSlab * LDN];  // h0, then g1
     float shi[Q], slo[Q], dt[Q];
@@ -71,7 +72,7 @@ __device__ __forceinline__ float frag_at(const FragF &f, int e) { return f.v[e];
 // Strips of 16 tokens that a wave owns: two in bfloat16, so that each operand read from LDS
 // serves two products and two independent chains run in a wave; one in float32, whose matrix
 // products leave LDS idle.
-template <typename T> constexpr int kOwn = Elem<T>::is_bf16 ? 1 : 1;
+template <typename T> constexpr int kOwn = 1;
 
 // One chunk, some heads of a group.  A wave has its strips of the chunk's tokens both as rows t
 // (grad_C, r) and as columns i (grad_x, grad_B, q).  Strips go in pairs, 32 of a contraction:
@@ -236,8 +237,8 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
         TileFetch<T, Q, NP, THREADS, false> bf, cf;
         bf.fetch(Bm + b * a.b_batch + (int64_t)c * Q * a.b_token + grp * d.N, a.b_token, n, d.N, tid);
         cf.fetch(Cm + b * a.c_batch + (int64_t)c * Q * a.c_token + grp * d.N, a.c_token, n, d.N, tid);
-        bf.put(s.b, n, d.N, tid);
-        cf.put(s.c, n, d.N, tid);
+        bf.put(s.b, LDN, n, d.N, tid);
+        cf.put(s.c, LDN, n, d.N, tid);
         fetch(0);
         fetch_adjoint(0);
         __syncthreads();
@@ -275,8 +276,8 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
         const int64_t chunk = chunk_of(it);
         const int tid = afresh(threadIdx.x);
         __syncthreads();
-        xf.put(s.x, n, d.P - p0, tid);
-        gf.put(s.g, n, d.P - p0, tid);
+        xf.put(s.x, LDP, n, d.P - p0, tid);
+        gf.put(s.g, LDP, n, d.P - p0, tid);
         if (has_h) put_planes(hf, p0, false);
         if (tid < Q) {
             s.shi[tid] = tf[0];

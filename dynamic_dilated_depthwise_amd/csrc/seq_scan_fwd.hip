@@ -130,14 +130,14 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
         TileFetch<T, Q, NP, kThreads, false> cg, bg;
         cg.fetch(Cm + b * a.c_batch + (int64_t)c * Q * a.c_token + grp * d.N, a.c_token, n, d.N, tid);
         bg.fetch(Bm + b * a.b_batch + (int64_t)c * Q * a.b_token + grp * d.N, a.b_token, n, d.N, tid);
-        cg.put(lds, n, d.N, tid);
+        cg.put(lds, LDN, n, d.N, tid);
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < SPW; ++j)
 #pragma unroll
             for (int k = 0; k < NP / 32; ++k) cf[j][k] = near_frag(lds + (16 * strip[j] + l16) * LDN + 32 * k, g);
         __syncthreads();
-        bg.put(lds, n, d.N, tid);
+        bg.put(lds, LDN, n, d.N, tid);
         __syncthreads();
         fetch(0);
 #pragma unroll
@@ -158,7 +158,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
     for (int it = 0; it < items; ++it) {
         const int h = h0 + it / slabs, p0 = it % slabs * kSlab;
         __syncthreads();
-        xf.put(xtile, n, d.P - p0, tid);
+        xf.put(xtile, LDP, n, d.P - p0, tid);
         if (has_h) {
 #pragma unroll
             for (int k = 0; k < decltype(hf)::kCount; ++k) {

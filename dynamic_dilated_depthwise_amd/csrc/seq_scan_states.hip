@@ -21,7 +21,8 @@ struct StateArgs {
 template <typename T, int NP, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void scan_states_kernel(StateArgs a, const T *__restrict__ X,
                                                                const T *__restrict__ Y, float *__restrict__ out) {
-    constexpr int Q = 16 * kStrips<T>, LDN = ld_of<T>(NP), LDP = ld_of<T>(kSlab);
+    // 16 bytes of padding only: a workgroup more fits a compute unit, which is worth more than its bank conflicts
+    constexpr int Q = 16 * kStrips<T>, LDN = NP + kVec<T>, LDP = kSlab + kVec<T>;
     __shared__ __align__(16) T ytile[Q * LDN];
     __shared__ __align__(16) T xtile[Q * LDP];
     __shared__ __align__(16) float w[Q];
@@ -43,11 +44,11 @@ __global__ __launch_bounds__(kThreads) void scan_states_kernel(StateArgs a, cons
     TileFetch<T, Q, kSlab, kThreads, WHOLE> xf;
     yf.fetch(Y + b * a.y_batch + (int64_t)c * Q * a.y_token + grp * d.N, a.y_token, n, d.N, tid);
     xf.fetch(xb + (int64_t)h0 * d.P, a.x_token, n, d.P, tid);
-    yf.put(ytile, n, d.N, tid);
+    yf.put(ytile, LDN, n, d.N, tid);
     for (int it = 0; it < items; ++it) {
         const int h = h0 + it / slabs, p0 = it % slabs * kSlab;
         __syncthreads();
-        xf.put(xtile, n, d.P - p0, tid);
+        xf.put(xtile, LDP, n, d.P - p0, tid);
         if (tid < Q) {
             const int64_t at = ((int64_t)(b * d.H + h) * d.nc + c) * Q;
             float f = d.shi[at + tid], l = d.slo[at + tid];
