@@ -291,6 +291,23 @@ __device__ __forceinline__ void split3(float f, __bf16 &hi, __bf16 &mid, __bf16 
     lo = (__bf16)(r - (float)mid);
 }
 
+// pack_frag in two bfloat16 terms, the second into `lo` (17 bits in all); float32 needs no second.
+template <typename T>
+__device__ __forceinline__ Frag<T> pack_frag2(const f32x4 &a, const f32x4 &b, Frag<T> &lo) {
+    const Frag<T> hi = pack_frag<T>(a, b);
+    if constexpr (Elem<T>::is_bf16) {
+        f32x4 ra, rb;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) { ra[e] = a[e] - (float)hi[e]; rb[e] = b[e] - (float)hi[4 + e]; }
+        lo = pack_frag<T>(ra, rb);
+    }
+    return hi;
+}
+__device__ __forceinline__ f32x4 mma2(const bf16x8 &a, const bf16x8 &hi, const bf16x8 &lo, f32x4 c) {
+    return mma(a, lo, mma(a, hi, c));
+}
+__device__ __forceinline__ f32x4 mma2(const FragF &a, const FragF &hi, const FragF &, f32x4 c) { return mma(a, hi, c); }
+
 // Terms an exact float32 operand takes in the type's matrix products.
 template <typename T> constexpr int kTerms = Elem<T>::is_bf16 ? 3 : 1;
 

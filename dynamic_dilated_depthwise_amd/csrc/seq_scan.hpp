@@ -14,6 +14,10 @@
 //   states   each chunk's own part of h1, all chunks at once
 //   pass     the recurrence over the chunks, in place: the part becomes the h0 of its chunk
 //   outputs  y of every chunk
+// A call that keeps nothing for a backward moves fewer states: `segments` in the place of
+// `states` runs the recurrence itself over a few chunks and writes what enters each of them
+// from the segment's own tokens in the inputs' type; `pass` then goes over segments only, and
+// `outputs` adds the two parts of h0.
 // The backward runs the same states and pass kernels over the chunks in reverse for the
 // gradient that enters each chunk's end (with grad and C in the place of x and B) and one
 // kernel for everything else.
@@ -37,7 +41,7 @@ constexpr int kSlab = 64;  // rows of the state (of P) that a workgroup works on
 template <typename T> constexpr int kStrips = Elem<T>::is_bf16 ? 8 : 4;
 
 struct ScanDims {
-    int B, L, H, P, G, N, nc;  // nc: chunks
+    int B, L, H, P, G, N, nc, seg;  // nc: chunks; seg: chunks of a segment (1: every chunk has its state)
     const int *lengths;
     float *dt, *shi, *slo;  // [B, H, nc * Q]
     float *decay;           // [B, H, nc]: exp of each chunk's whole sum
@@ -46,6 +50,9 @@ struct ScanDims {
 // Rows of N of the states in the workspaces start at multiples of four: [P, state_cols(N)],
 // zeros behind N.
 __host__ __device__ constexpr int state_cols(int N) { return (N + 3) / 4 * 4; }
+// The same for the running states of segments, in T: whole vectors.
+template <typename T>
+__host__ __device__ constexpr int before_cols(int N) { return (N + kVec<T> - 1) / kVec<T> * kVec<T>; }
 
 struct ChunkPlan {
     int per, splits;  // heads of a workgroup; workgroups that share a chunk and a group
@@ -70,21 +77,43 @@ __device__ __forceinline__ int valid_tokens(const int *lengths, int b, int L) {
 
 inline int64_t pad64(int64_t n) { return (n + 63) / 64 * 64; }
 
-// Sections of the forward's workspace, which the backward reads again.
-struct ScanWork {
-    int nc;
-    int64_t times, dt, shi, slo, decay, states, total;
+// Segments of a call that keeps nothing: the longest, up to 8 chunks, and the most heads at
+// once, up to 2, that leave 512 workgroups.  seg = 1: none, every chunk has its state.
+struct SegmentPlan {
+    int seg, hw;
 };
-inline ScanWork scan_work(int64_t B, int64_t L, int H, int P, int N, int Q) {
+inline SegmentPlan plan_segments(int64_t B, int64_t nc, int H, int P, int G) {
+    const int items = H / G * ((P + kSlab - 1) / kSlab);
+    for (int seg = 8; seg > 1; seg /= 2)
+        for (int hw = items > 1 ? 2 : 1; hw > 0; --hw)
+            if (nc > seg && B * ((nc + seg - 1) / seg) * G * ((items + hw - 1) / hw) >= 512) return {seg, hw};
+    return {1, 1};
+}
+
+// Sections of the forward's workspace, which the backward reads again.  With segments
+// `states` has one state a segment, `decays` their decays, and `carried` and `before` follow.
+struct ScanWork {
+    int nc, seg, hw;
+    int64_t times, dt, shi, slo, decay, states, carried, decays, before, total;
+};
+inline ScanWork scan_work(int64_t B, int64_t L, int H, int P, int G, int N, bool bf16, bool save) {
+    const int Q = 16 * (bf16 ? kStrips<bf16_t> : kStrips<float>);
     ScanWork w;
     w.nc = (int)((L + Q - 1) / Q);
+    const SegmentPlan p = save ? SegmentPlan{1, 1} : plan_segments(B, w.nc, H, P, G);
+    const int64_t state = (int64_t)P * state_cols(N), nseg = (w.nc + p.seg - 1) / p.seg;
+    w.seg = p.seg;
+    w.hw = p.hw;
     w.times = pad64(B * H * w.nc * Q);
     w.dt = 0;
     w.shi = w.times;
     w.slo = 2 * w.times;
     w.decay = 3 * w.times;
     w.states = w.decay + pad64(B * H * w.nc);
-    w.total = w.states + pad64(B * H * w.nc * (int64_t)P * state_cols(N));
+    w.carried = w.states + pad64(B * H * nseg * state);
+    w.decays = w.carried + (p.seg > 1 ? pad64(B * H * w.nc) : 0);
+    w.before = w.decays + (p.seg > 1 ? pad64(B * H * nseg) : 0);
+    w.total = w.before + (p.seg > 1 ? pad64(B * H * w.nc * P * (bf16 ? before_cols<bf16_t>(N) / 2 : before_cols<float>(N))) : 0);
     return w;
 }
 
@@ -92,9 +121,14 @@ inline ScanWork scan_work(int64_t B, int64_t L, int H, int P, int N, int Q) {
 template <typename T>
 hipError_t launch_scan_states(const ScanDims &d, const T *X, int64_t x_batch, int64_t x_token, const T *Y,
                               int64_t y_batch, int64_t y_token, float *out, bool reverse, hipStream_t stream);
-// The recurrence over the chunks, in place; first / final [B, H, P, N] or null.
-hipError_t launch_scan_pass(const ScanDims &d, float *states, const float *first, float *final_state, int Q,
-                            bool reverse, hipStream_t stream);
+// The running states of segments (d.seg chunks, hw heads at once).
+template <typename T>
+hipError_t launch_scan_segments(const ScanDims &d, int hw, const T *X, int64_t x_batch, int64_t x_token, const T *Y,
+                                int64_t y_batch, int64_t y_token, T *before, float *carried, float *ends,
+                                float *decays, hipStream_t stream);
+// The recurrence over the chunks (or segments), in place; first / final [B, H, P, N] or null.
+hipError_t launch_scan_pass(const ScanDims &d, float *states, const float *decays, const float *first, float *final_state,
+                            int Q, bool reverse, hipStream_t stream);
 
 // Runs X(NP, WHOLE) for the padded columns of the state and for P in whole vectors or not.
 #define DDPM_SEQ_SCAN_SHAPES(T, N, P, X)             \

@@ -23,8 +23,9 @@
 // grad_dt = (q / dt + A e) sigmoid(raw + dt_bias) and grad_A = sum_t dt e.  These are sums
 // of many terms of both signs, so every factor keeps float32's precision: Z and CB come
 // from products of the inputs themselves, and h0 and g1 enter as three bfloat16 terms.
-// grad_x, grad_B and grad_C are rounded to bfloat16 at their end; the scaled Z and CB that
-// they are summed from are operands rounded to bfloat16 once.
+// grad_B and grad_C, sums over heads that may cancel, take the scaled Z and g1 in two terms (17
+// bits) and are rounded to bfloat16 at their end; grad_x, with its large term D grad, takes the
+// scaled CB as an operand rounded to bfloat16 once.
 #include "seq_scan.hpp"
 
 namespace ddpm {
@@ -327,14 +328,14 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
                     }
                 }
             }
-            Frag<T> wf[OWN];
+            Frag<T> wf[OWN], wl[OWN];
 #pragma unroll
-            for (int j = 0; j < OWN; ++j) wf[j] = pack_frag<T>(wt[j][0], wt[j][1]);
+            for (int j = 0; j < OWN; ++j) wf[j] = pack_frag2<T>(wt[j][0], wt[j][1], wl[j]);
 #pragma unroll
             for (int m = 0; m < NS; ++m) {
                 const Frag<T> f = col_frag(s.b, LDN, 32 * k, 16 * m, l16, g);
 #pragma unroll
-                for (int j = 0; j < OWN; ++j) dC[j][m] = mma(f, wf[j], dC[j][m]);
+                for (int j = 0; j < OWN; ++j) dC[j][m] = mma2(f, wf[j], wl[j], dC[j][m]);
             }
         };
         // a pair of strips t = 2 k, 2 k + 1 against the wave's columns i
@@ -361,11 +362,11 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
                     }
                 }
             }
-            Frag<T> nf[OWN], wf[OWN];
+            Frag<T> nf[OWN], wf[OWN], wl[OWN];
 #pragma unroll
             for (int j = 0; j < OWN; ++j) {
                 nf[j] = pack_frag<T>(nt[j][0], nt[j][1]);
-                wf[j] = pack_frag<T>(wt[j][0], wt[j][1]);
+                wf[j] = pack_frag2<T>(wt[j][0], wt[j][1], wl[j]);
             }
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
@@ -377,7 +378,7 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
             for (int m = 0; m < NS; ++m) {
                 const Frag<T> f = col_frag(s.c, LDN, 32 * k, 16 * m, l16, g);
 #pragma unroll
-                for (int j = 0; j < OWN; ++j) dB[j][m] = mma(f, wf[j], dB[j][m]);
+                for (int j = 0; j < OWN; ++j) dB[j][m] = mma2(f, wf[j], wl[j], dB[j][m]);
             }
         };
         as_rows(kw, cbr, true);
@@ -455,11 +456,13 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
 #pragma unroll
                 for (int j = 0; j < OWN; ++j) xo[j] = row_frag(s.x + me[j] * LDP + 32 * q, g);
 #pragma unroll
-                for (int m = 0; m < NS; ++m) {
-                    const Frag<T> f = col_frag(s.plane[0], LDN, 32 * q, 16 * m, l16, g);
+                for (int t = 0; t < (kTerms<T> > 1 ? 2 : 1); ++t)
 #pragma unroll
-                    for (int j = 0; j < OWN; ++j) w[j][m] = mma(f, xo[j], w[j][m]);
-                }
+                    for (int m = 0; m < NS; ++m) {
+                        const Frag<T> f = col_frag(s.plane[t], LDN, 32 * q, 16 * m, l16, g);
+#pragma unroll
+                        for (int j = 0; j < OWN; ++j) w[j][m] = mma(f, xo[j], w[j][m]);
+                    }
             }
 #pragma unroll
             for (int j = 0; j < OWN; ++j) {
@@ -606,10 +609,10 @@ hipError_t scan_bwd(const Scan &a, const float *saved, const void *grad, int64_t
                     const float *grad_state, float *work, void *grad_x, void *grad_dt, float *grad_A, void *grad_B,
                     void *grad_C, float *grad_D, float *grad_dt_bias, float *grad_initial, hipStream_t stream) {
     constexpr int Q = 16 * kStrips<T>;
-    const ScanWork f = scan_work(a.B, a.L, a.H, a.P, a.N, Q);
+    const ScanWork f = scan_work(a.B, a.L, a.H, a.P, a.G, a.N, Elem<T>::is_bf16, true);
     const BwdWork w = bwd_work(a.B, a.L, a.H, a.P, a.G, a.N, Q);
     float *sv = const_cast<float *>(saved);  // only read here
-    const ScanDims d = {(int)a.B, (int)a.L, a.H, a.P, a.G, a.N, f.nc, a.lengths, sv + f.dt, sv + f.shi, sv + f.slo,
+    const ScanDims d = {(int)a.B, (int)a.L, a.H, a.P, a.G, a.N, f.nc, 1, a.lengths, sv + f.dt, sv + f.shi, sv + f.slo,
                         sv + f.decay};
     const int64_t blocks = a.B * f.nc * a.G * w.plan.splits, all = a.B * a.L * a.G * a.N;
     const int64_t blocks_part = w.plan.splits > 1 ? (2 * all + 1023) / 1024 : 0, blocks_sum = blocks_part + (3 * a.H + 3) / 4;
@@ -620,7 +623,7 @@ hipError_t scan_bwd(const Scan &a, const float *saved, const void *grad, int64_t
         adjoints = work + w.adjoints;
         e = launch_scan_states<T>(d, (const T *)grad, g_batch, g_token, (const T *)a.Cm, a.c_batch, a.c_token, adjoints,
                                   true, stream);
-        if (e == hipSuccess) e = launch_scan_pass(d, adjoints, grad_state, grad_initial, Q, true, stream);
+        if (e == hipSuccess) e = launch_scan_pass(d, adjoints, d.decay, grad_state, grad_initial, Q, true, stream);
     }
     if (e != hipSuccess) return e;
     const BwdArgs k = {d, w.plan, a.x_batch, a.x_token, a.b_batch, a.b_token, a.c_batch, a.c_token, g_batch, g_token,

@@ -64,8 +64,10 @@ struct OutArgs {
     ScanDims d;
     ChunkPlan plan;
     int64_t x_batch, x_token, b_batch, b_token, c_batch, c_token;
-    const float *states;  // [B, H, nc, P, cols]: the state that enters each chunk
-    int has_first;        // an initial state
+    const float *states;   // [B, H, nc, P, cols]: the state that enters each chunk, or each segment
+    const float *carried;  // [B, H, nc]: the factor of that state at a chunk of the segment
+    const void *before;    // [B, H, nc, P, before_cols]: what the segment's own tokens add to it there
+    int has_first;         // an initial state
     const float *D;
 };
 
@@ -76,16 +78,17 @@ struct OutArgs {
 // serves two strips.  The scaled C . B and the entering state are rounded to bfloat16 once, as
 // the operands of matrix products whose sums are float32; y is rounded to bfloat16 at the end
 // by as much, which is also why s alone (without its low part) is enough there.
-template <typename T, int NP, bool WHOLE>
+template <typename T, int NP, bool WHOLE, bool SEG>
 __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const T *__restrict__ X,
                                                                const T *__restrict__ Bm, const T *__restrict__ Cm,
                                                                T *__restrict__ y) {
     constexpr int QS = kStrips<T>, Q = 16 * QS, SPW = QS / 4;
     constexpr int LDN = ld_of<T>(NP), LDP = ld_of<T>(kSlab);
-    constexpr int kTiles = Q * LDP + kSlab * LDN;
+    constexpr bool TWO = SEG && Elem<T>::is_bf16;  // two parts of h0, rounded one by one, take a tile each
+    constexpr int kTiles = Q * LDP + (TWO ? 2 : 1) * kSlab * LDN;
     __shared__ __align__(16) T lds[kTiles > Q * LDN ? kTiles : Q * LDN];
     __shared__ __align__(16) float shi[Q], slo[Q], dts[Q];
-    T *xtile = lds, *htile = lds + Q * LDP;
+    T *xtile = lds, *htile = lds + Q * LDP, *btile = htile + kSlab * LDN;
     const ScanDims &d = a.d;
     const int tid = threadIdx.x, lane = tid % kWave, wave = wave_of(tid), l16 = lane % 16, g = lane / 16;
     int id = blockIdx.x;
@@ -99,9 +102,10 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
     n = n < 0 ? 0 : n > Q ? Q : n;
     const int hg = d.H / d.G, h0 = grp * hg + split * a.plan.per;
     const int h1 = h0 + a.plan.per < (grp + 1) * hg ? h0 + a.plan.per : (grp + 1) * hg;
-    const int slabs = (d.P + kSlab - 1) / kSlab, items = (h1 - h0) * slabs, cols = state_cols(d.N);
+    const int slabs = (d.P + kSlab - 1) / kSlab, items = (h1 - h0) * slabs, cols = state_cols(d.N), bcols = before_cols<T>(d.N);
     const T *xb = X + b * a.x_batch + (int64_t)c * Q * a.x_token;
-    const bool has_h = n > 0 && (c > 0 || a.has_first);
+    const int seg = SEG ? c / d.seg : c, nseg = SEG ? (d.nc + d.seg - 1) / d.seg : d.nc;
+    const bool has_h = n > 0 && (seg > 0 || a.has_first), has_b = SEG && n > 0 && c % d.seg > 0;
     int strip[SPW];
     const int below = l16 - 4 * g;  // on the diagonal tile, row v of this lane is column t's token at v == below
 #pragma unroll
@@ -109,13 +113,18 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
 
     TileFetch<T, Q, kSlab, kThreads, WHOLE> xf;
     TileFetch<float, kSlab, NP, kThreads, true> hf;
-    float tf[3], skip_next;
+    TileFetch<T, kSlab, NP, kThreads, true> bt;
+    float tf[3], skip_next, carry_next = 1.f;
     auto fetch = [&](int it) {
-        const int h = h0 + it / slabs, p0 = it % slabs * kSlab;
+        const int h = h0 + it / slabs, p0 = it % slabs * kSlab, tid = afresh(threadIdx.x);
         skip_next = a.D[h];
         xf.fetch(xb + (int64_t)h * d.P + p0, a.x_token, n, d.P - p0, tid);
         const int64_t chunk = ((int64_t)b * d.H + h) * d.nc + c;
-        if (has_h) hf.fetch(a.states + (chunk * d.P + p0) * cols, cols, d.P - p0, cols, tid);
+        if (has_h) hf.fetch(a.states + ((((int64_t)b * d.H + h) * nseg + seg) * d.P + p0) * cols, cols, d.P - p0, cols, tid);
+        if (has_b) {
+            carry_next = a.carried[chunk];
+            bt.fetch((const T *)a.before + (chunk * d.P + p0) * bcols, bcols, d.P - p0, bcols, tid);
+        }
         if (tid < Q) {
             tf[0] = d.shi[chunk * Q + tid];
             tf[1] = d.slo[chunk * Q + tid];
@@ -156,24 +165,22 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
     }
 
     for (int it = 0; it < items; ++it) {
-        const int h = h0 + it / slabs, p0 = it % slabs * kSlab;
+        const int h = h0 + it / slabs, p0 = it % slabs * kSlab, tid = afresh(threadIdx.x);
         __syncthreads();
         xf.put(xtile, LDP, n, d.P - p0, tid);
-        if (has_h) {
+        const float carry = carry_next;
+        if (has_h || (has_b && !TWO)) {
 #pragma unroll
             for (int k = 0; k < decltype(hf)::kCount; ++k) {
-                T *to = htile + hf.row_of(k, tid) * LDN + hf.col_of(k, tid);
-                const u32x4 f = hf.get(k, d.P - p0, cols, tid);
-                if constexpr (Elem<T>::is_bf16) {
-                    u16x4 v;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = f32_to_bf16_bits(__uint_as_float(f[e]));
-                    *(u16x4 *)to = v;
-                } else {
-                    *(u32x4 *)to = f;
-                }
+                f32x4 v = {0.f, 0.f, 0.f, 0.f};
+                if (has_h) v = __builtin_bit_cast(f32x4, hf.get(k, d.P - p0, cols, tid));
+                if constexpr (SEG && !TWO)
+                    if (has_b) v = v * carry + __builtin_bit_cast(f32x4, bt.get(k, d.P - p0, bcols, tid));
+                store4<T>(htile + hf.row_of(k, tid) * LDN + hf.col_of(k, tid), v, 4);
             }
         }
+        if constexpr (TWO)
+            if (has_b) bt.put(btile, LDN, d.P - p0, bcols, tid);
         if (tid < Q) {
             shi[tid] = tf[0];
             slo[tid] = tf[1];
@@ -193,21 +200,31 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
             th[j] = shi[16 * strip[j] + l16];
             tl[j] = slo[16 * strip[j] + l16];
         }
-        if (has_h) {
+        auto add_tile = [&](const T *tile) {
 #pragma unroll
             for (int k = 0; k < NP / 32; ++k)
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
-                    const Frag<T> hr = near_frag(htile + (16 * p + l16) * LDN + 32 * k, g);
+                    const Frag<T> hr = near_frag(tile + (16 * p + l16) * LDN + 32 * k, g);
 #pragma unroll
                     for (int j = 0; j < SPW; ++j) acc[j][p] = mma(hr, cf[j][k], acc[j][p]);
                 }
+        };
+        auto scale = [&](int j, float f) {
 #pragma unroll
-            for (int j = 0; j < SPW; ++j) {
-                const float f = __builtin_amdgcn_exp2f(th[j] + tl[j]);
+            for (int p = 0; p < 4; ++p) acc[j][p] *= f;
+        };
+        if (has_h || has_b) {
+            if (has_h || !TWO) add_tile(htile);
+            if constexpr (TWO) {
+                if (has_b) {
 #pragma unroll
-                for (int p = 0; p < 4; ++p) acc[j][p] *= f;
+                    for (int j = 0; j < SPW; ++j) scale(j, carry);
+                    add_tile(btile);
+                }
             }
+#pragma unroll
+            for (int j = 0; j < SPW; ++j) scale(j, __builtin_amdgcn_exp2f(th[j] + tl[j]));
         }
 #pragma unroll
         for (int i = 0; i < QS / 2; ++i) {
@@ -328,9 +345,9 @@ namespace {
 template <typename T>
 hipError_t scan_fwd(const Scan &a, float *work, void *y, float *final_state, bool save, hipStream_t stream) {
     constexpr int Q = 16 * kStrips<T>;
-    const ScanWork w = scan_work(a.B, a.L, a.H, a.P, a.N, Q);
-    const ScanDims d = {(int)a.B, (int)a.L, a.H, a.P, a.G, a.N, w.nc, a.lengths, work + w.dt, work + w.shi, work + w.slo,
-                        work + w.decay};
+    const ScanWork w = scan_work(a.B, a.L, a.H, a.P, a.G, a.N, Elem<T>::is_bf16, save);
+    const ScanDims d = {(int)a.B, (int)a.L, a.H, a.P, a.G, a.N, w.nc, w.seg, a.lengths, work + w.dt, work + w.shi,
+                        work + w.slo, work + w.decay};
     const int blocks_h = (a.H + kTimeHeads - 1) / kTimeHeads;
     const ChunkPlan plan = plan_heads(a.B, w.nc, a.H, a.G, 1024);
     const int64_t bt = a.B * w.nc * blocks_h, bo = a.B * w.nc * a.G * plan.splits;
@@ -338,19 +355,27 @@ hipError_t scan_fwd(const Scan &a, float *work, void *y, float *final_state, boo
     hipLaunchKernelGGL((scan_times_kernel<T>), dim3((unsigned)bt), dim3(kThreads), 0, stream, d, (const T *)a.dt, a.dt_batch,
                        a.dt_token, a.A, a.dt_bias, blocks_h);
     hipError_t e = hipGetLastError();
-    float *states = nullptr;
+    float *states = work + w.states;
+    T *before = (T *)(work + w.before);
     if (e == hipSuccess && (w.nc > 1 || a.initial != nullptr || final_state != nullptr || save)) {
-        states = work + w.states;
-        e = launch_scan_states<T>(d, (const T *)a.x, a.x_batch, a.x_token, (const T *)a.Bm, a.b_batch, a.b_token, states,
-                                  false, stream);
-        if (e == hipSuccess) e = launch_scan_pass(d, states, a.initial, final_state, Q, false, stream);
+        if (w.seg > 1)
+            e = launch_scan_segments<T>(d, w.hw, (const T *)a.x, a.x_batch, a.x_token, (const T *)a.Bm, a.b_batch,
+                                        a.b_token, before, work + w.carried, states, work + w.decays, stream);
+        else
+            e = launch_scan_states<T>(d, (const T *)a.x, a.x_batch, a.x_token, (const T *)a.Bm, a.b_batch, a.b_token,
+                                      states, false, stream);
+        if (e == hipSuccess) e = launch_scan_pass(d, states, w.seg > 1 ? work + w.decays : d.decay, a.initial, final_state, Q, false, stream);
     }
     if (e != hipSuccess) return e;
     const OutArgs o = {d, plan, a.x_batch, a.x_token, a.b_batch, a.b_token, a.c_batch, a.c_token, states,
-                       a.initial != nullptr, a.D};
+                       work + w.carried, before, a.initial != nullptr, a.D};
 #define X_(NP, WHOLE)                                                                                              \
-    hipLaunchKernelGGL((scan_out_kernel<T, NP, WHOLE>), dim3((unsigned)bo), dim3(kThreads), 0, stream, o,          \
-                       (const T *)a.x, (const T *)a.Bm, (const T *)a.Cm, (T *)y);
+    if (w.seg > 1)                                                                                                 \
+        hipLaunchKernelGGL((scan_out_kernel<T, NP, WHOLE, true>), dim3((unsigned)bo), dim3(kThreads), 0, stream,   \
+                           o, (const T *)a.x, (const T *)a.Bm, (const T *)a.Cm, (T *)y);                           \
+    else                                                                                                           \
+        hipLaunchKernelGGL((scan_out_kernel<T, NP, WHOLE, false>), dim3((unsigned)bo), dim3(kThreads), 0, stream,  \
+                           o, (const T *)a.x, (const T *)a.Bm, (const T *)a.Cm, (T *)y);
     DDPM_SEQ_SCAN_SHAPES(T, a.N, a.P, X_)
 #undef X_
     return hipGetLastError();
@@ -389,8 +414,8 @@ hipError_t scan_step(const Scan &a, float *state, const int *slots, int64_t S, v
 int scan_chunk(bool bf16) { return 16 * (bf16 ? kStrips<bf16_t> : kStrips<float>); }
 
 int64_t scan_fwd_floats(int64_t B, int64_t L, int H, int P, int G, int N, bool bf16) {
-    (void)G;
-    return scan_work(B, L, H, P, N, scan_chunk(bf16)).total;
+    const int64_t kept = scan_work(B, L, H, P, G, N, bf16, true).total, not_kept = scan_work(B, L, H, P, G, N, bf16, false).total;
+    return kept > not_kept ? kept : not_kept;
 }
 
 hipError_t launch_scan_fwd(const Scan &a, float *work, void *y, float *final_state, bool save, bool bf16,
