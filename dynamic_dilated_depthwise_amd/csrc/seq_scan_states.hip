@@ -216,27 +216,25 @@ __global__ __launch_bounds__(kThreads, 2) void scan_segments_kernel(StateArgs a,
     }
 }
 
-constexpr int kPassLanes = 16;
-
 // h = first; for every chunk in order: part = states[c], states[c] = h, h = decay[c] h + part.
 // `rows` states a head: the chunks, or segments of d.seg of them.
-// Sixteen lanes of four elements by PARTS runs of chunks: each run goes from zero, the runs'
-// ends are joined in LDS, and each run goes again from its true start; the parts stay in
-// registers between where a run has at most KEEP chunks and are read again otherwise.
-template <int PARTS>
-__global__ __launch_bounds__(PARTS *kPassLanes) void scan_pass_kernel(ScanDims d, int Q, int rows,
-                                                                      const float *__restrict__ decays,
-                                                                      float *__restrict__ states,
-                                                                      const float *__restrict__ first,
-                                                                      float *__restrict__ final_state, int groups,
-                                                                      int reverse) {
-    constexpr int KEEP = 4;
-    __shared__ f32x4 ends[PARTS][kPassLanes];
+// LANES of four elements by PARTS runs of states: each run goes from zero, the runs' ends are
+// joined in LDS, and each run goes again from its true start; the parts stay in registers
+// between where a run has at most KEEP of them and are read again otherwise.  PARTS = 1: one
+// run, whose states are all in registers.
+template <int PARTS, int LANES, int KEEP>
+__global__ __launch_bounds__(PARTS *LANES) void scan_pass_kernel(ScanDims d, int Q, int rows,
+                                                                 const float *__restrict__ decays,
+                                                                 float *__restrict__ states,
+                                                                 const float *__restrict__ first,
+                                                                 float *__restrict__ final_state, int groups,
+                                                                 int reverse) {
+    __shared__ f32x4 ends[PARTS > 1 ? PARTS : 1][PARTS > 1 ? LANES : 1];
     __shared__ float mults[PARTS];
-    const int lane = threadIdx.x % kPassLanes, part = threadIdx.x / kPassLanes;
+    const int lane = threadIdx.x % LANES, part = threadIdx.x / LANES;
     const int64_t head = blockIdx.x / groups;  // b * H + h
     const int cols = state_cols(d.N), per_row = cols / 4;
-    const int e = blockIdx.x % groups * kPassLanes + lane;  // in vectors of four
+    const int e = blockIdx.x % groups * LANES + lane;  // in vectors of four
     const int64_t E = (int64_t)d.P * cols;
     const bool on = e < d.P * per_row;
     const int n = valid_tokens(d.lengths, (int)(head / d.H), d.L), nc = (n + Q * d.seg - 1) / (Q * d.seg);
@@ -251,34 +249,39 @@ __global__ __launch_bounds__(PARTS *kPassLanes) void scan_pass_kernel(ScanDims d
     const int dir = reverse ? -1 : 1, c0 = reverse ? nc - 1 - from : from;
     f32x4 keep[KEEP];
     f32x4 h = {0.f, 0.f, 0.f, 0.f};
-    float m = 1.f;
     st += c0 * (E / 4);
     decay += c0;
-    if (per <= KEEP) {
+    const bool kept = PARTS == 1 || per <= KEEP;
+    if (kept) {
 #pragma unroll
         for (int k = 0; k < KEEP; ++k)
             if (from + k < to) keep[k] = st[k * step];
+    }
+    if constexpr (PARTS > 1) {
+        float m = 1.f;
+        if (kept) {
 #pragma unroll
-        for (int k = 0; k < KEEP; ++k)
-            if (from + k < to) {
-                h = h * decay[k * dir] + keep[k];
+            for (int k = 0; k < KEEP; ++k)
+                if (from + k < to) {
+                    h = h * decay[k * dir] + keep[k];
+                    m *= decay[k * dir];
+                }
+        } else {
+#pragma unroll 8
+            for (int k = 0; k < to - from; ++k) {
+                h = h * decay[k * dir] + st[k * step];
                 m *= decay[k * dir];
             }
-    } else {
-#pragma unroll 8
-        for (int k = 0; k < to - from; ++k) {
-            h = h * decay[k * dir] + st[k * step];
-            m *= decay[k * dir];
         }
+        ends[part][lane] = h;
+        if (lane == 0) mults[part] = m;
+        __syncthreads();
     }
-    ends[part][lane] = h;
-    if (lane == 0) mults[part] = m;
-    __syncthreads();
-    h = first != nullptr ? load4(first + user, left) : f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < part; ++k) h = h * mults[k] + ends[k][lane];
-    if (part == PARTS - 1 && final_state != nullptr && on) store4<float>(final_state + user, h * mults[part] + ends[part][lane], left);
     if (!on) return;
-    if (per <= KEEP) {
+    h = first != nullptr ? load4(first + user, left) : f32x4{0.f, 0.f, 0.f, 0.f};
+    if constexpr (PARTS > 1)
+        for (int k = 0; k < part; ++k) h = h * mults[k] + ends[k][lane];
+    if (kept) {
 #pragma unroll
         for (int k = 0; k < KEEP; ++k)
             if (from + k < to) {
@@ -293,6 +296,7 @@ __global__ __launch_bounds__(PARTS *kPassLanes) void scan_pass_kernel(ScanDims d
             h = h * decay[k * dir] + own;
         }
     }
+    if (part == PARTS - 1 && final_state != nullptr) store4<float>(final_state + user, h, left);
 }
 
 template <typename T>
@@ -340,17 +344,19 @@ template hipError_t launch_scan_states<bf16_t>(const ScanDims &, const bf16_t *,
 
 hipError_t launch_scan_pass(const ScanDims &d, float *states, const float *decays, const float *first, float *final_state,
                             int Q, bool reverse, hipStream_t stream) {
-    const int groups = (d.P * state_cols(d.N) / 4 + kPassLanes - 1) / kPassLanes;
+    const int rows = (d.nc + d.seg - 1) / d.seg, vectors = d.P * state_cols(d.N) / 4;
+    // A few states: a thread takes all of them.  Many: four times the runs, so that a run is
+    // short beside a memory access.
+    const int lanes = rows <= 8 ? 256 : 16, groups = (vectors + lanes - 1) / lanes;
     const int64_t blocks = (int64_t)d.B * d.H * groups;
     if (blocks > 0x7fffffff) return hipErrorInvalidConfiguration;
-    const int rows = (d.nc + d.seg - 1) / d.seg;
-    // many states: four times the runs, so that a run is short beside a memory access
-    if (rows <= 128)
-        hipLaunchKernelGGL((scan_pass_kernel<16>), dim3((unsigned)blocks), dim3(16 * kPassLanes), 0, stream, d, Q, rows,
-                           decays, states, first, final_state, groups, reverse ? 1 : 0);
-    else
-        hipLaunchKernelGGL((scan_pass_kernel<64>), dim3((unsigned)blocks), dim3(64 * kPassLanes), 0, stream, d, Q, rows,
-                           decays, states, first, final_state, groups, reverse ? 1 : 0);
+#define X(PARTS, LANES, KEEP)                                                                                        \
+    hipLaunchKernelGGL((scan_pass_kernel<PARTS, LANES, KEEP>), dim3((unsigned)blocks), dim3(PARTS * LANES), 0, stream, \
+                       d, Q, rows, decays, states, first, final_state, groups, reverse ? 1 : 0)
+    if (rows <= 8) X(1, 256, 8);
+    else if (rows <= 128) X(16, 16, 4);
+    else X(64, 16, 4);
+#undef X
     return hipGetLastError();
 }
 
