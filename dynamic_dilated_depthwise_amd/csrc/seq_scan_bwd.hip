@@ -576,7 +576,7 @@ struct BwdWork {
 BwdWork bwd_work(int64_t B, int64_t L, int H, int P, int G, int N, int Q) {
     const int64_t nc = (L + Q - 1) / Q;
     BwdWork w;
-    w.plan = plan_heads(B, nc, H, G, 512);
+    w.plan = plan_heads(B, nc, H, P, G, 256);
     w.adjoints = 0;
     w.heads = pad64(B * H * nc * P * state_cols(N));
     w.own = w.heads + pad64(3 * H * B * nc);

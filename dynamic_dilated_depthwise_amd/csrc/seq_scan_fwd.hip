@@ -349,7 +349,7 @@ hipError_t scan_fwd(const Scan &a, float *work, void *y, float *final_state, boo
     const ScanDims d = {(int)a.B, (int)a.L, a.H, a.P, a.G, a.N, w.nc, w.seg, a.lengths, work + w.dt, work + w.shi,
                         work + w.slo, work + w.decay};
     const int blocks_h = (a.H + kTimeHeads - 1) / kTimeHeads;
-    const ChunkPlan plan = plan_heads(a.B, w.nc, a.H, a.G, 1024);
+    const ChunkPlan plan = plan_heads(a.B, w.nc, a.H, a.P, a.G, 512);
     const int64_t bt = a.B * w.nc * blocks_h, bo = a.B * w.nc * a.G * plan.splits;
     if (bt > 0x7fffffff || bo > 0x7fffffff) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((scan_times_kernel<T>), dim3((unsigned)bt), dim3(kThreads), 0, stream, d, (const T *)a.dt, a.dt_batch,

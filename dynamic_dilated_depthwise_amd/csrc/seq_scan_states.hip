@@ -302,7 +302,7 @@ __global__ __launch_bounds__(PARTS *LANES) void scan_pass_kernel(ScanDims d, int
 template <typename T>
 hipError_t launch_scan_states(const ScanDims &d, const T *X, int64_t x_batch, int64_t x_token, const T *Y,
                               int64_t y_batch, int64_t y_token, float *out, bool reverse, hipStream_t stream) {
-    const ChunkPlan plan = plan_heads(d.B, d.nc, d.H, d.G, 1024);
+    const ChunkPlan plan = plan_heads(d.B, d.nc, d.H, d.P, d.G, 1024);
     const StateArgs a = {d, plan, x_batch, x_token, y_batch, y_token, reverse ? 1 : 0};
     const int64_t blocks = (int64_t)d.B * d.nc * d.G * plan.splits;
     if (blocks > 0x7fffffff) return hipErrorInvalidConfiguration;
