@@ -327,17 +327,18 @@ __device__ __forceinline__ f32x4 lds4(const bf16_t *p) {
 template <typename T, int ROWS, int COLS, int THREADS, bool WHOLE>
 struct TileFetch {
     static constexpr int kPerRow = COLS / kVec<T>;
-    static constexpr int kCount = ROWS * kPerRow / THREADS;
-    static_assert(ROWS * kPerRow % THREADS == 0, "tile must divide over the threads");
+    static constexpr int kAll = ROWS * kPerRow, kCount = (kAll + THREADS - 1) / THREADS;
     u32x4 r[kCount];
+    __device__ __forceinline__ static bool has(int k, int tid) { return kAll % THREADS == 0 || tid + k * THREADS < kAll; }
     __device__ __forceinline__ static int row_of(int k, int tid) { return (tid + k * THREADS) / kPerRow; }
     __device__ __forceinline__ static int col_of(int k, int tid) { return (tid + k * THREADS) % kPerRow * kVec<T>; }
     __device__ __forceinline__ void fetch(const T *__restrict__ base, int64_t stride, int rows, int ncols, int tid) {
 #pragma unroll
         for (int k = 0; k < kCount; ++k) {
             const int row = row_of(k, tid), c = col_of(k, tid);
-            if constexpr (WHOLE) r[k] = *(const u32x4_a2 *)(base + (row < rows && c < ncols ? row * stride + c : 0));
-            else r[k] = load_vec<T>(base + row * stride + c, row < rows ? ncols - c : 0);
+            const bool on = row < rows && has(k, tid);
+            if constexpr (WHOLE) r[k] = *(const u32x4_a2 *)(base + (on && c < ncols ? row * stride + c : 0));
+            else r[k] = load_vec<T>(base + (on ? row * stride + c : 0), on ? ncols - c : 0);
         }
     }
     // Vector k as it was fetched with these rows and ncols.
@@ -348,7 +349,7 @@ struct TileFetch {
     __device__ __forceinline__ void put(T *tile, int ld, int rows, int ncols, int tid) const {
 #pragma unroll
         for (int k = 0; k < kCount; ++k)
-            *(u32x4 *)(tile + row_of(k, tid) * ld + col_of(k, tid)) = get(k, rows, ncols, tid);
+            if (has(k, tid)) *(u32x4 *)(tile + row_of(k, tid) * ld + col_of(k, tid)) = get(k, rows, ncols, tid);
     }
 };
 

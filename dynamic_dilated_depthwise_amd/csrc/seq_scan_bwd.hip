@@ -51,7 +51,11 @@ struct BwdLds {
     static constexpr int QS = kStrips<T>, Q = 16 * QS, LDN = ld_of<T>(NP);
     static constexpr int LDP = NP <= 64 ? ld_of<T>(kSlab) : kSlab + kVec<T>;  // 160 KB hold no more at 128
     T b[Q * LDN], c[Q * LDN], x[Q * LDP], g[Q * LDP];
-    T plane[kTerms<T>][kSlab * LDN];  // h0, then g1
+    // h0 and g1: a set of planes each where 160 KB hold them, else g1 follows h0 into one
+    static constexpr int kTilesBytes = 2 * Q * (LDN + LDP) * (int)sizeof(T) + 3 * Q * 4;
+    static constexpr int kPlanes = kTerms<T> * kSlab * LDN;
+    static constexpr int kSets = kTilesBytes + 2 * kPlanes * (int)sizeof(T) <= 160 * 1024 ? 2 : 1;
+    T plane[kSets][kTerms<T>][kSlab * LDN];
     float shi[Q], slo[Q], dt[Q];
 };
 
@@ -86,7 +90,7 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
                                                                    T *__restrict__ grad_dt, T *__restrict__ grad_B,
                                                                    T *__restrict__ grad_C) {
     typedef BwdLds<T, NP> Lds;
-    constexpr int QS = Lds::QS, Q = Lds::Q, OWN = kOwn<T>, WAVES = QS / OWN, THREADS = 64 * WAVES;
+    constexpr int QS = Lds::QS, Q = Lds::Q, OWN = kOwn<T>, WAVES = QS / OWN, THREADS = 64 * WAVES, SETS = Lds::kSets;
     constexpr int LDN = Lds::LDN, LDP = Lds::LDP, NS = NP / 16;
     extern __shared__ __align__(16) char raw_lds[];
     Lds &s = *(Lds *)raw_lds;
@@ -118,7 +122,11 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
     TileFetch<float, kSlab, NP, THREADS, true> hf, af;
     float tf[3], skip_next;
     auto chunk_of = [&](int it) { return ((int64_t)b * d.H + h0 + it / slabs) * d.nc + c; };
-    // everything of an item but its adjoint, which is asked for when the one before has been used
+    auto fetch_adjoint = [&](int it) {
+        const int p0 = it % slabs * kSlab, tid = afresh(threadIdx.x);
+        if (has_g) af.fetch(a.adjoints + (chunk_of(it) * d.P + p0) * cols, cols, d.P - p0, cols, tid);
+    };
+    // an item's operands; with one set of planes the adjoint is asked for when the one before has been used
     auto fetch = [&](int it) {
         const int h = h0 + it / slabs, p0 = it % slabs * kSlab, tid = afresh(threadIdx.x);
         const int64_t chunk = chunk_of(it);
@@ -131,25 +139,30 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
         xf.fetch(xb + (int64_t)h * d.P + p0, a.x_token, n, d.P - p0, tid);
         gf.fetch(gb + (int64_t)h * d.P + p0, a.g_token, n, d.P - p0, tid);
         if (has_h) hf.fetch(a.states + (chunk * d.P + p0) * cols, cols, d.P - p0, cols, tid);
+        if (SETS == 2) fetch_adjoint(it);
     };
-    auto fetch_adjoint = [&](int it) {
-        const int p0 = it % slabs * kSlab, tid = afresh(threadIdx.x);
-        if (has_g) af.fetch(a.adjoints + (chunk_of(it) * d.P + p0) * cols, cols, d.P - p0, cols, tid);
-    };
-    // a float32 tile into the planes; `dot` gains its product with what this thread put there before
+    // A float32 tile into a set of planes.  `dot` gains the adjoint's product with the state: with
+    // one set the state is what this thread put there before.
     float dot = 0.f;
-    auto put_planes = [&](const decltype(hf) &f, int p0, bool against) {
+    auto put_planes = [&](const decltype(hf) &f, int set, int p0, bool against) {
         const int tid = afresh(threadIdx.x);
 #pragma unroll
         for (int k = 0; k < decltype(hf)::kCount; ++k) {
+            if (!hf.has(k, tid)) continue;
             const int at = f.row_of(k, tid) * LDN + f.col_of(k, tid);
             float v[4];
             widen<float>(f.get(k, d.P - p0, cols, tid), v);
+            if (against && SETS == 2) {
+                float w[4];
+                widen<float>(hf.get(k, d.P - p0, cols, tid), w);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dot += v[e] * w[e];
+            }
             if constexpr (Elem<T>::is_bf16) {
-                if (against) {
+                if (against && SETS == 1) {
                     u16x4 t[3];
 #pragma unroll
-                    for (int m = 0; m < 3; ++m) t[m] = *(const u16x4 *)(s.plane[m] + at);
+                    for (int m = 0; m < 3; ++m) t[m] = *(const u16x4 *)(s.plane[0][m] + at);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)  // the three terms' sum is the float32 that they came from
                         dot += v[e] * (bf16_bits_to_f32(t[0][e]) + (bf16_bits_to_f32(t[1][e]) + bf16_bits_to_f32(t[2][e])));
@@ -164,14 +177,14 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
                     t[2][e] = __builtin_bit_cast(uint16_t, q2);
                 }
 #pragma unroll
-                for (int m = 0; m < 3; ++m) *(u16x4 *)(s.plane[m] + at) = t[m];
+                for (int m = 0; m < 3; ++m) *(u16x4 *)(s.plane[set][m] + at) = t[m];
             } else {
-                if (against) {
-                    const f32x4 t = *(const f32x4 *)(s.plane[0] + at);
+                if (against && SETS == 1) {
+                    const f32x4 t = *(const f32x4 *)(s.plane[0][0] + at);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) dot += v[e] * t[e];
                 }
-                *(f32x4 *)(s.plane[0] + at) = f32x4{v[0], v[1], v[2], v[3]};
+                *(f32x4 *)(s.plane[set][0] + at) = f32x4{v[0], v[1], v[2], v[3]};
             }
         }
     };
@@ -241,7 +254,7 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
         bf.put(s.b, LDN, n, d.N, tid);
         cf.put(s.c, LDN, n, d.N, tid);
         fetch(0);
-        fetch_adjoint(0);
+        if (SETS == 1) fetch_adjoint(0);
         __syncthreads();
         auto tiles = [&](const T *rows_of, int strip, const T *cols_of, f32x4 (&r)[OWN][2], int u) {
 #pragma unroll
@@ -279,7 +292,8 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
         __syncthreads();
         xf.put(s.x, LDP, n, d.P - p0, tid);
         gf.put(s.g, LDP, n, d.P - p0, tid);
-        if (has_h) put_planes(hf, p0, false);
+        if (has_h) put_planes(hf, 0, p0, false);
+        if (SETS == 2 && has_g) put_planes(af, SETS - 1, p0, has_h);
         if (tid < Q) {
             s.shi[tid] = tf[0];
             s.slo[tid] = tf[1];
@@ -306,6 +320,9 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
 #pragma unroll
             for (int p = 0; p < 4; ++p) dx[j][p] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
+        int below[OWN];  // in the own pair, row 16 u + 4 g + v is this lane's token at 16 u + v == below
+#pragma unroll
+        for (int j = 0; j < OWN; ++j) below[j] = afresh(me[j]) - 32 * kw - 4 * g;
         // a pair of strips i = 2 k, 2 k + 1 against the wave's rows t
         auto as_rows = [&](int k, const f32x4 (&cb)[OWN][2], bool own) {
             f32x4 wt[OWN][2];
@@ -322,7 +339,7 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {
                         dif[v] = (mhi[j] - ih[v]) + (mlo[j] - il[v]);
-                        if (own) dif[v] = 16 * is + 4 * g + v <= me[j] ? dif[v] : -INFINITY;
+                        if (own) dif[v] = 16 * u + v <= below[j] ? dif[v] : -INFINITY;
                         wt[j][u][v] = z[v] * (__builtin_amdgcn_exp2f(dif[v]) * id4[v]);
                         rown[j] += cb[j][u][v] * wt[j][u][v];  // the columns add the very same products
                     }
@@ -353,7 +370,7 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {
                         dif[v] = (th[v] - mhi[j]) + (tl[v] - mlo[j]);
-                        if (own) dif[v] = 16 * ts + 4 * g + v >= me[j] ? dif[v] : -INFINITY;
+                        if (own) dif[v] = 16 * u + v >= below[j] ? dif[v] : -INFINITY;
                         const float e = __builtin_amdgcn_exp2f(dif[v]);
                         nt[j][u][v] = cb[j][u][v] * e;
                         wt[j][u][v] = z[v] * (e * mdt[j]);
@@ -403,7 +420,7 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
                 for (int t = 0; t < kTerms<T>; ++t)
 #pragma unroll
                     for (int m = 0; m < NS; ++m) {
-                        const Frag<T> f = col_frag(s.plane[t], LDN, 32 * q, 16 * m, l16, g);
+                        const Frag<T> f = col_frag(s.plane[0][t], LDN, 32 * q, 16 * m, l16, g);
 #pragma unroll
                         for (int j = 0; j < OWN; ++j) o[j][m] = mma(f, go[j], o[j][m]);
                     }
@@ -422,12 +439,13 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
             }
         }
 
-        // the gradient from later chunks, in the planes of h0
-        if (has_g) {
+        if (SETS == 1 && has_g) {
             __syncthreads();
-            put_planes(af, p0, has_h);
+            put_planes(af, 0, p0, has_h);
             if (it + 1 < items) fetch_adjoint(it + 1);
             __syncthreads();
+        }
+        if (has_g) {
             f32x4 o[OWN][4], w[OWN][NS];
 #pragma unroll
             for (int j = 0; j < OWN; ++j) {
@@ -445,7 +463,7 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
                 for (int t = 0; t < kTerms<T>; ++t)
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {
-                        const Frag<T> f = near_frag(s.plane[t] + (16 * p + l16) * LDN + 32 * k, g);
+                        const Frag<T> f = near_frag(s.plane[SETS - 1][t] + (16 * p + l16) * LDN + 32 * k, g);
 #pragma unroll
                         for (int j = 0; j < OWN; ++j) o[j][p] = mma(f, br[j], o[j][p]);
                     }
@@ -459,7 +477,7 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
                 for (int t = 0; t < (kTerms<T> > 1 ? 2 : 1); ++t)
 #pragma unroll
                     for (int m = 0; m < NS; ++m) {
-                        const Frag<T> f = col_frag(s.plane[t], LDN, 32 * q, 16 * m, l16, g);
+                        const Frag<T> f = col_frag(s.plane[SETS - 1][t], LDN, 32 * q, 16 * m, l16, g);
 #pragma unroll
                         for (int j = 0; j < OWN; ++j) w[j][m] = mma(f, xo[j], w[j][m]);
                     }
