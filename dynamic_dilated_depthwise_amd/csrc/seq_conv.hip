@@ -125,7 +125,7 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvArgs a, T *__res
 }
 
 constexpr int kBwdVec = 4;    // channels of a thread where it keeps windows and sums of them (backward), or has few (step)
-constexpr int kBwdBatch = 8;  // tokens asked for at once, a batch ahead of the one at work
+constexpr int kBwdBatch = 4;  // tokens that are asked for ahead of the one at work
 
 // Workgroup: cl threads along the channels by kThreads / cl walks of a.run tokens; its sums
 // over the walks go to row `split` of part [splits, D * W + D].
@@ -163,24 +163,14 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs a, const T 
             if (j > KW - a.W) win[j] = token<T, V, R>(a, xb, ib, t0 - KW + j, n, c);
             else win[j].r = typename Raw<T, V>::words(0);
         }
-        auto ask = [&](int from) {
-#pragma unroll
-            for (int k = 0; k < U; ++k) {
-                const int t = from + k;
-                const bool on = t < n && t < t1 + W1;
-                x[k].template load<R>(xb + (on ? (int64_t)t * a.x_token : 0), c, a.D, on);
-                g[k].template load<R>(gb + (on ? (int64_t)t * g_token : 0), c, a.D, on);
-            }
+        auto ask = [&](int k, int t) {  // token t into slot k
+            const bool on = t < n && t < t1 + W1;
+            x[k].template load<R>(xb + (on ? (int64_t)t * a.x_token : 0), c, a.D, on);
+            g[k].template load<R>(gb + (on ? (int64_t)t * g_token : 0), c, a.D, on);
         };
-        ask(t0);
-        for (int from = t0; from < t1 + W1; from += U) {
-            Raw<T, V> xc[U], gc[U];
 #pragma unroll
-            for (int k = 0; k < U; ++k) {
-                xc[k] = x[k];
-                gc[k] = g[k];
-            }
-            if (from + U < t1 + W1) ask(from + U);
+        for (int k = 0; k < U; ++k) ask(k, t0 + k);
+        for (int from = t0; from < t1 + W1; from += U) {
             // step t makes du[t] (zero past the length, as g is) and emits the gradient of x at t - W1, whose last
             // term it is
 #pragma unroll
@@ -193,7 +183,9 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs a, const T 
 #pragma unroll
                     for (int e = 0; e < V; ++e) du[j][e] = du[j + 1][e];
                 }
-                win[KW - 1] = xc[k];
+                win[KW - 1] = x[k];
+                const Raw<T, V> gc = g[k];
+                ask(k, t + U);
                 float o[V];
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
@@ -201,7 +193,7 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs a, const T 
 #pragma unroll
                     for (int j = 0; j < KW; ++j) u += w[j][e] * win[j][e];
                     const float sg = fast_sigmoid(u);
-                    const float d = gc[k][e] * (sg * (1.f + u * (1.f - sg)));
+                    const float d = gc[e] * (sg * (1.f + u * (1.f - sg)));
                     du[KW - 1][e] = d;
                     const float mine = d * own;
 #pragma unroll
@@ -303,14 +295,14 @@ struct BwdShape {
     int run, cl;
     int64_t blocks_c, splits;
 };
-// A walk takes whole batches with the W - 1 tokens past its run: four of them (the halo is
-// then a tenth for W = 4), fewer only where too few threads would be left.
+// A walk takes whole batches with the W - 1 tokens past its run: 32 tokens (the halo is then a
+// tenth for W = 4), fewer only where too few threads would be left.
 BwdShape bwd_shape(int64_t B, int64_t L, int64_t D, int W) {
     const int64_t nvec = (D + kBwdVec - 1) / kBwdVec;
     int cl = 8;
     while (cl < 64 && cl < nvec) cl *= 2;
-    int batches = 4;
-    while (batches > 1 && B * (L / (kBwdBatch * batches) + 1) * nvec < (1 << 16)) batches /= 2;
+    int batches = 8;
+    while (batches > 2 && B * (L / (kBwdBatch * batches) + 1) * nvec < (1 << 16)) batches /= 2;
     const int run = kBwdBatch * batches - (W - 1);
     const int64_t walks = B * ((L + run - 1) / run), per = kThreads / cl;
     return {run, cl, (nvec + cl - 1) / cl, (walks + per - 1) / per};
