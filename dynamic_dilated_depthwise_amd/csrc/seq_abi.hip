@@ -8,6 +8,7 @@
 namespace {
 
 constexpr int64_t kMax = 0x7fffffff;
+constexpr int64_t kMaxRun = kMax - 65535;  // of what kernels walk: the end of a last, partial block stays an int
 constexpr double kMostElements = 1e17;  // of a tensor: keeps every product of sizes in 64 bits
 
 struct Span {
@@ -24,7 +25,7 @@ struct Check {
 
     explicit Check(int dt) : dtype(dt), bad(dt != DDPM_F32 && dt != DDPM_BF16) {}
     int64_t es() const { return dtype == DDPM_BF16 ? 2 : 4; }
-    void size(int64_t v) { bad |= v < 1 || v > kMax; }
+    void size(int64_t v, int64_t most = kMax) { bad |= v < 1 || v > most; }
     void stride(int64_t v) { bad |= v < 0 || v > (int64_t(1) << 46); }
     void pointer(const void *p, int64_t align) { bad |= p == nullptr || (uintptr_t)p % align != 0; }
     void input(const void *p, double count, int64_t width) {
@@ -74,8 +75,8 @@ bool is_bf16(int dtype) { return dtype == DDPM_BF16; }
 
 int conv_sizes(Check &c, int64_t batch, int64_t length, int64_t D, int width, int64_t x_batch, int64_t x_token) {
     c.size(batch);
-    c.size(length);
-    c.size(D);
+    c.size(length, kMaxRun);
+    c.size(D, kMaxRun);
     c.size(width);
     c.stride(x_batch);
     c.stride(x_token);
@@ -87,8 +88,10 @@ bool scan_sizes_ok(const ddpm_scan *s) {
     if (s == nullptr || (s->dtype != DDPM_F32 && s->dtype != DDPM_BF16)) return false;
     for (int64_t v : {s->batch, s->length, (int64_t)s->heads, (int64_t)s->P, (int64_t)s->groups, (int64_t)s->N})
         if (v < 1 || v > kMax) return false;
-    // length + a chunk stays an int, and so do a head's state and a token's row
-    if (s->length > kMax - 1024 || (int64_t)s->P * s->N > kMax || (int64_t)s->heads * s->P > kMax) return false;
+    // a head's state, its rows padded, and a token's rows are walked as ints
+    if (s->length > kMaxRun || (int64_t)s->P * (s->N + 3) > kMaxRun || (int64_t)s->heads * s->P > kMaxRun ||
+        (int64_t)s->groups * s->N > kMaxRun)
+        return false;
     const double tokens = (double)s->batch * (s->length + 1024);
     if (tokens * s->heads * s->P > kMostElements || tokens * s->groups * s->N > kMostElements ||
         tokens / 64 * s->heads * s->P * s->N > kMostElements)
@@ -127,9 +130,9 @@ int ddpm_layer_norm_fwd(const void *x, const void *weight, const void *bias, voi
                         int64_t rows, int64_t C, int64_t x_row, float eps, int dtype, hipStream_t stream) {
     Check c(dtype);
     c.size(rows);
-    c.size(C);
+    c.size(C, kMaxRun);
     c.stride(x_row);
-    if (c.bad || (mean == nullptr) != (rstd == nullptr)) return DDPM_ERR_INVALID_ARG;
+    if (c.bad || !(eps >= 0.f) || (mean == nullptr) != (rstd == nullptr)) return DDPM_ERR_INVALID_ARG;
     c.input(x, extent(1, rows, C, 0, x_row), c.es());
     c.input(weight, C, c.es());
     c.input(bias, C, c.es());
@@ -145,7 +148,7 @@ int ddpm_layer_norm_fwd(const void *x, const void *weight, const void *bias, voi
 int64_t ddpm_layer_norm_bwd_workspace(int64_t rows, int64_t C, int dtype) {
     Check c(dtype);
     c.size(rows);
-    c.size(C);
+    c.size(C, kMaxRun);
     return c.bad ? 0 : (int64_t)ddpm::seq::norm_partials(rows, C, is_bf16(dtype)) * 2 * C * 4;
 }
 
@@ -154,7 +157,7 @@ int ddpm_layer_norm_bwd(const void *grad, const void *x, const void *weight, con
                         int64_t x_row, int64_t grad_row, int dtype, hipStream_t stream) {
     Check c(dtype);
     c.size(rows);
-    c.size(C);
+    c.size(C, kMaxRun);
     c.stride(x_row);
     c.stride(grad_row);
     if (c.bad) return DDPM_ERR_INVALID_ARG;

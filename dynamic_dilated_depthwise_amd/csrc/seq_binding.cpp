@@ -9,6 +9,7 @@
 #include <ATen/hip/EmptyTensor.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/core/StreamGuard.h>
+#include <c10/hip/HIPCachingAllocator.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -47,12 +48,14 @@ struct Call {
     std::optional<c10::DeviceGuard> at_device;
     int dtype = 0;
     hipStream_t stream = nullptr;
+    bool given = false;  // a stream other than the current one
 
     Call(PyObject *ox, const char *name, PyObject *stream_or_none) : x(tensor(ox, name)) {
         if (stream_or_none != Py_None) {
             if (!PyObject_IsInstance(stream_or_none, (PyObject *)THPStreamClass))
                 throw c10::TypeError({__func__, __FILE__, __LINE__}, "stream must be a torch.cuda.Stream");
             auto *s = (THPStream *)stream_or_none;
+            given = c10::hip::getCurrentHIPStream(x.device().index()).id() != s->stream_id;
             on.emplace(c10::Stream::unpack3(s->stream_id, (c10::DeviceIndex)s->device_index, (c10::DeviceType)s->device_type));
             if (s->device_index != x.device().index()) refuse("stream must be on ", x.device());
         } else if (x.device().index() != c10::hip::current_device()) {
@@ -62,6 +65,13 @@ struct Call {
         else if (x.scalar_type() == at::kBFloat16) dtype = DDPM_BF16;
         else refuse("unsupported dtype ", x.scalar_type(), "; use float32 or bfloat16");
         stream = c10::hip::getCurrentHIPStream(x.device().index()).stream();
+        use(x);
+    }
+
+    // On a given stream an argument's memory must not go to another tensor before the work is
+    // done, whenever its owner lets go of it; outputs and workspaces come from that stream.
+    void use(const Tensor &t) const {
+        if (given) c10::hip::HIPCachingAllocator::recordStream(t.storage().data_ptr(), c10::hip::getCurrentHIPStream(x.device().index()));
     }
 
     Tensor empty(at::IntArrayRef sizes, at::ScalarType t) const {
@@ -74,6 +84,7 @@ struct Call {
         if (t.scalar_type() != type) refuse(name, " must be ", type, " (got ", t.scalar_type(), ")");
         if (t.sizes() != sizes) refuse(name, " must have shape ", sizes, " (got ", t.sizes(), ")");
         if (t.device() != x.device()) refuse(name, " must be on ", x.device(), " (got ", t.device(), ")");
+        use(t);
     }
     // A contiguous tensor of this type and shape.
     void *like(PyObject *o, const char *name, at::ScalarType type, at::IntArrayRef sizes) const {

@@ -176,7 +176,7 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs a, const T 
 #pragma unroll
             for (int k = 0; k < U; ++k) {
                 const int t = from + k, at = t - W1;
-                const float own = t < t1 ? 1.f : 0.f;
+                const bool live = t < n, own = t < t1;
 #pragma unroll
                 for (int j = 0; j + 1 < KW; ++j) {
                     win[j].r = EXACT || j >= KW - a.W ? win[j + 1].r : typename Raw<T, V>::words(0);
@@ -193,9 +193,10 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs a, const T 
 #pragma unroll
                     for (int j = 0; j < KW; ++j) u += w[j][e] * win[j][e];
                     const float sg = fast_sigmoid(u);
-                    const float d = gc[e] * (sg * (1.f + u * (1.f - sg)));
+                    // past the length the taps may still reach infinities before it
+                    const float d = live ? gc[e] * (sg * (1.f + u * (1.f - sg))) : 0.f;
                     du[KW - 1][e] = d;
-                    const float mine = d * own;
+                    const float mine = own ? d : 0.f;
 #pragma unroll
                     for (int j = 0; j < KW; ++j) sw[j][e] += mine * win[j][e];
                     sb[e] += mine;

@@ -38,11 +38,10 @@ struct BwdArgs {
     const float *states, *adjoints;  // [B, H, nc, P, cols]; adjoints null: nothing reaches the only chunk's end
     const float *A, *D;
     float *part;   // [splits, 2, B, L, G, N] or null (one split: grad_B and grad_C at once)
-    float *heads;  // [3, H, B * nc]: every chunk's part of grad_A, grad_dt_bias, grad_D
-    // for the sums over a head's tokens at a workgroup's end, [B, H, nc, Q]: r_own - q_own,
-    // r_in, q / dt, q_end; and [B, H, nc, waves, 2]: the waves' parts of <g1, h0> and grad . x
-    double *own;
-    float *rin, *direct, *qend, *marks;
+    double *heads;  // [3, H, B * nc]: every chunk's part of grad_A, grad_dt_bias, grad_D
+    // for the sums over a head's tokens at a workgroup's end, [B, H, nc, Q]: r_in + r_own - q_own,
+    // q_end, q / dt; and [B, H, nc, waves, 2]: the waves' parts of <g1, h0> and grad . x
+    double *later, *qend, *direct, *marks;
     int has_first, has_last;  // an initial state, a gradient of the final one
 };
 
@@ -65,7 +64,8 @@ __device__ __forceinline__ V over_groups(V v) {
     v += __shfl_xor(v, 16, kWave);
     return v + __shfl_xor(v, 32, kWave);
 }
-__device__ __forceinline__ float over_wave(float v) {
+template <typename V>
+__device__ __forceinline__ V over_wave(V v) {
 #pragma unroll
     for (int m = 1; m < kWave; m *= 2) v += __shfl_xor(v, m, kWave);
     return v;
@@ -74,23 +74,18 @@ __device__ __forceinline__ float over_wave(float v) {
 __device__ __forceinline__ float frag_at(const bf16x8 &f, int e) { return (float)f[e]; }
 __device__ __forceinline__ float frag_at(const FragF &f, int e) { return f.v[e]; }
 
-// Strips of 16 tokens that a wave owns: two in bfloat16, so that each operand read from LDS
-// serves two products and two independent chains run in a wave; one in float32, whose matrix
-// products leave LDS idle.
-template <typename T> constexpr int kOwn = 1;
-
-// One chunk, some heads of a group.  A wave has its strips of the chunk's tokens both as rows t
+// One chunk, some heads of a group.  A wave has a strip of the chunk's tokens both as rows t
 // (grad_C, r) and as columns i (grad_x, grad_B, q).  Strips go in pairs, 32 of a contraction:
 // a wave in pair kw has the pairs before kw as rows, those after it as columns, and its own as
 // both, masked; the same work for every wave, and its tiles of C . B stay in registers.
 template <typename T, int NP, bool WHOLE>
-__global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(BwdArgs a, const T *__restrict__ X,
+__global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, const T *__restrict__ X,
                                                                    const T *__restrict__ Bm, const T *__restrict__ Cm,
                                                                    const T *__restrict__ grad, T *__restrict__ grad_x,
                                                                    T *__restrict__ grad_dt, T *__restrict__ grad_B,
                                                                    T *__restrict__ grad_C) {
     typedef BwdLds<T, NP> Lds;
-    constexpr int QS = Lds::QS, Q = Lds::Q, OWN = kOwn<T>, WAVES = QS / OWN, THREADS = 64 * WAVES, SETS = Lds::kSets;
+    constexpr int WAVES = Lds::QS, Q = Lds::Q, THREADS = 64 * WAVES, SETS = Lds::kSets;
     constexpr int LDN = Lds::LDN, LDP = Lds::LDP, NS = NP / 16;
     extern __shared__ __align__(16) char raw_lds[];
     Lds &s = *(Lds *)raw_lds;
@@ -113,10 +108,8 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
     const bool has_h = n > 0 && (c > 0 || a.has_first), has_g = (c + 1) * Q < len || (a.has_last && n > 0);
     const T *xb = X + b * a.x_batch + (int64_t)c * Q * a.x_token;
     const T *gb = grad + b * a.g_batch + (int64_t)c * Q * a.g_token;
-    const int kw = OWN == 2 ? wave : wave / 2;
-    int me[OWN];  // this lane's tokens, as rows t and as columns i
-#pragma unroll
-    for (int j = 0; j < OWN; ++j) me[j] = 16 * (OWN * wave + j) + l16;
+    const int kw = wave / 2;
+    const int me = 16 * wave + l16;  // this lane's token, as row t and as column i
 
     TileFetch<T, Q, kSlab, THREADS, WHOLE> xf, gf;
     TileFetch<float, kSlab, NP, THREADS, true> hf, af;
@@ -143,7 +136,7 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
     };
     // A float32 tile into a set of planes.  `dot` gains the adjoint's product with the state: with
     // one set the state is what this thread put there before.
-    float dot = 0.f;
+    double dot = 0.;
     auto put_planes = [&](const decltype(hf) &f, int set, int p0, bool against) {
         const int tid = afresh(threadIdx.x);
 #pragma unroll
@@ -192,14 +185,13 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
     auto finish_head = [&](int h) {
         constexpr int PER = Q / kWave;
         const int64_t chunk = ((int64_t)b * d.H + h) * d.nc + c, at = chunk * Q + lane * PER;
-        float dot = 0.f, diag = 0.f;
+        double dot = 0., diag = 0.;
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) {
             dot += a.marks[(chunk * WAVES + w) * 2];
             diag += a.marks[(chunk * WAVES + w) * 2 + 1];
         }
-        float pre[PER], before = 0.f;
-        double suf[PER], after = 0.;
+        double pre[PER], suf[PER], before = 0., after = 0.;
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
             pre[e] = before;
@@ -207,31 +199,30 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
         }
 #pragma unroll
         for (int e = PER - 1; e >= 0; --e) {
-            after += a.own[at + e] + a.rin[at + e];
+            after += a.later[at + e];
             suf[e] = after;
         }
-        float up = before;
-        double down = after;
+        double up = before, down = after;
 #pragma unroll
         for (int m = 1; m < kWave; m *= 2) {
-            const float u = __shfl_up(up, m, kWave);
-            const double o = __shfl_down(down, m, kWave);
+            const double u = __shfl_up(up, m, kWave), o = __shfl_down(down, m, kWave);
             if (lane >= m) up += u;
             if (lane + m < kWave) down += o;
         }
         up -= before;
         down -= after;
-        const float A = a.A[h], end = d.decay[chunk];
-        float sum_a = 0.f, sum_b = 0.f;
+        const double A = a.A[h], end = d.decay[chunk];
+        double sum_a = 0., sum_b = 0.;
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
             const int t = lane * PER + e;
-            const float dt = d.dt[at + e], flow = end * dot + (up + pre[e]) + (float)(down + suf[e]);
+            const float dt = d.dt[at + e];
+            const double flow = end * dot + (up + pre[e]) + (down + suf[e]);
             // softplus's derivative from its value: 1 - exp(-dt)
-            const float raw = t < n ? (a.direct[at + e] + A * flow) * -expm1f(-dt) : 0.f;
-            sum_a += t < n ? dt * flow : 0.f;
+            const double raw = t < n ? (a.direct[at + e] + A * flow) * -expm1f(-dt) : 0.;
+            sum_a += t < n ? dt * flow : 0.;
             sum_b += raw;
-            if (t < rows) grad_dt[(tok0 + t) * d.H + h] = Elem<T>::from_f32(raw);
+            if (t < rows) grad_dt[(tok0 + t) * d.H + h] = Elem<T>::from_f32((float)raw);
         }
         sum_a = over_wave(sum_a);
         sum_b = over_wave(sum_b);
@@ -245,8 +236,8 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
 
     // B and C, and the tiles of C . B: as rows transposed, D[i][t], as columns D[t][i].  Slot k
     // is pair k as rows for k < kw and pair k + 1 as columns from kw on.
-    constexpr int SLOTS = QS / 2 - 1;
-    f32x4 cbs[SLOTS][OWN][2], cbr[OWN][2], cbc[OWN][2];
+    constexpr int SLOTS = WAVES / 2 - 1;
+    f32x4 cbs[SLOTS][2], cbr[2], cbc[2];
     {
         TileFetch<T, Q, NP, THREADS, false> bf, cf;
         bf.fetch(Bm + b * a.b_batch + (int64_t)c * Q * a.b_token + grp * d.N, a.b_token, n, d.N, tid);
@@ -256,14 +247,12 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
         fetch(0);
         if (SETS == 1) fetch_adjoint(0);
         __syncthreads();
-        auto tiles = [&](const T *rows_of, int strip, const T *cols_of, f32x4 (&r)[OWN][2], int u) {
-#pragma unroll
-            for (int j = 0; j < OWN; ++j) r[j][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+        auto tiles = [&](const T *rows_of, int strip, const T *cols_of, f32x4 (&r)[2], int u) {
+            r[u] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int k = 0; k < NP / 32; ++k) {
                 const Frag<T> f = near_frag(rows_of + (16 * strip + l16) * LDN + 32 * k, g);
-#pragma unroll
-                for (int j = 0; j < OWN; ++j) r[j][u] = mma(f, near_frag(cols_of + me[j] * LDN + 32 * k, g), r[j][u]);
+                r[u] = mma(f, near_frag(cols_of + me * LDN + 32 * k, g), r[u]);
             }
         };
 #pragma unroll
@@ -277,14 +266,12 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
             tiles(s.c, 2 * kw + u, s.b, cbc, u);
         }
     }
-    f32x4 dB[OWN][NS], dC[OWN][NS];
+    f32x4 dB[NS], dC[NS];
 #pragma unroll
-    for (int j = 0; j < OWN; ++j)
-#pragma unroll
-        for (int k = 0; k < NS; ++k) dB[j][k] = dC[j][k] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < NS; ++k) dB[k] = dC[k] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    double rown[OWN] = {}, qown[OWN] = {};
-    float rin[OWN] = {}, qdt[OWN] = {}, qend[OWN] = {}, zdiag = 0.f;
+    double rown = 0., qown = 0., rin = 0., qdt = 0., qend = 0.;
+    float zdiag = 0.f;
     for (int it = 0; it < items; ++it) {
         const int h = h0 + it / slabs, slab = it % slabs, p0 = slab * kSlab;
         const int64_t chunk = chunk_of(it);
@@ -302,100 +289,79 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
         __syncthreads();
         const float skip = skip_next;  // asked for with the item: a read here would wait for the next item's too
         if (it + 1 < items) fetch(it + 1);
-        float mhi[OWN], mlo[OWN], mdt[OWN];
-        Frag<T> xr[OWN][2], gr[OWN][2];
-        f32x4 dx[OWN][4];
+        const float mhi = s.shi[me], mlo = s.slo[me], mdt = s.dt[me];
+        Frag<T> xr[2], gr[2];
+        f32x4 dx[4];
 #pragma unroll
-        for (int j = 0; j < OWN; ++j) {
-            mhi[j] = s.shi[me[j]];
-            mlo[j] = s.slo[me[j]];
-            mdt[j] = s.dt[me[j]];
+        for (int q = 0; q < 2; ++q) {
+            xr[q] = near_frag(s.x + me * LDP + 32 * q, g);
+            gr[q] = near_frag(s.g + me * LDP + 32 * q, g);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                xr[j][q] = near_frag(s.x + me[j] * LDP + 32 * q, g);
-                gr[j][q] = near_frag(s.g + me[j] * LDP + 32 * q, g);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) zdiag += frag_at(xr[j][q], e) * frag_at(gr[j][q], e);
-            }
-#pragma unroll
-            for (int p = 0; p < 4; ++p) dx[j][p] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int e = 0; e < 8; ++e) zdiag += frag_at(xr[q], e) * frag_at(gr[q], e);
         }
-        int below[OWN];  // in the own pair, row 16 u + 4 g + v is this lane's token at 16 u + v == below
 #pragma unroll
-        for (int j = 0; j < OWN; ++j) below[j] = afresh(me[j]) - 32 * kw - 4 * g;
+        for (int p = 0; p < 4; ++p) dx[p] = f32x4{0.f, 0.f, 0.f, 0.f};
+        // in the own pair, row 16 u + 4 g + v is this lane's token at 16 u + v == below
+        const int below = afresh(me) - 32 * kw - 4 * g;
         // a pair of strips i = 2 k, 2 k + 1 against the wave's rows t
-        auto as_rows = [&](int k, const f32x4 (&cb)[OWN][2], bool own) {
-            f32x4 wt[OWN][2];
+        auto as_rows = [&](int k, const f32x4 (&cb)[2], bool own) {
+            f32x4 wt[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int is = 2 * k + u;
                 const Frag<T> x0 = near_frag(s.x + (16 * is + l16) * LDP, g), x1 = near_frag(s.x + (16 * is + l16) * LDP + 32, g);
                 const f32x4 ih = *(const f32x4 *)(s.shi + 16 * is + 4 * g), il = *(const f32x4 *)(s.slo + 16 * is + 4 * g);
                 const f32x4 id4 = *(const f32x4 *)(s.dt + 16 * is + 4 * g);
+                f32x4 z = {0.f, 0.f, 0.f, 0.f}, dif;
+                z = mma(x1, gr[1], mma(x0, gr[0], z));
 #pragma unroll
-                for (int j = 0; j < OWN; ++j) {
-                    f32x4 z = {0.f, 0.f, 0.f, 0.f}, dif;
-                    z = mma(x1, gr[j][1], mma(x0, gr[j][0], z));
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        dif[v] = (mhi[j] - ih[v]) + (mlo[j] - il[v]);
-                        if (own) dif[v] = 16 * u + v <= below[j] ? dif[v] : -INFINITY;
-                        wt[j][u][v] = z[v] * (__builtin_amdgcn_exp2f(dif[v]) * id4[v]);
-                        rown[j] += cb[j][u][v] * wt[j][u][v];  // the columns add the very same products
-                    }
+                for (int v = 0; v < 4; ++v) {
+                    dif[v] = (mhi - ih[v]) + (mlo - il[v]);
+                    if (own) dif[v] = 16 * u + v <= below ? dif[v] : -INFINITY;
+                    wt[u][v] = z[v] * (__builtin_amdgcn_exp2f(dif[v]) * id4[v]);
+                    rown += cb[u][v] * wt[u][v];  // the columns add the very same products
                 }
             }
-            Frag<T> wf[OWN], wl[OWN];
-#pragma unroll
-            for (int j = 0; j < OWN; ++j) wf[j] = pack_frag2<T>(wt[j][0], wt[j][1], wl[j]);
+            Frag<T> wl;
+            const Frag<T> wf = pack_frag2<T>(wt[0], wt[1], wl);
 #pragma unroll
             for (int m = 0; m < NS; ++m) {
                 const Frag<T> f = col_frag(s.b, LDN, 32 * k, 16 * m, l16, g);
-#pragma unroll
-                for (int j = 0; j < OWN; ++j) dC[j][m] = mma2(f, wf[j], wl[j], dC[j][m]);
+                dC[m] = mma2(f, wf, wl, dC[m]);
             }
         };
         // a pair of strips t = 2 k, 2 k + 1 against the wave's columns i
-        auto as_columns = [&](int k, const f32x4 (&cb)[OWN][2], bool own) {
-            f32x4 nt[OWN][2], wt[OWN][2];
+        auto as_columns = [&](int k, const f32x4 (&cb)[2], bool own) {
+            f32x4 nt[2], wt[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int ts = 2 * k + u;
                 const Frag<T> g0 = near_frag(s.g + (16 * ts + l16) * LDP, g), g1 = near_frag(s.g + (16 * ts + l16) * LDP + 32, g);
                 const f32x4 th = *(const f32x4 *)(s.shi + 16 * ts + 4 * g), tl = *(const f32x4 *)(s.slo + 16 * ts + 4 * g);
+                f32x4 z = {0.f, 0.f, 0.f, 0.f}, dif;
+                z = mma(g1, xr[1], mma(g0, xr[0], z));
 #pragma unroll
-                for (int j = 0; j < OWN; ++j) {
-                    f32x4 z = {0.f, 0.f, 0.f, 0.f}, dif;
-                    z = mma(g1, xr[j][1], mma(g0, xr[j][0], z));
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        dif[v] = (th[v] - mhi[j]) + (tl[v] - mlo[j]);
-                        if (own) dif[v] = 16 * u + v >= below[j] ? dif[v] : -INFINITY;
-                        const float e = __builtin_amdgcn_exp2f(dif[v]);
-                        nt[j][u][v] = cb[j][u][v] * e;
-                        wt[j][u][v] = z[v] * (e * mdt[j]);
-                        qown[j] += cb[j][u][v] * wt[j][u][v];
-                        qdt[j] += nt[j][u][v] * z[v];
-                    }
+                for (int v = 0; v < 4; ++v) {
+                    dif[v] = (th[v] - mhi) + (tl[v] - mlo);
+                    if (own) dif[v] = 16 * u + v >= below ? dif[v] : -INFINITY;
+                    const float e = __builtin_amdgcn_exp2f(dif[v]);
+                    nt[u][v] = cb[u][v] * e;
+                    wt[u][v] = z[v] * (e * mdt);
+                    qown += cb[u][v] * wt[u][v];
+                    qdt += nt[u][v] * z[v];
                 }
             }
-            Frag<T> nf[OWN], wf[OWN], wl[OWN];
-#pragma unroll
-            for (int j = 0; j < OWN; ++j) {
-                nf[j] = pack_frag<T>(nt[j][0], nt[j][1]);
-                wf[j] = pack_frag2<T>(wt[j][0], wt[j][1], wl[j]);
-            }
+            Frag<T> wl;
+            const Frag<T> nf = pack_frag<T>(nt[0], nt[1]), wf = pack_frag2<T>(wt[0], wt[1], wl);
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
                 const Frag<T> f = col_frag(s.g, LDP, 32 * k, 16 * p, l16, g);
-#pragma unroll
-                for (int j = 0; j < OWN; ++j) dx[j][p] = mma(f, nf[j], dx[j][p]);
+                dx[p] = mma(f, nf, dx[p]);
             }
 #pragma unroll
             for (int m = 0; m < NS; ++m) {
                 const Frag<T> f = col_frag(s.c, LDN, 32 * k, 16 * m, l16, g);
-#pragma unroll
-                for (int j = 0; j < OWN; ++j) dB[j][m] = mma2(f, wf[j], wl[j], dB[j][m]);
+                dB[m] = mma2(f, wf, wl, dB[m]);
             }
         };
         as_rows(kw, cbr, true);
@@ -406,36 +372,28 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
             else as_columns(k + 1, cbs[k], false);
         }
         if (has_h) {
-            f32x4 o[OWN][NS];
+            f32x4 o[NS];
 #pragma unroll
-            for (int j = 0; j < OWN; ++j)
-#pragma unroll
-                for (int m = 0; m < NS; ++m) o[j][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int m = 0; m < NS; ++m) o[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                Frag<T> go[OWN];
-#pragma unroll
-                for (int j = 0; j < OWN; ++j) go[j] = row_frag(s.g + me[j] * LDP + 32 * q, g);
+                const Frag<T> go = row_frag(s.g + me * LDP + 32 * q, g);
 #pragma unroll
                 for (int t = 0; t < kTerms<T>; ++t)
 #pragma unroll
                     for (int m = 0; m < NS; ++m) {
                         const Frag<T> f = col_frag(s.plane[0][t], LDN, 32 * q, 16 * m, l16, g);
-#pragma unroll
-                        for (int j = 0; j < OWN; ++j) o[j][m] = mma(f, go[j], o[j][m]);
+                        o[m] = mma(f, go, o[m]);
                     }
             }
+            const float f = __builtin_amdgcn_exp2f(mhi + mlo);
 #pragma unroll
-            for (int j = 0; j < OWN; ++j) {
-                const float f = __builtin_amdgcn_exp2f(mhi[j] + mlo[j]);
+            for (int m = 0; m < NS; ++m) {
+                o[m] *= f;
+                dC[m] += o[m];
+                const f32x4 cv = lds4(s.c + me * LDN + 16 * m + 4 * g);
 #pragma unroll
-                for (int m = 0; m < NS; ++m) {
-                    o[j][m] *= f;
-                    dC[j][m] += o[j][m];
-                    const f32x4 cv = lds4(s.c + me[j] * LDN + 16 * m + 4 * g);
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) rin[j] += o[j][m][v] * cv[v];
-                }
+                for (int v = 0; v < 4; ++v) rin += o[m][v] * cv[v];
             }
         }
 
@@ -446,113 +404,91 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
             __syncthreads();
         }
         if (has_g) {
-            f32x4 o[OWN][4], w[OWN][NS];
+            f32x4 o[4], w[NS];
 #pragma unroll
-            for (int j = 0; j < OWN; ++j) {
+            for (int p = 0; p < 4; ++p) o[p] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int p = 0; p < 4; ++p) o[j][p] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int m = 0; m < NS; ++m) w[j][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-            }
+            for (int m = 0; m < NS; ++m) w[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int k = 0; k < NP / 32; ++k) {
-                Frag<T> br[OWN];
-#pragma unroll
-                for (int j = 0; j < OWN; ++j) br[j] = near_frag(s.b + me[j] * LDN + 32 * k, g);
+                const Frag<T> br = near_frag(s.b + me * LDN + 32 * k, g);
 #pragma unroll
                 for (int t = 0; t < kTerms<T>; ++t)
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {
                         const Frag<T> f = near_frag(s.plane[SETS - 1][t] + (16 * p + l16) * LDN + 32 * k, g);
-#pragma unroll
-                        for (int j = 0; j < OWN; ++j) o[j][p] = mma(f, br[j], o[j][p]);
+                        o[p] = mma(f, br, o[p]);
                     }
             }
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                Frag<T> xo[OWN];
-#pragma unroll
-                for (int j = 0; j < OWN; ++j) xo[j] = row_frag(s.x + me[j] * LDP + 32 * q, g);
+                const Frag<T> xo = row_frag(s.x + me * LDP + 32 * q, g);
 #pragma unroll
                 for (int t = 0; t < (kTerms<T> > 1 ? 2 : 1); ++t)
 #pragma unroll
                     for (int m = 0; m < NS; ++m) {
                         const Frag<T> f = col_frag(s.plane[SETS - 1][t], LDN, 32 * q, 16 * m, l16, g);
-#pragma unroll
-                        for (int j = 0; j < OWN; ++j) w[j][m] = mma(f, xo[j], w[j][m]);
+                        w[m] = mma(f, xo, w[m]);
                     }
             }
+            const float f1 = __builtin_amdgcn_exp2f((s.shi[Q - 1] - mhi) + (s.slo[Q - 1] - mlo)), f2 = f1 * mdt;
 #pragma unroll
-            for (int j = 0; j < OWN; ++j) {
-                const float f1 = __builtin_amdgcn_exp2f((s.shi[Q - 1] - mhi[j]) + (s.slo[Q - 1] - mlo[j])), f2 = f1 * mdt[j];
+            for (int p = 0; p < 4; ++p) {
+                o[p] *= f1;
+                dx[p] += o[p];
+                const f32x4 xv = lds4(s.x + me * LDP + 16 * p + 4 * g);
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    o[j][p] *= f1;
-                    dx[j][p] += o[j][p];
-                    const f32x4 xv = lds4(s.x + me[j] * LDP + 16 * p + 4 * g);
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) qend[j] += o[j][p][v] * xv[v];
-                }
-#pragma unroll
-                for (int m = 0; m < NS; ++m) dB[j][m] += w[j][m] * f2;
+                for (int v = 0; v < 4; ++v) qend += o[p][v] * xv[v];
             }
-        }
 #pragma unroll
-        for (int j = 0; j < OWN; ++j) {
-            if (me[j] >= rows) continue;
-            T *o = grad_x + ((tok0 + me[j]) * d.H + h) * d.P + p0;
+            for (int m = 0; m < NS; ++m) dB[m] += w[m] * f2;
+        }
+        if (me < rows) {
+            T *o = grad_x + ((tok0 + me) * d.H + h) * d.P + p0;
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
                 const int at = 16 * p + 4 * g;
-                f32x4 r = dx[j][p] * mdt[j] + skip * lds4(s.g + me[j] * LDP + at);
+                f32x4 r = dx[p] * mdt + skip * lds4(s.g + me * LDP + at);
 #pragma unroll
-                for (int v = 0; v < 4; ++v) r[v] = me[j] < n ? r[v] : 0.f;
+                for (int v = 0; v < 4; ++v) r[v] = me < n ? r[v] : 0.f;
                 if (p0 + at < d.P) store4<T>(o + at, r, WHOLE ? 4 : d.P - p0 - at);
             }
         }
         if (slab + 1 == slabs) {
-#pragma unroll
-            for (int j = 0; j < OWN; ++j) {
-                const double own = over_groups(rown[j] - qown[j]);
-                const float r = over_groups(rin[j]), q0 = over_groups(qdt[j]), q1 = over_groups(qend[j]);
-                if (g == 0) {
-                    const int64_t at = chunk * Q + me[j];
-                    a.own[at] = own;
-                    a.rin[at] = r;
-                    a.direct[at] = q0 + q1;
-                    a.qend[at] = mdt[j] * q1;
-                }
-                rown[j] = qown[j] = 0.;
-                rin[j] = qdt[j] = qend[j] = 0.f;
+            const double later = over_groups(rin + (rown - qown)), q0 = over_groups(qdt), q1 = over_groups(qend);
+            if (g == 0) {
+                const int64_t at = chunk * Q + me;
+                a.later[at] = later;
+                a.direct[at] = q0 + q1;
+                a.qend[at] = mdt * q1;
             }
+            rown = qown = rin = qdt = qend = 0.;
             dot = over_wave(dot);
-            zdiag = over_wave(zdiag);
+            const double diag = over_wave((double)zdiag);
             if (lane == 0) {
                 a.marks[(chunk * WAVES + wave) * 2] = dot;
-                a.marks[(chunk * WAVES + wave) * 2 + 1] = zdiag;
+                a.marks[(chunk * WAVES + wave) * 2 + 1] = diag;
             }
-            dot = zdiag = 0.f;
+            dot = 0.;
+            zdiag = 0.f;
         }
     }
     __syncthreads();
     for (int h = h0 + wave; h < h1; h += WAVES) finish_head(h);
 
+    if (me >= rows) return;
+    const int64_t at = ((tok0 + me) * d.G + grp) * d.N;
+    const int64_t all = (int64_t)d.B * d.L * d.G * d.N;
 #pragma unroll
-    for (int j = 0; j < OWN; ++j) {
-        if (me[j] >= rows) continue;
-        const int64_t at = ((tok0 + me[j]) * d.G + grp) * d.N;
-        const int64_t all = (int64_t)d.B * d.L * d.G * d.N;
-#pragma unroll
-        for (int m = 0; m < NS; ++m) {
-            const int k = 16 * m + 4 * g;
-            if (k >= d.N) continue;
-            if (a.part != nullptr) {
-                store4<float>(a.part + 2 * split * all + at + k, dB[j][m], d.N - k);
-                store4<float>(a.part + (2 * split + 1) * all + at + k, dC[j][m], d.N - k);
-            } else {
-                store4<T>(grad_B + at + k, dB[j][m], d.N - k);
-                store4<T>(grad_C + at + k, dC[j][m], d.N - k);
-            }
+    for (int m = 0; m < NS; ++m) {
+        const int k = 16 * m + 4 * g;
+        if (k >= d.N) continue;
+        if (a.part != nullptr) {
+            store4<float>(a.part + 2 * split * all + at + k, dB[m], d.N - k);
+            store4<float>(a.part + (2 * split + 1) * all + at + k, dC[m], d.N - k);
+        } else {
+            store4<T>(grad_B + at + k, dB[m], d.N - k);
+            store4<T>(grad_C + at + k, dC[m], d.N - k);
         }
     }
 }
@@ -562,7 +498,7 @@ __global__ __launch_bounds__(64 * kStrips<T> / kOwn<T>) void scan_bwd_kernel(Bwd
 template <typename T>
 __global__ __launch_bounds__(256) void scan_bwd_sum_kernel(const float *__restrict__ part, int splits, int64_t all,
                                                            T *__restrict__ grad_B, T *__restrict__ grad_C,
-                                                           const float *__restrict__ heads, int H, int64_t chunks,
+                                                           const double *__restrict__ heads, int H, int64_t chunks,
                                                            float *__restrict__ grad_A, float *__restrict__ grad_bias,
                                                            float *__restrict__ grad_D, int64_t blocks_part) {
     if (blockIdx.x < blocks_part) {
@@ -589,7 +525,7 @@ namespace {
 
 struct BwdWork {
     ChunkPlan plan;
-    int64_t adjoints, heads, own, tokens, rin, direct, qend, marks, part, total;
+    int64_t adjoints, heads, later, qend, direct, marks, part, total;
 };
 BwdWork bwd_work(int64_t B, int64_t L, int H, int P, int G, int N, int Q) {
     const int64_t nc = (L + Q - 1) / Q;
@@ -597,13 +533,12 @@ BwdWork bwd_work(int64_t B, int64_t L, int H, int P, int G, int N, int Q) {
     w.plan = plan_heads(B, nc, H, P, G, 256);
     w.adjoints = 0;
     w.heads = pad64(B * H * nc * P * state_cols(N));
-    w.own = w.heads + pad64(3 * H * B * nc);
-    w.tokens = pad64(B * H * nc * Q);
-    w.rin = w.own + 2 * w.tokens;
-    w.direct = w.rin + w.tokens;
-    w.qend = w.direct + w.tokens;
-    w.marks = w.qend + w.tokens;
-    w.part = w.marks + pad64(B * H * nc * (Q / 16) * 2);
+    const int64_t tokens = pad64(2 * B * H * nc * Q);  // these and what follows to `part` in 64 bits
+    w.later = w.heads + pad64(6 * H * B * nc);
+    w.qend = w.later + tokens;
+    w.direct = w.qend + tokens;
+    w.marks = w.direct + tokens;
+    w.part = w.marks + pad64(4 * B * H * nc * (Q / 16));
     w.total = w.part + (w.plan.splits > 1 ? pad64(2 * w.plan.splits * B * L * G * N) : 0);
     return w;
 }
@@ -616,7 +551,7 @@ hipError_t launch_main(const BwdArgs &k, int64_t blocks, const Scan &a, const vo
     auto kern = scan_bwd_kernel<T, NP, WHOLE>;
     hipError_t e = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(64 * kStrips<T> / kOwn<T>), bytes, stream, k, (const T *)a.x,
+    hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(64 * kStrips<T>), bytes, stream, k, (const T *)a.x,
                        (const T *)a.Bm, (const T *)a.Cm, (const T *)grad, (T *)grad_x, (T *)grad_dt, (T *)grad_B,
                        (T *)grad_C);
     return hipGetLastError();
@@ -645,8 +580,9 @@ hipError_t scan_bwd(const Scan &a, const float *saved, const void *grad, int64_t
     }
     if (e != hipSuccess) return e;
     const BwdArgs k = {d, w.plan, a.x_batch, a.x_token, a.b_batch, a.b_token, a.c_batch, a.c_token, g_batch, g_token,
-                       saved + f.states, adjoints, a.A, a.D, w.plan.splits > 1 ? work + w.part : nullptr, work + w.heads,
-                       (double *)(work + w.own), work + w.rin, work + w.direct, work + w.qend, work + w.marks,
+                       saved + f.states, adjoints, a.A, a.D, w.plan.splits > 1 ? work + w.part : nullptr,
+                       (double *)(work + w.heads), (double *)(work + w.later), (double *)(work + w.qend),
+                       (double *)(work + w.direct), (double *)(work + w.marks),
                        a.initial != nullptr, grad_state != nullptr};
 #define X_(NP, WHOLE) e = launch_main<T, NP, WHOLE>(k, blocks, a, grad, grad_x, grad_dt, grad_B, grad_C, stream);
     DDPM_SEQ_SCAN_SHAPES(T, a.N, a.P, X_)

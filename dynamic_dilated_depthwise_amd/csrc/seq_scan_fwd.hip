@@ -33,7 +33,7 @@ __global__ __launch_bounds__(kThreads) void scan_times_kernel(ScanDims d, const 
     const int k = threadIdx.x / kWave;
     if (h0 + k < d.H) {
         const double a = A[h0 + k] * kLog2e;
-        const int64_t at = ((int64_t)(b * d.H + h0 + k) * d.nc + c) * Q + lane * PER;
+        const int64_t at = (((int64_t)b * d.H + h0 + k) * d.nc + c) * Q + lane * PER;
         double s[PER], run = 0.;
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
@@ -56,7 +56,7 @@ __global__ __launch_bounds__(kThreads) void scan_times_kernel(ScanDims d, const 
             d.slo[at + e] = (float)(before + s[e] - hi);
         }
         if (lane == kWave - 1)
-            d.decay[(int64_t)(b * d.H + h0 + k) * d.nc + c] = __builtin_amdgcn_exp2f((float)(before + run));
+            d.decay[((int64_t)b * d.H + h0 + k) * d.nc + c] = __builtin_amdgcn_exp2f((float)(before + run));
     }
 }
 

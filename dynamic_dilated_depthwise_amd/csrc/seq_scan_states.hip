@@ -91,7 +91,7 @@ __global__ __launch_bounds__(kThreads) void scan_states_kernel(StateArgs a, cons
     TileFetch<T, Q, NP, kThreads, false> yf;
     TileFetch<T, Q, kSlab, kThreads, WHOLE> xf;
     TimesFetch tf;
-    auto chunk_of = [&](int it) { return (int64_t)(b * d.H + h0 + it / slabs) * d.nc + c; };
+    auto chunk_of = [&](int it) { return ((int64_t)b * d.H + h0 + it / slabs) * d.nc + c; };
     auto fetch = [&](int it) {
         const int p0 = it % slabs * kSlab;
         tf.fetch(d, chunk_of(it) * Q, Q, a.reverse, tid);

@@ -18,12 +18,19 @@ Inputs along a sequence may be views whose last axis (scan: all but the first tw
 contiguous, such as the slices of one projection.  lengths and slots are int32 [batch]; see
 the header for what they mean, and for widths (to 8) and state columns (to 128).
 
+Streams: a call on a given `stream` does not wait for work on the current one that makes its
+arguments; it keeps their memory from reuse until its own work is done.  All calls may be
+captured into a graph.  Before a training step is captured, let go of every eager result that
+still holds a graph of the same leaves: torch's engine joins the stream on which such a graph
+was made, which a capture does not allow and which ends the process.
+
 The checks and allocations are native (``csrc/seq_binding.cpp``): a single token's kernel
 takes 3 us, the same checks in Python four times that.
 """
 import os
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import raw_library
 
@@ -97,6 +104,10 @@ def selective_scan_step(x, dt, A, B, C, D, dt_bias, state, slots=None, stream=No
 
 
 # ------------------------------------------------------------------------------- autograd
+def _differentiated(*ts):
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in ts)
+
+
 def _rowwise(t, axes):
     """t itself if its axes after the first `axes` are contiguous, else a contiguous copy."""
     want = 1
@@ -115,6 +126,7 @@ class _LayerNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad):
         return (*layer_norm_bwd(grad.contiguous(), *ctx.saved_tensors), None)
 
@@ -127,6 +139,7 @@ class _CausalConv(torch.autograd.Function):
         return causal_conv_fwd(x, weight, bias, initial_state, lengths, return_state=True)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad, grad_state):
         x, weight, bias, initial_state, lengths = ctx.saved_tensors
         if grad is None:
@@ -145,6 +158,7 @@ class _SelectiveScan(torch.autograd.Function):
         return y, state
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad, grad_state):
         saved = ctx.saved_tensors
         if grad is None:
@@ -155,15 +169,23 @@ class _SelectiveScan(torch.autograd.Function):
 
 def layer_norm(x, weight, bias, eps=1e-5):
     """Differentiable layer norm over the last axis."""
-    return _LayerNorm.apply(x if x.dim() == 2 and x.stride(-1) == 1 else x.contiguous(), weight, bias, eps)
+    x = x if x.dim() == 2 and x.stride(-1) == 1 else x.contiguous()
+    if not _differentiated(x, weight, bias):
+        return layer_norm_fwd(x, weight, bias, eps)[0]
+    return _LayerNorm.apply(x, weight, bias, eps)
 
 
 def causal_conv(x, weight, bias, initial_state=None, lengths=None):
     """Differentiable (y, state) of causal_conv_fwd."""
-    return _CausalConv.apply(_rowwise(x, 2), weight, bias, initial_state, lengths)
+    args = _rowwise(x, 2), weight, bias, initial_state
+    if not _differentiated(*args):
+        return causal_conv_fwd(*args, lengths, return_state=True)
+    return _CausalConv.apply(*args, lengths)
 
 
 def selective_scan(x, dt, A, B, C, D, dt_bias, initial_state=None, lengths=None):
     """Differentiable (y, state) of selective_scan_fwd."""
-    return _SelectiveScan.apply(_rowwise(x, 2), _rowwise(dt, 2), A, _rowwise(B, 2), _rowwise(C, 2), D, dt_bias,
-                                initial_state, lengths)
+    args = _rowwise(x, 2), _rowwise(dt, 2), A, _rowwise(B, 2), _rowwise(C, 2), D, dt_bias, initial_state
+    if not _differentiated(*args):
+        return selective_scan_fwd(*args, lengths, return_state=True)[:2]
+    return _SelectiveScan.apply(*args, lengths)

@@ -27,9 +27,11 @@
  *   state[slots[b]].  A slot outside [0, num_slots) marks a place without a sequence: y is
  *   zero and no state is touched.  A slot may be named once in a call.
  * Errors.  As in ddpm.h; all arguments are checked before anything is enqueued.
- *     DDPM_ERR_INVALID_ARG  null or misaligned pointers, sizes below 1 or beyond 2^31 - 1,
- *                           negative strides, an unknown dtype, overlapping outputs,
- *                           heads not a multiple of groups;
+ *     DDPM_ERR_INVALID_ARG  null or misaligned pointers, sizes below 1 or beyond 2^31 - 1
+ *                           (2^31 - 2^16 for C, length and D, and in the scan for heads * P,
+ *                           groups * N and P * (N + 3)), a negative or NaN eps, negative
+ *                           strides, an unknown dtype, overlapping outputs, heads not a
+ *                           multiple of groups;
  *     DDPM_ERR_UNSUPPORTED  width > 8, state columns N > 128 (scan over sequences), or a
  *                           grid beyond 2^31 - 1 workgroups.
  */
