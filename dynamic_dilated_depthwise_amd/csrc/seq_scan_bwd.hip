@@ -136,7 +136,7 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
     };
     // A float32 tile into a set of planes.  `dot` gains the adjoint's product with the state: with
     // one set the state is what this thread put there before.
-    double dot = 0.;
+    float dot = 0.f;
     auto put_planes = [&](const decltype(hf) &f, int set, int p0, bool against) {
         const int tid = afresh(threadIdx.x);
 #pragma unroll
@@ -270,8 +270,8 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
 #pragma unroll
     for (int k = 0; k < NS; ++k) dB[k] = dC[k] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    double rown = 0., qown = 0., rin = 0., qdt = 0., qend = 0.;
-    float zdiag = 0.f;
+    double rown = 0., qown = 0.;
+    float rin = 0.f, qdt = 0.f, qend = 0.f, zdiag = 0.f;
     for (int it = 0; it < items; ++it) {
         const int h = h0 + it / slabs, slab = it % slabs, p0 = slab * kSlab;
         const int64_t chunk = chunk_of(it);
@@ -455,22 +455,21 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
             }
         }
         if (slab + 1 == slabs) {
-            const double later = over_groups(rin + (rown - qown)), q0 = over_groups(qdt), q1 = over_groups(qend);
+            const double later = over_groups(rin + (rown - qown)), q0 = over_groups((double)qdt), q1 = over_groups((double)qend);
             if (g == 0) {
                 const int64_t at = chunk * Q + me;
                 a.later[at] = later;
                 a.direct[at] = q0 + q1;
                 a.qend[at] = mdt * q1;
             }
-            rown = qown = rin = qdt = qend = 0.;
-            dot = over_wave(dot);
-            const double diag = over_wave((double)zdiag);
+            rown = qown = 0.;
+            rin = qdt = qend = 0.f;
+            const double all_dot = over_wave((double)dot), diag = over_wave((double)zdiag);
             if (lane == 0) {
-                a.marks[(chunk * WAVES + wave) * 2] = dot;
+                a.marks[(chunk * WAVES + wave) * 2] = all_dot;
                 a.marks[(chunk * WAVES + wave) * 2 + 1] = diag;
             }
-            dot = 0.;
-            zdiag = 0.f;
+            dot = zdiag = 0.f;
         }
     }
     __syncthreads();
