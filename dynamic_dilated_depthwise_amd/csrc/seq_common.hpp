@@ -215,10 +215,15 @@ template <typename T> using Frag = typename FragOf<T>::type;
 template <typename T> constexpr int ld_of(int cols) { return cols + (Elem<T>::is_bf16 && cols <= 64 ? 16 : kVec<T>); }
 
 __device__ __forceinline__ f32x4 mma(const bf16x8 &a, const bf16x8 &b, f32x4 c) { return mfma_16x16x32_bf16(a, b, c); }
+// Two chains of four, so that fewer roundings follow each other (and the second starts at once).
 __device__ __forceinline__ f32x4 mma(const FragF &a, const FragF &b, f32x4 c) {
+    f32x4 d = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) c = mfma_16x16x4_f32(a.v[e], b.v[e], c);
-    return c;
+    for (int e = 0; e < 8; e += 2) {
+        c = mfma_16x16x4_f32(a.v[e], b.v[e], c);
+        d = mfma_16x16x4_f32(a.v[e + 1], b.v[e + 1], d);
+    }
+    return c + d;
 }
 
 // Contraction along a row: `row` points at element k0 of the lane's own row.  near_frag is
