@@ -152,7 +152,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_segments_kernel(StateArgs a,
     // items past the group's last repeat it (and store nothing)
     auto item = [&](int i) { return split * HW + i < all ? split * HW + i : all - 1; };
     auto head = [&](int i) { return (int64_t)b * d.H + grp * (d.H / d.G) + item(i) / slabs; };
-    TileFetch<T, Q, NP, kThreads, false> yf;
+    TileFetch<T, Q, NP, kThreads, WHOLE> yf;
     TileFetch<T, Q, kSlab, kThreads, WHOLE> xf;
     TimesFetch tf;
     float decay = 1.f;
@@ -321,14 +321,14 @@ hipError_t launch_scan_segments(const ScanDims &d, int hw, const T *X, int64_t x
     const StateArgs a = {d, {hw, (items + hw - 1) / hw}, x_batch, x_token, y_batch, y_token, 0};
     const int64_t blocks = (int64_t)d.B * ((d.nc + d.seg - 1) / d.seg) * d.G * a.plan.splits;
     if (blocks > 0x7fffffff) return hipErrorInvalidConfiguration;
-#define X_(NP, WHOLE)                                                                                               \
-    if (hw == 2)                                                                                                    \
-        hipLaunchKernelGGL((scan_segments_kernel<T, NP, WHOLE, 2>), dim3((unsigned)blocks), dim3(kThreads), 0,      \
-                           stream, a, X, Y, before, carried, ends, decays);                                               \
-    else                                                                                                            \
-        hipLaunchKernelGGL((scan_segments_kernel<T, NP, WHOLE, 1>), dim3((unsigned)blocks), dim3(kThreads), 0,      \
-                           stream, a, X, Y, before, carried, ends, decays);
+#define LAUNCH(NP, WHOLE, HW)                                                                                      \
+    hipLaunchKernelGGL((scan_segments_kernel<T, NP, WHOLE, HW>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, \
+                       a, X, Y, before, carried, ends, decays)
+#define X_(NP, WHOLE)                                                                    \
+    if (WHOLE && d.N % kVec<T> == 0) { if (hw == 2) LAUNCH(NP, true, 2); else LAUNCH(NP, true, 1); } \
+    else { if (hw == 2) LAUNCH(NP, false, 2); else LAUNCH(NP, false, 1); }
     DDPM_SEQ_SCAN_SHAPES(T, d.N, d.P, X_)
+#undef LAUNCH
 #undef X_
     return hipGetLastError();
 }
