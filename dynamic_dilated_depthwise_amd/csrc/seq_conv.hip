@@ -154,14 +154,17 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs a, const T 
         const T *gs = grad_state ? grad_state + (int64_t)b * W1 * a.D : nullptr;
         T *gx = grad_x + (int64_t)b * a.L * a.D;
         T *gi = grad_initial ? grad_initial + (int64_t)b * W1 * a.D : nullptr;
-        float w[KW][V], du[KW][V] = {};
-        Raw<T, V> win[KW], bias, x[U], g[U];
+        float w[KW][V], win[KW][V], du[KW][V] = {};
+        Raw<T, V> bias, x[U], g[U];
         load_taps<T, KW, V, R, EXACT>((const T *)a.weight, c, a.D, a.W, w);
         bias.template load<R>((const T *)a.bias, c, a.D, true);
 #pragma unroll
         for (int j = 1; j < KW; ++j) {
-            if (j > KW - a.W) win[j] = token<T, V, R>(a, xb, ib, t0 - KW + j, n, c);
-            else win[j].r = typename Raw<T, V>::words(0);
+            Raw<T, V> r;
+            if (j > KW - a.W) r = token<T, V, R>(a, xb, ib, t0 - KW + j, n, c);
+            else r.r = typename Raw<T, V>::words(0);
+#pragma unroll
+            for (int e = 0; e < V; ++e) win[j][e] = r[e];
         }
         auto ask = [&](int k, int t) {  // token t into slot k
             const bool on = t < n && t < t1 + W1;
@@ -176,30 +179,41 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs a, const T 
 #pragma unroll
             for (int k = 0; k < U; ++k) {
                 const int t = from + k, at = t - W1;
-                const bool live = t < n, own = t < t1;
 #pragma unroll
-                for (int j = 0; j + 1 < KW; ++j) {
-                    win[j].r = EXACT || j >= KW - a.W ? win[j + 1].r : typename Raw<T, V>::words(0);
+                for (int j = 0; j + 1 < KW; ++j)
 #pragma unroll
-                    for (int e = 0; e < V; ++e) du[j][e] = du[j + 1][e];
-                }
-                win[KW - 1] = x[k];
+                    for (int e = 0; e < V; ++e) {
+                        win[j][e] = EXACT || j >= KW - a.W ? win[j + 1][e] : 0.f;
+                        du[j][e] = du[j + 1][e];
+                    }
+#pragma unroll
+                for (int e = 0; e < V; ++e) win[KW - 1][e] = x[k][e];
                 const Raw<T, V> gc = g[k];
                 ask(k, t + U);
                 float o[V];
+                if (t < n) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        float u = bias[e];
+#pragma unroll
+                        for (int j = 0; j < KW; ++j) u += w[j][e] * win[j][e];
+                        const float sg = fast_sigmoid(u);
+                        du[KW - 1][e] = gc[e] * (sg * (1.f + u * (1.f - sg)));
+                    }
+                } else {  // the taps may still reach infinities before the length
+#pragma unroll
+                    for (int e = 0; e < V; ++e) du[KW - 1][e] = 0.f;
+                }
+                if (t < t1) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+#pragma unroll
+                        for (int j = 0; j < KW; ++j) sw[j][e] += du[KW - 1][e] * win[j][e];
+                        sb[e] += du[KW - 1][e];
+                    }
+                }
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    float u = bias[e];
-#pragma unroll
-                    for (int j = 0; j < KW; ++j) u += w[j][e] * win[j][e];
-                    const float sg = fast_sigmoid(u);
-                    // past the length the taps may still reach infinities before it
-                    const float d = live ? gc[e] * (sg * (1.f + u * (1.f - sg))) : 0.f;
-                    du[KW - 1][e] = d;
-                    const float mine = own ? d : 0.f;
-#pragma unroll
-                    for (int j = 0; j < KW; ++j) sw[j][e] += mine * win[j][e];
-                    sb[e] += mine;
                     // du[at + k] is in slot KW - W + k, the tap that it meets W - 1 - k
                     float s = 0.f;
 #pragma unroll
