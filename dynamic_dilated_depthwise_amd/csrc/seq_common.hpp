@@ -184,6 +184,15 @@ __device__ __forceinline__ f32x4 load4(const float *__restrict__ p, int n) {
     return v;
 }
 
+// Workgroups go to the eight XCDs in turn; numbered like this, 32 neighbours at a time are on one,
+// and what they share in its L2.  No more than 32, so that sequences of different lengths still
+// spread over all XCDs.
+__device__ __forceinline__ int64_t block_in_stretch() {
+    constexpr int64_t kRow = 32, kAll = 8 * kRow;
+    const int64_t id = blockIdx.x, first = id / kAll * kAll, at = id - first;
+    return first + kAll <= gridDim.x ? first + at % 8 * kRow + at / 8 : id;
+}
+
 // The wave's number in its workgroup, as a scalar: branches on it are then branches and not
 // masks (left in a vector register it costs the scan's kernels a factor of two and more).
 __device__ __forceinline__ int wave_of(int tid) { return __builtin_amdgcn_readfirstlane(tid / kWave); }

@@ -73,20 +73,12 @@ __device__ __forceinline__ Raw<T, V> token(const ConvArgs &a, const T *xb, const
     return r;
 }
 
-// Workgroups go to the eight XCDs in turn; numbered like this, 32 neighbours at a time are on one,
-// and the tokens that their runs share in its L2 (37 -> 34 us at 2 x 8192 x 2304 bfloat16, width 4).
-// No more than 32, so that sequences of different lengths still spread over all XCDs.
-__device__ __forceinline__ int64_t block_in_stretch() {
-    constexpr int64_t kRow = 32, kAll = 8 * kRow;
-    const int64_t id = blockIdx.x, first = id / kAll * kAll, at = id - first;
-    return first + kAll <= gridDim.x ? first + at % 8 * kRow + at / 8 : id;
-}
-
 // A thread makes `RUN` tokens: their inputs and the W - 1 before are all asked for first.
 template <typename T, int KW, bool EXACT, int V, Reach R, int RUN>
 __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvArgs a, T *__restrict__ y, T *__restrict__ last,
                                                             int64_t walks) {
     if (EXACT) a.W = KW;
+    // shared tokens from the XCD's L2: 37 -> 34 us at 2 x 8192 x 2304 bfloat16, width 4
     const int64_t id = block_in_stretch() * kThreads + threadIdx.x;
     const int runs = (a.L + RUN - 1) / RUN;
     if (id >= walks) {  // the state behind the last token: W - 1 rows a sequence

@@ -91,7 +91,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
     T *xtile = lds, *htile = lds + Q * LDP, *btile = htile + kSlab * LDN;
     const ScanDims &d = a.d;
     const int tid = threadIdx.x, lane = tid % kWave, wave = wave_of(tid), l16 = lane % 16, g = lane / 16;
-    int id = blockIdx.x;
+    int id = (int)block_in_stretch();
     const int split = id % a.plan.splits;
     id /= a.plan.splits;
     const int grp = id % d.G;

@@ -76,7 +76,7 @@ __global__ __launch_bounds__(kThreads) void scan_states_kernel(StateArgs a, cons
     __shared__ __align__(16) float w[Q];
     const ScanDims &d = a.d;
     const int tid = threadIdx.x, lane = tid % kWave, wave = wave_of(tid), l16 = lane % 16, g = lane / 16;
-    int id = blockIdx.x;
+    int id = (int)block_in_stretch();
     const int split = id % a.plan.splits;
     id /= a.plan.splits;
     const int grp = id % d.G;
@@ -139,7 +139,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_segments_kernel(StateArgs a,
     const ScanDims &d = a.d;
     const int tid = threadIdx.x, lane = tid % kWave, wave = wave_of(tid), l16 = lane % 16, g = lane / 16;
     const int nseg = (d.nc + d.seg - 1) / d.seg;
-    int id = blockIdx.x;
+    int id = (int)block_in_stretch();
     const int split = id % a.plan.splits;
     id /= a.plan.splits;
     const int grp = id % d.G;
