@@ -47,7 +47,6 @@ struct Scan {
     int64_t B, L;
     int H, P, G, N;
 };
-constexpr int kMaxStateColumns = 128;  // largest N of the chunked scan
 
 int scan_chunk(bool bf16);
 // Floats of the forward's workspace and of the backward's.

