@@ -126,10 +126,10 @@ __global__ __launch_bounds__(kThreads) void scan_states_kernel(StateArgs a, cons
 // enters each chunk after the segment's first, from zero at the segment's start, in the
 // inputs' type (it is used as a matrix operand, rounded anyway), the factor that a state at
 // the segment's start has there, and the state behind the segment in float32 with the
-// segment's decay.  HW heads (or
-// slabs of them) at once share the chunk's Y and stay in registers over the segment.  WHOLE: P
-// and N are in whole vectors.  Bound by the chain of chunks and its vector instructions (the
-// three terms): ragged prompts 4 x 4096 bfloat16, 32 heads, P = 64, N = 128: 52 us.
+// segment's decay.  HW heads (or slabs of them) at once share the chunk's Y and stay in
+// registers over the segment.  WHOLE: P and N are in whole vectors.  Bound by the chain of
+// chunks and its vector instructions (the three terms): ragged prompts 4 x 4096 bfloat16, 32
+// heads, P = 64, N = 128: 52 us.
 template <typename T, int NP, bool WHOLE, int HW>
 __global__ __launch_bounds__(kThreads, 2) void scan_segments_kernel(StateArgs a, const T *__restrict__ X,
                                                                  const T *__restrict__ Y, T *__restrict__ before,
