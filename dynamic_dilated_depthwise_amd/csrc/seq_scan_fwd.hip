@@ -75,11 +75,13 @@ struct OutArgs {
 // (transposed: rows i, columns t); each head scales it by its decays, which makes it the
 // operand that x is multiplied by.  A wave has rows t of strips w and 7 - w (bfloat16), so
 // that the four waves have the same share of the triangle i <= t and each operand from LDS
-// serves two strips.  The scaled C . B and the entering state are rounded to bfloat16 once, as
-// the operands of matrix products whose sums are float32; y is rounded to bfloat16 at the end
-// by as much, which is also why s alone (without its low part) is enough there.  Bound by memory
+// serves two strips.  The scaled C . B is rounded to bfloat16 once, as the operand of matrix
+// products whose sums are float32, and y at the end by as much, which is also why s alone (without
+// its low part) is enough there.  The entering state has two bfloat16 terms: rounded to one it made
+// the error of y 1.4 times its own rounding's where it dominates (two cost 1.5 us of 48, 7 of 65 for
+// ragged prompts); what a segment adds to it has one.  Bound by memory
 // and vector instructions together: 2 x 8192 tokens bfloat16, 32 heads, P = N = 64: 48 us, 4.2 TB/s
-// with the states; ragged prompts 4 x 4096, N = 128: 65 us; 65536 tokens float32, 2 heads, N = 64:
+// with the states; ragged prompts 4 x 4096, N = 128: 72 us; 65536 tokens float32, 2 heads, N = 64:
 // 44 us, half the rate of its matrix instructions.
 template <typename T, int NP, bool WHOLE, bool SEG>
 __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const T *__restrict__ X,
@@ -88,10 +90,10 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
     constexpr int QS = kStrips<T>, Q = 16 * QS, SPW = QS / 4;
     constexpr int LDN = ld_of<T>(NP), LDP = ld_of<T>(kSlab);
     constexpr bool TWO = SEG && Elem<T>::is_bf16;  // two parts of h0, rounded one by one, take a tile each
-    constexpr int kTiles = Q * LDP + (TWO ? 2 : 1) * kSlab * LDN;
+    constexpr int kTerm = kSlab * LDN, kTiles = Q * LDP + (Elem<T>::is_bf16 ? 2 : 1) * kTerm + (TWO ? kTerm : 0);
     __shared__ __align__(16) T lds[kTiles > Q * LDN ? kTiles : Q * LDN];
     __shared__ __align__(16) float shi[Q], slo[Q], dts[Q];
-    T *xtile = lds, *htile = lds + Q * LDP, *btile = htile + kSlab * LDN;
+    T *xtile = lds, *htile = lds + Q * LDP, *btile = htile + 2 * kTerm;  // of the state two terms in bfloat16
     const ScanDims &d = a.d;
     const int tid = threadIdx.x, lane = tid % kWave, wave = wave_of(tid), l16 = lane % 16, g = lane / 16;
     int id = (int)block_in_stretch();
@@ -179,7 +181,13 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
                 if (has_h) v = __builtin_bit_cast(f32x4, hf.get(k, d.P - p0, cols, tid));
                 if constexpr (SEG && !TWO)
                     if (has_b) v = v * carry + __builtin_bit_cast(f32x4, bt.get(k, d.P - p0, bcols, tid));
-                store4<T>(htile + hf.row_of(k, tid) * LDN + hf.col_of(k, tid), v, 4);
+                T *to = htile + hf.row_of(k, tid) * LDN + hf.col_of(k, tid);
+                store4<T>(to, v, 4);
+                if constexpr (Elem<T>::is_bf16) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] -= (float)(__bf16)v[e];
+                    store4<T>(to + kTerm, v, 4);
+                }
             }
         }
         if constexpr (TWO)
@@ -218,7 +226,10 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
             for (int p = 0; p < 4; ++p) acc[j][p] *= f;
         };
         if (has_h || has_b) {
-            if (has_h || !TWO) add_tile(htile);
+            if (has_h || !TWO) {
+                add_tile(htile);
+                if constexpr (Elem<T>::is_bf16) add_tile(htile + kTerm);
+            }
             if constexpr (TWO) {
                 if (has_b) {
 #pragma unroll
