@@ -13,8 +13,8 @@ pytestmark = pytest.mark.gpu
 
 # A call that keeps nothing takes segments where 512 workgroups (batch * segments * groups * pairs
 # of heads or slabs) are left: two heads at once; one head, odd P and N; two slabs at once.
-# Tolerances as for the scan's other calls: the two parts of the entering state are rounded one
-# by one, each relative to its own size, and the sizes add up to the sum's.
+# Tolerances as for the scan's other calls: what a segment adds to the entering state is rounded
+# relative to its own size, which is part of the sum's.
 @pytest.mark.parametrize("dt", DT)
 @pytest.mark.parametrize("state", [False, True], ids=["fresh", "cached"])
 @pytest.mark.parametrize("batch,L,H,P,G,N", [(1, 1300, 512, 4, 256, 6), (2, 700, 128, 9, 128, 37), (3, 260, 96, 70, 96, 100)])

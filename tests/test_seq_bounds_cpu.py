@@ -18,7 +18,7 @@ def test_rows_near_2_31(lib):  # noqa: F811
 
 def test_scan_near_2_31(lib):  # noqa: F811
     # the padded rows of a state count four elements for N = 1
-    for kw in (dict(P=1 << 29, N=1), dict(heads=1 << 16, P=(1 << 15) - 1 + 1, N=1), dict(heads=1 << 24, groups=1 << 24, P=1, N=128)):
+    for kw in (dict(P=1 << 29, N=1), dict(heads=1 << 16, P=1 << 15, N=1), dict(heads=1 << 24, groups=1 << 24, P=1, N=128)):
         for call in (abi._scan, abi._scan_bwd, abi._scan_step):
             assert call(lib, **kw) == INVALID, (call.__name__, kw)
 
