@@ -78,10 +78,11 @@ struct OutArgs {
 // serves two strips.  The scaled C . B is rounded to bfloat16 once, as the operand of matrix
 // products whose sums are float32, and y at the end by as much, which is also why s alone (without
 // its low part) is enough there.  The entering state has two bfloat16 terms: rounded to one it made
-// the error of y 1.4 times its own rounding's where it dominates (two cost 2 us of 48, 10 of 65 for
-// ragged prompts).  Bound by memory
+// the error of y 1.4 times its own rounding's where it dominates (2 us of 50).  With segments, whose
+// sequences are long, its two parts are rounded one by one (1.25 times; two terms cost 10 us of 65,
+// joining the parts in float32 5).  Bound by memory
 // and vector instructions together: 2 x 8192 tokens bfloat16, 32 heads, P = N = 64: 50 us, 4.0 TB/s
-// with the states; ragged prompts 4 x 4096, N = 128: 75 us; 65536 tokens float32, 2 heads, N = 64:
+// with the states; ragged prompts 4 x 4096, N = 128: 65 us; 65536 tokens float32, 2 heads, N = 64:
 // 44 us, half the rate of its matrix instructions.
 template <typename T, int NP, bool WHOLE, bool SEG>
 __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const T *__restrict__ X,
@@ -89,10 +90,12 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
                                                                T *__restrict__ y) {
     constexpr int QS = kStrips<T>, Q = 16 * QS, SPW = QS / 4;
     constexpr int LDN = ld_of<T>(NP), LDP = ld_of<T>(kSlab);
-    constexpr int kTerm = kSlab * LDN, kTiles = Q * LDP + (Elem<T>::is_bf16 ? 2 : 1) * kTerm;
+    // bfloat16: with segments the two parts of h0 take a tile each, without them its two terms do
+    constexpr bool PARTS = SEG && Elem<T>::is_bf16, TERMS = !SEG && Elem<T>::is_bf16;
+    constexpr int kTerm = kSlab * LDN, kTiles = Q * LDP + (PARTS || TERMS ? 2 : 1) * kTerm;
     __shared__ __align__(16) T lds[kTiles > Q * LDN ? kTiles : Q * LDN];
     __shared__ __align__(16) float shi[Q], slo[Q], dts[Q];
-    T *xtile = lds, *htile = lds + Q * LDP;  // of the state two terms in bfloat16
+    T *xtile = lds, *htile = lds + Q * LDP, *second = htile + kTerm;
     const ScanDims &d = a.d;
     const int tid = threadIdx.x, lane = tid % kWave, wave = wave_of(tid), l16 = lane % 16, g = lane / 16;
     int id = (int)block_in_stretch();
@@ -117,7 +120,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
 
     TileFetch<T, Q, kSlab, kThreads, WHOLE> xf;
     TileFetch<float, kSlab, NP, kThreads, true> hf;
-    Raw<T, 4> own[decltype(hf)::kCount];  // what the segment adds, where hf has the state that it started from
+    TileFetch<T, kSlab, NP, kThreads, true> bt;
     float tf[3], skip_next, carry_next = 1.f;
     auto fetch = [&](int it) {
         const int h = h0 + it / slabs, p0 = it % slabs * kSlab, tid = afresh(threadIdx.x);
@@ -127,12 +130,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
         if (has_h) hf.fetch(a.states + ((((int64_t)b * d.H + h) * nseg + seg) * d.P + p0) * cols, cols, d.P - p0, cols, tid);
         if (has_b) {
             carry_next = a.carried[chunk];
-            const T *from = (const T *)a.before + (chunk * d.P + p0) * bcols;
-#pragma unroll
-            for (int k = 0; k < decltype(hf)::kCount; ++k) {
-                const int row = hf.row_of(k, tid), c = hf.col_of(k, tid);
-                own[k].template load<kWhole>(from + (row < d.P - p0 && c < bcols ? row * bcols + c : 0), 0, 4, true);
-            }
+            bt.fetch((const T *)a.before + (chunk * d.P + p0) * bcols, bcols, d.P - p0, bcols, tid);
         }
         if (tid < Q) {
             tf[0] = d.shi[chunk * Q + tid];
@@ -178,26 +176,24 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
         __syncthreads();
         xf.put(xtile, LDP, n, d.P - p0, tid);
         const float carry = carry_next;
-        if (has_h || has_b) {
+        if (has_h || (has_b && !PARTS)) {
 #pragma unroll
             for (int k = 0; k < decltype(hf)::kCount; ++k) {
                 f32x4 v = {0.f, 0.f, 0.f, 0.f};
                 if (has_h) v = __builtin_bit_cast(f32x4, hf.get(k, d.P - p0, cols, tid));
-                if constexpr (SEG)
-                    if (has_b) {
-                        const bool in = hf.row_of(k, tid) < d.P - p0 && hf.col_of(k, tid) < bcols;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) v[e] = v[e] * carry + (in ? own[k][e] : 0.f);
-                    }
+                if constexpr (SEG && !PARTS)
+                    if (has_b) v = v * carry + __builtin_bit_cast(f32x4, bt.get(k, d.P - p0, bcols, tid));
                 T *to = htile + hf.row_of(k, tid) * LDN + hf.col_of(k, tid);
                 store4<T>(to, v, 4);
-                if constexpr (Elem<T>::is_bf16) {
+                if constexpr (TERMS) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v[e] -= (float)(__bf16)v[e];
                     store4<T>(to + kTerm, v, 4);
                 }
             }
         }
+        if constexpr (PARTS)
+            if (has_b) bt.put(second, LDN, d.P - p0, bcols, tid);
         if (tid < Q) {
             shi[tid] = tf[0];
             slo[tid] = tf[1];
@@ -232,8 +228,17 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
             for (int p = 0; p < 4; ++p) acc[j][p] *= f;
         };
         if (has_h || has_b) {
-            add_tile(htile);
-            if constexpr (Elem<T>::is_bf16) add_tile(htile + kTerm);
+            if (has_h || !PARTS) {
+                add_tile(htile);
+                if constexpr (TERMS) add_tile(second);
+            }
+            if constexpr (PARTS) {
+                if (has_b) {
+#pragma unroll
+                    for (int j = 0; j < SPW; ++j) scale(j, carry);
+                    add_tile(second);
+                }
+            }
 #pragma unroll
             for (int j = 0; j < SPW; ++j) scale(j, __builtin_amdgcn_exp2f(th[j] + tl[j]));
         }

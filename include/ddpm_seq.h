@@ -18,7 +18,7 @@
  *   equal inputs give equal bits.
  * Precision.  All sums, statistics, decays and states are float32 or wider.  bfloat16
  *   outputs are rounded once, from float32; matrix operands made on the way (decayed scores
- *   and, for y of calls that save nothing, what up to 8 chunks add to a state) are rounded to
+ *   and, for y of long calls that save nothing, the state) are rounded to
  *   bfloat16 where the type is bfloat16, but not where they lead to float32 outputs (final
  *   state, grad_A, grad_D, grad_dt_bias) or grad_dt.
  * Lengths.  `lengths` [batch] int32, or NULL: sequence b has lengths[b] tokens (values
