@@ -75,13 +75,13 @@ struct OutArgs {
 // (transposed: rows i, columns t); each head scales it by its decays, which makes it the
 // operand that x is multiplied by.  A wave has rows t of strips w and 7 - w (bfloat16), so
 // that the four waves have the same share of the triangle i <= t and each operand from LDS
-// serves two strips.  The scaled C . B is rounded to bfloat16 once, as the operand of matrix
-// products whose sums are float32, and y at the end by as much, which is also why s alone (without
-// its low part) is enough there.  The entering state has two bfloat16 terms: rounded to one it made
-// the error of y 1.4 times its own rounding's where it dominates (2 us of 50).  With segments, whose
-// sequences are long, its two parts are rounded one by one (1.25 times; two terms cost 10 us of 65,
+// serves two strips.  The scaled C . B enters the product as two bfloat16 terms (rounded to one it
+// made the error of y up to 1.35 times its own rounding's; 6 us of 56), and so does the entering
+// state (1.4 times where it dominates; 2 us).  y is rounded once, at the end, which is also why s
+// alone (without its low part) is enough there.  With segments, whose
+// sequences are long, the state's two parts are rounded one by one (1.25 times; two terms cost 10 us of 65,
 // joining the parts in float32 5).  Bound by memory
-// and vector instructions together: 2 x 8192 tokens bfloat16, 32 heads, P = N = 64: 50 us, 4.0 TB/s
+// and vector instructions together: 2 x 8192 tokens bfloat16, 32 heads, P = N = 64: 56 us, 3.6 TB/s
 // with the states; ragged prompts 4 x 4096, N = 128: 65 us; 65536 tokens float32, 2 heads, N = 64:
 // 44 us, half the rate of its matrix instructions.
 template <typename T, int NP, bool WHOLE, bool SEG>
@@ -272,9 +272,10 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
 #pragma unroll
                     for (int v = 0; v < 4; ++v) m[u][v] = cb[j][is][v] * (__builtin_amdgcn_exp2f(dif[v]) * id4[v]);
                 }
-                const Frag<T> mf = pack_frag<T>(m[0], m[1]);
+                Frag<T> ml;
+                const Frag<T> mf = pack_frag2<T>(m[0], m[1], ml);
 #pragma unroll
-                for (int p = 0; p < 4; ++p) acc[j][p] = mma(xr[p], mf, acc[j][p]);
+                for (int p = 0; p < 4; ++p) acc[j][p] = mma2(xr[p], mf, ml, acc[j][p]);
             }
         }
 #pragma unroll
