@@ -16,7 +16,7 @@
 //   outputs  y of every chunk
 // A call that keeps nothing for a backward moves fewer states: `segments` in the place of
 // `states` runs the recurrence itself over a few chunks and writes what enters each of them
-// from the segment's own tokens in the inputs' type; `pass` then goes over segments only, and
+// from the segment's own tokens, in float32 as all states; `pass` then goes over segments only, and
 // `outputs` adds the two parts of h0.
 // The backward runs the same states and pass kernels over the chunks in reverse for the
 // gradient that enters each chunk's end (with grad and C in the place of x and B) and one
@@ -51,9 +51,6 @@ struct ScanDims {
 // Rows of N of the states in the workspaces start at multiples of four: [P, state_cols(N)],
 // zeros behind N.
 __host__ __device__ constexpr int state_cols(int N) { return (N + 3) / 4 * 4; }
-// The same for the running states of segments, in T: whole vectors.
-template <typename T>
-__host__ __device__ constexpr int before_cols(int N) { return (N + kVec<T> - 1) / kVec<T> * kVec<T>; }
 
 struct ChunkPlan {
     int per, splits;  // heads of a workgroup; workgroups that share a chunk and a group
@@ -90,7 +87,7 @@ inline int64_t pad64(int64_t n) { return (n + 63) / 64 * 64; }
 
 // Segments of a call that keeps nothing: the longest, up to 8 chunks, and the most heads at
 // once, up to 2, that leave 512 workgroups.  seg = 1: none, every chunk has its state.  With segments and without: ragged
-// prompts 4 x 4096 bfloat16, 32 heads, P = 64, N = 128: 123 and 157 us; 65536 tokens float32, 2
+// prompts 4 x 4096 bfloat16, 32 heads, P = 64, N = 128: 155 and 168 us; 65536 tokens float32, 2
 // heads, P = N = 64: 75 and 78 us.
 struct SegmentPlan {
     int seg, hw;
@@ -103,11 +100,12 @@ inline SegmentPlan plan_segments(int64_t B, int64_t nc, int H, int P, int G) {
     return {1, 1};
 }
 
-// Sections of the forward's workspace, which the backward reads again.  With segments
-// `states` has one state a segment, `decays` their decays, and `carried` and `before` follow.
+// Sections of the forward's workspace, which the backward reads again.  With segments the
+// state of a segment's first chunk is what enters the segment, those of the others what its own
+// tokens add to that, and `carried` and `decays`, the segments' decays, follow.
 struct ScanWork {
     int nc, seg, hw;
-    int64_t times, dt, shi, slo, decay, states, carried, decays, before, total;
+    int64_t times, dt, shi, slo, decay, states, carried, decays, total;
 };
 inline ScanWork scan_work(int64_t B, int64_t L, int H, int P, int G, int N, bool bf16, bool save) {
     const int Q = 16 * (bf16 ? kStrips<bf16_t> : kStrips<float>);
@@ -123,10 +121,9 @@ inline ScanWork scan_work(int64_t B, int64_t L, int H, int P, int G, int N, bool
     w.slo = 2 * w.times;
     w.decay = 3 * w.times;
     w.states = w.decay + pad64(B * H * w.nc);
-    w.carried = w.states + pad64(B * H * nseg * state);
+    w.carried = w.states + pad64(B * H * w.nc * state);
     w.decays = w.carried + (p.seg > 1 ? pad64(B * H * w.nc) : 0);
-    w.before = w.decays + (p.seg > 1 ? pad64(B * H * nseg) : 0);
-    w.total = w.before + (p.seg > 1 ? pad64(B * H * w.nc * P * (bf16 ? before_cols<bf16_t>(N) / 2 : before_cols<float>(N))) : 0);
+    w.total = w.decays + (p.seg > 1 ? pad64(B * H * nseg) : 0);
     return w;
 }
 
@@ -137,8 +134,8 @@ hipError_t launch_scan_states(const ScanDims &d, const T *X, int64_t x_batch, in
 // The running states of segments (d.seg chunks, hw heads at once).
 template <typename T>
 hipError_t launch_scan_segments(const ScanDims &d, int hw, const T *X, int64_t x_batch, int64_t x_token, const T *Y,
-                                int64_t y_batch, int64_t y_token, T *before, float *carried, float *ends,
-                                float *decays, hipStream_t stream);
+                                int64_t y_batch, int64_t y_token, float *states, float *carried, float *decays,
+                                hipStream_t stream);
 // The recurrence over the chunks (or segments), in place; first / final [B, H, P, N] or null.
 hipError_t launch_scan_pass(const ScanDims &d, float *states, const float *decays, const float *first, float *final_state,
                             int Q, bool reverse, hipStream_t stream);

@@ -64,9 +64,9 @@ struct OutArgs {
     ScanDims d;
     ChunkPlan plan;
     int64_t x_batch, x_token, b_batch, b_token, c_batch, c_token;
-    const float *states;   // [B, H, nc, P, cols]: the state that enters each chunk, or each segment
-    const float *carried;  // [B, H, nc]: the factor of that state at a chunk of the segment
-    const void *before;    // [B, H, nc, P, before_cols]: what the segment's own tokens add to it there
+    const float *states;   // [B, H, nc, P, cols]: the state that enters each chunk; with segments that of a
+                           // segment at its first, and at the others what the segment's own tokens add to it there
+    const float *carried;  // [B, H, nc]: the factor of the segment's state at a chunk of it
     int has_first;         // an initial state
     const float *D;
 };
@@ -77,12 +77,10 @@ struct OutArgs {
 // that the four waves have the same share of the triangle i <= t and each operand from LDS
 // serves two strips.  The scaled C . B enters the product as two bfloat16 terms (rounded to one it
 // made the error of y up to 1.35 times its own rounding's; 6 us of 56), and so does the entering
-// state (1.4 times where it dominates; 2 us).  y is rounded once, at the end, which is also why s
-// alone (without its low part) is enough there.  With segments, whose
-// sequences are long, the state's two parts are rounded one by one (1.25 times; two terms cost 10 us of 65,
-// joining the parts in float32 5).  Bound by memory
-// and vector instructions together: 2 x 8192 tokens bfloat16, 32 heads, P = N = 64: 56 us, 3.6 TB/s
-// with the states; ragged prompts 4 x 4096, N = 128: 65 us; 65536 tokens float32, 2 heads, N = 64:
+// state (1.4 times where it dominates; 2 us), whose two parts with segments are joined in float32.
+// y is rounded once, at the end, which is also why s alone (without its low part) is enough there.
+// Bound by memory and vector instructions together: 2 x 8192 tokens bfloat16, 32 heads, P = N = 64:
+// 56 us, 3.6 TB/s with the states; ragged prompts 4 x 4096, N = 128: 85 us; 65536 tokens float32, 2 heads, N = 64:
 // 44 us, half the rate of its matrix instructions.
 template <typename T, int NP, bool WHOLE, bool SEG>
 __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const T *__restrict__ X,
@@ -90,12 +88,11 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
                                                                T *__restrict__ y) {
     constexpr int QS = kStrips<T>, Q = 16 * QS, SPW = QS / 4;
     constexpr int LDN = ld_of<T>(NP), LDP = ld_of<T>(kSlab);
-    // bfloat16: with segments the two parts of h0 take a tile each, without them its two terms do
-    constexpr bool PARTS = SEG && Elem<T>::is_bf16, TERMS = !SEG && Elem<T>::is_bf16;
-    constexpr int kTerm = kSlab * LDN, kTiles = Q * LDP + (PARTS || TERMS ? 2 : 1) * kTerm;
+    constexpr bool TERMS = Elem<T>::is_bf16;  // the entering state's two
+    constexpr int kTerm = kSlab * LDN, kTiles = Q * LDP + (TERMS ? 2 : 1) * kTerm;
     __shared__ __align__(16) T lds[kTiles > Q * LDN ? kTiles : Q * LDN];
     __shared__ __align__(16) float shi[Q], slo[Q], dts[Q];
-    T *xtile = lds, *htile = lds + Q * LDP, *second = htile + kTerm;
+    T *xtile = lds, *htile = lds + Q * LDP;
     const ScanDims &d = a.d;
     const int tid = threadIdx.x, lane = tid % kWave, wave = wave_of(tid), l16 = lane % 16, g = lane / 16;
     int id = (int)block_in_stretch();
@@ -109,10 +106,10 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
     n = n < 0 ? 0 : n > Q ? Q : n;
     const int hg = d.H / d.G, h0 = grp * hg + split * a.plan.per;
     const int h1 = h0 + a.plan.per < (grp + 1) * hg ? h0 + a.plan.per : (grp + 1) * hg;
-    const int slabs = (d.P + kSlab - 1) / kSlab, items = (h1 - h0) * slabs, cols = state_cols(d.N), bcols = before_cols<T>(d.N);
+    const int slabs = (d.P + kSlab - 1) / kSlab, items = (h1 - h0) * slabs, cols = state_cols(d.N);
     const T *xb = X + b * a.x_batch + (int64_t)c * Q * a.x_token;
-    const int seg = SEG ? c / d.seg : c, nseg = SEG ? (d.nc + d.seg - 1) / d.seg : d.nc;
-    const bool has_h = n > 0 && (seg > 0 || a.has_first), has_b = SEG && n > 0 && c % d.seg > 0;
+    const int first = SEG ? c / d.seg * d.seg : c;  // the chunk whose place has the entering state, or the segment's
+    const bool has_h = n > 0 && (first > 0 || a.has_first), has_b = SEG && n > 0 && c > first;
     int strip[SPW];
     const int below = l16 - 4 * g;  // on the diagonal tile, row v of this lane is column t's token at v == below
 #pragma unroll
@@ -120,17 +117,17 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
 
     TileFetch<T, Q, kSlab, kThreads, WHOLE> xf;
     TileFetch<float, kSlab, NP, kThreads, true> hf;
-    TileFetch<T, kSlab, NP, kThreads, true> bt;
+    TileFetch<float, kSlab, NP, kThreads, true> bf;
     float tf[3], skip_next, carry_next = 1.f;
     auto fetch = [&](int it) {
         const int h = h0 + it / slabs, p0 = it % slabs * kSlab, tid = afresh(threadIdx.x);
         skip_next = a.D[h];
         xf.fetch(xb + (int64_t)h * d.P + p0, a.x_token, n, d.P - p0, tid);
         const int64_t chunk = ((int64_t)b * d.H + h) * d.nc + c;
-        if (has_h) hf.fetch(a.states + ((((int64_t)b * d.H + h) * nseg + seg) * d.P + p0) * cols, cols, d.P - p0, cols, tid);
+        if (has_h) hf.fetch(a.states + ((chunk - c + first) * d.P + p0) * cols, cols, d.P - p0, cols, tid);
         if (has_b) {
             carry_next = a.carried[chunk];
-            bt.fetch((const T *)a.before + (chunk * d.P + p0) * bcols, bcols, d.P - p0, bcols, tid);
+            bf.fetch(a.states + (chunk * d.P + p0) * cols, cols, d.P - p0, cols, tid);
         }
         if (tid < Q) {
             tf[0] = d.shi[chunk * Q + tid];
@@ -176,13 +173,15 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
         __syncthreads();
         xf.put(xtile, LDP, n, d.P - p0, tid);
         const float carry = carry_next;
-        if (has_h || (has_b && !PARTS)) {
+        if (has_h || has_b) {
 #pragma unroll
             for (int k = 0; k < decltype(hf)::kCount; ++k) {
                 f32x4 v = {0.f, 0.f, 0.f, 0.f};
-                if (has_h) v = __builtin_bit_cast(f32x4, hf.get(k, d.P - p0, cols, tid));
-                if constexpr (SEG && !PARTS)
-                    if (has_b) v = v * carry + __builtin_bit_cast(f32x4, bt.get(k, d.P - p0, bcols, tid));
+                if (has_h) v = __builtin_bit_cast(f32x4, hf.r[k]);
+                if constexpr (SEG)
+                    if (has_b) v = v * carry + __builtin_bit_cast(f32x4, bf.r[k]);
+                // zeros past the tensor, once for both parts
+                if (hf.row_of(k, tid) >= d.P - p0 || hf.col_of(k, tid) >= cols) v = f32x4{0.f, 0.f, 0.f, 0.f};
                 T *to = htile + hf.row_of(k, tid) * LDN + hf.col_of(k, tid);
                 store4<T>(to, v, 4);
                 if constexpr (TERMS) {
@@ -192,8 +191,6 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
                 }
             }
         }
-        if constexpr (PARTS)
-            if (has_b) bt.put(second, LDN, d.P - p0, bcols, tid);
         if (tid < Q) {
             shi[tid] = tf[0];
             slo[tid] = tf[1];
@@ -223,24 +220,15 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
                     for (int j = 0; j < SPW; ++j) acc[j][p] = mma(hr, cf[j][k], acc[j][p]);
                 }
         };
-        auto scale = [&](int j, float f) {
-#pragma unroll
-            for (int p = 0; p < 4; ++p) acc[j][p] *= f;
-        };
         if (has_h || has_b) {
-            if (has_h || !PARTS) {
-                add_tile(htile);
-                if constexpr (TERMS) add_tile(second);
-            }
-            if constexpr (PARTS) {
-                if (has_b) {
+            add_tile(htile);
+            if constexpr (TERMS) add_tile(htile + kTerm);
 #pragma unroll
-                    for (int j = 0; j < SPW; ++j) scale(j, carry);
-                    add_tile(second);
-                }
-            }
+            for (int j = 0; j < SPW; ++j) {
+                const float f = __builtin_amdgcn_exp2f(th[j] + tl[j]);
 #pragma unroll
-            for (int j = 0; j < SPW; ++j) scale(j, __builtin_amdgcn_exp2f(th[j] + tl[j]));
+                for (int p = 0; p < 4; ++p) acc[j][p] *= f;
+            }
         }
 #pragma unroll
         for (int i = 0; i < QS / 2; ++i) {
@@ -374,11 +362,10 @@ hipError_t scan_fwd(const Scan &a, float *work, void *y, float *final_state, boo
                        a.dt_token, a.A, a.dt_bias, blocks_h);
     hipError_t e = hipGetLastError();
     float *states = work + w.states;
-    T *before = (T *)(work + w.before);
     if (e == hipSuccess && (w.nc > 1 || a.initial != nullptr || final_state != nullptr || save)) {
         if (w.seg > 1)
             e = launch_scan_segments<T>(d, w.hw, (const T *)a.x, a.x_batch, a.x_token, (const T *)a.Bm, a.b_batch,
-                                        a.b_token, before, work + w.carried, states, work + w.decays, stream);
+                                        a.b_token, states, work + w.carried, work + w.decays, stream);
         else
             e = launch_scan_states<T>(d, (const T *)a.x, a.x_batch, a.x_token, (const T *)a.Bm, a.b_batch, a.b_token,
                                       states, false, stream);
@@ -386,7 +373,7 @@ hipError_t scan_fwd(const Scan &a, float *work, void *y, float *final_state, boo
     }
     if (e != hipSuccess) return e;
     const OutArgs o = {d, plan, a.x_batch, a.x_token, a.b_batch, a.b_token, a.c_batch, a.c_token, states,
-                       work + w.carried, before, a.initial != nullptr, a.D};
+                       work + w.carried, a.initial != nullptr, a.D};
 #define X_(NP, WHOLE)                                                                                              \
     if (w.seg > 1)                                                                                                 \
         hipLaunchKernelGGL((scan_out_kernel<T, NP, WHOLE, true>), dim3((unsigned)bo), dim3(kThreads), 0, stream,   \

@@ -123,17 +123,16 @@ __global__ __launch_bounds__(kThreads) void scan_states_kernel(StateArgs a, cons
 }
 
 // The same for a segment of d.seg chunks, for calls that keep nothing: the running state that
-// enters each chunk after the segment's first, from zero at the segment's start, in the
-// inputs' type (it is used as a matrix operand, rounded anyway), the factor that a state at
-// the segment's start has there, and the state behind the segment in float32 with the
-// segment's decay.  HW heads (or slabs of them) at once share the chunk's Y and stay in
-// registers over the segment.  WHOLE: P and N are in whole vectors.  Bound by the chain of
-// chunks and its vector instructions (the three terms): ragged prompts 4 x 4096 bfloat16, 32
-// heads, P = 64, N = 128: 52 us.
+// enters each chunk after the segment's first, from zero at the segment's start, the factor that a
+// state at the segment's start has there, and in the place of the first chunk the state behind the
+// segment, with the segment's decay.  HW heads (or slabs of them) at once share the chunk's Y and
+// stay in registers over the segment.  WHOLE: P and N are in whole vectors.  Bound by the chain of
+// chunks, its vector instructions (the three terms) and memory: ragged prompts 4 x 4096 bfloat16,
+// 32 heads, P = 64, N = 128: 54 us.
 template <typename T, int NP, bool WHOLE, int HW>
 __global__ __launch_bounds__(kThreads, 2) void scan_segments_kernel(StateArgs a, const T *__restrict__ X,
-                                                                 const T *__restrict__ Y, T *__restrict__ before,
-                                                                 float *__restrict__ carried, float *__restrict__ ends,
+                                                                 const T *__restrict__ Y, float *__restrict__ out,
+                                                                 float *__restrict__ carried,
                                                                  float *__restrict__ decays) {
     constexpr int Q = 16 * kStrips<T>, LDN = NP + kVec<T>, LDP = kSlab + kVec<T>;
     __shared__ __align__(16) T ytile[Q * LDN];
@@ -171,6 +170,12 @@ __global__ __launch_bounds__(kThreads, 2) void scan_segments_kernel(StateArgs a,
     };
     f32x4 acc[HW][NP / 16];
     float factor[HW];
+    auto put = [&](int i, int c, int row) {
+        float *o = out + ((head(i) * d.nc + c) * d.P + row) * cols;
+#pragma unroll
+        for (int k = 0; k < NP / 16; ++k)
+            if (16 * k + 4 * g < cols) *(f32x4 *)(o + 16 * k + 4 * g) = acc[i][k];
+    };
 #pragma unroll
     for (int i = 0; i < HW; ++i) {
         factor[i] = 1.f;
@@ -194,12 +199,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_segments_kernel(StateArgs a,
             if (i == 0 && c + 1 < c1) fetch_y(c + 1);
             if (i + 1 < HW) fetch(c, i + 1);
             else if (c + 1 < c1) fetch(c + 1, 0);
-            if (c > c0 && mine) {
-                T *o = before + ((head(i) * d.nc + c) * d.P + row) * before_cols<T>(d.N);
-#pragma unroll
-                for (int k = 0; k < NP / 16; ++k)
-                    if (16 * k + 4 * g < before_cols<T>(d.N)) store4<T>(o + 16 * k + 4 * g, acc[i][k], 4);
-            }
+            if (c > c0 && mine) put(i, c, row);
             if (tid == 0 && p0 == 0 && mine) carried[head(i) * d.nc + c] = factor[i];
             factor[i] *= a_c;
 #pragma unroll
@@ -212,15 +212,12 @@ __global__ __launch_bounds__(kThreads, 2) void scan_segments_kernel(StateArgs a,
         const int row = item(i) % slabs * kSlab + p + l16;
         if (split * HW + i >= all || row >= d.P) continue;
         if (row == 0) decays[head(i) * nseg + seg] = factor[i];
-        float *o = ends + ((head(i) * nseg + seg) * d.P + row) * cols;
-#pragma unroll
-        for (int k = 0; k < NP / 16; ++k)
-            if (16 * k + 4 * g < cols) *(f32x4 *)(o + 16 * k + 4 * g) = acc[i][k];
+        put(i, c0, row);
     }
 }
 
 // h = first; for every chunk in order: part = states[c], states[c] = h, h = decay[c] h + part.
-// `rows` states a head: the chunks, or segments of d.seg of them.
+// `rows` states a head: the chunks, or segments of d.seg of them, whose states lie d.seg apart.
 // LANES of four elements by PARTS runs of states: each run goes from zero, the runs' ends are
 // joined in LDS, and each run goes again from its true start; the parts stay in registers
 // between where a run has at most KEEP of them and are read again otherwise.  PARTS = 1: one
@@ -247,13 +244,13 @@ __global__ __launch_bounds__(PARTS *LANES) void scan_pass_kernel(ScanDims d, int
     // where the caller's unpadded states have these four
     const int64_t user = head * d.P * d.N + (int64_t)(e / per_row) * d.N + e % per_row * 4;
     const int left = on ? d.N - e % per_row * 4 : 0;
-    f32x4 *st = (f32x4 *)(states + head * rows * E) + (on ? e : 0);
+    f32x4 *st = (f32x4 *)(states + head * d.nc * E) + (on ? e : 0);
     const float *decay = decays + head * rows;
-    const int64_t step = reverse ? -E / 4 : E / 4;
+    const int64_t each = E / 4 * d.seg, step = reverse ? -each : each;
     const int dir = reverse ? -1 : 1, c0 = reverse ? nc - 1 - from : from;
     f32x4 keep[KEEP];
     f32x4 h = {0.f, 0.f, 0.f, 0.f};
-    st += c0 * (E / 4);
+    st += c0 * each;
     decay += c0;
     const bool kept = PARTS == 1 || per <= KEEP;
     if (kept) {
@@ -319,15 +316,15 @@ hipError_t launch_scan_states(const ScanDims &d, const T *X, int64_t x_batch, in
 
 template <typename T>
 hipError_t launch_scan_segments(const ScanDims &d, int hw, const T *X, int64_t x_batch, int64_t x_token, const T *Y,
-                                int64_t y_batch, int64_t y_token, T *before, float *carried, float *ends,
-                                float *decays, hipStream_t stream) {
+                                int64_t y_batch, int64_t y_token, float *states, float *carried, float *decays,
+                                hipStream_t stream) {
     const int items = d.H / d.G * ((d.P + kSlab - 1) / kSlab);
     const StateArgs a = {d, {hw, (items + hw - 1) / hw}, x_batch, x_token, y_batch, y_token, 0};
     const int64_t blocks = (int64_t)d.B * ((d.nc + d.seg - 1) / d.seg) * d.G * a.plan.splits;
     if (blocks > 0x7fffffff) return hipErrorInvalidConfiguration;
 #define LAUNCH(NP, WHOLE, HW)                                                                                      \
     hipLaunchKernelGGL((scan_segments_kernel<T, NP, WHOLE, HW>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, \
-                       a, X, Y, before, carried, ends, decays)
+                       a, X, Y, states, carried, decays)
 #define X_(NP, WHOLE)                                                                    \
     if (WHOLE && d.N % kVec<T> == 0) { if (hw == 2) LAUNCH(NP, true, 2); else LAUNCH(NP, true, 1); } \
     else { if (hw == 2) LAUNCH(NP, false, 2); else LAUNCH(NP, false, 1); }
@@ -337,10 +334,9 @@ hipError_t launch_scan_segments(const ScanDims &d, int hw, const T *X, int64_t x
     return hipGetLastError();
 }
 template hipError_t launch_scan_segments<float>(const ScanDims &, int, const float *, int64_t, int64_t, const float *,
-                                                int64_t, int64_t, float *, float *, float *, float *, hipStream_t);
+                                                int64_t, int64_t, float *, float *, float *, hipStream_t);
 template hipError_t launch_scan_segments<bf16_t>(const ScanDims &, int, const bf16_t *, int64_t, int64_t, const bf16_t *,
-                                                 int64_t, int64_t, bf16_t *, float *, float *, float *,
-                                                 hipStream_t);
+                                                 int64_t, int64_t, float *, float *, float *, hipStream_t);
 template hipError_t launch_scan_states<float>(const ScanDims &, const float *, int64_t, int64_t, const float *, int64_t,
                                               int64_t, float *, bool, hipStream_t);
 template hipError_t launch_scan_states<bf16_t>(const ScanDims &, const bf16_t *, int64_t, int64_t, const bf16_t *,

@@ -35,3 +35,16 @@ def test_outputs(batch, L, H, P, G, N, state):
     init = randn(gen_of(12), batch, H, P, N) if state else None
     y, last, _ = seq.selective_scan_fwd(*args, init, return_state=True, save=True)
     close({"y": y, "state": last}, *orc.scan(*args, init))
+
+
+# calls that keep nothing and take segments of chunks (512 workgroups of them)
+@pytest.mark.parametrize("state", [False, True], ids=["fresh", "cached"])
+@pytest.mark.parametrize("batch,L,H,P,G,N", [(1, 300, 512, 8, 256, 24), (1, 1100, 512, 8, 256, 16), (2, 260, 256, 9, 128, 64),
+                                             (1, 300, 256, 72, 256, 37)])
+def test_segments(batch, L, H, P, G, N, state):
+    announce("segments precision", batch, L, H, P, G, N, state)
+    args = case(batch, L, H, P, G, N, BF16)
+    init = randn(gen_of(12), batch, H, P, N) if state else None
+    lengths = ragged(batch, L) if batch > 1 else None
+    y, last, _ = seq.selective_scan_fwd(*args, init, lengths, return_state=True)
+    close({"y": y, "state": last}, *orc.scan(*args, init, lengths))
