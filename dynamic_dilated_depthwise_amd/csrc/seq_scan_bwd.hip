@@ -23,9 +23,8 @@
 // grad_dt = (q / dt + A e) sigmoid(raw + dt_bias) and grad_A = sum_t dt e.  These are sums
 // of many terms of both signs, so every factor keeps float32's precision: Z and CB come
 // from products of the inputs themselves, and h0 and g1 enter as three bfloat16 terms.
-// grad_B and grad_C, sums over heads that may cancel, take the scaled Z and g1 in two terms (17
-// bits) and are rounded to bfloat16 at their end; grad_x, with its large term D grad, takes the
-// scaled CB as an operand rounded to bfloat16 once.
+// grad_x, grad_B and grad_C take the scaled CB, Z and g1 in two terms (17 bits) and are rounded to
+// bfloat16 at their end.
 #include "seq_scan.hpp"
 
 namespace ddpm {
@@ -81,7 +80,7 @@ __device__ __forceinline__ float frag_at(const FragF &f, int e) { return f.v[e];
 // a SIMD with all registers taken; a head costs a wave 1570 vector, 134 matrix and 285 LDS
 // instructions, and those three and the barriers around the tiles add up more than they overlap
 // (vector issue 46 %, LDS 31 %, matrix 16 % of the time): 2 x 8192 tokens bfloat16, 32 heads, P =
-// N = 64: 192 us.  N = 128 takes 570 us: one set of planes, and 130 registers spill.
+// N = 64: 200 us.  N = 128 takes 580 us: one set of planes, and 130 registers spill.
 template <typename T, int NP, bool WHOLE>
 __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, const T *__restrict__ X,
                                                                    const T *__restrict__ Bm, const T *__restrict__ Cm,
@@ -355,13 +354,14 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
                     qdt += nt[u][v] * z[v];
                 }
             }
-            Frag<T> wl;
-            const Frag<T> nf = pack_frag<T>(nt[0], nt[1]), wf = pack_frag2<T>(wt[0], wt[1], wl);
+            Frag<T> nl, wl;
+            const Frag<T> nf = pack_frag2<T>(nt[0], nt[1], nl);
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
                 const Frag<T> f = col_frag(s.g, LDP, 32 * k, 16 * p, l16, g);
-                dx[p] = mma(f, nf, dx[p]);
+                dx[p] = mma2(f, nf, nl, dx[p]);
             }
+            const Frag<T> wf = pack_frag2<T>(wt[0], wt[1], wl);
 #pragma unroll
             for (int m = 0; m < NS; ++m) {
                 const Frag<T> f = col_frag(s.c, LDN, 32 * k, 16 * m, l16, g);

@@ -19,8 +19,7 @@
  * Precision.  All sums, statistics, decays and states are float32 or wider.  bfloat16
  *   outputs are rounded once, from float32; matrix operands made on the way are two bfloat16
  *   terms (17 bits) where the type is bfloat16, and where they lead to float32 outputs (final
- *   state, grad_A, grad_D, grad_dt_bias) or grad_dt three or more.  Rounded to one term are the
- *   decayed scores of grad_x.
+ *   state, grad_A, grad_D, grad_dt_bias) or grad_dt three or more.
  * Lengths.  `lengths` [batch] int32, or NULL: sequence b has lengths[b] tokens (values
  *   outside [0, length] are taken as the nearest).  Later positions are not read; y and the
  *   gradients there are zero and the state is that behind the last token.

@@ -48,3 +48,14 @@ def test_segments(batch, L, H, P, G, N, state):
     lengths = ragged(batch, L) if batch > 1 else None
     y, last, _ = seq.selective_scan_fwd(*args, init, lengths, return_state=True)
     close({"y": y, "state": last}, *orc.scan(*args, init, lengths))
+
+
+@pytest.mark.parametrize("batch,L,H,P,G,N", SIZES)
+def test_gradients(batch, L, H, P, G, N):
+    announce("scan gradients' precision", batch, L, H, P, G, N)
+    args = case(batch, L, H, P, G, N, BF16)
+    g = gen_of(12)
+    grad, init, gs = randn(g, batch, L, H, P, dtype=BF16), randn(g, batch, H, P, N), randn(g, batch, H, P, N)
+    saved = seq.selective_scan_fwd(*args, init, save=True)[2]
+    got = dict(zip(NAMES, seq.selective_scan_bwd(grad, *args, saved, init, None, gs)))
+    close(got, *orc.scan(*args, init, grad=grad, grad_state=gs))
