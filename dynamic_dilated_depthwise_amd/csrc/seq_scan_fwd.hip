@@ -78,7 +78,7 @@ struct OutArgs {
 // serves two strips.  The scaled C . B enters the product as two bfloat16 terms (rounded to one it
 // made the error of y up to 1.35 times its own rounding's; 6 us of 56), and so does the entering
 // state (1.4 times where it dominates; 2 us), whose two parts with segments are joined in float32.
-// y is rounded once, at the end, which is also why s alone (without its low part) is enough there.
+// y is rounded once, at the end.
 // Bound by memory and vector instructions together: 2 x 8192 tokens bfloat16, 32 heads, P = N = 64:
 // 56 us, 3.6 TB/s with the states; ragged prompts 4 x 4096, N = 128: 85 us; 65536 tokens float32, 2 heads, N = 64:
 // 44 us, half the rate of its matrix instructions.
@@ -245,15 +245,11 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
                     const int is = 2 * i + u;
                     m[u] = f32x4{0.f, 0.f, 0.f, 0.f};
                     if (is > strip[j]) continue;
-                    const f32x4 ih = *(const f32x4 *)(shi + 16 * is + 4 * g), id4 = *(const f32x4 *)(dts + 16 * is + 4 * g);
+                    const f32x4 ih = *(const f32x4 *)(shi + 16 * is + 4 * g), il = *(const f32x4 *)(slo + 16 * is + 4 * g);
+                    const f32x4 id4 = *(const f32x4 *)(dts + 16 * is + 4 * g);
                     f32x4 dif;
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) dif[v] = th[j] - ih[v];
-                    if constexpr (!Elem<T>::is_bf16) {
-                        const f32x4 il = *(const f32x4 *)(slo + 16 * is + 4 * g);
-#pragma unroll
-                        for (int v = 0; v < 4; ++v) dif[v] += tl[j] - il[v];
-                    }
+                    for (int v = 0; v < 4; ++v) dif[v] = (th[j] - ih[v]) + (tl[j] - il[v]);
                     if (is == strip[j])
 #pragma unroll
                         for (int v = 0; v < 4; ++v) dif[v] = v <= below ? dif[v] : -INFINITY;

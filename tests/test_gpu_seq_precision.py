@@ -10,7 +10,7 @@ import torch
 
 import seq_oracle as orc
 from dynamic_dilated_depthwise_amd import sequence as seq
-from test_gpu_seq_norm_conv import announce, gen_of, ragged, randn
+from test_gpu_seq_norm_conv import DT, announce, gen_of, ragged, randn
 from test_gpu_seq_scan import NAMES, case
 
 pytestmark = pytest.mark.gpu
@@ -59,3 +59,14 @@ def test_gradients(batch, L, H, P, G, N):
     saved = seq.selective_scan_fwd(*args, init, save=True)[2]
     got = dict(zip(NAMES, seq.selective_scan_bwd(grad, *args, saved, init, None, gs)))
     close(got, *orc.scan(*args, init, grad=grad, grad_state=gs))
+
+
+@pytest.mark.parametrize("dt", DT)
+def test_slow_after_fast(dt):
+    """Small steps that follow many strong ones in a chunk: their decays are differences of large sums."""
+    announce("scan slow after fast", dt)
+    args = list(case(1, 250, 2, 16, 1, 12, DT[dt], fast=True))
+    args[1][:, :60] = 1000.0
+    args[1][:, 60:] = -4.0 - args[6].to(DT[dt])  # dt about 0.02 whatever the bias
+    y, last, _ = seq.selective_scan_fwd(*args, return_state=True)
+    close({"y": y, "state": last}, *orc.scan(*args))
