@@ -86,7 +86,7 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvArgs a, T *__res
         const int64_t k = id - walks;
         const int W1 = a.W - 1;
         if (last == nullptr || k >= (int64_t)a.B * W1 * a.nvec) return;
-        const int c = (int)(k % a.nvec) * V, j = (int)(k / a.nvec) % W1, b = (int)(k / a.nvec / W1);
+        const int c = (int)(k % a.nvec) * V, j = (int)(k / a.nvec % W1), b = (int)(k / a.nvec / W1);  // rows may pass 2^31
         const T *ib = a.initial ? (const T *)a.initial + (int64_t)b * W1 * a.D : nullptr;
         const int n = length_of(a.lengths, b, a.L);
         token<T, V, R>(a, (const T *)a.x + b * a.x_batch, ib, n - W1 + j, n, c)
