@@ -8,6 +8,7 @@
 #include <ATen/ATen.h>
 #include <ATen/hip/EmptyTensor.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/GradMode.h>
 #include <c10/core/StreamGuard.h>
 #include <c10/hip/HIPCachingAllocator.h>
 #include <c10/hip/HIPFunctions.h>
@@ -138,6 +139,16 @@ PyObject *tuple(std::initializer_list<Tensor> ts) {
     Py_ssize_t k = 0;
     for (const Tensor &t : ts) PyTuple_SET_ITEM(r, k++, wrap(t));
     return r;
+}
+
+// A state that a step writes in place, as torch's own in-place forms treat it: not where autograd
+// would have to follow the write, and counted, so that a backward pass that has kept it raises.
+void writable(const Tensor &t, const char *name) {
+    if (t.requires_grad() && c10::GradMode::is_enabled())
+        refuse(name, " requires grad and a step writes it in place; call it under torch.no_grad()");
+}
+void written(const Tensor &t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
 }
 
 void *at_of(const Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; }
@@ -276,11 +287,13 @@ PyObject *causal_conv_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const Tensor &state = tensor(a[3], "state");
     const int64_t S = state.dim() == 3 ? state.size(0) : 0;
     void *st = c.like(a[3], "state", {S, t.W - 1, D});
+    writable(state, "state");
     const void *slots = c.maybe(a[4], "slots", at::kInt, {batch});
     const Tensor y = c.empty({batch, D});
     done("ddpm_causal_conv_step",
          ddpm_causal_conv_step(c.x.data_ptr(), t.weight, t.bias, t.W > 1 ? st : nullptr, (const int32_t *)slots, y.data_ptr(),
                                batch, S, D, (int)t.W, c.x.stride(0), c.dtype, c.stream));
+    written(state);
     return wrap(y);
     END_HANDLE_TH_ERRORS
 }
@@ -377,9 +390,11 @@ PyObject *selective_scan_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const Tensor &state = tensor(a[7], "state");
     const int64_t S = state.dim() == 4 ? state.size(0) : 0;
     float *st = (float *)c.like(a[7], "state", at::kFloat, {S, s.heads, s.P, s.N});
+    writable(state, "state");
     const void *slots = c.maybe(a[8], "slots", at::kInt, {s.batch});
     const Tensor y = c.empty(c.x.sizes());
     done("ddpm_selective_scan_step", ddpm_selective_scan_step(&s, st, (const int32_t *)slots, S, y.data_ptr(), c.stream));
+    written(state);
     return wrap(y);
     END_HANDLE_TH_ERRORS
 }

@@ -18,6 +18,9 @@ Inputs along a sequence may be views whose last axis (scan: all but the first tw
 contiguous, such as the slices of one projection.  lengths and slots are int32 [batch]; see
 the header for what they mean, and for widths (to 8) and state columns (to 128).
 
+The step functions write `state` in place as torch's in-place forms do: a state that requires grad
+is refused in grad mode, and a backward pass that has kept the state raises after the step.
+
 Streams: a call on a given `stream` does not wait for work on the current one that makes its
 arguments; it keeps their memory from reuse until its own work is done.  All calls may be
 captured into a graph.  Before a training step is captured, let go of every eager result that
