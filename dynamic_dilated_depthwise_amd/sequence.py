@@ -7,7 +7,8 @@ in ``include/ddpm_seq.h`` without the prefix: it checks its arguments, allocates
 and the workspace, and enqueues the library's kernels on ``stream`` (the current stream by
 default).  Wrong arguments raise TypeError or ValueError, what the library refuses
 ``DDPMError``.  The functions know nothing of autograd; ``layer_norm``, ``causal_conv`` and
-``selective_scan`` are their differentiable forms.  There is no CPU or PyTorch fallback.
+``selective_scan`` are their differentiable forms (once, in reverse mode; inputs with a
+forward-mode tangent raise).  There is no CPU or PyTorch fallback.
 
 Layouts (float32 or bfloat16 unless stated; ``L`` tokens, ``H`` heads in ``G`` groups):
   x of the norm [..., C], weight and bias [C]
@@ -33,6 +34,7 @@ takes 3 us, the same checks in Python four times that.
 import os
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import raw_library
@@ -108,7 +110,11 @@ def selective_scan_step(x, dt, A, B, C, D, dt_bias, state, slots=None, stream=No
 
 # ------------------------------------------------------------------------------- autograd
 def _differentiated(*ts):
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in ts)
+    """Whether autograd has to see the call.  A tangent counts in any grad mode: the autograd forms
+    have no forward-mode rule and raise, where the plain call would drop it."""
+    ts = [t for t in ts if t is not None]
+    return (torch.is_grad_enabled() and any(t.requires_grad for t in ts) or
+            forward_ad._current_level >= 0 and any(forward_ad.unpack_dual(t).tangent is not None for t in ts))
 
 
 def _rowwise(t, axes):

@@ -1,10 +1,11 @@
-"""The sequence operators beside torch's autograd: states written in place."""
+"""The sequence operators beside torch's autograd: states written in place, forward-mode tangents."""
 import pytest
 import torch
+import torch.autograd.forward_ad as fwAD
 
 from dynamic_dilated_depthwise_amd import sequence as seq
 from dynamic_dilated_depthwise_amd.mixer import PixelMixer
-from test_gpu_seq_norm_conv import announce, conv_case, gen_of, randn
+from test_gpu_seq_norm_conv import announce, conv_case, gen_of, norm_case, randn
 from test_gpu_seq_scan import case
 
 pytestmark = pytest.mark.gpu
@@ -48,3 +49,23 @@ def test_states_that_require_grad():
         plain = state.clone()
         step(plain)
         assert torch.equal(plain, leaf.detach())
+
+
+def test_forward_mode_is_refused():
+    """A tangent is never dropped: the differentiable forms raise for dual inputs."""
+    announce("forward mode")
+    x, w, b, grad = norm_case(6, 40, torch.float32)
+    cx, cw, cb, init, _, _ = conv_case(2, 9, 12, 4, torch.float32)
+    args = case(2, 9, 2, 8, 1, 6, torch.float32)
+    m = PixelMixer(dim=12, heads=2, head_dim=8, state_dim=6).cuda()
+    tokens = randn(gen_of(6), 1, 5, 12)
+    for mode in (torch.enable_grad, torch.no_grad):
+        with mode(), fwAD.dual_level():
+            for call in (lambda: seq.layer_norm(fwAD.make_dual(x, grad), w, b),
+                         lambda: seq.layer_norm(x, fwAD.make_dual(w, b), b),
+                         lambda: seq.causal_conv(cx, cw, cb, fwAD.make_dual(init, init)),
+                         lambda: seq.selective_scan(*args[:6], fwAD.make_dual(args[6], args[6])),
+                         lambda: m.prompt(fwAD.make_dual(tokens, tokens))):
+                with pytest.raises(RuntimeError, match="jvp|forward"):
+                    call()
+            assert seq.layer_norm(x, w, b).shape == x.shape  # no tangent, no refusal

@@ -23,3 +23,15 @@ def test_states_and_sizes():
 def test_host_tensors_are_refused():
     with pytest.raises(ValueError, match="device tensor"):
         PixelMixer()(torch.zeros(1, 64, 4, 4))
+
+
+def test_tangents_are_seen():
+    """Forward-mode tangents have no requires_grad; the choice of the autograd form sees them."""
+    import torch.autograd.forward_ad as fwAD
+    from dynamic_dilated_depthwise_amd import sequence as seq
+    t = torch.ones(3)
+    assert not seq._differentiated(t, None) and seq._differentiated(t, torch.ones(3, requires_grad=True))
+    with torch.no_grad():
+        assert not seq._differentiated(torch.ones(3, requires_grad=True))
+        with fwAD.dual_level():
+            assert seq._differentiated(None, t, fwAD.make_dual(t, t)) and not seq._differentiated(t)
