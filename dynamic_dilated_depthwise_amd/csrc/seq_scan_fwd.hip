@@ -11,7 +11,7 @@ constexpr double kLog2e = 1.4426950408889634;
 
 // dt and the running sums s of a chunk, four heads a workgroup (dt's rows lie token by
 // token in memory, what comes out head by head), a wave a head, 64-bit sums.  A token past
-// the sequence's length has dt = 0: it leaves the state alone.  A step's decay is bounded
+// the sequence's length has dt = 0 and no decay: it leaves the state alone.  A step's decay is bounded
 // to 2^-2000 and 2^2000, beyond which float32 has only 0 and infinity, so that s stays
 // finite.  2 x 8192 tokens, 32 heads: 6.7 us, most of it latency.
 template <typename T>
@@ -39,7 +39,8 @@ __global__ __launch_bounds__(kThreads) void scan_times_kernel(ScanDims d, const 
         for (int e = 0; e < PER; ++e) {
             const float v = tile[k][lane * PER + e];
             d.dt[at + e] = v;
-            run += fmin(fmax(v * a, -2000.), 2000.);
+            const double step = v * a;
+            run += lane * PER + e >= n ? 0. : step < -2000. ? -2000. : step > 2000. ? 2000. : step;  // NaN stays NaN
             s[e] = run;
         }
         double before = run;
