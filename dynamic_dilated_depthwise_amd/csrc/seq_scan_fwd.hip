@@ -43,13 +43,14 @@ __global__ __launch_bounds__(kThreads) void scan_times_kernel(ScanDims d, const 
             run += lane * PER + e >= n ? 0. : step < -2000. ? -2000. : step > 2000. ? 2000. : step;  // NaN stays NaN
             s[e] = run;
         }
-        double before = run;
+        double all = run;
 #pragma unroll
         for (int m = 1; m < kWave; m *= 2) {
-            const double o = __shfl_up(before, m, kWave);
-            if (lane >= m) before += o;
+            const double o = __shfl_up(all, m, kWave);
+            if (lane >= m) all += o;
         }
-        before -= run;
+        double before = __shfl_up(all, 1, kWave);  // not all - run: NaN must reach no earlier token
+        if (lane == 0) before = 0.;
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
             const float hi = (float)(before + s[e]);
@@ -57,7 +58,7 @@ __global__ __launch_bounds__(kThreads) void scan_times_kernel(ScanDims d, const 
             d.slo[at + e] = (float)(before + s[e] - hi);
         }
         if (lane == kWave - 1)
-            d.decay[((int64_t)b * d.H + h0 + k) * d.nc + c] = __builtin_amdgcn_exp2f((float)(before + run));
+            d.decay[((int64_t)b * d.H + h0 + k) * d.nc + c] = __builtin_amdgcn_exp2f((float)all);
     }
 }
 
@@ -72,6 +73,34 @@ struct OutArgs {
     const float *D;
 };
 
+// One row of the state over the n tokens of a chunk, in four threads, from what enters it in v: the
+// y that are not finite become the recurrence's.
+template <typename T, int NP>
+__device__ __forceinline__ void recur(const ScanDims &d, int64_t head, int c, int n, bool mine, float (&v)[NP / 4],
+                                      const T *x, int64_t x_token, const T *B, int64_t b_token, const T *C,
+                                      int64_t c_token, float skip, T *y) {
+    const int64_t at = (head * d.nc + c) * (16 * kStrips<T>);
+    float hi = 0.f, lo = 0.f;
+    for (int t = 0; t < n; ++t) {
+        const float next_hi = d.shi[at + t], next_lo = d.slo[at + t], xv = Elem<T>::to_f32(x[t * x_token]);
+        const float decay = __builtin_amdgcn_exp2f((next_hi - hi) + (next_lo - lo)), dx = d.dt[at + t] * xv;
+        hi = next_hi;
+        lo = next_lo;
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < NP / 4; ++k) {
+            const int m = threadIdx.x % 4 + 4 * k;
+            if (m >= d.N) continue;
+            v[k] = decay * v[k] + dx * Elem<T>::to_f32(B[t * b_token + m]);
+            sum += v[k] * Elem<T>::to_f32(C[t * c_token + m]);
+        }
+        sum += __shfl_xor(sum, 1, kWave);
+        sum += __shfl_xor(sum, 2, kWave);
+        T *to = y + (int64_t)t * d.H * d.P;
+        if (mine && threadIdx.x % 4 == 0 && Elem<T>::to_f32(*to) * 0.f != 0.f) *to = Elem<T>::from_f32(sum + skip * xv);
+    }
+}
+
 // y of a chunk for some heads of a group.  C . B is theirs together and stays in registers
 // (transposed: rows i, columns t); each head scales it by its decays, which makes it the
 // operand that x is multiplied by.  A wave has rows t of strips w and 7 - w (bfloat16), so
@@ -79,7 +108,9 @@ struct OutArgs {
 // serves two strips.  The scaled C . B enters the product as two bfloat16 terms (rounded to one it
 // made the error of y up to 1.35 times its own rounding's; 6 us of 56), and so does the entering
 // state (1.4 times where it dominates; 2 us), whose two parts with segments are joined in float32.
-// y is rounded once, at the end.
+// y is rounded once, at the end.  A factor of zero in a matrix product does not keep what is not
+// finite from the tokens before it, so a workgroup that made such a y goes over its own once more,
+// token by token, and corrects those (the look at every y: 1 us of 58).
 // Bound by memory and vector instructions together: 2 x 8192 tokens bfloat16, 32 heads, P = N = 64:
 // 56 us, 3.6 TB/s with the states; ragged prompts 4 x 4096, N = 128: 85 us; 65536 tokens float32, 2 heads, N = 64:
 // 44 us, half the rate of its matrix instructions.
@@ -169,6 +200,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
         }
     }
 
+    float largest = 0.f;  // of this lane's results; NaN counts as the largest
     for (int it = 0; it < items; ++it) {
         const int h = h0 + it / slabs, p0 = it % slabs * kSlab, tid = afresh(threadIdx.x);
         __syncthreads();
@@ -273,10 +305,35 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
                 const int at = 16 * p + 4 * g;
                 f32x4 o = acc[j][p] + skip * lds4(xtile + t * LDP + at);
 #pragma unroll
-                for (int v = 0; v < 4; ++v) o[v] = t < n ? o[v] : 0.f;
+                for (int v = 0; v < 4; ++v) {
+                    o[v] = t < n ? o[v] : 0.f;
+                    largest = __builtin_elementwise_maximum(largest, __builtin_fabsf(o[v]));
+                }
                 if (p0 + at < d.P) store4<T>(yr + at, o, WHOLE ? 4 : d.P - p0 - at);
             }
         }
+    }
+    if (!__syncthreads_or(!(largest < INFINITY))) return;
+    for (int it = 0; it < items; ++it) {
+        const int64_t head = (int64_t)b * d.H + h0 + it / slabs;
+        const int p = it % slabs * kSlab + tid / 4;  // four threads a row of the state
+        const bool mine = p < d.P;
+        const float *place = a.states + (head * d.nc * d.P + (mine ? p : 0)) * cols;
+        const float carry = has_b ? a.carried[head * d.nc + c] : 1.f;
+        float v[NP / 4];
+#pragma unroll
+        for (int k = 0; k < NP / 4; ++k) {
+            const int m = tid % 4 + 4 * k;
+            v[k] = 0.f;
+            if (m < cols) {
+                if (has_h) v[k] = place[(int64_t)first * d.P * cols + m];
+                if (has_b) v[k] = v[k] * carry + place[(int64_t)c * d.P * cols + m];
+            }
+        }
+        recur<T, NP>(d, head, c, n, mine, v, xb + (int64_t)(h0 + it / slabs) * d.P + (mine ? p : 0), a.x_token,
+                     Bm + b * a.b_batch + (int64_t)c * Q * a.b_token + grp * d.N, a.b_token,
+                     Cm + b * a.c_batch + (int64_t)c * Q * a.c_token + grp * d.N, a.c_token, a.D[h0 + it / slabs],
+                     y + (((int64_t)b * d.L + c * Q) * d.H + h0 + it / slabs) * d.P + (mine ? p : 0));
     }
 }
 

@@ -23,6 +23,9 @@
  * Lengths.  `lengths` [batch] int32, or NULL: sequence b has lengths[b] tokens (values
  *   outside [0, length] are taken as the nearest).  Later positions are not read; y and the
  *   gradients there are zero and the state is that behind the last token.
+ * Not finite.  In the scan an infinity or NaN of a token reaches y of that token and later ones
+ *   and the states, as in the recurrence, and nothing before it.  In its backward any gradient of
+ *   the same chunk of tokens (128 in bfloat16, 64 in float32) and head or group may become NaN.
  * Slots.  `slots` [batch] int32, or NULL for 0, 1, ...: the state of sequence b is
  *   state[slots[b]].  A slot outside [0, num_slots) marks a place without a sequence: y is
  *   zero and no state is touched.  A slot may be named once in a call.

@@ -4,7 +4,7 @@ import torch
 
 import seq_oracle as orc
 from dynamic_dilated_depthwise_amd import sequence as seq
-from test_gpu_seq_norm_conv import DT, announce
+from test_gpu_seq_norm_conv import DT, announce, gen_of, randn
 from test_gpu_seq_scan import case
 
 pytestmark = pytest.mark.gpu
@@ -23,3 +23,69 @@ def test_nan_decay_rate(save, dt):
     assert bool(y2[:, :, 1].isnan().all()) and bool(last2[:, 1].isnan().all())
     for h in (0, 2):
         assert torch.equal(y2[:, :, h], y[:, :, h]) and torch.equal(last2[:, h], last[:, h])
+
+
+BAD = {"nan": float("nan"), "inf": float("inf")}
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("bad", BAD)
+@pytest.mark.parametrize("where", ["x", "dt", "B", "C"])
+@pytest.mark.parametrize("at", [0, 15, 16, 31, 40, 63, 64, 90, 127, 128, 140])
+def test_tokens_before(at, where, bad, dt):
+    """A value that is not finite reaches its token and those behind it, and no earlier one: not in its
+    tile of tokens either."""
+    announce("scan not finite", at, where, bad, dt)
+    P, N = 20, 12
+    args = list(case(2, 150, 4, P, 2, N, DT[dt]))
+    want, size = orc.scan(*args)
+    k = {"x": 0, "dt": 1, "B": 3, "C": 4}[where]
+    args[k] = args[k].clone()
+    args[k][(1, at, 1, 3)[:args[k].dim()]] = BAD[bad]  # of sequence 1: head 1 (x, dt) or group 1 (B, C)
+    y, last, _ = seq.selective_scan_fwd(*args, return_state=True)
+    heads = [1] if where in ("x", "dt") else [2, 3]
+    touched = torch.zeros(2, 150, 4, P, dtype=torch.bool)
+    for h in heads:
+        if where == "C":
+            touched[1, at, h] = True
+        elif where == "x":
+            touched[1, at:, h, 3] = True
+        else:
+            touched[1, at:, h] = True
+    y = y.cpu()
+    assert not bool(y[touched].isfinite().any())
+    assert bool(y[~touched].isfinite().all())
+    clean = want["y"].masked_fill(touched, 0)
+    orc.check(y.masked_fill(touched, 0), clean, size["y"], DT[dt], "y", operand=None)
+    tstate = torch.zeros(2, 4, P, N, dtype=torch.bool)
+    if where == "x":
+        tstate[1, 1, 3] = True
+    elif where == "B":
+        tstate[1, 2:, :, 3] = True
+    elif where == "dt":
+        tstate[1, 1] = True
+    last = last.cpu()
+    assert not bool(last[tstate].isfinite().any())
+    orc.check(last.masked_fill(tstate, 0), want["state"].masked_fill(tstate, 0), size["state"], torch.float32, "state")
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("at", [0, 70, 130, 299])
+def test_tokens_before_in_segments(at, dt):
+    """The same where the call takes segments of chunks, with states that enter them and a length."""
+    announce("scan not finite, segments", at, dt)
+    H, P, G, N = 512, 8, 256, 12
+    args = list(case(1, 310, H, P, G, N, DT[dt]))
+    init = randn(gen_of(12), 1, H, P, N)
+    lengths = torch.tensor([300], dtype=torch.int32, device="cuda")
+    want, size = orc.scan(*args, init, lengths)
+    args[0][0, at, 100, 5] = float("nan")
+    args[0][0, 300:, 7] = float("nan")
+    y, last, _ = seq.selective_scan_fwd(*args, init, lengths, return_state=True)
+    touched = torch.zeros(1, 310, H, P, dtype=torch.bool)
+    touched[0, at:300, 100, 5] = True
+    y, last = y.cpu(), last.cpu()
+    assert bool(y[touched].isnan().all()) and bool(last[0, 100, 5].isnan().all())
+    orc.check(y.masked_fill(touched, 0), want["y"].masked_fill(touched, 0), size["y"], DT[dt], "y")
+    last[0, 100, 5] = want["state"][0, 100, 5].float()
+    orc.check(last, want["state"], size["state"], torch.float32, "state")
