@@ -63,12 +63,13 @@ __device__ __forceinline__ float fast_sigmoid(float u) {
     return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * u));
 }
 
-// x of sequence b (ib: its initial state) at token t < n, zero before the state's first.
+// x of sequence b (ib: its initial state) at token t < n, zero before the state's first.  A vector
+// that is not there is asked for at the bias, where a row of D channels can be read in any case.
 template <typename T, int V, Reach R>
 __device__ __forceinline__ Raw<T, V> token(const ConvArgs &a, const T *xb, const T *ib, int t, int n, int c) {
     Raw<T, V> r;
     const bool early = t < 0, on = t < n && (!early || (ib != nullptr && t > -a.W));
-    const T *p = on ? (early ? ib + (int64_t)(a.W - 1 + t) * a.D : xb + (int64_t)t * a.x_token) : xb;
+    const T *p = on ? (early ? ib + (int64_t)(a.W - 1 + t) * a.D : xb + (int64_t)t * a.x_token) : (const T *)a.bias;
     r.template load<R>(p, c, a.D, on);
     return r;
 }
@@ -172,8 +173,8 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvArgs a, const T 
         }
         auto ask = [&](int k, int t) {  // token t into slot k
             const bool on = t < n && t < t1 + W1;
-            x[k].template load<R>(xb + (on ? (int64_t)t * a.x_token : 0), c, a.D, on);
-            g[k].template load<R>(gb + (on ? (int64_t)t * g_token : 0), c, a.D, on);
+            x[k].template load<R>(on ? xb + (int64_t)t * a.x_token : (const T *)a.bias, c, a.D, on);
+            g[k].template load<R>(on ? gb + (int64_t)t * g_token : (const T *)a.bias, c, a.D, on);
         };
 #pragma unroll
         for (int k = 0; k < U; ++k) ask(k, t0 + k);

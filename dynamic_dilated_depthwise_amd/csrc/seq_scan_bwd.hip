@@ -132,8 +132,10 @@ __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, co
             tf[1] = d.slo[chunk * Q + tid];
             tf[2] = d.dt[chunk * Q + tid];
         }
-        xf.fetch(xb + (int64_t)h * d.P + p0, a.x_token, n, d.P - p0, tid);
-        gf.fetch(gb + (int64_t)h * d.P + p0, a.g_token, n, d.P - p0, tid);
+        if (!WHOLE || n > 0) {  // nothing of a chunk past the length may be read (vectors of parts are not)
+            xf.fetch(xb + (int64_t)h * d.P + p0, a.x_token, n, d.P - p0, tid);
+            gf.fetch(gb + (int64_t)h * d.P + p0, a.g_token, n, d.P - p0, tid);
+        }
         if (has_h) hf.fetch(a.states + (chunk * d.P + p0) * cols, cols, d.P - p0, cols, tid);
         if (SETS == 2) fetch_adjoint(it);
     };

@@ -138,6 +138,12 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
     n = n < 0 ? 0 : n > Q ? Q : n;
     const int hg = d.H / d.G, h0 = grp * hg + split * a.plan.per;
     const int h1 = h0 + a.plan.per < (grp + 1) * hg ? h0 + a.plan.per : (grp + 1) * hg;
+    if (n == 0) {  // nothing of this chunk may be read
+        const int64_t each = (int64_t)(h1 - h0) * d.P, tok = (int64_t)b * d.L + c * Q;
+        for (int t = 0; t < rows; ++t)
+            for (int64_t i = tid; i < each; i += kThreads) y[((tok + t) * d.H + h0) * d.P + i] = Elem<T>::from_f32(0.f);
+        return;
+    }
     const int slabs = (d.P + kSlab - 1) / kSlab, items = (h1 - h0) * slabs, cols = state_cols(d.N);
     const T *xb = X + b * a.x_batch + (int64_t)c * Q * a.x_token;
     const int first = SEG ? c / d.seg * d.seg : c;  // the chunk whose place has the entering state, or the segment's
