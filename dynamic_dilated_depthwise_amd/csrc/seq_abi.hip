@@ -245,6 +245,7 @@ int ddpm_causal_conv_step(const void *x, const void *weight, const void *bias, v
     c.size(num_slots);
     int st = conv_sizes(c, batch, 1, D, width, x_batch, 0);
     if (st != DDPM_OK) return st;
+    if (slots == nullptr && num_slots < batch) return DDPM_ERR_INVALID_ARG;
     c.input(x, extent(batch, 1, D, x_batch, 0), c.es());
     c.input(weight, (double)D * width, c.es());
     c.input(bias, D, c.es());
@@ -326,6 +327,7 @@ int ddpm_selective_scan_bwd(const ddpm_scan *s, const void *saved, const void *g
 int ddpm_selective_scan_step(const ddpm_scan *s, float *state, const int32_t *slots, int64_t num_slots, void *y,
                              hipStream_t stream) {
     if (!scan_sizes_ok(s) || s->length != 1 || num_slots < 1 || num_slots > kMax) return DDPM_ERR_INVALID_ARG;
+    if (slots == nullptr && num_slots < s->batch) return DDPM_ERR_INVALID_ARG;
     Check c(s->dtype);
     scan_inputs(c, s, 1);
     if (c.bad) return DDPM_ERR_INVALID_ARG;

@@ -147,6 +147,11 @@ void writable(const Tensor &t, const char *name) {
     if (t.requires_grad() && c10::GradMode::is_enabled())
         refuse(name, " requires grad and a step writes it in place; call it under torch.no_grad()");
 }
+// slots, or none: the places 0, 1, ... must then be there.
+const void *slots_of(const Call &c, PyObject *o, int64_t batch, int64_t S) {
+    if (o == Py_None && S < batch) refuse("state has ", S, " places for ", batch, " sequences without slots");
+    return c.maybe(o, "slots", at::kInt, {batch});
+}
 void written(const Tensor &t) {
     if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
 }
@@ -288,7 +293,7 @@ PyObject *causal_conv_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int64_t S = state.dim() == 3 ? state.size(0) : 0;
     void *st = c.like(a[3], "state", {S, t.W - 1, D});
     writable(state, "state");
-    const void *slots = c.maybe(a[4], "slots", at::kInt, {batch});
+    const void *slots = slots_of(c, a[4], batch, S);
     const Tensor y = c.empty({batch, D});
     done("ddpm_causal_conv_step",
          ddpm_causal_conv_step(c.x.data_ptr(), t.weight, t.bias, t.W > 1 ? st : nullptr, (const int32_t *)slots, y.data_ptr(),
@@ -391,7 +396,7 @@ PyObject *selective_scan_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int64_t S = state.dim() == 4 ? state.size(0) : 0;
     float *st = (float *)c.like(a[7], "state", at::kFloat, {S, s.heads, s.P, s.N});
     writable(state, "state");
-    const void *slots = c.maybe(a[8], "slots", at::kInt, {s.batch});
+    const void *slots = slots_of(c, a[8], s.batch, S);
     const Tensor y = c.empty(c.x.sizes());
     done("ddpm_selective_scan_step", ddpm_selective_scan_step(&s, st, (const int32_t *)slots, S, y.data_ptr(), c.stream));
     written(state);

@@ -28,7 +28,8 @@
  *   the same chunk of tokens (128 in bfloat16, 64 in float32) and head or group may become NaN.
  * Slots.  `slots` [batch] int32, or NULL for 0, 1, ...: the state of sequence b is
  *   state[slots[b]].  A slot outside [0, num_slots) marks a place without a sequence: y is
- *   zero and no state is touched.  A slot may be named once in a call.
+ *   zero and no state is touched.  A slot may be named once in a call.  Without slots
+ *   num_slots is at least batch.
  * Errors.  As in ddpm.h; all arguments are checked before anything is enqueued.
  *     DDPM_ERR_INVALID_ARG  null or misaligned pointers, sizes below 1 or beyond 2^31 - 1
  *                           (2^31 - 2^16 for C, length and D, and in the scan for heads * P,

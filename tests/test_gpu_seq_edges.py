@@ -82,3 +82,16 @@ def test_without_gradients():
     with pytest.raises(RuntimeError):  # once differentiable
         g, = torch.autograd.grad(y, leaf, grad, create_graph=True)
         g.sum().backward()
+
+
+def test_steps_without_slots():
+    """Fewer states than sequences are refused: the rest would have had no output and no state."""
+    announce("steps without slots")
+    x, w, b, line, _, _ = conv_case(3, 1, 16, 4, torch.float32)
+    with pytest.raises(ValueError, match="places"):
+        seq.causal_conv_step(x[:, 0], w, b, line[:2].contiguous())
+    sx, draw, A, Bm, Cm, D, bias = case(3, 1, 2, 8, 1, 6, torch.float32)
+    with pytest.raises(ValueError, match="places"):
+        seq.selective_scan_step(sx[:, 0], draw[:, 0], A, Bm[:, 0], Cm[:, 0], D, bias, torch.zeros(2, 2, 8, 6, device="cuda"))
+    seq.selective_scan_step(sx[:, 0], draw[:, 0], A, Bm[:, 0], Cm[:, 0], D, bias, torch.zeros(2, 2, 8, 6, device="cuda"),
+                            torch.tensor([1, 0, -1], dtype=torch.int32, device="cuda"))

@@ -27,3 +27,10 @@ def test_scan_near_2_31(lib):  # noqa: F811
 def test_eps(lib, eps):  # noqa: F811
     A = abi.A
     assert lib.ddpm_layer_norm_fwd(A[0], A[1], A[2], A[3], None, None, 4, 8, 8, eps, abi.F32, None) == INVALID
+
+
+def test_steps_without_slots(lib):  # noqa: F811
+    """Without slots sequence b's state is the b-th: there must be as many (the struct's and the call's batch is 2)."""
+    for call in (abi._conv_step, abi._scan_step):
+        name = "n" if call is abi._conv_step else "slots"
+        assert call(lib, S=1, **{name: None}) == INVALID, call.__name__
