@@ -28,7 +28,8 @@ __all__ = ["PixelMixer"]
 class PixelMixer(nn.Module):
     """heads of head_dim channels each keep a [head_dim, state_dim] state; the heads of one of
     ``groups`` share B and C; width is the convolution's.  float32 or bfloat16, on the GPU;
-    A, D and dt_bias enter the scan in float32 whatever the module's type."""
+    A, D and dt_bias enter the scan in float32 whatever the module's type.  Under autocast the
+    projections run in its type, the operators between them and the states stay in the module's."""
 
     def __init__(self, dim=64, heads=2, head_dim=64, state_dim=64, groups=1, width=4, eps=1e-5):
         super().__init__()
@@ -60,8 +61,12 @@ class PixelMixer(nn.Module):
                 torch.zeros(slots, self.heads, self.head_dim, self.state_dim, device=w.device, dtype=torch.float32))
 
     def _enter(self, tokens):
+        dtype = self.norm_weight.dtype
+        if torch.is_autocast_enabled("cuda"):
+            tokens = tokens.to(dtype)
         t = seq.layer_norm(tokens, self.norm_weight, self.norm_bias, self.eps)
-        return self.in_proj(t).split([self.inner, self.channels, self.heads], -1)
+        z, u, raw = self.in_proj(t).split([self.inner, self.channels, self.heads], -1)
+        return z, u.to(dtype), raw.to(dtype)
 
     def _per_head(self, u):
         v, B, C = u.split([self.inner, self.shared, self.shared], -1)

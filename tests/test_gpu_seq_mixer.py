@@ -158,3 +158,35 @@ def test_refusals():
         m.step(torch.zeros(1, 63, device="cuda"), m.new_state(1))
     with pytest.raises(ValueError):
         m(torch.zeros(1, 64, 4, 4, device="cuda", dtype=torch.float16))
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+def test_autocast(kind):
+    """A float32 mixer under autocast: the projections in autocast's type, the operators and states in
+    float32.  Tolerances as for the bfloat16 mixer, whose roundings are a part of these or coarser."""
+    announce("mixer autocast", kind)
+    m = mixer(torch.float32, dim=24, heads=4, head_dim=20, state_dim=18, groups=2, width=3)
+    g = gen_of(35)
+    x, grad = randn(g, 2, 24, 5, 7), randn(g, 2, 24, 5, 7)
+    x.requires_grad_()
+    with torch.autocast("cuda", dtype=kind):
+        out = m(x)
+    out.backward(grad)
+    p = wide(m)
+    xd = x.detach().double().cpu().requires_grad_()
+    want, _ = plain(m, xd.flatten(2).transpose(1, 2), p)
+    want = want.transpose(1, 2).unflatten(2, (5, 7))
+    want.backward(grad.double().cpu())
+    near(out, want, torch.bfloat16, "out")
+    near(x.grad, xd.grad, torch.bfloat16, "grad x")
+    for k, t in m.named_parameters():
+        assert t.grad.dtype == torch.float32
+        near(t.grad, p[k].grad, torch.bfloat16, "grad " + k, 4)
+    # a prompt in autocast's own type, its states, and tokens from there
+    tokens = randn(g, 2, 6, 24).to(kind)
+    with torch.no_grad(), torch.autocast("cuda", dtype=kind):
+        start, state = m.prompt(tokens[:, :4].contiguous())
+        rest = [m.step(tokens[:, t].contiguous(), state) for t in (4, 5)]
+    assert all(t.dtype == torch.float32 for t in state)
+    want, _ = plain(m, tokens.double().cpu(), {k: t.detach() for k, t in p.items()})
+    near(torch.cat([start, torch.stack(rest, 1)], 1), want, torch.bfloat16, "prompt and tokens")
