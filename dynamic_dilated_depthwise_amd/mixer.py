@@ -82,16 +82,23 @@ class PixelMixer(nn.Module):
     def prompt(self, tokens, state=None, lengths=None):
         """(out, state): tokens [batch, L, dim], of which sequence b has lengths[b] (int32; L
         without lengths); state from new_state or an earlier call.  Past a length out repeats
-        the tokens."""
+        the tokens, which take part in nothing else: neither they nor gradients there need be finite."""
         if tokens.dim() != 3 or tokens.shape[2] != self.dim:
             raise ValueError(f"tokens must have shape (batch, length, {self.dim}) (got {tuple(tokens.shape)})")
         first, h = state if state is not None else (None, None)
-        z, u, raw = self._enter(tokens)
+        inside = None
+        if lengths is not None:
+            if lengths.dtype != torch.int32 or lengths.shape != tokens.shape[:1] or lengths.device != tokens.device:
+                raise ValueError(f"lengths must be int32 of shape ({tokens.shape[0]},) on {tokens.device} (got "
+                                 f"{lengths.dtype}, {tuple(lengths.shape)}, {lengths.device})")
+            inside = (torch.arange(tokens.shape[1], device=tokens.device) < lengths[:, None])[..., None]
+        z, u, raw = self._enter(tokens if inside is None else torch.where(inside, tokens, 0))
         u, last = seq.causal_conv(u, self.conv_weight, self.conv_bias, first, lengths)
         v, B, C = self._per_head(u)
         A, D, bias = self._scan_parameters()
         y, h = seq.selective_scan(v, raw, A, B, C, D, bias, h, lengths)
-        return self._leave(tokens, y, z), (last, h)
+        out = self._leave(tokens, y, z)
+        return out if inside is None else torch.where(inside, out, tokens), (last, h)
 
     @torch.no_grad()
     def step(self, tokens, state, slots=None):

@@ -190,3 +190,32 @@ def test_autocast(kind):
     assert all(t.dtype == torch.float32 for t in state)
     want, _ = plain(m, tokens.double().cpu(), {k: t.detach() for k, t in p.items()})
     near(torch.cat([start, torch.stack(rest, 1)], 1), want, torch.bfloat16, "prompt and tokens")
+
+
+@pytest.mark.parametrize("dt", DT)
+def test_past_a_length(dt):
+    """Tokens past a length come out as they are and take part in no gradient, whatever they and the
+    gradients there hold."""
+    announce("mixer past a length", dt)
+    dtype = DT[dt]
+    m = mixer(dtype, dim=24, heads=2, head_dim=16, state_dim=12)
+    g = gen_of(36)
+    tokens, grad = randn(g, 2, 9, 24, dtype=dtype), randn(g, 2, 9, 24, dtype=dtype)
+    lengths = torch.tensor([9, 4], dtype=torch.int32, device="cuda")
+    params = list(m.parameters())
+
+    def run(fill, gfill):
+        t, gr = tokens.clone(), grad.clone()
+        t[1, 4:], gr[1, 4:] = fill, gfill
+        t.requires_grad_()
+        out, _ = m.prompt(t, lengths=lengths)
+        return out.detach(), torch.autograd.grad(out, [t, *params], gr)
+
+    out, (gt, *gp) = run(0.0, 0.0)
+    for bad in (float("nan"), float("inf")):
+        out2, (gt2, *gp2) = run(bad, bad)
+        same = torch.full_like(out2[1, 4:], bad)
+        assert torch.equal(out2[0], out[0]) and torch.equal(out2[1, :4], out[1, :4])
+        assert torch.equal(out2[1, 4:], same) or bool(out2[1, 4:].isnan().all() and same.isnan().all())
+        assert torch.equal(gt2[0], gt[0]) and torch.equal(gt2[1, :4], gt[1, :4])
+        assert all(torch.equal(p, q) for p, q in zip(gp, gp2))

@@ -35,3 +35,10 @@ def test_tangents_are_seen():
         assert not seq._differentiated(torch.ones(3, requires_grad=True))
         with fwAD.dual_level():
             assert seq._differentiated(None, t, fwAD.make_dual(t, t)) and not seq._differentiated(t)
+
+
+@pytest.mark.parametrize("lengths", [torch.zeros(2, dtype=torch.int32), torch.zeros(1), torch.zeros(1, 1, dtype=torch.int32),
+                                     torch.zeros(1, dtype=torch.int32, device="meta")])
+def test_lengths_are_checked(lengths):
+    with pytest.raises(ValueError, match="lengths must be"):
+        PixelMixer().prompt(torch.zeros(1, 4, 64), lengths=lengths)
