@@ -34,3 +34,13 @@ def test_steps_without_slots(lib):  # noqa: F811
     for call in (abi._conv_step, abi._scan_step):
         name = "n" if call is abi._conv_step else "slots"
         assert call(lib, S=1, **{name: None}) == INVALID, call.__name__
+
+
+@pytest.mark.parametrize("dtype,Q", [(abi.F32, 64), (abi.BF16, 128)])
+def test_workspace_with_segments(lib, dtype, Q):  # noqa: F811
+    """Long calls hold one float32 state a chunk and head whether they keep it or not, and two numbers a chunk and head."""
+    batch, L, H, P, N = 4, 4096, 32, 64, 128
+    nc = L // Q
+    kept = batch * H * nc * (3 * Q + 1 + P * N)
+    got = lib.ddpm_selective_scan_fwd_workspace(abi._struct(batch=batch, L=L, heads=H, P=P, groups=1, N=N, dtype=dtype)) // 4
+    assert kept <= got <= kept + 2 * batch * H * nc + 6 * 64
