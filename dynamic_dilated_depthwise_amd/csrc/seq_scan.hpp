@@ -37,8 +37,9 @@ constexpr int kSlab = 64;  // rows of the state (of P) that a workgroup works on
 
 // Tokens of a chunk, in strips of 16.  bfloat16: 128, so that the states in memory, which
 // shrink with the chunk, and the products inside a chunk, which grow with it, cost about
-// the same (training at 2 x 8192 tokens, 32 heads, P = N = 64: 340 us, with 64 tokens 512 us;
-// ragged prompts 4 x 4096, 32 heads, N = 128: 123 and 157 us).  float32: 64, since its matrix products cost 16 times as much.
+// the same (training at 2 x 8192 tokens, 32 heads, P = N = 64: 372 us, with 64 tokens 515 us;
+// ragged prompts 4 x 4096, 32 heads, N = 128: 152 and 213 us).  float32: 64, since its matrix
+// products cost 16 times as much.
 template <typename T> constexpr int kStrips = Elem<T>::is_bf16 ? 8 : 4;
 
 struct ScanDims {
@@ -59,8 +60,8 @@ struct ChunkPlan {
 // Workgroups over (batch, chunk, group, split of the group's heads).  Heads of one group
 // share B and C, which a workgroup prepares first, at about the cost of a head: the split with
 // the shortest time for `slots` workgroups at once, in rounds of (heads + 1), and the fewest
-// workgroups among equals.  (An earlier form of the backward at 2 x 64 chunks, 32 heads: 2 splits
-// 206 us, 4 splits 219 us.)
+// workgroups among equals.  (Training in bfloat16 at 2 x 64 chunks, 32 heads, with 2 and with 4
+// splits in the backward: 356 and 366 us.)
 inline ChunkPlan plan_heads(int64_t B, int64_t nc, int H, int P, int G, int64_t slots) {
     const int64_t base = B * nc * G, slabs = (P + kSlab - 1) / kSlab;
     const int hg = H / G;
@@ -86,9 +87,9 @@ __device__ __forceinline__ int valid_tokens(const int *lengths, int b, int L) {
 inline int64_t pad64(int64_t n) { return (n + 63) / 64 * 64; }
 
 // Segments of a call that keeps nothing: the longest, up to 8 chunks, and the most heads at
-// once, up to 2, that leave 512 workgroups.  seg = 1: none, every chunk has its state.  With segments and without: ragged
-// prompts 4 x 4096 bfloat16, 32 heads, P = 64, N = 128: 155 and 168 us; 65536 tokens float32, 2
-// heads, P = N = 64: 75 and 78 us.
+// once, up to 2, that leave 512 workgroups.  seg = 1: none, every chunk has its state.  With
+// segments and without: ragged prompts 4 x 4096 bfloat16, 32 heads, P = 64, N = 128: 152 and 172 us;
+// 65536 tokens float32, 2 heads, P = N = 64: 71 and 80 us.
 struct SegmentPlan {
     int seg, hw;
 };

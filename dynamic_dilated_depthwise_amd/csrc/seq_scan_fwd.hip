@@ -73,8 +73,8 @@ struct OutArgs {
     const float *D;
 };
 
-// One row of the state over the n tokens of a chunk, in four threads, from what enters it in v: the
-// y that are not finite become the recurrence's.
+// One row of the state over the n tokens of a chunk, in four threads, from what enters it in v (a
+// quarter of the columns in each): the y that are not finite become the recurrence's.
 template <typename T, int NP>
 __device__ __forceinline__ void recur(const ScanDims &d, int64_t head, int c, int n, bool mine, float (&v)[NP / 4],
                                       const T *x, int64_t x_token, const T *B, int64_t b_token, const T *C,
@@ -88,11 +88,16 @@ __device__ __forceinline__ void recur(const ScanDims &d, int64_t head, int c, in
         lo = next_lo;
         float sum = 0.f;
 #pragma unroll
-        for (int k = 0; k < NP / 4; ++k) {
-            const int m = threadIdx.x % 4 + 4 * k;
-            if (m >= d.N) continue;
-            v[k] = decay * v[k] + dx * Elem<T>::to_f32(B[t * b_token + m]);
-            sum += v[k] * Elem<T>::to_f32(C[t * c_token + m]);
+        for (int k = 0; k < NP / 4; k += kVec<T>) {
+            const int m = threadIdx.x % 4 * (NP / 4) + k;
+            float bv[kVec<T>], cv[kVec<T>];
+            widen<T>(load_vec<T>(B + t * b_token + m, d.N - m), bv);
+            widen<T>(load_vec<T>(C + t * c_token + m, d.N - m), cv);
+#pragma unroll
+            for (int e = 0; e < kVec<T>; ++e) {
+                v[k + e] = decay * v[k + e] + dx * bv[e];
+                sum += v[k + e] * cv[e];
+            }
         }
         sum += __shfl_xor(sum, 1, kWave);
         sum += __shfl_xor(sum, 2, kWave);
@@ -162,7 +167,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
         skip_next = a.D[h];
         xf.fetch(xb + (int64_t)h * d.P + p0, a.x_token, n, d.P - p0, tid);
         const int64_t chunk = ((int64_t)b * d.H + h) * d.nc + c;
-        if (has_h) hf.fetch(a.states + ((chunk - c + first) * d.P + p0) * cols, cols, d.P - p0, cols, tid);
+        if (!SEG && has_h) hf.fetch(a.states + ((chunk - c + first) * d.P + p0) * cols, cols, d.P - p0, cols, tid);
         if (has_b) {
             carry_next = a.carried[chunk];
             bf.fetch(a.states + (chunk * d.P + p0) * cols, cols, d.P - p0, cols, tid);
@@ -209,6 +214,9 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
     float largest = 0.f;  // of this lane's results; NaN counts as the largest
     for (int it = 0; it < items; ++it) {
         const int h = h0 + it / slabs, p0 = it % slabs * kSlab, tid = afresh(threadIdx.x);
+        // not an item ahead like the rest: a segment's chunks read the same from the L2, and the registers of
+        // both parts are too many (ragged prompts, N = 128: 27 spill, 167 -> 152 us; float32 pixels 75 -> 71)
+        if (SEG && has_h) hf.fetch(a.states + ((((int64_t)b * d.H + h) * d.nc + first) * d.P + p0) * cols, cols, d.P - p0, cols, tid);
         __syncthreads();
         xf.put(xtile, LDP, n, d.P - p0, tid);
         const float carry = carry_next;
@@ -329,17 +337,27 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
         float v[NP / 4];
 #pragma unroll
         for (int k = 0; k < NP / 4; ++k) {
-            const int m = tid % 4 + 4 * k;
+            const int m = tid % 4 * (NP / 4) + k;
             v[k] = 0.f;
             if (m < cols) {
                 if (has_h) v[k] = place[(int64_t)first * d.P * cols + m];
                 if (has_b) v[k] = v[k] * carry + place[(int64_t)c * d.P * cols + m];
             }
         }
+        // a row whose entering state is not finite has no y to correct
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < NP / 4; ++k) sum += v[k] * 0.f;
+        sum += __shfl_xor(sum, 1, kWave);
+        sum += __shfl_xor(sum, 2, kWave);
+        T *yr = y + (((int64_t)b * d.L + c * Q) * d.H + h0 + it / slabs) * d.P + (mine ? p : 0);
+        bool any = false;
+        for (int t = tid % 4; mine && sum == 0.f && t < n; t += 4)
+            any |= Elem<T>::to_f32(yr[(int64_t)t * d.H * d.P]) * 0.f != 0.f;
+        if (!__any(any)) continue;
         recur<T, NP>(d, head, c, n, mine, v, xb + (int64_t)(h0 + it / slabs) * d.P + (mine ? p : 0), a.x_token,
                      Bm + b * a.b_batch + (int64_t)c * Q * a.b_token + grp * d.N, a.b_token,
-                     Cm + b * a.c_batch + (int64_t)c * Q * a.c_token + grp * d.N, a.c_token, a.D[h0 + it / slabs],
-                     y + (((int64_t)b * d.L + c * Q) * d.H + h0 + it / slabs) * d.P + (mine ? p : 0));
+                     Cm + b * a.c_batch + (int64_t)c * Q * a.c_token + grp * d.N, a.c_token, a.D[h0 + it / slabs], yr);
     }
 }
 

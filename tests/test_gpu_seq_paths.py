@@ -99,17 +99,18 @@ def test_heads_of_a_workgroup(lib, sizes, splits, dt):  # noqa: F811
 
 
 # The pass over the chunks, whose states are float32 whatever the inputs' type: 16 runs with more
-# states than a run keeps, 64 runs, 64 runs with more than they keep.
-@pytest.mark.parametrize("chunks", [70, 140, 260])
-def test_many_chunks(chunks):
+# states than a run keeps, and 64 with more and, in a shorter sequence, with fewer.
+@pytest.mark.parametrize("chunks,lengths", [(70, [70 * 64 - 17, 33 * 64]), (260, [260 * 64 - 17, 100 * 64 + 1])])
+def test_many_chunks(chunks, lengths):
     announce("scan chunks", chunks)
-    L = 64 * chunks - 17
-    args = case(1, L, 1, 3, 1, 5, torch.float32)
+    L = lengths[0]
+    args = case(2, L, 1, 3, 1, 5, torch.float32)
     g = gen_of(12)
-    grad, init, gs = randn(g, 1, L, 1, 3), randn(g, 1, 1, 3, 5), randn(g, 1, 1, 3, 5)
-    y, last, saved = seq.selective_scan_fwd(*args, init, return_state=True, save=True)
-    got = dict(zip(NAMES, seq.selective_scan_bwd(grad, *args, saved, init, None, gs)))
-    close({"y": y, "state": last, **got}, *orc.scan(*args, init, None, grad, gs))
+    grad, init, gs = randn(g, 2, L, 1, 3), randn(g, 2, 1, 3, 5), randn(g, 2, 1, 3, 5)
+    lengths = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    y, last, saved = seq.selective_scan_fwd(*args, init, lengths, return_state=True, save=True)
+    got = dict(zip(NAMES, seq.selective_scan_bwd(grad, *args, saved, init, lengths, gs)))
+    close({"y": y, "state": last, **got}, *orc.scan(*args, init, lengths, grad, gs))
 
 
 # Segments of chunks whose P and N are in whole vectors of both types, for each width of the state;
