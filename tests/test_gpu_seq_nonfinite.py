@@ -89,3 +89,32 @@ def test_tokens_before_in_segments(at, dt):
     orc.check(y.masked_fill(touched, 0), want["y"].masked_fill(touched, 0), size["y"], DT[dt], "y")
     last[0, 100, 5] = want["state"][0, 100, 5].float()
     orc.check(last, want["state"], size["state"], torch.float32, "state")
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("where", ["x", "grad"])
+def test_gradients_elsewhere(where, dt):
+    """What a NaN may reach in the backward: its chunk, what flows on from there in the recurrence and its
+    adjoint, and sums over the tokens; not another sequence, nor another head's x and dt."""
+    announce("scan gradients not finite", where, dt)
+    L, at = 600, 300  # in the third chunk of 128, the fifth of 64: tokens 256 to 383 and 256 to 319
+    args = list(case(2, L, 4, 20, 2, 12, DT[dt]))
+    grad = randn(gen_of(12), 2, L, 4, 20, dtype=DT[dt])
+    saved = seq.selective_scan_fwd(*args, save=True)[2]
+    clean = seq.selective_scan_bwd(grad, *args, saved)
+    t = args[0] if where == "x" else grad
+    t[1, at, 1, 3] = float("nan")
+    saved = seq.selective_scan_fwd(*args, save=True)[2]
+    got = seq.selective_scan_bwd(grad, *args, saved)
+    gx, gdt, gA, gB, gC, gD, gbias, _ = range(8)
+    away = slice(0, 256) if where == "x" else slice(384, L)  # x flows on to later states, grad to earlier adjoints
+    for k in (gx, gdt, gB, gC):
+        assert torch.equal(got[k][0], clean[k][0])
+        assert torch.equal(got[k][1, away], clean[k][1, away])
+    for k in (gx, gdt):
+        assert torch.equal(got[k][:, :, [0, 2, 3]], clean[k][:, :, [0, 2, 3]])
+    for k in (gB, gC):
+        assert torch.equal(got[k][:, :, 1], clean[k][:, :, 1])
+    for k in (gA, gD, gbias):
+        assert torch.equal(got[k][[0, 2, 3]], clean[k][[0, 2, 3]])
+    assert bool(got[gA][1].isnan()) and bool(got[gD][1].isnan()) and bool(got[gbias][1].isnan())
