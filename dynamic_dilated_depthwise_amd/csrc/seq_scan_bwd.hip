@@ -77,9 +77,9 @@ __device__ __forceinline__ float frag_at(const FragF &f, int e) { return f.v[e];
 // (grad_C, r) and as columns i (grad_x, grad_B, q).  Strips go in pairs, 32 of a contraction:
 // a wave in pair kw has the pairs before kw as rows, those after it as columns, and its own as
 // both, masked; the same work for every wave, and its tiles of C . B stay in registers.  Two waves
-// a SIMD with all registers taken; a head costs a wave 1570 vector, 134 matrix and 285 LDS
+// a SIMD with all registers taken; a head costs a wave 1660 vector, 144 matrix and 285 LDS
 // instructions, and those three and the barriers around the tiles add up more than they overlap
-// (vector issue 46 %, LDS 31 %, matrix 16 % of the time): 2 x 8192 tokens bfloat16, 32 heads, P =
+// (vector issue 50 %, LDS 30 %, matrix 17 % of the time): 2 x 8192 tokens bfloat16, 32 heads, P =
 // N = 64: 200 us.  N = 128 takes 580 us: one set of planes, and 130 registers spill.
 template <typename T, int NP, bool WHOLE>
 __global__ __launch_bounds__(64 * kStrips<T>) void scan_bwd_kernel(BwdArgs a, const T *__restrict__ X,

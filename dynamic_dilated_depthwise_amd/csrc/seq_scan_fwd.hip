@@ -111,14 +111,14 @@ __device__ __forceinline__ void recur(const ScanDims &d, int64_t head, int c, in
 // operand that x is multiplied by.  A wave has rows t of strips w and 7 - w (bfloat16), so
 // that the four waves have the same share of the triangle i <= t and each operand from LDS
 // serves two strips.  The scaled C . B enters the product as two bfloat16 terms (rounded to one it
-// made the error of y up to 1.35 times its own rounding's; 6 us of 56), and so does the entering
+// made the error of y up to 1.35 times its own rounding's; 6 us of 59), and so does the entering
 // state (1.4 times where it dominates; 2 us), whose two parts with segments are joined in float32.
 // y is rounded once, at the end.  A factor of zero in a matrix product does not keep what is not
 // finite from the tokens before it, so a workgroup that made such a y goes over its own once more,
-// token by token, and corrects those (the look at every y: 1 us of 58).
-// Bound by memory and vector instructions together: 2 x 8192 tokens bfloat16, 32 heads, P = N = 64:
-// 56 us, 3.6 TB/s with the states; ragged prompts 4 x 4096, N = 128: 85 us; 65536 tokens float32, 2 heads, N = 64:
-// 44 us, half the rate of its matrix instructions.
+// token by token, and corrects those (the look at every y: 1 us of 59).  Bound by memory and vector
+// instructions together: 2 x 8192 tokens bfloat16, 32 heads, P = N = 64: 59 us, 3.4 TB/s with the
+// states; ragged prompts 4 x 4096, N = 128: 82 us; 65536 tokens float32, 2 heads, N = 64: 40 us, a
+// little over half the rate of its matrix instructions.
 template <typename T, int NP, bool WHOLE, bool SEG>
 __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const T *__restrict__ X,
                                                                const T *__restrict__ Bm, const T *__restrict__ Cm,

@@ -16,7 +16,8 @@ Layouts (float32 or bfloat16 unless stated; ``L`` tokens, ``H`` heads in ``G`` g
   x of the scan [batch, L, H, P], dt [batch, L, H], B and C [batch, L, G, N];
   A, D, dt_bias [H] and states [batch, H, P, N] float32
 Inputs along a sequence may be views whose last axis (scan: all but the first two) is
-contiguous, such as the slices of one projection.  lengths and slots are int32 [batch]; see
+contiguous, such as the slices of one projection.  Every size is at least one (a sequence of a
+ragged batch may have no tokens).  lengths and slots are int32 [batch]; see
 the header for what they mean, and for widths (to 8) and state columns (to 128).
 
 The step functions write `state` in place as torch's in-place forms do: a state that requires grad
