@@ -167,7 +167,7 @@ __global__ __launch_bounds__(kThreads, 2) void scan_out_kernel(OutArgs a, const 
         skip_next = a.D[h];
         xf.fetch(xb + (int64_t)h * d.P + p0, a.x_token, n, d.P - p0, tid);
         const int64_t chunk = ((int64_t)b * d.H + h) * d.nc + c;
-        if (!SEG && has_h) hf.fetch(a.states + ((chunk - c + first) * d.P + p0) * cols, cols, d.P - p0, cols, tid);
+        if (!SEG && has_h) hf.fetch(a.states + (chunk * d.P + p0) * cols, cols, d.P - p0, cols, tid);
         if (has_b) {
             carry_next = a.carried[chunk];
             bf.fetch(a.states + (chunk * d.P + p0) * cols, cols, d.P - p0, cols, tid);
