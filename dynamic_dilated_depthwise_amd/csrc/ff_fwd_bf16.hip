@@ -1,0 +1,10 @@
+// ff_fwd_bf16.hip -- one kind of the feed-forward operators' products (ff_gemm.hpp).
+#include "ff_product.hpp"
+
+namespace ddpm {
+namespace ff {
+
+hipError_t product_fwd_bf16(const Product &a, float *part, hipStream_t stream) { return product<bf16_t, kForward>(a, part, stream); }
+
+}  // namespace ff
+}  // namespace ddpm

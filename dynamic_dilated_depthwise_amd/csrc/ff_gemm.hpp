@@ -1,0 +1,445 @@
+// ff_gemm.hpp -- the tiled matrix product of the feed-forward operators, forward and backward:
+//
+//   out[q][p] = sum over k of P(p, k) Q(q, k)
+//
+// p runs along the output's rows in memory, q over its rows.  Each operand lies in memory either
+// with its contraction along its rows (kAlong: element [index][k]) or down its columns (kDown:
+// element [k][index]), so one kernel serves
+//   y = x W^T          P = W along,  Q = x along
+//   grad_x = dz W      P = W down,   Q = dz along
+//   grad_W = dz^T x    P = x down,   Q = dz down
+//
+// A step of the contraction is 128 bytes of it (64 bfloat16 or 32 float32).  A step's tile of an
+// operand is TILE * 128 bytes of LDS in 16-byte chunks, placed by an exclusive or of the chunk's
+// number with bits of its row, so that the fragment reads of a wave spread over the banks.  Two
+// steps' tiles are held: one is computed while the next one arrives.
+//   DIRECT   the chunks go straight from memory to LDS (no registers, nothing to wait for but the
+//            step's end); needs 16-byte aligned rows and whole chunks.  Chunks outside the
+//            operand are asked for past the buffer's end, which reads zero.
+//   else     through registers, any alignment and any size, element by element at the ends.
+// Rows and columns outside the operands are zero in LDS, so that nothing that is not finite in one
+// row of x reaches another's output.
+#pragma once
+
+#include "ff_launch.hpp"
+#include "seq_common.hpp"
+
+namespace ddpm {
+namespace ff {
+
+using namespace ddpm::seq;
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+enum Side { kAlong, kDown };
+enum Epi { kStore, kLinear, kGated, kWeight };
+
+constexpr int kStepBytes = 128;
+template <typename T> constexpr int kStep = kStepBytes / (int)sizeof(T);  // elements of a step
+
+constexpr uint32_t kRecords = 0x7fffffe0u, kOutside = 0x7ffffff0u;  // of a buffer; an offset past it
+
+// All but N of this wave's loads to LDS are there and its own LDS accesses done; then the workgroup.
+__device__ __forceinline__ void arrive_all() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+__device__ __forceinline__ void arrive_lds() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// The bits that a row's chunk numbers are placed by.  kAlong: eight rows read at one chunk.  kDown,
+// bfloat16: the transposing reads take four rows of 32 bytes in each of two lane groups, eight rows
+// 0..3 and 8..11 (or 16 more, 4 more); float32: rows 8 apart, 64 bytes of each.
+template <typename T, Side S, int CH>
+__device__ __forceinline__ int swizzle(int row) {
+    if constexpr (S == kAlong) return row & 7;
+    else if constexpr (!Elem<T>::is_bf16) return (row >> 3 & 3) << 2;
+    else if constexpr (CH >= 16) return ((row & 3) | (row >> 3 & 1) << 2) << 1;
+    else return ((row >> 1 & 1) | (row >> 3 & 1) << 1) << 1;
+}
+
+// Rows of P in the gated product: 16 of the gate's, then the same 16 of the other half.
+__device__ __forceinline__ int64_t gated_row(int64_t r, int64_t N) { return (r >> 5 << 4) + (r & 15) + (r & 16 ? N : 0); }
+
+// One operand's tile: TILE indices from `first` of `extent`, contraction from k0.
+template <typename T, Side S, int TILE, int THREADS, bool DIRECT, bool GATED>
+struct Tile {
+    static constexpr int kPer = kVec<T>, kCh = S == kAlong ? 8 : TILE / kPer;
+    static constexpr int kCount = TILE * 8 / THREADS;
+    static_assert(TILE * 8 % THREADS == 0, "whole rounds of chunks");
+    const T *p;
+    int64_t ld, first, extent, k;  // extent: of the index (gated: columns of the result)
+    uint32_t off[DIRECT ? kCount : 1];
+    u32x4 r[DIRECT ? 1 : kCount];
+
+    __device__ __forceinline__ static int row_of(int i, int tid) { return (i * THREADS + tid) / kCh; }
+    __device__ __forceinline__ static int chunk_of(int i, int tid) {
+        return (i * THREADS + tid) % kCh ^ swizzle<T, S, kCh>(row_of(i, tid));
+    }
+    __device__ __forceinline__ void start(const void *base, int64_t ld_, int64_t first_, int64_t extent_, int64_t k0, int tid) {
+        p = (const T *)base;
+        ld = ld_;
+        first = first_;
+        extent = extent_;
+        k = k0;
+        if constexpr (DIRECT) {
+#pragma unroll
+            for (int i = 0; i < kCount; ++i) {
+                const int row = row_of(i, tid), c = chunk_of(i, tid);
+                if constexpr (S == kAlong) {
+                    const bool on = GATED ? (first >> 1) + (row >> 5 << 4) + (row & 15) < extent : first + row < extent;
+                    const int64_t at = GATED ? gated_row(row, extent) : row;
+                    off[i] = on ? (uint32_t)(at * ld * sizeof(T)) + c * 16 : kOutside;
+                } else {
+                    off[i] = first + c * kPer < extent ? (uint32_t)(row * ld * sizeof(T)) + c * 16 : kOutside;
+                }
+            }
+            p += S == kAlong ? (GATED ? first >> 1 : first) * ld + k : k * ld + first;
+        }
+    }
+    // The tile of the next step, of which `left` elements of the contraction are there.
+    __device__ __forceinline__ void ask(char *lds, int64_t left, int tid) {
+        if constexpr (DIRECT) {
+            const __amdgpu_buffer_rsrc_t b = __builtin_amdgcn_make_buffer_rsrc(const_cast<T *>(p), 0, (int)kRecords, 0x00020000);
+            char *at = lds + wave_of(tid) * (kWave * 16);
+#pragma unroll
+            for (int i = 0; i < kCount; ++i) {
+                uint32_t o = off[i];
+                if (left < kStep<T>) {
+                    const bool on = S == kAlong ? chunk_of(i, tid) * kPer < left : row_of(i, tid) < left;
+                    o = on ? o : kOutside;
+                }
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void *)(at + i * THREADS * 16), 16, o, 0, 0, 0);
+            }
+            p += S == kAlong ? kStep<T> : kStep<T> * ld;
+        } else {
+#pragma unroll
+            for (int i = 0; i < kCount; ++i) {
+                const int row = row_of(i, tid), c = chunk_of(i, tid) * kPer;
+                if constexpr (S == kAlong) {
+                    const int64_t f = GATED ? (first >> 1) + (row >> 5 << 4) + (row & 15) : first + row;
+                    const bool on = f < extent;
+                    const int64_t at = GATED ? (first >> 1) + gated_row(row, extent) : f;
+                    r[i] = load_vec<T>(p + (on ? at * ld + k + c : 0), on ? left - c : 0);
+                } else {
+                    const bool on = row < left;
+                    r[i] = load_vec<T>(p + (on ? (k + row) * ld + first + c : 0), on ? extent - first - c : 0);
+                }
+            }
+            k += kStep<T>;
+        }
+    }
+    __device__ __forceinline__ void put(char *lds, int tid) const {
+        if constexpr (!DIRECT) {
+#pragma unroll
+            for (int i = 0; i < kCount; ++i) *(u32x4 *)(lds + (i * THREADS + tid) * 16) = r[i];
+        }
+    }
+};
+
+// Fragments: slot e of lane group g stands for contraction index 8 g + e of a run of 32.
+template <typename T, Side S, int TILE>
+struct Reader {
+    static constexpr int kCh = S == kAlong ? 8 : TILE / kVec<T>, kRow = kCh * 16;
+    uint32_t base;
+    __device__ __forceinline__ void start(int lane) {
+        const int l16 = lane % 16, g = lane / 16;
+        if constexpr (S == kAlong) {
+            base = l16 * kRow + (((Elem<T>::is_bf16 ? g : 2 * g) ^ (l16 & 7)) << 4);
+        } else if constexpr (Elem<T>::is_bf16) {
+            const int k = 8 * g + l16 / 4;
+            base = k * kRow + ((swizzle<T, S, kCh>(k) | (l16 % 4) / 2) << 4) + (l16 & 1) * 8;
+        } else {
+            const int k = 8 * g;
+            base = k * kRow + ((swizzle<T, S, kCh>(k) | l16 / 4) << 4) + (l16 % 4) * 4;
+        }
+    }
+    // Of the 16 indices from 16 * t, run s of the step.
+    __device__ __forceinline__ Frag<T> get(const char *lds, int t, int s) const {
+        if constexpr (S == kAlong && Elem<T>::is_bf16) {
+            return *(const bf16x8 *)(lds + t * (16 * kRow) + (base ^ s * 64));
+        } else if constexpr (S == kAlong) {
+            FragF f;
+            const f32x4 a = *(const f32x4 *)(lds + t * (16 * kRow) + base), b = *(const f32x4 *)(lds + t * (16 * kRow) + (base ^ 16));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) { f.v[e] = a[e]; f.v[4 + e] = b[e]; }
+            return f;
+        } else if constexpr (Elem<T>::is_bf16) {
+            typedef __attribute__((address_space(3))) s16x4 *lds_ptr;
+            const char *at = lds + (base ^ t * 32) + s * (32 * kRow);
+            const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)at);
+            const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(at + 4 * kRow));
+            u16x8 r;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) { r[e] = (uint16_t)a[e]; r[4 + e] = (uint16_t)b[e]; }
+            return __builtin_bit_cast(bf16x8, r);
+        } else {
+            FragF f;
+            const char *at = lds + (base ^ t * 64);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f.v[e] = *(const float *)(at + e * kRow);
+            return f;
+        }
+    }
+};
+
+template <typename T> __device__ __forceinline__ Frag<T> ones() {
+    Frag<T> f;
+    if constexpr (Elem<T>::is_bf16) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = (__bf16)1.f;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f.v[e] = 1.f;
+    }
+    return f;
+}
+
+// Eight neighbouring elements: of a vector in memory (element-aligned), the first n of them.
+template <typename T>
+__device__ __forceinline__ void read8(const T *p, int64_t n, float (&v)[8]) {
+    if constexpr (Elem<T>::is_bf16) {
+        widen<T>(load_vec<T>(p, n), v);
+    } else {
+        float a[4], b[4];
+        widen<T>(load_vec<T>(p, n), a);
+        widen<T>(load_vec<T>(p + (n > 4 ? 4 : 0), n - 4), b);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) { v[e] = a[e]; v[4 + e] = b[e]; }
+    }
+}
+template <typename T>
+__device__ __forceinline__ void write8(T *p, int64_t n, const float (&v)[8]) {
+    if (n >= 8) {
+        u32x4 w[sizeof(T) / 2];
+        if constexpr (Elem<T>::is_bf16) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[0][e] = (uint32_t)f32_to_bf16_bits(v[2 * e]) | (uint32_t)f32_to_bf16_bits(v[2 * e + 1]) << 16;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e / 4][e % 4] = __float_as_uint(v[e]);
+        }
+#pragma unroll
+        for (int h = 0; h < (int)sizeof(T) / 2; ++h) *(u32x4_a2 *)(p + h * kVec<T>) = w[h];
+    } else {
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+            if (e < n) p[e] = Elem<T>::from_f32(v[e]);
+    }
+}
+
+template <int ACT> __device__ __forceinline__ float curve_of(float z) {
+    if constexpr (ACT == DDPM_ACT_RELU) return z < 0.f ? 0.f : z;  // NaN stays
+    else if constexpr (ACT == DDPM_ACT_SILU) return z / (1.f + expf(-z));
+    else if constexpr (ACT == DDPM_ACT_GELU) return 0.5f * z * erfcf(-0.70710678118654752f * z);  // no cancellation below zero
+    else return z;
+}
+// v = act(v), the choice outside the loop.
+__device__ __forceinline__ void activate(float (&v)[8], int act) {
+    if (act == DDPM_ACT_RELU) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = curve_of<DDPM_ACT_RELU>(v[e]);
+    } else if (act == DDPM_ACT_SILU) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = curve_of<DDPM_ACT_SILU>(v[e]);
+    } else if (act == DDPM_ACT_GELU) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = curve_of<DDPM_ACT_GELU>(v[e]);
+    }
+}
+
+// What follows the product for eight neighbouring columns p of row q: z without its bias.
+template <typename T>
+__device__ __forceinline__ void finish_linear(const Product &a, int64_t q, int64_t p, float (&z)[8], const float (&bias)[8]) {
+    const int64_t n = a.np - p;
+    if (q >= a.nq || n <= 0) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] += bias[e];
+    if (a.saved != nullptr) write8<float>(a.saved + q * a.np + p, n, z);
+    activate(z, a.act);
+    if (a.residual != nullptr) {
+        float r[8];
+        read8<T>((const T *)a.residual + q * a.residual_ld + p, n, r);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[e] += r[e];
+    }
+    write8<T>((T *)a.out + q * a.np + p, n, z);
+}
+// Of the gated product: columns p of the gate's half and of the other's.
+template <typename T>
+__device__ __forceinline__ void finish_gated(const Product &a, int64_t q, int64_t p, float (&g)[8], float (&u)[8],
+                                             const float (&gb)[8], const float (&ub)[8]) {
+    const int64_t n = a.np - p;
+    if (q >= a.nq || n <= 0) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) { g[e] += gb[e]; u[e] += ub[e]; }
+    if (a.saved != nullptr) {
+        float *s = a.saved + q * 2 * a.np + p;
+        write8<float>(s, n, g);
+        write8<float>(s + a.np, n, u);
+    }
+    activate(g, a.act);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[e] *= u[e];
+    write8<T>((T *)a.out + q * a.np + p, n, g);
+}
+template <typename T>
+__device__ __forceinline__ void bias8(const Product &a, int64_t p, float (&v)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    if (a.bias != nullptr && p < a.np) read8<T>((const T *)a.bias + p, a.np - p, v);
+}
+
+// WP * WQ waves of 16 MP by 16 NQ each.
+template <typename T, Side SP, Side SQ, Epi E, int WP, int WQ, int MP, int NQ, bool DIRECT>
+struct Gemm {
+    static constexpr int kThreads = WP * WQ * kWave, kP = WP * MP * 16, kQ = WQ * NQ * 16;
+    static constexpr int kStageBytes = (kP + kQ) * kStepBytes;
+    static constexpr int kLd = 16 * MP + 4;  // floats of a row of the result in LDS
+    static constexpr int kOutBytes = WP * WQ * 16 * kLd * 4;
+    static constexpr int kLds = 2 * kStageBytes > kOutBytes ? 2 * kStageBytes : kOutBytes;
+
+    __device__ static void run(const Product &a, char *lds) {
+        const int tid = threadIdx.x, wave = wave_of(tid), lane = tid % kWave;
+        const int wp = wave % WP, wq = wave / WP;
+        uint32_t id = xcd_contiguous((int)blockIdx.x, (int)gridDim.x);
+        const uint32_t tiles = a.tiles_p * a.tiles_q, split = id / tiles;
+        id -= split * tiles;
+        // neighbouring workgroups take eight tiles of q for each tile of p, so that both stay in the L2
+        constexpr uint32_t kBand = 8;
+        const uint32_t band = id / (kBand * a.tiles_p), in_band = id - band * kBand * a.tiles_p;
+        const uint32_t rows = a.tiles_q - band * kBand < kBand ? a.tiles_q - band * kBand : kBand;
+        const int64_t q0 = (int64_t)(band * kBand + in_band % rows) * kQ, p0 = (int64_t)(in_band / rows) * kP;
+        const int64_t k0 = split * a.run, k1 = k0 + a.run < a.nk ? k0 + a.run : a.nk;
+
+        Tile<T, SP, kP, kThreads, DIRECT, E == kGated> tile_p;
+        Tile<T, SQ, kQ, kThreads, DIRECT, false> tile_q;
+        tile_p.start(a.p, a.p_ld, p0, a.np, k0, tid);
+        tile_q.start(a.q, a.q_ld, q0, a.nq, k0, tid);
+        Reader<T, SP, kP> read_p;
+        Reader<T, SQ, kQ> read_q;
+        read_p.start(lane);
+        read_q.start(lane);
+
+        f32x4 acc[MP][NQ], sum[E == kWeight ? NQ : 1];
+#pragma unroll
+        for (int i = 0; i < MP; ++i)
+#pragma unroll
+            for (int j = 0; j < NQ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < (E == kWeight ? NQ : 1); ++j) sum[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const bool sums = E == kWeight && p0 == 0 && wp == 0;
+
+        const auto compute = [&](const char *at) {
+#pragma unroll
+            for (int s = 0; s < kStep<T> / 32; ++s) {
+                Frag<T> fq[NQ];
+#pragma unroll
+                for (int j = 0; j < NQ; ++j) fq[j] = read_q.get(at + kP * kStepBytes, wq * NQ + j, s);
+                if (sums) {
+#pragma unroll
+                    for (int j = 0; j < NQ; ++j) sum[E == kWeight ? j : 0] = mma(ones<T>(), fq[j], sum[E == kWeight ? j : 0]);
+                }
+#pragma unroll
+                for (int i = 0; i < MP; ++i) {
+                    const Frag<T> fp = read_p.get(at, wp * MP + i, s);
+#pragma unroll
+                    for (int j = 0; j < NQ; ++j) acc[i][j] = mma(fp, fq[j], acc[i][j]);
+                }
+            }
+        };
+
+        const int steps = (int)((k1 - k0 + kStep<T> - 1) / kStep<T>);
+        int64_t left = k1 - k0;
+        tile_p.ask(lds, left, tid);
+        tile_q.ask(lds + kP * kStepBytes, left, tid);
+        for (int s = 0; s < steps; ++s) {
+            char *now = lds + (s & 1) * kStageBytes, *next = lds + (~s & 1) * kStageBytes;
+            left -= kStep<T>;
+            if constexpr (DIRECT) {
+                arrive_all();  // the step is there, and nobody reads the other half any more
+                if (s + 1 < steps) {
+                    tile_p.ask(next, left, tid);
+                    tile_q.ask(next + kP * kStepBytes, left, tid);
+                }
+            } else {
+                tile_p.put(now, tid);
+                tile_q.put(now + kP * kStepBytes, tid);
+                arrive_lds();
+                if (s + 1 < steps) {
+                    tile_p.ask(next, left, tid);
+                    tile_q.ask(next + kP * kStepBytes, left, tid);
+                }
+            }
+            compute(now);
+        }
+        arrive_lds();
+
+        // Out through LDS, 16 rows of the wave's at a time, so that a lane has eight neighbouring columns
+        // (the same ones in every row) and rows leave in whole runs.
+        float *mine = (float *)lds + wave * 16 * kLd;
+        constexpr bool kPair = E == kGated;
+        constexpr int kPerRow = kPair ? MP : 2 * MP, kRows = kWave / kPerRow;  // lanes of a row, rows at a time
+        const int c = lane % kPerRow, r0 = lane / kPerRow;
+        const int at = kPair ? (c >> 1) * 32 + (c & 1) * 8 : c * 8;
+        const int64_t p = kPair ? (p0 >> 1) + wp * MP * 8 + c * 8 : p0 + wp * MP * 16 + c * 8;
+        float b0[8], b1[8];
+        if (E == kLinear || E == kGated) bias8<T>(a, p, b0);
+        if constexpr (E == kGated) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) b1[e] = 0.f;
+            if (a.bias != nullptr && p < a.np) read8<T>((const T *)a.bias + a.np + p, a.np - p, b1);
+        }
+        const int64_t cols = kPair ? 2 * a.np : a.np;
+        float *part = a.part != nullptr ? a.part + split * a.part_stride : nullptr;
+#pragma unroll
+        for (int j = 0; j < NQ; ++j) {
+#pragma unroll
+            for (int i = 0; i < MP; ++i) *(f32x4 *)(mine + (lane % 16) * kLd + 16 * i + 4 * (lane / 16)) = acc[i][j];
+            const int64_t q = q0 + (wq * NQ + j) * 16;
+#pragma unroll
+            for (int r = r0; r < 16; r += kRows) {
+                float v[8], w[8];
+                const f32x4 x0 = *(const f32x4 *)(mine + r * kLd + at), x1 = *(const f32x4 *)(mine + r * kLd + at + 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) { v[e] = x0[e]; v[4 + e] = x1[e]; }
+                if constexpr (kPair) {
+                    const f32x4 y0 = *(const f32x4 *)(mine + r * kLd + at + 16), y1 = *(const f32x4 *)(mine + r * kLd + at + 20);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) { w[e] = y0[e]; w[4 + e] = y1[e]; }
+                }
+                if (part != nullptr) {
+                    if (q + r < a.nq && p < a.np) {
+                        write8<float>(part + (q + r) * cols + p, a.np - p, v);
+                        if constexpr (kPair) write8<float>(part + (q + r) * cols + a.np + p, a.np - p, w);
+                    }
+                } else if constexpr (E == kLinear) {
+                    finish_linear<T>(a, q + r, p, v, b0);
+                } else if constexpr (E == kGated) {
+                    finish_gated<T>(a, q + r, p, v, w, b0, b1);
+                } else {
+                    if (q + r < a.nq && p < a.np) write8<T>((T *)a.out + (q + r) * a.np + p, a.np - p, v);
+                }
+            }
+        }
+        if constexpr (E == kWeight) {  // every row of `sum` holds the sums over k of Q
+            if (sums && lane < 16) {
+#pragma unroll
+                for (int j = 0; j < NQ; ++j) {
+                    const int64_t q = q0 + (wq * NQ + j) * 16 + lane;
+                    if (q < a.nq) {
+                        if (part != nullptr) part[a.nq * a.np + q] = sum[j][0];
+                        else ((T *)a.sums)[q] = Elem<T>::from_f32(sum[j][0]);
+                    }
+                }
+            }
+        }
+    }
+};
+
+template <typename G>
+__global__ __launch_bounds__(G::kThreads, 2) void gemm_kernel(const Product a) {
+    __shared__ __attribute__((aligned(16))) char lds[G::kLds];
+    G::run(a, lds);
+}
+
+}  // namespace ff
+}  // namespace ddpm

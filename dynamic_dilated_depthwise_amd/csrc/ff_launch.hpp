@@ -1,0 +1,44 @@
+// ff_launch.hpp -- kernel launchers of the feed-forward operators.  They check nothing but grid
+// limits (hipErrorInvalidConfiguration); arguments are validated in ff_abi.hip.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/ddpm_ff.h"
+
+namespace ddpm {
+namespace ff {
+
+// out[q][p] = sum over k < nk of P(p, k) Q(q, k), out [nq, np] contiguous; the gated product has np
+// columns and 2 np rows of P.  Strides in elements.
+struct Product {
+    const void *p, *q;
+    int64_t p_ld, q_ld, np, nq, nk;
+    void *out;
+    void *sums;                         // weight's gradient: [nq], sums over k of Q
+    float *saved;                       // forward: what the activation is applied to, or null
+    const void *bias, *residual;        // forward: or null
+    int64_t residual_ld;
+    int act;
+    float *part;                        // with several splits: their results, part_stride floats each
+    int64_t part_stride, run;           // run: elements of the contraction of a split
+    uint32_t tiles_p, tiles_q;
+};
+
+enum Kind { kForward, kGatedForward, kGradX, kGradWeight };
+
+// Floats that launch_product needs at `part` (for these sizes, any strides).
+int64_t product_floats(Kind kind, int64_t np, int64_t nq, int64_t nk, bool bf16);
+hipError_t launch_product(Kind kind, const Product &a, float *part, bool bf16, hipStream_t stream);
+
+// Sums of the splits' results and what follows them.
+hipError_t launch_finish(Kind kind, const Product &a, int splits, bool bf16, hipStream_t stream);
+
+// dz = grad * act'(saved), [rows, N]; gated: saved [rows, 2 N] and dz [rows, 2 N],
+// the gate's half grad * u * act'(g), the other grad * act(g).
+hipError_t launch_dz(bool gated, const void *grad, int64_t grad_ld, const float *saved, void *dz, int64_t rows, int64_t N,
+                     int act, bool bf16, hipStream_t stream);
+
+}  // namespace ff
+}  // namespace ddpm

@@ -1,6 +1,7 @@
-"""A state space mixer over the pixels of a feature map: ``PixelMixer(dim)(x)``.
+"""Blocks over the pixels of a feature map: a state space mixer, ``PixelMixer(dim)(x)``, a gated
+feed-forward, ``PixelFeedForward(dim, hidden)(x)``, and both, ``PixelBlock(dim, hidden)(x)``.
 
-The feature maps that DDPM filters, [N, dim, H, W], mix neighbours by their taps; this module
+The feature maps that DDPM filters, [N, dim, H, W], mix neighbours by their taps; the mixer
 carries information along the whole map.  Its pixels in row order are a sequence of H * W
 tokens of ``dim`` channels:
 
@@ -13,6 +14,12 @@ with the norm, the convolution and the scan from ``sequence`` (HIP kernels, forw
 backward) and the two projections and the gate from torch.  A prompt that arrives in parts,
 or token by token, runs through ``prompt`` and ``step`` with the states of the convolution and
 the scan kept between calls; both give what one call over the whole sequence gives.
+
+The feed-forward mixes the channels of each token by itself, all of it in HIP kernels (``sequence``
+and ``feedforward``), forward and backward:
+
+    h = gated_linear(layer_norm(tokens))       act(gate) * up, hidden channels
+    tokens + h down^T + bias                   the residual in the product's epilogue
 """
 import math
 
@@ -20,9 +27,26 @@ import torch
 import torch.nn as nn
 import torch.nn.functional as F
 
+from . import feedforward as ff
 from . import sequence as seq
 
-__all__ = ["PixelMixer"]
+__all__ = ["PixelMixer", "PixelFeedForward", "PixelBlock"]
+
+
+def _inside(tokens, lengths):
+    """[batch, L, 1] truth values: the tokens [batch, L, dim] before each sequence's length."""
+    if lengths.dtype != torch.int32 or lengths.shape != tokens.shape[:1] or lengths.device != tokens.device:
+        raise ValueError(f"lengths must be int32 of shape ({tokens.shape[0]},) on {tokens.device} (got "
+                         f"{lengths.dtype}, {tuple(lengths.shape)}, {lengths.device})")
+    return (torch.arange(tokens.shape[1], device=tokens.device) < lengths[:, None])[..., None]
+
+
+def _over_map(x, dim, prompt):
+    """prompt over the pixels of a map [N, dim, H, W] in row order."""
+    if x.dim() != 4 or x.shape[1] != dim:
+        raise ValueError(f"x must have shape (N, {dim}, H, W) (got {tuple(x.shape)})")
+    out = prompt(x.flatten(2).transpose(1, 2).contiguous())
+    return out.transpose(1, 2).unflatten(2, x.shape[2:])
 
 
 class PixelMixer(nn.Module):
@@ -86,12 +110,7 @@ class PixelMixer(nn.Module):
         if tokens.dim() != 3 or tokens.shape[2] != self.dim:
             raise ValueError(f"tokens must have shape (batch, length, {self.dim}) (got {tuple(tokens.shape)})")
         first, h = state if state is not None else (None, None)
-        inside = None
-        if lengths is not None:
-            if lengths.dtype != torch.int32 or lengths.shape != tokens.shape[:1] or lengths.device != tokens.device:
-                raise ValueError(f"lengths must be int32 of shape ({tokens.shape[0]},) on {tokens.device} (got "
-                                 f"{lengths.dtype}, {tuple(lengths.shape)}, {lengths.device})")
-            inside = (torch.arange(tokens.shape[1], device=tokens.device) < lengths[:, None])[..., None]
+        inside = _inside(tokens, lengths) if lengths is not None else None
         z, u, raw = self._enter(tokens if inside is None else torch.where(inside, tokens, 0))
         u, last = seq.causal_conv(u, self.conv_weight, self.conv_bias, first, lengths)
         v, B, C = self._per_head(u)
@@ -115,7 +134,70 @@ class PixelMixer(nn.Module):
         return self._leave(tokens, y, z)
 
     def forward(self, x):
-        if x.dim() != 4 or x.shape[1] != self.dim:
-            raise ValueError(f"x must have shape (N, {self.dim}, H, W) (got {tuple(x.shape)})")
-        out, _ = self.prompt(x.flatten(2).transpose(1, 2).contiguous())
-        return out.transpose(1, 2).unflatten(2, x.shape[2:])
+        return _over_map(x, self.dim, lambda tokens: self.prompt(tokens)[0])
+
+
+class PixelFeedForward(nn.Module):
+    """Layer norm, a gated projection to ``hidden`` channels and the projection back, added to its input.
+    float32 or bfloat16, on the GPU.  Under autocast everything runs in the module's type, and so does
+    what comes out."""
+
+    def __init__(self, dim=64, hidden=128, activation="silu", bias=True, eps=1e-5):
+        super().__init__()
+        if activation not in ff.ACTIVATIONS:
+            raise ValueError(f"activation must be one of {', '.join(ff.ACTIVATIONS)} (got {activation!r})")
+        if dim < 1 or hidden < 1:
+            raise ValueError(f"dim and hidden must be at least one (got {dim}, {hidden})")
+        self.dim, self.hidden, self.activation, self.eps = dim, hidden, activation, eps
+        self.norm_weight = nn.Parameter(torch.ones(dim))
+        self.norm_bias = nn.Parameter(torch.zeros(dim))
+        self.up_weight = nn.Parameter((torch.rand(2 * hidden, dim) * 2 - 1) / math.sqrt(dim))  # the gate's rows first
+        self.down_weight = nn.Parameter((torch.rand(dim, hidden) * 2 - 1) / math.sqrt(hidden))
+        self.up_bias = nn.Parameter(torch.zeros(2 * hidden)) if bias else None
+        self.down_bias = nn.Parameter(torch.zeros(dim)) if bias else None
+
+    def tokens(self, tokens, lengths=None):
+        """tokens [..., dim]; with lengths (int32) [batch, L, dim], of which sequence b has lengths[b]:
+        past them out repeats the tokens, which take part in nothing else."""
+        if tokens.dim() < 1 or tokens.shape[-1] != self.dim or lengths is not None and tokens.dim() != 3:
+            raise ValueError(f"tokens must have shape ({'batch, length' if lengths is not None else '...'}, {self.dim}) "
+                             f"(got {tuple(tokens.shape)})")
+        inside = _inside(tokens, lengths) if lengths is not None else None
+        x = tokens if inside is None else torch.where(inside, tokens, 0)
+        if torch.is_autocast_enabled("cuda"):
+            x = x.to(self.norm_weight.dtype)
+        h = seq.layer_norm(x, self.norm_weight, self.norm_bias, self.eps)
+        h = ff.gated_linear(h, self.up_weight, self.up_bias, self.activation)
+        out = ff.linear(h, self.down_weight, self.down_bias, x)
+        return out if inside is None else torch.where(inside, out, tokens.to(out.dtype))
+
+    def forward(self, x):
+        return _over_map(x, self.dim, self.tokens)
+
+
+class PixelBlock(nn.Module):
+    """A PixelMixer, then a PixelFeedForward: maps, prompts in parts and single tokens as the mixer
+    takes them.  mixer: further arguments of PixelMixer."""
+
+    def __init__(self, dim=64, hidden=128, activation="silu", bias=True, eps=1e-5, **mixer):
+        super().__init__()
+        self.dim = dim
+        self.mixer = PixelMixer(dim, eps=eps, **mixer)
+        self.feed_forward = PixelFeedForward(dim, hidden, activation, bias, eps)
+
+    def new_state(self, slots):
+        """The mixer's states of `slots` sequences before their first token."""
+        return self.mixer.new_state(slots)
+
+    def prompt(self, tokens, state=None, lengths=None):
+        """(out, state) as PixelMixer.prompt; past a length out repeats the tokens."""
+        mixed, state = self.mixer.prompt(tokens, state, lengths)
+        return self.feed_forward.tokens(mixed, lengths), state
+
+    @torch.no_grad()
+    def step(self, tokens, state, slots=None):
+        """out [batch, dim] of one token of each sequence, as PixelMixer.step."""
+        return self.feed_forward.tokens(self.mixer.step(tokens, state, slots))
+
+    def forward(self, x):
+        return _over_map(x, self.dim, lambda tokens: self.prompt(tokens)[0])

@@ -1,0 +1,284 @@
+"""The feed-forward operators against their definitions in 64 bits, forward and backward, at the sizes
+where their forms change; views, refusals, streams, graphs, gradients against differences.
+
+Tolerances (ff_oracle.check): one rounding of the output, one of the gradient that an activation's or a
+gate's input takes to the type, and as many float32 roundings as the sums have terms, twice.
+"""
+import pytest
+import torch
+
+import ff_oracle as orc
+from dynamic_dilated_depthwise_amd import feedforward as ff
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def announce(*a):
+    print("[gpu case]", *a, flush=True)
+
+
+def gen_of(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def randn(gen, *shape, dtype=torch.float32, scale=1.0):
+    return (torch.randn(*shape, generator=gen) * scale).to(dtype).cuda()
+
+
+def case(rows, C, N, dtype, gated=False, seed=1):
+    """x, weight, bias, residual (gated: None), grad"""
+    g = gen_of(seed)
+    width = 2 * N if gated else N
+    return (randn(g, rows, C, dtype=dtype), randn(g, width, C, dtype=dtype, scale=C ** -0.5),
+            randn(g, width, dtype=dtype, scale=0.3), None if gated else randn(g, rows, N, dtype=dtype),
+            randn(g, rows, N, dtype=dtype))
+
+
+def forward(x, w, b, r, act, gated, **kw):
+    return ff.gated_linear_fwd(x, w, b, act, **kw) if gated else ff.linear_fwd(x, w, b, r, act, **kw)
+
+
+def backward(grad, x, w, saved, act, gated, **kw):
+    return (ff.gated_linear_bwd if gated else ff.linear_bwd)(grad, x, w, saved, act, **kw)
+
+
+def compare(x, w, b, r, grad, act, gated):
+    dtype, rows, C, width = x.dtype, x.numel() // x.shape[-1], x.shape[-1], w.shape[0]
+    y, saved = forward(x, w, b, r, act, gated, save=True)
+    alone, none = forward(x, w, b, r, act, gated)
+    assert none is None and torch.equal(alone, y)
+    assert (saved is None) == (act == "none" and not gated)
+    gx, gw, gb = backward(grad, x, w, saved, act, gated)
+    want = orc.run(x, w, b, r, act, grad, gated)
+    orc.check(y, want["y"], dtype, "y", 2 * C + 64)
+    orc.check(gx, want["grad_x"], dtype, "grad_x", 2 * (C + width) + 64)
+    orc.check(gw, want["grad_weight"], dtype, "grad_weight", 2 * (C + rows) + 64)
+    orc.check(gb, want["grad_bias"], dtype, "grad_bias", 2 * (C + rows) + 64)
+
+
+# (rows, C, N): one element; sizes below, at and above a step of the contraction, a fragment and a
+# tile; whole chunks (straight to LDS) and others; a few tokens; long contractions with few tiles
+# (split); many tiles
+SIZES = [(1, 1, 1), (2, 3, 5), (1, 64, 16), (1, 129, 70), (3, 8, 8), (7, 72, 24), (16, 64, 64), (17, 65, 33), (33, 128, 96),
+         (48, 200, 136), (65, 56, 130), (100, 257, 31), (130, 136, 264), (128, 128, 128), (129, 127, 129), (300, 64, 128),
+         (5, 2048, 40), (64, 1024, 72), (2100, 40, 48), (1500, 33, 17)]
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("gated", [False, True], ids=["linear", "gated"])
+@pytest.mark.parametrize("rows,C,N", SIZES)
+def test_sizes(rows, C, N, gated, dt):
+    announce("ff sizes", rows, C, N, gated, dt)
+    compare(*case(rows, C, N, DT[dt], gated), "silu" if gated else "none", gated)
+
+
+# Many tiles, so that bfloat16 takes the large ones, for each product of the two passes: y, grad_x, grad_weight.
+@pytest.mark.parametrize("gated", [False, True], ids=["linear", "gated"])
+@pytest.mark.parametrize("rows,C,N", [(3400, 88, 3304), (3333, 2944, 104), (104, 3368, 3400)])
+def test_large_tiles(rows, C, N, gated):
+    announce("ff large tiles", rows, C, N, gated)
+    compare(*case(rows, C, N, torch.bfloat16, gated), "gelu", gated)
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("gated", [False, True], ids=["linear", "gated"])
+@pytest.mark.parametrize("act", ff.ACTIVATIONS)
+def test_activations(act, gated, dt):
+    announce("ff activations", act, gated, dt)
+    x, w, b, r, grad = case(70, 40, 56, DT[dt], gated, seed=3)
+    compare(x, w, b, r, grad, act, gated)
+    compare(x, w, None, None, grad, act, gated)
+
+
+@pytest.mark.parametrize("dt", DT)
+def test_far_values(dt):
+    """Activations far from zero: nothing overflows on the way, small results keep their size."""
+    announce("ff far values", dt)
+    dtype = DT[dt]
+    z = torch.tensor([-1e4, -200., -100., -20., -9., -5., -1., -1e-3, -0., 0., 1e-3, 1., 9., 100., 1e4]).to(dtype)
+    x, w = z[:, None].cuda(), torch.ones(1, 1, dtype=dtype).cuda()
+    for act in ff.ACTIVATIONS:
+        y, saved = ff.linear_fwd(x, w, activation=act, save=True)
+        gx, _, _ = ff.linear_bwd(torch.ones_like(x), x, w, saved, act)
+        a, da = orc.curve(x.double(), act)
+        # the functions' own error: a few roundings of float32, of their argument times the logarithm's slope too
+        tol = (orc.u(dtype) + 16 * orc.u(torch.float32) * (1 + x.double() ** 2))
+        assert bool(((y.double() - a).abs() <= tol * a.abs() + 1e-37).all()), act
+        assert bool(((gx.double() - da).abs() <= tol * da.abs() + 1e-37 + 2.0 ** -22 * da.abs().clamp(max=1)).all()), act
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("gated", [False, True], ids=["linear", "gated"])
+def test_views_and_axes(gated, dt):
+    """Rows of a wider tensor, more axes, one row for all; unaligned starts."""
+    announce("ff views", gated, dt)
+    dtype, act = DT[dt], "silu"
+    x, w, b, r, grad = case(30, 72, 40, dtype, gated)
+    y, saved = forward(x, w, b, r, act, gated, save=True)
+    grads = backward(grad, x, w, saved, act, gated)
+
+    def inside(t, left, right):
+        wide = torch.full((t.shape[0], left + t.shape[1] + right), float("nan"), device="cuda", dtype=dtype)
+        wide[:, left:left + t.shape[1]] = t
+        return wide[:, left:left + t.shape[1]]
+
+    for left, right in ((8, 16), (3, 2)):
+        xv, gv, rv = inside(x, left, right), inside(grad, left, right), inside(r, left, right) if r is not None else None
+        y2, saved2 = forward(xv, w, b, rv, act, gated, save=True)
+        assert torch.equal(y2, y) and torch.equal(saved2, saved)
+        for p, q in zip(backward(gv, xv, w, saved2, act, gated), grads):
+            assert torch.equal(p, q)
+    x3, r3 = x.view(2, 3, 5, 72), r.view(2, 3, 5, 40) if r is not None else None
+    y3, saved3 = forward(x3, w, b, r3, act, gated, save=True)
+    assert y3.shape == (2, 3, 5, 40) and torch.equal(y3.view(30, 40), y)
+    for p, q in zip(backward(grad.view(2, 3, 5, 40), x3, w, saved3, act, gated), grads):
+        assert torch.equal(p.view(q.shape), q)
+    y4, _ = forward(x[:1].expand(30, 72), w, b, r[:1].expand(30, 40) if r is not None else None, act, gated)
+    assert all(torch.equal(y4[k], y[0]) for k in range(30))
+    one = forward(x[0], w, b, r[0] if r is not None else None, act, gated)[0]
+    assert one.shape == (40,)
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("gated", [False, True], ids=["linear", "gated"])
+@pytest.mark.parametrize("rows,C,N", [(9, 40, 24), (9, 77, 35), (140, 72, 24), (140, 1100, 24)])
+def test_not_finite(rows, C, N, gated, dt):
+    """Infinities and NaN stay in their rows; the gradients of other rows are what they are without them."""
+    announce("ff not finite", rows, C, N, gated, dt)
+    x, w, b, r, grad = case(rows, C, N, DT[dt], gated)
+    y, saved = forward(x, w, b, r, "silu", gated, save=True)
+    gx = backward(grad, x, w, saved, "silu", gated, need_weight=False)[0]
+    bad, bgrad = x.clone(), grad.clone()
+    bad[3, C - 1], bad[5, 0] = float("nan"), float("inf")
+    bgrad[6, N - 1] = float("inf")
+    y2, saved2 = forward(bad, w, b, r, "silu", gated, save=True)
+    gx2, gw2, _ = backward(bgrad, bad, w, saved2, "silu", gated)
+    keep = [k for k in range(rows) if k not in (3, 5, 6)]
+    assert bool(y2[3].isnan().all()) and not bool(y2[5].isfinite().all())
+    assert torch.equal(y2[keep], y[keep]) and torch.equal(gx2[keep], gx[keep])
+    assert not bool(gx2[6].isfinite().all()) and not bool(gw2.isfinite().all())
+
+
+def test_gradients_against_differences():
+    announce("ff differences")
+    for gated in (False, True):
+        x, w, b, r, grad = case(9, 14, 11, torch.float32, gated)
+        for act in ("none", "silu", "gelu"):
+            saved = forward(x, w, b, r, act, gated, save=True)[1]
+            grads = backward(grad, x, w, saved, act, gated)
+            g = gen_of(5)
+            d = [torch.randn(t.shape, generator=g, dtype=torch.float64).cuda() for t in (x, w, b)]
+            h = 1e-6
+
+            def value(s):
+                args = [t.double() + s * h * v for t, v in zip((x, w, b), d)]
+                return (orc.run(*args, r, act, gated=gated)["y"][0] * grad.double()).sum()
+
+            diff = float((value(1) - value(-1)) / (2 * h))
+            got = float(sum((v * q.double()).sum() for v, q in zip(d, grads)))
+            # gradients to a few dozen float32 roundings, differences to h^2 and 1e-16 / h
+            assert abs(diff - got) <= 1e-4 * max(1, abs(diff)), (gated, act)
+
+
+@pytest.mark.parametrize("gated", [False, True], ids=["linear", "gated"])
+def test_autograd(gated):
+    announce("ff autograd", gated)
+    x, w, b, r, grad = case(12, 40, 24, torch.float32, gated)
+    act = "silu"
+    saved = forward(x, w, b, r, act, gated, save=True)[1]
+    want = list(backward(grad, x, w, saved, act, gated)) + ([] if gated else [grad])
+    leaves = [t.clone().requires_grad_() for t in (x, w, b, r) if t is not None]
+    call = (lambda *t: ff.gated_linear(*t, activation=act)) if gated else (lambda *t: ff.linear(*t, activation=act))
+    y = call(*leaves)
+    assert torch.equal(y, forward(x, w, b, r, act, gated)[0])
+    got = torch.autograd.grad(y, leaves, grad)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    for k in range(len(leaves)):  # one of them alone
+        some = [t.detach().requires_grad_(i == k) for i, t in enumerate(leaves)]
+        g, = torch.autograd.grad(call(*some), some[k], grad)
+        assert torch.equal(g, want[k]), k
+    # without gradients, and gradients that are no contiguous rows
+    with torch.no_grad():
+        assert not call(*leaves).requires_grad
+    got = torch.autograd.grad(call(*leaves).sum(), leaves)
+    ones = backward(torch.ones_like(grad), x, w, saved, act, gated)
+    assert all(torch.equal(p, q) for p, q in zip(got, ones))
+    got = torch.autograd.grad(call(*leaves).t(), leaves, grad.t().contiguous())
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    # a broadcast row: its gradient is the sum over where it went
+    one = x[:1].clone().requires_grad_()
+    g1, = torch.autograd.grad(call(one.expand(12, 40), *leaves[1:]), one, grad)
+    xs = x[:1].expand(12, 40)
+    gx = backward(grad, xs, w, forward(xs, w, b, r, act, gated, save=True)[1], act, gated)[0]
+    assert torch.equal(g1, gx.sum(0, keepdim=True))
+    with pytest.raises(RuntimeError):  # once differentiable
+        g, = torch.autograd.grad(call(*leaves), leaves[0], grad, create_graph=True)
+        g.sum().backward()
+
+
+def test_forward_mode_is_refused():
+    announce("ff forward mode")
+    import torch.autograd.forward_ad as fwAD
+    x, w, b, r, _ = case(6, 10, 8, torch.float32)
+    for mode in (torch.enable_grad, torch.no_grad):
+        with mode(), fwAD.dual_level():
+            for call in (lambda: ff.linear(fwAD.make_dual(x, x), w), lambda: ff.linear(x, w, b, fwAD.make_dual(r, r)),
+                         lambda: ff.gated_linear(x, fwAD.make_dual(w, w))):
+                with pytest.raises(RuntimeError, match="jvp|forward"):
+                    call()
+
+
+def test_refusals():
+    announce("ff refusals")
+    x, w, b, r, grad = case(6, 16, 8, torch.float32)
+    w2 = torch.cat([w, w])
+    for call in (lambda: ff.linear_fwd(x, w[:, :8]), lambda: ff.linear_fwd(x, w.t()), lambda: ff.linear_fwd(x, w, b[:4]),
+                 lambda: ff.linear_fwd(x, w, b, r[:4]), lambda: ff.linear_fwd(x, w, b, r.bfloat16()),
+                 lambda: ff.linear_fwd(x.bfloat16(), w), lambda: ff.linear_fwd(x.half(), w.half()),
+                 lambda: ff.linear_fwd(x[:0], w), lambda: ff.linear_fwd(x.t().contiguous().t(), w),
+                 lambda: ff.linear_fwd(x, w[:0]), lambda: ff.linear_fwd(x, w.cpu()), lambda: ff.linear_fwd(x, w, activation="tanh"),
+                 lambda: ff.linear_bwd(grad[:3], x, w), lambda: ff.linear_bwd(grad, x, w, grad),
+                 lambda: ff.linear_bwd(grad, x, w, grad.bfloat16(), "silu"), lambda: ff.gated_linear_fwd(x, w2[:15]),
+                 lambda: ff.gated_linear_fwd(x, w2, b), lambda: ff.gated_linear_bwd(grad, x, w2, grad)):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: ff.linear_fwd(x, w, activation=1), lambda: ff.linear_bwd(grad, x, w, None, "silu"),
+                 lambda: ff.gated_linear_bwd(grad, x, w2, None), lambda: ff.linear_fwd(x, [1.0])):
+        with pytest.raises(TypeError):
+            call()
+
+
+def test_streams_and_graph():
+    """Every entry point on a stream of its own, and captured and replayed among eager work."""
+    announce("ff streams and graph")
+    few, many = case(5, 2048, 264, torch.bfloat16), case(300, 72, 264, torch.bfloat16)
+    gfew, gmany = case(5, 2048, 264, torch.bfloat16, True), case(300, 72, 264, torch.bfloat16, True)
+
+    def step(stream=None):
+        outs = []
+        for args, gated in ((few, False), (many, False), (gfew, True), (gmany, True)):
+            x, w, b, r, grad = args
+            y, saved = forward(x, w, b, r, "gelu", gated, save=True, stream=stream)
+            outs += [y, saved, *backward(grad, x, w, saved, "gelu", gated, stream=stream)]
+        return outs
+
+    eager = [t.clone() for t in step()]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    outs = step(side)
+    side.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(outs, eager))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    junk = torch.randn(256, 256, device="cuda")
+    for _ in range(3):
+        for t in outs:
+            t.fill_(float("nan"))
+        junk = torch.tanh(junk @ junk / 256)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(outs, eager))
