@@ -135,6 +135,68 @@ struct Tile {
     }
 };
 
+// A float32 as three bfloat16 (8 + 8 + 8 bits, the float32 itself down to the subnormals).  Of the nine
+// products of two such numbers the six above 2^-25 of the whole are taken, so that a float32 product
+// costs six bfloat16 matrix instructions (96 cycles where the float32 ones take 256) at float32's
+// precision.  The nearest bfloat16 is taken each time: with bits cut off instead, the terms left out
+// would be four times larger and all of the product's sign.
+constexpr int kParts = 3;
+struct Split {
+    bf16x8 part[kParts];
+};
+template <typename T> struct OperandOf { typedef Split type; };
+template <> struct OperandOf<bf16_t> { typedef bf16x8 type; };
+template <typename T> using Operand = typename OperandOf<T>::type;
+
+__device__ __forceinline__ Split split_of(const f32x4 &a, const f32x4 &b) {
+    Split r;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        float v = e < 4 ? a[e] : b[e - 4];
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) {
+            const __bf16 t = (__bf16)v;
+            r.part[k][e] = t;
+            v -= (float)t;
+        }
+    }
+    return r;
+}
+
+// acc[j] += p q[j], the smallest terms first; neighbouring instructions have different results.
+template <int NQ>
+__device__ __forceinline__ void multiply(f32x4 (&acc)[NQ], const bf16x8 &p, const bf16x8 (&q)[NQ]) {
+#pragma unroll
+    for (int j = 0; j < NQ; ++j) acc[j] = mma(p, q[j], acc[j]);
+}
+template <int NQ>
+__device__ __forceinline__ void multiply(f32x4 (&acc)[NQ], const Split &p, const Split (&q)[NQ]) {
+#pragma unroll
+    for (int order = kParts - 1; order >= 0; --order)
+#pragma unroll
+        for (int k = order; k >= 0; --k)
+#pragma unroll
+            for (int j = 0; j < NQ; ++j) acc[j] = mma(p.part[k], q[j].part[order - k], acc[j]);
+}
+__device__ __forceinline__ bf16x8 ones_frag() {
+    bf16x8 f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = (__bf16)1.f;
+    return f;
+}
+// sum[j] += the sums of q[j] over the contraction, in every row.
+template <int NQ>
+__device__ __forceinline__ void add_up(f32x4 (&sum)[NQ], const bf16x8 (&q)[NQ]) {
+    multiply<NQ>(sum, ones_frag(), q);
+}
+template <int NQ>
+__device__ __forceinline__ void add_up(f32x4 (&sum)[NQ], const Split (&q)[NQ]) {
+#pragma unroll
+    for (int k = kParts - 1; k >= 0; --k)
+#pragma unroll
+        for (int j = 0; j < NQ; ++j) sum[j] = mma(ones_frag(), q[j].part[k], sum[j]);
+}
+
 // Fragments: slot e of lane group g stands for contraction index 8 g + e of a run of 32.
 template <typename T, Side S, int TILE>
 struct Reader {
@@ -153,15 +215,11 @@ struct Reader {
         }
     }
     // Of the 16 indices from 16 * t, run s of the step.
-    __device__ __forceinline__ Frag<T> get(const char *lds, int t, int s) const {
+    __device__ __forceinline__ Operand<T> get(const char *lds, int t, int s) const {
         if constexpr (S == kAlong && Elem<T>::is_bf16) {
             return *(const bf16x8 *)(lds + t * (16 * kRow) + (base ^ s * 64));
         } else if constexpr (S == kAlong) {
-            FragF f;
-            const f32x4 a = *(const f32x4 *)(lds + t * (16 * kRow) + base), b = *(const f32x4 *)(lds + t * (16 * kRow) + (base ^ 16));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) { f.v[e] = a[e]; f.v[4 + e] = b[e]; }
-            return f;
+            return split_of(*(const f32x4 *)(lds + t * (16 * kRow) + base), *(const f32x4 *)(lds + t * (16 * kRow) + (base ^ 16)));
         } else if constexpr (Elem<T>::is_bf16) {
             typedef __attribute__((address_space(3))) s16x4 *lds_ptr;
             const char *at = lds + (base ^ t * 32) + s * (32 * kRow);
@@ -172,26 +230,14 @@ struct Reader {
             for (int e = 0; e < 4; ++e) { r[e] = (uint16_t)a[e]; r[4 + e] = (uint16_t)b[e]; }
             return __builtin_bit_cast(bf16x8, r);
         } else {
-            FragF f;
+            f32x4 a, b;
             const char *at = lds + (base ^ t * 64);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f.v[e] = *(const float *)(at + e * kRow);
-            return f;
+            for (int e = 0; e < 4; ++e) { a[e] = *(const float *)(at + e * kRow); b[e] = *(const float *)(at + (4 + e) * kRow); }
+            return split_of(a, b);
         }
     }
 };
-
-template <typename T> __device__ __forceinline__ Frag<T> ones() {
-    Frag<T> f;
-    if constexpr (Elem<T>::is_bf16) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = (__bf16)1.f;
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f.v[e] = 1.f;
-    }
-    return f;
-}
 
 // Eight neighbouring elements: of a vector in memory (element-aligned), the first n of them.
 template <typename T>
@@ -288,27 +334,51 @@ __device__ __forceinline__ void bias8(const Product &a, int64_t p, float (&v)[8]
     if (a.bias != nullptr && p < a.np) read8<T>((const T *)a.bias + p, a.np - p, v);
 }
 
+template <typename T>
+__device__ __forceinline__ void other_bias8(const Product &a, int64_t p, float (&v)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    if (a.bias != nullptr && p < a.np) read8<T>((const T *)a.bias + a.np + p, a.np - p, v);
+}
+
 // WP * WQ waves of 16 MP by 16 NQ each.
 template <typename T, Side SP, Side SQ, Epi E, int WP, int WQ, int MP, int NQ, bool DIRECT>
 struct Gemm {
+    static constexpr Epi kE = E;
     static constexpr int kThreads = WP * WQ * kWave, kP = WP * MP * 16, kQ = WQ * NQ * 16;
     static constexpr int kStageBytes = (kP + kQ) * kStepBytes;
     static constexpr int kLd = 16 * MP + 4;  // floats of a row of the result in LDS
     static constexpr int kOutBytes = WP * WQ * 16 * kLd * 4;
     static constexpr int kLds = 2 * kStageBytes > kOutBytes ? 2 * kStageBytes : kOutBytes;
 
-    __device__ static void run(const Product &a, char *lds) {
-        const int tid = threadIdx.x, wave = wave_of(tid), lane = tid % kWave;
-        const int wp = wave % WP, wq = wave / WP;
-        uint32_t id = xcd_contiguous((int)blockIdx.x, (int)gridDim.x);
-        const uint32_t tiles = a.tiles_p * a.tiles_q, split = id / tiles;
-        id -= split * tiles;
-        // neighbouring workgroups take eight tiles of q for each tile of p, so that both stay in the L2
+    static constexpr int64_t kSlot = (int64_t)kP * kQ + (E == kWeight ? kQ : 0);  // floats of a piece's result
+
+    // Where tile `id` starts: neighbours take eight tiles of q for each tile of p, so that both stay in the L2.
+    __device__ __forceinline__ static void place(const Product &a, uint32_t id, int64_t &p0, int64_t &q0) {
         constexpr uint32_t kBand = 8;
         const uint32_t band = id / (kBand * a.tiles_p), in_band = id - band * kBand * a.tiles_p;
         const uint32_t rows = a.tiles_q - band * kBand < kBand ? a.tiles_q - band * kBand : kBand;
-        const int64_t q0 = (int64_t)(band * kBand + in_band % rows) * kQ, p0 = (int64_t)(in_band / rows) * kP;
-        const int64_t k0 = split * a.run, k1 = k0 + a.run < a.nk ? k0 + a.run : a.nk;
+        q0 = (int64_t)(band * kBand + in_band % rows) * kQ;
+        p0 = (int64_t)(in_band / rows) * kP;
+    }
+
+    __device__ static void run(const Product &a, char *lds) {
+        const int tid = threadIdx.x, wave = wave_of(tid), lane = tid % kWave;
+        const int wp = wave % WP, wq = wave / WP;
+        // whole tiles first, then the pieces of the last ones, each kind in stretches of an XCD
+        uint32_t tile, piece = 0, slot = 0;
+        if (blockIdx.x < a.whole) {
+            tile = xcd_contiguous((int)blockIdx.x, (int)a.whole);
+        } else {
+            slot = xcd_contiguous((int)(blockIdx.x - a.whole), (int)(gridDim.x - a.whole));
+            const uint32_t cut = a.tiles_p * a.tiles_q - a.whole;
+            piece = slot / cut;
+            tile = a.whole + slot - piece * cut;
+        }
+        int64_t p0, q0;
+        place(a, tile, p0, q0);
+        const int64_t k0 = piece * a.run, k1 = blockIdx.x < a.whole || k0 + a.run > a.nk ? a.nk : k0 + a.run;
+        float *part = blockIdx.x < a.whole ? nullptr : a.part + slot * kSlot;
 
         Tile<T, SP, kP, kThreads, DIRECT, E == kGated> tile_p;
         Tile<T, SQ, kQ, kThreads, DIRECT, false> tile_q;
@@ -331,19 +401,14 @@ struct Gemm {
         const auto compute = [&](const char *at) {
 #pragma unroll
             for (int s = 0; s < kStep<T> / 32; ++s) {
-                Frag<T> fq[NQ];
+                Operand<T> fq[NQ];
 #pragma unroll
                 for (int j = 0; j < NQ; ++j) fq[j] = read_q.get(at + kP * kStepBytes, wq * NQ + j, s);
-                if (sums) {
-#pragma unroll
-                    for (int j = 0; j < NQ; ++j) sum[E == kWeight ? j : 0] = mma(ones<T>(), fq[j], sum[E == kWeight ? j : 0]);
+                if constexpr (E == kWeight) {
+                    if (sums) add_up<NQ>(sum, fq);
                 }
 #pragma unroll
-                for (int i = 0; i < MP; ++i) {
-                    const Frag<T> fp = read_p.get(at, wp * MP + i, s);
-#pragma unroll
-                    for (int j = 0; j < NQ; ++j) acc[i][j] = mma(fp, fq[j], acc[i][j]);
-                }
+                for (int i = 0; i < MP; ++i) multiply<NQ>(acc[i], read_p.get(at, wp * MP + i, s), fq);
             }
         };
 
@@ -383,19 +448,13 @@ struct Gemm {
         const int64_t p = kPair ? (p0 >> 1) + wp * MP * 8 + c * 8 : p0 + wp * MP * 16 + c * 8;
         float b0[8], b1[8];
         if (E == kLinear || E == kGated) bias8<T>(a, p, b0);
-        if constexpr (E == kGated) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) b1[e] = 0.f;
-            if (a.bias != nullptr && p < a.np) read8<T>((const T *)a.bias + a.np + p, a.np - p, b1);
-        }
-        const int64_t cols = kPair ? 2 * a.np : a.np;
-        float *part = a.part != nullptr ? a.part + split * a.part_stride : nullptr;
+        if constexpr (E == kGated) other_bias8<T>(a, p, b1);
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
 #pragma unroll
             for (int i = 0; i < MP; ++i) *(f32x4 *)(mine + (lane % 16) * kLd + 16 * i + 4 * (lane / 16)) = acc[i][j];
             const int64_t q = q0 + (wq * NQ + j) * 16;
-#pragma unroll
+#pragma unroll 1
             for (int r = r0; r < 16; r += kRows) {
                 float v[8], w[8];
                 const f32x4 x0 = *(const f32x4 *)(mine + r * kLd + at), x1 = *(const f32x4 *)(mine + r * kLd + at + 4);
@@ -407,10 +466,9 @@ struct Gemm {
                     for (int e = 0; e < 4; ++e) { w[e] = y0[e]; w[4 + e] = y1[e]; }
                 }
                 if (part != nullptr) {
-                    if (q + r < a.nq && p < a.np) {
-                        write8<float>(part + (q + r) * cols + p, a.np - p, v);
-                        if constexpr (kPair) write8<float>(part + (q + r) * cols + a.np + p, a.np - p, w);
-                    }
+                    float *t = part + ((wq * NQ + j) * 16 + r) * kP + wp * MP * 16 + at;
+                    write8<float>(t, 8, v);
+                    if constexpr (kPair) write8<float>(t + 16, 8, w);
                 } else if constexpr (E == kLinear) {
                     finish_linear<T>(a, q + r, p, v, b0);
                 } else if constexpr (E == kGated) {
@@ -424,16 +482,84 @@ struct Gemm {
             if (sums && lane < 16) {
 #pragma unroll
                 for (int j = 0; j < NQ; ++j) {
-                    const int64_t q = q0 + (wq * NQ + j) * 16 + lane;
-                    if (q < a.nq) {
-                        if (part != nullptr) part[a.nq * a.np + q] = sum[j][0];
-                        else ((T *)a.sums)[q] = Elem<T>::from_f32(sum[j][0]);
-                    }
+                    const int at_q = (wq * NQ + j) * 16 + lane;
+                    if (part != nullptr) part[kP * kQ + at_q] = sum[j][0];
+                    else if (q0 + at_q < a.nq) ((T *)a.sums)[q0 + at_q] = Elem<T>::from_f32(sum[j][0]);
                 }
             }
         }
     }
+
+    // The sums of the pieces of the last tiles and what follows them.  Eight lanes share the pieces of
+    // eight neighbouring columns; their sums are joined in a fixed order.
+    static constexpr int kFinishThreads = 256, kLanes = 8, kItems = kFinishThreads / kLanes;
+    static constexpr int kPerTile = (E == kGated ? kP / 2 : kP) * kQ / 8;
+    static_assert(kPerTile % kItems == 0, "a workgroup stays in one tile");
+    __device__ static void finish(const Product &a, float (*red)[kItems][E == kGated ? 17 : 9]) {
+        constexpr int kCols = (E == kGated ? kP / 2 : kP) / 8, kBlocks = kPerTile / kItems;
+        const uint32_t cut = a.tiles_p * a.tiles_q - a.whole, tile = blockIdx.x / kBlocks;
+        const int item = threadIdx.x % kItems, lane = threadIdx.x / kItems;
+        const int i = (int)(blockIdx.x % kBlocks) * kItems + item, row = i / kCols, c = i % kCols;
+        const int at = E == kGated ? (c >> 1) * 32 + (c & 1) * 8 : c * 8;
+        int64_t p0, q0;
+        place(a, a.whole + tile, p0, q0);
+        float v[8], w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = w[e] = 0.f;
+        for (int s = lane; s < a.pieces; s += kLanes) {
+            const float *t = a.part + ((int64_t)s * cut + tile) * kSlot + row * kP + at;
+            const f32x4 x0 = *(const f32x4 *)t, x1 = *(const f32x4 *)(t + 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) { v[e] += x0[e]; v[4 + e] += x1[e]; }
+            if constexpr (E == kGated) {
+                const f32x4 y0 = *(const f32x4 *)(t + 16), y1 = *(const f32x4 *)(t + 20);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) { w[e] += y0[e]; w[4 + e] += y1[e]; }
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            red[lane][item][e] = v[e];
+            if constexpr (E == kGated) red[lane][item][8 + e] = w[e];
+        }
+        __syncthreads();
+        const int64_t q = q0 + row, p = E == kGated ? (p0 >> 1) + c * 8 : p0 + c * 8;
+        if (lane == 0) {
+#pragma unroll
+            for (int l = 1; l < kLanes; ++l)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    v[e] += red[l][item][e];
+                    if constexpr (E == kGated) w[e] += red[l][item][8 + e];
+                }
+            if constexpr (E == kLinear) {
+                float b[8];
+                bias8<T>(a, p, b);
+                finish_linear<T>(a, q, p, v, b);
+            } else if constexpr (E == kGated) {
+                float g[8], u[8];
+                bias8<T>(a, p, g);
+                other_bias8<T>(a, p, u);
+                finish_gated<T>(a, q, p, v, w, g, u);
+            } else if (q < a.nq && p < a.np) {
+                write8<T>((T *)a.out + q * a.np + p, a.np - p, v);
+            }
+        }
+        if constexpr (E == kWeight) {
+            if (p0 == 0 && c == 0 && lane == 1 && q < a.nq) {
+                float t = 0.f;
+                for (int s = 0; s < a.pieces; ++s) t += a.part[((int64_t)s * cut + tile) * kSlot + kP * kQ + row];
+                ((T *)a.sums)[q] = Elem<T>::from_f32(t);
+            }
+        }
+    }
 };
+
+template <typename G>
+__global__ __launch_bounds__(G::kFinishThreads) void finish_kernel(const Product a) {
+    __shared__ float red[G::kLanes][G::kItems][G::kE == kGated ? 17 : 9];
+    G::finish(a, red);
+}
 
 template <typename G>
 __global__ __launch_bounds__(G::kThreads, 2) void gemm_kernel(const Product a) {

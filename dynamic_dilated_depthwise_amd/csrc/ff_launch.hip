@@ -22,12 +22,12 @@ hipError_t launch_product(Kind kind, const Product &a, float *part, bool bf16, h
 }
 
 int64_t product_floats(Kind kind, int64_t np, int64_t nq, int64_t nk, bool bf16) {
-    int splits = 1;
+    int64_t most = 0;
     for (const bool direct : {false, true}) {
         const Cut c = bf16 ? cut_of<bf16_t>(kind, np, nq, nk, direct) : cut_of<float>(kind, np, nq, nk, direct);
-        splits = std::max(splits, c.splits);
+        most = std::max(most, c.pieces > 1 ? part_floats(kind, c) : 0);
     }
-    return splits > 1 ? splits * part_stride(kind, np, nq) : 0;
+    return most;
 }
 
 }  // namespace ff

@@ -21,19 +21,19 @@ struct Product {
     const void *bias, *residual;        // forward: or null
     int64_t residual_ld;
     int act;
-    float *part;                        // with several splits: their results, part_stride floats each
-    int64_t part_stride, run;           // run: elements of the contraction of a split
-    uint32_t tiles_p, tiles_q;
+    // The first `whole` of tiles_p * tiles_q tiles are a workgroup's each; the others are cut along the
+    // contraction into `pieces` of `run` elements, whose results go to `part` in float32.
+    uint32_t tiles_p, tiles_q, whole;
+    int pieces;
+    int64_t run;
+    float *part;
 };
 
 enum Kind { kForward, kGatedForward, kGradX, kGradWeight };
 
-// Floats that launch_product needs at `part` (for these sizes, any strides).
+// Floats that launch_product needs at `part` (for these sizes, any strides and alignment).
 int64_t product_floats(Kind kind, int64_t np, int64_t nq, int64_t nk, bool bf16);
 hipError_t launch_product(Kind kind, const Product &a, float *part, bool bf16, hipStream_t stream);
-
-// Sums of the splits' results and what follows them.
-hipError_t launch_finish(Kind kind, const Product &a, int splits, bool bf16, hipStream_t stream);
 
 // dz = grad * act'(saved), [rows, N]; gated: saved [rows, 2 N] and dz [rows, 2 N],
 // the gate's half grad * u * act'(g), the other grad * act(g).

@@ -1,6 +1,5 @@
-// ff_point.hip -- what the feed-forward operators do element by element outside the products'
-// kernels: the gradient of an activation's or a gate's input, and the end of a product that was
-// split along its contraction.  Both are bound by memory; a thread takes eight neighbouring columns.
+// ff_point.hip -- the gradient of an activation's or a gate's input, element by element.  Bound by
+// memory; a thread takes eight neighbouring columns.
 #include "ff_gemm.hpp"
 
 namespace ddpm {
@@ -77,64 +76,9 @@ __global__ __launch_bounds__(kThreads) void dz_kernel(const T *__restrict__ grad
     }
 }
 
-__device__ __forceinline__ void add_parts(const float *p, int64_t stride, int splits, int64_t n, float (&v)[8]) {
-    read8<float>(p, n, v);
-    for (int s = 1; s < splits; ++s) {
-        float w[8];
-        read8<float>(p + s * stride, n, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += w[e];
-    }
-}
-
-template <typename T, Kind K>
-__global__ __launch_bounds__(kThreads) void finish_kernel(const Product a, int splits) {
-    const int64_t per = (a.np + 7) / 8, all = a.nq * per, stride = (int64_t)gridDim.x * kThreads;
-    const int64_t cols = K == kGatedForward ? 2 * a.np : a.np;
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < all; i += stride) {
-        const Place at = place_of(i, per);
-        const int64_t n = a.np - at.col;
-        const float *p = a.part + at.row * cols + at.col;
-        float v[8];
-        add_parts(p, a.part_stride, splits, n, v);
-        if constexpr (K == kGatedForward) {
-            float u[8], gb[8], ub[8];
-            add_parts(p + a.np, a.part_stride, splits, n, u);
-            bias8<T>(a, at.col, gb);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ub[e] = 0.f;
-            if (a.bias != nullptr) read8<T>((const T *)a.bias + a.np + at.col, n, ub);
-            finish_gated<T>(a, at.row, at.col, v, u, gb, ub);
-        } else if constexpr (K == kForward) {
-            float b[8];
-            bias8<T>(a, at.col, b);
-            finish_linear<T>(a, at.row, at.col, v, b);
-        } else {
-            write8<T>((T *)a.out + at.row * a.np + at.col, n, v);
-        }
-    }
-    if constexpr (K == kGradWeight) {
-        for (int64_t q = (int64_t)blockIdx.x * kThreads + threadIdx.x; q < a.nq; q += stride) {
-            float t = 0.f;
-            for (int s = 0; s < splits; ++s) t += a.part[s * a.part_stride + a.nq * a.np + q];
-            ((T *)a.sums)[q] = Elem<T>::from_f32(t);
-        }
-    }
-}
-
 unsigned blocks_for(int64_t rows, int64_t N) {
     const int64_t items = rows * ((N + 7) / 8), blocks = (items + kThreads - 1) / kThreads;
     return (unsigned)(blocks < 8192 ? blocks : 8192);
-}
-
-template <typename T>
-hipError_t finish(Kind kind, const Product &a, int splits, hipStream_t stream) {
-    const dim3 grid(blocks_for(a.nq, a.np)), threads(kThreads);
-    if (kind == kForward) hipLaunchKernelGGL((finish_kernel<T, kForward>), grid, threads, 0, stream, a, splits);
-    else if (kind == kGatedForward) hipLaunchKernelGGL((finish_kernel<T, kGatedForward>), grid, threads, 0, stream, a, splits);
-    else if (kind == kGradX) hipLaunchKernelGGL((finish_kernel<T, kGradX>), grid, threads, 0, stream, a, splits);
-    else hipLaunchKernelGGL((finish_kernel<T, kGradWeight>), grid, threads, 0, stream, a, splits);
-    return hipGetLastError();
 }
 
 template <typename T>
@@ -147,10 +91,6 @@ hipError_t dz_of(bool gated, const void *grad, int64_t grad_ld, const float *sav
 }
 
 }  // namespace
-
-hipError_t launch_finish(Kind kind, const Product &a, int splits, bool bf16, hipStream_t stream) {
-    return bf16 ? finish<bf16_t>(kind, a, splits, stream) : finish<float>(kind, a, splits, stream);
-}
 
 hipError_t launch_dz(bool gated, const void *grad, int64_t grad_ld, const float *saved, void *dz, int64_t rows, int64_t N,
                      int act, bool bf16, hipStream_t stream) {

@@ -22,42 +22,96 @@ inline bool direct_ok(Side s, const void *p, int64_t ld, int64_t extent, int64_t
     return (rows * ld + kStep<T>) * (int64_t)sizeof(T) < (int64_t)kRecords;
 }
 
-// How a call is cut: the tile and the runs of the contraction.
-struct Cut {
-    int kp, kq, splits;
-    int64_t run;
+// The tiles that a call may take: waves in p and q, fragments of a wave in p and q, workgroups of a
+// compute unit, and the share of the large tile's rate that it reaches (8192^3: bfloat16 1228 TFLOP/s
+// with tiles of 256 and 750 to 900 with 128).
+struct Form {
+    int wp, wq, mp, nq, per_cu;
+    double rate;
+    int kp() const { return wp * mp * 16; }
+    int kq() const { return wq * nq * 16; }
 };
-template <typename T>
-inline Cut cut_of(Kind kind, int64_t np, int64_t nq, int64_t nk, bool direct) {
-    const int64_t p = kind == kGatedForward ? 2 * np : np, steps = (nk + kStep<T> - 1) / kStep<T>;
-    const auto tiles = [&](int64_t kp, int64_t kq) { return (double)((p + kp - 1) / kp) * (double)((nq + kq - 1) / kq); };
-    Cut c = {128, 128, 1, 0};
-    if (direct && Elem<T>::is_bf16 && tiles(256, 256) >= 160) c.kp = c.kq = 256;
-    const double t = tiles(c.kp, c.kq);
-    // few tiles: the contraction is split until there are two workgroups for each compute unit, but
-    // not into runs of less than 8 steps
-    if (t < 256 && steps >= 16) {
-        int64_t s = (int64_t)(512 / t);
-        if (s > steps / 8) s = steps / 8;
-        if (s > 1) c.splits = (int)s;
+constexpr Form kForms[] = {{2, 4, 8, 4, 1, 1.0},    // 256 x 256, bfloat16 straight to LDS
+                           {2, 2, 4, 4, 2, 0.75},   // 128 x 128
+                           {1, 4, 4, 4, 2, 0.75}};  // 64 x 256, results of few columns
+
+// How a call is cut.  The tiles of the last round of workgroups, which would leave compute units idle,
+// are cut along the contraction into pieces that fill them; the sums of the pieces take a second kernel.
+struct Cut {
+    int form = 0, pieces = 1;
+    int64_t tiles_p = 0, tiles_q = 0, whole = 0, run = 0;
+    double cost = 0.;
+    int64_t slots() const { return (tiles_p * tiles_q - whole) * pieces; }
+};
+constexpr int64_t kUnits = 256;       // compute units
+constexpr int64_t kLeastSteps = 4;    // of a piece: below that its loads are not hidden
+constexpr double kPieceSteps = 6.;    // what a piece's result costs on its way through memory, in steps
+constexpr double kFinishSteps = 4.;   // the second kernel
+
+inline Cut cut_for(int form, int64_t p, int64_t q, int64_t steps) {
+    const Form &f = kForms[form];
+    Cut c;
+    c.form = form;
+    c.tiles_p = (p + f.kp() - 1) / f.kp();
+    c.tiles_q = (q + f.kq() - 1) / f.kq();
+    const double tiles = (double)c.tiles_p * (double)c.tiles_q;
+    const int64_t slots = kUnits * f.per_cu;
+    const double step = f.kp() * f.kq() * f.per_cu / f.rate;  // time of a step, all slots busy
+    if (tiles >= 16. * slots) {  // rounds enough
+        c.whole = (int64_t)(tiles < 4e9 ? tiles : 4e9);
+        c.cost = tiles / slots * steps * step;
+        return c;
     }
-    c.run = (steps + c.splits - 1) / c.splits * kStep<T>;
-    c.splits = (int)((nk + c.run - 1) / c.run);
+    const int64_t n = (int64_t)tiles, rest = n % slots;
+    const double before = (double)(n / slots) * steps;
+    double best = before + (rest ? steps : 0);
+    c.whole = n;
+    for (int s = 2; rest && s <= 256 && (steps + s - 1) / s >= kLeastSteps; ++s) {
+        const int64_t rounds = (rest * s + slots - 1) / slots;
+        const double t = before + rounds * ((double)((steps + s - 1) / s) + kPieceSteps) + kFinishSteps;
+        if (t < best) {
+            best = t;
+            c.pieces = s;
+            c.whole = n - rest;
+        }
+    }
+    c.cost = best * step;
     return c;
 }
 
-inline int64_t part_stride(Kind kind, int64_t np, int64_t nq) {
-    return (kind == kGatedForward ? 2 * np : np) * nq + (kind == kGradWeight ? nq : 0);
+template <typename T>
+inline Cut cut_of(Kind kind, int64_t np, int64_t nq, int64_t nk, bool direct) {
+    const int64_t p = kind == kGatedForward ? 2 * np : np, steps = (nk + kStep<T> - 1) / kStep<T>;
+    Cut best;
+    for (int form = direct && Elem<T>::is_bf16 ? 0 : 1; form < 3; ++form) {
+        const Cut c = cut_for(form, p, nq, steps);
+        if (best.tiles_p == 0 || c.cost < best.cost) best = c;
+    }
+    best.run = (steps + best.pieces - 1) / best.pieces * kStep<T>;
+    best.pieces = (int)((nk + best.run - 1) / best.run);  // none is empty
+    return best;
+}
+
+// Floats of the pieces' results.
+inline int64_t part_floats(Kind kind, const Cut &c) {
+    const int64_t kp = kForms[c.form].kp(), kq = kForms[c.form].kq();
+    return c.slots() * (kp * kq + (kind == kGradWeight ? kq : 0));
 }
 
 template <typename G>
-hipError_t launch_gemm(Product &a, const Cut &c, int64_t p, hipStream_t stream) {
-    const int64_t tp = (p + G::kP - 1) / G::kP, tq = (a.nq + G::kQ - 1) / G::kQ;
-    if ((double)tp * (double)tq * c.splits > 2147483647.) return hipErrorInvalidConfiguration;
-    a.tiles_p = (uint32_t)tp;
-    a.tiles_q = (uint32_t)tq;
+hipError_t launch_gemm(Product &a, const Cut &c, hipStream_t stream) {
+    const double blocks = (double)c.whole + (double)c.slots();
+    if (blocks > 2147483647. || (double)c.tiles_p * (double)c.tiles_q > 2147483647.) return hipErrorInvalidConfiguration;
+    a.tiles_p = (uint32_t)c.tiles_p;
+    a.tiles_q = (uint32_t)c.tiles_q;
+    a.whole = (uint32_t)c.whole;
+    a.pieces = c.pieces;
     a.run = c.run;
-    hipLaunchKernelGGL((gemm_kernel<G>), dim3((unsigned)(tp * tq * c.splits)), dim3(G::kThreads), 0, stream, a);
+    hipLaunchKernelGGL((gemm_kernel<G>), dim3((unsigned)blocks), dim3(G::kThreads), 0, stream, a);
+    const hipError_t r = hipGetLastError();
+    if (r != hipSuccess || c.pieces == 1) return r;
+    const int64_t cut = c.tiles_p * c.tiles_q - c.whole;
+    hipLaunchKernelGGL((finish_kernel<G>), dim3((unsigned)(cut * (G::kPerTile / G::kItems))), dim3(G::kFinishThreads), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -65,25 +119,25 @@ template <typename T, Kind K>
 hipError_t product(Product a, float *part, hipStream_t stream) {
     constexpr Side sp = KindOf<K>::sp, sq = KindOf<K>::sq;
     constexpr Epi e = KindOf<K>::e;
-    const int64_t p = K == kGatedForward ? 2 * a.np : a.np;
     const bool direct = direct_ok<T>(sp, a.p, a.p_ld, a.np, a.nk, K == kGatedForward ? a.np + 256 : 256) &&
                         direct_ok<T>(sq, a.q, a.q_ld, a.nq, a.nk, 256);
     const Cut c = cut_of<T>(K, a.np, a.nq, a.nk, direct);
-    if (c.splits > 1) {
-        a.part = part;
-        a.part_stride = part_stride(K, a.np, a.nq);
-    }
-    hipError_t r;
-    if (!direct) {
-        r = launch_gemm<Gemm<T, sp, sq, e, 2, 2, 4, 4, false>>(a, c, p, stream);
-    } else if (c.kp == 256) {
-        if constexpr (Elem<T>::is_bf16) r = launch_gemm<Gemm<T, sp, sq, e, 2, 4, 8, 4, true>>(a, c, p, stream);
-        else r = hipErrorInvalidConfiguration;
+    a.part = part;
+#define DDPM_FF_FORM(k, DIRECT) \
+    if (c.form == k) \
+        return launch_gemm<Gemm<T, sp, sq, e, kForms[k].wp, kForms[k].wq, kForms[k].mp, kForms[k].nq, DIRECT>>(a, c, stream);
+    if (direct) {
+        if constexpr (Elem<T>::is_bf16) {
+            DDPM_FF_FORM(0, true)
+        }
+        DDPM_FF_FORM(1, true)
+        DDPM_FF_FORM(2, true)
     } else {
-        r = launch_gemm<Gemm<T, sp, sq, e, 2, 2, 4, 4, true>>(a, c, p, stream);
+        DDPM_FF_FORM(1, false)
+        DDPM_FF_FORM(2, false)
     }
-    if (r != hipSuccess || c.splits == 1) return r;
-    return launch_finish(K, a, c.splits, Elem<T>::is_bf16, stream);
+#undef DDPM_FF_FORM
+    return hipErrorInvalidValue;
 }
 
 }  // namespace ff

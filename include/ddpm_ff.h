@@ -14,11 +14,13 @@
  * Streams.  As in ddpm.h: work is enqueued on `stream` and the call returns.  Nothing is cleared
  *   by memset, so every call may be captured into a graph.  No atomics are used: equal inputs
  *   give equal bits.
- * Precision.  Products are summed in float32; bias, activation and residual are applied to that
- *   sum, and outputs are rounded once.  In the backward of an activation or a gate the gradient
+ * Precision.  Products are summed in float32; float32 operands enter the matrix instructions as
+ *   three bfloat16 terms each, six products of them, which is float32's own precision.  Bias,
+ *   activation and residual are applied to that sum, and outputs are rounded once.  In the backward of an activation or a gate the gradient
  *   of its input is rounded to the call's dtype before the two products take it.
  * Not finite.  An infinity or NaN in a row of x or grad reaches that row of y or grad_x, and the
- *   parameters' gradients, as in the formulas.
+ *   parameters' gradients, and no other row; in float32 an infinity (or a value above 3.39e38, the
+ *   largest bfloat16) in an operand of a product gives NaN.
  * Errors.  As in ddpm.h; all arguments are checked before anything is enqueued.
  *     DDPM_ERR_INVALID_ARG  null or misaligned pointers, sizes below 1 or beyond 2^31 - 2^16,
  *                           negative strides, an unknown dtype or activation, overlapping
