@@ -45,6 +45,18 @@ __device__ __forceinline__ void arrive_all() {
 }
 __device__ __forceinline__ void arrive_lds() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
+// 16 bytes a lane from `off` behind `p` (uniform; zeros from kRecords on) to LDS at `at` (uniform) + 16 lane.
+// In assembly, because the compiler takes the builtin for a write to all of LDS and makes the fragment
+// reads behind it wait for it (grad_x 930 -> 570 TFLOP/s with loads between them).  It has no result, so
+// no register is held by a load in flight; arrive_all waits for it.  The compiler keeps nothing in m0; a
+// change of it needs one wait state.
+__device__ __forceinline__ void load_to_lds(const void *p, uint32_t off, char *at) {
+    const uint64_t a = (uint64_t)p;
+    const u32x4 r = {(uint32_t)a, (uint32_t)(a >> 32) & 0xffffu, kRecords, 0x00020000u};
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+                 :: "v"(off), "s"(r), "s"((uint32_t)(uintptr_t)(lds_void *)at));
+}
+
 // The bits that a row's chunk numbers are placed by.  kAlong: eight rows read at one chunk.  kDown,
 // bfloat16: the transposing reads take four rows of 32 bytes in each of two lane groups, eight rows
 // 0..3 and 8..11 (or 16 more, 4 more); float32: rows 8 apart, 64 bytes of each.
@@ -95,43 +107,36 @@ struct Tile {
             p += S == kAlong ? (GATED ? first >> 1 : first) * ld + k : k * ld + first;
         }
     }
-    // The tile of the next step, of which `left` elements of the contraction are there.
-    __device__ __forceinline__ void ask(char *lds, int64_t left, int tid) {
-        if constexpr (DIRECT) {
-            const __amdgpu_buffer_rsrc_t b = __builtin_amdgcn_make_buffer_rsrc(const_cast<T *>(p), 0, (int)kRecords, 0x00020000);
-            char *at = lds + wave_of(tid) * (kWave * 16);
-#pragma unroll
-            for (int i = 0; i < kCount; ++i) {
-                uint32_t o = off[i];
-                if (left < kStep<T>) {
-                    const bool on = S == kAlong ? chunk_of(i, tid) * kPer < left : row_of(i, tid) < left;
-                    o = on ? o : kOutside;
-                }
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void *)(at + i * THREADS * 16), 16, o, 0, 0, 0);
-            }
-            p += S == kAlong ? kStep<T> : kStep<T> * ld;
-        } else {
-#pragma unroll
-            for (int i = 0; i < kCount; ++i) {
-                const int row = row_of(i, tid), c = chunk_of(i, tid) * kPer;
-                if constexpr (S == kAlong) {
-                    const int64_t f = GATED ? (first >> 1) + (row >> 5 << 4) + (row & 15) : first + row;
-                    const bool on = f < extent;
-                    const int64_t at = GATED ? (first >> 1) + gated_row(row, extent) : f;
-                    r[i] = load_vec<T>(p + (on ? at * ld + k + c : 0), on ? left - c : 0);
-                } else {
-                    const bool on = row < left;
-                    r[i] = load_vec<T>(p + (on ? (k + row) * ld + first + c : 0), on ? extent - first - c : 0);
-                }
-            }
-            k += kStep<T>;
+    // Round i of the chunks of the next step, of which `left` elements of the contraction are there, straight to LDS.
+    __device__ __forceinline__ void ask(int i, char *lds, int64_t left, int tid) const {
+        uint32_t o = off[i];
+        if (left < kStep<T>) {
+            const bool on = S == kAlong ? chunk_of(i, tid) * kPer < left : row_of(i, tid) < left;
+            o = on ? o : kOutside;
         }
+        load_to_lds(p, o, lds + (i * THREADS + wave_of(tid) * kWave) * 16);
+    }
+    __device__ __forceinline__ void next() { p += S == kAlong ? kStep<T> : kStep<T> * ld; }
+    // The next step's chunks into registers; put: from there into LDS.
+    __device__ __forceinline__ void fetch(int64_t left, int tid) {
+#pragma unroll
+        for (int i = 0; i < kCount; ++i) {
+            const int row = row_of(i, tid), c = chunk_of(i, tid) * kPer;
+            if constexpr (S == kAlong) {
+                const int64_t f = GATED ? (first >> 1) + (row >> 5 << 4) + (row & 15) : first + row;
+                const bool on = f < extent;
+                const int64_t at = GATED ? (first >> 1) + gated_row(row, extent) : f;
+                r[i] = load_vec<T>(p + (on ? at * ld + k + c : 0), on ? left - c : 0);
+            } else {
+                const bool on = row < left;
+                r[i] = load_vec<T>(p + (on ? (k + row) * ld + first + c : 0), on ? extent - first - c : 0);
+            }
+        }
+        k += kStep<T>;
     }
     __device__ __forceinline__ void put(char *lds, int tid) const {
-        if constexpr (!DIRECT) {
 #pragma unroll
-            for (int i = 0; i < kCount; ++i) *(u32x4 *)(lds + (i * THREADS + tid) * 16) = r[i];
-        }
+        for (int i = 0; i < kCount; ++i) *(u32x4 *)(lds + (i * THREADS + tid) * 16) = r[i];
     }
 };
 
@@ -398,7 +403,9 @@ struct Gemm {
         for (int j = 0; j < (E == kWeight ? NQ : 1); ++j) sum[j] = f32x4{0.f, 0.f, 0.f, 0.f};
         const bool sums = E == kWeight && p0 == 0 && wp == 0;
 
-        const auto compute = [&](const char *at) {
+        // One step; between(n) is called before the n-th of its kBetween runs of matrix instructions.
+        constexpr int kBetween = kStep<T> / 32 * MP;
+        const auto compute = [&](const char *at, auto between) {
 #pragma unroll
             for (int s = 0; s < kStep<T> / 32; ++s) {
                 Operand<T> fq[NQ];
@@ -408,33 +415,54 @@ struct Gemm {
                     if (sums) add_up<NQ>(sum, fq);
                 }
 #pragma unroll
-                for (int i = 0; i < MP; ++i) multiply<NQ>(acc[i], read_p.get(at, wp * MP + i, s), fq);
+                for (int i = 0; i < MP; ++i) {
+                    between(s * MP + i);
+                    multiply<NQ>(acc[i], read_p.get(at, wp * MP + i, s), fq);
+                }
             }
         };
 
         const int steps = (int)((k1 - k0 + kStep<T> - 1) / kStep<T>);
         int64_t left = k1 - k0;
-        tile_p.ask(lds, left, tid);
-        tile_q.ask(lds + kP * kStepBytes, left, tid);
-        for (int s = 0; s < steps; ++s) {
-            char *now = lds + (s & 1) * kStageBytes, *next = lds + (~s & 1) * kStageBytes;
-            left -= kStep<T>;
-            if constexpr (DIRECT) {
+        if constexpr (DIRECT) {
+            constexpr int kP1 = decltype(tile_p)::kCount, kAll = kP1 + decltype(tile_q)::kCount;
+            const auto ask = [&](int i, char *at) {
+                if (i < kP1) tile_p.ask(i, at, left, tid);
+                else tile_q.ask(i - kP1, at + kP * kStepBytes, left, tid);
+            };
+#pragma unroll
+            for (int i = 0; i < kAll; ++i) ask(i, lds);
+            for (int s = 0; s < steps; ++s) {
+                char *now = lds + (s & 1) * kStageBytes, *next = lds + (~s & 1) * kStageBytes;
+                left -= kStep<T>;
+                tile_p.next();
+                tile_q.next();
                 arrive_all();  // the step is there, and nobody reads the other half any more
-                if (s + 1 < steps) {
-                    tile_p.ask(next, left, tid);
-                    tile_q.ask(next + kP * kStepBytes, left, tid);
-                }
-            } else {
+                // The next step's chunks are asked for a few at a time: all of them at once would hold the
+                // wave up at its first read (gated 16384 x 2048 x 2 5632: see below).
+                compute(now, [&](int n) {
+                    constexpr int kEach = (kAll + kBetween - 1) / kBetween;
+                    if (s + 1 < steps) {
+#pragma unroll
+                        for (int i = n * kEach; i < (n + 1) * kEach && i < kAll; ++i) ask(i, next);
+                    }
+                });
+            }
+        } else {
+            tile_p.fetch(left, tid);
+            tile_q.fetch(left, tid);
+            for (int s = 0; s < steps; ++s) {
+                char *now = lds + (s & 1) * kStageBytes;
+                left -= kStep<T>;
                 tile_p.put(now, tid);
                 tile_q.put(now + kP * kStepBytes, tid);
                 arrive_lds();
                 if (s + 1 < steps) {
-                    tile_p.ask(next, left, tid);
-                    tile_q.ask(next + kP * kStepBytes, left, tid);
+                    tile_p.fetch(left, tid);
+                    tile_q.fetch(left, tid);
                 }
+                compute(now, [](int) {});
             }
-            compute(now);
         }
         arrive_lds();
 
@@ -490,24 +518,29 @@ struct Gemm {
         }
     }
 
-    // The sums of the pieces of the last tiles and what follows them.  Eight lanes share the pieces of
+    // The sums of the pieces of the last tiles and what follows them.  A few lanes share the pieces of
     // eight neighbouring columns; their sums are joined in a fixed order.
-    static constexpr int kFinishThreads = 256, kLanes = 8, kItems = kFinishThreads / kLanes;
+    static constexpr int kFinishThreads = 256, kReds = E == kGated ? 17 : 9;
     static constexpr int kPerTile = (E == kGated ? kP / 2 : kP) * kQ / 8;
-    static_assert(kPerTile % kItems == 0, "a workgroup stays in one tile");
-    __device__ static void finish(const Product &a, float (*red)[kItems][E == kGated ? 17 : 9]) {
-        constexpr int kCols = (E == kGated ? kP / 2 : kP) / 8, kBlocks = kPerTile / kItems;
-        const uint32_t cut = a.tiles_p * a.tiles_q - a.whole, tile = blockIdx.x / kBlocks;
-        const int item = threadIdx.x % kItems, lane = threadIdx.x / kItems;
-        const int i = (int)(blockIdx.x % kBlocks) * kItems + item, row = i / kCols, c = i % kCols;
+    static_assert(kPerTile % kFinishThreads == 0, "a workgroup stays in one tile");
+    __host__ __device__ static int lanes(int pieces) { return pieces >= 16 ? 8 : pieces >= 4 ? 2 : 1; }
+    __device__ static void finish(const Product &a, float (*red)[kReds]) {
+        constexpr int kCols = (E == kGated ? kP / 2 : kP) / 8;
+        const int kLanes = lanes(a.pieces), items = kFinishThreads / kLanes;
+        const uint32_t cut = a.tiles_p * a.tiles_q - a.whole, blocks = kPerTile / items, tile = blockIdx.x / blocks;
+        const int item = threadIdx.x % items, lane = threadIdx.x / items;
+        const int i = (int)(blockIdx.x - tile * blocks) * items + item, row = i / kCols, c = i % kCols;
         const int at = E == kGated ? (c >> 1) * 32 + (c & 1) * 8 : c * 8;
         int64_t p0, q0;
         place(a, a.whole + tile, p0, q0);
-        float v[8], w[8];
+        float v[8], w[8], sum = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = w[e] = 0.f;
-        for (int s = lane; s < a.pieces; s += kLanes) {
-            const float *t = a.part + ((int64_t)s * cut + tile) * kSlot + row * kP + at;
+        const bool sums = E == kWeight && p0 == 0 && c == 0;
+        const float *t = a.part + ((int64_t)lane * cut + tile) * kSlot + row * kP + at;
+        const int64_t far = (int64_t)kLanes * cut * kSlot;
+#pragma unroll 4
+        for (int s = lane; s < a.pieces; s += kLanes, t += far) {
             const f32x4 x0 = *(const f32x4 *)t, x1 = *(const f32x4 *)(t + 4);
 #pragma unroll
             for (int e = 0; e < 4; ++e) { v[e] += x0[e]; v[4 + e] += x1[e]; }
@@ -516,22 +549,27 @@ struct Gemm {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) { w[e] += y0[e]; w[4 + e] += y1[e]; }
             }
+            if (E == kWeight && sums) sum += t[kP * kQ + row - (row * kP + at)];
         }
+        if (kLanes > 1) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            red[lane][item][e] = v[e];
-            if constexpr (E == kGated) red[lane][item][8 + e] = w[e];
+            for (int e = 0; e < 8; ++e) {
+                red[threadIdx.x][e] = v[e];
+                if constexpr (E == kGated) red[threadIdx.x][8 + e] = w[e];
+            }
+            if constexpr (E == kWeight) red[threadIdx.x][8] = sum;
+            __syncthreads();
         }
-        __syncthreads();
         const int64_t q = q0 + row, p = E == kGated ? (p0 >> 1) + c * 8 : p0 + c * 8;
         if (lane == 0) {
-#pragma unroll
-            for (int l = 1; l < kLanes; ++l)
+            for (int l = 1; l < kLanes; ++l) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    v[e] += red[l][item][e];
-                    if constexpr (E == kGated) w[e] += red[l][item][8 + e];
+                    v[e] += red[l * items + item][e];
+                    if constexpr (E == kGated) w[e] += red[l * items + item][8 + e];
                 }
+                if constexpr (E == kWeight) sum += red[l * items + item][8];
+            }
             if constexpr (E == kLinear) {
                 float b[8];
                 bias8<T>(a, p, b);
@@ -543,13 +581,9 @@ struct Gemm {
                 finish_gated<T>(a, q, p, v, w, g, u);
             } else if (q < a.nq && p < a.np) {
                 write8<T>((T *)a.out + q * a.np + p, a.np - p, v);
-            }
-        }
-        if constexpr (E == kWeight) {
-            if (p0 == 0 && c == 0 && lane == 1 && q < a.nq) {
-                float t = 0.f;
-                for (int s = 0; s < a.pieces; ++s) t += a.part[((int64_t)s * cut + tile) * kSlot + kP * kQ + row];
-                ((T *)a.sums)[q] = Elem<T>::from_f32(t);
+                if constexpr (E == kWeight) {
+                    if (sums) ((T *)a.sums)[q] = Elem<T>::from_f32(sum);
+                }
             }
         }
     }
@@ -557,7 +591,7 @@ struct Gemm {
 
 template <typename G>
 __global__ __launch_bounds__(G::kFinishThreads) void finish_kernel(const Product a) {
-    __shared__ float red[G::kLanes][G::kItems][G::kE == kGated ? 17 : 9];
+    __shared__ float red[G::kFinishThreads][G::kReds];
     G::finish(a, red);
 }
 

@@ -23,59 +23,57 @@ inline bool direct_ok(Side s, const void *p, int64_t ld, int64_t extent, int64_t
 }
 
 // The tiles that a call may take: waves in p and q, fragments of a wave in p and q, workgroups of a
-// compute unit, and the share of the large tile's rate that it reaches (8192^3: bfloat16 1228 TFLOP/s
-// with tiles of 256 and 750 to 900 with 128).
+// compute unit, and the rate that a full chip reaches with them (TFLOP/s, bfloat16 and float32).
 struct Form {
     int wp, wq, mp, nq, per_cu;
-    double rate;
+    double rate[2];
     int kp() const { return wp * mp * 16; }
     int kq() const { return wq * nq * 16; }
 };
-constexpr Form kForms[] = {{2, 4, 8, 4, 1, 1.0},    // 256 x 256, bfloat16 straight to LDS
-                           {2, 2, 4, 4, 2, 0.75},   // 128 x 128
-                           {1, 4, 4, 4, 2, 0.75}};  // 64 x 256, results of few columns
+constexpr Form kForms[] = {{2, 4, 8, 4, 1, {1250, 190}},    // 256 x 256, bfloat16 straight to LDS
+                           {2, 2, 4, 4, 2, {900, 165}},   // 128 x 128
+                           {1, 4, 4, 4, 2, {900, 165}}};  // 64 x 256, results of few columns
 
 // How a call is cut.  The tiles of the last round of workgroups, which would leave compute units idle,
-// are cut along the contraction into pieces that fill them; the sums of the pieces take a second kernel.
+// are cut along the contraction into pieces that fill them, where the way of the pieces' results
+// through memory and the second kernel that joins them cost less than what that saves.
 struct Cut {
     int form = 0, pieces = 1;
     int64_t tiles_p = 0, tiles_q = 0, whole = 0, run = 0;
-    double cost = 0.;
+    double cost = 0.;  // microseconds
     int64_t slots() const { return (tiles_p * tiles_q - whole) * pieces; }
 };
-constexpr int64_t kUnits = 256;       // compute units
-constexpr int64_t kLeastSteps = 4;    // of a piece: below that its loads are not hidden
-constexpr double kPieceSteps = 6.;    // what a piece's result costs on its way through memory, in steps
-constexpr double kFinishSteps = 4.;   // the second kernel
+constexpr int64_t kUnits = 256;                // compute units
+constexpr int64_t kLeastSteps = 4;             // of a piece: below that its loads are not hidden
+constexpr double kUnitBytes = 4.5e6 / kUnits;  // bytes a microsecond of a compute unit's share of the memory
+constexpr double kSecondKernel = 4.;           // microseconds
 
-inline Cut cut_for(int form, int64_t p, int64_t q, int64_t steps) {
+inline Cut cut_for(int form, bool bf16, int64_t p, int64_t q, int64_t steps) {
     const Form &f = kForms[form];
     Cut c;
     c.form = form;
     c.tiles_p = (p + f.kp() - 1) / f.kp();
     c.tiles_q = (q + f.kq() - 1) / f.kq();
-    const double tiles = (double)c.tiles_p * (double)c.tiles_q;
-    const int64_t slots = kUnits * f.per_cu;
-    const double step = f.kp() * f.kq() * f.per_cu / f.rate;  // time of a step, all slots busy
-    if (tiles >= 16. * slots) {  // rounds enough
-        c.whole = (int64_t)(tiles < 4e9 ? tiles : 4e9);
-        c.cost = tiles / slots * steps * step;
-        return c;
-    }
-    const int64_t n = (int64_t)tiles, rest = n % slots;
-    const double before = (double)(n / slots) * steps;
-    double best = before + (rest ? steps : 0);
-    c.whole = n;
-    for (int s = 2; rest && s <= 256 && (steps + s - 1) / s >= kLeastSteps; ++s) {
-        const int64_t rounds = (rest * s + slots - 1) / slots;
-        const double t = before + rounds * ((double)((steps + s - 1) / s) + kPieceSteps) + kFinishSteps;
-        if (t < best) {
-            best = t;
-            c.pieces = s;
-            c.whole = n - rest;
+    const double tiles = (double)c.tiles_p * (double)c.tiles_q, area = (double)f.kp() * f.kq();
+    const double step = 2. * area * (bf16 ? 64 : 32) / (f.rate[bf16 ? 0 : 1] * 1e6 / kUnits);  // of one workgroup on a unit's full rate
+    const double out = area * 4 / kUnitBytes;
+    // One workgroup alone on its unit hides less where two would fit.
+    const auto rounds = [&](double n) { return n <= kUnits && f.per_cu == 2 ? 1.3 : __builtin_ceil(n / kUnits); };
+    double best = rounds(tiles) * (steps * step + out / 2);
+    c.whole = (int64_t)(tiles < 4e9 ? tiles : 4e9);
+    if (tiles < 16. * kUnits * f.per_cu) {
+        const int64_t n = (int64_t)tiles, rest = n % (kUnits * f.per_cu);
+        const double before = (double)((n - rest) / kUnits) * (steps * step + out / 2);
+        for (int s = 2; rest && s <= 256 && (steps + s - 1) / s >= kLeastSteps; ++s) {
+            const double t = before + rounds((double)rest * s) * ((double)((steps + s - 1) / s) * step + 2 * out) + kSecondKernel;
+            if (t < best) {
+                best = t;
+                c.pieces = s;
+                c.whole = n - rest;
+            }
         }
     }
-    c.cost = best * step;
+    c.cost = best;
     return c;
 }
 
@@ -83,8 +81,8 @@ template <typename T>
 inline Cut cut_of(Kind kind, int64_t np, int64_t nq, int64_t nk, bool direct) {
     const int64_t p = kind == kGatedForward ? 2 * np : np, steps = (nk + kStep<T> - 1) / kStep<T>;
     Cut best;
-    for (int form = direct && Elem<T>::is_bf16 ? 0 : 1; form < 3; ++form) {
-        const Cut c = cut_for(form, p, nq, steps);
+    for (int form = direct ? 0 : 1; form < 3; ++form) {
+        const Cut c = cut_for(form, Elem<T>::is_bf16, p, nq, steps);
         if (best.tiles_p == 0 || c.cost < best.cost) best = c;
     }
     best.run = (steps + best.pieces - 1) / best.pieces * kStep<T>;
@@ -111,7 +109,7 @@ hipError_t launch_gemm(Product &a, const Cut &c, hipStream_t stream) {
     const hipError_t r = hipGetLastError();
     if (r != hipSuccess || c.pieces == 1) return r;
     const int64_t cut = c.tiles_p * c.tiles_q - c.whole;
-    hipLaunchKernelGGL((finish_kernel<G>), dim3((unsigned)(cut * (G::kPerTile / G::kItems))), dim3(G::kFinishThreads), 0, stream, a);
+    hipLaunchKernelGGL((finish_kernel<G>), dim3((unsigned)(cut * (G::kPerTile / (G::kFinishThreads / G::lanes(c.pieces))))), dim3(G::kFinishThreads), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -127,9 +125,7 @@ hipError_t product(Product a, float *part, hipStream_t stream) {
     if (c.form == k) \
         return launch_gemm<Gemm<T, sp, sq, e, kForms[k].wp, kForms[k].wq, kForms[k].mp, kForms[k].nq, DIRECT>>(a, c, stream);
     if (direct) {
-        if constexpr (Elem<T>::is_bf16) {
-            DDPM_FF_FORM(0, true)
-        }
+        DDPM_FF_FORM(0, true)
         DDPM_FF_FORM(1, true)
         DDPM_FF_FORM(2, true)
     } else {
