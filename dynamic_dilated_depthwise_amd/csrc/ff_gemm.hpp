@@ -21,6 +21,8 @@
 // row of x reaches another's output.
 #pragma once
 
+#include <type_traits>
+
 #include "ff_launch.hpp"
 #include "seq_common.hpp"
 
@@ -45,6 +47,10 @@ __device__ __forceinline__ void arrive_all() {
 }
 __device__ __forceinline__ void arrive_lds() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
+// Between a wave's writes to LDS and other lanes' reads of them: the hardware keeps their order, the
+// compiler only a lane's own.
+__device__ __forceinline__ void wave_order() { asm volatile("" ::: "memory"); }
+
 // 16 bytes a lane from `off` behind `p` (uniform; zeros from kRecords on) to LDS at `at` (uniform) + 16 lane.
 // In assembly, because the compiler takes the builtin for a write to all of LDS and makes the fragment
 // reads behind it wait for it (grad_x 930 -> 570 TFLOP/s with loads between them).  It has no result, so
@@ -63,13 +69,12 @@ __device__ __forceinline__ void load_to_lds(const void *p, uint32_t off, char *a
 template <typename T, Side S, int CH>
 __device__ __forceinline__ int swizzle(int row) {
     if constexpr (S == kAlong) return row & 7;
-    else if constexpr (!Elem<T>::is_bf16) return (row >> 3 & 3) << 2;
+    else if constexpr (!Elem<T>::is_bf16) return (row >> 3 & 3) << 2 & (CH - 1);
     else if constexpr (CH >= 16) return ((row & 3) | (row >> 3 & 1) << 2) << 1;
-    else return ((row >> 1 & 1) | (row >> 3 & 1) << 1) << 1;
+    else return ((row >> 1 & 1) | (row >> 3 & 1) << 1) << 1 & (CH - 1);
 }
 
-// Rows of P in the gated product: 16 of the gate's, then the same 16 of the other half.
-__device__ __forceinline__ int64_t gated_row(int64_t r, int64_t N) { return (r >> 5 << 4) + (r & 15) + (r & 16 ? N : 0); }
+// The gated product's tile of P has 16 of the gate's rows, the same 16 of the other half, and so on.
 
 // One operand's tile: TILE indices from `first` of `extent`, contraction from k0.
 template <typename T, Side S, int TILE, int THREADS, bool DIRECT, bool GATED>
@@ -77,62 +82,65 @@ struct Tile {
     static constexpr int kPer = kVec<T>, kCh = S == kAlong ? 8 : TILE / kPer;
     static constexpr int kCount = TILE * 8 / THREADS;
     static_assert(TILE * 8 % THREADS == 0, "whole rounds of chunks");
+    typedef std::conditional_t<DIRECT, uint32_t, int64_t> Offset;  // direct_ok: within 2^31 bytes
     const T *p;
-    int64_t ld, first, extent, k;  // extent: of the index (gated: columns of the result)
-    uint32_t off[DIRECT ? kCount : 1];
+    int64_t ld;
+    Offset off[kCount];  // of the chunks in a step's tile, in bytes
     u32x4 r[DIRECT ? 1 : kCount];
+    int columns;  // kDown, through registers: of the tile that are there
 
     __device__ __forceinline__ static int row_of(int i, int tid) { return (i * THREADS + tid) / kCh; }
     __device__ __forceinline__ static int chunk_of(int i, int tid) {
         return (i * THREADS + tid) % kCh ^ swizzle<T, S, kCh>(row_of(i, tid));
     }
-    __device__ __forceinline__ void start(const void *base, int64_t ld_, int64_t first_, int64_t extent_, int64_t k0, int tid) {
-        p = (const T *)base;
+    // Rows (kAlong) that are not there: zeros, or through registers the last one's, which nobody takes
+    // (extent: of the index; gated: columns of the result).
+    __device__ __forceinline__ void start(const void *base, int64_t ld_, int64_t first, int64_t extent, int64_t k0, int tid) {
         ld = ld_;
-        first = first_;
-        extent = extent_;
-        k = k0;
-        if constexpr (DIRECT) {
+        const int64_t from = GATED ? first >> 1 : first;
 #pragma unroll
-            for (int i = 0; i < kCount; ++i) {
-                const int row = row_of(i, tid), c = chunk_of(i, tid);
-                if constexpr (S == kAlong) {
-                    const bool on = GATED ? (first >> 1) + (row >> 5 << 4) + (row & 15) < extent : first + row < extent;
-                    const int64_t at = GATED ? gated_row(row, extent) : row;
-                    off[i] = on ? (uint32_t)(at * ld * sizeof(T)) + c * 16 : kOutside;
-                } else {
-                    off[i] = first + c * kPer < extent ? (uint32_t)(row * ld * sizeof(T)) + c * 16 : kOutside;
-                }
+        for (int i = 0; i < kCount; ++i) {
+            const int row = row_of(i, tid), c = chunk_of(i, tid);
+            if constexpr (S == kAlong) {
+                const int64_t at = GATED ? (row >> 5 << 4) + (row & 15) : row, last = extent - from - 1;
+                const int64_t there = (at <= last ? at : last) + (GATED && row & 16 ? extent : 0);
+                off[i] = DIRECT && at > last ? kOutside : (Offset)(there * ld * sizeof(T)) + c * 16;
+            } else {
+                off[i] = DIRECT && first + c * kPer >= extent ? kOutside : (Offset)(row * ld * sizeof(T)) + c * 16;
             }
-            p += S == kAlong ? (GATED ? first >> 1 : first) * ld + k : k * ld + first;
         }
+        p = (const T *)base + (S == kAlong ? from * ld + k0 : k0 * ld + from);
+        columns = (int)(extent - from < TILE ? extent - from : TILE);
     }
-    // Round i of the chunks of the next step, of which `left` elements of the contraction are there, straight to LDS.
+    __device__ __forceinline__ void next() { p += S == kAlong ? kStep<T> : kStep<T> * ld; }
+    // Round i of the chunks of the step, of which `left` elements of the contraction are there, straight to LDS.
     __device__ __forceinline__ void ask(int i, char *lds, int64_t left, int tid) const {
-        uint32_t o = off[i];
+        Offset o = off[i];
         if (left < kStep<T>) {
             const bool on = S == kAlong ? chunk_of(i, tid) * kPer < left : row_of(i, tid) < left;
             o = on ? o : kOutside;
         }
         load_to_lds(p, o, lds + (i * THREADS + wave_of(tid) * kWave) * 16);
     }
-    __device__ __forceinline__ void next() { p += S == kAlong ? kStep<T> : kStep<T> * ld; }
-    // The next step's chunks into registers; put: from there into LDS.
+    // The step's chunks into registers; put: from there into LDS.  Only the contraction's last step and
+    // the last tile of a kDown operand's columns look at how many elements are there.
     __device__ __forceinline__ void fetch(int64_t left, int tid) {
+        const bool whole = left >= kStep<T>;
 #pragma unroll
         for (int i = 0; i < kCount; ++i) {
             const int row = row_of(i, tid), c = chunk_of(i, tid) * kPer;
+            const char *at = (const char *)p + off[i];
             if constexpr (S == kAlong) {
-                const int64_t f = GATED ? (first >> 1) + (row >> 5 << 4) + (row & 15) : first + row;
-                const bool on = f < extent;
-                const int64_t at = GATED ? (first >> 1) + gated_row(row, extent) : f;
-                r[i] = load_vec<T>(p + (on ? at * ld + k + c : 0), on ? left - c : 0);
+                if (whole) r[i] = *(const u32x4_a2 *)at;
+                else r[i] = load_vec<T>((const T *)at, left - c);
             } else {
-                const bool on = row < left;
-                r[i] = load_vec<T>(p + (on ? (k + row) * ld + first + c : 0), on ? extent - first - c : 0);
+                const bool on = whole || row < left;
+                at -= on ? 0 : row * ld * (int64_t)sizeof(T);
+                if (columns == TILE) r[i] = *(const u32x4_a2 *)at;
+                else r[i] = load_vec<T>((const T *)at, columns - c);
+                if (!on) r[i] = u32x4{0, 0, 0, 0};
             }
         }
-        k += kStep<T>;
     }
     __device__ __forceinline__ void put(char *lds, int tid) const {
 #pragma unroll
@@ -458,6 +466,8 @@ struct Gemm {
                 tile_q.put(now + kP * kStepBytes, tid);
                 arrive_lds();
                 if (s + 1 < steps) {
+                    tile_p.next();
+                    tile_q.next();
                     tile_p.fetch(left, tid);
                     tile_q.fetch(left, tid);
                 }
@@ -481,6 +491,7 @@ struct Gemm {
         for (int j = 0; j < NQ; ++j) {
 #pragma unroll
             for (int i = 0; i < MP; ++i) *(f32x4 *)(mine + (lane % 16) * kLd + 16 * i + 4 * (lane / 16)) = acc[i][j];
+            wave_order();
             const int64_t q = q0 + (wq * NQ + j) * 16;
 #pragma unroll 1
             for (int r = r0; r < 16; r += kRows) {
@@ -505,6 +516,7 @@ struct Gemm {
                     if (q + r < a.nq && p < a.np) write8<T>((T *)a.out + (q + r) * a.np + p, a.np - p, v);
                 }
             }
+            wave_order();
         }
         if constexpr (E == kWeight) {  // every row of `sum` holds the sums over k of Q
             if (sums && lane < 16) {

@@ -13,14 +13,7 @@ namespace ff {
 DDPM_FF_KINDS(X)
 #undef X
 
-namespace {
-
-bool few_rows(Kind kind, int64_t nq) { return (kind == kForward || kind == kGatedForward) && nq <= kFewRows; }
-
-}  // namespace
-
 hipError_t launch_product(Kind kind, const Product &a, float *part, bool bf16, hipStream_t stream) {
-    if (few_rows(kind, a.nq)) return launch_rows(kind == kGatedForward, a, bf16, stream);
 #define X(K, name) \
     if (kind == K) return bf16 ? product_##name##_bf16(a, part, stream) : product_##name##_f32(a, part, stream);
     DDPM_FF_KINDS(X)
@@ -29,9 +22,9 @@ hipError_t launch_product(Kind kind, const Product &a, float *part, bool bf16, h
 }
 
 int64_t product_floats(Kind kind, int64_t np, int64_t nq, int64_t nk, bool bf16) {
-    if (few_rows(kind, nq)) return 0;
     int64_t most = 0;
     for (const bool direct : {false, true}) {
+        if (few_rows(kind, nq, direct)) continue;
         const Cut c = bf16 ? cut_of<bf16_t>(kind, np, nq, nk, direct) : cut_of<float>(kind, np, nq, nk, direct);
         most = std::max(most, c.pieces > 1 ? part_floats(kind, c) : 0);
     }

@@ -35,8 +35,9 @@ enum Kind { kForward, kGatedForward, kGradX, kGradWeight };
 int64_t product_floats(Kind kind, int64_t np, int64_t nq, int64_t nk, bool bf16);
 hipError_t launch_product(Kind kind, const Product &a, float *part, bool bf16, hipStream_t stream);
 
-// The forward products of up to kFewRows rows (ff_rows.hip); launch_product takes it for them.
-constexpr int64_t kFewRows = 64;
+// The forward products of few rows (ff_rows.hip): up to kMostRows, of which launch_product takes it for
+// kFewRows, or all of them where the operands cannot go straight to LDS.
+constexpr int64_t kFewRows = 16, kMostRows = 64;
 hipError_t launch_rows(bool gated, const Product &a, bool bf16, hipStream_t stream);
 
 // dz = grad * act'(saved), [rows, N]; gated: saved [rows, 2 N] and dz [rows, 2 N],

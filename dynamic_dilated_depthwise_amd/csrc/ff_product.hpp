@@ -30,9 +30,12 @@ struct Form {
     int kp() const { return wp * mp * 16; }
     int kq() const { return wq * nq * 16; }
 };
-constexpr Form kForms[] = {{2, 4, 8, 4, 1, {1250, 190}},    // 256 x 256, bfloat16 straight to LDS
+constexpr Form kForms[] = {{2, 4, 8, 4, 1, {1250, 200}},  // 256 x 256, straight to LDS
                            {2, 2, 4, 4, 2, {900, 165}},   // 128 x 128
-                           {1, 4, 4, 4, 2, {900, 165}}};  // 64 x 256, results of few columns
+                           {1, 4, 4, 4, 2, {900, 165}},   // 64 x 256, straight to LDS: results of few columns
+                           {4, 1, 2, 4, 3, {700, 120}},   // 128 x 64, straight to LDS: few rows
+                           {4, 1, 2, 2, 3, {500, 90}}};   // 128 x 32
+constexpr int kFormCount = 5, kGeneral = 1;  // kGeneral: the one for operands that cannot go straight to LDS
 
 // How a call is cut.  The tiles of the last round of workgroups, which would leave compute units idle,
 // are cut along the contraction into pieces that fill them, where the way of the pieces' results
@@ -43,10 +46,11 @@ struct Cut {
     double cost = 0.;  // microseconds
     int64_t slots() const { return (tiles_p * tiles_q - whole) * pieces; }
 };
-constexpr int64_t kUnits = 256;                // compute units
-constexpr int64_t kLeastSteps = 4;             // of a piece: below that its loads are not hidden
-constexpr double kUnitBytes = 4.5e6 / kUnits;  // bytes a microsecond of a compute unit's share of the memory
-constexpr double kSecondKernel = 4.;           // microseconds
+constexpr int64_t kUnits = 256;        // compute units
+constexpr int kLeastSteps = 2;         // of a piece
+constexpr double kBytes = 4.5e6;       // bytes of results a microsecond
+constexpr double kLatency = 1.;        // microseconds of a step at least: its loads on their way
+constexpr double kSecondKernel = 4.;   // microseconds
 
 inline Cut cut_for(int form, bool bf16, int64_t p, int64_t q, int64_t steps) {
     const Form &f = kForms[form];
@@ -55,25 +59,29 @@ inline Cut cut_for(int form, bool bf16, int64_t p, int64_t q, int64_t steps) {
     c.tiles_p = (p + f.kp() - 1) / f.kp();
     c.tiles_q = (q + f.kq() - 1) / f.kq();
     const double tiles = (double)c.tiles_p * (double)c.tiles_q, area = (double)f.kp() * f.kq();
-    const double step = 2. * area * (bf16 ? 64 : 32) / (f.rate[bf16 ? 0 : 1] * 1e6 / kUnits);  // of one workgroup on a unit's full rate
-    const double out = area * 4 / kUnitBytes;
-    // One workgroup alone on its unit hides less where two would fit.
-    const auto rounds = [&](double n) { return n <= kUnits && f.per_cu == 2 ? 1.3 : __builtin_ceil(n / kUnits); };
-    double best = rounds(tiles) * (steps * step + out / 2);
-    c.whole = (int64_t)(tiles < 4e9 ? tiles : 4e9);
-    if (tiles < 16. * kUnits * f.per_cu) {
-        const int64_t n = (int64_t)tiles, rest = n % (kUnits * f.per_cu);
-        const double before = (double)((n - rest) / kUnits) * (steps * step + out / 2);
+    const double step = 2. * area * (bf16 ? 64 : 32) / (f.rate[bf16 ? 0 : 1] * 1e6 / kUnits);  // of one workgroup, at the unit's full rate
+    const int64_t slots = kUnits * f.per_cu;
+    // n workgroups of so many steps: whole rounds, and what the last one has on the fullest unit
+    const auto time = [&](int64_t n, int64_t steps_) {
+        const auto round = [&](int64_t m) { return m * step > kLatency ? m * step : kLatency; };
+        const int64_t last = (n % slots + kUnits - 1) / kUnits;
+        return steps_ * ((double)(n / slots) * round(f.per_cu) + (last ? round(last) : 0.));
+    };
+    const double out = area * (bf16 ? 2 : 4) / kBytes, part = area * 8 / kBytes;
+    const int64_t n = (int64_t)(tiles < 4e9 ? tiles : 4e9), rest = n % slots;
+    c.whole = n;
+    c.cost = time(n, steps) + n * out;
+    if (n < 16 * slots) {
+        const double before = time(n - rest, steps) + n * out + kSecondKernel;
         for (int s = 2; rest && s <= 256 && (steps + s - 1) / s >= kLeastSteps; ++s) {
-            const double t = before + rounds((double)rest * s) * ((double)((steps + s - 1) / s) * step + 2 * out) + kSecondKernel;
-            if (t < best) {
-                best = t;
+            const double t = before + time(rest * s, (steps + s - 1) / s) + rest * s * part;
+            if (t < c.cost) {
+                c.cost = t;
                 c.pieces = s;
                 c.whole = n - rest;
             }
         }
     }
-    c.cost = best;
     return c;
 }
 
@@ -81,13 +89,19 @@ template <typename T>
 inline Cut cut_of(Kind kind, int64_t np, int64_t nq, int64_t nk, bool direct) {
     const int64_t p = kind == kGatedForward ? 2 * np : np, steps = (nk + kStep<T> - 1) / kStep<T>;
     Cut best;
-    for (int form = direct ? 0 : 1; form < 3; ++form) {
+    for (int form = 0; form < kFormCount; ++form) {
+        if (!direct && form != kGeneral) continue;
         const Cut c = cut_for(form, Elem<T>::is_bf16, p, nq, steps);
         if (best.tiles_p == 0 || c.cost < best.cost) best = c;
     }
     best.run = (steps + best.pieces - 1) / best.pieces * kStep<T>;
     best.pieces = (int)((nk + best.run - 1) / best.run);  // none is empty
     return best;
+}
+
+// Whether the forward takes the kernel of few rows (ff_rows.hip).
+inline bool few_rows(Kind kind, int64_t nq, bool direct) {
+    return (kind == kForward || kind == kGatedForward) && nq <= (direct ? kFewRows : kMostRows);
 }
 
 // Floats of the pieces' results.
@@ -119,18 +133,20 @@ hipError_t product(Product a, float *part, hipStream_t stream) {
     constexpr Epi e = KindOf<K>::e;
     const bool direct = direct_ok<T>(sp, a.p, a.p_ld, a.np, a.nk, K == kGatedForward ? a.np + 256 : 256) &&
                         direct_ok<T>(sq, a.q, a.q_ld, a.nq, a.nk, 256);
+    if (few_rows(K, a.nq, direct)) return launch_rows(K == kGatedForward, a, Elem<T>::is_bf16, stream);
     const Cut c = cut_of<T>(K, a.np, a.nq, a.nk, direct);
     a.part = part;
 #define DDPM_FF_FORM(k, DIRECT) \
     if (c.form == k) \
         return launch_gemm<Gemm<T, sp, sq, e, kForms[k].wp, kForms[k].wq, kForms[k].mp, kForms[k].nq, DIRECT>>(a, c, stream);
-    if (direct) {
+    if (!direct) {
+        DDPM_FF_FORM(kGeneral, false)
+    } else {
         DDPM_FF_FORM(0, true)
         DDPM_FF_FORM(1, true)
         DDPM_FF_FORM(2, true)
-    } else {
-        DDPM_FF_FORM(1, false)
-        DDPM_FF_FORM(2, false)
+        DDPM_FF_FORM(3, true)
+        DDPM_FF_FORM(4, true)
     }
 #undef DDPM_FF_FORM
     return hipErrorInvalidValue;

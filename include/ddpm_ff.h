@@ -13,7 +13,7 @@
  *   function returns in bytes (NULL where that is 0; their contents need no preparation).
  * Streams.  As in ddpm.h: work is enqueued on `stream` and the call returns.  Nothing is cleared
  *   by memset, so every call may be captured into a graph.  No atomics are used: equal inputs
- *   give equal bits.
+ *   at equally aligned addresses give equal bits.
  * Precision.  Products are summed in float32; float32 operands enter the matrix instructions as
  *   three bfloat16 terms each, six products of them, which is float32's own precision.  Bias,
  *   activation and residual are applied to that sum, and outputs are rounded once.  In the backward of an activation or a gate the gradient

@@ -124,12 +124,13 @@ def test_views_and_axes(gated, dt):
         wide[:, left:left + t.shape[1]] = t
         return wide[:, left:left + t.shape[1]]
 
-    for left, right in ((8, 16), (3, 2)):
-        xv, gv, rv = inside(x, left, right), inside(grad, left, right), inside(r, left, right) if r is not None else None
-        y2, saved2 = forward(xv, w, b, rv, act, gated, save=True)
-        assert torch.equal(y2, y) and torch.equal(saved2, saved)
-        for p, q in zip(backward(gv, xv, w, saved2, act, gated), grads):
-            assert torch.equal(p, q)
+    xv, gv, rv = (inside(t, 8, 16) if t is not None else None for t in (x, grad, r))
+    y2, saved2 = forward(xv, w, b, rv, act, gated, save=True)
+    assert torch.equal(y2, y) and torch.equal(saved2, saved)
+    for p, q in zip(backward(gv, xv, w, saved2, act, gated), grads):
+        assert torch.equal(p, q)
+    # starts of no whole chunk: another form, other orders of the sums
+    compare(inside(x, 3, 2), w, b, inside(r, 1, 0) if r is not None else None, inside(grad, 1, 6), act, gated)
     x3, r3 = x.view(2, 3, 5, 72), r.view(2, 3, 5, 40) if r is not None else None
     y3, saved3 = forward(x3, w, b, r3, act, gated, save=True)
     assert y3.shape == (2, 3, 5, 40) and torch.equal(y3.view(30, 40), y)
