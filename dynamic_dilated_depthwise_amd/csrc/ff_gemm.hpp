@@ -608,7 +608,7 @@ __global__ __launch_bounds__(G::kFinishThreads) void finish_kernel(const Product
 }
 
 template <typename G>
-__global__ __launch_bounds__(G::kThreads, 2) void gemm_kernel(const Product a) {
+__global__ __launch_bounds__(G::kThreads, G::kThreads == 1024 ? 4 : 2) void gemm_kernel(const Product a) {
     __shared__ __attribute__((aligned(16))) char lds[G::kLds];
     G::run(a, lds);
 }

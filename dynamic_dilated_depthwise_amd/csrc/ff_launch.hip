@@ -26,7 +26,7 @@ int64_t product_floats(Kind kind, int64_t np, int64_t nq, int64_t nk, bool bf16)
     for (const bool direct : {false, true}) {
         if (few_rows(kind, nq, direct)) continue;
         const Cut c = bf16 ? cut_of<bf16_t>(kind, np, nq, nk, direct) : cut_of<float>(kind, np, nq, nk, direct);
-        most = std::max(most, c.pieces > 1 ? part_floats(kind, c) : 0);
+        most = std::max(most, c.pieces > 1 ? part_floats(bf16, kind, c) : 0);
     }
     return most;
 }

@@ -23,19 +23,32 @@ inline bool direct_ok(Side s, const void *p, int64_t ld, int64_t extent, int64_t
 }
 
 // The tiles that a call may take: waves in p and q, fragments of a wave in p and q, workgroups of a
-// compute unit, and the rate that a full chip reaches with them (TFLOP/s, bfloat16 and float32).
+// compute unit, and the microseconds of a step of the contraction: of one workgroup's share where the
+// unit is full, and at least, with its loads on their way (measured: products of 8192^3 and 4096^3, and
+// of 512 x 2048 x 2048, whose few tiles are alone on their units).
 struct Form {
     int wp, wq, mp, nq, per_cu;
-    double rate[2];
-    int kp() const { return wp * mp * 16; }
-    int kq() const { return wq * nq * 16; }
+    double busy, alone;
+    constexpr int kp() const { return wp * mp * 16; }
+    constexpr int kq() const { return wq * nq * 16; }
 };
-constexpr Form kForms[] = {{2, 4, 8, 4, 1, {1250, 200}},  // 256 x 256, straight to LDS
-                           {2, 2, 4, 4, 2, {900, 165}},   // 128 x 128
-                           {1, 4, 4, 4, 2, {900, 165}},   // 64 x 256, straight to LDS: results of few columns
-                           {4, 1, 2, 4, 3, {700, 120}},   // 128 x 64, straight to LDS: few rows
-                           {4, 1, 2, 2, 3, {500, 90}}};   // 128 x 32
 constexpr int kFormCount = 5, kGeneral = 1;  // kGeneral: the one for operands that cannot go straight to LDS
+// bfloat16: as many waves as registers allow, so that one's reads of LDS run behind another's products
+// (256 x 256 with 16 waves 798 us at 8192^3, with 8 848; 128 x 128 with 8 1103, with 4 1370).  Where both
+// operands are read by columns 16 waves do not hold their addresses (1129 us, with 8 872).
+// float32: waves with large tiles, which split their operands for more products (256 x 256 with 8 waves
+// 692 us at 4096^3, with 16 1115; 128 x 128 with 4 830, with 8 1041).
+constexpr Form form_of(bool bf16, Kind kind, int k) {
+    constexpr Form low[] = {{4, 4, 4, 4, 1, 1.55, 1.5},   // 256 x 256
+                            {4, 2, 2, 4, 2, 0.54, 0.65},  // 128 x 128
+                            {2, 4, 2, 4, 2, 0.56, 0.7},   // 64 x 256: results of few columns
+                            {4, 1, 2, 4, 3, 0.33, 0.5},   // 128 x 64
+                            {4, 1, 2, 2, 3, 0.22, 0.43}}; // 128 x 32: few rows
+    constexpr Form full[] = {{2, 4, 8, 4, 1, 5.3, 5.3}, {2, 2, 4, 4, 2, 1.6, 1.9}, {1, 4, 4, 4, 2, 1.6, 1.9}, {4, 1, 2, 4, 3, 0.83, 1.4},
+                             {4, 1, 2, 2, 3, 0.49, 1.}};
+    constexpr Form weight = {2, 4, 8, 4, 1, 1.7, 1.6};
+    return bf16 ? k == 0 && kind == kGradWeight ? weight : low[k] : full[k];
+}
 
 // How a call is cut.  The tiles of the last round of workgroups, which would leave compute units idle,
 // are cut along the contraction into pieces that fill them, where the way of the pieces' results
@@ -46,24 +59,20 @@ struct Cut {
     double cost = 0.;  // microseconds
     int64_t slots() const { return (tiles_p * tiles_q - whole) * pieces; }
 };
-constexpr int64_t kUnits = 256;        // compute units
-constexpr int kLeastSteps = 2;         // of a piece
-constexpr double kBytes = 4.5e6;       // bytes of results a microsecond
-constexpr double kLatency = 1.;        // microseconds of a step at least: its loads on their way
-constexpr double kSecondKernel = 4.;   // microseconds
+constexpr int64_t kUnits = 256;       // compute units
+constexpr int kLeastSteps = 2;        // of a piece
+constexpr double kBytes = 4.5e6;      // bytes of results a microsecond
+constexpr double kSecondKernel = 6.;  // microseconds
 
-inline Cut cut_for(int form, bool bf16, int64_t p, int64_t q, int64_t steps) {
-    const Form &f = kForms[form];
+inline Cut cut_for(const Form &f, bool bf16, int64_t p, int64_t q, int64_t steps) {
     Cut c;
-    c.form = form;
     c.tiles_p = (p + f.kp() - 1) / f.kp();
     c.tiles_q = (q + f.kq() - 1) / f.kq();
     const double tiles = (double)c.tiles_p * (double)c.tiles_q, area = (double)f.kp() * f.kq();
-    const double step = 2. * area * (bf16 ? 64 : 32) / (f.rate[bf16 ? 0 : 1] * 1e6 / kUnits);  // of one workgroup, at the unit's full rate
     const int64_t slots = kUnits * f.per_cu;
     // n workgroups of so many steps: whole rounds, and what the last one has on the fullest unit
     const auto time = [&](int64_t n, int64_t steps_) {
-        const auto round = [&](int64_t m) { return m * step > kLatency ? m * step : kLatency; };
+        const auto round = [&](int64_t m) { return m * f.busy > f.alone ? m * f.busy : f.alone; };
         const int64_t last = (n % slots + kUnits - 1) / kUnits;
         return steps_ * ((double)(n / slots) * round(f.per_cu) + (last ? round(last) : 0.));
     };
@@ -87,11 +96,13 @@ inline Cut cut_for(int form, bool bf16, int64_t p, int64_t q, int64_t steps) {
 
 template <typename T>
 inline Cut cut_of(Kind kind, int64_t np, int64_t nq, int64_t nk, bool direct) {
+    constexpr bool bf16 = Elem<T>::is_bf16;
     const int64_t p = kind == kGatedForward ? 2 * np : np, steps = (nk + kStep<T> - 1) / kStep<T>;
     Cut best;
-    for (int form = 0; form < kFormCount; ++form) {
-        if (!direct && form != kGeneral) continue;
-        const Cut c = cut_for(form, Elem<T>::is_bf16, p, nq, steps);
+    for (int k = 0; k < kFormCount; ++k) {
+        if (!direct && k != kGeneral) continue;
+        Cut c = cut_for(form_of(bf16, kind, k), bf16, p, nq, steps);
+        c.form = k;
         if (best.tiles_p == 0 || c.cost < best.cost) best = c;
     }
     best.run = (steps + best.pieces - 1) / best.pieces * kStep<T>;
@@ -105,8 +116,9 @@ inline bool few_rows(Kind kind, int64_t nq, bool direct) {
 }
 
 // Floats of the pieces' results.
-inline int64_t part_floats(Kind kind, const Cut &c) {
-    const int64_t kp = kForms[c.form].kp(), kq = kForms[c.form].kq();
+inline int64_t part_floats(bool bf16, Kind kind, const Cut &c) {
+    const Form f = form_of(bf16, kind, c.form);
+    const int64_t kp = f.kp(), kq = f.kq();
     return c.slots() * (kp * kq + (kind == kGradWeight ? kq : 0));
 }
 
@@ -136,9 +148,11 @@ hipError_t product(Product a, float *part, hipStream_t stream) {
     if (few_rows(K, a.nq, direct)) return launch_rows(K == kGatedForward, a, Elem<T>::is_bf16, stream);
     const Cut c = cut_of<T>(K, a.np, a.nq, a.nk, direct);
     a.part = part;
-#define DDPM_FF_FORM(k, DIRECT) \
-    if (c.form == k) \
-        return launch_gemm<Gemm<T, sp, sq, e, kForms[k].wp, kForms[k].wq, kForms[k].mp, kForms[k].nq, DIRECT>>(a, c, stream);
+#define DDPM_FF_FORM(k, DIRECT)                                                                       \
+    if (c.form == k) {                                                                                \
+        constexpr Form f = form_of(Elem<T>::is_bf16, K, k);                                           \
+        return launch_gemm<Gemm<T, sp, sq, e, f.wp, f.wq, f.mp, f.nq, DIRECT>>(a, c, stream);         \
+    }
     if (!direct) {
         DDPM_FF_FORM(kGeneral, false)
     } else {
