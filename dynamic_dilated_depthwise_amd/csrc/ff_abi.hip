@@ -26,21 +26,26 @@ bool sizes_ok(Check &c, const Sizes &s, int activation) {
 
 int64_t rounded(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
-// Of the backward: dz, where the activation makes it another tensor than grad, then the products' splits.
+// Of the backward: dz, where it is another tensor than grad (behind an activation or a gate, and where
+// grad's rows are no whole chunks and many enough), then what the products need.
 struct Room {
-    int64_t dz, part;
-    int64_t all() const { return dz + part; }
+    int64_t dz, rest;
+    int64_t all() const { return dz + rest; }
 };
 Room backward_room(const Sizes &s, bool own_dz, int dtype) {
     const bool bf16 = is_bf16(dtype);
-    return {own_dz ? rounded(s.rows * s.width * (bf16 ? 2 : 4)) : 0,
-            4 * std::max(product_floats(kGradX, s.C, s.rows, s.width, bf16), product_floats(kGradWeight, s.C, s.width, s.rows, bf16))};
+    return {own_dz ? rounded(s.rows * padded(s.width, bf16) * (bf16 ? 2 : 4)) : 0,
+            std::max(product_bytes(kGradX, s.C, s.rows, s.width, bf16), product_bytes(kGradWeight, s.C, s.width, s.rows, bf16))};
+}
+constexpr double kManyFlops = 5e9;  // of one product: from here on a copy of grad costs less than what it saves
+bool copies_grad(const Sizes &s, int dtype) {
+    return s.N % (is_bf16(dtype) ? 8 : 4) != 0 && 2. * s.rows * s.N * s.C >= kManyFlops;
 }
 
 int64_t forward_workspace(Kind kind, const Sizes &s, int dtype) {
     Check c(dtype);
     if (!sizes_ok(c, s, DDPM_ACT_NONE)) return 0;
-    return 4 * product_floats(kind, s.N, s.rows, s.C, is_bf16(dtype));
+    return product_bytes(kind, s.N, s.rows, s.C, is_bf16(dtype));
 }
 
 int forward(Kind kind, const void *x, const void *weight, const void *bias, const void *residual, void *y, float *saved,
@@ -76,12 +81,12 @@ int forward(Kind kind, const void *x, const void *weight, const void *bias, cons
     a.residual_ld = residual_row;
     a.act = activation;
     (void)hipGetLastError();
-    return status_of(launch_product(kind, a, (float *)workspace, is_bf16(dtype), stream));
+    return status_of(launch_product(kind, a, workspace, is_bf16(dtype), stream));
 }
 
-int64_t backward_workspace(const Sizes &s, bool own_dz, int activation, int dtype) {
+int64_t backward_workspace(const Sizes &s, bool through, int activation, int dtype) {
     Check c(dtype);
-    return sizes_ok(c, s, activation) ? backward_room(s, own_dz, dtype).all() : 0;
+    return sizes_ok(c, s, activation) ? backward_room(s, through || copies_grad(s, dtype), dtype).all() : 0;
 }
 
 int backward(bool gated, const void *grad, const void *x, const void *weight, const float *saved, void *grad_x,
@@ -92,11 +97,11 @@ int backward(bool gated, const void *grad, const void *x, const void *weight, co
     c.stride(x_row);
     c.stride(grad_row);
     if (c.bad) return DDPM_ERR_INVALID_ARG;
-    const bool own_dz = gated || activation != DDPM_ACT_NONE, bf16 = is_bf16(dtype);
+    const bool through = gated || activation != DDPM_ACT_NONE, own_dz = through || copies_grad(s, dtype), bf16 = is_bf16(dtype);
     c.input(grad, extent(1, s.rows, s.N, 0, grad_row), c.es());
     c.input(x, extent(1, s.rows, s.C, 0, x_row), c.es());
     c.input(weight, (double)s.width * s.C, c.es());
-    if (own_dz) c.input(saved, (double)s.rows * s.width, 4);
+    if (through) c.input(saved, (double)s.rows * s.width, 4);
     c.maybe_out(grad_x, (double)s.rows * s.C, c.es());
     c.maybe_out(grad_weight, (double)s.width * s.C, c.es());
     c.maybe_out(grad_bias, s.width, c.es());
@@ -109,12 +114,14 @@ int backward(bool gated, const void *grad, const void *x, const void *weight, co
     a.q = grad;
     a.q_ld = grad_row;
     if (own_dz) {
-        const hipError_t e = launch_dz(gated, grad, grad_row, saved, workspace, s.rows, s.N, activation, bf16, stream);
+        const hipError_t e = through ? launch_dz(gated, grad, grad_row, saved, workspace, s.rows, s.N, activation, bf16, stream)
+                                     : launch_copies({grad, grad_row, s.rows, s.N, workspace}, {}, bf16, stream);
         if (e != hipSuccess) return status_of(e);
         a.q = workspace;
-        a.q_ld = s.width;
+        a.q_ld = padded(s.width, bf16);
+        a.q_padded = true;
     }
-    float *part = (float *)((char *)workspace + room.dz);
+    void *rest = (char *)workspace + room.dz;
     if (grad_x != nullptr) {
         Product b = a;
         b.p = weight;
@@ -123,7 +130,7 @@ int backward(bool gated, const void *grad, const void *x, const void *weight, co
         b.nq = s.rows;
         b.nk = s.width;
         b.out = grad_x;
-        const hipError_t e = launch_product(kGradX, b, part, bf16, stream);
+        const hipError_t e = launch_product(kGradX, b, rest, bf16, stream);
         if (e != hipSuccess) return status_of(e);
     }
     if (grad_weight != nullptr) {
@@ -134,7 +141,7 @@ int backward(bool gated, const void *grad, const void *x, const void *weight, co
         a.nk = s.rows;
         a.out = grad_weight;
         a.sums = grad_bias;
-        const hipError_t e = launch_product(kGradWeight, a, part, bf16, stream);
+        const hipError_t e = launch_product(kGradWeight, a, rest, bf16, stream);
         if (e != hipSuccess) return status_of(e);
     }
     return DDPM_OK;

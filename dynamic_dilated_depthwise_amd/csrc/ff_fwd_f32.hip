@@ -4,7 +4,7 @@
 namespace ddpm {
 namespace ff {
 
-hipError_t product_fwd_f32(const Product &a, float *part, hipStream_t stream) { return product<float, kForward>(a, part, stream); }
+hipError_t product_fwd_f32(const Product &a, void *work, hipStream_t stream) { return product<float, kForward>(a, work, stream); }
 
 }  // namespace ff
 }  // namespace ddpm

@@ -23,6 +23,7 @@
 
 #include <type_traits>
 
+#include "ff_curves.hpp"
 #include "ff_launch.hpp"
 #include "seq_common.hpp"
 
@@ -282,26 +283,6 @@ __device__ __forceinline__ void write8(T *p, int64_t n, const float (&v)[8]) {
 #pragma unroll
         for (int e = 0; e < 7; ++e)
             if (e < n) p[e] = Elem<T>::from_f32(v[e]);
-    }
-}
-
-template <int ACT> __device__ __forceinline__ float curve_of(float z) {
-    if constexpr (ACT == DDPM_ACT_RELU) return z < 0.f ? 0.f : z;  // NaN stays
-    else if constexpr (ACT == DDPM_ACT_SILU) return z / (1.f + expf(-z));
-    else if constexpr (ACT == DDPM_ACT_GELU) return 0.5f * z * erfcf(-0.70710678118654752f * z);  // no cancellation below zero
-    else return z;
-}
-// v = act(v), the choice outside the loop.
-__device__ __forceinline__ void activate(float (&v)[8], int act) {
-    if (act == DDPM_ACT_RELU) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = curve_of<DDPM_ACT_RELU>(v[e]);
-    } else if (act == DDPM_ACT_SILU) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = curve_of<DDPM_ACT_SILU>(v[e]);
-    } else if (act == DDPM_ACT_GELU) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = curve_of<DDPM_ACT_GELU>(v[e]);
     }
 }
 

@@ -4,7 +4,7 @@
 namespace ddpm {
 namespace ff {
 
-hipError_t product_gradx_bf16(const Product &a, float *part, hipStream_t stream) { return product<bf16_t, kGradX>(a, part, stream); }
+hipError_t product_gradx_bf16(const Product &a, void *work, hipStream_t stream) { return product<bf16_t, kGradX>(a, work, stream); }
 
 }  // namespace ff
 }  // namespace ddpm

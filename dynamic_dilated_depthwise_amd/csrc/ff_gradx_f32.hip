@@ -4,7 +4,7 @@
 namespace ddpm {
 namespace ff {
 
-hipError_t product_gradx_f32(const Product &a, float *part, hipStream_t stream) { return product<float, kGradX>(a, part, stream); }
+hipError_t product_gradx_f32(const Product &a, void *work, hipStream_t stream) { return product<float, kGradX>(a, work, stream); }
 
 }  // namespace ff
 }  // namespace ddpm

@@ -15,6 +15,7 @@ namespace ff {
 struct Product {
     const void *p, *q;
     int64_t p_ld, q_ld, np, nq, nk;
+    bool q_padded;                      // Q's rows end in zeros up to whole 16-byte chunks
     void *out;
     void *sums;                         // weight's gradient: [nq], sums over k of Q
     float *saved;                       // forward: what the activation is applied to, or null
@@ -31,9 +32,20 @@ struct Product {
 
 enum Kind { kForward, kGatedForward, kGradX, kGradWeight };
 
-// Floats that launch_product needs at `part` (for these sizes, any strides and alignment).
-int64_t product_floats(Kind kind, int64_t np, int64_t nq, int64_t nk, bool bf16);
-hipError_t launch_product(Kind kind, const Product &a, float *part, bool bf16, hipStream_t stream);
+// Bytes that launch_product needs at `work` (for these sizes, any strides and alignment).
+int64_t product_bytes(Kind kind, int64_t np, int64_t nq, int64_t nk, bool bf16);
+hipError_t launch_product(Kind kind, const Product &a, void *work, bool bf16, hipStream_t stream);
+
+// Rows of whole 128-byte lines, their last 16-byte chunk filled up with zeros: copies of an operand
+// whose rows would otherwise start anywhere.
+__host__ __device__ inline int64_t padded(int64_t cols, bool bf16) { return (cols + (bf16 ? 63 : 31)) / (bf16 ? 64 : 32) * (bf16 ? 64 : 32); }
+struct Copy {
+    const void *src;
+    int64_t ld, rows, cols;
+    void *dst;  // [rows, padded(cols)]; 16-byte aligned
+};
+// One or two copies; the second may have no rows.
+hipError_t launch_copies(const Copy &a, const Copy &b, bool bf16, hipStream_t stream);
 
 // The forward products of few rows (ff_rows.hip): up to kMostRows, of which launch_product takes it for
 // kFewRows, or all of them where the operands cannot go straight to LDS.
@@ -42,6 +54,7 @@ hipError_t launch_rows(bool gated, const Product &a, bool bf16, hipStream_t stre
 
 // dz = grad * act'(saved), [rows, N]; gated: saved [rows, 2 N] and dz [rows, 2 N],
 // the gate's half grad * u * act'(g), the other grad * act(g).
+// dz's rows are padded as a Copy's.
 hipError_t launch_dz(bool gated, const void *grad, int64_t grad_ld, const float *saved, void *dz, int64_t rows, int64_t N,
                      int act, bool bf16, hipStream_t stream);
 

@@ -1,5 +1,6 @@
-// ff_point.hip -- the gradient of an activation's or a gate's input, element by element.  Bound by
-// memory; a thread takes eight neighbouring columns.
+// ff_point.hip -- the gradient of an activation's or a gate's input, element by element, and copies of
+// operands to rows of whole chunks.  Bound by memory; a thread takes eight neighbouring columns, or a
+// chunk.
 #include "ff_gemm.hpp"
 
 namespace ddpm {
@@ -22,57 +23,50 @@ __device__ __forceinline__ Place place_of(int64_t i, int64_t per) {
     return {r, (i - r * per) * 8};
 }
 
-template <int ACT> __device__ __forceinline__ void slopes(const float (&z)[8], float (&d)[8]) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        if constexpr (ACT == DDPM_ACT_RELU) {
-            d[e] = z[e] > 0.f ? 1.f : z[e] <= 0.f ? 0.f : z[e];
-        } else if constexpr (ACT == DDPM_ACT_SILU) {
-            const float s = 1.f / (1.f + expf(-z[e]));
-            d[e] = s * (1.f + z[e] * (1.f - s));
-        } else {
-            d[e] = 0.5f * erfcf(-0.70710678118654752f * z[e]) + z[e] * 0.39894228040143268f * expf(-0.5f * z[e] * z[e]);
-        }
-    }
-}
-__device__ __forceinline__ void slope(const float (&z)[8], float (&d)[8], int act) {
-    if (act == DDPM_ACT_RELU) {
-        slopes<DDPM_ACT_RELU>(z, d);
-    } else if (act == DDPM_ACT_SILU) {
-        slopes<DDPM_ACT_SILU>(z, d);
-    } else if (act == DDPM_ACT_GELU) {
-        slopes<DDPM_ACT_GELU>(z, d);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) d[e] = 1.f;
-    }
-}
-
 template <typename T, bool GATED>
 __global__ __launch_bounds__(kThreads) void dz_kernel(const T *__restrict__ grad, int64_t grad_ld, const float *__restrict__ saved,
-                                                      T *__restrict__ dz, int64_t rows, int64_t N, int act) {
+                                                      T *__restrict__ dz, int64_t ld, int64_t rows, int64_t N, int act) {
     const int64_t per = (N + 7) / 8, all = rows * per, stride = (int64_t)gridDim.x * kThreads;
     for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < all; i += stride) {
         const Place at = place_of(i, per);
         const int64_t n = N - at.col;
-        float g[8], z[8], d[8];
+        float g[8], z[8], v[8], d[8];
         read8<T>(grad + at.row * grad_ld + at.col, n, g);
-        const int64_t o = at.row * (GATED ? 2 * N : N) + at.col;
-        read8<float>(saved + o, n, z);
-        slope(z, d, act);
+        const float *s = saved + at.row * (GATED ? 2 * N : N) + at.col;
+        T *o = dz + at.row * ld + at.col;
+        read8<float>(s, n, z);
+        slopes(z, v, d, act);
         if constexpr (GATED) {
             float u[8];
-            read8<float>(saved + o + N, n, u);
-            activate(z, act);
+            read8<float>(s + N, n, u);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) { d[e] = g[e] * u[e] * d[e]; z[e] = g[e] * z[e]; }
-            write8<T>(dz + o, n, d);
-            write8<T>(dz + o + N, n, z);
+            for (int e = 0; e < 8; ++e) { d[e] = g[e] * u[e] * d[e]; v[e] = g[e] * v[e]; }
+            write8<T>(o, n, d);
+            write8<T>(o + N, n, v);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) d[e] *= g[e];
-            write8<T>(dz + o, n, d);
+            write8<T>(o, n, d);
         }
+        if (n <= 8) {  // the row's last columns: and the zeros of its last chunk
+            const int64_t width = GATED ? 2 * N : N;
+            for (int64_t c = width; c % kVec<T> != 0; ++c) dz[at.row * ld + c] = 0;
+        }
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void copies_kernel(const Copy a, const Copy b) {
+    constexpr int kPer = kVec<T>;
+    const int64_t pa = (a.cols + kPer - 1) / kPer, pb = (b.cols + kPer - 1) / kPer, na = a.rows * pa, all = na + b.rows * pb;
+    const int64_t stride = (int64_t)gridDim.x * kThreads;
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < all; i += stride) {
+        const Copy &c = i < na ? a : b;
+        const int64_t k = i < na ? i : i - na, per = i < na ? pa : pb;
+        const Place at = place_of(k, per);
+        const int64_t col = at.col / 8 * kPer;
+        const u32x4 v = load_vec<T>((const T *)c.src + at.row * c.ld + col, c.cols - col);
+        *(u32x4 *)((T *)c.dst + at.row * padded(c.cols, Elem<T>::is_bf16) + col) = v;
     }
 }
 
@@ -85,8 +79,9 @@ template <typename T>
 hipError_t dz_of(bool gated, const void *grad, int64_t grad_ld, const float *saved, void *dz, int64_t rows, int64_t N, int act,
                  hipStream_t stream) {
     const dim3 grid(blocks_for(rows, N)), threads(kThreads);
-    if (gated) hipLaunchKernelGGL((dz_kernel<T, true>), grid, threads, 0, stream, (const T *)grad, grad_ld, saved, (T *)dz, rows, N, act);
-    else hipLaunchKernelGGL((dz_kernel<T, false>), grid, threads, 0, stream, (const T *)grad, grad_ld, saved, (T *)dz, rows, N, act);
+    const int64_t ld = padded(gated ? 2 * N : N, Elem<T>::is_bf16);
+    if (gated) hipLaunchKernelGGL((dz_kernel<T, true>), grid, threads, 0, stream, (const T *)grad, grad_ld, saved, (T *)dz, ld, rows, N, act);
+    else hipLaunchKernelGGL((dz_kernel<T, false>), grid, threads, 0, stream, (const T *)grad, grad_ld, saved, (T *)dz, ld, rows, N, act);
     return hipGetLastError();
 }
 
@@ -96,6 +91,14 @@ hipError_t launch_dz(bool gated, const void *grad, int64_t grad_ld, const float 
                      int act, bool bf16, hipStream_t stream) {
     return bf16 ? dz_of<bf16_t>(gated, grad, grad_ld, saved, dz, rows, N, act, stream)
                 : dz_of<float>(gated, grad, grad_ld, saved, dz, rows, N, act, stream);
+}
+
+hipError_t launch_copies(const Copy &a, const Copy &b, bool bf16, hipStream_t stream) {
+    const int64_t chunks = (a.rows * padded(a.cols, bf16) + b.rows * padded(b.cols, bf16)) / (bf16 ? 8 : 4);
+    const dim3 grid(blocks_for(chunks, 8)), threads(kThreads);
+    if (bf16) hipLaunchKernelGGL((copies_kernel<bf16_t>), grid, threads, 0, stream, a, b);
+    else hipLaunchKernelGGL((copies_kernel<float>), grid, threads, 0, stream, a, b);
+    return hipGetLastError();
 }
 
 }  // namespace ff

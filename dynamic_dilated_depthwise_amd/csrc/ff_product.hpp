@@ -16,9 +16,9 @@ template <> struct KindOf<kGradWeight> { static constexpr Side sp = kDown, sq = 
 // Whether an operand can go straight to LDS: whole 16-byte chunks, and a step's tile within a
 // buffer's offsets.  rows: those of the tile in memory.
 template <typename T>
-inline bool direct_ok(Side s, const void *p, int64_t ld, int64_t extent, int64_t nk, int64_t rows) {
+inline bool direct_ok(Side s, const void *p, int64_t ld, int64_t extent, int64_t nk, int64_t rows, bool padded) {
     constexpr int64_t per = 16 / (int64_t)sizeof(T);
-    if ((uintptr_t)p % 16 != 0 || ld % per != 0 || (s == kAlong ? nk : extent) % per != 0) return false;
+    if ((uintptr_t)p % 16 != 0 || ld % per != 0 || (!padded && (s == kAlong ? nk : extent) % per != 0)) return false;
     return (rows * ld + kStep<T>) * (int64_t)sizeof(T) < (int64_t)kRecords;
 }
 
@@ -115,11 +115,38 @@ inline bool few_rows(Kind kind, int64_t nq, bool direct) {
     return (kind == kForward || kind == kGatedForward) && nq <= (direct ? kFewRows : kMostRows);
 }
 
-// Floats of the pieces' results.
-inline int64_t part_floats(bool bf16, Kind kind, const Cut &c) {
+// Bytes of the pieces' results.
+inline int64_t part_bytes(bool bf16, Kind kind, const Cut &c) {
+    if (c.pieces == 1) return 0;
     const Form f = form_of(bf16, kind, c.form);
     const int64_t kp = f.kp(), kq = f.kq();
-    return c.slots() * (kp * kq + (kind == kGradWeight ? kq : 0));
+    return c.slots() * (kp * kq + (kind == kGradWeight ? kq : 0)) * 4;
+}
+
+// Operands whose rows are no whole chunks (P's, and Q's where it does not come padded) are copied to
+// rows that are, where that costs less than the form for any alignment: that form takes 1.7 times as
+// long with both operands along their rows, and 3.3 and 5.5 times with one and both read by columns
+// (bfloat16, products of 4095^3), a copy a launch and two passes over the operand.
+struct Copies {
+    bool p = false, q = false;
+    int64_t p_bytes = 0, q_bytes = 0;
+};
+template <typename T>
+inline Copies copies_for(Kind kind, int64_t np, int64_t nq, int64_t nk) {
+    constexpr bool bf16 = Elem<T>::is_bf16;
+    constexpr int64_t per = 16 / (int64_t)sizeof(T);
+    Copies c;
+    const bool forward = kind == kForward || kind == kGatedForward;
+    const int64_t p_cols = forward ? nk : np, p_rows = forward ? (kind == kGatedForward ? 2 * np : np) : nk;
+    if (p_cols % per == 0 || few_rows(kind, nq, false)) return c;
+    c.p = true;
+    c.q = forward;  // the backward's Q is dz, which comes padded
+    c.p_bytes = p_rows * padded(p_cols, bf16) * (int64_t)sizeof(T);
+    c.q_bytes = c.q ? nq * padded(nk, bf16) * (int64_t)sizeof(T) : 0;
+    const double slower = !bf16 ? 1.3 : forward ? 1.7 : kind == kGradX ? 3.3 : 5.5;
+    const double copied = cut_of<T>(kind, np, nq, nk, true).cost + 5. + 2. * (double)(c.p_bytes + c.q_bytes) / kBytes;
+    if (cut_of<T>(kind, np, nq, nk, false).cost * slower < copied) c = Copies();
+    return c;
 }
 
 template <typename G>
@@ -140,14 +167,34 @@ hipError_t launch_gemm(Product &a, const Cut &c, hipStream_t stream) {
 }
 
 template <typename T, Kind K>
-hipError_t product(Product a, float *part, hipStream_t stream) {
+hipError_t product(Product a, void *work, hipStream_t stream) {
     constexpr Side sp = KindOf<K>::sp, sq = KindOf<K>::sq;
     constexpr Epi e = KindOf<K>::e;
-    const bool direct = direct_ok<T>(sp, a.p, a.p_ld, a.np, a.nk, K == kGatedForward ? a.np + 256 : 256) &&
-                        direct_ok<T>(sq, a.q, a.q_ld, a.nq, a.nk, 256);
-    if (few_rows(K, a.nq, direct)) return launch_rows(K == kGatedForward, a, Elem<T>::is_bf16, stream);
+    constexpr bool bf16 = Elem<T>::is_bf16, forward = K == kForward || K == kGatedForward;
+    bool p_padded = false;
+    const Copies copies = copies_for<T>(K, a.np, a.nq, a.nk);
+    if (copies.p) {
+        const int64_t width = K == kGatedForward ? 2 * a.np : a.np;
+        Copy p = {a.p, a.p_ld, forward ? width : a.nk, forward ? a.nk : a.np, work}, q = {};
+        a.p = p.dst;
+        a.p_ld = padded(p.cols, bf16);
+        p_padded = true;
+        work = (char *)work + copies.p_bytes;
+        if (copies.q) {
+            q = {a.q, a.q_ld, a.nq, a.nk, work};
+            a.q = q.dst;
+            a.q_ld = padded(q.cols, bf16);
+            a.q_padded = true;
+            work = (char *)work + copies.q_bytes;
+        }
+        const hipError_t r = launch_copies(p, q, bf16, stream);
+        if (r != hipSuccess) return r;
+    }
+    const bool direct = direct_ok<T>(sp, a.p, a.p_ld, a.np, a.nk, K == kGatedForward ? a.np + 256 : 256, p_padded) &&
+                        direct_ok<T>(sq, a.q, a.q_ld, a.nq, a.nk, 256, a.q_padded);
+    if (few_rows(K, a.nq, direct)) return launch_rows(K == kGatedForward, a, bf16, stream);
     const Cut c = cut_of<T>(K, a.np, a.nq, a.nk, direct);
-    a.part = part;
+    a.part = (float *)work;
 #define DDPM_FF_FORM(k, DIRECT)                                                                       \
     if (c.form == k) {                                                                                \
         constexpr Form f = form_of(Elem<T>::is_bf16, K, k);                                           \
