@@ -42,9 +42,9 @@ template <typename T> constexpr int kStep = kStepBytes / (int)sizeof(T);  // ele
 
 constexpr uint32_t kRecords = 0x7fffffe0u, kOutside = 0x7ffffff0u;  // of a buffer; an offset past it
 
-// All but N of this wave's loads to LDS are there and its own LDS accesses done; then the workgroup.
-__device__ __forceinline__ void arrive_all() {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+// All but this wave's last N loads to LDS are there and its own LDS accesses done; then the workgroup.
+template <int N> __device__ __forceinline__ void arrive_but() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"(N) : "memory");
 }
 __device__ __forceinline__ void arrive_lds() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
@@ -336,14 +336,15 @@ __device__ __forceinline__ void other_bias8(const Product &a, int64_t p, float (
 }
 
 // WP * WQ waves of 16 MP by 16 NQ each.
-template <typename T, Side SP, Side SQ, Epi E, int WP, int WQ, int MP, int NQ, bool DIRECT>
+template <typename T, Side SP, Side SQ, Epi E, int WP, int WQ, int MP, int NQ, int STAGES, bool DIRECT>
 struct Gemm {
     static constexpr Epi kE = E;
     static constexpr int kThreads = WP * WQ * kWave, kP = WP * MP * 16, kQ = WQ * NQ * 16;
     static constexpr int kStageBytes = (kP + kQ) * kStepBytes;
     static constexpr int kLd = 16 * MP + 4;  // floats of a row of the result in LDS
     static constexpr int kOutBytes = WP * WQ * 16 * kLd * 4;
-    static constexpr int kLds = 2 * kStageBytes > kOutBytes ? 2 * kStageBytes : kOutBytes;
+    static constexpr int kStages = DIRECT ? STAGES : 2;
+    static constexpr int kLds = kStages * kStageBytes > kOutBytes ? kStages * kStageBytes : kOutBytes;
 
     static constexpr int64_t kSlot = (int64_t)kP * kQ + (E == kWeight ? kQ : 0);  // floats of a piece's result
 
@@ -419,24 +420,35 @@ struct Gemm {
                 if (i < kP1) tile_p.ask(i, at, left, tid);
                 else tile_q.ask(i - kP1, at + kP * kStepBytes, left, tid);
             };
-#pragma unroll
-            for (int i = 0; i < kAll; ++i) ask(i, lds);
-            for (int s = 0; s < steps; ++s) {
-                char *now = lds + (s & 1) * kStageBytes, *next = lds + (~s & 1) * kStageBytes;
+            // Loads of kStages - 1 steps are under way behind the one that is computed; what is asked for
+            // past the last step is nothing (zeros for LDS that nobody reads), so that a wave's count of
+            // loads in flight is the same in every step.
+            const auto advance = [&] {
                 left -= kStep<T>;
                 tile_p.next();
                 tile_q.next();
-                arrive_all();  // the step is there, and nobody reads the other half any more
-                // The next step's chunks are asked for a few at a time: all of them at once would hold the
-                // wave up at its first read (gated 16384 x 2048 x 2 5632: see below).
-                compute(now, [&](int n) {
-                    constexpr int kEach = (kAll + kBetween - 1) / kBetween;
-                    if (s + 1 < steps) {
+            };
 #pragma unroll
-                        for (int i = n * kEach; i < (n + 1) * kEach && i < kAll; ++i) ask(i, next);
-                    }
-                });
+            for (int t = 0; t < kStages - 1; ++t) {
+#pragma unroll
+                for (int i = 0; i < kAll; ++i) ask(i, lds + t * kStageBytes);
+                advance();
             }
+            int now = 0, next = kStages - 1;
+            for (int s = 0; s < steps; ++s) {
+                arrive_but<(kStages - 2) * kAll>();  // the step is there, and nobody reads the one before it any more
+                // The chunks are asked for a few at a time: all of them at once would hold the wave up at
+                // its first read (grad_x of 8192^3 bfloat16 1065 -> 867 us).
+                compute(lds + now * kStageBytes, [&](int n) {
+                    constexpr int kEach = (kAll + kBetween - 1) / kBetween;
+#pragma unroll
+                    for (int i = n * kEach; i < (n + 1) * kEach && i < kAll; ++i) ask(i, lds + next * kStageBytes);
+                });
+                advance();
+                now = now + 1 == kStages ? 0 : now + 1;
+                next = next + 1 == kStages ? 0 : next + 1;
+            }
+            arrive_but<0>();
         } else {
             tile_p.fetch(left, tid);
             tile_q.fetch(left, tid);
@@ -454,8 +466,8 @@ struct Gemm {
                 }
                 compute(now, [](int) {});
             }
+            arrive_lds();
         }
-        arrive_lds();
 
         // Out through LDS, 16 rows of the wave's at a time, so that a lane has eight neighbouring columns
         // (the same ones in every row) and rows leave in whole runs.

@@ -22,12 +22,12 @@ inline bool direct_ok(Side s, const void *p, int64_t ld, int64_t extent, int64_t
     return (rows * ld + kStep<T>) * (int64_t)sizeof(T) < (int64_t)kRecords;
 }
 
-// The tiles that a call may take: waves in p and q, fragments of a wave in p and q, workgroups of a
-// compute unit, and the microseconds of a step of the contraction: of one workgroup's share where the
+// The tiles that a call may take: waves in p and q, fragments of a wave in p and q, stages, workgroups
+// of a compute unit, and the microseconds of a step of the contraction: of one workgroup's share where the
 // unit is full, and at least, with its loads on their way (measured: products of 8192^3 and 4096^3, and
 // of 512 x 2048 x 2048, whose few tiles are alone on their units).
 struct Form {
-    int wp, wq, mp, nq, per_cu;
+    int wp, wq, mp, nq, stages, per_cu;
     double busy, alone;
     constexpr int kp() const { return wp * mp * 16; }
     constexpr int kq() const { return wq * nq * 16; }
@@ -37,16 +37,18 @@ constexpr int kFormCount = 5, kGeneral = 1;  // kGeneral: the one for operands t
 // (256 x 256 with 16 waves 798 us at 8192^3, with 8 848; 128 x 128 with 8 1103, with 4 1370).  Where both
 // operands are read by columns 16 waves do not hold their addresses (1129 us, with 8 872).
 // float32: waves with large tiles, which split their operands for more products (256 x 256 with 8 waves
-// 692 us at 4096^3, with 16 1115; 128 x 128 with 4 830, with 8 1041).
+// 692 us at 4096^3, with 16 1115; 128 x 128 with 4 766, with 8 1041).
+// Stages: of LDS that steps' chunks are under way to or in; more than two where the tile leaves room and
+// a step is shorter than its loads' way (512 x 2048 x 2048 with 128 x 32: 16 -> 12 us with four).
 constexpr Form form_of(bool bf16, Kind kind, int k) {
-    constexpr Form low[] = {{4, 4, 4, 4, 1, 1.55, 1.5},   // 256 x 256
-                            {4, 2, 2, 4, 2, 0.54, 0.65},  // 128 x 128
-                            {2, 4, 2, 4, 2, 0.56, 0.7},   // 64 x 256: results of few columns
-                            {4, 1, 2, 4, 3, 0.33, 0.5},   // 128 x 64
-                            {4, 1, 2, 2, 3, 0.22, 0.43}}; // 128 x 32: few rows
-    constexpr Form full[] = {{2, 4, 8, 4, 1, 5.3, 5.3}, {2, 2, 4, 4, 2, 1.6, 1.9}, {1, 4, 4, 4, 2, 1.6, 1.9}, {4, 1, 2, 4, 3, 0.83, 1.4},
-                             {4, 1, 2, 2, 3, 0.49, 1.}};
-    constexpr Form weight = {2, 4, 8, 4, 1, 1.7, 1.6};
+    constexpr Form low[] = {{4, 4, 4, 4, 2, 1, 1.6, 1.3},     // 256 x 256
+                            {4, 2, 2, 4, 2, 2, 0.48, 0.5},    // 128 x 128
+                            {2, 4, 2, 4, 2, 2, 0.56, 0.53},   // 64 x 256: results of few columns
+                            {4, 1, 2, 4, 3, 2, 0.3, 0.39},    // 128 x 64
+                            {4, 1, 2, 2, 4, 2, 0.21, 0.28}};  // 128 x 32: few rows
+    constexpr Form full[] = {{2, 4, 8, 4, 2, 1, 5.3, 4.7}, {2, 2, 4, 4, 2, 2, 1.5, 1.75}, {1, 4, 4, 4, 2, 2, 1.53, 1.72}, {4, 1, 2, 4, 3, 2, 0.93, 1.19},
+                             {4, 1, 2, 2, 4, 2, 0.57, 0.8}};
+    constexpr Form weight = {2, 4, 8, 4, 2, 1, 1.65, 1.5};
     return bf16 ? k == 0 && kind == kGradWeight ? weight : low[k] : full[k];
 }
 
@@ -70,24 +72,28 @@ inline Cut cut_for(const Form &f, bool bf16, int64_t p, int64_t q, int64_t steps
     c.tiles_q = (q + f.kq() - 1) / f.kq();
     const double tiles = (double)c.tiles_p * (double)c.tiles_q, area = (double)f.kp() * f.kq();
     const int64_t slots = kUnits * f.per_cu;
-    // n workgroups of so many steps: whole rounds, and what the last one has on the fullest unit
-    const auto time = [&](int64_t n, int64_t steps_) {
-        const auto round = [&](int64_t m) { return m * f.busy > f.alone ? m * f.busy : f.alone; };
-        const int64_t last = (n % slots + kUnits - 1) / kUnits;
-        return steps_ * ((double)(n / slots) * round(f.per_cu) + (last ? round(last) : 0.));
-    };
+    // a step of m workgroups on a unit; n workgroups of so many steps: whole rounds, and what the last
+    // one has on the fullest unit
+    const auto step = [&](int64_t m) { return m == 0 ? 0. : m * f.busy > f.alone ? m * f.busy : f.alone; };
+    const auto last = [&](int64_t n) { return (n % slots + kUnits - 1) / kUnits; };
+    const auto time = [&](int64_t n, int64_t steps_) { return steps_ * ((double)(n / slots) * step(f.per_cu) + step(last(n))); };
     const double out = area * (bf16 ? 2 : 4) / kBytes, part = area * 8 / kBytes;
-    const int64_t n = (int64_t)(tiles < 4e9 ? tiles : 4e9), rest = n % slots;
+    const int64_t n = (int64_t)(tiles < 4e9 ? tiles : 4e9);
     c.whole = n;
     c.cost = time(n, steps) + n * out;
-    if (n < 16 * slots) {
-        const double before = time(n - rest, steps) + n * out + kSecondKernel;
+    for (const int64_t round : {slots, kUnits}) {
+        const int64_t rest = n % round, whole = n - rest, beside = f.per_cu - last(whole);
+        if (n >= 16 * slots) break;
         for (int s = 2; rest && s <= 256 && (steps + s - 1) / s >= kLeastSteps; ++s) {
-            const double t = before + time(rest * s, (steps + s - 1) / s) + rest * s * part;
+            const int64_t run = (steps + s - 1) / s, m = (rest * s + kUnits - 1) / kUnits;
+            // pieces that find room beside the last round's whole tiles run with them
+            const double t = (last(whole) != 0 && m <= beside ? time(whole, steps) + run * (step(last(whole) + m) - step(last(whole)))
+                                                              : time(whole, steps) + time(rest * s, run)) +
+                             n * out + kSecondKernel + rest * s * part;
             if (t < c.cost) {
                 c.cost = t;
                 c.pieces = s;
-                c.whole = n - rest;
+                c.whole = whole;
             }
         }
     }
@@ -198,7 +204,7 @@ hipError_t product(Product a, void *work, hipStream_t stream) {
 #define DDPM_FF_FORM(k, DIRECT)                                                                       \
     if (c.form == k) {                                                                                \
         constexpr Form f = form_of(Elem<T>::is_bf16, K, k);                                           \
-        return launch_gemm<Gemm<T, sp, sq, e, f.wp, f.wq, f.mp, f.nq, DIRECT>>(a, c, stream);         \
+        return launch_gemm<Gemm<T, sp, sq, e, f.wp, f.wq, f.mp, f.nq, f.stages, DIRECT>>(a, c, stream);         \
     }
     if (!direct) {
         DDPM_FF_FORM(kGeneral, false)
