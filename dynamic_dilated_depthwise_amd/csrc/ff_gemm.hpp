@@ -162,18 +162,24 @@ template <typename T> struct OperandOf { typedef Split type; };
 template <> struct OperandOf<bf16_t> { typedef bf16x8 type; };
 template <typename T> using Operand = typename OperandOf<T>::type;
 
+// In pairs, as the conversion takes them: 11 instructions for two values.
 __device__ __forceinline__ Split split_of(const f32x4 &a, const f32x4 &b) {
-    Split r;
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    u32x4 part[kParts];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        float v = e < 4 ? a[e] : b[e - 4];
+    for (int e = 0; e < 4; ++e) {
+        f32x2 v = e < 2 ? f32x2{a[2 * e], a[2 * e + 1]} : f32x2{b[2 * e - 4], b[2 * e - 3]};
 #pragma unroll
         for (int k = 0; k < kParts; ++k) {
-            const __bf16 t = (__bf16)v;
-            r.part[k][e] = t;
-            v -= (float)t;
+            const uint32_t t = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
+            part[k][e] = t;
+            v[0] -= __uint_as_float(t << 16);
+            v[1] -= __uint_as_float(t & 0xffff0000u);
         }
     }
+    Split r;
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) r.part[k] = __builtin_bit_cast(bf16x8, part[k]);
     return r;
 }
 
@@ -528,7 +534,7 @@ struct Gemm {
     static constexpr int kFinishThreads = 256, kReds = E == kGated ? 17 : 9;
     static constexpr int kPerTile = (E == kGated ? kP / 2 : kP) * kQ / 8;
     static_assert(kPerTile % kFinishThreads == 0, "a workgroup stays in one tile");
-    __host__ __device__ static int lanes(int pieces) { return pieces >= 16 ? 8 : pieces >= 4 ? 2 : 1; }
+    __host__ __device__ static int lanes(int pieces) { return pieces >= 64 ? 32 : pieces >= 16 ? 8 : pieces >= 4 ? 2 : 1; }
     __device__ static void finish(const Product &a, float (*red)[kReds]) {
         constexpr int kCols = (E == kGated ? kP / 2 : kP) / 8;
         const int kLanes = lanes(a.pieces), items = kFinishThreads / kLanes;

@@ -37,7 +37,7 @@ constexpr int kFormCount = 5, kGeneral = 1;  // kGeneral: the one for operands t
 // (256 x 256 with 16 waves 798 us at 8192^3, with 8 848; 128 x 128 with 8 1103, with 4 1370).  Where both
 // operands are read by columns 16 waves do not hold their addresses (1129 us, with 8 872).
 // float32: waves with large tiles, which split their operands for more products (256 x 256 with 8 waves
-// 692 us at 4096^3, with 16 1115; 128 x 128 with 4 766, with 8 1041).
+// 609 us at 4096^3; before the split took pairs 692, with 16 1115; 128 x 128 with 4 766, with 8 1041).
 // Stages: of LDS that steps' chunks are under way to or in; more than two where the tile leaves room and
 // a step is shorter than its loads' way (512 x 2048 x 2048 with 128 x 32: 16 -> 12 us with four).
 constexpr Form form_of(bool bf16, Kind kind, int k) {
@@ -46,8 +46,11 @@ constexpr Form form_of(bool bf16, Kind kind, int k) {
                             {2, 4, 2, 4, 2, 2, 0.56, 0.53},   // 64 x 256: results of few columns
                             {4, 1, 2, 4, 3, 2, 0.3, 0.39},    // 128 x 64
                             {4, 1, 2, 2, 4, 2, 0.21, 0.28}};  // 128 x 32: few rows
-    constexpr Form full[] = {{2, 4, 8, 4, 2, 1, 5.3, 4.7}, {2, 2, 4, 4, 2, 2, 1.5, 1.75}, {1, 4, 4, 4, 2, 2, 1.53, 1.72}, {4, 1, 2, 4, 3, 2, 0.93, 1.19},
-                             {4, 1, 2, 2, 4, 2, 0.57, 0.8}};
+    constexpr Form full[] = {{2, 4, 8, 4, 2, 1, 4.75, 4.},
+                             {2, 2, 4, 4, 2, 2, 1.36, 1.47},
+                             {1, 4, 4, 4, 2, 2, 1.38, 1.55},
+                             {4, 1, 2, 4, 3, 2, 0.82, 1.},
+                             {4, 1, 2, 2, 4, 2, 0.49, 0.64}};
     constexpr Form weight = {2, 4, 8, 4, 2, 1, 1.65, 1.5};
     return bf16 ? k == 0 && kind == kGradWeight ? weight : low[k] : full[k];
 }
