@@ -23,9 +23,8 @@ inline bool direct_ok(Side s, const void *p, int64_t ld, int64_t extent, int64_t
 }
 
 // The tiles that a call may take: waves in p and q, fragments of a wave in p and q, stages, workgroups
-// of a compute unit, and the microseconds of a step of the contraction: of one workgroup's share where the
-// unit is full, and at least, with its loads on their way (measured: products of 8192^3 and 4096^3, and
-// of 512 x 2048 x 2048, whose few tiles are alone on their units).
+// of a compute unit, and the microseconds of a step of the contraction: of one workgroup's share where
+// every unit is full, and where every unit has one.
 struct Form {
     int wp, wq, mp, nq, stages, per_cu;
     double busy, alone;
@@ -41,18 +40,26 @@ constexpr int kFormCount = 5, kGeneral = 1;  // kGeneral: the one for operands t
 // Stages: of LDS that steps' chunks are under way to or in; more than two where the tile leaves room and
 // a step is shorter than its loads' way (512 x 2048 x 2048 with 128 x 32: 16 -> 12 us with four).
 constexpr Form form_of(bool bf16, Kind kind, int k) {
-    constexpr Form low[] = {{4, 4, 4, 4, 2, 1, 1.6, 1.3},     // 256 x 256
-                            {4, 2, 2, 4, 2, 2, 0.48, 0.5},    // 128 x 128
-                            {2, 4, 2, 4, 2, 2, 0.56, 0.53},   // 64 x 256: results of few columns
-                            {4, 1, 2, 4, 3, 2, 0.3, 0.39},    // 128 x 64
-                            {4, 1, 2, 2, 4, 2, 0.21, 0.28}};  // 128 x 32: few rows
-    constexpr Form full[] = {{2, 4, 8, 4, 2, 1, 4.75, 4.},
-                             {2, 2, 4, 4, 2, 2, 1.36, 1.47},
-                             {1, 4, 4, 4, 2, 2, 1.38, 1.55},
-                             {4, 1, 2, 4, 3, 2, 0.82, 1.},
-                             {4, 1, 2, 2, 4, 2, 0.49, 0.64}};
-    constexpr Form weight = {2, 4, 8, 4, 2, 1, 1.65, 1.5};
-    return bf16 ? k == 0 && kind == kGradWeight ? weight : low[k] : full[k];
+    constexpr Form low[] = {{4, 4, 4, 4, 2, 1, 0, 0},   // 256 x 256
+                            {4, 2, 2, 4, 2, 2, 0, 0},   // 128 x 128
+                            {2, 4, 2, 4, 2, 2, 0, 0},   // 64 x 256: results of few columns
+                            {4, 1, 2, 4, 3, 2, 0, 0},   // 128 x 64
+                            {4, 1, 2, 2, 4, 2, 0, 0}};  // 128 x 32: few rows
+    constexpr Form full[] = {{2, 4, 8, 4, 2, 1, 0, 0}, {2, 2, 4, 4, 2, 2, 0, 0}, {1, 4, 4, 4, 2, 2, 0, 0}, {4, 1, 2, 4, 3, 2, 0, 0},
+                             {4, 1, 2, 2, 4, 2, 0, 0}};
+    // Of 256 tiles and of 512 (256 where one fits), the difference between 72 steps and 24.
+    constexpr double times[2][3][5][2] = {{{{4.56, 4.56}, {1.32, 1.55}, {1.35, 1.59}, {0.81, 0.95}, {0.50, 0.62}},    // float32: y
+                                           {{4.45, 4.45}, {1.32, 1.45}, {1.36, 1.68}, {0.81, 0.96}, {0.50, 0.65}},    // grad_x
+                                           {{4.60, 4.60}, {1.31, 1.67}, {1.39, 1.70}, {0.86, 1.29}, {0.57, 0.85}}},   // grad_W
+                                          {{{1.55, 1.55}, {0.45, 0.68}, {0.52, 0.77}, {0.28, 0.40}, {0.22, 0.26}},    // bfloat16
+                                           {{1.53, 1.53}, {0.45, 0.73}, {0.51, 0.77}, {0.27, 0.39}, {0.24, 0.31}},
+                                           {{1.55, 1.55}, {0.50, 0.84}, {0.51, 0.85}, {0.29, 0.50}, {0.27, 0.37}}}};
+    Form f = bf16 ? low[k] : full[k];
+    if (bf16 && kind == kGradWeight && k == 0) f.wp = 2, f.mp = 8;
+    const int row = kind == kGradX ? 1 : kind == kGradWeight ? 2 : 0;
+    f.busy = times[bf16][row][k][0];
+    f.alone = times[bf16][row][k][1];
+    return f;
 }
 
 // How a call is cut.  The tiles of the last round of workgroups, which would leave compute units idle,
