@@ -25,27 +25,63 @@ bool sizes_ok(Check &c, const Sizes &s, int activation) {
 }
 
 int64_t rounded(int64_t bytes) { return (bytes + 255) / 256 * 256; }
+int64_t element(bool bf16) { return bf16 ? 2 : 4; }
+int64_t chunk(bool bf16) { return 16 / element(bf16); }
 
-// Of the backward: dz, where it is another tensor than grad (behind an activation or a gate, and where
-// grad's rows are no whole chunks and many enough), then what the products need.
-struct Room {
-    int64_t dz, rest;
-    int64_t all() const { return dz + rest; }
-};
-Room backward_room(const Sizes &s, bool own_dz, int dtype) {
-    const bool bf16 = is_bf16(dtype);
-    return {own_dz ? rounded(s.rows * padded(s.width, bf16) * (bf16 ? 2 : 4)) : 0,
-            std::max(product_bytes(kGradX, s.C, s.rows, s.width, bf16), product_bytes(kGradWeight, s.C, s.width, s.rows, bf16))};
+// What the forward saves for an activation's or a gate's backward: z in float32, or, with few columns of
+// x and more of z than the caches hold, its bias alone, and the backward makes z again (training 16384
+// rows to 2 2048 columns, bfloat16, microseconds with z saved and made again: C = 256 323, 227; 768
+// 472, 419; 1536 750, 780; one half with gelu: 512 220, 213; 768 266, 275; 65536 rows to 2 128 in
+// float32: 64 114, 105; 128 143, 143.  Where z stays in the caches both are the same up to C = 256 and
+// saving is faster beyond).
+bool makes_again(const Sizes &s, bool bf16) {
+    const int64_t most = !bf16 ? 96 : s.width == s.N ? 512 : 768;
+    return s.C <= most && (double)s.rows * s.width >= 12e6;
 }
-constexpr double kManyFlops = 5e9;  // of one product: from here on a copy of grad costs less than what it saves
-bool copies_grad(const Sizes &s, int dtype) {
-    return s.N % (is_bf16(dtype) ? 8 : 4) != 0 && 2. * s.rows * s.N * s.C >= kManyFlops;
+int64_t saved_floats(const Sizes &s, bool through, bool bf16) { return !through ? 0 : makes_again(s, bf16) ? s.width : s.rows * s.width; }
+
+// x and weight, whose rows of C elements are no whole chunks, as copies with rows that are, where those
+// cost less than the products' form for any alignment.
+int64_t x_copy_bytes(const Sizes &s, bool bf16) { return rounded(s.rows * padded(s.C, bf16) * element(bf16)); }
+int64_t weight_copy_bytes(const Sizes &s, bool bf16) { return rounded(s.width * padded(s.C, bf16) * element(bf16)); }
+double forward_time(Kind kind, const Sizes &s, bool bf16, bool straight) {
+    return product_time(kind, s.N, s.rows, s.C, bf16, straight);
+}
+bool forward_copies(Kind kind, const Sizes &s, bool bf16) {
+    if (s.C % chunk(bf16) == 0 || s.rows <= kMostRows) return false;
+    return forward_time(kind, s, bf16, true) + copies_time(x_copy_bytes(s, bf16) + weight_copy_bytes(s, bf16)) <
+           forward_time(kind, s, bf16, false);
+}
+bool backward_copies(Kind kind, const Sizes &s, bool again, bool bf16) {
+    if (s.C % chunk(bf16) == 0) return false;
+    const auto all = [&](bool straight) {
+        return product_time(kGradX, s.C, s.rows, s.width, bf16, straight) +
+               product_time(kGradWeight, s.C, s.width, s.rows, bf16, straight) + (again ? forward_time(kind, s, bf16, straight) : 0.);
+    };
+    return all(true) + copies_time(x_copy_bytes(s, bf16) + weight_copy_bytes(s, bf16)) < all(false);
+}
+// Copies x and weight to `work` and points the product at them.
+hipError_t copy_operands(const Sizes &s, const void *&x, int64_t &x_row, const void *&weight, int64_t &weight_row, char *&work,
+                         bool bf16, hipStream_t stream) {
+    const Copy cx = {x, x_row, s.rows, s.C, work}, cw = {weight, s.C, s.width, s.C, work + x_copy_bytes(s, bf16)};
+    x = cx.dst;
+    weight = cw.dst;
+    x_row = weight_row = padded(s.C, bf16);
+    work += x_copy_bytes(s, bf16) + weight_copy_bytes(s, bf16);
+    return launch_copies(cx, cw, bf16, stream);
 }
 
 int64_t forward_workspace(Kind kind, const Sizes &s, int dtype) {
     Check c(dtype);
     if (!sizes_ok(c, s, DDPM_ACT_NONE)) return 0;
-    return product_bytes(kind, s.N, s.rows, s.C, is_bf16(dtype));
+    const bool bf16 = is_bf16(dtype);
+    return (forward_copies(kind, s, bf16) ? x_copy_bytes(s, bf16) + weight_copy_bytes(s, bf16) : 0) +
+           product_bytes(kind, s.N, s.rows, s.C, bf16);
+}
+
+int64_t saved_count(const Sizes &s, bool gated, int activation, int dtype) {
+    Check c(dtype);
+    return sizes_ok(c, s, activation) ? saved_floats(s, gated || activation != DDPM_ACT_NONE, is_bf16(dtype)) : 0;
 }
 
 int forward(Kind kind, const void *x, const void *weight, const void *bias, const void *residual, void *y, float *saved,
@@ -56,40 +92,68 @@ int forward(Kind kind, const void *x, const void *weight, const void *bias, cons
     c.stride(x_row);
     if (residual != nullptr) c.stride(residual_row);
     if (c.bad) return DDPM_ERR_INVALID_ARG;
+    const bool bf16 = is_bf16(dtype), through = kind == kGatedForward || activation != DDPM_ACT_NONE;
     c.input(x, extent(1, s.rows, s.C, 0, x_row), c.es());
     c.input(weight, (double)s.width * s.C, c.es());
     c.maybe_in(bias, s.width, c.es());
     if (residual != nullptr) c.input(residual, extent(1, s.rows, s.N, 0, residual_row), c.es());
     c.output(y, (double)s.rows * s.N, c.es());
-    c.maybe_out(saved, (double)s.rows * s.width, 4);
+    if (!through && saved != nullptr) return DDPM_ERR_INVALID_ARG;
+    c.maybe_out(saved, (double)saved_floats(s, through, bf16), 4);
     const int64_t room = forward_workspace(kind, s, dtype);
     if (room > 0) c.workspace(workspace, (double)room);
     const int st = c.done();
     if (st != DDPM_OK) return st;
+    (void)hipGetLastError();
+    char *work = (char *)workspace;
+    int64_t weight_row = s.C;
     Product a = {};
+    if (forward_copies(kind, s, bf16)) {
+        const hipError_t e = copy_operands(s, x, x_row, weight, weight_row, work, bf16, stream);
+        if (e != hipSuccess) return status_of(e);
+        a.p_padded = a.q_padded = true;
+    }
     a.p = weight;
     a.q = x;
-    a.p_ld = s.C;
+    a.p_ld = weight_row;
     a.q_ld = x_row;
     a.np = s.N;
     a.nq = s.rows;
     a.nk = s.C;
     a.out = y;
-    a.saved = saved;
+    (makes_again(s, bf16) ? a.kept : a.saved) = saved;
     a.bias = bias;
     a.residual = residual;
     a.residual_ld = residual_row;
     a.act = activation;
-    (void)hipGetLastError();
-    return status_of(launch_product(kind, a, workspace, is_bf16(dtype), stream));
+    return status_of(launch_product(kind, a, work, bf16, stream));
 }
 
-int64_t backward_workspace(const Sizes &s, bool through, int activation, int dtype) {
+// What the backward has in its workspace: dz, where it is another tensor than grad (behind an activation
+// or a gate, and where grad's rows are no whole chunks and many enough), copies, the products' pieces.
+struct Room {
+    bool own_dz, copies, again;
+    int64_t dz, all;
+};
+constexpr double kManyFlops = 5e9;  // of one product: from here on a copy of grad costs less than what it saves
+Room backward_room(Kind kind, const Sizes &s, bool through, bool bf16) {
+    Room r;
+    r.own_dz = through || (s.N % chunk(bf16) != 0 && 2. * s.rows * s.N * s.C >= kManyFlops);
+    r.again = through && makes_again(s, bf16);
+    r.copies = backward_copies(kind, s, r.again, bf16);
+    r.dz = r.own_dz ? rounded(s.rows * padded(s.width, bf16) * element(bf16)) : 0;
+    int64_t part = std::max(product_bytes(kGradX, s.C, s.rows, s.width, bf16), product_bytes(kGradWeight, s.C, s.width, s.rows, bf16));
+    if (r.again) part = std::max(part, product_bytes(kind, s.N, s.rows, s.C, bf16));
+    r.all = r.dz + (r.copies ? x_copy_bytes(s, bf16) + weight_copy_bytes(s, bf16) : 0) + part;
+    return r;
+}
+
+int64_t backward_workspace(Kind kind, const Sizes &s, bool through, int activation, int dtype) {
     Check c(dtype);
-    return sizes_ok(c, s, activation) ? backward_room(s, through || copies_grad(s, dtype), dtype).all() : 0;
+    return sizes_ok(c, s, activation) ? backward_room(kind, s, through, is_bf16(dtype)).all : 0;
 }
 
-int backward(bool gated, const void *grad, const void *x, const void *weight, const float *saved, void *grad_x,
+int backward(Kind kind, const void *grad, const void *x, const void *weight, const float *saved, void *grad_x,
              void *grad_weight, void *grad_bias, void *workspace, const Sizes &s, int64_t x_row, int64_t grad_row,
              int activation, int dtype, hipStream_t stream) {
     Check c(dtype);
@@ -97,54 +161,71 @@ int backward(bool gated, const void *grad, const void *x, const void *weight, co
     c.stride(x_row);
     c.stride(grad_row);
     if (c.bad) return DDPM_ERR_INVALID_ARG;
-    const bool through = gated || activation != DDPM_ACT_NONE, own_dz = through || copies_grad(s, dtype), bf16 = is_bf16(dtype);
+    const bool gated = kind == kGatedForward, through = gated || activation != DDPM_ACT_NONE, bf16 = is_bf16(dtype);
     c.input(grad, extent(1, s.rows, s.N, 0, grad_row), c.es());
     c.input(x, extent(1, s.rows, s.C, 0, x_row), c.es());
     c.input(weight, (double)s.width * s.C, c.es());
-    if (through) c.input(saved, (double)s.rows * s.width, 4);
+    if (through) c.input(saved, (double)saved_floats(s, through, bf16), 4);
     c.maybe_out(grad_x, (double)s.rows * s.C, c.es());
     c.maybe_out(grad_weight, (double)s.width * s.C, c.es());
     c.maybe_out(grad_bias, s.width, c.es());
-    const Room room = backward_room(s, own_dz, dtype);
-    if (room.all() > 0) c.workspace(workspace, (double)room.all());
+    const Room room = backward_room(kind, s, through, bf16);
+    if (room.all > 0) c.workspace(workspace, (double)room.all);
     const int st = c.done();
     if (st != DDPM_OK) return st;
     (void)hipGetLastError();
-    Product a = {};
-    a.q = grad;
-    a.q_ld = grad_row;
-    if (own_dz) {
-        const hipError_t e = through ? launch_dz(gated, grad, grad_row, saved, workspace, s.rows, s.N, activation, bf16, stream)
-                                     : launch_copies({grad, grad_row, s.rows, s.N, workspace}, {}, bf16, stream);
-        if (e != hipSuccess) return status_of(e);
-        a.q = workspace;
-        a.q_ld = padded(s.width, bf16);
-        a.q_padded = true;
+    char *work = (char *)workspace + room.dz;
+    int64_t weight_row = s.C;
+    hipError_t e = hipSuccess;
+    if (room.copies) e = copy_operands(s, x, x_row, weight, weight_row, work, bf16, stream);
+    if (e == hipSuccess && room.own_dz) {
+        if (room.again) {
+            Product z = {};
+            z.p = weight;
+            z.q = x;
+            z.p_ld = weight_row;
+            z.q_ld = x_row;
+            z.p_padded = z.q_padded = room.copies;
+            z.np = s.N;
+            z.nq = s.rows;
+            z.nk = s.C;
+            z.out = workspace;
+            z.kept = const_cast<float *>(saved);
+            z.grad = grad;
+            z.grad_ld = grad_row;
+            z.act = activation;
+            e = launch_product(kind, z, work, bf16, stream);
+        } else if (through) {
+            e = launch_dz(gated, grad, grad_row, saved, workspace, s.rows, s.N, activation, bf16, stream);
+        } else {
+            e = launch_copies({grad, grad_row, s.rows, s.N, workspace}, {}, bf16, stream);
+        }
     }
-    void *rest = (char *)workspace + room.dz;
-    if (grad_x != nullptr) {
+    Product a = {};
+    a.q = room.own_dz ? workspace : grad;
+    a.q_ld = room.own_dz ? padded(s.width, bf16) : grad_row;
+    a.q_padded = room.own_dz;
+    a.p_padded = room.copies;
+    a.np = s.C;
+    if (e == hipSuccess && grad_x != nullptr) {
         Product b = a;
         b.p = weight;
-        b.p_ld = s.C;
-        b.np = s.C;
+        b.p_ld = weight_row;
         b.nq = s.rows;
         b.nk = s.width;
         b.out = grad_x;
-        const hipError_t e = launch_product(kGradX, b, rest, bf16, stream);
-        if (e != hipSuccess) return status_of(e);
+        e = launch_product(kGradX, b, work, bf16, stream);
     }
-    if (grad_weight != nullptr) {
+    if (e == hipSuccess && grad_weight != nullptr) {
         a.p = x;
         a.p_ld = x_row;
-        a.np = s.C;
         a.nq = s.width;
         a.nk = s.rows;
         a.out = grad_weight;
         a.sums = grad_bias;
-        const hipError_t e = launch_product(kGradWeight, a, rest, bf16, stream);
-        if (e != hipSuccess) return status_of(e);
+        e = launch_product(kGradWeight, a, work, bf16, stream);
     }
-    return DDPM_OK;
+    return status_of(e);
 }
 
 }  // namespace
@@ -162,14 +243,18 @@ int ddpm_linear_fwd(const void *x, const void *weight, const void *bias, const v
                    dtype, stream);
 }
 
+int64_t ddpm_linear_saved(int64_t rows, int64_t C, int64_t N, int activation, int dtype) {
+    return saved_count({rows, C, N, N}, false, activation, dtype);
+}
+
 int64_t ddpm_linear_bwd_workspace(int64_t rows, int64_t C, int64_t N, int activation, int dtype) {
-    return backward_workspace({rows, C, N, N}, activation != DDPM_ACT_NONE, activation, dtype);
+    return backward_workspace(kForward, {rows, C, N, N}, activation != DDPM_ACT_NONE, activation, dtype);
 }
 
 int ddpm_linear_bwd(const void *grad, const void *x, const void *weight, const float *saved, void *grad_x,
                     void *grad_weight, void *grad_bias, void *workspace, int64_t rows, int64_t C, int64_t N, int64_t x_row,
                     int64_t grad_row, int activation, int dtype, hipStream_t stream) {
-    return backward(false, grad, x, weight, saved, grad_x, grad_weight, grad_bias, workspace, {rows, C, N, N}, x_row, grad_row,
+    return backward(kForward, grad, x, weight, saved, grad_x, grad_weight, grad_bias, workspace, {rows, C, N, N}, x_row, grad_row,
                     activation, dtype, stream);
 }
 
@@ -183,14 +268,18 @@ int ddpm_gated_linear_fwd(const void *x, const void *weight, const void *bias, v
                    stream);
 }
 
+int64_t ddpm_gated_linear_saved(int64_t rows, int64_t C, int64_t N, int dtype) {
+    return saved_count({rows, C, N, 2 * N}, true, DDPM_ACT_NONE, dtype);
+}
+
 int64_t ddpm_gated_linear_bwd_workspace(int64_t rows, int64_t C, int64_t N, int dtype) {
-    return backward_workspace({rows, C, N, 2 * N}, true, DDPM_ACT_NONE, dtype);
+    return backward_workspace(kGatedForward, {rows, C, N, 2 * N}, true, DDPM_ACT_NONE, dtype);
 }
 
 int ddpm_gated_linear_bwd(const void *grad, const void *x, const void *weight, const float *saved, void *grad_x,
                           void *grad_weight, void *grad_bias, void *workspace, int64_t rows, int64_t C, int64_t N,
                           int64_t x_row, int64_t grad_row, int activation, int dtype, hipStream_t stream) {
-    return backward(true, grad, x, weight, saved, grad_x, grad_weight, grad_bias, workspace, {rows, C, N, 2 * N}, x_row, grad_row,
+    return backward(kGatedForward, grad, x, weight, saved, grad_x, grad_weight, grad_bias, workspace, {rows, C, N, 2 * N}, x_row, grad_row,
                     activation, dtype, stream);
 }
 

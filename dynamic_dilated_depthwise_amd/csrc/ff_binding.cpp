@@ -47,6 +47,11 @@ Weight weight_of(const Call &c, PyObject *o, int64_t C, int64_t halves) {
 
 Tensor room(const Call &c, int64_t bytes) { return bytes > 0 ? c.bytes(bytes) : Tensor(); }
 
+// Floats of what the forward saves.
+int64_t saved_of(const Call &c, const Rows &r, const Weight &w, int act, bool gated) {
+    return gated ? ddpm_gated_linear_saved(r.rows, r.C, w.N, c.dtype) : ddpm_linear_saved(r.rows, r.C, w.N, act, c.dtype);
+}
+
 PyObject *forward(PyObject *const *a, bool gated) {
     PyObject *residual = gated ? Py_None : a[3];
     PyObject *const *rest = a + (gated ? 3 : 4);  // activation save stream
@@ -64,7 +69,7 @@ PyObject *forward(PyObject *const *a, bool gated) {
     }
     const Tensor y = c.empty(out);
     Tensor saved;
-    if (truth(rest[1]) && (gated || act != DDPM_ACT_NONE)) saved = c.empty(with_last(c.x, w.width), at::kFloat);
+    if (truth(rest[1]) && (gated || act != DDPM_ACT_NONE)) saved = c.empty({saved_of(c, r, w, act, gated)}, at::kFloat);
     const Tensor work = room(c, gated ? ddpm_gated_linear_fwd_workspace(r.rows, r.C, w.N, c.dtype)
                                       : ddpm_linear_fwd_workspace(r.rows, r.C, w.N, c.dtype));
     if (gated)
@@ -86,7 +91,7 @@ PyObject *backward(PyObject *const *a, bool gated) {
     const Tensor &grad = tensor(a[0], "grad");
     const int act = activation_of(a[4]);
     const float *saved = nullptr;
-    if (gated || act != DDPM_ACT_NONE) saved = (const float *)c.like(a[3], "saved", at::kFloat, with_last(c.x, w.width));
+    if (gated || act != DDPM_ACT_NONE) saved = (const float *)c.like(a[3], "saved", at::kFloat, {saved_of(c, r, w, act, gated)});
     else if (a[3] != Py_None) refuse("saved must be None without an activation");
     Tensor gx, gw, gb;
     if (truth(a[5])) gx = c.empty(c.x.sizes());

@@ -292,6 +292,51 @@ __device__ __forceinline__ void write8(T *p, int64_t n, const float (&v)[8]) {
     }
 }
 
+// The bias of eight columns from p: of the gate's or the only half (half 0), or of the other (half 1).
+template <typename T>
+__device__ __forceinline__ void bias8(const Product &a, int64_t p, int half, float (&v)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    const int64_t at = half * a.np + p;
+    if (p >= a.np) return;
+    if (a.grad != nullptr) read8<float>(a.kept + at, a.np - p, v);
+    else if (a.bias != nullptr) read8<T>((const T *)a.bias + at, a.np - p, v);
+}
+// For the backward, in float32.
+__device__ __forceinline__ void keep8(const Product &a, int64_t p, int half, const float (&v)[8]) {
+    if (a.kept != nullptr && a.grad == nullptr && p < a.np) write8<float>(a.kept + half * a.np + p, a.np - p, v);
+}
+// Row q of dz: its zeros behind the last of `width` columns, up to a whole chunk.
+template <typename T>
+__device__ __forceinline__ void pad_row(T *row, int64_t width) {
+    for (int64_t c = width; c % kVec<T> != 0; ++c) row[c] = 0;
+}
+// dz of eight columns from p: grad act'(z); gated: grad u act'(g) and grad act(g).
+template <typename T>
+__device__ __forceinline__ void finish_dz(T *row, int64_t p, int64_t N, const T *grad, int act, const float (&z)[8]) {
+    const int64_t n = N - p;
+    float g[8], v[8], d[8];
+    read8<T>(grad + p, n, g);
+    slopes(z, v, d, act);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) d[e] *= g[e];
+    write8<T>(row + p, n, d);
+    if (n <= 8) pad_row(row, N);
+}
+template <typename T>
+__device__ __forceinline__ void finish_gated_dz(T *row, int64_t p, int64_t N, const T *grad, int act, const float (&z)[8],
+                                                const float (&u)[8]) {
+    const int64_t n = N - p;
+    float g[8], v[8], d[8];
+    read8<T>(grad + p, n, g);
+    slopes(z, v, d, act);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) { d[e] = g[e] * u[e] * d[e]; v[e] = g[e] * v[e]; }
+    write8<T>(row + p, n, d);
+    write8<T>(row + N + p, n, v);
+    if (n <= 8) pad_row(row, 2 * N);
+}
+
 // What follows the product for eight neighbouring columns p of row q: z without its bias.
 template <typename T>
 __device__ __forceinline__ void finish_linear(const Product &a, int64_t q, int64_t p, float (&z)[8], const float (&bias)[8]) {
@@ -299,6 +344,10 @@ __device__ __forceinline__ void finish_linear(const Product &a, int64_t q, int64
     if (q >= a.nq || n <= 0) return;
 #pragma unroll
     for (int e = 0; e < 8; ++e) z[e] += bias[e];
+    if (a.grad != nullptr) {
+        finish_dz<T>((T *)a.out + q * padded(a.np, Elem<T>::is_bf16), p, a.np, (const T *)a.grad + q * a.grad_ld, a.act, z);
+        return;
+    }
     if (a.saved != nullptr) write8<float>(a.saved + q * a.np + p, n, z);
     activate(z, a.act);
     if (a.residual != nullptr) {
@@ -317,6 +366,10 @@ __device__ __forceinline__ void finish_gated(const Product &a, int64_t q, int64_
     if (q >= a.nq || n <= 0) return;
 #pragma unroll
     for (int e = 0; e < 8; ++e) { g[e] += gb[e]; u[e] += ub[e]; }
+    if (a.grad != nullptr) {
+        finish_gated_dz<T>((T *)a.out + q * padded(2 * a.np, Elem<T>::is_bf16), p, a.np, (const T *)a.grad + q * a.grad_ld, a.act, g, u);
+        return;
+    }
     if (a.saved != nullptr) {
         float *s = a.saved + q * 2 * a.np + p;
         write8<float>(s, n, g);
@@ -326,19 +379,6 @@ __device__ __forceinline__ void finish_gated(const Product &a, int64_t q, int64_
 #pragma unroll
     for (int e = 0; e < 8; ++e) g[e] *= u[e];
     write8<T>((T *)a.out + q * a.np + p, n, g);
-}
-template <typename T>
-__device__ __forceinline__ void bias8(const Product &a, int64_t p, float (&v)[8]) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 0.f;
-    if (a.bias != nullptr && p < a.np) read8<T>((const T *)a.bias + p, a.np - p, v);
-}
-
-template <typename T>
-__device__ __forceinline__ void other_bias8(const Product &a, int64_t p, float (&v)[8]) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 0.f;
-    if (a.bias != nullptr && p < a.np) read8<T>((const T *)a.bias + a.np + p, a.np - p, v);
 }
 
 // WP * WQ waves of 16 MP by 16 NQ each.
@@ -484,8 +524,15 @@ struct Gemm {
         const int at = kPair ? (c >> 1) * 32 + (c & 1) * 8 : c * 8;
         const int64_t p = kPair ? (p0 >> 1) + wp * MP * 8 + c * 8 : p0 + wp * MP * 16 + c * 8;
         float b0[8], b1[8];
-        if (E == kLinear || E == kGated) bias8<T>(a, p, b0);
-        if constexpr (E == kGated) other_bias8<T>(a, p, b1);
+        const bool keeps = q0 == 0 && piece == 0 && wq == 0 && r0 == 0;
+        if constexpr (E == kLinear || E == kGated) {
+            bias8<T>(a, p, 0, b0);
+            if (keeps) keep8(a, p, 0, b0);
+        }
+        if constexpr (E == kGated) {
+            bias8<T>(a, p, 1, b1);
+            if (keeps) keep8(a, p, 1, b1);
+        }
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
 #pragma unroll
@@ -583,12 +630,12 @@ struct Gemm {
             }
             if constexpr (E == kLinear) {
                 float b[8];
-                bias8<T>(a, p, b);
+                bias8<T>(a, p, 0, b);
                 finish_linear<T>(a, q, p, v, b);
             } else if constexpr (E == kGated) {
                 float g[8], u[8];
-                bias8<T>(a, p, g);
-                other_bias8<T>(a, p, u);
+                bias8<T>(a, p, 0, g);
+                bias8<T>(a, p, 1, u);
                 finish_gated<T>(a, q, p, v, w, g, u);
             } else if (q < a.nq && p < a.np) {
                 write8<T>((T *)a.out + q * a.np + p, a.np - p, v);

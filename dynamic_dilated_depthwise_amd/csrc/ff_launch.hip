@@ -28,13 +28,21 @@ static int64_t bytes_of(Kind kind, int64_t np, int64_t nq, int64_t nk) {
         if (few_rows(kind, nq, direct)) continue;
         most = std::max(most, part_bytes(Elem<T>::is_bf16, kind, cut_of<T>(kind, np, nq, nk, direct)));
     }
-    const Copies c = copies_for<T>(kind, np, nq, nk);
-    return most + c.p_bytes + c.q_bytes;
+    return most;
 }
 
 int64_t product_bytes(Kind kind, int64_t np, int64_t nq, int64_t nk, bool bf16) {
     return bf16 ? bytes_of<bf16_t>(kind, np, nq, nk) : bytes_of<float>(kind, np, nq, nk);
 }
+
+double product_time(Kind kind, int64_t np, int64_t nq, int64_t nk, bool bf16, bool straight) {
+    const double t = bf16 ? cut_of<bf16_t>(kind, np, nq, nk, straight).cost : cut_of<float>(kind, np, nq, nk, straight).cost;
+    // The form for any alignment takes 1.7 times as long with both operands along their rows, and 3.3 and
+    // 5.5 times with one and both read by columns (bfloat16, products of 4095^3; float32 1.1 to 1.4).
+    return straight ? t : t * (!bf16 ? 1.25 : kind == kGradX ? 3.3 : kind == kGradWeight ? 5.5 : 1.7);
+}
+
+double copies_time(int64_t bytes) { return 5. + 2. * (double)bytes / kBytes; }
 
 }  // namespace ff
 }  // namespace ddpm

@@ -15,13 +15,18 @@ namespace ff {
 struct Product {
     const void *p, *q;
     int64_t p_ld, q_ld, np, nq, nk;
-    bool q_padded;                      // Q's rows end in zeros up to whole 16-byte chunks
+    bool p_padded, q_padded;            // rows that end in zeros up to whole 16-byte chunks
     void *out;
     void *sums;                         // weight's gradient: [nq], sums over k of Q
     float *saved;                       // forward: what the activation is applied to, or null
     const void *bias, *residual;        // forward: or null
     int64_t residual_ld;
     int act;
+    // Where the backward makes z again: the forward writes its bias here in float32, and the backward's
+    // call has it with grad [nq, np], and out is dz (rows as launch_dz writes them).
+    float *kept;
+    const void *grad;
+    int64_t grad_ld;
     // The first `whole` of tiles_p * tiles_q tiles are a workgroup's each; the others are cut along the
     // contraction into `pieces` of `run` elements, whose results go to `part` in float32.
     uint32_t tiles_p, tiles_q, whole;
@@ -35,6 +40,10 @@ enum Kind { kForward, kGatedForward, kGradX, kGradWeight };
 // Bytes that launch_product needs at `work` (for these sizes, any strides and alignment).
 int64_t product_bytes(Kind kind, int64_t np, int64_t nq, int64_t nk, bool bf16);
 hipError_t launch_product(Kind kind, const Product &a, void *work, bool bf16, hipStream_t stream);
+// Microseconds of a product, straight to LDS or not, as far as its cut foresees.
+double product_time(Kind kind, int64_t np, int64_t nq, int64_t nk, bool bf16, bool straight);
+// Those of copies (below) of so many bytes.
+double copies_time(int64_t bytes);
 
 // Rows of whole 128-byte lines, their last 16-byte chunk filled up with zeros: copies of an operand
 // whose rows would otherwise start anywhere.

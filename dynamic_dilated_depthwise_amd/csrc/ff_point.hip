@@ -30,27 +30,16 @@ __global__ __launch_bounds__(kThreads) void dz_kernel(const T *__restrict__ grad
     for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < all; i += stride) {
         const Place at = place_of(i, per);
         const int64_t n = N - at.col;
-        float g[8], z[8], v[8], d[8];
-        read8<T>(grad + at.row * grad_ld + at.col, n, g);
+        const T *g = grad + at.row * grad_ld;
         const float *s = saved + at.row * (GATED ? 2 * N : N) + at.col;
-        T *o = dz + at.row * ld + at.col;
+        T *o = dz + at.row * ld;
+        float z[8], u[8];
         read8<float>(s, n, z);
-        slopes(z, v, d, act);
         if constexpr (GATED) {
-            float u[8];
             read8<float>(s + N, n, u);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) { d[e] = g[e] * u[e] * d[e]; v[e] = g[e] * v[e]; }
-            write8<T>(o, n, d);
-            write8<T>(o + N, n, v);
+            finish_gated_dz<T>(o, at.col, N, g, act, z, u);
         } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) d[e] *= g[e];
-            write8<T>(o, n, d);
-        }
-        if (n <= 8) {  // the row's last columns: and the zeros of its last chunk
-            const int64_t width = GATED ? 2 * N : N;
-            for (int64_t c = width; c % kVec<T> != 0; ++c) dz[at.row * ld + c] = 0;
+            finish_dz<T>(o, at.col, N, g, act, z);
         }
     }
 }

@@ -139,32 +139,6 @@ inline int64_t part_bytes(bool bf16, Kind kind, const Cut &c) {
     return c.slots() * (kp * kq + (kind == kGradWeight ? kq : 0)) * 4;
 }
 
-// Operands whose rows are no whole chunks (P's, and Q's where it does not come padded) are copied to
-// rows that are, where that costs less than the form for any alignment: that form takes 1.7 times as
-// long with both operands along their rows, and 3.3 and 5.5 times with one and both read by columns
-// (bfloat16, products of 4095^3), a copy a launch and two passes over the operand.
-struct Copies {
-    bool p = false, q = false;
-    int64_t p_bytes = 0, q_bytes = 0;
-};
-template <typename T>
-inline Copies copies_for(Kind kind, int64_t np, int64_t nq, int64_t nk) {
-    constexpr bool bf16 = Elem<T>::is_bf16;
-    constexpr int64_t per = 16 / (int64_t)sizeof(T);
-    Copies c;
-    const bool forward = kind == kForward || kind == kGatedForward;
-    const int64_t p_cols = forward ? nk : np, p_rows = forward ? (kind == kGatedForward ? 2 * np : np) : nk;
-    if (p_cols % per == 0 || few_rows(kind, nq, false)) return c;
-    c.p = true;
-    c.q = forward;  // the backward's Q is dz, which comes padded
-    c.p_bytes = p_rows * padded(p_cols, bf16) * (int64_t)sizeof(T);
-    c.q_bytes = c.q ? nq * padded(nk, bf16) * (int64_t)sizeof(T) : 0;
-    const double slower = !bf16 ? 1.3 : forward ? 1.7 : kind == kGradX ? 3.3 : 5.5;
-    const double copied = cut_of<T>(kind, np, nq, nk, true).cost + 5. + 2. * (double)(c.p_bytes + c.q_bytes) / kBytes;
-    if (cut_of<T>(kind, np, nq, nk, false).cost * slower < copied) c = Copies();
-    return c;
-}
-
 template <typename G>
 hipError_t launch_gemm(Product &a, const Cut &c, hipStream_t stream) {
     const double blocks = (double)c.whole + (double)c.slots();
@@ -186,29 +160,9 @@ template <typename T, Kind K>
 hipError_t product(Product a, void *work, hipStream_t stream) {
     constexpr Side sp = KindOf<K>::sp, sq = KindOf<K>::sq;
     constexpr Epi e = KindOf<K>::e;
-    constexpr bool bf16 = Elem<T>::is_bf16, forward = K == kForward || K == kGatedForward;
-    bool p_padded = false;
-    const Copies copies = copies_for<T>(K, a.np, a.nq, a.nk);
-    if (copies.p) {
-        const int64_t width = K == kGatedForward ? 2 * a.np : a.np;
-        Copy p = {a.p, a.p_ld, forward ? width : a.nk, forward ? a.nk : a.np, work}, q = {};
-        a.p = p.dst;
-        a.p_ld = padded(p.cols, bf16);
-        p_padded = true;
-        work = (char *)work + copies.p_bytes;
-        if (copies.q) {
-            q = {a.q, a.q_ld, a.nq, a.nk, work};
-            a.q = q.dst;
-            a.q_ld = padded(q.cols, bf16);
-            a.q_padded = true;
-            work = (char *)work + copies.q_bytes;
-        }
-        const hipError_t r = launch_copies(p, q, bf16, stream);
-        if (r != hipSuccess) return r;
-    }
-    const bool direct = direct_ok<T>(sp, a.p, a.p_ld, a.np, a.nk, K == kGatedForward ? a.np + 256 : 256, p_padded) &&
+    const bool direct = direct_ok<T>(sp, a.p, a.p_ld, a.np, a.nk, K == kGatedForward ? a.np + 256 : 256, a.p_padded) &&
                         direct_ok<T>(sq, a.q, a.q_ld, a.nq, a.nk, 256, a.q_padded);
-    if (few_rows(K, a.nq, direct)) return launch_rows(K == kGatedForward, a, bf16, stream);
+    if (few_rows(K, a.nq, direct)) return launch_rows(K == kGatedForward, a, Elem<T>::is_bf16, stream);
     const Cut c = cut_of<T>(K, a.np, a.nq, a.nk, direct);
     a.part = (float *)work;
 #define DDPM_FF_FORM(k, DIRECT)                                                                       \

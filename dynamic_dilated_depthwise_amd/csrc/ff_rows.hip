@@ -114,9 +114,11 @@ __global__ __launch_bounds__(kMostWaves *kWave) void rows_kernel(const Product a
                 if constexpr (GATED) u[e] += red[s][MT + q / 16][q % 16][c + e];
             }
         }
-        bias8<T>(a, p0 + c, b);
+        bias8<T>(a, p0 + c, 0, b);
+        if (q == 0) keep8(a, p0 + c, 0, b);
         if constexpr (GATED) {
-            other_bias8<T>(a, p0 + c, bu);
+            bias8<T>(a, p0 + c, 1, bu);
+            if (q == 0) keep8(a, p0 + c, 1, bu);
             finish_gated<T>(a, q, p0 + c, v, u, b, bu);
         } else {
             finish_linear<T>(a, q, p0 + c, v, b);

@@ -18,8 +18,8 @@ contiguous or have two axes with contiguous rows; weight and bias are contiguous
 least one.  activation is "none", "relu", "silu" or "gelu" (z times the normal distribution at z).
 
 Sums are float32; outputs are rounded once.  Where an activation or a gate lies between, its
-input's gradient is rounded to the type before the two products of the backward take it; the
-forward keeps that input in float32.
+input's gradient is rounded to the type before the two products of the backward take it; that
+input itself is not: the forward keeps it in float32, or the backward makes it again.
 
 Streams, captured graphs and training steps in them are as in ``sequence``.
 """
@@ -44,7 +44,7 @@ except ImportError as e:
 
 
 def linear_fwd(x, weight, bias=None, residual=None, activation="none", save=False, stream=None):
-    """(y, saved): saved is z, which linear_bwd takes, in float32 (None unless save, and without an activation)."""
+    """(y, saved): saved is what linear_bwd needs from this call (None unless save, and without an activation)."""
     return _feedforward.linear_fwd(x, weight, bias, residual, activation, save, stream)
 
 
@@ -55,7 +55,7 @@ def linear_bwd(grad, x, weight, saved=None, activation="none", need_x=True, need
 
 
 def gated_linear_fwd(x, weight, bias=None, activation="silu", save=False, stream=None):
-    """(y, saved): saved is [g, u], which gated_linear_bwd takes, in float32 (None unless save)."""
+    """(y, saved): saved is what gated_linear_bwd needs from this call (None unless save)."""
     return _feedforward.gated_linear_fwd(x, weight, bias, activation, save, stream)
 
 

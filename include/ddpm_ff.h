@@ -41,9 +41,11 @@ typedef enum { DDPM_ACT_NONE = 0, DDPM_ACT_RELU = 1, DDPM_ACT_SILU = 2, DDPM_ACT
 
 /*
  * z = x weight^T + bias,  y = act(z) + residual:  x [rows, C], weight [N, C], bias [N] or NULL,
- * residual [rows, N] or NULL, y [rows, N].  saved [rows, N] float32, or NULL, receives z, which
- * the backward of an activation takes.
+ * residual [rows, N] or NULL, y [rows, N].  saved, or NULL, receives what the backward of an
+ * activation takes: *_saved floats (z, or where making z again costs less, the bias; none, and
+ * NULL, with DDPM_ACT_NONE).
  */
+int64_t ddpm_linear_saved(int64_t rows, int64_t C, int64_t N, int activation, int dtype);
 int64_t ddpm_linear_fwd_workspace(int64_t rows, int64_t C, int64_t N, int dtype);
 int ddpm_linear_fwd(const void *x, const void *weight, const void *bias, const void *residual, void *y, float *saved,
                     void *workspace, int64_t rows, int64_t C, int64_t N, int64_t x_row, int64_t residual_row,
@@ -60,9 +62,10 @@ int ddpm_linear_bwd(const void *grad, const void *x, const void *weight, const f
 
 /*
  * [g, u] = x weight^T + bias, N columns each,  y = act(g) u:  x [rows, C], weight [2 N, C] (g's
- * rows, then u's), bias [2 N] or NULL, y [rows, N].  saved [rows, 2 N] float32, or NULL,
- * receives g and u, which the backward takes.
+ * rows, then u's), bias [2 N] or NULL, y [rows, N].  saved, or NULL, receives what the backward
+ * takes: *_saved floats.
  */
+int64_t ddpm_gated_linear_saved(int64_t rows, int64_t C, int64_t N, int dtype);
 int64_t ddpm_gated_linear_fwd_workspace(int64_t rows, int64_t C, int64_t N, int dtype);
 int ddpm_gated_linear_fwd(const void *x, const void *weight, const void *bias, void *y, float *saved, void *workspace,
                           int64_t rows, int64_t C, int64_t N, int64_t x_row, int activation, int dtype, hipStream_t stream);

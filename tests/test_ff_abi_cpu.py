@@ -25,6 +25,8 @@ SIGNATURES = {
     "ddpm_linear_bwd": [_P] * 8 + [_I64] * 5 + [_I, _I, _P],
     "ddpm_gated_linear_fwd": [_P] * 6 + [_I64] * 4 + [_I, _I, _P],
     "ddpm_gated_linear_bwd": [_P] * 8 + [_I64] * 5 + [_I, _I, _P],
+    "ddpm_linear_saved": [_I64] * 3 + [_I, _I],
+    "ddpm_gated_linear_saved": [_I64] * 3 + [_I],
     "ddpm_linear_fwd_workspace": [_I64] * 3 + [_I],
     "ddpm_linear_bwd_workspace": [_I64] * 3 + [_I, _I],
     "ddpm_gated_linear_fwd_workspace": [_I64] * 3 + [_I],
@@ -41,7 +43,7 @@ def lib():
     for name, args in SIGNATURES.items():
         f = getattr(lib, name)
         f.argtypes = args
-        f.restype = _I64 if name.endswith("_workspace") else _I
+        f.restype = _I64 if name.endswith(("_workspace", "_saved")) else _I
     return lib
 
 
@@ -117,6 +119,17 @@ def test_workspace_sizes(lib):
         assert lib.ddpm_linear_fwd_workspace(5, 8, 16, dt) == 0
     assert lib.ddpm_linear_fwd_workspace(0, 8, 16, F32) == 0 and lib.ddpm_linear_fwd_workspace(5, 8, 16, 7) == 0
     assert lib.ddpm_linear_bwd_workspace(5, 8, 16, 9, F32) == 0 and lib.ddpm_gated_linear_bwd_workspace(5, -8, 16, F32) == 0
+
+
+def test_saved_sizes(lib):
+    for dt, again in ((F32, 64), (BF16, 256)):
+        # few columns of x and many rows: the bias, otherwise z
+        rows = 1 << 20
+        assert lib.ddpm_linear_saved(rows, again, 40, GELU, dt) == 40 and lib.ddpm_gated_linear_saved(rows, again, 40, dt) == 80
+        for r, C in ((100, again), (rows, 4096)):
+            assert lib.ddpm_linear_saved(r, C, 40, GELU, dt) == 40 * r and lib.ddpm_gated_linear_saved(r, C, 40, dt) == 80 * r
+        assert lib.ddpm_linear_saved(rows, again, 40, NONE, dt) == 0 and lib.ddpm_linear_saved(100, 4096, 40, NONE, dt) == 0
+    assert lib.ddpm_linear_saved(0, 8, 8, SILU, F32) == 0 and lib.ddpm_gated_linear_saved(8, 8, 8, 5) == 0
 
 
 def test_binding_rejects_host_tensors(lib):

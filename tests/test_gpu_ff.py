@@ -82,6 +82,19 @@ def test_large_tiles(rows, C, N, gated):
     compare(*case(rows, C, N, torch.bfloat16, gated), "gelu", gated)
 
 
+# Few columns of x and many of z: the backward makes z again, from whole chunks and from others.
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("gated", [False, True], ids=["linear", "gated"])
+@pytest.mark.parametrize("rows,C,N", [(9001, 24, 1352), (8200, 37, 1501), (61, 40, 200040)])
+def test_made_again(rows, C, N, gated, dt):
+    announce("ff made again", rows, C, N, gated, dt)
+    args = case(rows, C, N, DT[dt], gated)
+    saved = forward(*args[:4], "silu", gated, save=True)[1]
+    assert saved.numel() == args[1].shape[0] and torch.equal(saved, args[2].float())
+    compare(*args, "silu", gated)
+    assert not forward(args[0], args[1], None, None, "silu", gated, save=True)[1].any()
+
+
 @pytest.mark.parametrize("dt", DT)
 @pytest.mark.parametrize("gated", [False, True], ids=["linear", "gated"])
 @pytest.mark.parametrize("act", ff.ACTIVATIONS)
