@@ -456,6 +456,16 @@ struct Gemm {
                     multiply<NQ>(acc[i], read_p.get(at, wp * MP + i, s), fq);
                 }
             }
+            // The splits' vector instructions between the products: left in runs, they and the matrix
+            // instructions do not overlap (39 % and 57 % of the cycles; 4096^3 597 -> 577 us).
+            if constexpr (!Elem<T>::is_bf16) {
+                constexpr int kProducts = 6 * MP * NQ, kVector = 44 * (MP + NQ) / kProducts + 1;
+#pragma unroll
+                for (int n = 0; n < kProducts; ++n) {
+                    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x2, kVector, 0);
+                }
+            }
         };
 
         const int steps = (int)((k1 - k0 + kStep<T> - 1) / kStep<T>);
