@@ -34,7 +34,9 @@ int64_t chunk(bool bf16) { return 16 / element(bf16); }
 // 472, 419; 1536 750, 780; one half with gelu: 512 220, 213; 768 266, 275; 65536 rows to 2 128 in
 // float32: 64 114, 105; 128 143, 143.  Where z stays in the caches both are the same up to C = 256 and
 // saving is faster beyond).
+// Backwards of few channels (ff_small.hip) always make it again, on the chip.
 bool makes_again(const Sizes &s, bool bf16) {
+    if (small_backward(s.C, s.width)) return true;
     const int64_t most = !bf16 ? 96 : s.width == s.N ? 512 : 768;
     return s.C <= most && (double)s.rows * s.width >= 12e6;
 }
@@ -132,12 +134,17 @@ int forward(Kind kind, const void *x, const void *weight, const void *bias, cons
 // What the backward has in its workspace: dz, where it is another tensor than grad (behind an activation
 // or a gate, and where grad's rows are no whole chunks and many enough), copies, the products' pieces.
 struct Room {
-    bool own_dz, copies, again;
+    bool small, own_dz, copies, again;
     int64_t dz, all;
 };
 constexpr double kManyFlops = 5e9;  // of one product: from here on a copy of grad costs less than what it saves
 Room backward_room(Kind kind, const Sizes &s, bool through, bool bf16) {
-    Room r;
+    Room r = {};
+    r.small = through && small_backward(s.C, s.width);
+    if (r.small) {
+        r.all = small_bytes(s.rows, s.C, s.width, bf16);
+        return r;
+    }
     r.own_dz = through || (s.N % chunk(bf16) != 0 && 2. * s.rows * s.N * s.C >= kManyFlops);
     r.again = through && makes_again(s, bf16);
     r.copies = backward_copies(kind, s, r.again, bf16);
@@ -174,6 +181,11 @@ int backward(Kind kind, const void *grad, const void *x, const void *weight, con
     const int st = c.done();
     if (st != DDPM_OK) return st;
     (void)hipGetLastError();
+    if (room.small) {
+        const SmallBackward b = {grad, x, weight, saved, s.rows, grad_row, x_row, s.C, (int)s.C, (int)s.N, activation, grad_x,
+                                 grad_weight != nullptr ? (float *)workspace : nullptr};
+        return status_of(launch_small_backward(gated, b, grad_weight, grad_bias, bf16, stream));
+    }
     char *work = (char *)workspace + room.dz;
     int64_t weight_row = s.C;
     hipError_t e = hipSuccess;

@@ -85,10 +85,11 @@ __device__ __forceinline__ void activate(float (&v)[8], int act) {
 #undef X
 }
 // a = act(z), d = act'(z).
-__device__ __forceinline__ void slopes(const float (&z)[8], float (&a)[8], float (&d)[8], int act) {
+template <int n>
+__device__ __forceinline__ void slopes(const float (&z)[n], float (&a)[n], float (&d)[n], int act) {
 #define X(ACT)                                              \
     if (act == ACT) {                                       \
-        _Pragma("unroll") for (int e = 0; e < 8; ++e) curve_and_slope<ACT>(z[e], a[e], d[e]); \
+        _Pragma("unroll") for (int e = 0; e < n; ++e) curve_and_slope<ACT>(z[e], a[e], d[e]); \
     }
     X(DDPM_ACT_NONE) else X(DDPM_ACT_RELU) else X(DDPM_ACT_SILU) else X(DDPM_ACT_GELU)
 #undef X

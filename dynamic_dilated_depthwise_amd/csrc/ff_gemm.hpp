@@ -259,6 +259,17 @@ struct Reader {
     }
 };
 
+// Four neighbouring elements (element-aligned), widened.
+template <typename T>
+__device__ __forceinline__ f32x4 load_four(const T *p) {
+    if constexpr (Elem<T>::is_bf16) {
+        const u16x4 u = *(const u16x4_a2 *)p;
+        return f32x4{bf16_bits_to_f32(u[0]), bf16_bits_to_f32(u[1]), bf16_bits_to_f32(u[2]), bf16_bits_to_f32(u[3])};
+    } else {
+        return *(const f32x4_a4 *)p;
+    }
+}
+
 // Eight neighbouring elements: of a vector in memory (element-aligned), the first n of them.
 template <typename T>
 __device__ __forceinline__ void read8(const T *p, int64_t n, float (&v)[8]) {

@@ -67,5 +67,19 @@ hipError_t launch_rows(bool gated, const Product &a, bool bf16, hipStream_t stre
 hipError_t launch_dz(bool gated, const void *grad, int64_t grad_ld, const float *saved, void *dz, int64_t rows, int64_t N,
                      int act, bool bf16, hipStream_t stream);
 
+// The whole backward through an activation or a gate of few channels, which makes z again
+// (ff_small.hip): whether these sizes are, the bytes of its partials, and the call.
+struct SmallBackward {
+    const void *grad, *x, *weight;
+    const float *bias;                  // [N], gated [2 N]
+    int64_t rows, grad_ld, x_ld, weight_ld;
+    int C, N, act;
+    void *grad_x;                       // [rows, C] or null
+    float *part;                        // of grad_weight and grad_bias, or null with them
+};
+bool small_backward(int64_t C, int64_t width);
+int64_t small_bytes(int64_t rows, int64_t C, int64_t width, bool bf16);
+hipError_t launch_small_backward(bool gated, SmallBackward a, void *grad_weight, void *grad_bias, bool bf16, hipStream_t stream);
+
 }  // namespace ff
 }  // namespace ddpm

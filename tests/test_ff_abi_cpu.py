@@ -126,8 +126,9 @@ def test_saved_sizes(lib):
         # few columns of x and many rows: the bias, otherwise z
         rows = 1 << 20
         assert lib.ddpm_linear_saved(rows, again, 40, GELU, dt) == 40 and lib.ddpm_gated_linear_saved(rows, again, 40, dt) == 80
-        for r, C in ((100, again), (rows, 4096)):
-            assert lib.ddpm_linear_saved(r, C, 40, GELU, dt) == 40 * r and lib.ddpm_gated_linear_saved(r, C, 40, dt) == 80 * r
+        assert lib.ddpm_linear_saved(3, 64, 256, GELU, dt) == 256 and lib.ddpm_gated_linear_saved(3, 64, 128, dt) == 256
+        for r, C, N in ((100, again, 400), (rows, 4096, 40)):
+            assert lib.ddpm_linear_saved(r, C, N, GELU, dt) == N * r and lib.ddpm_gated_linear_saved(r, C, N, dt) == 2 * N * r
         assert lib.ddpm_linear_saved(rows, again, 40, NONE, dt) == 0 and lib.ddpm_linear_saved(100, 4096, 40, NONE, dt) == 0
     assert lib.ddpm_linear_saved(0, 8, 8, SILU, F32) == 0 and lib.ddpm_gated_linear_saved(8, 8, 8, 5) == 0
 

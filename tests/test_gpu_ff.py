@@ -95,6 +95,23 @@ def test_made_again(rows, C, N, gated, dt):
     assert not forward(args[0], args[1], None, None, "silu", gated, save=True)[1].any()
 
 
+# Few channels, whose backward is one kernel: rows below, at and above a tile and a round of the chip.
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("gated", [False, True], ids=["linear", "gated"])
+@pytest.mark.parametrize("rows,C,N", [(1, 1, 1), (63, 64, 128), (64, 8, 16), (65, 63, 127), (130, 33, 20), (1000, 17, 90), (33100, 64, 128),
+                                      (40001, 50, 77)])
+def test_few_channels(rows, C, N, gated, dt):
+    announce("ff few channels", rows, C, N, gated, dt)
+    args = case(rows, C, N if gated else 2 * N, DT[dt], gated)
+    compare(*args, "gelu", gated)
+    x, w, b, r, grad = args
+    saved = forward(x, w, b, r, "gelu", gated, save=True)[1]
+    gx, gw, gb = backward(grad, x, w, saved, "gelu", gated)
+    assert torch.equal(backward(grad, x, w, saved, "gelu", gated, need_weight=False)[0], gx)
+    for p, q in zip(backward(grad, x, w, saved, "gelu", gated, need_x=False)[1:], (gw, gb)):
+        assert torch.equal(p, q)
+
+
 @pytest.mark.parametrize("dt", DT)
 @pytest.mark.parametrize("gated", [False, True], ids=["linear", "gated"])
 @pytest.mark.parametrize("act", ff.ACTIVATIONS)
