@@ -11,8 +11,8 @@
 //
 // A step of the contraction is 128 bytes of it (64 bfloat16 or 32 float32).  A step's tile of an
 // operand is TILE * 128 bytes of LDS in 16-byte chunks, placed by an exclusive or of the chunk's
-// number with bits of its row, so that the fragment reads of a wave spread over the banks.  Two
-// steps' tiles are held: one is computed while the next one arrives.
+// number with bits of its row, so that the fragment reads of a wave spread over the banks.  The tiles of
+// two to four steps are held (see form_of): one is computed while the next ones arrive.
 //   DIRECT   the chunks go straight from memory to LDS (no registers, nothing to wait for but the
 //            step's end); needs 16-byte aligned rows and whole chunks.  Chunks outside the
 //            operand are asked for past the buffer's end, which reads zero.
@@ -55,7 +55,7 @@ __device__ __forceinline__ void wave_order() { asm volatile("" ::: "memory"); }
 // 16 bytes a lane from `off` behind `p` (uniform; zeros from kRecords on) to LDS at `at` (uniform) + 16 lane.
 // In assembly, because the compiler takes the builtin for a write to all of LDS and makes the fragment
 // reads behind it wait for it (grad_x 930 -> 570 TFLOP/s with loads between them).  It has no result, so
-// no register is held by a load in flight; arrive_all waits for it.  The compiler keeps nothing in m0; a
+// no register is held by a load in flight; arrive_but waits for it.  The compiler keeps nothing in m0; a
 // change of it needs one wait state.
 __device__ __forceinline__ void load_to_lds(const void *p, uint32_t off, char *at) {
     const uint64_t a = (uint64_t)p;
@@ -75,9 +75,8 @@ __device__ __forceinline__ int swizzle(int row) {
     else return ((row >> 1 & 1) | (row >> 3 & 1) << 1) << 1 & (CH - 1);
 }
 
-// The gated product's tile of P has 16 of the gate's rows, the same 16 of the other half, and so on.
-
-// One operand's tile: TILE indices from `first` of `extent`, contraction from k0.
+// One operand's tile: TILE indices from `first` of `extent`, contraction from k0.  The gated product's
+// tile of P has 16 of the gate's rows, the same 16 of the other half, and so on.
 template <typename T, Side S, int TILE, int THREADS, bool DIRECT, bool GATED>
 struct Tile {
     static constexpr int kPer = kVec<T>, kCh = S == kAlong ? 8 : TILE / kPer;

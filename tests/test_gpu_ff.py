@@ -313,3 +313,165 @@ def test_streams_and_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(outs, eager))
+
+
+# Long contractions with few tiles, for each product of the two passes: cut into pieces that a second kernel adds up.
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("gated", [False, True], ids=["linear", "gated"])
+@pytest.mark.parametrize("rows,C,N", [(5000, 72, 40), (5001, 77, 41), (90, 72, 5000), (90, 5000, 72), (70, 4999, 71)])
+def test_long_sums(rows, C, N, gated, dt):
+    announce("ff long sums", rows, C, N, gated, dt)
+    compare(*case(rows, C, N, DT[dt], gated), "silu", gated)
+
+
+@pytest.mark.parametrize("dt", DT)
+def test_copied_gradient(dt):
+    """Without an activation the products take grad itself; of many rows that are no whole chunks, a copy."""
+    announce("ff copied gradient", dt)
+    x, w, b, r, grad = case(2051, 1030, 1203, DT[dt])
+    compare(x, w, b, r, grad, "none", False)
+    wide = torch.full((2051, 1210), float("nan"), device="cuda", dtype=DT[dt])
+    wide[:, 3:1206] = grad
+    want = ff.linear_bwd(grad, x, w)
+    for p, q in zip(ff.linear_bwd(wide[:, 3:1206], x, w), want):
+        assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("gated", [False, True], ids=["linear", "gated"])
+@pytest.mark.parametrize("C,N", [(64, 32), (128, 32), (77, 32), (128, 70)])
+def test_far_rows(C, N, gated):
+    """Rows whose offsets pass 32 bits, in elements: what they are among near ones."""
+    announce("ff far rows", C, N, gated)
+    rows, ld, dtype = 300, 9000001 if C % 8 else 9000008, torch.bfloat16
+    x, w, b, r, grad = case(rows, C, N, dtype, gated)
+    base = torch.empty(rows * ld, device="cuda", dtype=dtype)
+
+    def far(t, at):
+        v = base.as_strided(t.shape, (ld, 1), at)
+        return v.copy_(t)
+
+    xf, gf, rf = far(x, 0), far(grad, 512), far(r, 1024) if r is not None else None
+    xn, gn = (torch.cat([t, t[:, :1 if ld % 8 else 8]], 1)[:, :t.shape[1]] for t in (x, grad))
+    y, saved = forward(xn, w, b, r, "silu", gated, save=True)
+    yf, savedf = forward(xf, w, b, rf, "silu", gated, save=True)
+    compare(xf, w, b, rf, gf, "silu", gated)
+    assert not bool((xf != x).any()) and not bool((gf != grad).any())
+    if C % 8:  # neither takes chunks: the same form, the same bits
+        assert torch.equal(y, yf) and torch.equal(saved, savedf)
+
+
+@pytest.mark.parametrize("gated", [False, True], ids=["linear", "gated"])
+@pytest.mark.parametrize("rows,C,N", [(1 << 20, 64, 2304), (1 << 20, 72, 2304), ((1 << 20) + 1, 65, 2305)])
+def test_far_results(rows, C, N, gated):
+    """More than 2^31 elements of y, z and dz."""
+    announce("ff far results", rows, C, N, gated)
+    dtype, k = torch.bfloat16, 300
+    gen = torch.Generator("cuda").manual_seed(4)
+    x = torch.randn(rows, C, generator=gen, device="cuda", dtype=dtype)
+    w = torch.randn(N * (2 if gated else 1), C, generator=gen, device="cuda", dtype=dtype) * C ** -0.5
+    grad = torch.randn(rows, N, generator=gen, device="cuda", dtype=dtype)
+    grad[:-k] = 0  # so that the parameters' gradients are the last rows' too
+    y, saved = forward(x, w, None, None, "gelu", gated, save=True)
+    gx, gw, gb = backward(grad, x, w, saved, "gelu", gated)
+    want = orc.run(x[-k:], w, None, None, "gelu", grad[-k:], gated)
+    width = w.shape[0]
+    orc.check(y[-k:], want["y"], dtype, "y", 2 * C + 64)
+    orc.check(gx[-k:], want["grad_x"], dtype, "grad_x", 2 * (C + width) + 64)
+    orc.check(gw, want["grad_weight"], dtype, "grad_weight", 2 * (C + k) + 64)
+    orc.check(gb, want["grad_bias"], dtype, "grad_bias", 2 * (C + k) + 64)
+    assert not gx[:-k].any()
+    head = forward(x[:k], w, None, None, "gelu", gated)[0]
+    orc.check(y[:k], orc.run(x[:k], w, None, None, "gelu", gated=gated)["y"], dtype, "y", 2 * C + 64)
+    orc.check(head, orc.run(x[:k], w, None, None, "gelu", gated=gated)["y"], dtype, "y", 2 * C + 64)
+
+
+def test_strides_of_single_elements():
+    """The strides of axes of one element mean nothing."""
+    announce("ff single elements")
+    for gated in (False, True):
+        x, w, b, r, grad = case(37, 1, 1, torch.float32, gated)
+        odd = [t.as_strided((37, 1), (1, 9)) if t is not None else None for t in (x, r, grad)]
+        saved = forward(x, w, b, r, "silu", gated, save=True)[1]
+        assert torch.equal(forward(odd[0], w, b, odd[1], "silu", gated)[0], forward(x, w, b, r, "silu", gated)[0])
+        for p, q in zip(backward(odd[2], odd[0], w, saved, "silu", gated), backward(grad, x, w, saved, "silu", gated)):
+            assert torch.equal(p, q)
+        x, w, b, r, grad = case(1, 40, 24, torch.float32, gated)
+        odd = x.as_strided((1, 40), (7, 1))
+        assert torch.equal(forward(odd, w, b, r, "silu", gated)[0], forward(x, w, b, r, "silu", gated)[0])
+
+
+# every path of a call: few rows, pieces, copies of x and the weight, few channels, z made again, a copied grad
+PATHS = [(5, 2048, 264, "gelu"), (300, 72, 264, "silu"), (2045, 321, 867, "gelu"), (3000, 64, 100, "silu"), (9001, 72, 1352, "silu"),
+         (2051, 1030, 1203, "none")]
+
+
+def step_of(args, act, gated, **kw):
+    x, w, b, r, grad = args
+    y, saved = forward(x, w, b, r, act, gated, save=True, **kw)
+    return [t for t in (y, saved, *backward(grad, x, w, saved, act, gated, **kw)) if t is not None]
+
+
+@pytest.mark.parametrize("gated", [False, True], ids=["linear", "gated"])
+def test_two_streams_at_once(gated):
+    announce("ff two streams", gated)
+    work = [(case(rows, C, N, torch.bfloat16, gated), act) for rows, C, N, act in PATHS]
+    want = [step_of(args, act, gated) for args, act in work]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        got = [[step_of(args, act, gated, stream=s) for args, act in work] for s in streams]
+        torch.cuda.synchronize()
+        for one in got:
+            for p, q in zip(one, want):
+                assert len(p) == len(q) and all(torch.equal(a, b) for a, b in zip(p, q))
+
+
+@pytest.mark.parametrize("gated", [False, True], ids=["linear", "gated"])
+def test_two_graphs_of_one_pool(gated):
+    """Their workspaces may be the same memory; each replay is whole by itself."""
+    announce("ff two graphs", gated)
+    work = [(case(rows, C, N, torch.bfloat16, gated), act) for rows, C, N, act in PATHS]
+    halves = [work[::2], work[1::2]]
+    want = [[t.clone() for args, act in half for t in step_of(args, act, gated)] for half in halves]
+    torch.cuda.synchronize()
+    graphs, outs, pool = [], [], None
+    for half in halves:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, pool=pool):
+            outs.append([t for args, act in half for t in step_of(args, act, gated)])
+        pool = g.pool()
+        graphs.append(g)
+    junk = torch.randn(256, 256, device="cuda")
+    for k in (0, 1, 1, 0, 1, 0):
+        for t in outs[k]:
+            t.fill_(float("nan"))
+        junk = torch.tanh(junk @ junk / 256)
+        torch.cuda.synchronize()
+        graphs[k].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(outs[k], want[k])), k
+
+
+def test_arguments_let_go_of():
+    """Tensors given up behind a call on another stream are not handed out before it has read them."""
+    announce("ff let go")
+    for gated in (False, True):
+        args = case(2045, 321, 867, torch.bfloat16, gated)
+        want = step_of(args, "gelu", gated)
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        busy = torch.randn(4096, 4096, device="cuda")
+        torch.cuda.synchronize()
+        for _ in range(3):
+            own = [t.clone() if t is not None else None for t in args]
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                for _ in range(4):
+                    busy @ busy
+            got = step_of(own, "gelu", gated, stream=side)
+            sizes = [t.shape for t in own if t is not None]
+            del own
+            junk = [torch.full(s, float("nan"), device="cuda", dtype=torch.bfloat16) for s in sizes for _ in range(2)]
+            torch.cuda.synchronize()
+            assert all(torch.equal(p, q) for p, q in zip(got, want))
+            del junk
