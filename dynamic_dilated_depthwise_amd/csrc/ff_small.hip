@@ -6,10 +6,10 @@
 // The weight stays in LDS, z and dz never leave the chip: a workgroup takes 64 rows at a time (float32:
 // 32), makes their z (its waves 32 columns each), puts dz into LDS, and multiplies it by both; grad_W
 // stays in registers until the workgroup's last rows and leaves as one row of float32 partials, which a
-// second kernel adds up.  65536 rows of 64 to 2 128 take 40 us in bfloat16 and 53 in float32, 262144 rows 92
-// and 183; as products of their own (z, dz, grad_x, grad_W) 44 and 84, 128 and 295.  The bytes alone are
-// 6.5 us and 13: what bounds it are the instructions between LDS and the matrix units (dz through LDS is
-// read both ways by every wave, float32's in three planes) and the barriers between the phases.
+// second kernel adds up.  65536 rows of 64 to 2 128 take 38 us in bfloat16 and 52 in float32, 262144 rows 86
+// and 172; as products of their own (z, dz, grad_x, grad_W) 44 and 84, 128 and 295.  The bytes alone are
+// 6.5 us and 13.  What bounds it are vector instructions (bfloat16: 76 % of the cycles; float32: 36 %, and 38 %
+// the matrix units), most of them the activation's slopes and the fragments' and rows' addresses.
 //
 // Everything in LDS is bfloat16, of float32 three planes (see split_of), each made once: split at every
 // read the kernel took 79 us for 65536 rows of 64 to 2 128, most of it vector instructions.  A sheet is
@@ -26,10 +26,34 @@ namespace {
 constexpr int kCols = 64, kWidth = 256, kThreads = 512;
 template <typename T> constexpr int kCopies = Elem<T>::is_bf16 ? 1 : kParts;  // planes of a sheet
 
-// A lane's number, made anew where a phase begins: what is computed from it is computed there and held by no
-// register between.  With bfloat16's 128 registers a lane that is 40 us for 65536 rows of 64 to 2 128 (53 with
-// the addresses held, and spilled); with float32's 256 it is 61 us, held 54.
+// A lane's number, made anew where a phase begins, so that what is computed from it holds no register between:
+// with bfloat16's 128 registers a lane 79 us for 262144 rows of 64 to 2 128 (held, and spilled, 120), with
+// float32's 256 204 us and held 202 (the kernel alone).
 template <typename T> __device__ __forceinline__ int anew(int v) { return Elem<T>::is_bf16 ? afresh(v) : v; }
+
+// A lane's places in a sheet, made once a phase: those of its fragments differ by an exclusive or of a chunk's
+// number with a constant below N and by constants that the instructions hold.
+template <int N> struct Turned { int to[N]; };
+// turn: uniform; by: bytes of a turn
+template <typename T, int N> __device__ __forceinline__ Turned<N> turned(int sheet, int lane_at, int turn, int by) {
+    Turned<N> r;
+    lane_at = anew<T>(lane_at);
+#pragma unroll
+    for (int v = 0; v < N; ++v) r.to[v] = anew<T>(sheet + (lane_at ^ (turn ^ v) * by));
+    return r;
+}
+// Row l16, column 8 g; a turn where 16 rows or 32 columns further.
+template <typename T> __device__ __forceinline__ Turned<2> lanes_along(int sheet, int l16, int g, int turn) {
+    return turned<T, 2>(sheet, l16 * 128 + (((g ^ l16 ^ l16 / 8 * 2) & 7) << 4), turn, 64);
+}
+// Row 8 g + l16 / 4, column 4 (l16 % 4); a turn for 16 columns, two turns where four rows further.
+template <typename T> __device__ __forceinline__ Turned<4> lanes_down(int sheet, int l16, int g, int turn) {
+    return turned<T, 4>(sheet, (8 * g + l16 / 4) * 128 + ((l16 % 4 / 2 ^ l16 / 4 ^ 2 * g) << 4) + l16 % 2 * 8, turn, 32);
+}
+// Row l16, column 4 g; a turn for 16 columns, two for 32 columns or 16 rows.
+template <typename T> __device__ __forceinline__ Turned<4> lanes_put(int sheet, int l16, int g, int turn) {
+    return turned<T, 4>(sheet, l16 * 128 + (((g / 2 ^ l16 ^ l16 / 8 * 2) & 7) << 4) + g % 2 * 8, turn, 32);
+}
 
 template <typename T, int ROWS, int COLS>
 struct Sheet {
@@ -39,9 +63,8 @@ struct Sheet {
     __device__ __forceinline__ static int at(int row, int c) {
         return c / 64 * kPane + row * 128 + ((c % 64 / 8 ^ bits(row)) << 4) + c % 8 * 2;
     }
-    // Four neighbours from column c (a multiple of four).
-    __device__ __forceinline__ static void put4(char *p, int row, int c, f32x4 v) {
-        char *to = p + at(row, c);
+    // Four neighbours.
+    __device__ __forceinline__ static void put4(char *to, f32x4 v) {
 #pragma unroll
         for (int k = 0; k < kCopies<T>; ++k) {
             u16x4 t;
@@ -55,11 +78,12 @@ struct Sheet {
     // A 16-byte vector of T from column c.
     __device__ __forceinline__ static void put(char *p, int row, int c, const u32x4 &v) {
         if constexpr (Elem<T>::is_bf16) *(u32x4 *)(p + at(row, c)) = v;
-        else put4(p, row, c, __builtin_bit_cast(f32x4, v));
+        else put4(p + at(row, c), __builtin_bit_cast(f32x4, v));
     }
-    // Index runs over the rows 16 t .., contraction over the columns 32 r ...
-    __device__ __forceinline__ static Operand<T> along(const char *p, int t, int r, int l16, int g) {
-        const char *from = p + at(16 * t + l16, 32 * r + 8 * g);
+    // A fragment: index over the rows 16 t .., contraction over the columns 32 r ..; at: lanes_along of the sheet
+    // (or of its rows from a t on, turned by t % 2, and then t counts from there).
+    __device__ __forceinline__ static Operand<T> along(const char *lds, const Turned<2> &at, int t, int r) {
+        const char *from = lds + at.to[(r ^ t) & 1] + t * 2048 + r / 2 * kPane;
         if constexpr (Elem<T>::is_bf16) {
             return *(const bf16x8 *)from;
         } else {
@@ -69,11 +93,11 @@ struct Sheet {
             return v;
         }
     }
-    // Index runs over the columns 16 t .., contraction over the rows 32 r ...
-    __device__ __forceinline__ static Operand<T> down(const char *p, int t, int r, int l16, int g) {
+    // Index over the columns 16 t .., contraction over the rows 32 r ..; at: lanes_down of the sheet (or of
+    // its columns from a t on, turned by t % 4).
+    __device__ __forceinline__ static Operand<T> down(const char *lds, const Turned<4> &at, int t, int r) {
         typedef __attribute__((address_space(3))) s16x4 *lds_ptr;
-        const int row = 32 * r + 8 * g + l16 / 4, c = 16 * t + 4 * (l16 % 4);
-        const char *first = p + at(row, c), *second = p + at(row + 4, c);
+        const char *first = lds + at.to[t] + r * 4096, *second = lds + at.to[t ^ 2] + 512 + r * 4096;
         bf16x8 v[kCopies<T>];
 #pragma unroll
         for (int k = 0; k < kCopies<T>; ++k) {
@@ -109,7 +133,7 @@ template <typename T, bool GATED>
 __global__ __launch_bounds__(kThreads, Elem<T>::is_bf16 ? 4 : 2) void small_backward_kernel(const SmallBackward a) {
     typedef Small<T> S;
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    char *w = lds, *x = w + S::W::kBytes, *dz = x + S::kXs * S::X::kBytes;
+    constexpr int w = 0, x = S::W::kBytes, dz = x + S::kXs * S::X::kBytes;  // where in LDS
     const int tid = threadIdx.x, wave = wave_of(tid), lane = tid % kWave, l16 = lane % 16, g = lane / 16;
     const int C = a.C, N = a.N;
     constexpr int kRows = S::kRows, kM = S::kM, kOwn = S::kOwn;
@@ -123,7 +147,7 @@ __global__ __launch_bounds__(kThreads, Elem<T>::is_bf16 ? 4 : 2) void small_back
         const int n = row_of(i), c = col_of(i), f = column_of<GATED>(n);
         const int64_t from = f + (GATED && n & 16 ? N : 0);
         const bool on = f < N && c < C;
-        S::W::put(w, n, c, load_vec<T>((const T *)a.weight + (on ? from * a.weight_ld + c : 0), on ? C - c : 0));
+        S::W::put(lds + w, n, c, load_vec<T>((const T *)a.weight + (on ? from * a.weight_ld + c : 0), on ? C - c : 0));
     }
     u32x4 xn[S::kXChunks];
     const auto fetch = [&](int64_t tile) {
@@ -148,17 +172,42 @@ __global__ __launch_bounds__(kThreads, Elem<T>::is_bf16 ? 4 : 2) void small_back
     }
 
     fetch(blockIdx.x);
-    put(x);
+    put(lds + x);
     int now = 0;
     for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, now ^= S::kXs - 1) {
         __syncthreads();  // x is there, and dz is read
-        const char *xt = x + now * S::X::kBytes;
+        const int xt = x + now * S::X::kBytes;
         const int64_t m0 = tile * kRows;
         const int left = (int)(a.rows - m0 < kRows ? a.rows - m0 : kRows);
         if (tile + gridDim.x < tiles) fetch(tile + gridDim.x);
-        int lf = anew<T>(l16), gf = anew<T>(g);
+        const auto grad_of = [&](int m, int f_, int n) {
+            f32x4 gr = {0.f, 0.f, 0.f, 0.f};
+            const T *grad = (const T *)a.grad + (n > 0 ? (m0 + m) * a.grad_ld + f_ : 0);
+            if (n >= 4) {
+                gr = load_four<T>(grad);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 3; ++e)
+                    if (e < n) gr[e] = Elem<T>::to_f32(grad[e]);
+            }
+            return gr;
+        };
+        // float32 has registers to ask for it before z is made (262144 rows of 64 to 2 128: 202 us, so 184);
+        // bfloat16 would spill (80 us, so 115).
+        constexpr bool kAhead = !Elem<T>::is_bf16;
+        f32x4 ahead[2][kAhead ? kM : 1];
+        if constexpr (kAhead) {
+#pragma unroll
+            for (int h = 0; h < (GATED ? 1 : 2); ++h)
+#pragma unroll
+                for (int j = 0; j < kM; ++j) {
+                    const int m = 16 * j + l16, at = column_of<GATED>(32 * wave + 16 * h) + 4 * g;
+                    ahead[h][j] = grad_of(m, at, m < left ? N - at : 0);
+                }
+        }
         // z: 32 columns of the wave's by 64 rows
         f32x4 z[2][kM];
+        const Turned<2> at_x = lanes_along<T>(xt, l16, g, 0), at_w = lanes_along<T>(w + wave * 4096, l16, g, 0);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -167,13 +216,14 @@ __global__ __launch_bounds__(kThreads, Elem<T>::is_bf16 ? 4 : 2) void small_back
         for (int r = 0; r < kCols / 32; ++r) {
             Operand<T> q[kM];
 #pragma unroll
-            for (int j = 0; j < kM; ++j) q[j] = S::X::along(xt, j, r, lf, gf);
+            for (int j = 0; j < kM; ++j) q[j] = S::X::along(lds, at_x, j, r);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) multiply<kM>(z[h], S::W::along(w, 2 * wave + h, r, lf, gf), q);
+            for (int h = 0; h < 2; ++h) multiply<kM>(z[h], S::W::along(lds, at_w, h, r), q);
         }
         // dz, rounded to the type.  The wave's two sixteens of z's columns, in the sheet's order, are a gate's
         // and its other half's, or neighbours; a lane has four of each.
-        lf = anew<T>(l16), gf = anew<T>(g);
+        const Turned<4> at_put = lanes_put<T>(dz + wave / 2 * S::Z::kPane, l16, g, wave % 2 * 2);
+        const int lf = anew<T>(l16), gf = anew<T>(g);
         int f[2];
         f32x4 bias[2];
 #pragma unroll
@@ -184,19 +234,11 @@ __global__ __launch_bounds__(kThreads, Elem<T>::is_bf16 ? 4 : 2) void small_back
 #pragma unroll
         for (int j = 0; j < kM; ++j) {
             const int m = 16 * j + lf;
-            const T *grad = (const T *)a.grad + (m < left ? (m0 + m) * a.grad_ld : 0);
             f32x4 d[2];
 #pragma unroll
             for (int h = 0; h < (GATED ? 1 : 2); ++h) {
                 const int n = m < left ? N - f[h] : 0;
-                f32x4 gr = {0.f, 0.f, 0.f, 0.f};
-                if (n >= 4) {
-                    gr = load_four<T>(grad + f[h]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 3; ++e)
-                        if (e < n) gr[e] = Elem<T>::to_f32(grad[f[h] + e]);
-                }
+                const f32x4 gr = kAhead ? ahead[h][kAhead ? j : 0] : grad_of(m, f[h], n);
                 float v[4], s[4], t[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) t[e] = z[h][j][e] + bias[h][e];
@@ -209,24 +251,25 @@ __global__ __launch_bounds__(kThreads, Elem<T>::is_bf16 ? 4 : 2) void small_back
                 }
             }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) S::Z::put4(dz, m, 32 * wave + 16 * h + 4 * gf, d[h]);
+            for (int h = 0; h < 2; ++h) S::Z::put4(lds + at_put.to[h ^ j % 2 * 2] + j * 2048, d[h]);
         }
         __syncthreads();
         // grad_x: 16 columns of C by 32 rows a wave (float32: 16)
         if (a.grad_x != nullptr) {
             f32x4 gx[kOwn];
-            lf = anew<T>(l16), gf = anew<T>(g);
             const int t = wave % 4, j0 = wave / 4 * kOwn;
+            const Turned<2> at_z = lanes_along<T>(dz + j0 * 2048, l16, g, j0 % 2);
+            const Turned<4> at_wd = lanes_down<T>(w, l16, g, t);
 #pragma unroll
             for (int j = 0; j < kOwn; ++j) gx[j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int r = 0; r < kWidth / 32; ++r) {
                 Operand<T> q[kOwn];
 #pragma unroll
-                for (int j = 0; j < kOwn; ++j) q[j] = S::Z::along(dz, j0 + j, r, lf, gf);
-                multiply<kOwn>(gx, S::W::down(w, t, r, lf, gf), q);
+                for (int j = 0; j < kOwn; ++j) q[j] = S::Z::along(lds, at_z, j, r);
+                multiply<kOwn>(gx, S::W::down(lds, at_wd, 0, r), q);
             }
-            const int c = 16 * t + 4 * gf;
+            const int lf = anew<T>(l16), c = 16 * t + 4 * anew<T>(g);
 #pragma unroll
             for (int j = 0; j < kOwn; ++j) {
                 const int m = 16 * (j0 + j) + lf;
@@ -235,18 +278,18 @@ __global__ __launch_bounds__(kThreads, Elem<T>::is_bf16 ? 4 : 2) void small_back
         }
         // grad_W: all columns of C by the wave's 32 of z
         if (a.part != nullptr) {
-            lf = anew<T>(l16), gf = anew<T>(g);
+            const Turned<4> at_z = lanes_down<T>(dz + wave / 2 * S::Z::kPane, l16, g, wave % 2 * 2), at_xd = lanes_down<T>(xt, l16, g, 0);
 #pragma unroll
             for (int r = 0; r < kRows / 32; ++r) {
-                const Operand<T> q[2] = {S::Z::down(dz, 2 * wave, r, lf, gf), S::Z::down(dz, 2 * wave + 1, r, lf, gf)};
+                const Operand<T> q[2] = {S::Z::down(lds, at_z, 0, r), S::Z::down(lds, at_z, 1, r)};
                 add_up<2>(sum, q);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) multiply<2>(gw[i], S::X::down(xt, i, r, lf, gf), q);
+                for (int i = 0; i < 4; ++i) multiply<2>(gw[i], S::X::down(lds, at_xd, i, r), q);
             }
         }
         if (tile + gridDim.x < tiles) {
             if constexpr (S::kXs == 1) __syncthreads();  // x is read
-            put(x + (now ^ (S::kXs - 1)) * S::X::kBytes);
+            put(lds + x + (now ^ (S::kXs - 1)) * S::X::kBytes);
         }
     }
     if (a.part != nullptr) {
