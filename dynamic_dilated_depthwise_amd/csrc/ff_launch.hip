@@ -25,7 +25,7 @@ template <typename T>
 static int64_t bytes_of(Kind kind, int64_t np, int64_t nq, int64_t nk) {
     int64_t most = 0;
     for (const bool direct : {false, true}) {
-        if (few_rows(kind, nq, direct)) continue;
+        if (few_rows(kind, np, nq, nk, Elem<T>::is_bf16, direct)) continue;
         most = std::max(most, part_bytes(Elem<T>::is_bf16, kind, cut_of<T>(kind, np, nq, nk, direct)));
     }
     return most;

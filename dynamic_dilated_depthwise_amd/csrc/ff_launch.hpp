@@ -56,10 +56,10 @@ struct Copy {
 // One or two copies; the second may have no rows.
 hipError_t launch_copies(const Copy &a, const Copy &b, bool bf16, hipStream_t stream);
 
-// The forward products of few rows (ff_rows.hip): up to kMostRows, of which launch_product takes it for
-// kFewRows, or all of them where the operands cannot go straight to LDS.
-constexpr int64_t kFewRows = 16, kMostRows = 64;
-hipError_t launch_rows(bool gated, const Product &a, bool bf16, hipStream_t stream);
+// The forward products of few rows (ff_rows.hip): up to kMostRows, from operands that can go straight to LDS
+// (chunked; where few_rows says so) or from any.
+constexpr int64_t kMostRows = 64;
+hipError_t launch_rows(bool gated, bool chunked, const Product &a, bool bf16, hipStream_t stream);
 
 // dz = grad * act'(saved), [rows, N]; gated: saved [rows, 2 N] and dz [rows, 2 N],
 // the gate's half grad * u * act'(g), the other grad * act(g).

@@ -126,9 +126,19 @@ inline Cut cut_of(Kind kind, int64_t np, int64_t nq, int64_t nk, bool direct) {
     return best;
 }
 
-// Whether the forward takes the kernel of few rows (ff_rows.hip).
-inline bool few_rows(Kind kind, int64_t nq, bool direct) {
-    return (kind == kForward || kind == kGatedForward) && nq <= (direct ? kFewRows : kMostRows);
+// Whether the forward takes a kernel of few rows (ff_rows.hip): for operands that cannot go straight to LDS
+// the one of any alignment, else the chunked one.  That reads all of x for each 16 columns of the result, so
+// it is for few of them, or for little of x.  Microseconds, chunked and tiles.  bfloat16: 48 rows of 5632 to
+// 2048 9.1, 15.1, of 512 to 8192 6.3, 5.4; 24 of 2048 to 5632 6.9, 11.1, to 32000 29.8, 20.7; one of 2048 to
+// 5632 5.3, 9, to 16384 15.0, 12.2.  float32, which is split at each read: 24 of 2048 to 5632 16.2, 19.3,
+// of 16384 to 512 44.5, 28.1; 48 of 4096 to 4096 21.5, 27.1, of 5632 to 2048 23.4, 22.0; 64 of 1024 to 2304
+// 9.3, 12.2, of 2048 to 5632 29.5, 23.6.
+inline bool few_rows(Kind kind, int64_t np, int64_t nq, int64_t nk, bool bf16, bool direct) {
+    if ((kind != kForward && kind != kGatedForward) || nq > kMostRows) return false;
+    if (!direct) return true;
+    const int64_t blocks = (np + 15) / 16;
+    if (bf16) return blocks <= (nq <= 32 ? 512 : 256);
+    return nq <= 16 || (blocks <= 512 && nk <= (nq <= 32 ? 8192 : nq <= 48 ? 4096 : 1024));
 }
 
 // Bytes of the pieces' results.
@@ -162,7 +172,7 @@ hipError_t product(Product a, void *work, hipStream_t stream) {
     constexpr Epi e = KindOf<K>::e;
     const bool direct = direct_ok<T>(sp, a.p, a.p_ld, a.np, a.nk, K == kGatedForward ? a.np + 256 : 256, a.p_padded) &&
                         direct_ok<T>(sq, a.q, a.q_ld, a.nq, a.nk, 256, a.q_padded);
-    if (few_rows(K, a.nq, direct)) return launch_rows(K == kGatedForward, a, Elem<T>::is_bf16, stream);
+    if (few_rows(K, a.np, a.nq, a.nk, Elem<T>::is_bf16, direct)) return launch_rows(K == kGatedForward, direct, a, Elem<T>::is_bf16, stream);
     const Cut c = cut_of<T>(K, a.np, a.nq, a.nk, direct);
     a.part = (float *)work;
 #define DDPM_FF_FORM(k, DIRECT)                                                                       \

@@ -74,6 +74,20 @@ def test_sizes(rows, C, N, gated, dt):
     compare(*case(rows, C, N, DT[dt], gated), "silu" if gated else "none", gated)
 
 
+# A decoding batch's tokens, at each end of the forms' ranges of rows; contractions of a part of a step, of fewer
+# steps than waves, and of many; results that end inside sixteen columns.
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("gated", [False, True], ids=["linear", "gated"])
+@pytest.mark.parametrize("rows", [1, 8, 16, 17, 32, 33, 48, 49, 64])
+def test_tokens(rows, gated, dt):
+    announce("ff tokens", rows, gated, dt)
+    for C, N in ((8, 24), (104, 40), (1024, 72), (2056, 130), (8200, 16), (8, 8200)):
+        x, w, b, r, _ = case(rows, C, N, DT[dt], gated)
+        for act in ("none", "silu"):
+            y = forward(x, w, b, r, act, gated)[0]
+            orc.check(y, orc.run(x, w, b, r, act, gated=gated)["y"], DT[dt], f"y of {C} to {N}", 2 * C + 64)
+
+
 # Many tiles, so that bfloat16 takes the large ones, for each product of the two passes: y, grad_x, grad_weight.
 @pytest.mark.parametrize("gated", [False, True], ids=["linear", "gated"])
 @pytest.mark.parametrize("rows,C,N", [(3400, 88, 3304), (3333, 2944, 104), (104, 3368, 3400)])
