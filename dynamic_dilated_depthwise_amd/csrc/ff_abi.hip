@@ -49,10 +49,20 @@ int64_t weight_copy_bytes(const Sizes &s, bool bf16) { return rounded(s.width * 
 double forward_time(Kind kind, const Sizes &s, bool bf16, bool straight) {
     return product_time(kind, s.N, s.rows, s.C, bf16, straight);
 }
+// The same of few rows: nanoseconds of an element of the contraction, as measured with 1 to 64 rows and C from
+// 256 to 5632 (with copies at hand at least the weight's way).  Rows of odd length, straight and by copies,
+// microseconds: bfloat16 64 rows of 5633 to 128 85, 13, 24 of 4097 to 4096 35, 25, one 17, 23; float32 64 of
+// 5633 to 128 51, 26, of 4097 to 4096 39, 60.
+double rows_time(Kind kind, const Sizes &s, bool bf16, bool straight) {
+    const double halves = kind == kGatedForward ? 2. : 1., k = s.C * 1e-3, weight = (double)weight_copy_bytes(s, bf16) / 5e6;
+    if (straight) return 4. + std::max(k * (bf16 ? 0.2 * halves + 0.013 * s.rows : 1.5 * halves + 0.04 * s.rows), weight);
+    return 4. + k * (bf16 ? 3. * halves + 0.18 * s.rows : 2. * halves + 0.1 * s.rows) * std::max(1., s.N / 8192.);
+}
 bool forward_copies(Kind kind, const Sizes &s, bool bf16) {
-    if (s.C % chunk(bf16) == 0 || s.rows <= kMostRows) return false;
-    return forward_time(kind, s, bf16, true) + copies_time(x_copy_bytes(s, bf16) + weight_copy_bytes(s, bf16)) <
-           forward_time(kind, s, bf16, false);
+    if (s.C % chunk(bf16) == 0) return false;
+    const double copies = copies_time(x_copy_bytes(s, bf16) + weight_copy_bytes(s, bf16));
+    if (s.rows <= kMostRows) return copies + rows_time(kind, s, bf16, true) < rows_time(kind, s, bf16, false);
+    return forward_time(kind, s, bf16, true) + copies < forward_time(kind, s, bf16, false);
 }
 bool backward_copies(Kind kind, const Sizes &s, bool again, bool bf16) {
     if (s.C % chunk(bf16) == 0) return false;

@@ -81,7 +81,7 @@ def test_sizes(rows, C, N, gated, dt):
 @pytest.mark.parametrize("rows", [1, 8, 16, 17, 32, 33, 48, 49, 64])
 def test_tokens(rows, gated, dt):
     announce("ff tokens", rows, gated, dt)
-    for C, N in ((8, 24), (104, 40), (1024, 72), (2056, 130), (8200, 16), (8, 8200)):
+    for C, N in ((8, 24), (104, 40), (1024, 72), (2056, 130), (8200, 16), (8, 8200), (5633, 43), (1021, 2050)):
         x, w, b, r, _ = case(rows, C, N, DT[dt], gated)
         for act in ("none", "silu"):
             y = forward(x, w, b, r, act, gated)[0]
