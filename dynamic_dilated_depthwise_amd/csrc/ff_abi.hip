@@ -47,7 +47,7 @@ int64_t saved_floats(const Sizes &s, bool through, bool bf16) { return !through 
 int64_t x_copy_bytes(const Sizes &s, bool bf16) { return rounded(s.rows * padded(s.C, bf16) * element(bf16)); }
 int64_t weight_copy_bytes(const Sizes &s, bool bf16) { return rounded(s.width * padded(s.C, bf16) * element(bf16)); }
 double forward_time(Kind kind, const Sizes &s, bool bf16, bool straight) {
-    return product_time(kind, s.N, s.rows, s.C, bf16, straight);
+    return product_time(kind, s.N, s.rows, s.C, 1, bf16, straight);
 }
 // The same of few rows: nanoseconds of an element of the contraction, as measured with 1 to 64 rows and C from
 // 256 to 5632 (with copies at hand at least the weight's way).  Rows of odd length, straight and by copies,
@@ -64,11 +64,11 @@ bool forward_copies(Kind kind, const Sizes &s, bool bf16) {
     if (s.rows <= kMostRows) return copies + rows_time(kind, s, bf16, true) < rows_time(kind, s, bf16, false);
     return forward_time(kind, s, bf16, true) + copies < forward_time(kind, s, bf16, false);
 }
-bool backward_copies(Kind kind, const Sizes &s, bool again, bool bf16) {
+bool backward_copies(Kind kind, const Sizes &s, bool again, int terms, bool bf16) {
     if (s.C % chunk(bf16) == 0) return false;
     const auto all = [&](bool straight) {
-        return product_time(kGradX, s.C, s.rows, s.width, bf16, straight) +
-               product_time(kGradWeight, s.C, s.width, s.rows, bf16, straight) + (again ? forward_time(kind, s, bf16, straight) : 0.);
+        return product_time(kGradX, s.C, s.rows, s.width, terms, bf16, straight) +
+               product_time(kGradWeight, s.C, s.width, s.rows, terms, bf16, straight) + (again ? forward_time(kind, s, bf16, straight) : 0.);
     };
     return all(true) + copies_time(x_copy_bytes(s, bf16) + weight_copy_bytes(s, bf16)) < all(false);
 }
@@ -88,7 +88,7 @@ int64_t forward_workspace(Kind kind, const Sizes &s, int dtype) {
     if (!sizes_ok(c, s, DDPM_ACT_NONE)) return 0;
     const bool bf16 = is_bf16(dtype);
     return (forward_copies(kind, s, bf16) ? x_copy_bytes(s, bf16) + weight_copy_bytes(s, bf16) : 0) +
-           product_bytes(kind, s.N, s.rows, s.C, bf16);
+           product_bytes(kind, s.N, s.rows, s.C, 1, bf16);
 }
 
 int64_t saved_count(const Sizes &s, bool gated, int activation, int dtype) {
@@ -145,10 +145,14 @@ int forward(Kind kind, const void *x, const void *weight, const void *bias, cons
 // or a gate, and where grad's rows are no whole chunks and many enough), copies, the products' pieces.
 struct Room {
     bool small, own_dz, copies, again;
-    int64_t dz, all;
+    int64_t dz, low, all;  // dz's bytes, elements to its second term (or 0), all bytes
 };
+// Whether dz has more bits than the type: behind relu alone it is grad or zero.
+bool two_terms(Kind kind, bool through, int activation, bool bf16) {
+    return through && bf16 && (kind == kGatedForward || activation != DDPM_ACT_RELU);
+}
 constexpr double kManyFlops = 5e9;  // of one product: from here on a copy of grad costs less than what it saves
-Room backward_room(Kind kind, const Sizes &s, bool through, bool bf16) {
+Room backward_room(Kind kind, const Sizes &s, bool through, int activation, bool bf16) {
     Room r = {};
     r.small = through && small_backward(s.C, s.width);
     if (r.small) {
@@ -157,17 +161,21 @@ Room backward_room(Kind kind, const Sizes &s, bool through, bool bf16) {
     }
     r.own_dz = through || (s.N % chunk(bf16) != 0 && 2. * s.rows * s.N * s.C >= kManyFlops);
     r.again = through && makes_again(s, bf16);
-    r.copies = backward_copies(kind, s, r.again, bf16);
-    r.dz = r.own_dz ? rounded(s.rows * padded(s.width, bf16) * element(bf16)) : 0;
-    int64_t part = std::max(product_bytes(kGradX, s.C, s.rows, s.width, bf16), product_bytes(kGradWeight, s.C, s.width, s.rows, bf16));
-    if (r.again) part = std::max(part, product_bytes(kind, s.N, s.rows, s.C, bf16));
+    const int terms = two_terms(kind, through, activation, bf16) ? 2 : 1;
+    const int64_t dz = s.rows * padded(s.width, bf16);
+    r.copies = backward_copies(kind, s, r.again, terms, bf16);
+    r.dz = r.own_dz ? rounded(terms * dz * element(bf16)) : 0;
+    r.low = terms == 2 ? dz : 0;
+    int64_t part = std::max(product_bytes(kGradX, s.C, s.rows, s.width, terms, bf16),
+                            product_bytes(kGradWeight, s.C, s.width, s.rows, terms, bf16));
+    if (r.again) part = std::max(part, product_bytes(kind, s.N, s.rows, s.C, 1, bf16));
     r.all = r.dz + (r.copies ? x_copy_bytes(s, bf16) + weight_copy_bytes(s, bf16) : 0) + part;
     return r;
 }
 
 int64_t backward_workspace(Kind kind, const Sizes &s, bool through, int activation, int dtype) {
     Check c(dtype);
-    return sizes_ok(c, s, activation) ? backward_room(kind, s, through, is_bf16(dtype)).all : 0;
+    return sizes_ok(c, s, activation) ? backward_room(kind, s, through, activation, is_bf16(dtype)).all : 0;
 }
 
 int backward(Kind kind, const void *grad, const void *x, const void *weight, const float *saved, void *grad_x,
@@ -186,7 +194,7 @@ int backward(Kind kind, const void *grad, const void *x, const void *weight, con
     c.maybe_out(grad_x, (double)s.rows * s.C, c.es());
     c.maybe_out(grad_weight, (double)s.width * s.C, c.es());
     c.maybe_out(grad_bias, s.width, c.es());
-    const Room room = backward_room(kind, s, through, bf16);
+    const Room room = backward_room(kind, s, through, activation, bf16);
     if (room.all > 0) c.workspace(workspace, (double)room.all);
     const int st = c.done();
     if (st != DDPM_OK) return st;
@@ -212,13 +220,14 @@ int backward(Kind kind, const void *grad, const void *x, const void *weight, con
             z.nq = s.rows;
             z.nk = s.C;
             z.out = workspace;
+            z.low = room.low;
             z.kept = const_cast<float *>(saved);
             z.grad = grad;
             z.grad_ld = grad_row;
             z.act = activation;
             e = launch_product(kind, z, work, bf16, stream);
         } else if (through) {
-            e = launch_dz(gated, grad, grad_row, saved, workspace, s.rows, s.N, activation, bf16, stream);
+            e = launch_dz(gated, grad, grad_row, saved, workspace, room.low, s.rows, s.N, activation, bf16, stream);
         } else {
             e = launch_copies({grad, grad_row, s.rows, s.N, workspace}, {}, bf16, stream);
         }
@@ -227,6 +236,7 @@ int backward(Kind kind, const void *grad, const void *x, const void *weight, con
     a.q = room.own_dz ? workspace : grad;
     a.q_ld = room.own_dz ? padded(s.width, bf16) : grad_row;
     a.q_padded = room.own_dz;
+    a.low = room.low;
     a.p_padded = room.copies;
     a.np = s.C;
     if (e == hipSuccess && grad_x != nullptr) {

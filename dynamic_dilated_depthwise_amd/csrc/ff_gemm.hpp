@@ -40,6 +40,8 @@ enum Epi { kStore, kLinear, kGated, kWeight };
 constexpr int kStepBytes = 128;
 template <typename T> constexpr int kStep = kStepBytes / (int)sizeof(T);  // elements of a step
 
+constexpr float kMostBf16 = 3.38953139e38f;  // the largest bfloat16
+
 constexpr uint32_t kRecords = 0x7fffffe0u, kOutside = 0x7ffffff0u;  // of a buffer; an offset past it
 
 // All but this wave's last N loads to LDS are there and its own LDS accesses done; then the workgroup.
@@ -112,7 +114,7 @@ struct Tile {
         p = (const T *)base + (S == kAlong ? from * ld + k0 : k0 * ld + from);
         columns = (int)(extent - from < TILE ? extent - from : TILE);
     }
-    __device__ __forceinline__ void next() { p += S == kAlong ? kStep<T> : kStep<T> * ld; }
+    __device__ __forceinline__ int64_t step() const { return S == kAlong ? kStep<T> : kStep<T> * ld; }  // elements to the next one's
     // Round i of the chunks of the step, of which `left` elements of the contraction are there, straight to LDS.
     __device__ __forceinline__ void ask(int i, char *lds, int64_t left, int tid) const {
         Offset o = off[i];
@@ -154,9 +156,11 @@ struct Tile {
 // precision.  The nearest bfloat16 is taken each time: with bits cut off instead, the terms left out
 // would be four times larger and all of the product's sign.
 constexpr int kParts = 3;
-struct Split {
-    bf16x8 part[kParts];
+template <int N>
+struct Terms {
+    bf16x8 part[N];
 };
+typedef Terms<kParts> Split;
 template <typename T> struct OperandOf { typedef Split type; };
 template <> struct OperandOf<bf16_t> { typedef bf16x8 type; };
 template <typename T> using Operand = typename OperandOf<T>::type;
@@ -188,6 +192,13 @@ __device__ __forceinline__ void multiply(f32x4 (&acc)[NQ], const bf16x8 &p, cons
 #pragma unroll
     for (int j = 0; j < NQ; ++j) acc[j] = mma(p, q[j], acc[j]);
 }
+template <int NQ, int N>
+__device__ __forceinline__ void multiply(f32x4 (&acc)[NQ], const bf16x8 &p, const Terms<N> (&q)[NQ]) {
+#pragma unroll
+    for (int k = N - 1; k >= 0; --k)
+#pragma unroll
+        for (int j = 0; j < NQ; ++j) acc[j] = mma(p, q[j].part[k], acc[j]);
+}
 template <int NQ>
 __device__ __forceinline__ void multiply(f32x4 (&acc)[NQ], const Split &p, const Split (&q)[NQ]) {
 #pragma unroll
@@ -208,12 +219,9 @@ template <int NQ>
 __device__ __forceinline__ void add_up(f32x4 (&sum)[NQ], const bf16x8 (&q)[NQ]) {
     multiply<NQ>(sum, ones_frag(), q);
 }
-template <int NQ>
-__device__ __forceinline__ void add_up(f32x4 (&sum)[NQ], const Split (&q)[NQ]) {
-#pragma unroll
-    for (int k = kParts - 1; k >= 0; --k)
-#pragma unroll
-        for (int j = 0; j < NQ; ++j) sum[j] = mma(ones_frag(), q[j].part[k], sum[j]);
+template <int NQ, int N>
+__device__ __forceinline__ void add_up(f32x4 (&sum)[NQ], const Terms<N> (&q)[NQ]) {
+    multiply<NQ>(sum, ones_frag(), q);
 }
 
 // Fragments: slot e of lane group g stands for contraction index 8 g + e of a run of 32.
@@ -316,35 +324,56 @@ __device__ __forceinline__ void bias8(const Product &a, int64_t p, int half, flo
 __device__ __forceinline__ void keep8(const Product &a, int64_t p, int half, const float (&v)[8]) {
     if (a.kept != nullptr && a.grad == nullptr && p < a.np) write8<float>(a.kept + half * a.np + p, a.np - p, v);
 }
+// The value next to v that bfloat16 has; finite, so that what it leaves of v is its distance from v and not NaN.
+__device__ __forceinline__ float first_term(float v) { return round_to_bf16(__builtin_amdgcn_fmed3f(v, -kMostBf16, kMostBf16)); }
+// dz: rounded to bfloat16 alone it would make the gradients' error 1.4 times that of their own rounding, so
+// that what the rounding leaves is kept beside it, `low` elements behind (0: the values are bfloat16's, or
+// T is float32).  An infinity is the largest number and an infinity.
+template <typename T>
+__device__ __forceinline__ void write_dz(T *p, int64_t low, int64_t n, float (&v)[8]) {
+    if constexpr (Elem<T>::is_bf16) {
+        if (low != 0) {
+            float rest[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float t = first_term(v[e]);
+                rest[e] = v[e] - t;
+                v[e] = t;
+            }
+            write8<T>(p + low, n, rest);
+        }
+    }
+    write8<T>(p, n, v);
+}
 // Row q of dz: its zeros behind the last of `width` columns, up to a whole chunk.
 template <typename T>
-__device__ __forceinline__ void pad_row(T *row, int64_t width) {
-    for (int64_t c = width; c % kVec<T> != 0; ++c) row[c] = 0;
+__device__ __forceinline__ void pad_row(T *row, int64_t low, int64_t width) {
+    for (int64_t c = width; c % kVec<T> != 0; ++c) row[c] = row[low + c] = 0;
 }
 // dz of eight columns from p: grad act'(z); gated: grad u act'(g) and grad act(g).
 template <typename T>
-__device__ __forceinline__ void finish_dz(T *row, int64_t p, int64_t N, const T *grad, int act, const float (&z)[8]) {
+__device__ __forceinline__ void finish_dz(T *row, int64_t low, int64_t p, int64_t N, const T *grad, int act, const float (&z)[8]) {
     const int64_t n = N - p;
     float g[8], v[8], d[8];
     read8<T>(grad + p, n, g);
     slopes(z, v, d, act);
 #pragma unroll
     for (int e = 0; e < 8; ++e) d[e] *= g[e];
-    write8<T>(row + p, n, d);
-    if (n <= 8) pad_row(row, N);
+    write_dz<T>(row + p, low, n, d);
+    if (n <= 8) pad_row(row, low, N);
 }
 template <typename T>
-__device__ __forceinline__ void finish_gated_dz(T *row, int64_t p, int64_t N, const T *grad, int act, const float (&z)[8],
-                                                const float (&u)[8]) {
+__device__ __forceinline__ void finish_gated_dz(T *row, int64_t low, int64_t p, int64_t N, const T *grad, int act,
+                                                const float (&z)[8], const float (&u)[8]) {
     const int64_t n = N - p;
     float g[8], v[8], d[8];
     read8<T>(grad + p, n, g);
     slopes(z, v, d, act);
 #pragma unroll
     for (int e = 0; e < 8; ++e) { d[e] = g[e] * u[e] * d[e]; v[e] = g[e] * v[e]; }
-    write8<T>(row + p, n, d);
-    write8<T>(row + N + p, n, v);
-    if (n <= 8) pad_row(row, 2 * N);
+    write_dz<T>(row + p, low, n, d);
+    write_dz<T>(row + N + p, low, n, v);
+    if (n <= 8) pad_row(row, low, 2 * N);
 }
 
 // What follows the product for eight neighbouring columns p of row q: z without its bias.
@@ -355,7 +384,7 @@ __device__ __forceinline__ void finish_linear(const Product &a, int64_t q, int64
 #pragma unroll
     for (int e = 0; e < 8; ++e) z[e] += bias[e];
     if (a.grad != nullptr) {
-        finish_dz<T>((T *)a.out + q * padded(a.np, Elem<T>::is_bf16), p, a.np, (const T *)a.grad + q * a.grad_ld, a.act, z);
+        finish_dz<T>((T *)a.out + q * padded(a.np, Elem<T>::is_bf16), a.low, p, a.np, (const T *)a.grad + q * a.grad_ld, a.act, z);
         return;
     }
     if (a.saved != nullptr) write8<float>(a.saved + q * a.np + p, n, z);
@@ -377,7 +406,8 @@ __device__ __forceinline__ void finish_gated(const Product &a, int64_t q, int64_
 #pragma unroll
     for (int e = 0; e < 8; ++e) { g[e] += gb[e]; u[e] += ub[e]; }
     if (a.grad != nullptr) {
-        finish_gated_dz<T>((T *)a.out + q * padded(2 * a.np, Elem<T>::is_bf16), p, a.np, (const T *)a.grad + q * a.grad_ld, a.act, g, u);
+        finish_gated_dz<T>((T *)a.out + q * padded(2 * a.np, Elem<T>::is_bf16), a.low, p, a.np, (const T *)a.grad + q * a.grad_ld,
+                           a.act, g, u);
         return;
     }
     if (a.saved != nullptr) {
@@ -478,8 +508,25 @@ struct Gemm {
             }
         };
 
-        const int steps = (int)((k1 - k0 + kStep<T> - 1) / kStep<T>);
+        // With two terms of Q a step of the contraction is two: P's tile with that of Q's first term, then again
+        // with the second one's (behind each other, so that the L2 has P's the second time).
+        constexpr bool kMayTwo = Elem<T>::is_bf16 && (E == kStore || E == kWeight);
+        const bool two = kMayTwo && a.low != 0;
+        const int steps = (int)((k1 - k0 + kStep<T> - 1) / kStep<T>) << two;
         int64_t left = k1 - k0;
+        bool second = false;
+        const auto advance = [&] {
+            if constexpr (kMayTwo) {
+                second = two && !second;
+                tile_p.p += second ? 0 : tile_p.step();
+                tile_q.p += second ? a.low : tile_q.step() - a.low;
+                left -= second ? 0 : kStep<T>;
+            } else {
+                tile_p.p += tile_p.step();
+                tile_q.p += tile_q.step();
+                left -= kStep<T>;
+            }
+        };
         if constexpr (DIRECT) {
             constexpr int kP1 = decltype(tile_p)::kCount, kAll = kP1 + decltype(tile_q)::kCount;
             const auto ask = [&](int i, char *at) {
@@ -489,11 +536,6 @@ struct Gemm {
             // Loads of kStages - 1 steps are under way behind the one that is computed; what is asked for
             // past the last step is nothing (zeros for LDS that nobody reads), so that a wave's count of
             // loads in flight is the same in every step.
-            const auto advance = [&] {
-                left -= kStep<T>;
-                tile_p.next();
-                tile_q.next();
-            };
 #pragma unroll
             for (int t = 0; t < kStages - 1; ++t) {
 #pragma unroll
@@ -520,13 +562,11 @@ struct Gemm {
             tile_q.fetch(left, tid);
             for (int s = 0; s < steps; ++s) {
                 char *now = lds + (s & 1) * kStageBytes;
-                left -= kStep<T>;
                 tile_p.put(now, tid);
                 tile_q.put(now + kP * kStepBytes, tid);
                 arrive_lds();
                 if (s + 1 < steps) {
-                    tile_p.next();
-                    tile_q.next();
+                    advance();
                     tile_p.fetch(left, tid);
                     tile_q.fetch(left, tid);
                 }

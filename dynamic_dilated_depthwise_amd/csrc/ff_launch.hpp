@@ -16,6 +16,7 @@ struct Product {
     const void *p, *q;
     int64_t p_ld, q_ld, np, nq, nk;
     bool p_padded, q_padded;            // rows that end in zeros up to whole 16-byte chunks
+    int64_t low;                        // gradients: elements from Q to its second term (two_terms), or 0
     void *out;
     void *sums;                         // weight's gradient: [nq], sums over k of Q
     float *saved;                       // forward: what the activation is applied to, or null
@@ -23,7 +24,7 @@ struct Product {
     int64_t residual_ld;
     int act;
     // Where the backward makes z again: the forward writes its bias here in float32, and the backward's
-    // call has it with grad [nq, np], and out is dz (rows as launch_dz writes them).
+    // call has it with grad [nq, np], and out is dz (rows and terms, `low` apart, as launch_dz writes them).
     float *kept;
     const void *grad;
     int64_t grad_ld;
@@ -37,11 +38,11 @@ struct Product {
 
 enum Kind { kForward, kGatedForward, kGradX, kGradWeight };
 
-// Bytes that launch_product needs at `work` (for these sizes, any strides and alignment).
-int64_t product_bytes(Kind kind, int64_t np, int64_t nq, int64_t nk, bool bf16);
+// Bytes that launch_product needs at `work` (for these sizes, any strides and alignment); terms: of Q, one or two.
+int64_t product_bytes(Kind kind, int64_t np, int64_t nq, int64_t nk, int terms, bool bf16);
 hipError_t launch_product(Kind kind, const Product &a, void *work, bool bf16, hipStream_t stream);
 // Microseconds of a product, straight to LDS or not, as far as its cut foresees.
-double product_time(Kind kind, int64_t np, int64_t nq, int64_t nk, bool bf16, bool straight);
+double product_time(Kind kind, int64_t np, int64_t nq, int64_t nk, int terms, bool bf16, bool straight);
 // Those of copies (below) of so many bytes.
 double copies_time(int64_t bytes);
 
@@ -63,9 +64,10 @@ hipError_t launch_rows(bool gated, bool chunked, const Product &a, bool bf16, hi
 
 // dz = grad * act'(saved), [rows, N]; gated: saved [rows, 2 N] and dz [rows, 2 N],
 // the gate's half grad * u * act'(g), the other grad * act(g).
-// dz's rows are padded as a Copy's.
-hipError_t launch_dz(bool gated, const void *grad, int64_t grad_ld, const float *saved, void *dz, int64_t rows, int64_t N,
-                     int act, bool bf16, hipStream_t stream);
+// dz's rows are padded as a Copy's; its second term, what rounding the first one left, is `low` elements behind
+// it (0: one term).
+hipError_t launch_dz(bool gated, const void *grad, int64_t grad_ld, const float *saved, void *dz, int64_t low, int64_t rows,
+                     int64_t N, int act, bool bf16, hipStream_t stream);
 
 // The whole backward through an activation or a gate of few channels, which makes z again
 // (ff_small.hip): whether these sizes are, the bytes of its partials, and the call.

@@ -25,7 +25,7 @@ __device__ __forceinline__ Place place_of(int64_t i, int64_t per) {
 
 template <typename T, bool GATED>
 __global__ __launch_bounds__(kThreads) void dz_kernel(const T *__restrict__ grad, int64_t grad_ld, const float *__restrict__ saved,
-                                                      T *__restrict__ dz, int64_t ld, int64_t rows, int64_t N, int act) {
+                                                      T *__restrict__ dz, int64_t low, int64_t ld, int64_t rows, int64_t N, int act) {
     const int64_t per = (N + 7) / 8, all = rows * per, stride = (int64_t)gridDim.x * kThreads;
     for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < all; i += stride) {
         const Place at = place_of(i, per);
@@ -37,9 +37,9 @@ __global__ __launch_bounds__(kThreads) void dz_kernel(const T *__restrict__ grad
         read8<float>(s, n, z);
         if constexpr (GATED) {
             read8<float>(s + N, n, u);
-            finish_gated_dz<T>(o, at.col, N, g, act, z, u);
+            finish_gated_dz<T>(o, low, at.col, N, g, act, z, u);
         } else {
-            finish_dz<T>(o, at.col, N, g, act, z);
+            finish_dz<T>(o, low, at.col, N, g, act, z);
         }
     }
 }
@@ -75,21 +75,21 @@ unsigned blocks_for(int64_t rows, int64_t N) {
 }
 
 template <typename T>
-hipError_t dz_of(bool gated, const void *grad, int64_t grad_ld, const float *saved, void *dz, int64_t rows, int64_t N, int act,
-                 hipStream_t stream) {
+hipError_t dz_of(bool gated, const void *grad, int64_t grad_ld, const float *saved, void *dz, int64_t low, int64_t rows, int64_t N,
+                 int act, hipStream_t stream) {
     const dim3 grid(blocks_for(rows, N)), threads(kThreads);
     const int64_t ld = padded(gated ? 2 * N : N, Elem<T>::is_bf16);
-    if (gated) hipLaunchKernelGGL((dz_kernel<T, true>), grid, threads, 0, stream, (const T *)grad, grad_ld, saved, (T *)dz, ld, rows, N, act);
-    else hipLaunchKernelGGL((dz_kernel<T, false>), grid, threads, 0, stream, (const T *)grad, grad_ld, saved, (T *)dz, ld, rows, N, act);
+    if (gated) hipLaunchKernelGGL((dz_kernel<T, true>), grid, threads, 0, stream, (const T *)grad, grad_ld, saved, (T *)dz, low, ld, rows, N, act);
+    else hipLaunchKernelGGL((dz_kernel<T, false>), grid, threads, 0, stream, (const T *)grad, grad_ld, saved, (T *)dz, low, ld, rows, N, act);
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_dz(bool gated, const void *grad, int64_t grad_ld, const float *saved, void *dz, int64_t rows, int64_t N,
-                     int act, bool bf16, hipStream_t stream) {
-    return bf16 ? dz_of<bf16_t>(gated, grad, grad_ld, saved, dz, rows, N, act, stream)
-                : dz_of<float>(gated, grad, grad_ld, saved, dz, rows, N, act, stream);
+hipError_t launch_dz(bool gated, const void *grad, int64_t grad_ld, const float *saved, void *dz, int64_t low, int64_t rows,
+                     int64_t N, int act, bool bf16, hipStream_t stream) {
+    return bf16 ? dz_of<bf16_t>(gated, grad, grad_ld, saved, dz, low, rows, N, act, stream)
+                : dz_of<float>(gated, grad, grad_ld, saved, dz, low, rows, N, act, stream);
 }
 
 hipError_t launch_copies(const Copy &a, const Copy &b, bool bf16, hipStream_t stream) {

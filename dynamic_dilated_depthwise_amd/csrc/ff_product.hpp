@@ -111,13 +111,16 @@ inline Cut cut_for(const Form &f, bool bf16, int64_t p, int64_t q, int64_t steps
 }
 
 template <typename T>
-inline Cut cut_of(Kind kind, int64_t np, int64_t nq, int64_t nk, bool direct) {
+inline Cut cut_of(Kind kind, int64_t np, int64_t nq, int64_t nk, int terms, bool direct) {
     constexpr bool bf16 = Elem<T>::is_bf16;
     const int64_t p = kind == kGatedForward ? 2 * np : np, steps = (nk + kStep<T> - 1) / kStep<T>;
     Cut best;
     for (int k = 0; k < kFormCount; ++k) {
         if (!direct && k != kGeneral) continue;
-        Cut c = cut_for(form_of(bf16, kind, k), bf16, p, nq, steps);
+        Form f = form_of(bf16, kind, k);
+        f.busy *= terms;  // a step of each term
+        f.alone *= terms;
+        Cut c = cut_for(f, bf16, p, nq, steps);
         c.form = k;
         if (best.tiles_p == 0 || c.cost < best.cost) best = c;
     }
@@ -173,7 +176,7 @@ hipError_t product(Product a, void *work, hipStream_t stream) {
     const bool direct = direct_ok<T>(sp, a.p, a.p_ld, a.np, a.nk, K == kGatedForward ? a.np + 256 : 256, a.p_padded) &&
                         direct_ok<T>(sq, a.q, a.q_ld, a.nq, a.nk, 256, a.q_padded);
     if (few_rows(K, a.np, a.nq, a.nk, Elem<T>::is_bf16, direct)) return launch_rows(K == kGatedForward, direct, a, Elem<T>::is_bf16, stream);
-    const Cut c = cut_of<T>(K, a.np, a.nq, a.nk, direct);
+    const Cut c = cut_of<T>(K, a.np, a.nq, a.nk, (K == kGradX || K == kGradWeight) && a.low != 0 ? 2 : 1, direct);
     a.part = (float *)work;
 #define DDPM_FF_FORM(k, DIRECT)                                                                       \
     if (c.form == k) {                                                                                \

@@ -6,12 +6,11 @@
 // The weight stays in LDS, z and dz never leave the chip: a workgroup takes 64 rows at a time (float32:
 // 32), makes their z (its waves 32 columns each), puts dz into LDS, and multiplies it by both; grad_W
 // stays in registers until the workgroup's last rows and leaves as one row of float32 partials, which a
-// second kernel adds up.  65536 rows of 64 to 2 128 take 38 us in bfloat16 and 52 in float32, 262144 rows 86
-// and 172; as products of their own (z, dz, grad_x, grad_W) 44 and 84, 128 and 295.  The bytes alone are
-// 6.5 us and 13.  What bounds it are vector instructions (bfloat16: 76 % of the cycles; float32: 36 %, and 38 %
+// second kernel adds up.  65536 rows of 64 to 2 128 take 36 us in bfloat16 and 52 in float32, 262144 rows 103
+// and 169.  The bytes alone are 6.5 us and 13.  What bounds it are vector instructions (bfloat16: 76 % of the cycles; float32: 36 %, and 38 %
 // the matrix units), most of them the activation's slopes and the fragments' and rows' addresses.
 //
-// Everything in LDS is bfloat16, of float32 three planes (see split_of), each made once: split at every
+// Everything in LDS is bfloat16, of float32 three planes (see split_of), of bfloat16's dz two, each made once: split at every
 // read the kernel took 79 us for 65536 rows of 64 to 2 128, most of it vector instructions.  A sheet is
 // ROWS rows of 128 bytes for each 64 columns, its 16-byte chunks placed by an exclusive or with bits of
 // the row, such that fragments are read both along its rows and down its columns with few conflicts.
@@ -25,39 +24,35 @@ namespace {
 
 constexpr int kCols = 64, kWidth = 256, kThreads = 512;
 template <typename T> constexpr int kCopies = Elem<T>::is_bf16 ? 1 : kParts;  // planes of a sheet
-
-// A lane's number, made anew where a phase begins, so that what is computed from it holds no register between:
-// with bfloat16's 128 registers a lane 79 us for 262144 rows of 64 to 2 128 (held, and spilled, 120), with
-// float32's 256 204 us and held 202 (the kernel alone).
-template <typename T> __device__ __forceinline__ int anew(int v) { return Elem<T>::is_bf16 ? afresh(v) : v; }
+template <typename T> constexpr int kTermsOfZ = Elem<T>::is_bf16 ? 2 : kParts;      // of dz's
 
 // A lane's places in a sheet, made once a phase: those of its fragments differ by an exclusive or of a chunk's
 // number with a constant below N and by constants that the instructions hold.
 template <int N> struct Turned { int to[N]; };
 // turn: uniform; by: bytes of a turn
-template <typename T, int N> __device__ __forceinline__ Turned<N> turned(int sheet, int lane_at, int turn, int by) {
+template <int N> __device__ __forceinline__ Turned<N> turned(int sheet, int lane_at, int turn, int by) {
     Turned<N> r;
-    lane_at = anew<T>(lane_at);
 #pragma unroll
-    for (int v = 0; v < N; ++v) r.to[v] = anew<T>(sheet + (lane_at ^ (turn ^ v) * by));
+    for (int v = 0; v < N; ++v) r.to[v] = sheet + (lane_at ^ (turn ^ v) * by);
     return r;
 }
 // Row l16, column 8 g; a turn where 16 rows or 32 columns further.
-template <typename T> __device__ __forceinline__ Turned<2> lanes_along(int sheet, int l16, int g, int turn) {
-    return turned<T, 2>(sheet, l16 * 128 + (((g ^ l16 ^ l16 / 8 * 2) & 7) << 4), turn, 64);
+__device__ __forceinline__ Turned<2> lanes_along(int sheet, int l16, int g, int turn) {
+    return turned<2>(sheet, l16 * 128 + (((g ^ l16 ^ l16 / 8 * 2) & 7) << 4), turn, 64);
 }
 // Row 8 g + l16 / 4, column 4 (l16 % 4); a turn for 16 columns, two turns where four rows further.
-template <typename T> __device__ __forceinline__ Turned<4> lanes_down(int sheet, int l16, int g, int turn) {
-    return turned<T, 4>(sheet, (8 * g + l16 / 4) * 128 + ((l16 % 4 / 2 ^ l16 / 4 ^ 2 * g) << 4) + l16 % 2 * 8, turn, 32);
+__device__ __forceinline__ Turned<4> lanes_down(int sheet, int l16, int g, int turn) {
+    return turned<4>(sheet, (8 * g + l16 / 4) * 128 + ((l16 % 4 / 2 ^ l16 / 4 ^ 2 * g) << 4) + l16 % 2 * 8, turn, 32);
 }
 // Row l16, column 4 g; a turn for 16 columns, two for 32 columns or 16 rows.
-template <typename T> __device__ __forceinline__ Turned<4> lanes_put(int sheet, int l16, int g, int turn) {
-    return turned<T, 4>(sheet, l16 * 128 + (((g / 2 ^ l16 ^ l16 / 8 * 2) & 7) << 4) + g % 2 * 8, turn, 32);
+__device__ __forceinline__ Turned<4> lanes_put(int sheet, int l16, int g, int turn) {
+    return turned<4>(sheet, l16 * 128 + (((g / 2 ^ l16 ^ l16 / 8 * 2) & 7) << 4) + g % 2 * 8, turn, 32);
 }
 
-template <typename T, int ROWS, int COLS>
+template <typename T, int ROWS, int COLS, int PLANES = kCopies<T>>
 struct Sheet {
-    static constexpr int kPane = ROWS * 128, kPlane = COLS / 64 * kPane, kBytes = kPlane * kCopies<T>;
+    static constexpr int kPane = ROWS * 128, kPlane = COLS / 64 * kPane, kBytes = kPlane * PLANES;
+    typedef std::conditional_t<PLANES == 1, bf16x8, Terms<PLANES>> Fragment;
     __device__ __forceinline__ static int bits(int row) { return (row ^ (row >> 3) << 1) & 7; }
     // Byte offset of column c of a row; eight neighbours stay together.
     __device__ __forceinline__ static int at(int row, int c) {
@@ -66,10 +61,10 @@ struct Sheet {
     // Four neighbours.
     __device__ __forceinline__ static void put4(char *to, f32x4 v) {
 #pragma unroll
-        for (int k = 0; k < kCopies<T>; ++k) {
+        for (int k = 0; k < PLANES; ++k) {
             u16x4 t;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) t[e] = f32_to_bf16_bits(v[e]);
+            for (int e = 0; e < 4; ++e) t[e] = f32_to_bf16_bits(Elem<T>::is_bf16 && PLANES > 1 && k == 0 ? first_term(v[e]) : v[e]);
             *(u16x4 *)(to + k * kPlane) = t;
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] -= bf16_bits_to_f32(t[e]);
@@ -82,25 +77,25 @@ struct Sheet {
     }
     // A fragment: index over the rows 16 t .., contraction over the columns 32 r ..; at: lanes_along of the sheet
     // (or of its rows from a t on, turned by t % 2, and then t counts from there).
-    __device__ __forceinline__ static Operand<T> along(const char *lds, const Turned<2> &at, int t, int r) {
+    __device__ __forceinline__ static Fragment along(const char *lds, const Turned<2> &at, int t, int r) {
         const char *from = lds + at.to[(r ^ t) & 1] + t * 2048 + r / 2 * kPane;
-        if constexpr (Elem<T>::is_bf16) {
+        if constexpr (PLANES == 1) {
             return *(const bf16x8 *)from;
         } else {
-            Split v;
+            Fragment v;
 #pragma unroll
-            for (int k = 0; k < kParts; ++k) v.part[k] = *(const bf16x8 *)(from + k * kPlane);
+            for (int k = 0; k < PLANES; ++k) v.part[k] = *(const bf16x8 *)(from + k * kPlane);
             return v;
         }
     }
     // Index over the columns 16 t .., contraction over the rows 32 r ..; at: lanes_down of the sheet (or of
     // its columns from a t on, turned by t % 4).
-    __device__ __forceinline__ static Operand<T> down(const char *lds, const Turned<4> &at, int t, int r) {
+    __device__ __forceinline__ static Fragment down(const char *lds, const Turned<4> &at, int t, int r) {
         typedef __attribute__((address_space(3))) s16x4 *lds_ptr;
         const char *first = lds + at.to[t] + r * 4096, *second = lds + at.to[t ^ 2] + 512 + r * 4096;
-        bf16x8 v[kCopies<T>];
+        bf16x8 v[PLANES];
 #pragma unroll
-        for (int k = 0; k < kCopies<T>; ++k) {
+        for (int k = 0; k < PLANES; ++k) {
             const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(first + k * kPlane));
             const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(second + k * kPlane));
             u16x8 u;
@@ -108,8 +103,9 @@ struct Sheet {
             for (int e = 0; e < 4; ++e) { u[e] = (uint16_t)a[e]; u[4 + e] = (uint16_t)b[e]; }
             v[k] = __builtin_bit_cast(bf16x8, u);
         }
-        if constexpr (Elem<T>::is_bf16) return v[0];
-        else return Split{{v[0], v[1], v[2]}};
+        if constexpr (PLANES == 1) return v[0];
+        else if constexpr (PLANES == 2) return Fragment{{v[0], v[1]}};
+        else return Fragment{{v[0], v[1], v[2]}};
     }
 };
 
@@ -117,20 +113,20 @@ template <typename T> struct Small {
     static constexpr int kRows = Elem<T>::is_bf16 ? 64 : 32, kXs = Elem<T>::is_bf16 ? 2 : 1;  // x: being read, being put
     typedef Sheet<T, kWidth, kCols> W;
     typedef Sheet<T, kRows, kCols> X;
-    typedef Sheet<T, kRows, kWidth> Z;
+    typedef Sheet<T, kRows, kWidth, kTermsOfZ<T>> Z;
     static constexpr int kLds = W::kBytes + kXs * X::kBytes + Z::kBytes;
     static constexpr int kPer = kVec<T>, kXChunks = kRows * kCols / kPer / kThreads, kWChunks = kWidth * kCols / kPer / kThreads;
     static constexpr int kM = kRows / 16, kOwn = 4 * kM / 8;  // sixteens of rows; of a wave's in grad_x
 };
 static_assert(Small<float>::kLds <= 160 * 1024, "one compute unit's LDS");
-static_assert(2 * Small<bf16_t>::kLds <= 160 * 1024, "two workgroups in it");
+static_assert(Small<bf16_t>::kLds <= 160 * 1024, "one compute unit's LDS");
 
 // Row of W that is row n of its sheet: gated, 16 of the gate's, the same 16 of the other half, and so on.
 template <bool GATED>
 __device__ __forceinline__ int column_of(int n) { return GATED ? (n >> 5 << 4) + (n & 15) : n; }
 
 template <typename T, bool GATED>
-__global__ __launch_bounds__(kThreads, Elem<T>::is_bf16 ? 4 : 2) void small_backward_kernel(const SmallBackward a) {
+__global__ __launch_bounds__(kThreads, 2) void small_backward_kernel(const SmallBackward a) {
     typedef Small<T> S;
     extern __shared__ __attribute__((aligned(16))) char lds[];
     constexpr int w = 0, x = S::W::kBytes, dz = x + S::kXs * S::X::kBytes;  // where in LDS
@@ -153,7 +149,7 @@ __global__ __launch_bounds__(kThreads, Elem<T>::is_bf16 ? 4 : 2) void small_back
     const auto fetch = [&](int64_t tile) {
 #pragma unroll
         for (int i = 0; i < S::kXChunks; ++i) {
-            const int c = anew<T>(col_of(i));
+            const int c = col_of(i);
             const int64_t m = tile * kRows + row_of(i);
             const bool on = m < a.rows && c < C;
             xn[i] = load_vec<T>((const T *)a.x + (on ? m * a.x_ld + c : 0), on ? C - c : 0);
@@ -192,8 +188,8 @@ __global__ __launch_bounds__(kThreads, Elem<T>::is_bf16 ? 4 : 2) void small_back
             }
             return gr;
         };
-        // float32 has registers to ask for it before z is made (262144 rows of 64 to 2 128: 202 us, so 184);
-        // bfloat16 would spill (80 us, so 115).
+        // Before z is made in float32 (262144 rows of 64 to 2 128: 202 us, so 184); bfloat16 gains nothing (103 us,
+        // so 104; of 64 to 256 145 and 154).
         constexpr bool kAhead = !Elem<T>::is_bf16;
         f32x4 ahead[2][kAhead ? kM : 1];
         if constexpr (kAhead) {
@@ -207,7 +203,7 @@ __global__ __launch_bounds__(kThreads, Elem<T>::is_bf16 ? 4 : 2) void small_back
         }
         // z: 32 columns of the wave's by 64 rows
         f32x4 z[2][kM];
-        const Turned<2> at_x = lanes_along<T>(xt, l16, g, 0), at_w = lanes_along<T>(w + wave * 4096, l16, g, 0);
+        const Turned<2> at_x = lanes_along(xt, l16, g, 0), at_w = lanes_along(w + wave * 4096, l16, g, 0);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -220,20 +216,20 @@ __global__ __launch_bounds__(kThreads, Elem<T>::is_bf16 ? 4 : 2) void small_back
 #pragma unroll
             for (int h = 0; h < 2; ++h) multiply<kM>(z[h], S::W::along(lds, at_w, h, r), q);
         }
-        // dz, rounded to the type.  The wave's two sixteens of z's columns, in the sheet's order, are a gate's
+        // dz, in bfloat16 as two terms (one would make the gradients' error 1.4 times that of their own rounding).
+        // The wave's two sixteens of z's columns, in the sheet's order, are a gate's
         // and its other half's, or neighbours; a lane has four of each.
-        const Turned<4> at_put = lanes_put<T>(dz + wave / 2 * S::Z::kPane, l16, g, wave % 2 * 2);
-        const int lf = anew<T>(l16), gf = anew<T>(g);
+        const Turned<4> at_put = lanes_put(dz + wave / 2 * S::Z::kPane, l16, g, wave % 2 * 2);
         int f[2];
         f32x4 bias[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            f[h] = column_of<GATED>(32 * wave + 16 * h) + 4 * gf;
+            f[h] = column_of<GATED>(32 * wave + 16 * h) + 4 * g;
             bias[h] = load4(a.bias + (f[h] < N ? (GATED && h ? N : 0) + f[h] : 0), f[h] < N ? N - f[h] : 0);
         }
 #pragma unroll
         for (int j = 0; j < kM; ++j) {
-            const int m = 16 * j + lf;
+            const int m = 16 * j + l16;
             f32x4 d[2];
 #pragma unroll
             for (int h = 0; h < (GATED ? 1 : 2); ++h) {
@@ -258,30 +254,30 @@ __global__ __launch_bounds__(kThreads, Elem<T>::is_bf16 ? 4 : 2) void small_back
         if (a.grad_x != nullptr) {
             f32x4 gx[kOwn];
             const int t = wave % 4, j0 = wave / 4 * kOwn;
-            const Turned<2> at_z = lanes_along<T>(dz + j0 * 2048, l16, g, j0 % 2);
-            const Turned<4> at_wd = lanes_down<T>(w, l16, g, t);
+            const Turned<2> at_z = lanes_along(dz + j0 * 2048, l16, g, j0 % 2);
+            const Turned<4> at_wd = lanes_down(w, l16, g, t);
 #pragma unroll
             for (int j = 0; j < kOwn; ++j) gx[j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int r = 0; r < kWidth / 32; ++r) {
-                Operand<T> q[kOwn];
+                typename S::Z::Fragment q[kOwn];
 #pragma unroll
                 for (int j = 0; j < kOwn; ++j) q[j] = S::Z::along(lds, at_z, j, r);
                 multiply<kOwn>(gx, S::W::down(lds, at_wd, 0, r), q);
             }
-            const int lf = anew<T>(l16), c = 16 * t + 4 * anew<T>(g);
+            const int c = 16 * t + 4 * g;
 #pragma unroll
             for (int j = 0; j < kOwn; ++j) {
-                const int m = 16 * (j0 + j) + lf;
+                const int m = 16 * (j0 + j) + l16;
                 if (m < left && c < C) store4<T>((T *)a.grad_x + (m0 + m) * C + c, gx[j], C - c);
             }
         }
         // grad_W: all columns of C by the wave's 32 of z
         if (a.part != nullptr) {
-            const Turned<4> at_z = lanes_down<T>(dz + wave / 2 * S::Z::kPane, l16, g, wave % 2 * 2), at_xd = lanes_down<T>(xt, l16, g, 0);
+            const Turned<4> at_z = lanes_down(dz + wave / 2 * S::Z::kPane, l16, g, wave % 2 * 2), at_xd = lanes_down(xt, l16, g, 0);
 #pragma unroll
             for (int r = 0; r < kRows / 32; ++r) {
-                const Operand<T> q[2] = {S::Z::down(lds, at_z, 0, r), S::Z::down(lds, at_z, 1, r)};
+                const typename S::Z::Fragment q[2] = {S::Z::down(lds, at_z, 0, r), S::Z::down(lds, at_z, 1, r)};
                 add_up<2>(sum, q);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) multiply<2>(gw[i], S::X::down(lds, at_xd, i, r), q);
@@ -310,7 +306,7 @@ __global__ __launch_bounds__(kThreads, Elem<T>::is_bf16 ? 4 : 2) void small_back
 
 // Workgroups: as many as fit the chip, each with rows to work on.
 int groups(int64_t rows, bool bf16) {
-    const int64_t tiles = bf16 ? (rows + 63) / 64 : (rows + 31) / 32, fit = bf16 ? 512 : 256;
+    const int64_t tiles = bf16 ? (rows + 63) / 64 : (rows + 31) / 32, fit = 256;
     return (int)(tiles < fit ? tiles : fit);
 }
 

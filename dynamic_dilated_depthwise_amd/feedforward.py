@@ -17,9 +17,9 @@ Layouts (float32 or bfloat16): x [..., C], y, residual and grad [..., N]; weight
 contiguous or have two axes with contiguous rows; weight and bias are contiguous.  Every size is at
 least one.  activation is "none", "relu", "silu" or "gelu" (z times the normal distribution at z).
 
-Sums are float32; outputs are rounded once.  Where an activation or a gate lies between, its
-input's gradient is rounded to the type before the two products of the backward take it; that
-input itself is not: the forward keeps it in float32, or the backward makes it again.
+Sums are float32; outputs are rounded once, and nothing on the way.  Where an activation or a gate
+lies between, its input is kept in float32 by the forward, or made again by the backward, and the
+gradient of it enters the backward's two products in float32 or as two bfloat16 terms.
 
 Streams, captured graphs and training steps in them are as in ``sequence``.
 """

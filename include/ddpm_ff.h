@@ -17,8 +17,8 @@
  * Precision.  Products are summed in float32; float32 operands enter the matrix instructions as
  *   three bfloat16 terms each, six products of them, which is float32's own precision.  Bias,
  *   activation and residual are applied to that sum, and outputs are rounded once.  In the
- *   backward of an activation or a gate the gradient of its input is rounded to the call's dtype
- *   before the two products take it.
+ *   backward of an activation or a gate the gradient of its input enters the two products in
+ *   float32 or as two bfloat16 terms.
  * Not finite.  An infinity or NaN in a row of x or grad reaches that row of y or grad_x, and the
  *   parameters' gradients, and no other row; in float32 an infinity (or a value above 3.39e38, the
  *   largest bfloat16) in an operand of a product gives NaN.
