@@ -40,8 +40,6 @@ enum Epi { kStore, kLinear, kGated, kWeight };
 constexpr int kStepBytes = 128;
 template <typename T> constexpr int kStep = kStepBytes / (int)sizeof(T);  // elements of a step
 
-constexpr float kMostBf16 = 3.38953139e38f;  // the largest bfloat16
-
 constexpr uint32_t kRecords = 0x7fffffe0u, kOutside = 0x7ffffff0u;  // of a buffer; an offset past it
 
 // All but this wave's last N loads to LDS are there and its own LDS accesses done; then the workgroup.
@@ -150,6 +148,11 @@ struct Tile {
     }
 };
 
+// The bfloat16 next to a number: the largest for those above it, so that what it leaves of them is finite.
+constexpr float kMostBf16 = 3.38953139e38f;
+__device__ __forceinline__ float within_bf16(float v) { return __builtin_amdgcn_fmed3f(v, -kMostBf16, kMostBf16); }
+__device__ __forceinline__ float first_term(float v) { return round_to_bf16(within_bf16(v)); }
+
 // A float32 as three bfloat16 (8 + 8 + 8 bits, the float32 itself down to the subnormals).  Of the nine
 // products of two such numbers the six above 2^-25 of the whole are taken, so that a float32 product
 // costs six bfloat16 matrix instructions (96 cycles where the float32 ones take 256) at float32's
@@ -165,7 +168,7 @@ template <typename T> struct OperandOf { typedef Split type; };
 template <> struct OperandOf<bf16_t> { typedef bf16x8 type; };
 template <typename T> using Operand = typename OperandOf<T>::type;
 
-// In pairs, as the conversion takes them: 11 instructions for two values.
+// In pairs, as the conversion takes them: 13 instructions for two values.
 __device__ __forceinline__ Split split_of(const f32x4 &a, const f32x4 &b) {
     typedef float f32x2 __attribute__((ext_vector_type(2)));
     u32x4 part[kParts];
@@ -174,7 +177,8 @@ __device__ __forceinline__ Split split_of(const f32x4 &a, const f32x4 &b) {
         f32x2 v = e < 2 ? f32x2{a[2 * e], a[2 * e + 1]} : f32x2{b[2 * e - 4], b[2 * e - 3]};
 #pragma unroll
         for (int k = 0; k < kParts; ++k) {
-            const uint32_t t = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
+            const f32x2 c = k == 0 ? f32x2{within_bf16(v[0]), within_bf16(v[1])} : v;
+            const uint32_t t = __builtin_bit_cast(uint32_t, __builtin_convertvector(c, bf16x2_t));
             part[k][e] = t;
             v[0] -= __uint_as_float(t << 16);
             v[1] -= __uint_as_float(t & 0xffff0000u);
@@ -324,8 +328,6 @@ __device__ __forceinline__ void bias8(const Product &a, int64_t p, int half, flo
 __device__ __forceinline__ void keep8(const Product &a, int64_t p, int half, const float (&v)[8]) {
     if (a.kept != nullptr && a.grad == nullptr && p < a.np) write8<float>(a.kept + half * a.np + p, a.np - p, v);
 }
-// The value next to v that bfloat16 has; finite, so that what it leaves of v is its distance from v and not NaN.
-__device__ __forceinline__ float first_term(float v) { return round_to_bf16(__builtin_amdgcn_fmed3f(v, -kMostBf16, kMostBf16)); }
 // dz: rounded to bfloat16 alone it would make the gradients' error 1.4 times that of their own rounding, so
 // that what the rounding leaves is kept beside it, `low` elements behind (0: the values are bfloat16's, or
 // T is float32).  An infinity is the largest number and an infinity.
@@ -499,7 +501,7 @@ struct Gemm {
             // The splits' vector instructions between the products: left in runs, they and the matrix
             // instructions do not overlap (39 % and 57 % of the cycles; 4096^3 597 -> 577 us).
             if constexpr (!Elem<T>::is_bf16) {
-                constexpr int kProducts = 6 * MP * NQ, kVector = 44 * (MP + NQ) / kProducts + 1;
+                constexpr int kProducts = 6 * MP * NQ, kVector = 52 * (MP + NQ) / kProducts + 1;
 #pragma unroll
                 for (int n = 0; n < kProducts; ++n) {
                     __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);

@@ -64,7 +64,7 @@ struct Sheet {
         for (int k = 0; k < PLANES; ++k) {
             u16x4 t;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) t[e] = f32_to_bf16_bits(Elem<T>::is_bf16 && PLANES > 1 && k == 0 ? first_term(v[e]) : v[e]);
+            for (int e = 0; e < 4; ++e) t[e] = f32_to_bf16_bits(PLANES > 1 && k == 0 ? within_bf16(v[e]) : v[e]);
             *(u16x4 *)(to + k * kPlane) = t;
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] -= bf16_bits_to_f32(t[e]);

@@ -21,6 +21,9 @@ Sums are float32; outputs are rounded once, and nothing on the way.  Where an ac
 lies between, its input is kept in float32 by the forward, or made again by the backward, and the
 gradient of it enters the backward's two products in float32 or as two bfloat16 terms.
 
+An infinity or NaN in a row of x or grad reaches that row of y or of grad_x and the parameters'
+gradients, and no other row.  In float32 a sum that is infinite may come out as NaN.
+
 Streams, captured graphs and training steps in them are as in ``sequence``.
 """
 import os

@@ -15,13 +15,16 @@
  *   by memset, so every call may be captured into a graph.  No atomics are used: equal inputs
  *   at equally aligned addresses give equal bits.
  * Precision.  Products are summed in float32; float32 operands enter the matrix instructions as
- *   three bfloat16 terms each, six products of them, which is float32's own precision.  Bias,
+ *   three bfloat16 terms each, six products of them, which is float32's own precision (operands
+ *   below 2^-110 lose bits of the third term, at 2^-126 all but eight); up to 64 rows of a forward
+ *   whose rows are no whole 16-byte chunks may be multiplied in float32 itself.  Bias,
  *   activation and residual are applied to that sum, and outputs are rounded once.  In the
  *   backward of an activation or a gate the gradient of its input enters the two products in
  *   float32 or as two bfloat16 terms.
  * Not finite.  An infinity or NaN in a row of x or grad reaches that row of y or grad_x, and the
- *   parameters' gradients, and no other row; in float32 an infinity (or a value above 3.39e38, the
- *   largest bfloat16) in an operand of a product gives NaN.
+ *   parameters' gradients, and no other row.  In float32 an infinity in an operand of a product may
+ *   give NaN where the sum is infinite; finite operands give what float32 holds of their sum, up to
+ *   the largest of them (a sum that leaves float32's range gives an infinity or NaN).
  * Errors.  As in ddpm.h; all arguments are checked before anything is enqueued.
  *     DDPM_ERR_INVALID_ARG  null or misaligned pointers, sizes below 1 or beyond 2^31 - 2^16,
  *                           negative strides, an unknown dtype or activation, overlapping
