@@ -6,16 +6,12 @@
 
 #include "abi_check.hpp"
 #include "ff_launch.hpp"
+#include "ff_plan.hpp"
 
 namespace {
 
 using namespace ddpm::abi;
 using namespace ddpm::ff;
-
-// Sizes of a call: x [rows, C], y [rows, N], `width` = N or 2 N columns of z.
-struct Sizes {
-    int64_t rows, C, N, width;
-};
 
 bool sizes_ok(Check &c, const Sizes &s, int activation) {
     for (int64_t v : {s.rows, s.C, s.N}) c.size(v, kMaxRun);
@@ -24,54 +20,6 @@ bool sizes_ok(Check &c, const Sizes &s, int activation) {
            (double)s.width * s.C <= kMostElements;
 }
 
-int64_t rounded(int64_t bytes) { return (bytes + 255) / 256 * 256; }
-int64_t element(bool bf16) { return bf16 ? 2 : 4; }
-int64_t chunk(bool bf16) { return 16 / element(bf16); }
-
-// What the forward saves for an activation's or a gate's backward: z in float32, or, with few columns of
-// x and more of z than the caches hold, its bias alone, and the backward makes z again (training 16384
-// rows to 2 2048 columns, bfloat16, microseconds with z saved and made again: C = 256 323, 227; 768
-// 472, 419; 1536 750, 780; one half with gelu: 512 220, 213; 768 266, 275; 65536 rows to 2 128 in
-// float32: 64 114, 105; 128 143, 143.  Where z stays in the caches both are the same up to C = 256 and
-// saving is faster beyond).
-// Backwards of few channels (ff_small.hip) always make it again, on the chip.
-bool makes_again(const Sizes &s, bool bf16) {
-    if (small_backward(s.C, s.width)) return true;
-    const int64_t most = !bf16 ? 96 : s.width == s.N ? 512 : 768;
-    return s.C <= most && (double)s.rows * s.width >= 12e6;
-}
-int64_t saved_floats(const Sizes &s, bool through, bool bf16) { return !through ? 0 : makes_again(s, bf16) ? s.width : s.rows * s.width; }
-
-// x and weight, whose rows of C elements are no whole chunks, as copies with rows that are, where those
-// cost less than the products' form for any alignment.
-int64_t x_copy_bytes(const Sizes &s, bool bf16) { return rounded(s.rows * padded(s.C, bf16) * element(bf16)); }
-int64_t weight_copy_bytes(const Sizes &s, bool bf16) { return rounded(s.width * padded(s.C, bf16) * element(bf16)); }
-double forward_time(Kind kind, const Sizes &s, bool bf16, bool straight) {
-    return product_time(kind, s.N, s.rows, s.C, 1, bf16, straight);
-}
-// The same of few rows: nanoseconds of an element of the contraction, as measured with 1 to 64 rows and C from
-// 256 to 5632 (with copies at hand at least the weight's way).  Rows of odd length, straight and by copies,
-// microseconds: bfloat16 64 rows of 5633 to 128 85, 13, 24 of 4097 to 4096 35, 25, one 17, 23; float32 64 of
-// 5633 to 128 51, 26, of 4097 to 4096 39, 60.
-double rows_time(Kind kind, const Sizes &s, bool bf16, bool straight) {
-    const double halves = kind == kGatedForward ? 2. : 1., k = s.C * 1e-3, weight = (double)weight_copy_bytes(s, bf16) / 5e6;
-    if (straight) return 4. + std::max(k * (bf16 ? 0.2 * halves + 0.013 * s.rows : 1.5 * halves + 0.04 * s.rows), weight);
-    return 4. + k * (bf16 ? 3. * halves + 0.18 * s.rows : 2. * halves + 0.1 * s.rows) * std::max(1., s.N / 8192.);
-}
-bool forward_copies(Kind kind, const Sizes &s, bool bf16) {
-    if (s.C % chunk(bf16) == 0) return false;
-    const double copies = copies_time(x_copy_bytes(s, bf16) + weight_copy_bytes(s, bf16));
-    if (s.rows <= kMostRows) return copies + rows_time(kind, s, bf16, true) < rows_time(kind, s, bf16, false);
-    return forward_time(kind, s, bf16, true) + copies < forward_time(kind, s, bf16, false);
-}
-bool backward_copies(Kind kind, const Sizes &s, bool again, int terms, bool bf16) {
-    if (s.C % chunk(bf16) == 0) return false;
-    const auto all = [&](bool straight) {
-        return product_time(kGradX, s.C, s.rows, s.width, terms, bf16, straight) +
-               product_time(kGradWeight, s.C, s.width, s.rows, terms, bf16, straight) + (again ? forward_time(kind, s, bf16, straight) : 0.);
-    };
-    return all(true) + copies_time(x_copy_bytes(s, bf16) + weight_copy_bytes(s, bf16)) < all(false);
-}
 // Copies x and weight to `work` and points the product at them.
 hipError_t copy_operands(const Sizes &s, const void *&x, int64_t &x_row, const void *&weight, int64_t &weight_row, char *&work,
                          bool bf16, hipStream_t stream) {
@@ -139,38 +87,6 @@ int forward(Kind kind, const void *x, const void *weight, const void *bias, cons
     a.residual_ld = residual_row;
     a.act = activation;
     return status_of(launch_product(kind, a, work, bf16, stream));
-}
-
-// What the backward has in its workspace: dz, where it is another tensor than grad (behind an activation
-// or a gate, and where grad's rows are no whole chunks and many enough), copies, the products' pieces.
-struct Room {
-    bool small, own_dz, copies, again;
-    int64_t dz, low, all;  // dz's bytes, elements to its second term (or 0), all bytes
-};
-// Whether dz has more bits than the type: behind relu alone it is grad or zero.
-bool two_terms(Kind kind, bool through, int activation, bool bf16) {
-    return through && bf16 && (kind == kGatedForward || activation != DDPM_ACT_RELU);
-}
-constexpr double kManyFlops = 5e9;  // of one product: from here on a copy of grad costs less than what it saves
-Room backward_room(Kind kind, const Sizes &s, bool through, int activation, bool bf16) {
-    Room r = {};
-    r.small = through && small_backward(s.C, s.width);
-    if (r.small) {
-        r.all = small_bytes(s.rows, s.C, s.width, bf16);
-        return r;
-    }
-    r.own_dz = through || (s.N % chunk(bf16) != 0 && 2. * s.rows * s.N * s.C >= kManyFlops);
-    r.again = through && makes_again(s, bf16);
-    const int terms = two_terms(kind, through, activation, bf16) ? 2 : 1;
-    const int64_t dz = s.rows * padded(s.width, bf16);
-    r.copies = backward_copies(kind, s, r.again, terms, bf16);
-    r.dz = r.own_dz ? rounded(terms * dz * element(bf16)) : 0;
-    r.low = terms == 2 ? dz : 0;
-    int64_t part = std::max(product_bytes(kGradX, s.C, s.rows, s.width, terms, bf16),
-                            product_bytes(kGradWeight, s.C, s.width, s.rows, terms, bf16));
-    if (r.again) part = std::max(part, product_bytes(kind, s.N, s.rows, s.C, 1, bf16));
-    r.all = r.dz + (r.copies ? x_copy_bytes(s, bf16) + weight_copy_bytes(s, bf16) : 0) + part;
-    return r;
 }
 
 int64_t backward_workspace(Kind kind, const Sizes &s, bool through, int activation, int dtype) {

@@ -643,10 +643,9 @@ struct Gemm {
     static constexpr int kFinishThreads = 256, kReds = E == kGated ? 17 : 9;
     static constexpr int kPerTile = (E == kGated ? kP / 2 : kP) * kQ / 8;
     static_assert(kPerTile % kFinishThreads == 0, "a workgroup stays in one tile");
-    __host__ __device__ static int lanes(int pieces) { return pieces >= 64 ? 32 : pieces >= 16 ? 8 : pieces >= 4 ? 2 : 1; }
     __device__ static void finish(const Product &a, float (*red)[kReds]) {
         constexpr int kCols = (E == kGated ? kP / 2 : kP) / 8;
-        const int kLanes = lanes(a.pieces), items = kFinishThreads / kLanes;
+        const int kLanes = finish_lanes(a.pieces), items = kFinishThreads / kLanes;
         const uint32_t cut = a.tiles_p * a.tiles_q - a.whole, blocks = kPerTile / items, tile = blockIdx.x / blocks;
         const int item = threadIdx.x % items, lane = threadIdx.x / items;
         const int i = (int)(blockIdx.x - tile * blocks) * items + item, row = i / kCols, c = i % kCols;

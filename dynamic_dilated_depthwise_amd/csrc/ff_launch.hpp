@@ -5,7 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "../../include/ddpm_ff.h"
+#include "ff_plan.hpp"
 
 namespace ddpm {
 namespace ff {
@@ -36,19 +36,10 @@ struct Product {
     float *part;
 };
 
-enum Kind { kForward, kGatedForward, kGradX, kGradWeight };
-
-// Bytes that launch_product needs at `work` (for these sizes, any strides and alignment); terms: of Q, one or two.
-int64_t product_bytes(Kind kind, int64_t np, int64_t nq, int64_t nk, int terms, bool bf16);
 hipError_t launch_product(Kind kind, const Product &a, void *work, bool bf16, hipStream_t stream);
-// Microseconds of a product, straight to LDS or not, as far as its cut foresees.
-double product_time(Kind kind, int64_t np, int64_t nq, int64_t nk, int terms, bool bf16, bool straight);
-// Those of copies (below) of so many bytes.
-double copies_time(int64_t bytes);
 
-// Rows of whole 128-byte lines, their last 16-byte chunk filled up with zeros: copies of an operand
-// whose rows would otherwise start anywhere.
-__host__ __device__ inline int64_t padded(int64_t cols, bool bf16) { return (cols + (bf16 ? 63 : 31)) / (bf16 ? 64 : 32) * (bf16 ? 64 : 32); }
+// A copy of an operand whose rows would otherwise start anywhere: rows of whole lines (padded), their last 16-byte chunk
+// filled up with zeros.
 struct Copy {
     const void *src;
     int64_t ld, rows, cols;
@@ -57,9 +48,7 @@ struct Copy {
 // One or two copies; the second may have no rows.
 hipError_t launch_copies(const Copy &a, const Copy &b, bool bf16, hipStream_t stream);
 
-// The forward products of few rows (ff_rows.hip): up to kMostRows, from operands that can go straight to LDS
-// (chunked; where few_rows says so) or from any.
-constexpr int64_t kMostRows = 64;
+// The forward products of few rows (ff_rows.hip), from operands that can go straight to LDS (chunked) or from any.
 hipError_t launch_rows(bool gated, bool chunked, const Product &a, bool bf16, hipStream_t stream);
 
 // dz = grad * act'(saved), [rows, N]; gated: saved [rows, 2 N] and dz [rows, 2 N],
@@ -70,7 +59,7 @@ hipError_t launch_dz(bool gated, const void *grad, int64_t grad_ld, const float 
                      int64_t N, int act, bool bf16, hipStream_t stream);
 
 // The whole backward through an activation or a gate of few channels, which makes z again
-// (ff_small.hip): whether these sizes are, the bytes of its partials, and the call.
+// (ff_small.hip).
 struct SmallBackward {
     const void *grad, *x, *weight;
     const float *bias;                  // [N], gated [2 N]
@@ -79,8 +68,6 @@ struct SmallBackward {
     void *grad_x;                       // [rows, C] or null
     float *part;                        // of grad_weight and grad_bias, or null with them
 };
-bool small_backward(int64_t C, int64_t width);
-int64_t small_bytes(int64_t rows, int64_t C, int64_t width, bool bf16);
 hipError_t launch_small_backward(bool gated, SmallBackward a, void *grad_weight, void *grad_bias, bool bf16, hipStream_t stream);
 
 }  // namespace ff

@@ -22,7 +22,7 @@ namespace ff {
 
 namespace {
 
-constexpr int kCols = 64, kWidth = 256, kThreads = 512;
+constexpr int kCols = kSmallCols, kWidth = kSmallWidth, kThreads = 512;
 template <typename T> constexpr int kCopies = Elem<T>::is_bf16 ? 1 : kParts;  // planes of a sheet
 template <typename T> constexpr int kTermsOfZ = Elem<T>::is_bf16 ? 2 : kParts;      // of dz's
 
@@ -110,7 +110,7 @@ struct Sheet {
 };
 
 template <typename T> struct Small {
-    static constexpr int kRows = Elem<T>::is_bf16 ? 64 : 32, kXs = Elem<T>::is_bf16 ? 2 : 1;  // x: being read, being put
+    static constexpr int kRows = small_rows(Elem<T>::is_bf16), kXs = Elem<T>::is_bf16 ? 2 : 1;  // x: being read, being put
     typedef Sheet<T, kWidth, kCols> W;
     typedef Sheet<T, kRows, kCols> X;
     typedef Sheet<T, kRows, kWidth, kTermsOfZ<T>> Z;
@@ -304,33 +304,23 @@ __global__ __launch_bounds__(kThreads, 2) void small_backward_kernel(const Small
     }
 }
 
-// Workgroups: as many as fit the chip, each with rows to work on.
-int groups(int64_t rows, bool bf16) {
-    const int64_t tiles = bf16 ? (rows + 63) / 64 : (rows + 31) / 32, fit = 256;
-    return (int)(tiles < fit ? tiles : fit);
-}
-
 template <typename T, bool GATED>
 hipError_t run(SmallBackward a, hipStream_t stream) {
     const auto kernel = small_backward_kernel<T, GATED>;
     const hipError_t e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, Small<T>::kLds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, dim3(groups(a.rows, Elem<T>::is_bf16)), dim3(kThreads), Small<T>::kLds, stream, a);
+    hipLaunchKernelGGL(kernel, dim3(small_groups(a.rows, Elem<T>::is_bf16)), dim3(kThreads), Small<T>::kLds, stream, a);
     return hipGetLastError();
 }
 
 }  // namespace
-
-bool small_backward(int64_t C, int64_t width) { return C <= kCols && width <= kWidth; }
-
-int64_t small_bytes(int64_t rows, int64_t C, int64_t width, bool bf16) { return groups(rows, bf16) * (width * C + width) * 4; }
 
 hipError_t launch_small_backward(bool gated, SmallBackward a, void *grad_weight, void *grad_bias, bool bf16, hipStream_t stream) {
     const hipError_t e = bf16 ? gated ? run<bf16_t, true>(a, stream) : run<bf16_t, false>(a, stream)
                               : gated ? run<float, true>(a, stream) : run<float, false>(a, stream);
     if (e != hipSuccess || a.part == nullptr) return e;
     const int64_t width = gated ? 2 * a.N : a.N;
-    return seq::launch_sum_rows(a.part, groups(a.rows, bf16), width * a.C, width, grad_weight, grad_bias, bf16, stream);
+    return seq::launch_sum_rows(a.part, small_groups(a.rows, bf16), width * a.C, width, grad_weight, grad_bias, bf16, stream);
 }
 
 }  // namespace ff
