@@ -76,8 +76,10 @@ def _rows(t):
 class _Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, residual, activation):
-        y, saved = linear_fwd(x, weight, bias, residual, activation, save=True)
-        ctx.save_for_backward(x, weight, saved)
+        product = any(ctx.needs_input_grad[:3])  # the residual's gradient needs nothing
+        y, saved = linear_fwd(x, weight, bias, residual, activation, save=product)
+        if product:
+            ctx.save_for_backward(x, weight, saved)
         ctx.activation = activation
         return y
 
