@@ -55,8 +55,9 @@ __device__ __forceinline__ void wave_order() { asm volatile("" ::: "memory"); }
 // 16 bytes a lane from `off` behind `p` (uniform; zeros from kRecords on) to LDS at `at` (uniform) + 16 lane.
 // In assembly, because the compiler takes the builtin for a write to all of LDS and makes the fragment
 // reads behind it wait for it (grad_x 930 -> 570 TFLOP/s with loads between them).  It has no result, so
-// no register is held by a load in flight; arrive_but waits for it.  The compiler keeps nothing in m0; a
-// change of it needs one wait state.
+// no register is held by a load in flight; arrive_but waits for it.  m0 is one of the
+// registers that the compiler holds nothing in (it refuses them in a list of clobbered ones); a change of it
+// needs one wait state.
 __device__ __forceinline__ void load_to_lds(const void *p, uint32_t off, char *at) {
     const uint64_t a = (uint64_t)p;
     const u32x4 r = {(uint32_t)a, (uint32_t)(a >> 32) & 0xffffu, kRecords, 0x00020000u};
@@ -426,7 +427,6 @@ __device__ __forceinline__ void finish_gated(const Product &a, int64_t q, int64_
 // WP * WQ waves of 16 MP by 16 NQ each.
 template <typename T, Side SP, Side SQ, Epi E, int WP, int WQ, int MP, int NQ, int STAGES, bool DIRECT>
 struct Gemm {
-    static constexpr Epi kE = E;
     static constexpr int kThreads = WP * WQ * kWave, kP = WP * MP * 16, kQ = WQ * NQ * 16;
     static constexpr int kStageBytes = (kP + kQ) * kStepBytes;
     static constexpr int kLd = 16 * MP + 4;  // floats of a row of the result in LDS
