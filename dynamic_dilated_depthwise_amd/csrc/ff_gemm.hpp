@@ -499,7 +499,8 @@ struct Gemm {
                 }
             }
             // The splits' vector instructions between the products: left in runs, they and the matrix
-            // instructions do not overlap (39 % and 57 % of the cycles; 4096^3 597 -> 577 us).
+            // instructions do not overlap (39 % and 57 % of the cycles; 4096^3 597 -> 577 us,
+            // 602 since the splits hold operands to bfloat16's range).
             if constexpr (!Elem<T>::is_bf16) {
                 constexpr int kProducts = 6 * MP * NQ, kVector = 52 * (MP + NQ) / kProducts + 1;
 #pragma unroll

@@ -43,7 +43,8 @@ constexpr Form form_of(bool bf16, Kind kind, int k) {
                             {4, 1, 2, 2, 4, 2, 0, 0}};  // 128 x 32: few rows
     constexpr Form full[] = {{2, 4, 8, 4, 2, 1, 0, 0}, {2, 2, 4, 4, 2, 2, 0, 0}, {1, 4, 4, 4, 2, 2, 0, 0}, {4, 1, 2, 4, 3, 2, 0, 0},
                              {4, 1, 2, 2, 4, 2, 0, 0}};
-    // Of 256 tiles and of 512 (256 where one fits), the difference between 72 steps and 24.
+    // Of 256 tiles and of 512 (256 where one fits), the difference between 72 steps and 24 (float32's before its
+    // splits held operands to bfloat16's range, 4 % in every form).
     constexpr double times[2][3][5][2] = {{{{4.56, 4.56}, {1.32, 1.55}, {1.35, 1.59}, {0.81, 0.95}, {0.50, 0.62}},    // float32: y
                                            {{4.45, 4.45}, {1.32, 1.45}, {1.36, 1.68}, {0.81, 0.96}, {0.50, 0.65}},    // grad_x
                                            {{4.60, 4.60}, {1.31, 1.67}, {1.39, 1.70}, {0.86, 1.29}, {0.57, 0.85}}},   // grad_W
@@ -128,9 +129,10 @@ inline Cut cut_of(Kind kind, int64_t np, int64_t nq, int64_t nk, int terms, bool
 constexpr int64_t kMostRows = 64;  // of the kernels for few rows
 // Whether the forward takes a kernel of few rows (ff_rows.hip): for operands that cannot go straight to LDS
 // the one of any alignment, else the chunked one.  That reads all of x for each 16 columns of the result, so
-// it is for few of them, or for little of x.  Microseconds, chunked and tiles.  bfloat16: 48 rows of 5632 to
+// it is for few of them, or for little of x.  Microseconds, chunked and tiles (calls behind one another).  bfloat16: 48 rows of 5632 to
 // 2048 9.1, 15.1, of 512 to 8192 6.3, 5.4; 24 of 2048 to 5632 6.9, 11.1, to 32000 29.8, 20.7; one of 2048 to
-// 5632 5.3, 9, to 16384 15.0, 12.2.  float32, which is split at each read: 24 of 2048 to 5632 16.2, 19.3,
+// 5632 5.3, 9, to 16384 15.0, 12.2.  float32, which is split at each read (4 to 7 % more since the splits hold
+// operands to bfloat16's range): 24 of 2048 to 5632 16.2, 19.3,
 // of 16384 to 512 44.5, 28.1; 48 of 4096 to 4096 21.5, 27.1, of 5632 to 2048 23.4, 22.0; 64 of 1024 to 2304
 // 9.3, 12.2, of 2048 to 5632 29.5, 23.6.
 inline bool few_rows(Kind kind, int64_t np, int64_t nq, int64_t nk, bool bf16, bool direct) {
@@ -192,9 +194,9 @@ inline int64_t chunk(bool bf16) { return 16 / element(bf16); }
 
 // What the forward saves for an activation's or a gate's backward: z in float32, or, with few columns of
 // x and more of z than the caches hold, its bias alone, and the backward makes z again (training 16384
-// rows to 2 2048 columns, bfloat16, microseconds with z saved and made again: C = 256 323, 227; 768
-// 472, 419; 1536 750, 780; one half with gelu: 512 220, 213; 768 266, 275; 65536 rows to 2 128 in
-// float32: 64 114, 105; 128 143, 143.  Where z stays in the caches both are the same up to C = 256 and
+// rows to 2 2048 columns, bfloat16, microseconds with z saved and made again: C = 256 434, 396; 768
+// 685, 691; 1536 1064, 1144; one half with gelu: 512 315, 306; 768 369, 376; 65536 rows to 2 128 in
+// float32: 72 139, 133; 128 149, 150.  Where z stays in the caches both are the same up to C = 256 and
 // saving is faster beyond).
 // Backwards of few channels (ff_small.hip) always make it again, on the chip.
 inline bool makes_again(const Sizes &s, bool bf16) {

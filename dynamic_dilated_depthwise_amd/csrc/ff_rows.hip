@@ -3,9 +3,10 @@
 // waves take steps of the contraction in turn and their sums are joined in LDS, wave after wave.  No pieces
 // of results go through memory and no second kernel joins them, as the tiles' would.
 //
-//   chunked_rows_kernel  operands through LDS, whole chunks (one row of 2048 to 2 5632, bfloat16: 9.3 us, 46 MB,
-//                        5.0 TB/s; 48 of 5632 to 2048 9.1 us)
-//   rows_kernel          straight from memory into matrix operands, any alignment (12.6 us; 22 us)
+//   chunked_rows_kernel  operands through LDS, whole chunks (one row of 2048 to 2 5632, bfloat16: 8.7 us, 46 MB,
+//                        5.3 TB/s; 48 of 5632 to 2048 10.5 us: its 128 workgroups leave half of the units idle)
+//   rows_kernel          straight from memory into matrix operands, any alignment (12.6 us; 22 us; weights that
+//                        start at odd addresses 33 and 36)
 #include "ff_gemm.hpp"
 
 namespace ddpm {

@@ -7,13 +7,15 @@
 // 32), makes their z (its waves 32 columns each), puts dz into LDS, and multiplies it by both; grad_W
 // stays in registers until the workgroup's last rows and leaves as one row of float32 partials, which a
 // second kernel adds up.  65536 rows of 64 to 2 128 take 36 us in bfloat16 and 52 in float32, 262144 rows 103
-// and 169.  The bytes alone are 6.5 us and 13.  What bounds it are vector instructions (bfloat16: 76 % of the cycles; float32: 36 %, and 38 %
-// the matrix units), most of them the activation's slopes and the fragments' and rows' addresses.
+// and 169.  The bytes of 65536 rows alone are 6.5 us and 13.  What bounds it are vector instructions (47 % of the
+// cycles of 262144 rows in bfloat16, 37 % in float32; the matrix units 23 % and 42 %), most of them the activation's
+// slopes and the fragments' and rows' addresses, and eight waves a compute unit to hide the rest behind.
 //
-// Everything in LDS is bfloat16, of float32 three planes (see split_of), of bfloat16's dz two, each made once: split at every
-// read the kernel took 79 us for 65536 rows of 64 to 2 128, most of it vector instructions.  A sheet is
-// ROWS rows of 128 bytes for each 64 columns, its 16-byte chunks placed by an exclusive or with bits of
-// the row, such that fragments are read both along its rows and down its columns with few conflicts.
+// Everything in LDS is bfloat16, of float32 three planes (see split_of), of bfloat16's dz two, each made once:
+// split at every read the float32 kernel took 79 us for 65536 rows of 64 to 2 128, most of it vector
+// instructions.  A sheet is ROWS rows of 128 bytes for each 64 columns, its 16-byte chunks placed by an exclusive
+// or with bits of the row, such that fragments are read both along its rows and down its columns with few
+// conflicts.
 #include "ff_gemm.hpp"
 #include "seq_launch.hpp"
 

@@ -11,6 +11,11 @@
  *   element.  Outputs must not overlap inputs or each other.  The library allocates nothing:
  *   workspaces come from the caller, 16-byte aligned, of the size that the matching *_workspace
  *   function returns in bytes (NULL where that is 0; their contents need no preparation).
+ * Alignment costs time only.  Products are fastest where the rows of x, weight and grad start at
+ *   multiples of 16 bytes.  Rows of C elements that are no such multiple are copied where that pays;
+ *   views whose address or stride is none are not, and take 1.3 to 3 times as long (4096^3, us: y, grad_x
+ *   and grad_weight in bfloat16 113, 112, 114, from odd addresses 174, 180, 371; in float32 603, 608,
+ *   611, and 794, 829, 839).
  * Streams.  As in ddpm.h: work is enqueued on `stream` and the call returns.  Nothing is cleared
  *   by memset, so every call may be captured into a graph.  No atomics are used: equal inputs
  *   at equally aligned addresses give equal bits.
